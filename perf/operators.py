@@ -381,8 +381,7 @@ def _plain_scan(s):
     if case["pass"] == "forward":
         return {"h": h.to(dt), "h_last": h_last}
     # backward: G_t = dh_t + a_{t+1} G_{t+1}, down the rows turned round
-    G = s["dh"].float()
-    G[last] += s["dh_last"][full]
+    G = s["dh"].float().index_add(0, last, s["dh_last"][full])
     back = torch.cat([inner[1:], torch.zeros_like(inner[:1])])  # 0 behind each sequence's last token
     G = _doubling(back.flip(0), G.flip(0), s["longest"]).flip(0)
     previous = torch.cat([torch.zeros_like(h[:1]), h[:-1]])
