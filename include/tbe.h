@@ -359,6 +359,226 @@ int tbe_backward_reduce(const tbe_plan* plan, const tbe_optimizer* opt, void* we
                         void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Training operators beside the tables
+ * ---------------------------------------------------------------------------
+ * What one training step of a model over jagged histories needs next to the
+ * tables' forward, backward and exact update: a recurrence that mixes a
+ * history's rows over time (tbe_gated_scan), a loss over scored catalogue
+ * rows (tbe_preference_loss) and an optimizer for the dense parameters
+ * (tbe_adamw_step).  The conventions above hold for them too.  dtype codes
+ * are TBE_F32 / TBE_F16 / TBE_BF16; arithmetic, states and sums are fp32.
+ */
+
+/*
+ * Gated linear recurrence over jagged sequences.  For every channel c and
+ * every sequence s (tokens offsets[s] .. offsets[s+1] - 1, in order):
+ *   u_t = sharpness * softplus(decay[c]) * sigmoid(recur[t, c])
+ *   a_t = exp(-u_t)
+ *   h_t = a_t * h_{t-1} + sqrt(1 - a_t^2) * sigmoid(gate[t, c]) * x[t, c]
+ * with h_{-1} = h0[s, c] (0 where h0 is NULL).  A softplus below 2^-126, the
+ * smallest normal fp32 number, counts as 0: the channel keeps its state.
+ *   x, recur, gate  : device, [tokens, channels] of dtype; consecutive
+ *                     channels, *_stride elements from token to token (so
+ *                     the three may be slices of one projection); not
+ *                     overlapping any output
+ *   decay           : device fp32 [channels]
+ *   offsets         : device int64 (or int32 where offsets_i32 != 0)
+ *                     [sequences + 1], from 0 to tokens; empty sequences are
+ *                     allowed.  Broken offsets set TBE_DEV_BAD_OFFSETS;
+ *                     results are then unspecified, accesses in bounds
+ *   h0              : device fp32 [sequences, channels] or NULL
+ * Limits: tokens < 2^38, channels <= 2^20, ceil(tokens / TBE_SCAN_TILE) *
+ * ceil(channels / 32) < 2^31.
+ */
+#define TBE_SCAN_TILE 128 /* tokens between two saved states */
+typedef struct tbe_scan_inputs {
+  int64_t tokens;
+  int32_t sequences;
+  int32_t channels;
+  int32_t dtype;
+  int32_t offsets_i32;
+  const void* x;
+  const void* recur;
+  const void* gate;
+  int64_t x_stride;
+  int64_t recur_stride;
+  int64_t gate_stride;
+  const float* decay;
+  const void* offsets;
+  const float* h0;
+  float sharpness;
+} tbe_scan_inputs;
+
+/* Saved states per channel for a batch of `tokens`: ceil(tokens /
+ * TBE_SCAN_TILE), at least 1. */
+int64_t tbe_gated_scan_states(int64_t tokens);
+/* Workspace (device, 256-byte aligned; no initialisation needed) of
+ * tbe_gated_scan (backward = 0) or tbe_gated_scan_backward (1). */
+size_t tbe_gated_scan_workspace_bytes(int64_t tokens, int32_t channels, int32_t backward);
+
+/*   h       : device [tokens, channels] of dtype, h_stride elements from
+ *             token to token: every h_t, rounded once
+ *   h_last  : device fp32 [sequences, channels]: each sequence's last state
+ *             (an empty sequence's h0)
+ *   states  : device fp32 [tbe_gated_scan_states(tokens), channels] or NULL:
+ *             what the backward needs of the forward
+ * Errors: TBE_ERR_INVALID_ARG, TBE_ERR_UNSUPPORTED (limits, alignment),
+ * TBE_ERR_WORKSPACE, TBE_ERR_CUDA; TBE_DEV_BAD_OFFSETS, TBE_DEV_TIMEOUT. */
+int tbe_gated_scan(const tbe_scan_inputs* in, void* h, int64_t h_stride, float* h_last, float* states,
+                   void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Gradients of sum(dh * h) + sum(dh_last * h_last).
+ *   in       : as given to the forward
+ *   dh       : device [tokens, channels] of dtype, dh_stride apart
+ *   dh_last  : device fp32 [sequences, channels] or NULL (zero)
+ *   states   : as the forward wrote them
+ *   out      : dx, drecur, dgate (device, dtype, own strides), ddecay
+ *              (device fp32 [channels]) and dh0 (device fp32 [sequences,
+ *              channels] or NULL)
+ * Results do not depend on timing (no atomic sums). */
+typedef struct tbe_scan_grads {
+  void* dx;
+  void* drecur;
+  void* dgate;
+  int64_t dx_stride;
+  int64_t drecur_stride;
+  int64_t dgate_stride;
+  float* ddecay;
+  float* dh0;
+} tbe_scan_grads;
+int tbe_gated_scan_backward(const tbe_scan_inputs* in, const void* dh, int64_t dh_stride, const float* dh_last,
+                            const float* states, const tbe_scan_grads* out, void* workspace, size_t workspace_bytes,
+                            int32_t* dev_status, void* stream);
+
+/* One token of every sequence: tokens == sequences, token s is sequence s's
+ * next; offsets and h0 are not used (h0 must be NULL).
+ *   state : device fp32 [sequences, channels], moved on in place
+ *   h     : device [sequences, channels] of dtype */
+int tbe_gated_scan_step(const tbe_scan_inputs* in, float* state, void* h, int64_t h_stride, void* stream);
+
+/*
+ * Preference loss over pairs of label sequences.  Sequences are the bags of
+ * two features (0: preferred, 1: rejected) of `pairs` bags each, in the
+ * feature-major layout: token n belongs to sequence q = t * pairs + b where
+ * offsets[q] <= n < offsets[q+1].  With y = labels[n]:
+ *   lp_n = logits[n, y] - log sum_v exp(logits[n, v])
+ *   s_q  = sum of lp_n over the tokens of q
+ *   d_b  = beta * ((s_{0,b} - ref_{0,b}) - (s_{1,b} - ref_{1,b}))
+ *   loss = mean_b (1 - label_smoothing) log(1 + exp(-d_b)) + label_smoothing log(1 + exp(d_b))
+ * A token with y < 0 takes no part and gets a zero gradient; so does one
+ * with y >= vocab (TBE_DEV_BAD_INDEX is set) and one whose logits are all
+ * -inf.  Single -inf entries have probability 0.
+ *   logits    : device, [tokens, vocab] of dtype, logits_stride apart
+ *   labels    : device int64 [tokens]
+ *   offsets   : device int64 [2 * pairs + 1], from 0 to tokens, else
+ *               TBE_DEV_BAD_OFFSETS (results unspecified, accesses in bounds)
+ *   ref_logps : device fp32 [2 * pairs], the reference's s_q
+ * tokens, vocab and pairs are at least 1; tokens * pieces per row < 2^31.
+ */
+typedef struct tbe_preference_inputs {
+  const void* logits;
+  int64_t logits_stride;
+  const int64_t* labels;
+  const int64_t* offsets;
+  const float* ref_logps;
+  int64_t tokens;
+  int32_t vocab;
+  int32_t pairs;
+  int32_t dtype;
+  float beta;
+  float label_smoothing;
+} tbe_preference_inputs;
+
+/* Workspace (device, 256-byte aligned, no initialisation needed). */
+size_t tbe_preference_workspace_bytes(int64_t tokens, int32_t vocab, int32_t pairs);
+
+/*   loss      : device fp32 scalar
+ *   seq_logps : device fp32 [2 * pairs], s_q
+ *   margins   : device fp32 [pairs], d_b
+ *   lse, coef : device fp32 [tokens], what the backward needs
+ *   dlogits   : device [tokens, vocab] of dtype, or NULL for the loss alone:
+ *               grad_scale * d loss / d logits, every element written; may
+ *               be `logits` itself (with its stride) */
+int tbe_preference_loss(const tbe_preference_inputs* in, float* loss, float* seq_logps, float* margins, float* lse,
+                        float* coef, void* dlogits, int64_t dlogits_stride, float grad_scale, void* workspace,
+                        size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* The gradient on its own, from the lse and coef of tbe_preference_loss. */
+int tbe_preference_loss_backward(const tbe_preference_inputs* in, const float* lse, const float* coef,
+                                 float grad_scale, void* dlogits, int64_t dlogits_stride, void* stream);
+
+/*
+ * One AdamW step over a list of tensors in one launch:
+ *   g = grad * *grad_scale
+ *   m <- beta1 m + (1 - beta1) g
+ *   v <- beta2 v + (1 - beta2) g^2
+ *   w <- (1 - learning_rate weight_decay) w
+ *        - learning_rate / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32, w rounded once to its type.  States are flat: tensor i's begin
+ * at the first free block of TBE_ADAMW_BLOCK elements after tensor i - 1's
+ * (tbe_adamw_state_blocks blocks in all).
+ *   state_bits 32 : exp_avg, exp_avg_sq fp32 [blocks * TBE_ADAMW_BLOCK];
+ *                   padding is neither read nor written
+ *   state_bits 8  : int8 and uint8 codes of that many elements and one fp32
+ *                   scale per block each: m = sign(q) (q / 127)^2 scale,
+ *                   v = (q / 255)^4 scale, scale the block's largest
+ *                   magnitude, q the code whose root is nearest (at least 1
+ *                   for a v above 0).  A block that holds an infinite or NaN
+ *                   moment reads back as NaN.  Start from zero codes and
+ *                   scales.
+ * The plan packs the tensors' device pointers and sizes into caller-provided
+ * device memory (tbe_adamw_plan_device_bytes, 16-byte aligned, kept alive
+ * while the plan is in use) as tbe_plan_create does; the tensors must stay
+ * where they are while it is used.
+ */
+#define TBE_ADAMW_BLOCK 256
+#define TBE_ADAMW_MAX_TENSORS 65536
+typedef struct tbe_adamw_tensors {
+  int32_t n;
+  int32_t state_bits;
+  const int64_t* numel;       /* host [n]; 0 is allowed */
+  void* const* params;        /* host [n] of device pointers */
+  const void* const* grads;   /* host [n] of device pointers */
+  const int32_t* param_dtype; /* host [n] */
+  const int32_t* grad_dtype;  /* host [n] */
+} tbe_adamw_tensors;
+typedef struct tbe_adamw {
+  double learning_rate;
+  double beta1;
+  double beta2;
+  double eps;
+  double weight_decay;
+  int64_t step; /* 1 for the first */
+} tbe_adamw;
+typedef struct tbe_adamw_plan tbe_adamw_plan;
+
+/* State blocks of the list, or -1 (sizes out of range, 2^31 blocks or more). */
+int64_t tbe_adamw_state_blocks(int32_t n, const int64_t* numel);
+size_t tbe_adamw_plan_device_bytes(int32_t n, const int64_t* numel);
+int tbe_adamw_plan_create(const tbe_adamw_tensors* L, void* dev_meta, size_t dev_meta_bytes, void* stream,
+                          tbe_adamw_plan** plan_out);
+void tbe_adamw_plan_destroy(tbe_adamw_plan* plan);
+
+/*   exp_avg, exp_avg_sq : device, 32-byte aligned, updated in place
+ *   *_scale             : device fp32 [blocks] (8-bit states) or NULL
+ *   grad_scale          : device fp32 scalar or NULL (1)
+ *   skip                : device int32 scalar or NULL; where it is not 0 the
+ *                         step changes nothing
+ * Errors: TBE_ERR_INVALID_ARG (nulls, step < 1, a beta outside [0, 1), a
+ * value that is not finite, another device), TBE_ERR_UNSUPPORTED (alignment),
+ * TBE_ERR_CUDA. */
+int tbe_adamw_step(const tbe_adamw_plan* plan, const tbe_adamw* opt, void* exp_avg, void* exp_avg_sq,
+                   float* exp_avg_scale, float* exp_avg_sq_scale, const float* grad_scale, const int32_t* skip,
+                   void* stream);
+
+/* 8-bit states as the fp32 values they stand for ([blocks *
+ * TBE_ADAMW_BLOCK] each, 32-byte aligned), for checkpoints and inspection. */
+int tbe_adamw_state(const tbe_adamw_plan* plan, const void* exp_avg, const void* exp_avg_sq,
+                    const float* exp_avg_scale, const float* exp_avg_sq_scale, float* exp_avg_out,
+                    float* exp_avg_sq_out, void* stream);
+
+/*
  * Tuning knobs (process-wide; set them before launching work that should
  * use them, not concurrently with launches).
  *   long_run_threshold : runs with at least this many lookups take the

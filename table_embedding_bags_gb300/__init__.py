@@ -34,6 +34,10 @@ EXPORTED = [
     "tbe_backward_static_workspace", "tbe_exact_update", "tbe_wait_selftest", "tbe_backward_update",
     "tbe_forward_i32", "tbe_backward_i32", "tbe_backward_update_i32", "tbe_backward_index", "tbe_backward_index_i32",
     "tbe_backward_reduce",
+    "tbe_gated_scan_states", "tbe_gated_scan_workspace_bytes", "tbe_gated_scan", "tbe_gated_scan_backward",
+    "tbe_gated_scan_step", "tbe_preference_workspace_bytes", "tbe_preference_loss", "tbe_preference_loss_backward",
+    "tbe_adamw_state_blocks", "tbe_adamw_plan_device_bytes", "tbe_adamw_plan_create", "tbe_adamw_plan_destroy",
+    "tbe_adamw_step", "tbe_adamw_state",
 ]
 TBE_STATIC_WORKSPACE_BYTES = 32 << 20
 
@@ -124,6 +128,7 @@ def load_library(path: str = LIB_PATH):
                                         P]
     lib.tbe_wait_selftest.restype = ctypes.c_int
     lib.tbe_wait_selftest.argtypes = [i32, i32, P, P]
+    training.declare(lib)
     _lib = lib
     return lib
 
@@ -518,3 +523,9 @@ def wait_selftest(kind: int, polls: int, dev_status, stream=None):
 
 def version() -> str:
     return load_library().tbe_version().decode()
+
+
+from . import training  # noqa: E402  (the training operators beside the tables; uses this module's helpers)
+from .training import (TBE_ADAMW_BLOCK, TBE_SCAN_TILE, AdamWPlan, GatedScan, GatedScanGrads,  # noqa: E402, F401
+                       PreferenceLoss, tbe_adamw_state, tbe_adamw_step, tbe_gated_scan, tbe_gated_scan_backward,
+                       tbe_gated_scan_step, tbe_preference_loss, tbe_preference_loss_backward)

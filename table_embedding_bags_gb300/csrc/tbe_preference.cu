@@ -1,0 +1,521 @@
+// tbe_preference.cu -- a paired-log-ratio preference loss over catalogue
+// logits, with its gradient.
+//
+//   lp_n  = logit[n, y_n] - lse_n            lse_n = log sum_v exp(logit[n, v])
+//   s(q)  = sum of lp_n over sequence q's tokens
+//   d_b   = beta ((s(0, b) - ref(0, b)) - (s(1, b) - ref(1, b)))
+//   loss  = mean_b (1 - e) log(1 + exp(-d_b)) + e log(1 + exp(d_b))
+//   dlogit[n, v] = coef_n ([v = y_n] - exp(logit[n, v] - lse_n))
+// with coef_n = +- beta / P ((e - 1) / (1 + exp(d_b)) + e / (1 + exp(-d_b))),
+// + for a preferred token, - for a rejected one.  Sequences are the bags of
+// two features (0 preferred, 1 rejected) in the feature-major layout.
+//
+// Three kernels: the rows' log-sums (one pass over the logits with a running
+// maximum and sum per thread; a long row is cut over several thread blocks
+// where there are few rows), the pairs, and the gradient.
+#include "tbe_internal.cuh"
+
+#include <cmath>
+
+namespace tbe {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLowest = -3.402823466e38f;
+
+struct PrefArgs {
+  const void* logits;
+  int64_t stride;
+  const int64_t* labels;
+  const int64_t* offsets;
+  const float* ref;
+  int64_t N;
+  int32_t V;
+  int32_t P;
+  int32_t splits;
+  float beta, smoothing, scale;
+  float* loss;
+  float* logps;
+  float* margins;
+  float* lse;
+  float* coef;
+  void* dlogits;
+  int64_t dstride;
+  float2* part;      // [N, splits] running maximum and sum
+  float* lp;         // [N]
+  float* block_loss; // one per block of the pairs' kernel
+  uint32_t* arrived;
+  int32_t* status;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Running maximum and sum of exp(x - maximum).  The maximum starts at the
+// lowest finite value: entries of -inf add exp(-inf) = 0, and a row of
+// nothing else keeps the sum 0.
+struct Run {
+  float m, s;
+};
+__device__ __forceinline__ Run merge(Run a, Run b) {
+  Run r;
+  r.m = fmaxf(a.m, b.m);
+  r.s = a.s * ex2((a.m - r.m) * kLog2e) + b.s * ex2((b.m - r.m) * kLog2e);
+  return r;
+}
+
+template <int DT>
+struct Vec {
+  static constexpr int kElems = Chunk<DT>::kElems;
+  static constexpr int kSize = DT == TBE_F32 ? 4 : 2;
+};
+
+template <int DT>
+__device__ __forceinline__ float load_one(const void* p, int64_t i) {
+  if (DT == TBE_F32) return static_cast<const float*>(p)[i];
+  if (DT == TBE_F16) return __half2float(static_cast<const __half*>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+template <int DT>
+__device__ __forceinline__ void store_one(void* p, int64_t i, float f) {
+  if (DT == TBE_F32) static_cast<float*>(p)[i] = f;
+  else if (DT == TBE_F16) static_cast<__half*>(p)[i] = __float2half_rn(f);
+  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(f);
+}
+template <int DT>
+__device__ __forceinline__ const uint8_t* elem_ptr(const void* p, int64_t i) {
+  return static_cast<const uint8_t*>(p) + i * Vec<DT>::kSize;
+}
+template <int DT>
+__device__ __forceinline__ uint8_t* elem_ptr(void* p, int64_t i) {
+  return static_cast<uint8_t*>(p) + i * Vec<DT>::kSize;
+}
+
+__device__ __forceinline__ uint4 ld_plain16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// A run of n elements from p on, read by `workers` threads of which this is
+// number `me`: elements before the first 16-byte boundary and after the last
+// one on their own, the rest in 16-byte pieces, four in flight per thread.
+template <int DT>
+__device__ __forceinline__ Run sum_row(const uint8_t* p, int64_t n, int me, int workers) {
+  constexpr int kE = Vec<DT>::kElems, kS = Vec<DT>::kSize, kFlight = 4;
+  Run r{kLowest, 0.f};
+  int64_t head = (16 - ((uintptr_t)p & 15)) % 16 / kS;
+  if (head > n) head = n;
+  const int64_t pieces = (n - head) / kE, tail = head + pieces * kE;
+  auto one = [&](float x) {
+    const float m = fmaxf(r.m, x);
+    r.s = r.s * ex2((r.m - m) * kLog2e) + ex2((x - m) * kLog2e);
+    r.m = m;
+  };
+  for (int64_t i = me; i < head; i += workers) one(load_one<DT>(p, i));
+  for (int64_t i = tail + me; i < n; i += workers) one(load_one<DT>(p, i));
+  const uint8_t* body = p + head * kS;
+  for (int64_t i = me; i < pieces; i += (int64_t)workers * kFlight) {
+    uint4 raw[kFlight];
+    bool in[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      in[k] = i + (int64_t)k * workers < pieces;
+      if (in[k]) raw[k] = ld_plain16(body + (i + (int64_t)k * workers) * 16);
+    }
+    float x[kFlight][kE], top = r.m;
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      if (in[k]) {
+        Chunk<DT>::to_float(raw[k], x[k]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) x[k][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int e = 0; e < kE; ++e) top = fmaxf(top, x[k][e]);
+    }
+    float s = r.s * ex2((r.m - top) * kLog2e);
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+#pragma unroll
+      for (int e = 0; e < kE; ++e) s += ex2((x[k][e] - top) * kLog2e);
+    r.m = top;
+    r.s = s;
+  }
+  return r;
+}
+
+__device__ __forceinline__ Run warp_merge(Run r) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    Run n;
+    n.m = __shfl_xor_sync(kFull, r.m, o);
+    n.s = __shfl_xor_sync(kFull, r.s, o);
+    r = merge(r, n);
+  }
+  return r;
+}
+
+// The label of row n, or -1 where the row takes no part.
+__device__ __forceinline__ int64_t label_of(const PrefArgs& a, int64_t n) {
+  const int64_t y = a.labels[n];
+  if (y >= a.V) {
+    report(a.status, TBE_DEV_BAD_INDEX);
+    return -1;
+  }
+  return y < 0 ? -1 : y;
+}
+
+// A row's log-sum and its label's log-probability.  A row of which every
+// entry is -inf has nothing to choose from: it takes no part (lse = -inf).
+template <int DT>
+__device__ __forceinline__ void finish_row(const PrefArgs& a, int64_t n, Run r) {
+  const int64_t y = label_of(a, n);
+  const float lse = r.s == 0.f ? -INFINITY : r.m + logf(r.s);
+  a.lse[n] = lse;
+  a.lp[n] = y >= 0 && lse != -INFINITY ? load_one<DT>(a.logits, n * a.stride + y) - lse : 0.f;
+}
+
+// One thread block per (row, split), or one warp per row (WARP).
+template <int DT, bool WARP>
+__global__ void __launch_bounds__(kThreads) rows_kernel(PrefArgs a) {
+  __shared__ Run s_run[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.arrived = 0;
+  if (WARP) {
+    const int64_t n = (int64_t)blockIdx.x * kWarps + warp;
+    if (n >= a.N) return;
+    const Run r = warp_merge(sum_row<DT>(elem_ptr<DT>(a.logits, n * a.stride), a.V, lane, 32));
+    if (lane == 0) {
+      finish_row<DT>(a, n, r);
+      a.coef[n] = 0.f;
+    }
+    return;
+  }
+  const int64_t n = blockIdx.x / a.splits, part = blockIdx.x % a.splits;
+  const int64_t lo = a.V * part / a.splits, hi = a.V * (part + 1) / a.splits;
+  Run r = warp_merge(sum_row<DT>(elem_ptr<DT>(a.logits, n * a.stride + lo), hi - lo, threadIdx.x, kThreads));
+  if (lane == 0) s_run[warp] = r;
+  __syncthreads();
+  if (warp == 0) {
+    r = lane < kWarps ? s_run[lane] : Run{kLowest, 0.f};
+    r = warp_merge(r);
+    if (lane == 0) {
+      if (a.splits == 1) finish_row<DT>(a, n, r);
+      else a.part[n * a.splits + part] = make_float2(r.m, r.s);
+      if (part == 0) a.coef[n] = 0.f;
+    }
+  }
+}
+
+// A warp per pair.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) pairs_kernel(PrefArgs a) {
+  __shared__ float s_loss[kWarps];
+  __shared__ bool s_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t b = (int64_t)blockIdx.x * kWarps + warp;
+  float loss = 0.f;
+  if (b < a.P) {
+    float logp[2];
+    int64_t lo[2], hi[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int64_t q = (int64_t)t * a.P + b;
+      lo[t] = a.offsets[q];
+      hi[t] = a.offsets[q + 1];
+      const bool bad = lo[t] < 0 || hi[t] < lo[t] || hi[t] > a.N || (q == 0 && lo[t] != 0) ||
+                       (q == 2 * (int64_t)a.P - 1 && hi[t] != a.N);
+      if (bad && lane == 0) report(a.status, TBE_DEV_BAD_OFFSETS);
+      if (lo[t] < 0) lo[t] = 0;
+      if (hi[t] > a.N) hi[t] = a.N;
+      float s = 0.f;
+      for (int64_t n = lo[t] + lane; n < hi[t]; n += 32) {
+        if (a.splits > 1) {
+          Run r{kLowest, 0.f};
+          for (int p = 0; p < a.splits; ++p) {
+            const float2 v = a.part[n * a.splits + p];
+            r = merge(r, Run{v.x, v.y});
+          }
+          finish_row<DT>(a, n, r);
+        }
+        s += a.lp[n];
+      }
+      logp[t] = warp_sum(s);
+      if (lane == 0) a.logps[q] = logp[t];
+    }
+    const float d = a.beta * ((logp[0] - a.ref[b]) - (logp[1] - a.ref[a.P + b]));
+    // log(1 + exp(-d)) and log(1 + exp(d)) without overflow
+    const float l = log1pf(expf(-fabsf(d)));
+    loss = (1.f - a.smoothing) * (fmaxf(-d, 0.f) + l) + a.smoothing * (fmaxf(d, 0.f) + l);
+    const float up = 1.f / (1.f + expf(-d)), down = 1.f / (1.f + expf(d));
+    const float c = a.beta / (float)a.P * (a.smoothing * up - (1.f - a.smoothing) * down);
+    if (lane == 0) a.margins[b] = d;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      for (int64_t n = lo[t] + lane; n < hi[t]; n += 32) {
+        const int64_t y = a.labels[n];
+        a.coef[n] = y < 0 || y >= a.V || a.lse[n] == -INFINITY ? 0.f : (t == 0 ? c : -c);
+      }
+  }
+  if (lane == 0) s_loss[warp] = loss;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float s = 0.f;
+    for (int w = 0; w < kWarps; ++w) s += s_loss[w];
+    a.block_loss[blockIdx.x] = s;
+    __threadfence();
+    s_last = atomicAdd(a.arrived, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last || warp != 0) return;
+  // the last block to finish adds the blocks' sums, always in the same order
+  __threadfence();
+  float s = 0.f;
+  for (unsigned i = lane; i < gridDim.x; i += 32) s += __ldcg(a.block_loss + i);
+  s = warp_sum(s);
+  if (lane == 0) *a.loss = s / (float)a.P;
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 pack(const float* f);
+template <>
+__device__ __forceinline__ uint4 pack<TBE_F32>(const float* f) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+template <>
+__device__ __forceinline__ uint4 pack<TBE_F16>(const float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __half2 h = __floats2half2_rn(f[2 * k], f[2 * k + 1]);
+    w[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <>
+__device__ __forceinline__ uint4 pack<TBE_BF16>(const float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+    w[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// dlogit over n elements, y the label's place among them (or outside).
+template <int DT>
+__device__ __forceinline__ void grad_row(const uint8_t* p, uint8_t* o, int64_t n, int64_t y, float coef, float lse,
+                                         int me, int workers) {
+  constexpr int kE = Vec<DT>::kElems, kS = Vec<DT>::kSize, kFlight = 4;
+  // both rows in 16-byte pieces only where they lie alike
+  int64_t head = (16 - ((uintptr_t)p & 15)) % 16 / kS;
+  if (head > n || (((uintptr_t)p ^ (uintptr_t)o) & 15) != 0) head = n;
+  const int64_t pieces = (n - head) / kE, tail = head + pieces * kE;
+  auto value = [&](float x, bool label) {
+    const float e = -coef * ex2((x - lse) * kLog2e);
+    return label ? e + coef : e;
+  };
+  for (int64_t i = me; i < head; i += workers)
+    store_one<DT>(o, i, coef == 0.f ? 0.f : value(load_one<DT>(p, i), i == y));
+  for (int64_t i = tail + me; i < n; i += workers)
+    store_one<DT>(o, i, coef == 0.f ? 0.f : value(load_one<DT>(p, i), i == y));
+  const uint8_t* pb = p + head * kS;
+  uint8_t* ob = o + head * kS;
+  if (coef == 0.f) {  // a row that takes no part is not read
+    for (int64_t i = me; i < pieces; i += workers) *reinterpret_cast<uint4*>(ob + i * 16) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  for (int64_t i = me; i < pieces; i += (int64_t)workers * kFlight) {
+    uint4 raw[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+      if (i + (int64_t)k * workers < pieces) raw[k] = ld_plain16(pb + (i + (int64_t)k * workers) * 16);
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int64_t at = i + (int64_t)k * workers;
+      if (at < pieces) {
+        float x[kE];
+        Chunk<DT>::to_float(raw[k], x);
+        const int64_t first = head + at * kE;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) x[e] = value(x[e], first + e == y);
+        *reinterpret_cast<uint4*>(ob + at * 16) = pack<DT>(x);
+      }
+    }
+  }
+}
+
+template <int DT, bool WARP>
+__global__ void __launch_bounds__(kThreads) grad_kernel(PrefArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n = WARP ? (int64_t)blockIdx.x * kWarps + warp : blockIdx.x / a.splits;
+  if (n >= a.N) return;
+  const int64_t part = WARP ? 0 : blockIdx.x % a.splits, splits = WARP ? 1 : a.splits;
+  const int64_t lo = a.V * part / splits, hi = a.V * (part + 1) / splits;
+  const float coef = a.coef[n] * a.scale;
+  grad_row<DT>(elem_ptr<DT>(a.logits, n * a.stride + lo), elem_ptr<DT>(a.dlogits, n * a.dstride + lo), hi - lo,
+               a.labels[n] - lo, coef, a.lse[n], WARP ? lane : threadIdx.x, WARP ? 32 : kThreads);
+}
+
+// A warp takes a row where rows are short enough.
+constexpr int kWarpRow = 1024;
+
+// Blocks per row: where there are fewer rows than would fill the GPU twice
+// over, rows are cut, into pieces of at least 2048 entries.
+int32_t splits_of(int64_t N, int32_t V) {
+  if (N <= 0 || V <= kWarpRow) return 1;
+  const int64_t want = (4 * (int64_t)sm_count() + N - 1) / N, most = V / 2048;
+  const int64_t s = want < most ? want : most;
+  return s < 1 ? 1 : (int32_t)s;
+}
+
+struct Workspace {
+  size_t part, lp, block_loss, bytes;
+};
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+Workspace layout(int64_t N, int32_t V, int32_t P) {
+  Workspace w;
+  size_t at = 256;  // the arrival counter
+  w.part = at;
+  const int32_t s = splits_of(N, V);
+  if (s > 1) at += round256((size_t)N * s * sizeof(float2));
+  w.lp = at;
+  at += round256((size_t)N * 4);
+  w.block_loss = at;
+  at += round256(((size_t)P + kWarps - 1) / kWarps * 4);
+  w.bytes = at;
+  return w;
+}
+
+template <int DT>
+int launch_grad(const PrefArgs& a, cudaStream_t s) {
+  if (a.V <= kWarpRow) grad_kernel<DT, true><<<(unsigned)((a.N + kWarps - 1) / kWarps), kThreads, 0, s>>>(a);
+  else grad_kernel<DT, false><<<(unsigned)(a.N * a.splits), kThreads, 0, s>>>(a);
+  return check_launch();
+}
+
+template <int DT>
+int launch_loss(const PrefArgs& a, cudaStream_t s) {
+  if (a.V <= kWarpRow) rows_kernel<DT, true><<<(unsigned)((a.N + kWarps - 1) / kWarps), kThreads, 0, s>>>(a);
+  else rows_kernel<DT, false><<<(unsigned)(a.N * a.splits), kThreads, 0, s>>>(a);
+  int st = check_launch();
+  if (st != TBE_OK) return st;
+  trace_mark(s, "preference_rows");
+  pairs_kernel<DT><<<(unsigned)((a.P + kWarps - 1) / kWarps), kThreads, 0, s>>>(a);
+  st = check_launch();
+  if (st != TBE_OK) return st;
+  trace_mark(s, "preference_pairs");
+  if (a.dlogits) {
+    st = launch_grad<DT>(a, s);
+    trace_mark(s, "preference_grad");
+  }
+  return st;
+}
+
+bool aligned_for(const void* p, int32_t dtype) { return ((uintptr_t)p & (dtype == TBE_F32 ? 3 : 1)) == 0; }
+
+int check(const tbe_preference_inputs* in) {
+  if (!in) return TBE_ERR_INVALID_ARG;
+  if (in->dtype < TBE_F32 || in->dtype > TBE_BF16) return TBE_ERR_INVALID_ARG;
+  if (in->tokens < 1 || in->vocab < 1 || in->pairs < 1 || in->logits_stride < in->vocab) return TBE_ERR_INVALID_ARG;
+  if (!std::isfinite(in->beta) || !(in->label_smoothing >= 0.f && in->label_smoothing <= 1.f)) return TBE_ERR_INVALID_ARG;
+  if (!in->logits || !in->labels || !in->offsets || !in->ref_logps) return TBE_ERR_INVALID_ARG;
+  if (!aligned_for(in->logits, in->dtype)) return TBE_ERR_UNSUPPORTED;
+  if (in->tokens * (int64_t)splits_of(in->tokens, in->vocab) >= (int64_t(1) << 31) || in->pairs >= (1 << 30))
+    return TBE_ERR_UNSUPPORTED;
+  return TBE_OK;
+}
+
+PrefArgs args_of(const tbe_preference_inputs* in) {
+  PrefArgs a = {};
+  a.logits = in->logits;
+  a.stride = in->logits_stride;
+  a.labels = in->labels;
+  a.offsets = in->offsets;
+  a.ref = in->ref_logps;
+  a.N = in->tokens;
+  a.V = in->vocab;
+  a.P = in->pairs;
+  a.beta = in->beta;
+  a.smoothing = in->label_smoothing;
+  a.splits = splits_of(in->tokens, in->vocab);
+  return a;
+}
+
+}  // namespace
+}  // namespace tbe
+
+using namespace tbe;
+
+extern "C" {
+
+size_t tbe_preference_workspace_bytes(int64_t tokens, int32_t vocab, int32_t pairs) {
+  if (tokens < 1 || vocab < 1 || pairs < 1) return 0;
+  return layout(tokens, vocab, pairs).bytes;
+}
+
+int tbe_preference_loss(const tbe_preference_inputs* in, float* loss, float* seq_logps, float* margins, float* lse,
+                        float* coef, void* dlogits, int64_t dlogits_stride, float grad_scale, void* workspace,
+                        size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  const int st = check(in);
+  if (st != TBE_OK) return st;
+  if (!loss || !seq_logps || !margins || !lse || !coef || !workspace) return TBE_ERR_INVALID_ARG;
+  if (dlogits && (dlogits_stride < in->vocab || !std::isfinite(grad_scale))) return TBE_ERR_INVALID_ARG;
+  if (!aligned_for(dlogits, in->dtype) || ((uintptr_t)workspace & 255)) return TBE_ERR_UNSUPPORTED;
+  const Workspace w = layout(in->tokens, in->vocab, in->pairs);
+  if (workspace_bytes < w.bytes) return TBE_ERR_WORKSPACE;
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  PrefArgs a = args_of(in);
+  a.loss = loss;
+  a.logps = seq_logps;
+  a.margins = margins;
+  a.lse = lse;
+  a.coef = coef;
+  a.dlogits = dlogits;
+  a.dstride = dlogits_stride;
+  a.scale = grad_scale;
+  a.arrived = reinterpret_cast<uint32_t*>(p);
+  a.part = reinterpret_cast<float2*>(p + w.part);
+  a.lp = reinterpret_cast<float*>(p + w.lp);
+  a.block_loss = reinterpret_cast<float*>(p + w.block_loss);
+  a.status = dev_status;
+  cudaStream_t s = (cudaStream_t)stream;
+  trace_begin(s);
+  if (in->dtype == TBE_F32) return launch_loss<TBE_F32>(a, s);
+  if (in->dtype == TBE_F16) return launch_loss<TBE_F16>(a, s);
+  return launch_loss<TBE_BF16>(a, s);
+}
+
+int tbe_preference_loss_backward(const tbe_preference_inputs* in, const float* lse, const float* coef,
+                                 float grad_scale, void* dlogits, int64_t dlogits_stride, void* stream) {
+  const int st = check(in);
+  if (st != TBE_OK) return st;
+  if (!lse || !coef || !dlogits || dlogits_stride < in->vocab || !std::isfinite(grad_scale)) return TBE_ERR_INVALID_ARG;
+  if (!aligned_for(dlogits, in->dtype)) return TBE_ERR_UNSUPPORTED;
+  PrefArgs a = args_of(in);
+  a.lse = const_cast<float*>(lse);    // only read
+  a.coef = const_cast<float*>(coef);  // only read
+  a.dlogits = dlogits;
+  a.dstride = dlogits_stride;
+  a.scale = grad_scale;
+  cudaStream_t s = (cudaStream_t)stream;
+  trace_begin(s);
+  const int rc = in->dtype == TBE_F32   ? launch_grad<TBE_F32>(a, s)
+                 : in->dtype == TBE_F16 ? launch_grad<TBE_F16>(a, s)
+                                        : launch_grad<TBE_BF16>(a, s);
+  trace_mark(s, "preference_grad");
+  return rc;
+}
+
+}  // extern "C"
