@@ -388,10 +388,9 @@ int tbe_backward_reduce(const tbe_plan* plan, const tbe_optimizer* opt, void* we
  *                     allowed.  Broken offsets set TBE_DEV_BAD_OFFSETS;
  *                     results are then unspecified, accesses in bounds
  *   h0              : device fp32 [sequences, channels] or NULL
- * Limits: tokens < 2^38, channels <= 2^20, ceil(tokens / TBE_SCAN_TILE) *
- * ceil(channels / 32) < 2^31.
+ * Limits: tokens < 2^38, channels <= 2^20.
  */
-#define TBE_SCAN_TILE 128 /* tokens between two saved states */
+#define TBE_SCAN_STEP 8 /* tokens between two saved states */
 typedef struct tbe_scan_inputs {
   int64_t tokens;
   int32_t sequences;
@@ -411,11 +410,12 @@ typedef struct tbe_scan_inputs {
 } tbe_scan_inputs;
 
 /* Saved states per channel for a batch of `tokens`: ceil(tokens /
- * TBE_SCAN_TILE), at least 1. */
+ * TBE_SCAN_STEP), at least 1. */
 int64_t tbe_gated_scan_states(int64_t tokens);
-/* Workspace (device, 256-byte aligned; no initialisation needed) of
- * tbe_gated_scan (backward = 0) or tbe_gated_scan_backward (1). */
-size_t tbe_gated_scan_workspace_bytes(int64_t tokens, int32_t channels, int32_t backward);
+/* Workspace (device, 256-byte aligned; no initialisation needed; 0 bytes for
+ * the smallest batches) of tbe_gated_scan (backward = 0) or
+ * tbe_gated_scan_backward (1) on the current device. */
+size_t tbe_gated_scan_workspace_bytes(int64_t tokens, int32_t channels, int32_t dtype, int32_t backward);
 
 /*   h       : device [tokens, channels] of dtype, h_stride elements from
  *             token to token: every h_t, rounded once
@@ -424,7 +424,7 @@ size_t tbe_gated_scan_workspace_bytes(int64_t tokens, int32_t channels, int32_t 
  *   states  : device fp32 [tbe_gated_scan_states(tokens), channels] or NULL:
  *             what the backward needs of the forward
  * Errors: TBE_ERR_INVALID_ARG, TBE_ERR_UNSUPPORTED (limits, alignment),
- * TBE_ERR_WORKSPACE, TBE_ERR_CUDA; TBE_DEV_BAD_OFFSETS, TBE_DEV_TIMEOUT. */
+ * TBE_ERR_WORKSPACE, TBE_ERR_CUDA; TBE_DEV_BAD_OFFSETS. */
 int tbe_gated_scan(const tbe_scan_inputs* in, void* h, int64_t h_stride, float* h_last, float* states,
                    void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
 

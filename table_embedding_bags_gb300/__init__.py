@@ -526,6 +526,6 @@ def version() -> str:
 
 
 from . import training  # noqa: E402  (the training operators beside the tables; uses this module's helpers)
-from .training import (TBE_ADAMW_BLOCK, TBE_SCAN_TILE, AdamWPlan, GatedScan, GatedScanGrads,  # noqa: E402, F401
+from .training import (TBE_ADAMW_BLOCK, TBE_SCAN_STEP, AdamWPlan, GatedScan, GatedScanGrads,  # noqa: E402, F401
                        PreferenceLoss, tbe_adamw_state, tbe_adamw_step, tbe_gated_scan, tbe_gated_scan_backward,
                        tbe_gated_scan_step, tbe_preference_loss, tbe_preference_loss_backward)
