@@ -9,9 +9,9 @@
 // is cut (its state enters as a term of its own), so the work splits into
 // equal runs of the token axis whatever the lengths are.
 //
-// A warp takes a run of tokens and 128 bytes of channels (a lane one fp32 or
-// two half-precision ones); a block's warps take neighbouring runs.  h over a
-// run is the linear map h_out = A h_in + B, so two passes do it:
+// A warp takes a run of tokens and 32 channels, a block's warps neighbouring
+// runs.  h over a run is the linear map h_out = A h_in + B, so two passes do
+// it:
 //  - maps: each run's map (only from the last start in it on, if there is
 //    one), joined over the block;
 //  - apply: each block joins the maps of the blocks before it, back to the
@@ -44,9 +44,11 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kStep = TBE_SCAN_STEP;  // tokens per step (and between saved states)
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBlocksPerSm = 2;
-constexpr int kRow = 128;            // bytes of a warp's row
-constexpr int kBox = kStep * kRow;   // one input's bytes of a step
+// blocks that stay resident on an SM: the forward fits 80 registers, the
+// backward would spill there
+template <bool BACK>
+constexpr int kBlocksPerSm = BACK ? 2 : 3;
+constexpr int kPairs = kStep / 2;  // neighbouring tokens of a step, two at a time
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct ScanArgs {
@@ -63,7 +65,6 @@ struct ScanArgs {
   int32_t run;      // tokens per warp, a multiple of kStep
   int32_t blocks;   // along the tokens
   int32_t cblocks;  // along the channels
-  int32_t pairs;    // half precision: every row of every array starts on 4 bytes
   int32_t copy;     // bytes per asynchronous copy: 16, 4, or 0 (plain loads)
   int64_t Cp;       // channels filled up to whole warps
   const float* h0;  // [S, C] or null
@@ -154,16 +155,31 @@ template <typename T>
 struct Decay {
   T a, q;
 };
-__device__ __forceinline__ Decay<Two> decay_near(Two u) {
-  Two p = fma2(u, two(-1.f / 720.f), two(1.f / 120.f));
-  p = fma2(u, p, two(-1.f / 24.f));
-  p = fma2(u, p, two(1.f / 6.f));
-  p = fma2(u, p, two(-0.5f));
-  p = fma2(u, p, two(1.f));
-  const Two n = u * p;
+// The constants of two-wide arithmetic, made once per thread: an instruction
+// takes them from registers only, and the compiler would otherwise move them
+// there again at each use.
+struct Constants {
+  Two one, minus_log2e, c5, c4, c3, c2, c1, c0;
+  static __device__ __forceinline__ Two keep(float f) {
+    Two t = two(f);
+    asm volatile("" : "+l"(t.v));
+    return t;
+  }
+  __device__ __forceinline__ Constants()
+      : one(keep(1.f)), minus_log2e(keep(-kLog2e)), c5(keep(1.f / 720.f)), c4(keep(-1.f / 120.f)), c3(keep(1.f / 24.f)),
+        c2(keep(-1.f / 6.f)), c1(keep(0.5f)), c0(keep(-1.f)) {}
+};
+__device__ __forceinline__ Two negative(Two t) { return two(-lo(t), -hi(t)); }
+__device__ __forceinline__ Decay<Two> decay_near(Two u, const Constants& k) {
+  Two p = fma2(u, k.c5, k.c4);
+  p = fma2(u, p, k.c3);
+  p = fma2(u, p, k.c2);
+  p = fma2(u, p, k.c1);
+  p = fma2(u, p, k.c0);
+  const Two m = u * p;  // a - 1
   Decay<Two> d;
-  d.a = fma2(n, two(-1.f), two(1.f));
-  d.q = n * fma2(n, two(-1.f), two(2.f));
+  d.a = m + k.one;
+  d.q = negative(m) * (d.a + k.one);
   return d;
 }
 __device__ __forceinline__ Decay<float> decay_of(float u) {
@@ -199,64 +215,46 @@ __device__ __forceinline__ float speed_of(const ScanArgs& a, int64_t c) {
 // the factors may not be told apart from infinity, and the run is done again
 // by gates_any.
 constexpr float kTop = 1e36f;
-__device__ __forceinline__ void gates_near(Two r, Two g, Two& sr, Two& sg, float& top) {
-  const Two pr = ex2(r * two(-kLog2e)) + two(1.f), pg = ex2(g * two(-kLog2e)) + two(1.f);
+__device__ __forceinline__ void gates_near(Two r, Two g, const Constants& k, Two& sr, Two& sg, float& top) {
+  const Two pr = ex2(r * k.minus_log2e) + k.one, pg = ex2(g * k.minus_log2e) + k.one;
   const Two product = pr * pg, inv = rcp(product);
   sr = inv * pg;
   sg = inv * pr;
-  top = fmaxf(top, fmaxf(lo(product), hi(product)));
+  top = fmaxf(fmaxf(top, lo(product)), hi(product));
 }
 __device__ __forceinline__ void gates_any(Two r, Two g, Two& sr, Two& sg) {
   sr = two(sigmoid(lo(r)), sigmoid(hi(r)));
   sg = two(sigmoid(lo(g)), sigmoid(hi(g)));
 }
 
-// A lane's channels: one fp32 or two half-precision ones, 4 bytes.  A Pair is
-// what two-wide arithmetic works on: a token's two channels, or two
-// neighbouring tokens of one fp32 channel.
 template <int DT>
-struct Lane {
-  static constexpr int kVec = DT == TBE_F32 ? 1 : 2;
-  static constexpr int kSize = DT == TBE_F32 ? 4 : 2;
-  static constexpr int kPairs = kStep * kVec / 2;  // of a step
-  static constexpr int kChannels = 32 * kVec;      // of a warp
-};
-template <int DT>
-__device__ __forceinline__ float2 halves(uint32_t v) {
-  if (DT == TBE_BF16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&v));
-}
-// Token j, channel v of an array of pairs.
-template <int DT>
-__device__ __forceinline__ float element(const Two* t, int j, int v) {
-  if (DT == TBE_F32) return j & 1 ? hi(t[j >> 1]) : lo(t[j >> 1]);
-  return v ? hi(t[j]) : lo(t[j]);
-}
-
+constexpr int kSize = DT == TBE_F32 ? 4 : 2;
 template <int DT>
 __device__ __forceinline__ const uint8_t* at(const void* p, int64_t e) {
-  return static_cast<const uint8_t*>(p) + e * Lane<DT>::kSize;
+  return static_cast<const uint8_t*>(p) + e * kSize<DT>;
 }
 template <int DT>
 __device__ __forceinline__ uint8_t* at(void* p, int64_t e) {
-  return static_cast<uint8_t*>(p) + e * Lane<DT>::kSize;
+  return static_cast<uint8_t*>(p) + e * kSize<DT>;
 }
-
-// A lane's word of a token straight from memory, for arrays that TMA cannot
-// read (not on 16 bytes): in one piece, or half by half.
+// An element's bits, and as a number.
 template <int DT>
-__device__ __forceinline__ uint32_t load_word(const uint8_t* p, bool pairs, int left) {
-  if (DT == TBE_F32) return left > 0 ? *reinterpret_cast<const uint32_t*>(p) : 0;
-  if (pairs && left > 1) return *reinterpret_cast<const uint32_t*>(p);
-  uint32_t v = left > 0 ? *reinterpret_cast<const uint16_t*>(p) : 0;
-  if (left > 1) v |= (uint32_t) * reinterpret_cast<const uint16_t*>(p + 2) << 16;
-  return v;
+__device__ __forceinline__ uint32_t load_bits(const uint8_t* p) {
+  if (DT == TBE_F32) return *reinterpret_cast<const uint32_t*>(p);
+  return *reinterpret_cast<const uint16_t*>(p);
 }
-// Stores a token's channels (`left` of them lie inside the array).
 template <int DT>
-__device__ __forceinline__ void store_word(uint8_t* p, bool pairs, int left, float a, float b) {
+__device__ __forceinline__ float number(uint32_t b) {
+  if (DT == TBE_F32) return __uint_as_float(b);
+  if (DT == TBE_BF16) return __uint_as_float(b << 16);
+  return __half2float(__ushort_as_half((unsigned short)b));
+}
+// Stores a pair's two tokens; `both`: the second lies inside the batch.
+template <int DT>
+__device__ __forceinline__ void store_pair(uint8_t* p, int64_t row, float a, float b, bool one, bool both) {
   if (DT == TBE_F32) {
-    if (left > 0) *reinterpret_cast<float*>(p) = a;
+    if (one) *reinterpret_cast<float*>(p) = a;
+    if (both) *reinterpret_cast<float*>(p + row) = b;
     return;
   }
   uint32_t v;
@@ -267,13 +265,10 @@ __device__ __forceinline__ void store_word(uint8_t* p, bool pairs, int left, flo
     const __half2 h = __floats2half2_rn(a, b);
     v = *reinterpret_cast<const uint32_t*>(&h);
   }
-  if (pairs && left > 1) {
-    *reinterpret_cast<uint32_t*>(p) = v;
-  } else {
-    if (left > 0) *reinterpret_cast<uint16_t*>(p) = (uint16_t)v;
-    if (left > 1) *reinterpret_cast<uint16_t*>(p + 2) = (uint16_t)(v >> 16);
-  }
+  if (one) *reinterpret_cast<uint16_t*>(p) = (uint16_t)v;
+  if (both) *reinterpret_cast<uint16_t*>(p + row) = (uint16_t)(v >> 16);
 }
+__device__ __forceinline__ float element(const Two* t, int j) { return j & 1 ? hi(t[j >> 1]) : lo(t[j >> 1]); }
 
 // The linear map of a run of tokens; A < 0: it does not depend on what comes in.
 struct Map {
@@ -345,11 +340,14 @@ struct Events {
   int32_t s;
   int64_t first, end;  // of the sequence looked up last
   int32_t owner;
-  __device__ __forceinline__ Events() : starts(0), ends(0), s(0), first(0), end(-1), owner(0) {}
+  int32_t quiet;  // steps to come that lie inside it
+  __device__ __forceinline__ Events() : starts(0), ends(0), s(0), first(0), end(-1), owner(0), quiet(0) {}
   __device__ __forceinline__ void find(Cursor& cur, int64_t t, int count, bool down, int lane) {
     starts = ends = 0;
-    s = owner;
-    if (first < t && t + count < end) return;
+    if (quiet > 0) {
+      --quiet;
+      return;
+    }
     for (int j = 0; j < count;) {
       const int64_t at = t + j;
       owner = (int32_t)cur.owner(at, down, first, end);
@@ -361,148 +359,208 @@ struct Events {
       if (lane >= j && lane < next) s = owner;
       j = next;
     }
-    if (down && count > 0) owner = (int32_t)cur.owner(t, true, first, end);  // goes on below
+    if (down) cur.owner(t, true, first, end);  // the sequence that goes on below
+    // later steps t' with t' + kStep < end (downwards: first < t')
+    const int64_t room = down ? (t - first - 1) / kStep : (end - t - kStep - 1) / kStep;
+    quiet = room < 0 ? 0 : (room < (1 << 30) ? (int)room : 1 << 30);
   }
   __device__ __forceinline__ int64_t sequence(int j) const { return __shfl_sync(kFull, s, j); }
 };
 
-// A warp's ring.  Slot layout: kBox bytes per input, then (backward) the
-// states of the step's start.
-template <int DT, int INPUTS, int SLOTS, bool STATES>
+// A warp's ring.  A slot holds kStep tokens of 32 channels of each input, then
+// (DOWN) the states that the step starts from.  fill() asks for the next
+// step, upwards or downwards from where the ring was set.  WIDE: rows start
+// on 16 bytes and channels come in whole 16-byte pieces; otherwise a copy is
+// of 4 bytes, or (half precision at odd places) an element at a time.
+template <int DT, int INPUTS, int SLOTS, bool DOWN, bool WIDE>
 struct Ring {
-  static constexpr int kSlot = INPUTS * kBox + (STATES ? 256 : 0);
+  static constexpr int kRow = 32 * kSize<DT>, kBox = kStep * kRow;
+  static constexpr int kSlot = INPUTS * kBox + (DOWN ? 128 : 0);
   static constexpr int kBytes = SLOTS * kSlot;
-  uint8_t* mem;
-  const void* in[INPUTS];
-  int64_t stride[INPUTS];
+  static constexpr int kLanes = kRow / 16;  // of a row, 16 bytes each
+  const uint8_t* mem;
+  const uint8_t* src[INPUTS];  // this lane's first piece of the next step
+  int64_t row[INPUTS];         // bytes between tokens
+  const float* state;
   const ScanArgs& a;
-  int64_t cb;  // the warp's first channel
+  uint32_t base;  // of slot 0, in shared memory
+  int bytes;      // of a lane's piece inside the array
   int lane;
+  int read, write;  // bytes from slot 0: the oldest step, the next to be filled
 
-  __device__ __forceinline__ Ring(const ScanArgs& args, uint8_t* m, int64_t c, int l) : mem(m), a(args), cb(c), lane(l) {}
-
-  static __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  __device__ __forceinline__ Ring(const ScanArgs& args, uint8_t* m, int64_t cb, int l)
+      : mem(m), state(nullptr), a(args), base(smem_u32(m)), lane(l), read(0), write(0) {
+    const int left = (int)((a.C - cb) * kSize<DT> < kRow ? (a.C - cb) * kSize<DT> : kRow);
+    const int piece = WIDE ? 16 : a.copy == 4 ? 4 : kSize<DT>;
+    const int b = left - col();
+    bytes = b < 0 ? 0 : (b < piece ? b : piece);
   }
-  static __device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  // the lane's place in a row, and the first row it copies
+  __device__ __forceinline__ int col() const {
+    return WIDE ? lane % kLanes * 16 : a.copy == 4 ? lane % (kRow / 4) * 4 : lane * kSize<DT>;
   }
-
-  // Asks for the step of tokens t .. t + count - 1 (count may be 0: nothing
-  // is read).  Tokens and channels outside the batch read as 0.
-  __device__ __forceinline__ void fill(int slot, int64_t t, int count) {
-    constexpr int kSize = Lane<DT>::kSize;
-    uint8_t* to = mem + slot * kSlot;
-    const int left = (int)((a.C - cb) * kSize < kRow ? (a.C - cb) * kSize : kRow);  // bytes of a row
+  __device__ __forceinline__ int first_row() const { return WIDE ? lane / kLanes : a.copy == 4 ? lane / (kRow / 4) : 0; }
+  __device__ __forceinline__ void input(int i, const void* p, int64_t stride, int64_t t, int64_t cb) {
+    row[i] = stride * kSize<DT>;
+    src[i] = at<DT>(p, t * stride + cb) + first_row() * row[i] + col();
+  }
+  static __device__ __forceinline__ void copy16(uint32_t dst, const void* from, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
+  }
+  static __device__ __forceinline__ void copy4(uint32_t dst, const void* from, int n) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
+  }
+  // `count` tokens of the step lie inside the run (0: nothing is read); what
+  // lies outside, or outside the channels, reads as 0.
+  __device__ __forceinline__ void fill(int count) {
+    const uint32_t to = base + write;
+    const bool whole = count == kStep;
 #pragma unroll
     for (int i = 0; i < INPUTS; ++i) {
-      const uint8_t* p = at<DT>(in[i], t * stride[i] + cb);
-      const int64_t row_bytes = stride[i] * kSize;
-      if (a.copy == 16) {
+      if (WIDE) {
+        constexpr int kRows = 32 / kLanes;
 #pragma unroll
-        for (int k = 0; k < kStep / 4; ++k) {
-          const int row = k * 4 + (lane >> 3), col = (lane & 7) * 16;
-          const int n = row < count ? (left - col < 0 ? 0 : (left - col < 16 ? left - col : 16)) : 0;
-          copy16(smem_u32(to + i * kBox + row * kRow + col), n > 0 ? p + row * row_bytes + col : in[i], n);
+        for (int k = 0; k < kStep / kRows; ++k) {
+          const uint32_t dst = to + i * kBox + k * 512 + lane * 16;
+          const uint8_t* from = src[i] + k * kRows * row[i];
+          if (whole) {
+            copy16(dst, from, bytes);
+          } else {
+            const int n = k * kRows + first_row() < count ? bytes : 0;
+            copy16(dst, n ? from : a.x, n);
+          }
         }
       } else if (a.copy == 4) {
+        constexpr int kRows = 128 / kRow;
+        const uint8_t* from = src[i];
 #pragma unroll
-        for (int row = 0; row < kStep; ++row) {
-          const int col = lane * 4;
-          const int n = row < count ? (left - col < 0 ? 0 : (left - col < 4 ? left - col : 4)) : 0;
-          copy4(smem_u32(to + i * kBox + row * kRow + col), n > 0 ? p + row * row_bytes + col : in[i], n);
+        for (int k = 0; k < kStep / kRows; ++k) {
+          const int n = whole || k * kRows + first_row() < count ? bytes : 0;
+          copy4(to + i * kBox + k * 128 + lane * 4, n ? from : a.x, n);
+          from += kRows * row[i];
         }
       } else {
         uint32_t w[kStep];
 #pragma unroll
-        for (int row = 0; row < kStep; ++row)
-          w[row] = row < count ? load_word<DT>(p + row * row_bytes + lane * 4, false, (left - lane * 4) / kSize) : 0;
+        for (int k = 0; k < kStep; ++k) w[k] = k < count && bytes ? load_bits<DT>(src[i] + k * row[i]) : 0;
 #pragma unroll
-        for (int row = 0; row < kStep; ++row) *reinterpret_cast<uint32_t*>(to + i * kBox + row * kRow + lane * 4) = w[row];
+        for (int k = 0; k < kStep; ++k)
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + i * kBox + k * kRow + lane * 2), "h"((uint16_t)w[k]) : "memory");
       }
+      src[i] += (DOWN ? -kStep : kStep) * row[i];
     }
-    if (STATES) {
-#pragma unroll
-      for (int v = 0; v < Lane<DT>::kVec; ++v) {
-        const int64_t c = cb + v * 32 + lane;
-        const bool ok = count > 0 && c < a.C;
-        copy4(smem_u32(to + INPUTS * kBox + (v * 32 + lane) * 4), ok ? a.states + t / kStep * a.C + c : a.states, ok ? 4 : 0);
-      }
+    if (DOWN) {
+      const int n = count > 0 && state ? 4 : 0;
+      copy4(to + INPUTS * kBox + lane * 4, n ? (const void*)state : a.x, n);
+      if (state) state -= a.C;
     }
     cp_commit();
+    write = write + kSlot == kBytes ? 0 : write + kSlot;
   }
-  // All but the SLOTS - 1 newest steps have landed, for the whole warp.
+  // The oldest step has landed, for the whole warp.
   __device__ __forceinline__ void ready() const {
     cp_wait<SLOTS - 1>();
     __syncwarp();
   }
-  // The slot has been read by the whole warp.
-  __device__ __forceinline__ void done() const { __syncwarp(); }
-  __device__ __forceinline__ uint32_t word(int slot, int i, int j) const {
-    return *reinterpret_cast<const uint32_t*>(mem + slot * kSlot + i * kBox + j * kRow + lane * 4);
+  // It has been read by the whole warp: its slot takes another step.
+  __device__ __forceinline__ void done(int count) {
+    __syncwarp();
+    fill(count);
+    read = write;
+  }
+  __device__ __forceinline__ uint32_t bits(int i, int j) const {
+    return load_bits<DT>(mem + read + lane * kSize<DT> + (i * kBox + j * kRow));
   }
   // `again`: read anew where it was read before, so that nothing made from
   // it the first time is kept in registers for the second
-  __device__ __forceinline__ Two pair(int slot, int i, int p, bool again = false) const {
-    uint32_t w = DT == TBE_F32 ? word(slot, i, 2 * p) : word(slot, i, p), w1 = DT == TBE_F32 ? word(slot, i, 2 * p + 1) : 0;
-    if (again) asm volatile("" : "+r"(w), "+r"(w1));
-    if (DT == TBE_F32) return two(__uint_as_float(w), __uint_as_float(w1));
-    const float2 f = halves<DT>(w);
-    return two(f.x, f.y);
+  __device__ __forceinline__ Two pair(int i, int p, bool again = false) const {
+    uint32_t w0 = bits(i, 2 * p), w1 = bits(i, 2 * p + 1);
+    if (again) asm volatile("" : "+r"(w0), "+r"(w1));
+    return two(number<DT>(w0), number<DT>(w1));
   }
-  __device__ __forceinline__ float state(int slot, int v) const {
-    return *reinterpret_cast<const float*>(mem + slot * kSlot + INPUTS * kBox + (lane * Lane<DT>::kVec + v) * 4);
+  __device__ __forceinline__ float first_state() const {
+    return *reinterpret_cast<const float*>(mem + read + INPUTS * kBox + lane * 4);
   }
 };
-constexpr int kX = 2, kR = 0, kG = 1, kD = 3;  // inputs of the rings that hold them all
+
+// One output of a warp, a step at a time.  WIDE: gathered in shared memory and
+// written 16 bytes to a lane; otherwise each element on its own.
+template <int DT, bool DOWN, bool WIDE>
+struct Out {
+  static constexpr int kRow = 32 * kSize<DT>, kLanes = kRow / 16, kRows = 32 / kLanes;
+  uint8_t* to;    // this lane's first piece of the step
+  uint8_t* room;  // kStep rows of shared memory (WIDE)
+  int64_t row;
+  int lane;
+  bool on;
+  __device__ __forceinline__ Out(void* p, int64_t stride, int64_t t, int64_t cb, int32_t C, uint8_t* m, int l)
+      : room(m), row(stride * kSize<DT>), lane(l) {
+    const int col = WIDE ? l % kLanes * 16 : l * kSize<DT>;
+    on = cb * kSize<DT> + col < (int64_t)C * kSize<DT>;
+    to = at<DT>(p, t * stride + cb) + col + (WIDE ? l / kLanes * row : 0);
+  }
+  // pair q of the step (`n` tokens of it lie inside the batch)
+  __device__ __forceinline__ void put(int q, Two v, int n) {
+    if (WIDE) store_pair<DT>(room + lane * kSize<DT> + 2 * q * kRow, kRow, lo(v), hi(v), true, true);
+    else store_pair<DT>(to + 2 * q * row, row, lo(v), hi(v), on && 2 * q < n, on && 2 * q + 1 < n);
+  }
+  // the step is complete (the caller puts a __syncwarp before and after)
+  __device__ __forceinline__ void flush(int n) {
+    if (WIDE) {
+#pragma unroll
+      for (int k = 0; k < kStep / kRows; ++k)
+        if (on && k * kRows + lane / kLanes < n)
+          *reinterpret_cast<uint4*>(to + k * kRows * row) = *reinterpret_cast<const uint4*>(room + k * 512 + lane * 16);
+    }
+    to += (DOWN ? -kStep : kStep) * row;
+  }
+};
+constexpr int kR = 0, kG = 1, kX = 2, kD = 3;  // inputs of the rings that hold them all
 
 // A warp's place: its run of tokens and its lanes' channels.
 struct Place {
   int64_t t0, t1, c, cb;
-  int left;  // channels of the lane inside the array
+  bool on;  // the lane's channel lies inside the array
+  __device__ __forceinline__ int count(int64_t t) const { return t >= t1 || t < t0 ? 0 : (t1 - t < kStep ? (int)(t1 - t) : kStep); }
 };
-template <int DT>
 __device__ __forceinline__ Place place_of(const ScanArgs& a, int warp, int lane) {
   Place p;
   const int64_t k = blockIdx.x / a.cblocks;
-  p.cb = (int64_t)(blockIdx.x % a.cblocks) * Lane<DT>::kChannels;
-  p.c = p.cb + lane * Lane<DT>::kVec;
+  p.cb = (int64_t)(blockIdx.x % a.cblocks) * 32;
+  p.c = p.cb + lane;
   p.t0 = (k * kWarps + warp) * a.run;
   p.t1 = p.t0 + a.run < a.N ? p.t0 + a.run : a.N;
   if (p.t0 > p.t1) p.t0 = p.t1;
-  p.left = p.c >= a.C ? 0 : (a.C - p.c < 2 ? 1 : 2);
+  p.on = p.c < a.C;
   return p;
 }
 
-// The lane's decay rates; `near`: whether the whole warp's stay where the
+// The lane's decay rate; `near`: whether the whole warp's stay where the
 // series holds (at most kNear, as sigmoids do not pass 1).
-template <int DT>
-__device__ __forceinline__ Two speeds(const ScanArgs& a, const Place& p, bool& near) {
-  const float s0 = p.left > 0 ? speed_of(a, p.c) : 0.f;
-  const float s1 = DT == TBE_F32 ? s0 : (p.left > 1 ? speed_of(a, p.c + 1) : 0.f);
-  near = __all_sync(kFull, s0 < kNear && s1 < kNear);
-  return two(s0, s1);
+__device__ __forceinline__ Two speed_at(const ScanArgs& a, const Place& p, bool& near) {
+  const float s = p.on ? speed_of(a, p.c) : 0.f;
+  near = __all_sync(kFull, s < kNear);
+  return two(s);
 }
 
 // Sigmoids, decays a and 1 - a^2 of a step.
-template <int DT, typename RING>
-__device__ __forceinline__ void step_gates(const RING& ring, int slot, Two speed, bool near, Two* sr, Two* sg, Two* A,
-                                           Two* Q) {
-  constexpr int kP = Lane<DT>::kPairs;
+template <typename RING>
+__device__ __forceinline__ void step_gates(const RING& ring, const Constants& k, Two speed, bool near, Two* sr, Two* sg,
+                                           Two* A, Two* Q) {
   float top = 0.f;
   if (near) {
 #pragma unroll
-    for (int p = 0; p < kP; ++p) {
-      gates_near(ring.pair(slot, kR, p), ring.pair(slot, kG, p), sr[p], sg[p], top);
-      const Decay<Two> d = decay_near(speed * sr[p]);
+    for (int p = 0; p < kPairs; ++p) {
+      gates_near(ring.pair(kR, p), ring.pair(kG, p), k, sr[p], sg[p], top);
+      const Decay<Two> d = decay_near(speed * sr[p], k);
       A[p] = d.a;
       Q[p] = d.q;
     }
   }
   if (!__all_sync(kFull, near && top < kTop)) {
 #pragma unroll
-    for (int p = 0; p < kP; ++p) {
-      gates_any(ring.pair(slot, kR, p, true), ring.pair(slot, kG, p, true), sr[p], sg[p]);
+    for (int p = 0; p < kPairs; ++p) {
+      gates_any(ring.pair(kR, p, true), ring.pair(kG, p, true), sr[p], sg[p]);
       const Decay<Two> d = decay_any(speed * sr[p]);
       A[p] = d.a;
       Q[p] = d.q;
@@ -510,129 +568,125 @@ __device__ __forceinline__ void step_gates(const RING& ring, int slot, Two speed
   }
 }
 
-constexpr int kForwardSlots = 4, kBackwardSlots = 3, kBackMapSlots = 6;
+// Slots: as many as leave room for those blocks (at most 72 KB a block
+// forward, 108 KB backward).
 template <int DT>
-using ForwardRing = Ring<DT, 3, kForwardSlots, false>;
+constexpr int kForwardSlots = DT == TBE_F32 ? 2 : 4;
 template <int DT>
-using BackwardRing = Ring<DT, 4, kBackwardSlots, true>;
+constexpr int kBackwardSlots = DT == TBE_F32 ? 2 : 5;
 template <int DT>
-using BackMapRing = Ring<DT, 2, kBackMapSlots, false>;
+constexpr int kBackMapSlots = DT == TBE_F32 ? 4 : 6;
+template <int DT, bool WIDE>
+using ForwardRing = Ring<DT, 3, kForwardSlots<DT>, false, WIDE>;
+template <int DT, bool WIDE>
+using BackwardRing = Ring<DT, 4, kBackwardSlots<DT>, true, WIDE>;
+template <int DT, bool WIDE>
+using BackMapRing = Ring<DT, 2, kBackMapSlots<DT>, false, WIDE>;
+// shared memory of a warp, with room for its outputs
+template <int DT>
+constexpr int kForwardBytes = ForwardRing<DT, true>::kBytes + ForwardRing<DT, true>::kBox;
+template <int DT>
+constexpr int kBackwardBytes = BackwardRing<DT, true>::kBytes + 3 * BackwardRing<DT, true>::kBox;
+template <int DT>
+constexpr int kMapBytes(bool back) {
+  return back ? BackMapRing<DT, true>::kBytes : ForwardRing<DT, true>::kBytes;
+}
 
 // The map of a run, forward: h at its end from h at its start.  Only the
 // tokens from the run's last start on count.
-template <int DT>
-__device__ __forceinline__ void run_map(const ScanArgs& a, const Place& p, uint8_t* mem, Two speed, bool near, int lane,
-                                        Map* m) {
-  constexpr int VEC = Lane<DT>::kVec, kP = Lane<DT>::kPairs;
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) m[v] = Map{1.f, 0.f};
-  if (p.t0 >= p.t1) return;
+template <int DT, bool WIDE>
+__device__ __forceinline__ Map run_map(const ScanArgs& a, const Place& p, uint8_t* mem, Two speed, bool near, int lane) {
+  Map m{1.f, 0.f};
+  if (p.t0 >= p.t1) return m;
   Cursor cur(a, lane);
   int64_t first, end;
   const int64_t s = cur.owner(p.t1 - 1, true, first, end);
   const bool cut = first >= p.t0 && first < p.t1;
-  if (cut) {
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) m[v].B = a.h0 && v < p.left ? a.h0[s * a.C + p.c + v] : 0.f;
-  }
-  ForwardRing<DT> ring(a, mem, p.cb, lane);
-  ring.in[kX] = a.x, ring.in[kR] = a.r, ring.in[kG] = a.g;
-  ring.stride[kX] = a.sx, ring.stride[kR] = a.sr, ring.stride[kG] = a.sg;
+  if (cut && a.h0 && p.on) m.B = a.h0[s * a.C + p.c];
   const int64_t from = cut ? first : p.t0;
-  auto count = [&](int64_t t) { return t >= p.t1 ? 0 : (p.t1 - t < kStep ? (int)(p.t1 - t) : kStep); };
+  ForwardRing<DT, WIDE> ring(a, mem, p.cb, lane);
+  const Constants k;
+  ring.input(kR, a.r, a.sr, from, p.cb);
+  ring.input(kG, a.g, a.sg, from, p.cb);
+  ring.input(kX, a.x, a.sx, from, p.cb);
 #pragma unroll
-  for (int i = 0; i < kForwardSlots; ++i) ring.fill(i, from + i * kStep, count(from + i * kStep));
-  int slot = 0;
+  for (int i = 0; i < kForwardSlots<DT>; ++i) ring.fill(p.count(from + i * kStep));
   for (int64_t t = from; t < p.t1; t += kStep) {
     ring.ready();
-    Two sr[kP], sg[kP], A[kP], B[kP];
-    step_gates<DT>(ring, slot, speed, near, sr, sg, A, B);
+    Two sr[kPairs], sg[kPairs], A[kPairs], B[kPairs];
+    step_gates(ring, k, speed, near, sr, sg, A, B);
 #pragma unroll
-    for (int q = 0; q < kP; ++q) B[q] = root(B[q]) * sg[q] * ring.pair(slot, kX, q);
-    ring.done();
-    ring.fill(slot, t + kForwardSlots * kStep, count(t + kForwardSlots * kStep));
-    slot = slot + 1 == kForwardSlots ? 0 : slot + 1;
-    const int n = count(t);
+    for (int q = 0; q < kPairs; ++q) B[q] = root(B[q]) * sg[q] * ring.pair(kX, q);
+    ring.done(p.count(t + kForwardSlots<DT> * kStep));
+    const int n = p.count(t);
+    if (n < kStep) {  // tokens outside the run change nothing
 #pragma unroll
-    for (int j = 0; j < kStep; ++j) {
-      if (j < n) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          const float A_ = element<DT>(A, j, v);
-          m[v].B = fmaf(A_, m[v].B, element<DT>(B, j, v));
-          m[v].A *= A_;
-        }
+      for (int q = 0; q < kPairs; ++q) {
+        A[q] = two(2 * q < n ? lo(A[q]) : 1.f, 2 * q + 1 < n ? hi(A[q]) : 1.f);
+        B[q] = two(2 * q < n ? lo(B[q]) : 0.f, 2 * q + 1 < n ? hi(B[q]) : 0.f);
       }
     }
+#pragma unroll
+    for (int j = 0; j < kStep; ++j) m.B = fmaf(element(A, j), m.B, element(B, j));
+    const Two P = A[0] * A[1] * (A[2] * A[3]);
+    m.A *= lo(P) * hi(P);
   }
   cp_wait<0>();
-  if (cut) {
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) m[v].A = -1.f;
-  }
+  if (cut) m.A = -1.f;
+  return m;
 }
 
 // The map of a run, backward: a G at its start from a G behind its end.
 // Only the tokens up to the run's first end count.
-template <int DT>
-__device__ __forceinline__ void run_map_back(const ScanArgs& a, const Place& p, uint8_t* mem, Two speed, bool near,
-                                             int lane, Map* m) {
-  constexpr int VEC = Lane<DT>::kVec, kP = Lane<DT>::kPairs;
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) m[v] = Map{1.f, 0.f};
-  if (p.t0 >= p.t1) return;
+template <int DT, bool WIDE>
+__device__ __forceinline__ Map run_map_back(const ScanArgs& a, const Place& p, uint8_t* mem, Two speed, bool near, int lane) {
+  Map m{1.f, 0.f};
+  if (p.t0 >= p.t1) return m;
   Cursor cur(a, lane);
   int64_t first, end;
   const int64_t s = cur.owner(p.t0, false, first, end);
   const bool cut = end > p.t0 && end <= p.t1;
-  const int64_t stop = cut ? end : p.t1;
-  BackMapRing<DT> ring(a, mem, p.cb, lane);
-  ring.in[kR] = a.r, ring.in[1] = a.dh;
-  ring.stride[kR] = a.sr, ring.stride[1] = a.sdh;
-  auto count = [&](int64_t t) { return t >= stop ? 0 : (stop - t < kStep ? (int)(stop - t) : kStep); };
+  Place q = p;
+  if (cut) q.t1 = end;
+  BackMapRing<DT, WIDE> ring(a, mem, p.cb, lane);
+  const Constants k;
+  ring.input(0, a.r, a.sr, p.t0, p.cb);
+  ring.input(1, a.dh, a.sdh, p.t0, p.cb);
 #pragma unroll
-  for (int i = 0; i < kBackMapSlots; ++i) ring.fill(i, p.t0 + i * kStep, count(p.t0 + i * kStep));
-  int slot = 0;
-  for (int64_t t = p.t0; t < stop; t += kStep) {
+  for (int i = 0; i < kBackMapSlots<DT>; ++i) ring.fill(q.count(p.t0 + i * kStep));
+  for (int64_t t = p.t0; t < q.t1; t += kStep) {
     ring.ready();
-    Two A[kP], D[kP];
+    Two A[kPairs], D[kPairs];
     if (near) {
 #pragma unroll
-      for (int q = 0; q < kP; ++q) {
-        const Two e = ex2(ring.pair(slot, kR, q) * two(-kLog2e)) + two(1.f);
-        A[q] = decay_near(speed * rcp(e)).a;
-      }
+      for (int i = 0; i < kPairs; ++i)
+        A[i] = decay_near(speed * rcp(ex2(ring.pair(0, i) * k.minus_log2e) + k.one), k).a;
     } else {
 #pragma unroll
-      for (int q = 0; q < kP; ++q) {
-        const Two r = ring.pair(slot, kR, q);
-        A[q] = decay_any(speed * two(sigmoid(lo(r)), sigmoid(hi(r)))).a;
+      for (int i = 0; i < kPairs; ++i) {
+        const Two r = ring.pair(0, i);
+        A[i] = decay_any(speed * two(sigmoid(lo(r)), sigmoid(hi(r)))).a;
       }
     }
 #pragma unroll
-    for (int q = 0; q < kP; ++q) D[q] = ring.pair(slot, 1, q);
-    ring.done();
-    ring.fill(slot, t + kBackMapSlots * kStep, count(t + kBackMapSlots * kStep));
-    slot = slot + 1 == kBackMapSlots ? 0 : slot + 1;
-    const int n = count(t);
+    for (int i = 0; i < kPairs; ++i) D[i] = ring.pair(1, i);
+    ring.done(q.count(t + kBackMapSlots<DT> * kStep));
+    const int n = q.count(t);
+    if (n < kStep) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) A[i] = two(2 * i < n ? lo(A[i]) : 1.f, 2 * i + 1 < n ? hi(A[i]) : 1.f);
+    }
 #pragma unroll
     for (int j = 0; j < kStep; ++j) {
-      if (j < n) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          float d = element<DT>(D, j, v);
-          if (cut && t + j == stop - 1 && a.dh_last && v < p.left) d += a.dh_last[s * a.C + p.c + v];
-          m[v].A *= element<DT>(A, j, v);
-          m[v].B = fmaf(m[v].A, d, m[v].B);
-        }
-      }
+      float d = element(D, j);
+      if (cut && t + j == q.t1 - 1 && a.dh_last && p.on) d += a.dh_last[s * a.C + p.c];
+      m.A *= element(A, j);
+      m.B = fmaf(m.A, d, m.B);
     }
   }
   cp_wait<0>();
-  if (cut) {
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) m[v].A = -1.f;
-  }
+  if (cut) m.A = -1.f;
+  return m;
 }
 
 __device__ __forceinline__ float2 word_of(Map m) { return make_float2(m.A, m.B); }
@@ -640,108 +694,82 @@ __device__ __forceinline__ Map map_of(float2 w) { return Map{w.x, w.y}; }
 
 // The maps of every run and every block (scan order: BACK counts from the
 // last run down).
-template <int DT, bool BACK>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) maps_kernel(ScanArgs a) {
-  constexpr int VEC = Lane<DT>::kVec;
+template <int DT, bool BACK, bool WIDE>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm<BACK>) maps_kernel(ScanArgs a) {
   extern __shared__ __align__(128) uint8_t mem[];
-  __shared__ Map runs[kWarps][64];
+  __shared__ Map runs[kWarps][32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Place p = place_of<DT>(a, warp, lane);
+  const Place p = place_of(a, warp, lane);
   bool near;
-  const Two speed = speeds<DT>(a, p, near);
-  Map m[VEC];
-  if (BACK) run_map_back<DT>(a, p, mem + warp * BackMapRing<DT>::kBytes, speed, near, lane, m);
-  else run_map<DT>(a, p, mem + warp * ForwardRing<DT>::kBytes, speed, near, lane, m);
+  const Two speed = speed_at(a, p, near);
+  uint8_t* mine = mem + warp * kMapBytes<DT>(BACK);
+  const Map m = BACK ? run_map_back<DT, WIDE>(a, p, mine, speed, near, lane) : run_map<DT, WIDE>(a, p, mine, speed, near, lane);
   const int64_t k = blockIdx.x / a.cblocks;
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) {
-    runs[warp][lane * VEC + v] = m[v];
-    a.warp_map[(k * kWarps + warp) * a.Cp + p.c + v] = word_of(m[v]);
-  }
+  runs[warp][lane] = m;
+  a.warp_map[(k * kWarps + warp) * a.Cp + p.c] = word_of(m);
   __syncthreads();
   if (warp == 0) {
+    Map all = runs[BACK ? kWarps - 1 : 0][lane];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      Map all = runs[BACK ? kWarps - 1 : 0][lane * VEC + v];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) all = join(all, runs[BACK ? kWarps - 1 - w : w][lane * VEC + v]);
-      a.block_map[k * a.Cp + p.c + v] = word_of(all);
-    }
+    for (int w = 1; w < kWarps; ++w) all = join(all, runs[BACK ? kWarps - 1 - w : w][lane]);
+    a.block_map[k * a.Cp + p.c] = word_of(all);
   }
 }
 
-// What reaches a warp's run: the blocks before this one, in rounds of 64 from
-// the nearest on (eight to a warp), until nothing further back matters; then
-// the warps before this one.  Every thread of the block calls this.
-template <int DT, bool BACK>
-__device__ __forceinline__ void reach(const ScanArgs& a, const Place& p, int warp, int lane, float* in) {
-  constexpr int VEC = Lane<DT>::kVec;
-  __shared__ Map part[kWarps][64];
+// What reaches a warp's run: the blocks before this one, in rounds of 128
+// from the nearest on (sixteen to a warp), until nothing further back
+// matters; then the warps before this one.  Every thread of the block calls
+// this.
+template <bool BACK>
+__device__ __forceinline__ float reach(const ScanArgs& a, const Place& p, int warp, int lane) {
+  constexpr int kEach = 16;
+  __shared__ Map part[kWarps][32];
   const int64_t k = blockIdx.x / a.cblocks;
   const int64_t before = BACK ? a.blocks - 1 - k : k;  // blocks before this one in scan order
-  Map all[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) all[v] = Map{1.f, 0.f};
-  for (int64_t done = 0; done < before && !(all[0].A < 0.f); done += 8 * kWarps) {
-    // this warp's eight, farthest first, `done + 8 * warp` blocks away at least
-    Map m[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) m[v] = Map{1.f, 0.f};
-    float2 w[8][VEC];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t away = done + 8 * warp + 8 - j;  // 1: the neighbour
-      const int64_t b = BACK ? k + away : k - away;
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) w[j][v] = away <= before ? __ldcg(a.block_map + b * a.Cp + p.c + v) : make_float2(1.f, 0.f);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) m[v] = join(m[v], map_of(w[j][v]));
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) part[warp][lane * VEC + v] = m[v];
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      Map round = part[kWarps - 1][lane * VEC + v];
-#pragma unroll
-      for (int j = kWarps - 2; j >= 0; --j) round = join(round, part[j][lane * VEC + v]);
-      all[v] = join(round, all[v]);
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) in[v] = apply(all[v], 0.f);
-  float2 w[kWarps - 1][VEC];
+  float2 own[kWarps - 1];
 #pragma unroll
   for (int j = 0; j < kWarps - 1; ++j) {
     const int r = BACK ? kWarps - 1 - j : j;  // in scan order
     const bool mine = BACK ? r > warp : r < warp;
-#pragma unroll
-    for (int v = 0; v < VEC; ++v)
-      w[j][v] = mine ? __ldcg(a.warp_map + (k * kWarps + r) * a.Cp + p.c + v) : make_float2(1.f, 0.f);
+    own[j] = mine ? __ldcg(a.warp_map + (k * kWarps + r) * a.Cp + p.c) : make_float2(1.f, 0.f);
   }
+  Map all{1.f, 0.f};
+  for (int64_t done = 0; done < before && !(all.A < 0.f); done += kEach * kWarps) {
+    // this warp's share, farthest first
+    Map m{1.f, 0.f};
+    float2 w[kEach];
 #pragma unroll
-  for (int j = 0; j < kWarps - 1; ++j)
+    for (int j = 0; j < kEach; ++j) {
+      const int64_t away = done + kEach * warp + kEach - j;  // 1: the neighbour
+      const int64_t b = BACK ? k + away : k - away;
+      w[j] = away <= before ? __ldcg(a.block_map + b * a.Cp + p.c) : make_float2(1.f, 0.f);
+    }
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) in[v] = apply(map_of(w[j][v]), in[v]);
+    for (int j = 0; j < kEach; ++j) m = join(m, map_of(w[j]));
+    __syncthreads();
+    part[warp][lane] = m;
+    __syncthreads();
+    Map round = part[kWarps - 1][lane];
+#pragma unroll
+    for (int j = kWarps - 2; j >= 0; --j) round = join(round, part[j][lane]);
+    all = join(round, all);
+  }
+  float in = apply(all, 0.f);
+#pragma unroll
+  for (int j = 0; j < kWarps - 1; ++j) in = apply(map_of(own[j]), in);
+  return in;
 }
 
 // The same where one block holds all tokens: the warps' maps are made here.
-template <int DT, bool BACK>
-__device__ __forceinline__ void reach_alone(const Map* m, int warp, int lane, float* in) {
-  constexpr int VEC = Lane<DT>::kVec;
-  __shared__ Map runs[kWarps][64];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) runs[warp][lane * VEC + v] = m[v];
+template <bool BACK>
+__device__ __forceinline__ float reach_alone(Map m, int warp, int lane) {
+  __shared__ Map runs[kWarps][32];
+  runs[warp][lane] = m;
   __syncthreads();
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) {
-    in[v] = 0.f;
-    for (int j = BACK ? kWarps - 1 : 0; j != warp; j += BACK ? -1 : 1) in[v] = apply(runs[j][lane * VEC + v], in[v]);
-  }
+  float in = 0.f;
+  for (int j = BACK ? kWarps - 1 : 0; j != warp; j += BACK ? -1 : 1) in = apply(runs[j][lane], in);
+  return in;
 }
 
 // Empty sequences hand their states on (to[s] = from[s], 0 where there is no
@@ -773,193 +801,179 @@ __device__ __forceinline__ void empty_sequences(const ScanArgs& a, const float* 
 }
 
 // ALONE: the batch is one block's tokens, no maps kernel ran.
-template <int DT, bool ALONE>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) forward_kernel(ScanArgs a) {
-  constexpr int VEC = Lane<DT>::kVec, kP = Lane<DT>::kPairs;
+template <int DT, bool ALONE, bool WIDE>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm<false>) forward_kernel(ScanArgs a) {
   extern __shared__ __align__(128) uint8_t mem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Place p = place_of<DT>(a, warp, lane);
+  const Place p = place_of(a, warp, lane);
   bool near;
-  const Two speed = speeds<DT>(a, p, near);
-  float h[VEC];
-  if (ALONE) {
-    Map m[VEC];
-    run_map<DT>(a, p, mem + warp * ForwardRing<DT>::kBytes, speed, near, lane, m);
-    reach_alone<DT, false>(m, warp, lane, h);
-    __syncwarp();
-  }
-  ForwardRing<DT> ring(a, mem + warp * ForwardRing<DT>::kBytes, p.cb, lane);
-  ring.in[kX] = a.x, ring.in[kR] = a.r, ring.in[kG] = a.g;
-  ring.stride[kX] = a.sx, ring.stride[kR] = a.sr, ring.stride[kG] = a.sg;
-  auto count = [&](int64_t t) { return t >= p.t1 ? 0 : (p.t1 - t < kStep ? (int)(p.t1 - t) : kStep); };
+  const Two speed = speed_at(a, p, near);
+  uint8_t* mine = mem + warp * kForwardBytes<DT>;
+  float h = 0.f;
+  if (ALONE) h = reach_alone<false>(run_map<DT, WIDE>(a, p, mine, speed, near, lane), warp, lane);
+  ForwardRing<DT, WIDE> ring(a, mine, p.cb, lane);
+  ring.input(kR, a.r, a.sr, p.t0, p.cb);
+  ring.input(kG, a.g, a.sg, p.t0, p.cb);
+  ring.input(kX, a.x, a.sx, p.t0, p.cb);
 #pragma unroll
-  for (int i = 0; i < kForwardSlots; ++i) ring.fill(i, p.t0 + i * kStep, count(p.t0 + i * kStep));
+  for (int i = 0; i < kForwardSlots<DT>; ++i) ring.fill(p.count(p.t0 + i * kStep));
   empty_sequences(a, a.h0, a.h_last);
   if (!ALONE) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    reach<DT, false>(a, p, warp, lane, h);
+    h = reach<false>(a, p, warp, lane);
   }
   Cursor cur(a, lane);
   Events ev;
-  int slot = 0;
+  const Constants k;
+  Out<DT, false, WIDE> to(a.h, a.sh, p.t0, p.cb, a.C, mine + ForwardRing<DT, WIDE>::kBytes, lane);
+  float* state = a.states ? a.states + p.t0 / kStep * a.C + p.c : nullptr;
   for (int64_t t = p.t0; t < p.t1; t += kStep) {
-    const int n = count(t);
+    const int n = p.count(t);
     ev.find(cur, t, n, false, lane);
     ring.ready();
-    Two sr[kP], sg[kP], A[kP], B[kP];
-    step_gates<DT>(ring, slot, speed, near, sr, sg, A, B);
+    Two sr[kPairs], sg[kPairs], A[kPairs], B[kPairs];
+    step_gates(ring, k, speed, near, sr, sg, A, B);
 #pragma unroll
-    for (int q = 0; q < kP; ++q) B[q] = root(B[q]) * sg[q] * ring.pair(slot, kX, q);
-    ring.done();
-    ring.fill(slot, t + kForwardSlots * kStep, count(t + kForwardSlots * kStep));
-    slot = slot + 1 == kForwardSlots ? 0 : slot + 1;
-    if (a.states) {
-#pragma unroll
-      for (int v = 0; v < VEC; ++v)
-        if (v < p.left) a.states[t / kStep * a.C + p.c + v] = h[v];
+    for (int q = 0; q < kPairs; ++q) B[q] = root(B[q]) * sg[q] * ring.pair(kX, q);
+    ring.done(p.count(t + kForwardSlots<DT> * kStep));
+    if (state) {
+      if (p.on) *state = h;
+      state += a.C;
     }
-    uint8_t* to = at<DT>(a.h, t * a.sh + p.c);
-    const int64_t row = a.sh * Lane<DT>::kSize;
+    float out[kStep];
+    if ((ev.starts | ev.ends) == 0) {
 #pragma unroll
-    for (int j = 0; j < kStep; ++j) {
-      if (ev.starts >> j & 1) {
-        const int64_t s = ev.sequence(j);
+      for (int j = 0; j < kStep; ++j) out[j] = h = fmaf(element(A, j), h, element(B, j));
+    } else {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) h[v] = a.h0 && v < p.left ? a.h0[s * a.C + p.c + v] : 0.f;
-      }
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) h[v] = fmaf(element<DT>(A, j, v), h[v], element<DT>(B, j, v));
-      if (j < n) store_word<DT>(to + j * row, a.pairs, p.left, h[0], h[VEC - 1]);
-      if (ev.ends >> j & 1) {
-        const int64_t s = ev.sequence(j);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v)
-          if (v < p.left) a.h_last[s * a.C + p.c + v] = h[v];
+      for (int j = 0; j < kStep; ++j) {
+        if (ev.starts >> j & 1) {
+          const int64_t s = ev.sequence(j);
+          h = a.h0 && p.on ? a.h0[s * a.C + p.c] : 0.f;
+        }
+        out[j] = h = fmaf(element(A, j), h, element(B, j));
+        if (ev.ends >> j & 1) {
+          const int64_t s = ev.sequence(j);
+          if (p.on) a.h_last[s * a.C + p.c] = h;
+        }
       }
     }
+#pragma unroll
+    for (int q = 0; q < kPairs; ++q) to.put(q, two(out[2 * q], out[2 * q + 1]), n);
+    __syncwarp();
+    to.flush(n);  // the next step's ready() comes before the room is written again
   }
   cp_wait<0>();
 }
 
-template <int DT, bool ALONE>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) backward_kernel(ScanArgs a) {
-  constexpr int VEC = Lane<DT>::kVec, kP = Lane<DT>::kPairs;
+template <int DT, bool ALONE, bool WIDE>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm<true>) backward_kernel(ScanArgs a) {
   extern __shared__ __align__(128) uint8_t mem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Place p = place_of<DT>(a, warp, lane);
+  const Place p = place_of(a, warp, lane);
   bool near;
-  const Two speed = speeds<DT>(a, p, near);
-  float c[VEC], share[VEC];
-  if (ALONE) {
-    Map m[VEC];
-    run_map_back<DT>(a, p, mem + warp * BackwardRing<DT>::kBytes, speed, near, lane, m);
-    reach_alone<DT, true>(m, warp, lane, c);
-    __syncwarp();
-  }
-  BackwardRing<DT> ring(a, mem + warp * BackwardRing<DT>::kBytes, p.cb, lane);
-  ring.in[kX] = a.x, ring.in[kR] = a.r, ring.in[kG] = a.g, ring.in[kD] = a.dh;
-  ring.stride[kX] = a.sx, ring.stride[kR] = a.sr, ring.stride[kG] = a.sg, ring.stride[kD] = a.sdh;
+  const Two speed = speed_at(a, p, near);
+  uint8_t* mine = mem + warp * kBackwardBytes<DT>;
+  float c = 0.f;
+  Two sum = two(0.f);
+  if (ALONE) c = reach_alone<true>(run_map_back<DT, WIDE>(a, p, mine, speed, near, lane), warp, lane);
   // steps from the run's last one down
   const int64_t last = p.t0 < p.t1 ? p.t0 + (p.t1 - 1 - p.t0) / kStep * kStep : p.t0;
-  auto count = [&](int64_t t) { return t < p.t0 || t >= p.t1 ? 0 : (p.t1 - t < kStep ? (int)(p.t1 - t) : kStep); };
+  BackwardRing<DT, WIDE> ring(a, mine, p.cb, lane);
+  ring.input(kR, a.r, a.sr, last, p.cb);
+  ring.input(kG, a.g, a.sg, last, p.cb);
+  ring.input(kX, a.x, a.sx, last, p.cb);
+  ring.input(kD, a.dh, a.sdh, last, p.cb);
+  ring.state = p.on ? a.states + last / kStep * a.C + p.c : nullptr;
 #pragma unroll
-  for (int i = 0; i < kBackwardSlots; ++i) {
-    const int64_t t = last - (int64_t)i * kStep;
-    ring.fill(i, t < p.t0 ? p.t0 : t, count(t));
-  }
+  for (int i = 0; i < kBackwardSlots<DT>; ++i) ring.fill(p.count(last - i * kStep));
   empty_sequences(a, a.dh_last, a.dh0);
   if (!ALONE) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    reach<DT, true>(a, p, warp, lane, c);
+    c = reach<true>(a, p, warp, lane);
   }
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) share[v] = 0.f;
   Cursor cur(a, lane);
   Events ev;
-  int slot = 0;
-  if (p.t0 < p.t1) {
-    for (int64_t t = last; t >= p.t0; t -= kStep) {
-      const int n = count(t);
-      ev.find(cur, t, n, true, lane);
-      ring.ready();
-      Two sr[kP], sg[kP], A[kP], inv[kP], beta[kP];
-      step_gates<DT>(ring, slot, speed, near, sr, sg, A, beta);
-      // the states that the step's tokens find
-      float before[kStep][VEC], h[VEC];
+  uint8_t* room = mine + BackwardRing<DT, WIDE>::kBytes;
+  constexpr int kBox = BackwardRing<DT, WIDE>::kBox;
+  Out<DT, true, WIDE> px(a.dx, a.sdx, last, p.cb, a.C, room, lane);
+  Out<DT, true, WIDE> pr(a.dr, a.sdr, last, p.cb, a.C, room + kBox, lane);
+  Out<DT, true, WIDE> pg(a.dg, a.sdg, last, p.cb, a.C, room + 2 * kBox, lane);
+  const Constants k;
+  for (int64_t t = last; t >= p.t0 && p.t0 < p.t1; t -= kStep) {
+    const int n = p.count(t);
+    ev.find(cur, t, n, true, lane);
+    ring.ready();
+    Two sr[kPairs], sg[kPairs], A[kPairs], inv[kPairs], beta[kPairs], found[kPairs], G[kPairs];
+    step_gates(ring, k, speed, near, sr, sg, A, beta);
+    const bool plain = (ev.starts | ev.ends) == 0 && n == kStep;
+    // the states that the step's tokens find
+    float h = ring.first_state();
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) h[v] = ring.state(slot, v);
+    for (int q = 0; q < kPairs; ++q) {
+      // where 1 - a^2 is 0 the token takes nothing in, and its gate's slope
+      // u d beta / d u = u a^2 / beta goes to 0 with u
+      const Two safe = two(fmaxf(lo(beta[q]), 1e-37f), fmaxf(hi(beta[q]), 1e-37f));
+      inv[q] = inv_root(safe);
+      beta[q] = beta[q] * inv[q];
+      const Two b = beta[q] * sg[q] * ring.pair(kX, q);
+      float f[2];
 #pragma unroll
-      for (int q = 0; q < kP; ++q) {
-        // where 1 - a^2 is 0 the token takes nothing in, and its gate's slope
-        // u d beta / d u = u a^2 / beta goes to 0 with u
-        const Two safe = two(fmaxf(lo(beta[q]), 1e-37f), fmaxf(hi(beta[q]), 1e-37f));
-        inv[q] = inv_root(safe);
-        beta[q] = beta[q] * inv[q];
-        const Two b = beta[q] * sg[q] * ring.pair(slot, kX, q);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {  // the pair's tokens, or its channels
-          const int j = DT == TBE_F32 ? 2 * q + e : q, v = DT == TBE_F32 ? 0 : e;
-          if (ev.starts >> j & 1) {
-            const int64_t s = ev.sequence(j);
-            h[v] = a.h0 && v < p.left ? a.h0[s * a.C + p.c + v] : 0.f;
-          }
-          before[j][v] = h[v];
-          h[v] = fmaf(e ? hi(A[q]) : lo(A[q]), h[v], e ? hi(b) : lo(b));
+      for (int e = 0; e < 2; ++e) {
+        if (!plain && (ev.starts >> (2 * q + e) & 1)) {
+          const int64_t s = ev.sequence(2 * q + e);
+          h = a.h0 && p.on ? a.h0[s * a.C + p.c] : 0.f;
         }
+        f[e] = h;
+        h = fmaf(e ? hi(A[q]) : lo(A[q]), h, e ? hi(b) : lo(b));
       }
+      found[q] = two(f[0], f[1]);
+      G[q] = ring.pair(kD, q);
+    }
+    if (plain) {
 #pragma unroll
-      for (int q = kP - 1; q >= 0; --q) {
-        const Two x = ring.pair(slot, kX, q, true), dh = ring.pair(slot, kD, q);
-        float G[2];
+      for (int q = kPairs - 1; q >= 0; --q) {
+        const float g1 = hi(G[q]) + c, g0 = fmaf(hi(A[q]), g1, lo(G[q]));
+        c = lo(A[q]) * g0;
+        G[q] = two(g0, g1);
+      }
+    } else {
 #pragma unroll
-        for (int e = 1; e >= 0; --e) {
-          const int j = DT == TBE_F32 ? 2 * q + e : q, v = DT == TBE_F32 ? 0 : e;
-          G[e] = e ? hi(dh) : lo(dh);
+      for (int j = kStep - 1; j >= 0; --j) {
+        float g = element(G, j);
+        if (j < n) {
           if (ev.ends >> j & 1) {
             const int64_t s = ev.sequence(j);
-            if (a.dh_last && v < p.left) G[e] += a.dh_last[s * a.C + p.c + v];
-          } else if (j < n) {
-            G[e] += c[v];
+            if (a.dh_last && p.on) g += a.dh_last[s * a.C + p.c];
+          } else {
+            g += c;
           }
-          if (j < n) c[v] = (e ? hi(A[q]) : lo(A[q])) * G[e];
+          c = element(A, j) * g;
           if (ev.starts >> j & 1) {
             const int64_t s = ev.sequence(j);
-            if (a.dh0 && v < p.left) a.dh0[s * a.C + p.c + v] = c[v];
+            if (a.dh0 && p.on) a.dh0[s * a.C + p.c] = c;
           }
         }
-        const Two g2 = two(G[0], G[1]), minus = two(-1.f), one = two(1.f);
-        const Two ua = speed * sr[q] * A[q], sx = sg[q] * x;
-        const Two found = DT == TBE_F32 ? two(before[2 * q & 7][0], before[(2 * q + 1) & 7][0])
-                                        : two(before[q & 7][0], before[q & 7][VEC - 1]);
-        const Two w = g2 * ua * fma2(A[q] * inv[q], sx, minus * found);
-        const Two dx = g2 * beta[q] * sg[q], dg = dx * x * fma2(sg[q], minus, one), dr = w * fma2(sr[q], minus, one);
-#pragma unroll
-        for (int e = 0; e < (DT == TBE_F32 ? 2 : 1); ++e) {
-          const int j = DT == TBE_F32 ? 2 * q + e : q;
-          if (j < n) {
-            const int64_t tj = t + j;
-            store_word<DT>(at<DT>(a.dx, tj * a.sdx + p.c), a.pairs, p.left, e ? hi(dx) : lo(dx), hi(dx));
-            store_word<DT>(at<DT>(a.dr, tj * a.sdr + p.c), a.pairs, p.left, e ? hi(dr) : lo(dr), hi(dr));
-            store_word<DT>(at<DT>(a.dg, tj * a.sdg + p.c), a.pairs, p.left, e ? hi(dg) : lo(dg), hi(dg));
-            if (DT == TBE_F32) {
-              share[0] += e ? hi(w) : lo(w);
-            } else {
-              share[0] += lo(w);
-              share[VEC - 1] += hi(w);
-            }
-          }
-        }
+        G[j >> 1] = j & 1 ? two(lo(G[j >> 1]), g) : two(g, hi(G[j >> 1]));
       }
-      ring.done();
-      const int64_t next = t - kBackwardSlots * kStep;
-      ring.fill(slot, next < p.t0 ? p.t0 : next, count(next));
-      slot = slot + 1 == kBackwardSlots ? 0 : slot + 1;
     }
+#pragma unroll
+    for (int q = 0; q < kPairs; ++q) {
+      const Two x = ring.pair(kX, q, true);
+      const Two w = G[q] * (speed * sr[q]) * A[q] * fma2(A[q] * inv[q], sg[q] * x, negative(found[q]));
+      const Two dx = G[q] * beta[q] * sg[q], dg = dx * x * (k.one + negative(sg[q])), dr = w * (k.one + negative(sr[q]));
+      px.put(q, dx, n);
+      pr.put(q, dr, n);
+      pg.put(q, dg, n);
+      sum = sum + w;  // 0 behind the batch, where dh reads as 0
+    }
+    ring.done(p.count(t - kBackwardSlots<DT> * kStep));
+    px.flush(n);  // done() and the next step's ready() keep the warp together
+    pr.flush(n);
+    pg.flush(n);
   }
   cp_wait<0>();
-#pragma unroll
-  for (int v = 0; v < VEC; ++v)
-    if (v < p.left) a.partial[((int64_t)(blockIdx.x / a.cblocks) * kWarps + warp) * a.C + p.c + v] = share[v];
+  if (p.on) a.partial[((int64_t)(blockIdx.x / a.cblocks) * kWarps + warp) * a.C + p.c] = lo(sum) + hi(sum);
 }
 
 // ddecay = sigmoid(decay) / softplus(decay) * sum over the runs, 32 channels
@@ -987,37 +1001,20 @@ __global__ void __launch_bounds__(kSumWarps * 32)
 // One token of each of S sequences: the state moves on in place.
 template <int DT>
 __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a) {
-  constexpr int VEC = Lane<DT>::kVec;
-  const int64_t per_row = (a.C + VEC - 1) / VEC;
   const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  if (i >= per_row * a.S) return;
-  const int64_t s = i / per_row, c = (i - s * per_row) * VEC;
-  const int left = a.C - c < 2 ? 1 : 2;
-  const uint32_t x = load_word<DT>(at<DT>(a.x, s * a.sx + c), a.pairs, left);
-  const uint32_t r = load_word<DT>(at<DT>(a.r, s * a.sr + c), a.pairs, left);
-  const uint32_t g = load_word<DT>(at<DT>(a.g, s * a.sg + c), a.pairs, left);
-  float* state = a.h_last + s * a.C + c;
-  float h[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) {
-    h[v] = 0.f;
-    if (v < left) {
-      auto of = [&](uint32_t w) {
-        if (DT == TBE_F32) return __uint_as_float(w);
-        const float2 f = halves<DT>(w);
-        return v ? f.y : f.x;
-      };
-      const Decay<float> d = decay_of(speed_of(a, c + v) * sigmoid(of(r)));
-      h[v] = fmaf(d.a, state[v], root(d.q) * sigmoid(of(g)) * of(x));
-      state[v] = h[v];
-    }
-  }
-  store_word<DT>(at<DT>(a.h, s * a.sh + c), a.pairs, left, h[0], h[VEC - 1]);
+  if (i >= (int64_t)a.S * a.C) return;
+  const int64_t s = i / a.C, c = i - s * a.C;
+  const float x = number<DT>(load_bits<DT>(at<DT>(a.x, s * a.sx + c)));
+  const float r = number<DT>(load_bits<DT>(at<DT>(a.r, s * a.sr + c)));
+  const float g = number<DT>(load_bits<DT>(at<DT>(a.g, s * a.sg + c)));
+  const Decay<float> d = decay_of(speed_of(a, c) * sigmoid(r));
+  const float h = fmaf(d.a, a.h_last[i], root(d.q) * sigmoid(g) * x);
+  a.h_last[i] = h;
+  store_pair<DT>(at<DT>(a.h, s * a.sh + c), 0, h, h, true, false);
 }
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
-int64_t whole_channels(int32_t C) { return ((int64_t)C + 63) / 64 * 64; }
-int32_t channel_blocks(int32_t C, int32_t dtype) { return dtype == TBE_F32 ? (C + 31) / 32 : (C + 63) / 64; }
+int32_t channel_blocks(int32_t C) { return (C + 31) / 32; }
 
 // Tokens per warp: as many as give every warp that fits on the GPU one run,
 // in whole steps.  Up to kAlone tokens one block takes the whole batch (both
@@ -1026,8 +1023,8 @@ constexpr int64_t kAlone = 256;
 struct Split {
   int32_t run, blocks;
 };
-Split split_of(int64_t N, int32_t cblocks) {
-  const int64_t warps = (int64_t)sm_count() * kBlocksPerSm * kWarps / cblocks;
+Split split_of(int64_t N, int32_t cblocks, bool back) {
+  const int64_t warps = (int64_t)sm_count() * (back ? kBlocksPerSm<true> : kBlocksPerSm<false>) * kWarps / cblocks;
   const int64_t parts = N <= kAlone || warps < kWarps ? kWarps : warps / kWarps * kWarps;
   int64_t run = ((N + parts - 1) / parts + kStep - 1) / kStep * kStep;
   if (run < kStep) run = kStep;
@@ -1042,9 +1039,9 @@ Split split_of(int64_t N, int32_t cblocks) {
 struct Workspace {
   size_t block, warp, partial, bytes;
 };
-Workspace layout(int64_t N, int32_t C, int32_t dtype, bool backward) {
-  const Split sp = split_of(N, channel_blocks(C, dtype));
-  const size_t Cp = (size_t)whole_channels(C);
+Workspace layout(int64_t N, int32_t C, bool backward) {
+  const Split sp = split_of(N, channel_blocks(C), backward);
+  const size_t Cp = (size_t)channel_blocks(C) * 32;
   Workspace w;
   size_t at = 0;
   w.block = w.warp = 0;
@@ -1061,24 +1058,22 @@ Workspace layout(int64_t N, int32_t C, int32_t dtype, bool backward) {
 
 bool aligned_to(const void* p, int64_t stride_bytes, int n) { return ((uintptr_t)p & (n - 1)) == 0 && stride_bytes % n == 0; }
 
-// How rows may be read and written: bytes per asynchronous copy of an input,
-// and whether two half-precision channels can be stored at once.
+// How rows may be read: bytes per asynchronous copy of an input.
 void choose_access(ScanArgs& a, int32_t dtype) {
   const int size = dtype == TBE_F32 ? 4 : 2;
   auto all = [&](int n) {
     return aligned_to(a.x, a.sx * size, n) && aligned_to(a.r, a.sr * size, n) && aligned_to(a.g, a.sg * size, n) &&
            (!a.dh || aligned_to(a.dh, a.sdh * size, n));
   };
-  a.copy = all(16) ? 16 : all(4) ? 4 : 0;
-  a.pairs = a.copy != 0;  // the step kernel reads pairs too
-  if (dtype != TBE_F32 && a.h) a.pairs = a.pairs && aligned_to(a.h, a.sh * size, 4);
-  if (dtype != TBE_F32 && a.dh)
-    a.pairs = a.pairs && aligned_to(a.dx, a.sdx * size, 4) && aligned_to(a.dr, a.sdr * size, 4) && aligned_to(a.dg, a.sdg * size, 4);
+  auto out = [&](const void* p, int64_t stride) { return !p || aligned_to(p, stride * size, 16); };
+  a.copy = all(16) && a.C * size % 16 == 0 && out(a.h, a.sh) && out(a.dx, a.sdx) && out(a.dr, a.sdr) && out(a.dg, a.sdg)
+               ? 16
+               : all(4) ? 4 : 0;
 }
 
 template <typename K>
 int start(K kernel, unsigned grid, unsigned threads, size_t smem, bool after, cudaStream_t s, const ScanArgs& a) {
-  if (smem > 48 * 1024 &&
+  if (smem > 40 * 1024 &&  // beyond the default once the static slots are counted
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return TBE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -1094,27 +1089,30 @@ int start(K kernel, unsigned grid, unsigned threads, size_t smem, bool after, cu
   return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? check_launch() : TBE_ERR_CUDA;
 }
 
-template <int DT, bool BACK>
-int launch_scan(const ScanArgs& a, cudaStream_t s) {
-  constexpr size_t ring = kWarps * (size_t)(BACK ? BackwardRing<DT>::kBytes : ForwardRing<DT>::kBytes);
-  constexpr size_t map_ring = kWarps * (size_t)(BACK ? BackMapRing<DT>::kBytes : ForwardRing<DT>::kBytes);
-  static_assert(!BACK || ring >= map_ring, "the maps of a lone block use the same ring");
+template <int DT, bool BACK, bool WIDE>
+int launch_passes(const ScanArgs& a, cudaStream_t s) {
+  constexpr size_t bytes = kWarps * (size_t)(BACK ? kBackwardBytes<DT> : kForwardBytes<DT>);
+  constexpr size_t map_bytes = kWarps * (size_t)kMapBytes<DT>(BACK);
+  static_assert(bytes >= map_bytes, "the maps of a lone block use the same memory");
   const unsigned grid = (unsigned)a.blocks * (unsigned)a.cblocks;
   if (a.blocks == 1) {
-    if constexpr (BACK) return start(backward_kernel<DT, true>, grid, kThreads, ring, false, s, a);
-    else return start(forward_kernel<DT, true>, grid, kThreads, ring, false, s, a);
+    if constexpr (BACK) return start(backward_kernel<DT, true, WIDE>, grid, kThreads, bytes, false, s, a);
+    else return start(forward_kernel<DT, true, WIDE>, grid, kThreads, bytes, false, s, a);
   }
-  const int st = start(maps_kernel<DT, BACK>, grid, kThreads, map_ring, false, s, a);
+  const int st = start(maps_kernel<DT, BACK, WIDE>, grid, kThreads, map_bytes, false, s, a);
   if (st != TBE_OK) return st;
   trace_mark(s, BACK ? "gated_scan_maps_back" : "gated_scan_maps");
-  if constexpr (BACK) return start(backward_kernel<DT, false>, grid, kThreads, ring, true, s, a);
-  else return start(forward_kernel<DT, false>, grid, kThreads, ring, true, s, a);
+  if constexpr (BACK) return start(backward_kernel<DT, false, WIDE>, grid, kThreads, bytes, true, s, a);
+  else return start(forward_kernel<DT, false, WIDE>, grid, kThreads, bytes, true, s, a);
+}
+template <int DT, bool BACK>
+int launch_scan(const ScanArgs& a, cudaStream_t s) {
+  return a.copy == 16 ? launch_passes<DT, BACK, true>(a, s) : launch_passes<DT, BACK, false>(a, s);
 }
 
 template <int DT>
 int launch_step(const ScanArgs& a, cudaStream_t s) {
-  const int64_t n = (int64_t)a.S * ((a.C + Lane<DT>::kVec - 1) / Lane<DT>::kVec);
-  scan_step_kernel<DT><<<(unsigned)((n + 127) / 128), 128, 0, s>>>(a);
+  scan_step_kernel<DT><<<(unsigned)(((int64_t)a.S * a.C + 127) / 128), 128, 0, s>>>(a);
   return check_launch();
 }
 
@@ -1166,11 +1164,8 @@ ScanArgs args_of(const tbe_scan_inputs* in) {
   a.S = in->sequences;
   a.C = in->channels;
   a.h0 = in->h0;
-  a.cblocks = channel_blocks(in->channels, in->dtype);
-  const Split sp = split_of(in->tokens, a.cblocks);
-  a.run = sp.run;
-  a.blocks = sp.blocks;
-  a.Cp = whole_channels(in->channels);
+  a.cblocks = channel_blocks(in->channels);
+  a.Cp = (int64_t)a.cblocks * 32;
   return a;
 }
 
@@ -1181,8 +1176,11 @@ int check_jagged(const tbe_scan_inputs* in) {
   return TBE_OK;
 }
 
-int use_workspace(ScanArgs& a, int32_t dtype, bool backward, void* workspace, size_t bytes) {
-  const Workspace w = layout(a.N, a.C, dtype, backward);
+int use_workspace(ScanArgs& a, bool backward, void* workspace, size_t bytes) {
+  const Split sp = split_of(a.N, a.cblocks, backward);
+  a.run = sp.run;
+  a.blocks = sp.blocks;
+  const Workspace w = layout(a.N, a.C, backward);
   if (bytes < w.bytes) return TBE_ERR_WORKSPACE;
   if (w.bytes == 0) return TBE_OK;
   if (!workspace) return TBE_ERR_INVALID_ARG;
@@ -1203,9 +1201,9 @@ extern "C" {
 
 int64_t tbe_gated_scan_states(int64_t tokens) { return tokens < 1 ? 1 : (tokens + kStep - 1) / kStep; }
 
-size_t tbe_gated_scan_workspace_bytes(int64_t tokens, int32_t channels, int32_t dtype, int32_t backward) {
+size_t tbe_gated_scan_workspace_bytes(int64_t tokens, int32_t channels, int32_t backward) {
   if (tokens < 0 || channels < 1) return 0;
-  return layout(tokens, channels, dtype, backward != 0).bytes;
+  return layout(tokens, channels, backward != 0).bytes;
 }
 
 int tbe_gated_scan(const tbe_scan_inputs* in, void* h, int64_t h_stride, float* h_last, float* states,
@@ -1223,7 +1221,7 @@ int tbe_gated_scan(const tbe_scan_inputs* in, void* h, int64_t h_stride, float* 
   a.status = dev_status;
   cudaStream_t s = (cudaStream_t)stream;
   trace_begin(s);
-  st = use_workspace(a, in->dtype, false, workspace, workspace_bytes);
+  st = use_workspace(a, false, workspace, workspace_bytes);
   if (st != TBE_OK) return st;
   st = dispatch(a, in->dtype, kForward, s);
   trace_mark(s, "gated_scan");
@@ -1260,7 +1258,7 @@ int tbe_gated_scan_backward(const tbe_scan_inputs* in, const void* dh, int64_t d
   a.dh0 = out->dh0;
   a.status = dev_status;
   trace_begin(s);
-  st = use_workspace(a, in->dtype, true, workspace, workspace_bytes);
+  st = use_workspace(a, true, workspace, workspace_bytes);
   if (st != TBE_OK) return st;
   st = dispatch(a, in->dtype, kBackward, s);
   if (st != TBE_OK) return st;

@@ -60,7 +60,7 @@ def declare(lib):
     P, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     for name, res, args in [
         ("tbe_gated_scan_states", i64, [i64]),
-        ("tbe_gated_scan_workspace_bytes", sz, [i64, i32, i32, i32]),
+        ("tbe_gated_scan_workspace_bytes", sz, [i64, i32, i32]),
         ("tbe_gated_scan", ctypes.c_int, [P, P, i64, P, P, P, sz, P, P]),
         ("tbe_gated_scan_backward", ctypes.c_int, [P, P, i64, P, P, P, P, sz, P, P]),
         ("tbe_gated_scan_step", ctypes.c_int, [P, P, P, i64, P]),
@@ -187,7 +187,7 @@ def tbe_gated_scan(x, recur, gate, decay, offsets, h0=None, sharpness: float = 8
     states = None
     if want_states:
         states = torch.empty((lib.tbe_gated_scan_states(N), C), dtype=torch.float32, device=dev)
-    nbytes = lib.tbe_gated_scan_workspace_bytes(N, C, a.dtype, 0)
+    nbytes = lib.tbe_gated_scan_workspace_bytes(N, C, 0)
     ws = _workspace(nbytes, dev)
     _run(lib.tbe_gated_scan, "tbe_gated_scan", dev, stream, ctypes.byref(a), h.data_ptr(), h_stride,
          h_last.data_ptr(), _addr(states), _addr(ws), nbytes, _addr(dev_status))
@@ -216,7 +216,7 @@ def tbe_gated_scan_backward(dh, x, recur, gate, decay, offsets, states, h0=None,
     ddecay = torch.empty(C, dtype=torch.float32, device=dev)
     dh0 = None if h0 is None else torch.empty((S, C), dtype=torch.float32, device=dev)
     g = _ScanGrads(out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), *strides, ddecay.data_ptr(), _addr(dh0))
-    nbytes = lib.tbe_gated_scan_workspace_bytes(N, C, a.dtype, 1)
+    nbytes = lib.tbe_gated_scan_workspace_bytes(N, C, 1)
     ws = _workspace(nbytes, dev)
     _run(lib.tbe_gated_scan_backward, "tbe_gated_scan_backward", dev, stream, ctypes.byref(a), dh.data_ptr(),
          dh_stride, _addr(dh_last), states.data_ptr(), ctypes.byref(g), _addr(ws), nbytes, _addr(dev_status))
