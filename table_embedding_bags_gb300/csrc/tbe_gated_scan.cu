@@ -62,7 +62,7 @@ struct ScanArgs {
   int64_t N;
   int32_t S;
   int32_t C;
-  int32_t run;      // tokens per warp, a multiple of kStep
+  int32_t run;      // tokens per warp, whole slots of the rings
   int32_t blocks;   // along the tokens
   int32_t cblocks;  // along the channels
   int32_t copy;     // bytes per asynchronous copy: 16, 4, or 0 (plain loads)
@@ -367,18 +367,23 @@ struct Events {
   __device__ __forceinline__ int64_t sequence(int j) const { return __shfl_sync(kFull, s, j); }
 };
 
-// A warp's ring.  A slot holds kStep tokens of 32 channels of each input, then
-// (DOWN) the states that the step starts from.  fill() asks for the next
-// step, upwards or downwards from where the ring was set.  WIDE: rows start
+// A warp's ring.  A slot holds kTokens<DT> tokens of 32 channels of each input,
+// then (DOWN) the states that its steps start from.  Slots are filled upwards,
+// or downwards, from where the ring was set until the run's tokens are all
+// asked for.  WIDE: rows start
 // on 16 bytes and channels come in whole 16-byte pieces; otherwise a copy is
 // of 4 bytes, or (half precision at odd places) an element at a time.
+template <int DT>
+constexpr int kTokens = DT == TBE_F32 ? kStep : 2 * kStep;
 template <int DT, int INPUTS, int SLOTS, bool DOWN, bool WIDE>
 struct Ring {
-  static constexpr int kRow = 32 * kSize<DT>, kBox = kStep * kRow;
-  static constexpr int kSlot = INPUTS * kBox + (DOWN ? 128 : 0);
+  static constexpr int kTok = kTokens<DT>;
+  static constexpr int kRow = 32 * kSize<DT>, kBox = kTok * kRow;
+  static constexpr int kSlot = INPUTS * kBox + (DOWN ? kTok / kStep * 128 : 0);
   static constexpr int kBytes = SLOTS * kSlot;
   static constexpr int kLanes = kRow / 16;  // of a row, 16 bytes each
   const uint8_t* mem;
+  const uint8_t* now;
   const uint8_t* src[INPUTS];  // this lane's first piece of the next step
   int64_t row[INPUTS];         // bytes between tokens
   const float* state;
@@ -386,10 +391,12 @@ struct Ring {
   uint32_t base;  // of slot 0, in shared memory
   int bytes;      // of a lane's piece inside the array
   int lane;
-  int read, write;  // bytes from slot 0: the oldest step, the next to be filled
+  int read, write;  // bytes from slot 0: the oldest slot, the next to be filled
+  int left;         // tokens of the run that are not asked for yet
 
-  __device__ __forceinline__ Ring(const ScanArgs& args, uint8_t* m, int64_t cb, int l)
-      : mem(m), state(nullptr), a(args), base(smem_u32(m)), lane(l), read(0), write(0) {
+  // `tokens`: of the run; downwards the first slot takes what does not fill one
+  __device__ __forceinline__ Ring(const ScanArgs& args, uint8_t* m, int64_t cb, int l, int tokens)
+      : mem(m), now(m), state(nullptr), a(args), base(smem_u32(m)), lane(l), read(0), write(0), left(tokens) {
     const int left = (int)((a.C - cb) * kSize<DT> < kRow ? (a.C - cb) * kSize<DT> : kRow);
     const int piece = WIDE ? 16 : a.copy == 4 ? 4 : kSize<DT>;
     const int b = left - col();
@@ -410,17 +417,20 @@ struct Ring {
   static __device__ __forceinline__ void copy4(uint32_t dst, const void* from, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
   }
-  // `count` tokens of the step lie inside the run (0: nothing is read); what
-  // lies outside, or outside the channels, reads as 0.
-  __device__ __forceinline__ void fill(int count) {
+  // The next slot.  What lies outside the run (in the batch's last one), or
+  // outside the channels, reads as 0.
+  __device__ __forceinline__ void fill() {
+    int count = left < kTok ? left : kTok;
+    if (DOWN && left > kTok && left % kTok) count = left % kTok;
+    left -= count;
     const uint32_t to = base + write;
-    const bool whole = count == kStep;
+    const bool whole = count == kTok;
 #pragma unroll
     for (int i = 0; i < INPUTS; ++i) {
       if (WIDE) {
         constexpr int kRows = 32 / kLanes;
 #pragma unroll
-        for (int k = 0; k < kStep / kRows; ++k) {
+        for (int k = 0; k < kTok / kRows; ++k) {
           const uint32_t dst = to + i * kBox + k * 512 + lane * 16;
           const uint8_t* from = src[i] + k * kRows * row[i];
           if (whole) {
@@ -434,43 +444,46 @@ struct Ring {
         constexpr int kRows = 128 / kRow;
         const uint8_t* from = src[i];
 #pragma unroll
-        for (int k = 0; k < kStep / kRows; ++k) {
+        for (int k = 0; k < kTok / kRows; ++k) {
           const int n = whole || k * kRows + first_row() < count ? bytes : 0;
           copy4(to + i * kBox + k * 128 + lane * 4, n ? from : a.x, n);
           from += kRows * row[i];
         }
       } else {
-        uint32_t w[kStep];
+        uint32_t w[kTok];
 #pragma unroll
-        for (int k = 0; k < kStep; ++k) w[k] = k < count && bytes ? load_bits<DT>(src[i] + k * row[i]) : 0;
+        for (int k = 0; k < kTok; ++k) w[k] = k < count && bytes ? load_bits<DT>(src[i] + k * row[i]) : 0;
 #pragma unroll
-        for (int k = 0; k < kStep; ++k)
+        for (int k = 0; k < kTok; ++k)
           asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + i * kBox + k * kRow + lane * 2), "h"((uint16_t)w[k]) : "memory");
       }
-      src[i] += (DOWN ? -kStep : kStep) * row[i];
+      src[i] += (DOWN ? -kTok : kTok) * row[i];
     }
     if (DOWN) {
-      const int n = count > 0 && state ? 4 : 0;
-      copy4(to + INPUTS * kBox + lane * 4, n ? (const void*)state : a.x, n);
-      if (state) state -= a.C;
+#pragma unroll
+      for (int u = 0; u < kTok / kStep; ++u) {
+        const int n = u * kStep < count && state ? 4 : 0;
+        copy4(to + INPUTS * kBox + u * 128 + lane * 4, n ? (const void*)(state + (int64_t)u * a.C) : a.x, n);
+      }
+      if (state) state -= (int64_t)(kTok / kStep) * a.C;
     }
     cp_commit();
     write = write + kSlot == kBytes ? 0 : write + kSlot;
   }
-  // The oldest step has landed, for the whole warp.
+  // The oldest slot has landed, for the whole warp.
   __device__ __forceinline__ void ready() const {
     cp_wait<SLOTS - 1>();
     __syncwarp();
   }
-  // It has been read by the whole warp: its slot takes another step.
-  __device__ __forceinline__ void done(int count) {
+  // It has been read by the whole warp and takes other tokens.
+  __device__ __forceinline__ void done() {
     __syncwarp();
-    fill(count);
+    fill();
     read = write;
   }
-  __device__ __forceinline__ uint32_t bits(int i, int j) const {
-    return load_bits<DT>(mem + read + lane * kSize<DT> + (i * kBox + j * kRow));
-  }
+  // step u of the slot, of which the next reads are
+  __device__ __forceinline__ void step(int u) { now = mem + read + u * (kStep * kRow) + lane * kSize<DT>; }
+  __device__ __forceinline__ uint32_t bits(int i, int j) const { return load_bits<DT>(now + (i * kBox + j * kRow)); }
   // `again`: read anew where it was read before, so that nothing made from
   // it the first time is kept in registers for the second
   __device__ __forceinline__ Two pair(int i, int p, bool again = false) const {
@@ -478,8 +491,8 @@ struct Ring {
     if (again) asm volatile("" : "+r"(w0), "+r"(w1));
     return two(number<DT>(w0), number<DT>(w1));
   }
-  __device__ __forceinline__ float first_state() const {
-    return *reinterpret_cast<const float*>(mem + read + INPUTS * kBox + lane * 4);
+  __device__ __forceinline__ float first_state(int u) const {
+    return *reinterpret_cast<const float*>(mem + read + INPUTS * kBox + u * 128 + lane * 4);
   }
 };
 
@@ -521,7 +534,6 @@ constexpr int kR = 0, kG = 1, kX = 2, kD = 3;  // inputs of the rings that hold 
 struct Place {
   int64_t t0, t1, c, cb;
   bool on;  // the lane's channel lies inside the array
-  __device__ __forceinline__ int count(int64_t t) const { return t >= t1 || t < t0 ? 0 : (t1 - t < kStep ? (int)(t1 - t) : kStep); }
 };
 __device__ __forceinline__ Place place_of(const ScanArgs& a, int warp, int lane) {
   Place p;
@@ -570,23 +582,21 @@ __device__ __forceinline__ void step_gates(const RING& ring, const Constants& k,
 
 // Slots: as many as leave room for those blocks (at most 72 KB a block
 // forward, 108 KB backward).
+constexpr int kForwardSlots = 2;
+constexpr int kBackwardSlots = 2;
 template <int DT>
-constexpr int kForwardSlots = DT == TBE_F32 ? 2 : 4;
-template <int DT>
-constexpr int kBackwardSlots = DT == TBE_F32 ? 2 : 5;
-template <int DT>
-constexpr int kBackMapSlots = DT == TBE_F32 ? 4 : 6;
+constexpr int kBackMapSlots = DT == TBE_F32 ? 4 : 3;
 template <int DT, bool WIDE>
-using ForwardRing = Ring<DT, 3, kForwardSlots<DT>, false, WIDE>;
+using ForwardRing = Ring<DT, 3, kForwardSlots, false, WIDE>;
 template <int DT, bool WIDE>
-using BackwardRing = Ring<DT, 4, kBackwardSlots<DT>, true, WIDE>;
+using BackwardRing = Ring<DT, 4, kBackwardSlots, true, WIDE>;
 template <int DT, bool WIDE>
 using BackMapRing = Ring<DT, 2, kBackMapSlots<DT>, false, WIDE>;
 // shared memory of a warp, with room for its outputs
 template <int DT>
-constexpr int kForwardBytes = ForwardRing<DT, true>::kBytes + ForwardRing<DT, true>::kBox;
+constexpr int kForwardBytes = ForwardRing<DT, true>::kBytes + kStep * 32 * kSize<DT>;
 template <int DT>
-constexpr int kBackwardBytes = BackwardRing<DT, true>::kBytes + 3 * BackwardRing<DT, true>::kBox;
+constexpr int kBackwardBytes = BackwardRing<DT, true>::kBytes + 3 * kStep * 32 * kSize<DT>;
 template <int DT>
 constexpr int kMapBytes(bool back) {
   return back ? BackMapRing<DT, true>::kBytes : ForwardRing<DT, true>::kBytes;
@@ -604,32 +614,36 @@ __device__ __forceinline__ Map run_map(const ScanArgs& a, const Place& p, uint8_
   const bool cut = first >= p.t0 && first < p.t1;
   if (cut && a.h0 && p.on) m.B = a.h0[s * a.C + p.c];
   const int64_t from = cut ? first : p.t0;
-  ForwardRing<DT, WIDE> ring(a, mem, p.cb, lane);
+  int left = (int)(p.t1 - from);
+  ForwardRing<DT, WIDE> ring(a, mem, p.cb, lane, left);
   const Constants k;
   ring.input(kR, a.r, a.sr, from, p.cb);
   ring.input(kG, a.g, a.sg, from, p.cb);
   ring.input(kX, a.x, a.sx, from, p.cb);
 #pragma unroll
-  for (int i = 0; i < kForwardSlots<DT>; ++i) ring.fill(p.count(from + i * kStep));
-  for (int64_t t = from; t < p.t1; t += kStep) {
+  for (int i = 0; i < kForwardSlots; ++i) ring.fill();
+  while (left > 0) {
     ring.ready();
-    Two sr[kPairs], sg[kPairs], A[kPairs], B[kPairs];
-    step_gates(ring, k, speed, near, sr, sg, A, B);
+#pragma unroll 1
+    for (int u = 0; u < kTokens<DT> / kStep && left > 0; ++u, left -= kStep) {
+      ring.step(u);
+      Two sr[kPairs], sg[kPairs], A[kPairs], B[kPairs];
+      step_gates(ring, k, speed, near, sr, sg, A, B);
 #pragma unroll
-    for (int q = 0; q < kPairs; ++q) B[q] = root(B[q]) * sg[q] * ring.pair(kX, q);
-    ring.done(p.count(t + kForwardSlots<DT> * kStep));
-    const int n = p.count(t);
-    if (n < kStep) {  // tokens outside the run change nothing
+      for (int q = 0; q < kPairs; ++q) B[q] = root(B[q]) * sg[q] * ring.pair(kX, q);
+      if (left < kStep) {  // tokens outside the run change nothing
 #pragma unroll
-      for (int q = 0; q < kPairs; ++q) {
-        A[q] = two(2 * q < n ? lo(A[q]) : 1.f, 2 * q + 1 < n ? hi(A[q]) : 1.f);
-        B[q] = two(2 * q < n ? lo(B[q]) : 0.f, 2 * q + 1 < n ? hi(B[q]) : 0.f);
+        for (int q = 0; q < kPairs; ++q) {
+          A[q] = two(2 * q < left ? lo(A[q]) : 1.f, 2 * q + 1 < left ? hi(A[q]) : 1.f);
+          B[q] = two(2 * q < left ? lo(B[q]) : 0.f, 2 * q + 1 < left ? hi(B[q]) : 0.f);
+        }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kStep; ++j) m.B = fmaf(element(A, j), m.B, element(B, j));
-    const Two P = A[0] * A[1] * (A[2] * A[3]);
-    m.A *= lo(P) * hi(P);
+      for (int j = 0; j < kStep; ++j) m.B = fmaf(element(A, j), m.B, element(B, j));
+      const Two P = A[0] * A[1] * (A[2] * A[3]);
+      m.A *= lo(P) * hi(P);
+    }
+    ring.done();
   }
   cp_wait<0>();
   if (cut) m.A = -1.f;
@@ -646,43 +660,47 @@ __device__ __forceinline__ Map run_map_back(const ScanArgs& a, const Place& p, u
   int64_t first, end;
   const int64_t s = cur.owner(p.t0, false, first, end);
   const bool cut = end > p.t0 && end <= p.t1;
-  Place q = p;
-  if (cut) q.t1 = end;
-  BackMapRing<DT, WIDE> ring(a, mem, p.cb, lane);
+  int left = (int)((cut ? end : p.t1) - p.t0);
+  const float last = cut && a.dh_last && p.on ? a.dh_last[s * a.C + p.c] : 0.f;
+  BackMapRing<DT, WIDE> ring(a, mem, p.cb, lane, left);
   const Constants k;
   ring.input(0, a.r, a.sr, p.t0, p.cb);
   ring.input(1, a.dh, a.sdh, p.t0, p.cb);
 #pragma unroll
-  for (int i = 0; i < kBackMapSlots<DT>; ++i) ring.fill(q.count(p.t0 + i * kStep));
-  for (int64_t t = p.t0; t < q.t1; t += kStep) {
+  for (int i = 0; i < kBackMapSlots<DT>; ++i) ring.fill();
+  while (left > 0) {
     ring.ready();
-    Two A[kPairs], D[kPairs];
-    if (near) {
+#pragma unroll 1
+    for (int u = 0; u < kTokens<DT> / kStep && left > 0; ++u, left -= kStep) {
+      ring.step(u);
+      Two A[kPairs], D[kPairs];
+      if (near) {
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i)
-        A[i] = decay_near(speed * rcp(ex2(ring.pair(0, i) * k.minus_log2e) + k.one), k).a;
-    } else {
+        for (int i = 0; i < kPairs; ++i)
+          A[i] = decay_near(speed * rcp(ex2(ring.pair(0, i) * k.minus_log2e) + k.one), k).a;
+      } else {
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        const Two r = ring.pair(0, i);
-        A[i] = decay_any(speed * two(sigmoid(lo(r)), sigmoid(hi(r)))).a;
+        for (int i = 0; i < kPairs; ++i) {
+          const Two r = ring.pair(0, i);
+          A[i] = decay_any(speed * two(sigmoid(lo(r)), sigmoid(hi(r)))).a;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) D[i] = ring.pair(1, i);
+      if (left <= kStep) {  // the run's last token, and those outside it
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          A[i] = two(2 * i < left ? lo(A[i]) : 1.f, 2 * i + 1 < left ? hi(A[i]) : 1.f);
+          D[i] = D[i] + two(2 * i + 1 == left ? last : 0.f, 2 * i + 2 == left ? last : 0.f);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kStep; ++j) {
+        m.A *= element(A, j);
+        m.B = fmaf(m.A, element(D, j), m.B);
       }
     }
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) D[i] = ring.pair(1, i);
-    ring.done(q.count(t + kBackMapSlots<DT> * kStep));
-    const int n = q.count(t);
-    if (n < kStep) {
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i) A[i] = two(2 * i < n ? lo(A[i]) : 1.f, 2 * i + 1 < n ? hi(A[i]) : 1.f);
-    }
-#pragma unroll
-    for (int j = 0; j < kStep; ++j) {
-      float d = element(D, j);
-      if (cut && t + j == q.t1 - 1 && a.dh_last && p.on) d += a.dh_last[s * a.C + p.c];
-      m.A *= element(A, j);
-      m.B = fmaf(m.A, d, m.B);
-    }
+    ring.done();
   }
   cp_wait<0>();
   if (cut) m.A = -1.f;
@@ -811,12 +829,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<false>) forward_kernel(
   uint8_t* mine = mem + warp * kForwardBytes<DT>;
   float h = 0.f;
   if (ALONE) h = reach_alone<false>(run_map<DT, WIDE>(a, p, mine, speed, near, lane), warp, lane);
-  ForwardRing<DT, WIDE> ring(a, mine, p.cb, lane);
+  int left = (int)(p.t1 - p.t0);
+  ForwardRing<DT, WIDE> ring(a, mine, p.cb, lane, left);
   ring.input(kR, a.r, a.sr, p.t0, p.cb);
   ring.input(kG, a.g, a.sg, p.t0, p.cb);
   ring.input(kX, a.x, a.sx, p.t0, p.cb);
 #pragma unroll
-  for (int i = 0; i < kForwardSlots<DT>; ++i) ring.fill(p.count(p.t0 + i * kStep));
+  for (int i = 0; i < kForwardSlots; ++i) ring.fill();
   empty_sequences(a, a.h0, a.h_last);
   if (!ALONE) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -827,41 +846,47 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<false>) forward_kernel(
   const Constants k;
   Out<DT, false, WIDE> to(a.h, a.sh, p.t0, p.cb, a.C, mine + ForwardRing<DT, WIDE>::kBytes, lane);
   float* state = a.states ? a.states + p.t0 / kStep * a.C + p.c : nullptr;
-  for (int64_t t = p.t0; t < p.t1; t += kStep) {
-    const int n = p.count(t);
-    ev.find(cur, t, n, false, lane);
+  int64_t t = p.t0;
+  while (left > 0) {
     ring.ready();
-    Two sr[kPairs], sg[kPairs], A[kPairs], B[kPairs];
-    step_gates(ring, k, speed, near, sr, sg, A, B);
+#pragma unroll 1
+    for (int u = 0; u < kTokens<DT> / kStep && left > 0; ++u, left -= kStep, t += kStep) {
+      const int n = left < kStep ? left : kStep;
+      ev.find(cur, t, n, false, lane);
+      ring.step(u);
+      Two sr[kPairs], sg[kPairs], A[kPairs], B[kPairs];
+      step_gates(ring, k, speed, near, sr, sg, A, B);
 #pragma unroll
-    for (int q = 0; q < kPairs; ++q) B[q] = root(B[q]) * sg[q] * ring.pair(kX, q);
-    ring.done(p.count(t + kForwardSlots<DT> * kStep));
-    if (state) {
-      if (p.on) *state = h;
-      state += a.C;
-    }
-    float out[kStep];
-    if ((ev.starts | ev.ends) == 0) {
+      for (int q = 0; q < kPairs; ++q) B[q] = root(B[q]) * sg[q] * ring.pair(kX, q);
+      if (state) {
+        if (p.on) *state = h;
+        state += a.C;
+      }
+      float out[kStep];
+      if ((ev.starts | ev.ends) == 0) {
 #pragma unroll
-      for (int j = 0; j < kStep; ++j) out[j] = h = fmaf(element(A, j), h, element(B, j));
-    } else {
+        for (int j = 0; j < kStep; ++j) out[j] = h = fmaf(element(A, j), h, element(B, j));
+      } else {
 #pragma unroll
-      for (int j = 0; j < kStep; ++j) {
-        if (ev.starts >> j & 1) {
-          const int64_t s = ev.sequence(j);
-          h = a.h0 && p.on ? a.h0[s * a.C + p.c] : 0.f;
-        }
-        out[j] = h = fmaf(element(A, j), h, element(B, j));
-        if (ev.ends >> j & 1) {
-          const int64_t s = ev.sequence(j);
-          if (p.on) a.h_last[s * a.C + p.c] = h;
+        for (int j = 0; j < kStep; ++j) {
+          if (ev.starts >> j & 1) {
+            const int64_t s = ev.sequence(j);
+            h = a.h0 && p.on ? a.h0[s * a.C + p.c] : 0.f;
+          }
+          out[j] = h = fmaf(element(A, j), h, element(B, j));
+          if (ev.ends >> j & 1) {
+            const int64_t s = ev.sequence(j);
+            if (p.on) a.h_last[s * a.C + p.c] = h;
+          }
         }
       }
-    }
 #pragma unroll
-    for (int q = 0; q < kPairs; ++q) to.put(q, two(out[2 * q], out[2 * q + 1]), n);
-    __syncwarp();
-    to.flush(n);  // the next step's ready() comes before the room is written again
+      for (int q = 0; q < kPairs; ++q) to.put(q, two(out[2 * q], out[2 * q + 1]), n);
+      __syncwarp();
+      to.flush(n);
+      __syncwarp();
+    }
+    ring.done();
   }
   cp_wait<0>();
 }
@@ -877,16 +902,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<true>) backward_kernel(
   float c = 0.f;
   Two sum = two(0.f);
   if (ALONE) c = reach_alone<true>(run_map_back<DT, WIDE>(a, p, mine, speed, near, lane), warp, lane);
-  // steps from the run's last one down
-  const int64_t last = p.t0 < p.t1 ? p.t0 + (p.t1 - 1 - p.t0) / kStep * kStep : p.t0;
-  BackwardRing<DT, WIDE> ring(a, mine, p.cb, lane);
+  // slots from the run's last one down
+  const int tokens = (int)(p.t1 - p.t0);
+  const int slots = (tokens + kTokens<DT> - 1) / kTokens<DT>;
+  const int64_t last = p.t0 + (int64_t)(slots > 0 ? slots - 1 : 0) * kTokens<DT>;
+  BackwardRing<DT, WIDE> ring(a, mine, p.cb, lane, tokens);
   ring.input(kR, a.r, a.sr, last, p.cb);
   ring.input(kG, a.g, a.sg, last, p.cb);
   ring.input(kX, a.x, a.sx, last, p.cb);
   ring.input(kD, a.dh, a.sdh, last, p.cb);
   ring.state = p.on ? a.states + last / kStep * a.C + p.c : nullptr;
 #pragma unroll
-  for (int i = 0; i < kBackwardSlots<DT>; ++i) ring.fill(p.count(last - i * kStep));
+  for (int i = 0; i < kBackwardSlots; ++i) ring.fill();
   empty_sequences(a, a.dh_last, a.dh0);
   if (!ALONE) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -895,82 +922,90 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<true>) backward_kernel(
   Cursor cur(a, lane);
   Events ev;
   uint8_t* room = mine + BackwardRing<DT, WIDE>::kBytes;
-  constexpr int kBox = BackwardRing<DT, WIDE>::kBox;
-  Out<DT, true, WIDE> px(a.dx, a.sdx, last, p.cb, a.C, room, lane);
-  Out<DT, true, WIDE> pr(a.dr, a.sdr, last, p.cb, a.C, room + kBox, lane);
-  Out<DT, true, WIDE> pg(a.dg, a.sdg, last, p.cb, a.C, room + 2 * kBox, lane);
+  constexpr int kBox = kStep * 32 * kSize<DT>;
+  const int64_t top = tokens > 0 ? p.t0 + (tokens - 1) / kStep * kStep : p.t0;  // the run's last step
+  Out<DT, true, WIDE> px(a.dx, a.sdx, top, p.cb, a.C, room, lane);
+  Out<DT, true, WIDE> pr(a.dr, a.sdr, top, p.cb, a.C, room + kBox, lane);
+  Out<DT, true, WIDE> pg(a.dg, a.sdg, top, p.cb, a.C, room + 2 * kBox, lane);
   const Constants k;
-  for (int64_t t = last; t >= p.t0 && p.t0 < p.t1; t -= kStep) {
-    const int n = p.count(t);
-    ev.find(cur, t, n, true, lane);
+  int64_t t = top;
+  int n = tokens - (int)(top - p.t0);  // of the last step; the others are whole
+  for (int left = slots; left > 0; --left) {
     ring.ready();
-    Two sr[kPairs], sg[kPairs], A[kPairs], inv[kPairs], beta[kPairs], found[kPairs], G[kPairs];
-    step_gates(ring, k, speed, near, sr, sg, A, beta);
-    const bool plain = (ev.starts | ev.ends) == 0 && n == kStep;
-    // the states that the step's tokens find
-    float h = ring.first_state();
+#pragma unroll 1
+    for (int u = (int)(t - p.t0) / kStep % (kTokens<DT> / kStep); u >= 0; --u, t -= kStep, n = kStep) {
+      ev.find(cur, t, n, true, lane);
+      ring.step(u);
+      Two sr[kPairs], sg[kPairs], A[kPairs], inv[kPairs], beta[kPairs], found[kPairs], G[kPairs];
+      step_gates(ring, k, speed, near, sr, sg, A, beta);
+      const bool plain = (ev.starts | ev.ends) == 0 && n == kStep;
+      // the states that the step's tokens find
+      float h = ring.first_state(u);
 #pragma unroll
-    for (int q = 0; q < kPairs; ++q) {
-      // where 1 - a^2 is 0 the token takes nothing in, and its gate's slope
-      // u d beta / d u = u a^2 / beta goes to 0 with u
-      const Two safe = two(fmaxf(lo(beta[q]), 1e-37f), fmaxf(hi(beta[q]), 1e-37f));
-      inv[q] = inv_root(safe);
-      beta[q] = beta[q] * inv[q];
-      const Two b = beta[q] * sg[q] * ring.pair(kX, q);
-      float f[2];
+      for (int q = 0; q < kPairs; ++q) {
+        // where 1 - a^2 is 0 the token takes nothing in, and its gate's slope
+        // u d beta / d u = u a^2 / beta goes to 0 with u
+        const Two safe = two(fmaxf(lo(beta[q]), 1e-37f), fmaxf(hi(beta[q]), 1e-37f));
+        inv[q] = inv_root(safe);
+        beta[q] = beta[q] * inv[q];
+        const Two b = beta[q] * sg[q] * ring.pair(kX, q);
+        float f[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (!plain && (ev.starts >> (2 * q + e) & 1)) {
-          const int64_t s = ev.sequence(2 * q + e);
-          h = a.h0 && p.on ? a.h0[s * a.C + p.c] : 0.f;
-        }
-        f[e] = h;
-        h = fmaf(e ? hi(A[q]) : lo(A[q]), h, e ? hi(b) : lo(b));
-      }
-      found[q] = two(f[0], f[1]);
-      G[q] = ring.pair(kD, q);
-    }
-    if (plain) {
-#pragma unroll
-      for (int q = kPairs - 1; q >= 0; --q) {
-        const float g1 = hi(G[q]) + c, g0 = fmaf(hi(A[q]), g1, lo(G[q]));
-        c = lo(A[q]) * g0;
-        G[q] = two(g0, g1);
-      }
-    } else {
-#pragma unroll
-      for (int j = kStep - 1; j >= 0; --j) {
-        float g = element(G, j);
-        if (j < n) {
-          if (ev.ends >> j & 1) {
-            const int64_t s = ev.sequence(j);
-            if (a.dh_last && p.on) g += a.dh_last[s * a.C + p.c];
-          } else {
-            g += c;
+        for (int e = 0; e < 2; ++e) {
+          if (!plain && (ev.starts >> (2 * q + e) & 1)) {
+            const int64_t s = ev.sequence(2 * q + e);
+            h = a.h0 && p.on ? a.h0[s * a.C + p.c] : 0.f;
           }
-          c = element(A, j) * g;
-          if (ev.starts >> j & 1) {
-            const int64_t s = ev.sequence(j);
-            if (a.dh0 && p.on) a.dh0[s * a.C + p.c] = c;
-          }
+          f[e] = h;
+          h = fmaf(e ? hi(A[q]) : lo(A[q]), h, e ? hi(b) : lo(b));
         }
-        G[j >> 1] = j & 1 ? two(lo(G[j >> 1]), g) : two(g, hi(G[j >> 1]));
+        found[q] = two(f[0], f[1]);
+        G[q] = ring.pair(kD, q);
       }
-    }
+      if (plain) {
 #pragma unroll
-    for (int q = 0; q < kPairs; ++q) {
-      const Two x = ring.pair(kX, q, true);
-      const Two w = G[q] * (speed * sr[q]) * A[q] * fma2(A[q] * inv[q], sg[q] * x, negative(found[q]));
-      const Two dx = G[q] * beta[q] * sg[q], dg = dx * x * (k.one + negative(sg[q])), dr = w * (k.one + negative(sr[q]));
-      px.put(q, dx, n);
-      pr.put(q, dr, n);
-      pg.put(q, dg, n);
-      sum = sum + w;  // 0 behind the batch, where dh reads as 0
+        for (int q = kPairs - 1; q >= 0; --q) {
+          const float g1 = hi(G[q]) + c, g0 = fmaf(hi(A[q]), g1, lo(G[q]));
+          c = lo(A[q]) * g0;
+          G[q] = two(g0, g1);
+        }
+      } else {
+#pragma unroll
+        for (int j = kStep - 1; j >= 0; --j) {
+          float g = element(G, j);
+          if (j < n) {
+            if (ev.ends >> j & 1) {
+              const int64_t s = ev.sequence(j);
+              if (a.dh_last && p.on) g += a.dh_last[s * a.C + p.c];
+            } else {
+              g += c;
+            }
+            c = element(A, j) * g;
+            if (ev.starts >> j & 1) {
+              const int64_t s = ev.sequence(j);
+              if (a.dh0 && p.on) a.dh0[s * a.C + p.c] = c;
+            }
+          }
+          G[j >> 1] = j & 1 ? two(lo(G[j >> 1]), g) : two(g, hi(G[j >> 1]));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kPairs; ++q) {
+        const Two x = ring.pair(kX, q, true);
+        const Two w = G[q] * (speed * sr[q]) * A[q] * fma2(A[q] * inv[q], sg[q] * x, negative(found[q]));
+        const Two dx = G[q] * beta[q] * sg[q], dg = dx * x * (k.one + negative(sg[q])), dr = w * (k.one + negative(sr[q]));
+        px.put(q, dx, n);
+        pr.put(q, dr, n);
+        pg.put(q, dg, n);
+        sum = sum + w;  // 0 behind the batch, where dh reads as 0
+      }
+      __syncwarp();
+      px.flush(n);
+      pr.flush(n);
+      pg.flush(n);
+      __syncwarp();
     }
-    ring.done(p.count(t - kBackwardSlots<DT> * kStep));
-    px.flush(n);  // done() and the next step's ready() keep the warp together
-    pr.flush(n);
-    pg.flush(n);
+    ring.done();
   }
   cp_wait<0>();
   if (p.on) a.partial[((int64_t)(blockIdx.x / a.cblocks) * kWarps + warp) * a.C + p.c] = lo(sum) + hi(sum);
@@ -1026,8 +1061,9 @@ struct Split {
 Split split_of(int64_t N, int32_t cblocks, bool back) {
   const int64_t warps = (int64_t)sm_count() * (back ? kBlocksPerSm<true> : kBlocksPerSm<false>) * kWarps / cblocks;
   const int64_t parts = N <= kAlone || warps < kWarps ? kWarps : warps / kWarps * kWarps;
-  int64_t run = ((N + parts - 1) / parts + kStep - 1) / kStep * kStep;
-  if (run < kStep) run = kStep;
+  constexpr int kUnit = 2 * kStep;  // whole slots of every type
+  int64_t run = ((N + parts - 1) / parts + kUnit - 1) / kUnit * kUnit;
+  if (run < kUnit) run = kUnit;
   Split s;
   s.run = (int32_t)run;
   s.blocks = (int32_t)((N + run * kWarps - 1) / (run * kWarps));
