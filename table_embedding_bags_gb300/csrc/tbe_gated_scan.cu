@@ -390,6 +390,7 @@ struct Ring {
   const ScanArgs& a;
   uint32_t base;  // of slot 0, in shared memory
   int bytes;      // of a lane's piece inside the array
+  bool on;        // the lane's channel lies inside the array
   int lane;
   int read, write;  // bytes from slot 0: the oldest slot, the next to be filled
   int left;         // tokens of the run that are not asked for yet
@@ -401,6 +402,7 @@ struct Ring {
     const int piece = WIDE ? 16 : a.copy == 4 ? 4 : kSize<DT>;
     const int b = left - col();
     bytes = b < 0 ? 0 : (b < piece ? b : piece);
+    on = cb + l < a.C;
   }
   // the lane's place in a row, and the first row it copies
   __device__ __forceinline__ int col() const {
@@ -417,42 +419,33 @@ struct Ring {
   static __device__ __forceinline__ void copy4(uint32_t dst, const void* from, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
   }
-  // The next slot.  What lies outside the run (in the batch's last one), or
-  // outside the channels, reads as 0.
-  __device__ __forceinline__ void fill() {
-    int count = left < kTok ? left : kTok;
-    if (DOWN && left > kTok && left % kTok) count = left % kTok;
-    left -= count;
+  // A slot of `count` tokens, by any kind of copy.  What lies outside the run
+  // (in the batch's last one), or outside the channels, reads as 0.
+  __device__ __forceinline__ void fill_part(int count) {
     const uint32_t to = base + write;
-    const bool whole = count == kTok;
 #pragma unroll
     for (int i = 0; i < INPUTS; ++i) {
+      const uint8_t* from = src[i];
       if (WIDE) {
         constexpr int kRows = 32 / kLanes;
 #pragma unroll
         for (int k = 0; k < kTok / kRows; ++k) {
-          const uint32_t dst = to + i * kBox + k * 512 + lane * 16;
-          const uint8_t* from = src[i] + k * kRows * row[i];
-          if (whole) {
-            copy16(dst, from, bytes);
-          } else {
-            const int n = k * kRows + first_row() < count ? bytes : 0;
-            copy16(dst, n ? from : a.x, n);
-          }
+          const int n = k * kRows + first_row() < count ? bytes : 0;
+          copy16(to + i * kBox + k * 512 + lane * 16, n ? from : a.x, n);
+          from += kRows * row[i];
         }
       } else if (a.copy == 4) {
         constexpr int kRows = 128 / kRow;
-        const uint8_t* from = src[i];
 #pragma unroll
         for (int k = 0; k < kTok / kRows; ++k) {
-          const int n = whole || k * kRows + first_row() < count ? bytes : 0;
+          const int n = k * kRows + first_row() < count ? bytes : 0;
           copy4(to + i * kBox + k * 128 + lane * 4, n ? from : a.x, n);
           from += kRows * row[i];
         }
       } else {
         uint32_t w[kTok];
 #pragma unroll
-        for (int k = 0; k < kTok; ++k) w[k] = k < count && bytes ? load_bits<DT>(src[i] + k * row[i]) : 0;
+        for (int k = 0; k < kTok; ++k) w[k] = k < count && bytes ? load_bits<DT>(from + k * row[i]) : 0;
 #pragma unroll
         for (int k = 0; k < kTok; ++k)
           asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + i * kBox + k * kRow + lane * 2), "h"((uint16_t)w[k]) : "memory");
@@ -462,10 +455,34 @@ struct Ring {
     if (DOWN) {
 #pragma unroll
       for (int u = 0; u < kTok / kStep; ++u) {
-        const int n = u * kStep < count && state ? 4 : 0;
+        const int n = u * kStep < count && on ? 4 : 0;
         copy4(to + INPUTS * kBox + u * 128 + lane * 4, n ? (const void*)(state + (int64_t)u * a.C) : a.x, n);
       }
-      if (state) state -= (int64_t)(kTok / kStep) * a.C;
+      state -= (int64_t)(kTok / kStep) * a.C;
+    }
+  }
+  // The next slot.
+  __device__ __forceinline__ void fill() {
+    int count = left < kTok ? left : kTok;
+    if (DOWN && left > kTok && left % kTok) count = left % kTok;
+    left -= count;
+    if (WIDE && count == kTok) {
+      const uint32_t to = base + write + lane * 16;
+      constexpr int kRows = 32 / kLanes;
+#pragma unroll
+      for (int i = 0; i < INPUTS; ++i) {
+#pragma unroll
+        for (int k = 0; k < kTok / kRows; ++k) copy16(to + i * kBox + k * 512, src[i] + k * kRows * row[i], bytes);
+        src[i] += (DOWN ? -kTok : kTok) * row[i];
+      }
+      if (DOWN) {
+#pragma unroll
+        for (int u = 0; u < kTok / kStep; ++u)
+          copy4(base + write + lane * 4 + INPUTS * kBox + u * 128, state + (int64_t)u * a.C, on ? 4 : 0);
+        state -= (int64_t)(kTok / kStep) * a.C;
+      }
+    } else {
+      fill_part(count);
     }
     cp_commit();
     write = write + kSlot == kBytes ? 0 : write + kSlot;
@@ -513,16 +530,16 @@ struct Out {
     to = at<DT>(p, t * stride + cb) + col + (WIDE ? l / kLanes * row : 0);
   }
   // pair q of the step (`n` tokens of it lie inside the batch)
-  __device__ __forceinline__ void put(int q, Two v, int n) {
-    if (WIDE) store_pair<DT>(room + lane * kSize<DT> + 2 * q * kRow, kRow, lo(v), hi(v), true, true);
-    else store_pair<DT>(to + 2 * q * row, row, lo(v), hi(v), on && 2 * q < n, on && 2 * q + 1 < n);
+  __device__ __forceinline__ void put(int q, float a, float b, int n) {
+    if (WIDE) store_pair<DT>(room + lane * kSize<DT> + 2 * q * kRow, kRow, a, b, true, true);
+    else store_pair<DT>(to + 2 * q * row, row, a, b, on && 2 * q < n, on && 2 * q + 1 < n);
   }
   // the step is complete (the caller puts a __syncwarp before and after)
   __device__ __forceinline__ void flush(int n) {
     if (WIDE) {
 #pragma unroll
       for (int k = 0; k < kStep / kRows; ++k)
-        if (on && k * kRows + lane / kLanes < n)
+        if (on && (n == kStep || k * kRows + lane / kLanes < n))
           *reinterpret_cast<uint4*>(to + k * kRows * row) = *reinterpret_cast<const uint4*>(room + k * 512 + lane * 16);
     }
     to += (DOWN ? -kStep : kStep) * row;
@@ -881,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<false>) forward_kernel(
         }
       }
 #pragma unroll
-      for (int q = 0; q < kPairs; ++q) to.put(q, two(out[2 * q], out[2 * q + 1]), n);
+      for (int q = 0; q < kPairs; ++q) to.put(q, out[2 * q], out[2 * q + 1], n);
       __syncwarp();
       to.flush(n);
       __syncwarp();
@@ -911,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<true>) backward_kernel(
   ring.input(kG, a.g, a.sg, last, p.cb);
   ring.input(kX, a.x, a.sx, last, p.cb);
   ring.input(kD, a.dh, a.sdh, last, p.cb);
-  ring.state = p.on ? a.states + last / kStep * a.C + p.c : nullptr;
+  ring.state = a.states + last / kStep * a.C + p.c;
 #pragma unroll
   for (int i = 0; i < kBackwardSlots; ++i) ring.fill();
   empty_sequences(a, a.dh_last, a.dh0);
@@ -994,9 +1011,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<true>) backward_kernel(
         const Two x = ring.pair(kX, q, true);
         const Two w = G[q] * (speed * sr[q]) * A[q] * fma2(A[q] * inv[q], sg[q] * x, negative(found[q]));
         const Two dx = G[q] * beta[q] * sg[q], dg = dx * x * (k.one + negative(sg[q])), dr = w * (k.one + negative(sr[q]));
-        px.put(q, dx, n);
-        pr.put(q, dr, n);
-        pg.put(q, dg, n);
+        px.put(q, lo(dx), hi(dx), n);
+        pr.put(q, lo(dr), hi(dr), n);
+        pg.put(q, lo(dg), hi(dg), n);
         sum = sum + w;  // 0 behind the batch, where dh reads as 0
       }
       __syncwarp();
