@@ -1124,22 +1124,30 @@ void choose_access(ScanArgs& a, int32_t dtype) {
                : all(4) ? 4 : 0;
 }
 
-template <typename K>
-int start(K kernel, unsigned grid, unsigned threads, size_t smem, bool after, cudaStream_t s, const ScanArgs& a) {
-  if (smem > 40 * 1024 &&  // beyond the default once the static slots are counted
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return TBE_ERR_CUDA;
+// Launches KERNEL; `after`: it may start while the kernel before it ends.
+template <auto KERNEL>
+int start(unsigned grid, size_t smem, bool after, cudaStream_t s, const ScanArgs& a) {
+  if (smem > 40 * 1024) {  // beyond the default once the static slots are counted
+    static bool allowed[64] = {};  // once per device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !allowed[dev]) {
+      if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return TBE_ERR_CUDA;
+      if (dev >= 0 && dev < 64) allowed[dev] = true;
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = after ? 1 : 0;  // may start while the kernel before it ends
-  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? check_launch() : TBE_ERR_CUDA;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, KERNEL, a) == cudaSuccess ? check_launch() : TBE_ERR_CUDA;
 }
 
 template <int DT, bool BACK, bool WIDE>
@@ -1149,14 +1157,14 @@ int launch_passes(const ScanArgs& a, cudaStream_t s) {
   static_assert(bytes >= map_bytes, "the maps of a lone block use the same memory");
   const unsigned grid = (unsigned)a.blocks * (unsigned)a.cblocks;
   if (a.blocks == 1) {
-    if constexpr (BACK) return start(backward_kernel<DT, true, WIDE>, grid, kThreads, bytes, false, s, a);
-    else return start(forward_kernel<DT, true, WIDE>, grid, kThreads, bytes, false, s, a);
+    if constexpr (BACK) return start<backward_kernel<DT, true, WIDE>>(grid, bytes, false, s, a);
+    else return start<forward_kernel<DT, true, WIDE>>(grid, bytes, false, s, a);
   }
-  const int st = start(maps_kernel<DT, BACK, WIDE>, grid, kThreads, map_bytes, false, s, a);
+  const int st = start<maps_kernel<DT, BACK, WIDE>>(grid, map_bytes, false, s, a);
   if (st != TBE_OK) return st;
   trace_mark(s, BACK ? "gated_scan_maps_back" : "gated_scan_maps");
-  if constexpr (BACK) return start(backward_kernel<DT, false, WIDE>, grid, kThreads, bytes, true, s, a);
-  else return start(forward_kernel<DT, false, WIDE>, grid, kThreads, bytes, true, s, a);
+  if constexpr (BACK) return start<backward_kernel<DT, false, WIDE>>(grid, bytes, true, s, a);
+  else return start<forward_kernel<DT, false, WIDE>>(grid, bytes, true, s, a);
 }
 template <int DT, bool BACK>
 int launch_scan(const ScanArgs& a, cudaStream_t s) {

@@ -10,6 +10,8 @@ enqueued on the current stream (or ``stream``).
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import NamedTuple
 
 import numpy as np
@@ -23,36 +25,18 @@ TBE_ADAMW_BLOCK = 256
 _DTYPE = {torch.float32: _tbe.TBE_F32, torch.float16: _tbe.TBE_F16, torch.bfloat16: _tbe.TBE_BF16}
 
 
-class _ScanInputs(ctypes.Structure):
-    _fields_ = [("tokens", ctypes.c_int64), ("sequences", ctypes.c_int32), ("channels", ctypes.c_int32),
-                ("dtype", ctypes.c_int32), ("offsets_i32", ctypes.c_int32), ("x", ctypes.c_void_p),
-                ("recur", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
-                ("recur_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64), ("decay", ctypes.c_void_p),
-                ("offsets", ctypes.c_void_p), ("h0", ctypes.c_void_p), ("sharpness", ctypes.c_float)]
-
-
-class _ScanGrads(ctypes.Structure):
-    _fields_ = [("dx", ctypes.c_void_p), ("drecur", ctypes.c_void_p), ("dgate", ctypes.c_void_p),
-                ("dx_stride", ctypes.c_int64), ("drecur_stride", ctypes.c_int64), ("dgate_stride", ctypes.c_int64),
-                ("ddecay", ctypes.c_void_p), ("dh0", ctypes.c_void_p)]
-
-
-class _PreferenceInputs(ctypes.Structure):
-    _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64), ("labels", ctypes.c_void_p),
-                ("offsets", ctypes.c_void_p), ("ref_logps", ctypes.c_void_p), ("tokens", ctypes.c_int64),
-                ("vocab", ctypes.c_int32), ("pairs", ctypes.c_int32), ("dtype", ctypes.c_int32),
-                ("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float)]
+# The argument structs of include/tbe.h that are made at every call, packed
+# (native alignment): a ctypes.Structure costs several times as much to fill.
+_SCAN_INPUTS = struct.Struct("@qiiiiPPPqqqPPPf0P")
+_SCAN_GRADS = struct.Struct("@PPPqqqPP")
+_PREFERENCE_INPUTS = struct.Struct("@PqPPPqiiiff0P")
+_ADAMW = struct.Struct("@dddddq")
 
 
 class _AdamWTensors(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int32), ("state_bits", ctypes.c_int32), ("numel", ctypes.c_void_p),
                 ("params", ctypes.c_void_p), ("grads", ctypes.c_void_p), ("param_dtype", ctypes.c_void_p),
                 ("grad_dtype", ctypes.c_void_p)]
-
-
-class _AdamW(ctypes.Structure):
-    _fields_ = [("learning_rate", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
-                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64)]
 
 
 def declare(lib):
@@ -78,34 +62,31 @@ def declare(lib):
         getattr(lib, name).argtypes = args
 
 
-def _rows(t, rows, cols, dtype, device, what):
-    """Checks a [rows, cols] argument of ``dtype`` on ``device`` with
+def _rows(t, rows, cols, dtype, dev, what):
+    """Checks a [rows, cols] argument of ``dtype`` on CUDA device ``dev`` with
     consecutive columns; returns its row stride in elements (at least cols)."""
-    if t.device != device or device.type != "cuda":
+    if t.get_device() != dev or dev < 0:
         raise _tbe.TBEError(f"{what} must be a CUDA tensor on the device of the other arguments (got {t.device})")
     if t.dtype is not dtype:
         raise _tbe.TBEError(f"{what} has dtype {t.dtype}; expected {dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise _tbe.TBEError(f"{what} has shape {tuple(t.shape)}; expected ({rows}, {cols})")
-    stride = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and rows > 0 and t.stride(1) != 1) or stride < cols:
+    stride, step = t.stride()
+    if rows < 2:
+        stride = cols
+    if (step != 1 and cols > 1 and rows > 0) or stride < cols:
         raise _tbe.TBEError(f"{what} must have consecutive columns and rows that do not overlap")
     return stride
 
 
-def _vector(t, shape, dtypes, device, what, optional=False):
-    """Checks a contiguous argument of exactly ``shape``."""
+def _vector(t, shape, dtypes, dev, what):
+    """Checks a contiguous argument of exactly ``shape``; returns its address."""
     if t is None:
-        if optional:
-            return
         raise _tbe.TBEError(f"{what} is required")
-    if t.device != device or t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.get_device() != dev or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
         raise _tbe.TBEError(f"{what} must be a contiguous {' or '.join(map(str, dtypes))} tensor of shape {shape} on "
-                            f"{device} (got {t.dtype}, {tuple(t.shape)}, {t.device})")
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+                            f"CUDA device {dev} (got {t.dtype}, {tuple(t.shape)}, {t.device})")
+    return t.data_ptr()
 
 
 _F32 = (torch.float32,)
@@ -113,16 +94,33 @@ _I64 = (torch.int64,)
 _I32 = (torch.int32,)
 _IDS = (torch.int64, torch.int32)
 
+# the current stream's handle as an integer, without a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-def _run(fn, what, device, stream, *args):
-    """Calls ``fn(*args, stream)`` with ``device`` current."""
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            rc = fn(*args, _tbe._stream(stream))
+
+def _run(fn, what, dev, stream, *args):
+    """Calls ``fn(*args, stream)`` with CUDA device ``dev`` current."""
+    handle = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
     else:
-        rc = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+        rc = fn(*args, handle)
     if rc != _tbe.TBE_OK:
         _tbe._check(rc, what)
+
+
+@functools.lru_cache(maxsize=4096)
+def _scan_workspace(N, C, backward, dev):
+    with torch.cuda.device(dev):
+        return int(_tbe.load_library().tbe_gated_scan_workspace_bytes(N, C, backward))
+
+
+@functools.lru_cache(maxsize=4096)
+def _preference_workspace(N, V, P, dev):
+    with torch.cuda.device(dev):
+        return int(_tbe.load_library().tbe_preference_workspace_bytes(N, V, P))
 
 
 # ---------------------------------------------------------------------------
@@ -144,24 +142,33 @@ class GatedScanGrads(NamedTuple):
 
 
 def _scan_inputs(x, recur, gate, decay, sequences, offsets, h0, sharpness):
-    if x.dim() != 2 or x.dtype not in _DTYPE:
+    """Checks what the three scan calls share; returns the packed struct, the
+    sizes and the device."""
+    dt = x.dtype
+    if x.dim() != 2 or dt not in _DTYPE:
         raise _tbe.TBEError(f"x must be a [tokens, channels] tensor of float32, float16 or bfloat16 (got {x.dtype}, "
                             f"{tuple(x.shape)})")
     N, C = x.shape
-    dev, dt = x.device, x.dtype
-    strides = [_rows(t, N, C, dt, dev, name) for t, name in ((x, "x"), (recur, "recur"), (gate, "gate"))]
-    _vector(decay, (C,), _F32, dev, "decay")
-    _vector(h0, (sequences, C), _F32, dev, "h0", optional=True)
-    i32 = 0
+    dev = x.get_device()
+    sx = _rows(x, N, C, dt, dev, "x")
+    sr = _rows(recur, N, C, dt, dev, "recur")
+    sg = _rows(gate, N, C, dt, dev, "gate")
+    d = _vector(decay, (C,), _F32, dev, "decay")
+    h = 0 if h0 is None else _vector(h0, (sequences, C), _F32, dev, "h0")
+    o, i32 = 0, 0
     if offsets is not None:
-        _vector(offsets, (sequences + 1,), _IDS, dev, "offsets")
+        o = _vector(offsets, (sequences + 1,), _IDS, dev, "offsets")
         i32 = int(offsets.dtype is torch.int32)
-    return _ScanInputs(N, sequences, C, _DTYPE[dt], i32, x.data_ptr(), recur.data_ptr(), gate.data_ptr(), *strides,
-                       decay.data_ptr(), _addr(offsets), _addr(h0), float(sharpness))
+    packed = _SCAN_INPUTS.pack(N, sequences, C, _DTYPE[dt], i32, x.data_ptr(), recur.data_ptr(), gate.data_ptr(), sx,
+                               sr, sg, d, o, h, sharpness)
+    return packed, N, C, dt, dev
 
 
-def _workspace(nbytes, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+def _sequences(offsets):
+    S = offsets.numel() - 1
+    if S < 0:
+        raise _tbe.TBEError("offsets must hold at least one entry")
+    return S
 
 
 def tbe_gated_scan(x, recur, gate, decay, offsets, h0=None, sharpness: float = 8.0, want_states=False, out=None,
@@ -175,22 +182,19 @@ def tbe_gated_scan(x, recur, gate, decay, offsets, h0=None, sharpness: float = 8
     ``offsets`` int64 or int32 [sequences + 1]; ``h0`` fp32 [sequences,
     channels].  ``want_states`` keeps what ``tbe_gated_scan_backward`` needs."""
     lib = _tbe.load_library()
-    S = int(offsets.numel()) - 1
-    if S < 0:
-        raise _tbe.TBEError("offsets must hold at least one entry")
-    a = _scan_inputs(x, recur, gate, decay, S, offsets, h0, sharpness)
-    N, C, dev = a.tokens, a.channels, x.device
-    h = torch.empty((N, C), dtype=x.dtype, device=dev) if out is None else out
-    h_stride = C if out is None else _rows(out, N, C, x.dtype, dev, "out")
-    _vector(dev_status, (1,), _I32, dev, "dev_status", optional=True)
-    h_last = torch.empty((S, C), dtype=torch.float32, device=dev)
-    states = None
-    if want_states:
-        states = torch.empty((lib.tbe_gated_scan_states(N), C), dtype=torch.float32, device=dev)
-    nbytes = lib.tbe_gated_scan_workspace_bytes(N, C, 0)
-    ws = _workspace(nbytes, dev)
-    _run(lib.tbe_gated_scan, "tbe_gated_scan", dev, stream, ctypes.byref(a), h.data_ptr(), h_stride,
-         h_last.data_ptr(), _addr(states), _addr(ws), nbytes, _addr(dev_status))
+    S = _sequences(offsets)
+    a, N, C, dt, dev = _scan_inputs(x, recur, gate, decay, S, offsets, h0, sharpness)
+    if out is None:
+        h, h_stride = x.new_empty((N, C)), C
+    else:
+        h, h_stride = out, _rows(out, N, C, dt, dev, "out")
+    st = None if dev_status is None else _vector(dev_status, (1,), _I32, dev, "dev_status")
+    h_last = decay.new_empty((S, C))
+    states = decay.new_empty((max(1, -(-N // TBE_SCAN_STEP)), C)) if want_states else None
+    nbytes = _scan_workspace(N, C, 0, dev)
+    ws = decay.new_empty(nbytes // 4) if nbytes else None
+    _run(lib.tbe_gated_scan, "tbe_gated_scan", dev, stream, a, h.data_ptr(), h_stride, h_last.data_ptr(),
+         states.data_ptr() if want_states else None, ws.data_ptr() if nbytes else None, nbytes, st)
     return GatedScan(h, h_last, states)
 
 
@@ -201,40 +205,40 @@ def tbe_gated_scan_backward(dh, x, recur, gate, decay, offsets, states, h0=None,
     [tokens, channels] tensors to write dx, drecur and dgate to (rows may be
     strided).  dh0 is returned where ``h0`` was given."""
     lib = _tbe.load_library()
-    S = int(offsets.numel()) - 1
-    if S < 0:
-        raise _tbe.TBEError("offsets must hold at least one entry")
-    a = _scan_inputs(x, recur, gate, decay, S, offsets, h0, sharpness)
-    N, C, dev, dt = a.tokens, a.channels, x.device, x.dtype
+    S = _sequences(offsets)
+    a, N, C, dt, dev = _scan_inputs(x, recur, gate, decay, S, offsets, h0, sharpness)
     dh_stride = _rows(dh, N, C, dt, dev, "dh")
-    _vector(dh_last, (S, C), _F32, dev, "dh_last", optional=True)
-    _vector(states, (lib.tbe_gated_scan_states(N), C), _F32, dev, "states")
-    _vector(dev_status, (1,), _I32, dev, "dev_status", optional=True)
+    last = None if dh_last is None else _vector(dh_last, (S, C), _F32, dev, "dh_last")
+    kept = _vector(states, (max(1, -(-N // TBE_SCAN_STEP)), C), _F32, dev, "states")
+    st = None if dev_status is None else _vector(dev_status, (1,), _I32, dev, "dev_status")
     if out is None:
-        out = tuple(torch.empty((N, C), dtype=dt, device=dev) for _ in range(3))
-    strides = [_rows(t, N, C, dt, dev, "out") for t in out]
-    ddecay = torch.empty(C, dtype=torch.float32, device=dev)
-    dh0 = None if h0 is None else torch.empty((S, C), dtype=torch.float32, device=dev)
-    g = _ScanGrads(out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), *strides, ddecay.data_ptr(), _addr(dh0))
-    nbytes = lib.tbe_gated_scan_workspace_bytes(N, C, 1)
-    ws = _workspace(nbytes, dev)
-    _run(lib.tbe_gated_scan_backward, "tbe_gated_scan_backward", dev, stream, ctypes.byref(a), dh.data_ptr(),
-         dh_stride, _addr(dh_last), states.data_ptr(), ctypes.byref(g), _addr(ws), nbytes, _addr(dev_status))
-    return GatedScanGrads(*out, ddecay, dh0)
+        dx, dr, dg = x.new_empty((N, C)), x.new_empty((N, C)), x.new_empty((N, C))
+        strides = (C, C, C)
+    else:
+        dx, dr, dg = out
+        strides = (_rows(dx, N, C, dt, dev, "dx"), _rows(dr, N, C, dt, dev, "drecur"), _rows(dg, N, C, dt, dev, "dgate"))
+    ddecay = decay.new_empty(C)
+    dh0 = None if h0 is None else decay.new_empty((S, C))
+    g = _SCAN_GRADS.pack(dx.data_ptr(), dr.data_ptr(), dg.data_ptr(), *strides, ddecay.data_ptr(),
+                         0 if dh0 is None else dh0.data_ptr())
+    nbytes = _scan_workspace(N, C, 1, dev)
+    ws = decay.new_empty(nbytes // 4) if nbytes else None
+    _run(lib.tbe_gated_scan_backward, "tbe_gated_scan_backward", dev, stream, a, dh.data_ptr(), dh_stride, last, kept, g,
+         ws.data_ptr() if nbytes else None, nbytes, st)
+    return GatedScanGrads(dx, dr, dg, ddecay, dh0)
 
 
 def tbe_gated_scan_step(x, recur, gate, decay, state, sharpness: float = 8.0, out=None, stream=None):
     """One token of every sequence: ``state`` (fp32 [sequences, channels])
     moves on in place; returns h [sequences, channels] in x's dtype."""
     lib = _tbe.load_library()
-    S = int(x.shape[0])
-    a = _scan_inputs(x, recur, gate, decay, S, None, None, sharpness)
-    C, dev = a.channels, x.device
-    _vector(state, (S, C), _F32, dev, "state")
-    h = torch.empty((S, C), dtype=x.dtype, device=dev) if out is None else out
-    h_stride = C if out is None else _rows(out, S, C, x.dtype, dev, "out")
-    _run(lib.tbe_gated_scan_step, "tbe_gated_scan_step", dev, stream, ctypes.byref(a), state.data_ptr(),
-         h.data_ptr(), h_stride)
+    a, S, C, dt, dev = _scan_inputs(x, recur, gate, decay, x.shape[0], None, None, sharpness)
+    s = _vector(state, (S, C), _F32, dev, "state")
+    if out is None:
+        h, h_stride = x.new_empty((S, C)), C
+    else:
+        h, h_stride = out, _rows(out, S, C, dt, dev, "out")
+    _run(lib.tbe_gated_scan_step, "tbe_gated_scan_step", dev, stream, a, s, h.data_ptr(), h_stride)
     return h
 
 
@@ -252,29 +256,31 @@ class PreferenceLoss(NamedTuple):
 
 
 def _preference_inputs(logits, labels, offsets, ref_logps, beta, label_smoothing):
-    if logits.dim() != 2 or logits.dtype not in _DTYPE:
+    dt = logits.dtype
+    if logits.dim() != 2 or dt not in _DTYPE:
         raise _tbe.TBEError(f"logits must be a [tokens, vocab] tensor of float32, float16 or bfloat16 (got "
                             f"{logits.dtype}, {tuple(logits.shape)})")
     N, V = logits.shape
-    dev = logits.device
-    stride = _rows(logits, N, V, logits.dtype, dev, "logits")
+    dev = logits.get_device()
+    stride = _rows(logits, N, V, dt, dev, "logits")
     if N < 1 or V < 1 or V >= 1 << 31:
         raise _tbe.TBEError("logits must have at least one row and one column (and fewer than 2^31 columns)")
-    Q = int(ref_logps.numel())
+    Q = ref_logps.numel()
     if Q < 2 or Q % 2:
         raise _tbe.TBEError("ref_logps must hold two sequences per pair")
-    _vector(labels, (N,), _I64, dev, "labels")
-    _vector(offsets, (Q + 1,), _I64, dev, "offsets")
-    _vector(ref_logps, (Q,), _F32, dev, "ref_logps")
-    return _PreferenceInputs(logits.data_ptr(), stride, labels.data_ptr(), offsets.data_ptr(), ref_logps.data_ptr(),
-                             N, V, Q // 2, _DTYPE[logits.dtype], float(beta), float(label_smoothing))
+    y = _vector(labels, (N,), _I64, dev, "labels")
+    o = _vector(offsets, (Q + 1,), _I64, dev, "offsets")
+    r = _vector(ref_logps, (Q,), _F32, dev, "ref_logps")
+    packed = _PREFERENCE_INPUTS.pack(logits.data_ptr(), stride, y, o, r, N, V, Q // 2, _DTYPE[dt], beta, label_smoothing)
+    return packed, N, V, Q // 2, stride, dt, dev
 
 
-def _like_rows(logits, stride):
+def _like_rows(logits, N, V, stride):
     """Room for the gradient with the logits' row stride, so that both rows
     start on the same alignment."""
-    N, V = logits.shape
-    return torch.empty((N, stride), dtype=logits.dtype, device=logits.device)[:, :V]
+    if stride == V:
+        return logits.new_empty((N, V))
+    return logits.new_empty((N, stride))[:, :V]
 
 
 def tbe_preference_loss(logits, labels, offsets, ref_logps, beta: float = 0.1, label_smoothing: float = 0.0,
@@ -288,21 +294,24 @@ def tbe_preference_loss(logits, labels, offsets, ref_logps, beta: float = 0.1, l
     label is negative takes no part.  ``want_grad`` (or a ``dlogits`` tensor,
     which may be ``logits``) adds grad_scale * d loss / d logits."""
     lib = _tbe.load_library()
-    a = _preference_inputs(logits, labels, offsets, ref_logps, beta, label_smoothing)
-    N, V, P, dev = a.tokens, a.vocab, a.pairs, logits.device
+    a, N, V, P, stride, dt, dev = _preference_inputs(logits, labels, offsets, ref_logps, beta, label_smoothing)
     d_stride = 0
     if dlogits is not None:
-        d_stride = _rows(dlogits, N, V, logits.dtype, dev, "dlogits")
+        d_stride = _rows(dlogits, N, V, dt, dev, "dlogits")
     elif want_grad:
-        dlogits, d_stride = _like_rows(logits, a.logits_stride), a.logits_stride
-    _vector(dev_status, (1,), _I32, dev, "dev_status", optional=True)
-    loss, seq_logps, margins, lse, coef = torch.empty(1 + 3 * P + 2 * N, dtype=torch.float32, device=dev).split(
-        [1, 2 * P, P, N, N])
-    nbytes = lib.tbe_preference_workspace_bytes(N, V, P)
-    ws = _workspace(nbytes, dev)
-    _run(lib.tbe_preference_loss, "tbe_preference_loss", dev, stream, ctypes.byref(a), loss.data_ptr(),
-         seq_logps.data_ptr(), margins.data_ptr(), lse.data_ptr(), coef.data_ptr(), _addr(dlogits), d_stride,
-         float(grad_scale), ws.data_ptr(), nbytes, _addr(dev_status))
+        dlogits, d_stride = _like_rows(logits, N, V, stride), stride
+    st = None if dev_status is None else _vector(dev_status, (1,), _I32, dev, "dev_status")
+    # one allocation: the results, then the workspace on 256 bytes
+    sizes = (1, 2 * P, P, N, N)
+    used = 4 * (1 + 3 * P + 2 * N)
+    start = -(-used // 256) * 256
+    nbytes = _preference_workspace(N, V, P, dev)
+    room = ref_logps.new_empty((start + nbytes) // 4)
+    at = room.data_ptr()
+    _run(lib.tbe_preference_loss, "tbe_preference_loss", dev, stream, a, at, at + 4, at + 4 + 8 * P, at + 4 + 12 * P,
+         at + 4 + 12 * P + 4 * N, None if dlogits is None else dlogits.data_ptr(), d_stride, grad_scale, at + start,
+         nbytes, st)
+    loss, seq_logps, margins, lse, coef, _ = room.split_with_sizes((*sizes, room.numel() - used // 4))
     return PreferenceLoss(loss.view(()), seq_logps, margins, dlogits, lse, coef)
 
 
@@ -311,16 +320,15 @@ def tbe_preference_loss_backward(logits, labels, offsets, ref_logps, saved: Pref
     """grad_scale * d loss / d logits from the ``lse`` and ``coef`` of the
     ``tbe_preference_loss`` call on the same arguments."""
     lib = _tbe.load_library()
-    a = _preference_inputs(logits, labels, offsets, ref_logps, 1.0, 0.0)
-    N, V, dev = a.tokens, a.vocab, logits.device
-    _vector(saved.lse, (N,), _F32, dev, "saved.lse")
-    _vector(saved.coef, (N,), _F32, dev, "saved.coef")
+    a, N, V, _, stride, dt, dev = _preference_inputs(logits, labels, offsets, ref_logps, 1.0, 0.0)
+    lse = _vector(saved.lse, (N,), _F32, dev, "saved.lse")
+    coef = _vector(saved.coef, (N,), _F32, dev, "saved.coef")
     if dlogits is None:
-        dlogits, d_stride = _like_rows(logits, a.logits_stride), a.logits_stride
+        dlogits, d_stride = _like_rows(logits, N, V, stride), stride
     else:
-        d_stride = _rows(dlogits, N, V, logits.dtype, dev, "dlogits")
-    _run(lib.tbe_preference_loss_backward, "tbe_preference_loss_backward", dev, stream, ctypes.byref(a),
-         saved.lse.data_ptr(), saved.coef.data_ptr(), float(grad_scale), dlogits.data_ptr(), d_stride)
+        d_stride = _rows(dlogits, N, V, dt, dev, "dlogits")
+    _run(lib.tbe_preference_loss_backward, "tbe_preference_loss_backward", dev, stream, a, lse, coef, grad_scale,
+         dlogits.data_ptr(), d_stride)
     return dlogits
 
 
@@ -347,6 +355,8 @@ class AdamWPlan:
             raise _tbe.TBEError(f"state_bits must be 8 or 32 (got {state_bits})")
         self.state_bits = state_bits
         self.device = params[0].device
+        if self.device.type != "cuda":
+            raise _tbe.TBEError(f"parameter 0 must be a CUDA tensor (got {self.device})")
         self.numel = np.array([p.numel() for p in params], dtype=np.int64)
         ends = np.cumsum(-(-self.numel // TBE_ADAMW_BLOCK))
         self.blocks = int(ends[-1])
@@ -361,10 +371,12 @@ class AdamWPlan:
         for name, dt in want.items():
             n = self.blocks if name.endswith("scale") else self.blocks * TBE_ADAMW_BLOCK
             t = torch.zeros(n, dtype=dt, device=self.device) if state is None else state.get(name)
-            _vector(t, (n,), (dt,), self.device, f"state[{name!r}]")
+            _vector(t, (n,), (dt,), self.device.index, f"state[{name!r}]")
             setattr(self, name, t)
         if state_bits == 32:
             self.exp_avg_scale = self.exp_avg_sq_scale = None
+        self._state_addr = tuple(None if t is None else t.data_ptr() for t in (
+            self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale))
 
     def _bind(self, params, grads, stream):
         n = len(params)
@@ -420,10 +432,9 @@ def tbe_adamw_step(plan: AdamWPlan, step: int, learning_rate: float, beta1: floa
     for t, dt, what in ((grad_scale, torch.float32, "grad_scale"), (skip, torch.int32, "skip")):
         if t is not None and (t.device != plan.device or t.dtype is not dt or t.numel() != 1):
             raise _tbe.TBEError(f"{what} must be one {dt} on {plan.device}")
-    opt = _AdamW(learning_rate, beta1, beta2, eps, weight_decay, step)
-    _run(_tbe.load_library().tbe_adamw_step, "tbe_adamw_step", plan.device, stream, plan._h, ctypes.byref(opt),
-         plan.exp_avg.data_ptr(), plan.exp_avg_sq.data_ptr(), _addr(plan.exp_avg_scale),
-         _addr(plan.exp_avg_sq_scale), _addr(grad_scale), _addr(skip))
+    opt = _ADAMW.pack(learning_rate, beta1, beta2, eps, weight_decay, step)
+    _run(_tbe.load_library().tbe_adamw_step, "tbe_adamw_step", plan.device.index, stream, plan._h, opt,
+         *plan._state_addr, None if grad_scale is None else grad_scale.data_ptr(), None if skip is None else skip.data_ptr())
 
 
 def tbe_adamw_state(plan: AdamWPlan, stream=None):
@@ -433,7 +444,6 @@ def tbe_adamw_state(plan: AdamWPlan, stream=None):
         return plan.exp_avg, plan.exp_avg_sq
     m = torch.empty(plan.blocks * TBE_ADAMW_BLOCK, dtype=torch.float32, device=plan.device)
     v = torch.empty_like(m)
-    _run(_tbe.load_library().tbe_adamw_state, "tbe_adamw_state", plan.device, stream, plan._h,
-         plan.exp_avg.data_ptr(), plan.exp_avg_sq.data_ptr(), plan.exp_avg_scale.data_ptr(),
-         plan.exp_avg_sq_scale.data_ptr(), m.data_ptr(), v.data_ptr())
+    _run(_tbe.load_library().tbe_adamw_state, "tbe_adamw_state", plan.device.index, stream, plan._h, *plan._state_addr,
+         m.data_ptr(), v.data_ptr())
     return m, v
