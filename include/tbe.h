@@ -555,7 +555,8 @@ typedef struct tbe_adamw_plan tbe_adamw_plan;
 
 /* State blocks of the list, or -1 (sizes out of range, 2^31 blocks or more). */
 int64_t tbe_adamw_state_blocks(int32_t n, const int64_t* numel);
-size_t tbe_adamw_plan_device_bytes(int32_t n, const int64_t* numel);
+/* Device memory of a plan (on the current device); 0 for sizes out of range. */
+size_t tbe_adamw_plan_device_bytes(int32_t n, const int64_t* numel, int32_t state_bits);
 int tbe_adamw_plan_create(const tbe_adamw_tensors* L, void* dev_meta, size_t dev_meta_bytes, void* stream,
                           tbe_adamw_plan** plan_out);
 void tbe_adamw_plan_destroy(tbe_adamw_plan* plan);

@@ -18,6 +18,7 @@
 // into fused multiply-adds), so that codes do not depend on how the compiler
 // groups operations.
 #include "tbe_internal.cuh"
+#include "tbe_two.cuh"
 
 #include <cmath>
 #include <cstring>
@@ -30,7 +31,6 @@ constexpr int kBlock = TBE_ADAMW_BLOCK;  // elements of a state block
 constexpr int kPer = kBlock / 32;        // elements of a block per lane
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTileBlocks = 16;  // state blocks per thread block
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kTiny = 1.17549435e-38f;  // smallest normal fp32
 
@@ -47,8 +47,9 @@ static_assert(sizeof(TensorMeta) == 32, "TensorMeta must stay 32 bytes");
 
 struct StepArgs {
   const TensorMeta* meta;      // [n + 1], the last one a sentinel
-  const int32_t* tile_tensor;  // first tensor of each tile
+  const int32_t* tile_tensor;  // first tensor of each thread block's part
   int32_t blocks;
+  int32_t per_warp;  // state blocks of a warp
   void* m;
   void* v;
   float* ms;
@@ -77,17 +78,6 @@ __device__ __forceinline__ float sqrt_approx(float x) {
   asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float sqrt_ftz(float x) {
-  float y;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float div_approx(float a, float b) {
-  float y;
-  asm("div.approx.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-
 // Eight consecutive 32-bit words: one 32-byte access.
 __device__ __forceinline__ void ld8(const void* p, uint32_t* r) {
   asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -208,12 +198,13 @@ __device__ __forceinline__ float block_inverse(float top, float* scale) {
 }
 
 // The code whose root is nearest to y's: f = y's root in codes, from an
-// approximate square root (its error is below 2e-4 codes).  Where f is that
+// approximate square root (2^-23 of it; of 255 codes and twice: below 7e-5).  Where f is that
 // near to the middle between two codes, the exact level decides.
+constexpr float kNearLevel = 0.49992f;
 __device__ __forceinline__ int nearest_code(float f, float y, const float* level) {
   const float r = rintf(f);
   int q = (int)r;
-  if (fabsf(f - r) > 0.4995f) {
+  if (fabsf(f - r) > kNearLevel) {
     const int k = (int)floorf(f) + 1;
     q = y >= __ldg(level + k) ? k : k - 1;
   }
@@ -272,9 +263,9 @@ __device__ __forceinline__ void update_block(const StepArgs& a, const TensorMeta
     g[j] = __fmul_rn(g[j], gscale);
     m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(g[j], a.c1));
     v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(g[j], g[j]), a.c2));
-    const float root = fmaf(sqrt_approx(v[j]), a.root_scale, a.eps);
+    const float bottom = fmaf(sqrt_approx(v[j]), a.root_scale, a.eps);
     // the whole change first: the weight itself is rounded once
-    p[j] -= fmaf(a.size, div_approx(m[j], root), p[j] * a.decay);
+    p[j] -= fmaf(a.size, m[j] * rcp(bottom), p[j] * a.decay);
     if (BITS == 8 && (VEC || elem<VEC>(lane, j) < count)) {
       // magnitudes order like their bits, NaN above infinity
       bits_m = max(bits_m, __float_as_uint(m[j]) & 0x7fffffffu);
@@ -295,10 +286,10 @@ __device__ __forceinline__ void update_block(const StepArgs& a, const TensorMeta
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const float ym = fminf(__fmul_rn(fabsf(m[j]), inv_m), 1.f);
-    int q = nearest_code(127.f * sqrt_ftz(ym), ym, kLevels.m);
+    int q = nearest_code(127.f * root(ym), ym, kLevels.m);
     if (m[j] < 0.f) q = -q;
     const float yv = fminf(__fmul_rn(v[j], inv_v), 1.f);
-    int z = nearest_code(255.f * sqrt_ftz(sqrt_ftz(yv)), yv, kLevels.v);
+    int z = nearest_code(255.f * root(root(yv)), yv, kLevels.v);
     if (yv > 0.f) z = max(z, 1);
     if (VEC) {
       qm[j / 4] |= (uint32_t)(q & 0xff) << (8 * (j % 4));
@@ -321,23 +312,253 @@ __device__ __forceinline__ void update_block(const StepArgs& a, const TensorMeta
   }
 }
 
-template <int BITS>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(StepArgs a) {
+// Whole, aligned blocks of one tensor with 8-bit states: the same arithmetic
+// two elements at a time.  This case is bound by instructions, not by its 10
+// to 16 bytes an element, so codes are rounded by adding 1.5 * 2^23 (the code
+// is then the sum's low byte, in two's complement) and nearness to a level is
+// tested once for the lane's eight elements.  Blocks to come are copied into
+// a ring of the warp's own in shared memory while one is worked on.
+template <int PDT, int GDT>
+struct Ring8 {
+  static constexpr int kP = PDT == TBE_F32 ? 4 : 2, kG = GDT == TBE_F32 ? 4 : 2;  // bytes of an element
+  // a slot: weights, gradients, codes, scales
+  static constexpr int kGradAt = kBlock * kP, kMAt = kGradAt + kBlock * kG, kVAt = kMAt + kBlock, kScaleAt = kVAt + kBlock;
+  static constexpr int kSlot = kScaleAt + 16;
+  static constexpr int kSlots = kP + kG == 4 ? 3 : 2;  // at most 41 KB a block of eight warps
+  static constexpr int kBytes = kSlots * kSlot;
+  const uint8_t* mem;
+  uint32_t base;
+  int read, write, lane;
+  __device__ __forceinline__ Ring8(const uint8_t* m, int l) : mem(m), base(smem_u32(m)), read(0), write(0), lane(l) {}
+  static __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  }
+  // Asks for the next block (`more`: there is one); pp and gp: the lane's elements of it.
+  __device__ __forceinline__ void fill(const StepArgs& a, const uint8_t* pp, const uint8_t* gp, int64_t block, bool more) {
+    if (more) {
+      const uint32_t to = base + write;
+#pragma unroll
+      for (int i = 0; i < kG / 2; ++i) copy16(to + kGradAt + lane * kPer * kG + 16 * i, gp + 16 * i);
+#pragma unroll
+      for (int i = 0; i < kP / 2; ++i) copy16(to + lane * kPer * kP + 16 * i, pp + 16 * i);
+      cp_async8(to + kMAt + lane * kPer, static_cast<const uint8_t*>(a.m) + block * kBlock + lane * kPer);
+      cp_async8(to + kVAt + lane * kPer, static_cast<const uint8_t*>(a.v) + block * kBlock + lane * kPer);
+      if (lane < 2) cp_async4(to + kScaleAt + lane * 4, (lane ? a.vs : a.ms) + block);
+    }
+    cp_commit();
+    write = write + kSlot == kBytes ? 0 : write + kSlot;
+  }
+  __device__ __forceinline__ void ready() const {
+    cp_wait<kSlots - 1>();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void done() {
+    __syncwarp();
+    read = read + kSlot == kBytes ? 0 : read + kSlot;
+  }
+};
+// A lane's share of a block, as read.
+template <int PDT, int GDT>
+struct Raw8 {
+  uint32_t p[PDT == TBE_F32 ? 8 : 4], g[GDT == TBE_F32 ? 8 : 4], m[2], v[2];
+  float sm, sv;
+  __device__ __forceinline__ Raw8(const Ring8<PDT, GDT>& r) {
+    using R = Ring8<PDT, GDT>;
+    const uint8_t* s = r.mem + r.read;
+#pragma unroll
+    for (int i = 0; i < R::kP / 2; ++i)
+      *reinterpret_cast<uint4*>(p + 4 * i) = *reinterpret_cast<const uint4*>(s + r.lane * kPer * R::kP + 16 * i);
+#pragma unroll
+    for (int i = 0; i < R::kG / 2; ++i)
+      *reinterpret_cast<uint4*>(g + 4 * i) = *reinterpret_cast<const uint4*>(s + R::kGradAt + r.lane * kPer * R::kG + 16 * i);
+    *reinterpret_cast<uint2*>(m) = *reinterpret_cast<const uint2*>(s + R::kMAt + r.lane * kPer);
+    *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(s + R::kVAt + r.lane * kPer);
+    sm = *reinterpret_cast<const float*>(s + R::kScaleAt);
+    sv = *reinterpret_cast<const float*>(s + R::kScaleAt + 4);
+  }
+};
+template <int DT>
+__device__ __forceinline__ Two raw_pair(const uint32_t* r, int j) {
+  if (DT == TBE_F32) return two(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+  if (DT == TBE_BF16) return two(__uint_as_float(r[j] << 16), __uint_as_float(r[j] & 0xffff0000u));
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&r[j]));
+  return two(h.x, h.y);
+}
+// The sum of two products, each rounded, and the sum rounded: two-wide
+// multiplies and adds would be contracted.
+__device__ __forceinline__ Two rounded_sum(Two a, Two b) {
+  return two(__fadd_rn(lo(a), lo(b)), __fadd_rn(hi(a), hi(b)));
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack4(const uint32_t* c) {
+  return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+}
+
+template <int PDT, int GDT>
+__device__ __forceinline__ void step_8(const StepArgs& a, const Raw8<PDT, GDT>& x, uint8_t* pp, int64_t block, int lane,
+                                       Two gscale) {
+  const Two cm = two(__fmul_rn(x.sm, (float)(1.0 / (127.0 * 127.0))));
+  const Two cv = two(__fmul_rn(x.sv, (float)(1.0 / (255.0 * 255.0 * 255.0 * 255.0))));
+  Two m[kPer / 2], v[kPer / 2];
+  float top_m = 0.f, top_v = 0.f;
+#pragma unroll
+  for (int j = 0; j < kPer / 2; ++j) {
+    const uint32_t wm = x.m[j / 2] ^ 0x80808080u, wv = x.v[j / 2];  // the signed codes plus 128
+    const int b = 2 * j % 4;
+    auto byte = [](uint32_t w, int i) { return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + i)); };
+    const Two q = two(byte(wm, b), byte(wm, b + 1)) + two(-8388608.f - 128.f);
+    const Two z = two(byte(wv, b), byte(wv, b + 1)) + two(-8388608.f);
+    const Two z2 = z * z;
+    const Two g = raw_pair<GDT>(x.g, j) * gscale;
+    m[j] = rounded_sum(two(lo(q) * fabsf(lo(q)), hi(q) * fabsf(hi(q))) * cm * two(a.b1), g * two(a.c1));
+    v[j] = rounded_sum(z2 * z2 * cv * two(a.b2), g * g * two(a.c2));
+    top_m = max_nan(max_nan(top_m, fabsf(lo(m[j]))), fabsf(hi(m[j])));
+    top_v = max_nan(max_nan(top_v, lo(v[j])), hi(v[j]));
+  }
+  // magnitudes order like their bits, NaN above infinity
+  top_m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top_m)));
+  top_v = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top_v)));
+  Two w[kPer / 2];
+#pragma unroll
+  for (int j = 0; j < kPer / 2; ++j) {
+    // With an eps of at least 1e-10, the root of a v below the normal numbers
+    // (under 1.1e-19) does not show beside it, and may count as 0.
+    const Two top = a.eps >= 1e-10f ? two(root(lo(v[j])), root(hi(v[j]))) : two(sqrt_approx(lo(v[j])), sqrt_approx(hi(v[j])));
+    const Two bottom = fma2(top, two(a.root_scale), two(a.eps));
+    const Two p = raw_pair<PDT>(x.p, j);
+    // the whole change first: the weight itself is rounded once
+    w[j] = p + negative(fma2(two(a.size), m[j] * rcp(bottom), p * two(a.decay)));
+  }
+  float f[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer / 2; ++j) f[2 * j] = lo(w[j]), f[2 * j + 1] = hi(w[j]);
+  if (PDT == TBE_F32) st8(pp, reinterpret_cast<const uint32_t*>(f));
+  else if (PDT == TBE_F16) store_out(reinterpret_cast<__half*>(pp), f, kPer, true);
+  else store_out(reinterpret_cast<__nv_bfloat16*>(pp), f, kPer, true);
+  float scale_m, scale_v;
+  const Two inv_m = two(block_inverse(top_m, &scale_m)), inv_v = two(block_inverse(top_v, &scale_v));
+  const Two magic = two(12582912.f), back = two(-12582912.f);
+  uint32_t cq[kPer], cz[kPer];
+  float off = 0.f;
+#pragma unroll
+  for (int j = 0; j < kPer / 2; ++j) {
+    const Two ym = m[j] * inv_m, yv = v[j] * inv_v;
+    Two c = two(copysignf(root(fabsf(lo(ym))), lo(ym)), copysignf(root(fabsf(hi(ym))), hi(ym))) * two(127.f);
+    Two r = c + magic;
+    Two d = c + negative(r + back);
+    off = fmaxf(fmaxf(off, fabsf(lo(d))), fabsf(hi(d)));
+    cq[2 * j] = __float_as_uint(lo(r));
+    cq[2 * j + 1] = __float_as_uint(hi(r));
+    c = two(root(root(lo(yv))), root(root(hi(yv)))) * two(255.f);
+    r = c + magic;
+    d = c + negative(r + back);
+    off = fmaxf(fmaxf(off, fabsf(lo(d))), fabsf(hi(d)));
+    // at least 1 for what is not 0 (yv is not negative: its bits are at least 1 then)
+    cz[2 * j] = max(__float_as_uint(lo(r)), 0x4b400000u + min(__float_as_uint(lo(yv)), 1u));
+    cz[2 * j + 1] = max(__float_as_uint(hi(r)), 0x4b400000u + min(__float_as_uint(hi(yv)), 1u));
+  }
+  if (off > kNearLevel) {  // some code is close to its neighbour: its level decides
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const float mj = j & 1 ? hi(m[j / 2]) : lo(m[j / 2]), vj = j & 1 ? hi(v[j / 2]) : lo(v[j / 2]);
+      const float ym = fminf(__fmul_rn(fabsf(mj), lo(inv_m)), 1.f), yv = fminf(__fmul_rn(vj, lo(inv_v)), 1.f);
+      const int q = nearest_code(127.f * root(ym), ym, kLevels.m);
+      const int z = nearest_code(255.f * root(root(yv)), yv, kLevels.v);
+      cq[j] = mj < 0.f ? -q : q;
+      cz[j] = yv > 0.f ? max(z, 1) : z;
+    }
+  }
+  const int64_t s0 = block * kBlock + lane * kPer;
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + s0) = make_uint2(pack4(cq), pack4(cq + 4));
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + s0) = make_uint2(pack4(cz), pack4(cz + 4));
+  if (lane == 0) {
+    a.ms[block] = scale_m;
+    a.vs[block] = scale_v;
+  }
+}
+
+// `count` whole blocks from `block` on, at element `at` of the tensor.
+template <int PDT, int GDT>
+__device__ __forceinline__ void whole_blocks_8(const StepArgs& a, const TensorMeta& t, int64_t block, int64_t at, int count,
+                                               int lane, Two gscale, const uint8_t* mem) {
+  using R = Ring8<PDT, GDT>;
+  uint8_t* pp = static_cast<uint8_t*>(t.p) + (at + lane * kPer) * R::kP;
+  const uint8_t* from_p = pp;
+  const uint8_t* from_g = static_cast<const uint8_t*>(t.g) + (at + lane * kPer) * R::kG;
+  R ring(mem, lane);
+  int asked = 0;
+  auto ask = [&] {
+    ring.fill(a, from_p, from_g, block + asked, asked < count);
+    ++asked;
+    from_p += kBlock * R::kP;
+    from_g += kBlock * R::kG;
+  };
+#pragma unroll
+  for (int i = 0; i < R::kSlots; ++i) ask();
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    ring.ready();
+    const Raw8<PDT, GDT> x(ring);
+    ring.done();
+    ask();
+    step_8<PDT, GDT>(a, x, pp, block + i, lane, gscale);
+    pp += kBlock * R::kP;
+  }
+  cp_wait<0>();
+}
+
+// One launch for the whole list.  PDT, GDT: the types of every tensor, or
+// kMixed: looked up at each one.
+constexpr int kMixed = -1;
+template <int BITS, int PDT, int GDT>
+__global__ void __launch_bounds__(kThreads, BITS == 8 ? 4 : 3) adamw_kernel(StepArgs a) {
   if (a.skip && *a.skip != 0) return;
   const float gscale = a.grad_scale ? *a.grad_scale : 1.f;
+  constexpr bool kRing = BITS == 8 && PDT != kMixed;
+  __shared__ __align__(16) uint8_t mem[kRing ? kWarps * Ring8<PDT, GDT>::kBytes : 16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t first = (int64_t)blockIdx.x * kTileBlocks;
   int t = a.tile_tensor[blockIdx.x];
-  for (int i = warp; i < kTileBlocks; i += kWarps) {
-    const int64_t block = first + i;
-    if (block >= a.blocks) return;
-    while (a.meta[t + 1].block0 <= block) ++t;  // a tile holds at most kTileBlocks tensors that have blocks
-    const TensorMeta tm = a.meta[t];
+  // a warp takes neighbouring blocks
+  int64_t block = ((int64_t)blockIdx.x * kWarps + warp) * a.per_warp;
+  const int64_t end = block + a.per_warp < a.blocks ? block + a.per_warp : a.blocks;
+  while (block < end) {
+    while (a.meta[t + 1].block0 <= block) ++t;  // the sentinel's is above every block
+    TensorMeta tm = a.meta[t];
+    if constexpr (PDT != kMixed) tm.pdt = PDT, tm.gdt = GDT;
     const int64_t at = (block - tm.block0) * kBlock;
     const int64_t left = tm.numel - at;
-    if (tm.vec && left >= kBlock) update_block<BITS, true>(a, tm, block, at, kBlock, lane, gscale);
-    else update_block<BITS, false>(a, tm, block, at, left < kBlock ? (int)left : kBlock, lane, gscale);
+    if (kRing && tm.vec && left >= kBlock) {
+      const int64_t whole = left / kBlock;
+      const int count = (int)(whole < end - block ? whole : end - block);
+      if constexpr (kRing)
+        whole_blocks_8<PDT, GDT>(a, tm, block, at, count, lane, two(gscale), mem + warp * Ring8<PDT, GDT>::kBytes);
+      block += count;
+    } else {
+      if ((BITS == 32 || PDT == kMixed) && tm.vec && left >= kBlock)
+        update_block<BITS, true>(a, tm, block, at, kBlock, lane, gscale);
+      else
+        update_block<BITS, false>(a, tm, block, at, left < kBlock ? (int)left : kBlock, lane, gscale);
+      ++block;
+    }
   }
+}
+
+template <int BITS, int PDT>
+void launch_step(int gdt, int tiles, const StepArgs& a, cudaStream_t s) {
+  if (gdt == TBE_F32) adamw_kernel<BITS, PDT, TBE_F32><<<tiles, kThreads, 0, s>>>(a);
+  else if (gdt == TBE_F16) adamw_kernel<BITS, PDT, TBE_F16><<<tiles, kThreads, 0, s>>>(a);
+  else adamw_kernel<BITS, PDT, TBE_BF16><<<tiles, kThreads, 0, s>>>(a);
+}
+template <int BITS>
+void launch_step(int pdt, int gdt, int tiles, const StepArgs& a, cudaStream_t s) {
+  if (pdt == kMixed) adamw_kernel<BITS, kMixed, kMixed><<<tiles, kThreads, 0, s>>>(a);
+  else if (pdt == TBE_F32) launch_step<BITS, TBE_F32>(gdt, tiles, a, s);
+  else if (pdt == TBE_F16) launch_step<BITS, TBE_F16>(gdt, tiles, a, s);
+  else launch_step<BITS, TBE_BF16>(gdt, tiles, a, s);
 }
 
 // 8-bit states as the values they stand for: eight elements per thread.
@@ -370,7 +591,9 @@ struct AdamWPlan {
   int32_t bits;
   int32_t blocks;
   int32_t tiles;
+  int32_t per_warp;
   int32_t device;
+  int32_t pdt, gdt;  // of every tensor, or kMixed
   const TensorMeta* dmeta;
   const int32_t* dtile;
 };
@@ -384,13 +607,27 @@ int64_t count_blocks(int32_t n, const int64_t* numel) {
   for (int32_t i = 0; i < n; ++i) {
     if (numel[i] < 0 || numel[i] >= (int64_t(1) << 40)) return -1;
     blocks += (numel[i] + kBlock - 1) / kBlock;
-    if (blocks >= (int64_t(1) << 31) - kTileBlocks) return -1;
+    if (blocks >= (int64_t(1) << 31) - (1 << 20)) return -1;
   }
   return blocks;
 }
 
 size_t meta_bytes(int32_t n) { return ((size_t)(n + 1) * sizeof(TensorMeta) + 255) / 256 * 256; }
-int32_t tile_count(int64_t blocks) { return (int32_t)((blocks + kTileBlocks - 1) / kTileBlocks); }
+
+// State blocks per warp: 8-bit steps run through one wave of thread blocks,
+// each warp's ring filled once (64 M half-precision elements: 52 blocks a warp
+// PLACEHOLDER); 32-bit steps are bound by memory and take four blocks a warp in as
+// many waves as that makes.
+int32_t blocks_per_warp(int64_t blocks, int32_t bits) {
+  if (bits == 32) return 4;
+  const int64_t warps = (int64_t)sm_count() * 4 * kWarps;
+  const int64_t n = (blocks + warps - 1) / warps;
+  return n < 1 ? 1 : (int32_t)n;
+}
+int32_t tile_count(int64_t blocks, int32_t bits) {
+  const int64_t tile = (int64_t)blocks_per_warp(blocks, bits) * kWarps;
+  return (int32_t)((blocks + tile - 1) / tile);
+}
 
 }  // namespace
 }  // namespace tbe
@@ -403,10 +640,10 @@ extern "C" {
 
 int64_t tbe_adamw_state_blocks(int32_t n, const int64_t* numel) { return count_blocks(n, numel); }
 
-size_t tbe_adamw_plan_device_bytes(int32_t n, const int64_t* numel) {
+size_t tbe_adamw_plan_device_bytes(int32_t n, const int64_t* numel, int32_t state_bits) {
   const int64_t blocks = count_blocks(n, numel);
-  if (blocks < 0) return 0;
-  return meta_bytes(n) + ((size_t)tile_count(blocks) * 4 + 255) / 256 * 256;
+  if (blocks < 0 || (state_bits != 8 && state_bits != 32)) return 0;
+  return meta_bytes(n) + ((size_t)tile_count(blocks, state_bits) * 4 + 255) / 256 * 256;
 }
 
 int tbe_adamw_plan_create(const tbe_adamw_tensors* L, void* dev_meta, size_t dev_meta_bytes, void* stream,
@@ -417,7 +654,7 @@ int tbe_adamw_plan_create(const tbe_adamw_tensors* L, void* dev_meta, size_t dev
   const int64_t blocks = count_blocks(L->n, L->numel);
   if (blocks < 0) return TBE_ERR_INVALID_ARG;
   if (!aligned_to(dev_meta, 16)) return TBE_ERR_UNSUPPORTED;
-  const size_t need = tbe_adamw_plan_device_bytes(L->n, L->numel);
+  const size_t need = tbe_adamw_plan_device_bytes(L->n, L->numel, L->state_bits);
   if (dev_meta_bytes < need) return TBE_ERR_WORKSPACE;
   const size_t mb = meta_bytes(L->n);
   uint8_t* host = new (std::nothrow) uint8_t[need];
@@ -431,6 +668,7 @@ int tbe_adamw_plan_create(const tbe_adamw_tensors* L, void* dev_meta, size_t dev
   TensorMeta* meta = reinterpret_cast<TensorMeta*>(host);
   int32_t* tile = reinterpret_cast<int32_t*>(host + mb);
   int st = TBE_OK;
+  const int64_t tile_blocks = (int64_t)blocks_per_warp(blocks, L->state_bits) * kWarps;
   int64_t at = 0, next_tile = 0;
   for (int32_t i = 0; i < L->n && st == TBE_OK; ++i) {
     const int32_t pd = L->param_dtype[i], gd = L->grad_dtype[i];
@@ -447,7 +685,7 @@ int tbe_adamw_plan_create(const tbe_adamw_tensors* L, void* dev_meta, size_t dev
     m.gdt = (uint8_t)gd;
     m.vec = aligned_to(m.p, pd == TBE_F32 ? 32 : 16) && aligned_to(m.g, gd == TBE_F32 ? 32 : 16);
     const int64_t end = at + (m.numel + kBlock - 1) / kBlock;
-    while (next_tile * kTileBlocks < end) tile[next_tile++] = i;
+    while (next_tile * tile_blocks < end) tile[next_tile++] = i;
     at = end;
   }
   meta[L->n].block0 = 0x7fffffff;
@@ -455,7 +693,15 @@ int tbe_adamw_plan_create(const tbe_adamw_tensors* L, void* dev_meta, size_t dev
     p->n = L->n;
     p->bits = L->state_bits;
     p->blocks = (int32_t)blocks;
-    p->tiles = tile_count(blocks);
+    p->tiles = tile_count(blocks, L->state_bits);
+    p->per_warp = blocks_per_warp(blocks, L->state_bits);
+    p->pdt = L->param_dtype[0];
+    p->gdt = L->grad_dtype[0];
+    for (int32_t i = 1; i < L->n; ++i)
+      if (L->param_dtype[i] != p->pdt || L->grad_dtype[i] != p->gdt) {
+        p->pdt = p->gdt = kMixed;
+        break;
+      }
     cudaGetDevice(&p->device);
     p->dmeta = reinterpret_cast<const TensorMeta*>(dev_meta);
     p->dtile = reinterpret_cast<const int32_t*>(static_cast<uint8_t*>(dev_meta) + mb);
@@ -493,6 +739,7 @@ int tbe_adamw_step(const tbe_adamw_plan* plan, const tbe_adamw* opt, void* exp_a
   a.meta = plan->dmeta;
   a.tile_tensor = plan->dtile;
   a.blocks = plan->blocks;
+  a.per_warp = plan->per_warp;
   a.m = exp_avg;
   a.v = exp_avg_sq;
   a.ms = exp_avg_scale;
@@ -510,8 +757,8 @@ int tbe_adamw_step(const tbe_adamw_plan* plan, const tbe_adamw* opt, void* exp_a
   a.size = (float)(o.learning_rate / (1.0 - std::pow(o.beta1, (double)o.step)));
   cudaStream_t s = (cudaStream_t)stream;
   trace_begin(s);
-  if (plan->bits == 8) adamw_kernel<8><<<plan->tiles, kThreads, 0, s>>>(a);
-  else adamw_kernel<32><<<plan->tiles, kThreads, 0, s>>>(a);
+  if (plan->bits == 8) launch_step<8>(plan->pdt, plan->gdt, plan->tiles, a, s);
+  else launch_step<32>(plan->pdt, plan->gdt, plan->tiles, a, s);
   const int st = check_launch();
   trace_mark(s, "adamw");
   return st;

@@ -34,6 +34,7 @@
 // its end.  The states h_{t-1} of a step are made again from the state it
 // started from, which the forward saved in 32 bits, so h itself is not read.
 #include "tbe_internal.cuh"
+#include "tbe_two.cuh"
 
 #include <cmath>
 
@@ -88,63 +89,7 @@ struct ScanArgs {
   int32_t* status;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float root(float x) {
-  float y;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float inv_root(float x) {
-  float y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
-
-// Two fp32 numbers in one register pair: one instruction for both.
-struct Two {
-  uint64_t v;
-};
-__device__ __forceinline__ Two two(float a, float b) {
-  Two t;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(t.v) : "f"(a), "f"(b));
-  return t;
-}
-__device__ __forceinline__ Two two(float a) { return two(a, a); }
-__device__ __forceinline__ float lo(Two t) {
-  return __uint_as_float((uint32_t)t.v);
-}
-__device__ __forceinline__ float hi(Two t) {
-  return __uint_as_float((uint32_t)(t.v >> 32));
-}
-__device__ __forceinline__ Two operator*(Two a, Two b) {
-  Two t;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t.v) : "l"(a.v), "l"(b.v));
-  return t;
-}
-__device__ __forceinline__ Two operator+(Two a, Two b) {
-  Two t;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t.v) : "l"(a.v), "l"(b.v));
-  return t;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  Two t;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return t;
-}
-__device__ __forceinline__ Two ex2(Two a) { return two(ex2(lo(a)), ex2(hi(a))); }
-__device__ __forceinline__ Two rcp(Two a) { return two(rcp(lo(a)), rcp(hi(a))); }
-__device__ __forceinline__ Two root(Two a) { return two(root(lo(a)), root(hi(a))); }
-__device__ __forceinline__ Two inv_root(Two a) { return two(inv_root(lo(a)), inv_root(hi(a))); }
 
 // a = exp(-u) and 1 - a^2 for u >= 0, both to a few units of their own
 // size.  Below 1/4, n = 1 - a from its series (the next term is under 5e-8 of
@@ -160,16 +105,10 @@ struct Decay {
 // there again at each use.
 struct Constants {
   Two one, minus_log2e, c5, c4, c3, c2, c1, c0;
-  static __device__ __forceinline__ Two keep(float f) {
-    Two t = two(f);
-    asm volatile("" : "+l"(t.v));
-    return t;
-  }
   __device__ __forceinline__ Constants()
       : one(keep(1.f)), minus_log2e(keep(-kLog2e)), c5(keep(1.f / 720.f)), c4(keep(-1.f / 120.f)), c3(keep(1.f / 24.f)),
         c2(keep(-1.f / 6.f)), c1(keep(0.5f)), c0(keep(-1.f)) {}
 };
-__device__ __forceinline__ Two negative(Two t) { return two(-lo(t), -hi(t)); }
 __device__ __forceinline__ Decay<Two> decay_near(Two u, const Constants& k) {
   Two p = fma2(u, k.c5, k.c4);
   p = fma2(u, p, k.c3);

@@ -52,7 +52,7 @@ def declare(lib):
         ("tbe_preference_loss", ctypes.c_int, [P, P, P, P, P, P, P, i64, f32, P, sz, P, P]),
         ("tbe_preference_loss_backward", ctypes.c_int, [P, P, P, f32, P, i64, P]),
         ("tbe_adamw_state_blocks", i64, [i32, P]),
-        ("tbe_adamw_plan_device_bytes", sz, [i32, P]),
+        ("tbe_adamw_plan_device_bytes", sz, [i32, P, i32]),
         ("tbe_adamw_plan_create", ctypes.c_int, [P, P, sz, P, P]),
         ("tbe_adamw_plan_destroy", None, [P]),
         ("tbe_adamw_step", ctypes.c_int, [P, P, P, P, P, P, P, P, P]),
@@ -395,7 +395,7 @@ class AdamWPlan:
         g = np.array([t.data_ptr() for t in grads], dtype=np.uint64)
         pd = np.array([_DTYPE[t.dtype] for t in params], dtype=np.int32)
         gd = np.array([_DTYPE[t.dtype] for t in grads], dtype=np.int32)
-        nbytes = lib.tbe_adamw_plan_device_bytes(n, self.numel.ctypes.data)
+        nbytes = lib.tbe_adamw_plan_device_bytes(n, self.numel.ctypes.data, self.state_bits)
         if nbytes == 0:
             raise _tbe.TBEError("tbe_adamw_plan_device_bytes: sizes out of range")
         meta = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
