@@ -75,7 +75,7 @@ __device__ const Levels kLevels = Levels();
 
 __device__ __forceinline__ float sqrt_approx(float x) {
   float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm volatile("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 // Eight consecutive 32-bit words: one 32-byte access.
@@ -422,13 +422,19 @@ __device__ __forceinline__ void step_8(const StepArgs& a, const Raw8<PDT, GDT>& 
   // magnitudes order like their bits, NaN above infinity
   top_m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top_m)));
   top_v = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top_v)));
+  // With an eps of at least 1e-10, the root of a v below the normal numbers
+  // (under 1.1e-19) does not show beside it, and may count as 0.
   Two w[kPer / 2];
+  if (a.eps >= 1e-10f) {
+#pragma unroll
+    for (int j = 0; j < kPer / 2; ++j) w[j] = root(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer / 2; ++j) w[j] = two(sqrt_approx(lo(v[j])), sqrt_approx(hi(v[j])));
+  }
 #pragma unroll
   for (int j = 0; j < kPer / 2; ++j) {
-    // With an eps of at least 1e-10, the root of a v below the normal numbers
-    // (under 1.1e-19) does not show beside it, and may count as 0.
-    const Two top = a.eps >= 1e-10f ? two(root(lo(v[j])), root(hi(v[j]))) : two(sqrt_approx(lo(v[j])), sqrt_approx(hi(v[j])));
-    const Two bottom = fma2(top, two(a.root_scale), two(a.eps));
+    const Two bottom = fma2(w[j], two(a.root_scale), two(a.eps));
     const Two p = raw_pair<PDT>(x.p, j);
     // the whole change first: the weight itself is rounded once
     w[j] = p + negative(fma2(two(a.size), m[j] * rcp(bottom), p * two(a.decay)));
@@ -440,32 +446,35 @@ __device__ __forceinline__ void step_8(const StepArgs& a, const Raw8<PDT, GDT>& 
   else if (PDT == TBE_F16) store_out(reinterpret_cast<__half*>(pp), f, kPer, true);
   else store_out(reinterpret_cast<__nv_bfloat16*>(pp), f, kPer, true);
   float scale_m, scale_v;
-  const Two inv_m = two(block_inverse(top_m, &scale_m)), inv_v = two(block_inverse(top_v, &scale_v));
+  const float inv_m = block_inverse(top_m, &scale_m), inv_v = block_inverse(top_v, &scale_v);
+  // roots in codes: the codes' number goes under the root with the scale
+  const Two km = two(inv_m * 16129.f), kv = two(inv_v * 4228250625.f);
   const Two magic = two(12582912.f), back = two(-12582912.f);
   uint32_t cq[kPer], cz[kPer];
   float off = 0.f;
 #pragma unroll
   for (int j = 0; j < kPer / 2; ++j) {
-    const Two ym = m[j] * inv_m, yv = v[j] * inv_v;
-    Two c = two(copysignf(root(fabsf(lo(ym))), lo(ym)), copysignf(root(fabsf(hi(ym))), hi(ym))) * two(127.f);
+    const Two ym = m[j] * km, yv = v[j] * kv;
+    Two c = two(copysignf(root(fabsf(lo(ym))), lo(ym)), copysignf(root(fabsf(hi(ym))), hi(ym)));
     Two r = c + magic;
     Two d = c + negative(r + back);
     off = fmaxf(fmaxf(off, fabsf(lo(d))), fabsf(hi(d)));
     cq[2 * j] = __float_as_uint(lo(r));
     cq[2 * j + 1] = __float_as_uint(hi(r));
-    c = two(root(root(lo(yv))), root(root(hi(yv)))) * two(255.f);
+    c = root(root(yv));
+    // at least 1 for what is not 0
+    c = two(fmaxf(lo(c), __saturatef(lo(c) * 1e30f)), fmaxf(hi(c), __saturatef(hi(c) * 1e30f)));
     r = c + magic;
     d = c + negative(r + back);
     off = fmaxf(fmaxf(off, fabsf(lo(d))), fabsf(hi(d)));
-    // at least 1 for what is not 0 (yv is not negative: its bits are at least 1 then)
-    cz[2 * j] = max(__float_as_uint(lo(r)), 0x4b400000u + min(__float_as_uint(lo(yv)), 1u));
-    cz[2 * j + 1] = max(__float_as_uint(hi(r)), 0x4b400000u + min(__float_as_uint(hi(yv)), 1u));
+    cz[2 * j] = __float_as_uint(lo(r));
+    cz[2 * j + 1] = __float_as_uint(hi(r));
   }
   if (off > kNearLevel) {  // some code is close to its neighbour: its level decides
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const float mj = j & 1 ? hi(m[j / 2]) : lo(m[j / 2]), vj = j & 1 ? hi(v[j / 2]) : lo(v[j / 2]);
-      const float ym = fminf(__fmul_rn(fabsf(mj), lo(inv_m)), 1.f), yv = fminf(__fmul_rn(vj, lo(inv_v)), 1.f);
+      const float ym = fminf(__fmul_rn(fabsf(mj), inv_m), 1.f), yv = fminf(__fmul_rn(vj, inv_v), 1.f);
       const int q = nearest_code(127.f * root(ym), ym, kLevels.m);
       const int z = nearest_code(255.f * root(root(yv)), yv, kLevels.v);
       cq[j] = mj < 0.f ? -q : q;
