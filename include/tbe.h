@@ -490,8 +490,9 @@ typedef struct tbe_preference_inputs {
   float label_smoothing;
 } tbe_preference_inputs;
 
-/* Workspace (device, 256-byte aligned, no initialisation needed). */
-size_t tbe_preference_workspace_bytes(int64_t tokens, int32_t vocab, int32_t pairs);
+/* Workspace on the current device (device memory, 256-byte aligned, no
+ * initialisation needed). */
+size_t tbe_preference_workspace_bytes(int64_t tokens, int32_t vocab, int32_t pairs, int32_t dtype);
 
 /*   loss      : device fp32 scalar
  *   seq_logps : device fp32 [2 * pairs], s_q

@@ -25,6 +25,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;
+// A warp takes a row where rows are short enough.
+constexpr int kWarpRow = 1024;
 
 struct PrefArgs {
   const void* logits;
@@ -46,7 +48,7 @@ struct PrefArgs {
   int64_t dstride;
   float2* part;      // [N, splits] running maximum and sum
   float* lp;         // [N]
-  float* block_loss; // one per block of the pairs' kernel
+  float* block_loss; // one per block of the pairs' kernel, or per pair
   uint32_t* arrived;
   int32_t* status;
 };
@@ -191,6 +193,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(PrefArgs a) {
   __shared__ Run s_run[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.arrived = 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (WARP) {
     const int64_t n = (int64_t)blockIdx.x * kWarps + warp;
     if (n >= a.N) return;
@@ -217,56 +220,62 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(PrefArgs a) {
   }
 }
 
+// Pair b, by one warp: the sequences' sums, the margin, the loss (returned)
+// and the tokens' coefficients.
+template <int DT>
+__device__ __forceinline__ float pair_loss(const PrefArgs& a, int64_t b, int lane) {
+  float logp[2];
+  int64_t lo[2], hi[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int64_t q = (int64_t)t * a.P + b;
+    lo[t] = a.offsets[q];
+    hi[t] = a.offsets[q + 1];
+    const bool bad = lo[t] < 0 || hi[t] < lo[t] || hi[t] > a.N || (q == 0 && lo[t] != 0) ||
+                     (q == 2 * (int64_t)a.P - 1 && hi[t] != a.N);
+    if (bad && lane == 0) report(a.status, TBE_DEV_BAD_OFFSETS);
+    if (lo[t] < 0) lo[t] = 0;
+    if (hi[t] > a.N) hi[t] = a.N;
+    float s = 0.f;
+    for (int64_t n = lo[t] + lane; n < hi[t]; n += 32) {
+      if (a.splits > 1) {
+        Run r{kLowest, 0.f};
+        for (int p = 0; p < a.splits; ++p) {
+          const float2 v = __ldcg(a.part + n * a.splits + p);
+          r = merge(r, Run{v.x, v.y});
+        }
+        finish_row<DT>(a, n, r);
+      }
+      s += __ldcg(a.lp + n);
+    }
+    logp[t] = warp_sum(s);
+    if (lane == 0) a.logps[q] = logp[t];
+  }
+  const float d = a.beta * ((logp[0] - a.ref[b]) - (logp[1] - a.ref[a.P + b]));
+  // log(1 + exp(-d)) and log(1 + exp(d)) without overflow
+  const float l = log1pf(expf(-fabsf(d)));
+  const float loss = (1.f - a.smoothing) * (fmaxf(-d, 0.f) + l) + a.smoothing * (fmaxf(d, 0.f) + l);
+  const float up = 1.f / (1.f + expf(-d)), down = 1.f / (1.f + expf(d));
+  const float c = a.beta / (float)a.P * (a.smoothing * up - (1.f - a.smoothing) * down);
+  if (lane == 0) a.margins[b] = d;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+    for (int64_t n = lo[t] + lane; n < hi[t]; n += 32) {
+      const int64_t y = a.labels[n];
+      a.coef[n] = y < 0 || y >= a.V || __ldcg(a.lse + n) == -INFINITY ? 0.f : (t == 0 ? c : -c);
+    }
+  return loss;
+}
+
 // A warp per pair.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) pairs_kernel(PrefArgs a) {
   __shared__ float s_loss[kWarps];
   __shared__ bool s_last;
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t b = (int64_t)blockIdx.x * kWarps + warp;
-  float loss = 0.f;
-  if (b < a.P) {
-    float logp[2];
-    int64_t lo[2], hi[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int64_t q = (int64_t)t * a.P + b;
-      lo[t] = a.offsets[q];
-      hi[t] = a.offsets[q + 1];
-      const bool bad = lo[t] < 0 || hi[t] < lo[t] || hi[t] > a.N || (q == 0 && lo[t] != 0) ||
-                       (q == 2 * (int64_t)a.P - 1 && hi[t] != a.N);
-      if (bad && lane == 0) report(a.status, TBE_DEV_BAD_OFFSETS);
-      if (lo[t] < 0) lo[t] = 0;
-      if (hi[t] > a.N) hi[t] = a.N;
-      float s = 0.f;
-      for (int64_t n = lo[t] + lane; n < hi[t]; n += 32) {
-        if (a.splits > 1) {
-          Run r{kLowest, 0.f};
-          for (int p = 0; p < a.splits; ++p) {
-            const float2 v = a.part[n * a.splits + p];
-            r = merge(r, Run{v.x, v.y});
-          }
-          finish_row<DT>(a, n, r);
-        }
-        s += a.lp[n];
-      }
-      logp[t] = warp_sum(s);
-      if (lane == 0) a.logps[q] = logp[t];
-    }
-    const float d = a.beta * ((logp[0] - a.ref[b]) - (logp[1] - a.ref[a.P + b]));
-    // log(1 + exp(-d)) and log(1 + exp(d)) without overflow
-    const float l = log1pf(expf(-fabsf(d)));
-    loss = (1.f - a.smoothing) * (fmaxf(-d, 0.f) + l) + a.smoothing * (fmaxf(d, 0.f) + l);
-    const float up = 1.f / (1.f + expf(-d)), down = 1.f / (1.f + expf(d));
-    const float c = a.beta / (float)a.P * (a.smoothing * up - (1.f - a.smoothing) * down);
-    if (lane == 0) a.margins[b] = d;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      for (int64_t n = lo[t] + lane; n < hi[t]; n += 32) {
-        const int64_t y = a.labels[n];
-        a.coef[n] = y < 0 || y >= a.V || a.lse[n] == -INFINITY ? 0.f : (t == 0 ? c : -c);
-      }
-  }
+  const float loss = b < a.P ? pair_loss<DT>(a, b, lane) : 0.f;
   if (lane == 0) s_loss[warp] = loss;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -358,6 +367,7 @@ __device__ __forceinline__ void grad_row(const uint8_t* p, uint8_t* o, int64_t n
 
 template <int DT, bool WARP>
 __global__ void __launch_bounds__(kThreads) grad_kernel(PrefArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n = WARP ? (int64_t)blockIdx.x * kWarps + warp : blockIdx.x / a.splits;
   if (n >= a.N) return;
@@ -368,12 +378,84 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(PrefArgs a) {
                a.labels[n] - lo, coef, a.lse[n], WARP ? lane : threadIdx.x, WARP ? 32 : kThreads);
 }
 
-// A warp takes a row where rows are short enough.
-constexpr int kWarpRow = 1024;
+// Small batches in one launch: one cluster of kSmallBlocks thread blocks goes
+// through the three steps, its barrier between them.  A warp takes a short
+// row, a block a long one; long rows are cut over blocks where there are fewer
+// of them than blocks.
+constexpr int kSmallBlocks = 16, kSmallThreads = 512, kSmallWarps = kSmallThreads / 32;
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+template <int DT>
+__global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
+  __shared__ Run s_run[kSmallWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int me = blockIdx.x * kSmallWarps + warp;  // the grid is one cluster
+  const bool by_warp = a.V <= kWarpRow;
+  if (by_warp) {
+    for (int64_t n = me; n < a.N; n += kSmallBlocks * kSmallWarps) {
+      const Run r = warp_merge(sum_row<DT>(elem_ptr<DT>(a.logits, n * a.stride), a.V, lane, 32));
+      if (lane == 0) {
+        finish_row<DT>(a, n, r);
+        a.coef[n] = 0.f;
+      }
+    }
+  } else {
+    for (int64_t u = blockIdx.x; u < a.N * a.splits; u += kSmallBlocks) {
+      const int64_t n = u / a.splits, part = u % a.splits;
+      const int64_t lo = a.V * part / a.splits, hi = a.V * (part + 1) / a.splits;
+      Run r = warp_merge(sum_row<DT>(elem_ptr<DT>(a.logits, n * a.stride + lo), hi - lo, threadIdx.x, kSmallThreads));
+      if (lane == 0) s_run[warp] = r;
+      __syncthreads();
+      if (warp == 0) {
+        r = warp_merge(lane < kSmallWarps ? s_run[lane] : Run{kLowest, 0.f});
+        if (lane == 0) {
+          if (a.splits == 1) finish_row<DT>(a, n, r);
+          else a.part[u] = make_float2(r.m, r.s);
+          if (part == 0) a.coef[n] = 0.f;
+        }
+      }
+      __syncthreads();
+    }
+  }
+  cluster_sync();
+  for (int64_t b = me; b < a.P; b += kSmallBlocks * kSmallWarps) {
+    const float loss = pair_loss<DT>(a, b, lane);
+    if (lane == 0) a.block_loss[b] = loss;
+  }
+  cluster_sync();
+  if (me == 0) {
+    float s = 0.f;
+    for (int64_t b = lane; b < a.P; b += 32) s += __ldcg(a.block_loss + b);
+    s = warp_sum(s);
+    if (lane == 0) *a.loss = s / (float)a.P;
+  }
+  if (!a.dlogits) return;
+  const int64_t units = by_warp ? a.N : a.N * a.splits, step = by_warp ? kSmallBlocks * kSmallWarps : kSmallBlocks;
+  for (int64_t u = by_warp ? me : blockIdx.x; u < units; u += step) {
+    const int64_t n = u / a.splits, part = u % a.splits;
+    const int64_t lo = a.V * part / a.splits, hi = a.V * (part + 1) / a.splits;
+    grad_row<DT>(elem_ptr<DT>(a.logits, n * a.stride + lo), elem_ptr<DT>(a.dlogits, n * a.dstride + lo), hi - lo,
+                 a.labels[n] - lo, __ldcg(a.coef + n) * a.scale, __ldcg(a.lse + n), by_warp ? lane : threadIdx.x,
+                 by_warp ? 32 : kSmallThreads);
+  }
+}
+
+
+// Batches of at most this many bytes of logits go through one cluster.
+constexpr int64_t kSmallBytes = 4 << 20;
 
 // Blocks per row: where there are fewer rows than would fill the GPU twice
 // over, rows are cut, into pieces of at least 2048 entries.
-int32_t splits_of(int64_t N, int32_t V) {
+// (One cluster: as many as it has blocks.)
+bool is_small(int64_t N, int32_t V, int32_t dtype) { return N * (int64_t)V * (dtype == TBE_F32 ? 4 : 2) <= kSmallBytes; }
+int32_t splits_of(int64_t N, int32_t V, int32_t dtype) {
+  if (is_small(N, V, dtype)) {
+    if (V <= kWarpRow || N < 1) return 1;
+    const int64_t want = kSmallBlocks / N, most = V / 2048;
+    const int64_t s = want < most ? want : most;
+    return s < 1 ? 1 : (int32_t)s;
+  }
   if (N <= 0 || V <= kWarpRow) return 1;
   const int64_t want = (4 * (int64_t)sm_count() + N - 1) / N, most = V / 2048;
   const int64_t s = want < most ? want : most;
@@ -384,40 +466,81 @@ struct Workspace {
   size_t part, lp, block_loss, bytes;
 };
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
-Workspace layout(int64_t N, int32_t V, int32_t P) {
+Workspace layout(int64_t N, int32_t V, int32_t P, int32_t dtype) {
   Workspace w;
   size_t at = 256;  // the arrival counter
   w.part = at;
-  const int32_t s = splits_of(N, V);
+  const int32_t s = splits_of(N, V, dtype);
   if (s > 1) at += round256((size_t)N * s * sizeof(float2));
   w.lp = at;
   at += round256((size_t)N * 4);
   w.block_loss = at;
-  at += round256(((size_t)P + kWarps - 1) / kWarps * 4);
+  at += round256((size_t)P * 4);
   w.bytes = at;
   return w;
 }
 
-template <int DT>
-int launch_grad(const PrefArgs& a, cudaStream_t s) {
-  if (a.V <= kWarpRow) grad_kernel<DT, true><<<(unsigned)((a.N + kWarps - 1) / kWarps), kThreads, 0, s>>>(a);
-  else grad_kernel<DT, false><<<(unsigned)(a.N * a.splits), kThreads, 0, s>>>(a);
-  return check_launch();
+// A launch that may start while the kernel before it ends (`after`).
+template <typename K>
+int start(K kernel, int64_t grid, bool after, cudaStream_t s, const PrefArgs& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? check_launch() : TBE_ERR_CUDA;
 }
 
 template <int DT>
-int launch_loss(const PrefArgs& a, cudaStream_t s) {
-  if (a.V <= kWarpRow) rows_kernel<DT, true><<<(unsigned)((a.N + kWarps - 1) / kWarps), kThreads, 0, s>>>(a);
-  else rows_kernel<DT, false><<<(unsigned)(a.N * a.splits), kThreads, 0, s>>>(a);
-  int st = check_launch();
+int launch_grad(const PrefArgs& a, bool after, cudaStream_t s) {
+  // (a small batch's rows may be cut finer here than a block needs: still right)
+  return a.V <= kWarpRow ? start(grad_kernel<DT, true>, (a.N + kWarps - 1) / kWarps, after, s, a)
+                         : start(grad_kernel<DT, false>, a.N * a.splits, after, s, a);
+}
+
+template <int DT>
+int launch_small(const PrefArgs& a, cudaStream_t s) {
+  static bool allowed[64] = {};  // once per device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !allowed[dev]) {
+    if (cudaFuncSetAttribute(small_kernel<DT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return TBE_ERR_CUDA;
+    if (dev >= 0 && dev < 64) allowed[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSmallBlocks);
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kSmallBlocks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, small_kernel<DT>, a) == cudaSuccess ? check_launch() : TBE_ERR_CUDA;
+}
+
+template <int DT>
+int launch_loss(const PrefArgs& a, int32_t dtype, cudaStream_t s) {
+  if (is_small(a.N, a.V, dtype)) {
+    const int st = launch_small<DT>(a, s);
+    trace_mark(s, "preference_small");
+    return st;
+  }
+  int st = a.V <= kWarpRow ? start(rows_kernel<DT, true>, (a.N + kWarps - 1) / kWarps, false, s, a)
+                           : start(rows_kernel<DT, false>, a.N * a.splits, false, s, a);
   if (st != TBE_OK) return st;
   trace_mark(s, "preference_rows");
-  pairs_kernel<DT><<<(unsigned)((a.P + kWarps - 1) / kWarps), kThreads, 0, s>>>(a);
-  st = check_launch();
+  st = start(pairs_kernel<DT>, ((int64_t)a.P + kWarps - 1) / kWarps, true, s, a);
   if (st != TBE_OK) return st;
   trace_mark(s, "preference_pairs");
   if (a.dlogits) {
-    st = launch_grad<DT>(a, s);
+    st = launch_grad<DT>(a, true, s);
     trace_mark(s, "preference_grad");
   }
   return st;
@@ -432,7 +555,7 @@ int check(const tbe_preference_inputs* in) {
   if (!std::isfinite(in->beta) || !(in->label_smoothing >= 0.f && in->label_smoothing <= 1.f)) return TBE_ERR_INVALID_ARG;
   if (!in->logits || !in->labels || !in->offsets || !in->ref_logps) return TBE_ERR_INVALID_ARG;
   if (!aligned_for(in->logits, in->dtype)) return TBE_ERR_UNSUPPORTED;
-  if (in->tokens * (int64_t)splits_of(in->tokens, in->vocab) >= (int64_t(1) << 31) || in->pairs >= (1 << 30))
+  if (in->tokens * (int64_t)splits_of(in->tokens, in->vocab, in->dtype) >= (int64_t(1) << 31) || in->pairs >= (1 << 30))
     return TBE_ERR_UNSUPPORTED;
   return TBE_OK;
 }
@@ -449,7 +572,7 @@ PrefArgs args_of(const tbe_preference_inputs* in) {
   a.P = in->pairs;
   a.beta = in->beta;
   a.smoothing = in->label_smoothing;
-  a.splits = splits_of(in->tokens, in->vocab);
+  a.splits = splits_of(in->tokens, in->vocab, in->dtype);
   return a;
 }
 
@@ -460,9 +583,9 @@ using namespace tbe;
 
 extern "C" {
 
-size_t tbe_preference_workspace_bytes(int64_t tokens, int32_t vocab, int32_t pairs) {
+size_t tbe_preference_workspace_bytes(int64_t tokens, int32_t vocab, int32_t pairs, int32_t dtype) {
   if (tokens < 1 || vocab < 1 || pairs < 1) return 0;
-  return layout(tokens, vocab, pairs).bytes;
+  return layout(tokens, vocab, pairs, dtype).bytes;
 }
 
 int tbe_preference_loss(const tbe_preference_inputs* in, float* loss, float* seq_logps, float* margins, float* lse,
@@ -473,7 +596,7 @@ int tbe_preference_loss(const tbe_preference_inputs* in, float* loss, float* seq
   if (!loss || !seq_logps || !margins || !lse || !coef || !workspace) return TBE_ERR_INVALID_ARG;
   if (dlogits && (dlogits_stride < in->vocab || !std::isfinite(grad_scale))) return TBE_ERR_INVALID_ARG;
   if (!aligned_for(dlogits, in->dtype) || ((uintptr_t)workspace & 255)) return TBE_ERR_UNSUPPORTED;
-  const Workspace w = layout(in->tokens, in->vocab, in->pairs);
+  const Workspace w = layout(in->tokens, in->vocab, in->pairs, in->dtype);
   if (workspace_bytes < w.bytes) return TBE_ERR_WORKSPACE;
   uint8_t* p = static_cast<uint8_t*>(workspace);
   PrefArgs a = args_of(in);
@@ -492,9 +615,9 @@ int tbe_preference_loss(const tbe_preference_inputs* in, float* loss, float* seq
   a.status = dev_status;
   cudaStream_t s = (cudaStream_t)stream;
   trace_begin(s);
-  if (in->dtype == TBE_F32) return launch_loss<TBE_F32>(a, s);
-  if (in->dtype == TBE_F16) return launch_loss<TBE_F16>(a, s);
-  return launch_loss<TBE_BF16>(a, s);
+  if (in->dtype == TBE_F32) return launch_loss<TBE_F32>(a, in->dtype, s);
+  if (in->dtype == TBE_F16) return launch_loss<TBE_F16>(a, in->dtype, s);
+  return launch_loss<TBE_BF16>(a, in->dtype, s);
 }
 
 int tbe_preference_loss_backward(const tbe_preference_inputs* in, const float* lse, const float* coef,
@@ -511,9 +634,9 @@ int tbe_preference_loss_backward(const tbe_preference_inputs* in, const float* l
   a.scale = grad_scale;
   cudaStream_t s = (cudaStream_t)stream;
   trace_begin(s);
-  const int rc = in->dtype == TBE_F32   ? launch_grad<TBE_F32>(a, s)
-                 : in->dtype == TBE_F16 ? launch_grad<TBE_F16>(a, s)
-                                        : launch_grad<TBE_BF16>(a, s);
+  const int rc = in->dtype == TBE_F32   ? launch_grad<TBE_F32>(a, false, s)
+                 : in->dtype == TBE_F16 ? launch_grad<TBE_F16>(a, false, s)
+                                        : launch_grad<TBE_BF16>(a, false, s);
   trace_mark(s, "preference_grad");
   return rc;
 }

@@ -48,7 +48,7 @@ def declare(lib):
         ("tbe_gated_scan", ctypes.c_int, [P, P, i64, P, P, P, sz, P, P]),
         ("tbe_gated_scan_backward", ctypes.c_int, [P, P, i64, P, P, P, P, sz, P, P]),
         ("tbe_gated_scan_step", ctypes.c_int, [P, P, P, i64, P]),
-        ("tbe_preference_workspace_bytes", sz, [i64, i32, i32]),
+        ("tbe_preference_workspace_bytes", sz, [i64, i32, i32, i32]),
         ("tbe_preference_loss", ctypes.c_int, [P, P, P, P, P, P, P, i64, f32, P, sz, P, P]),
         ("tbe_preference_loss_backward", ctypes.c_int, [P, P, P, f32, P, i64, P]),
         ("tbe_adamw_state_blocks", i64, [i32, P]),
@@ -118,9 +118,9 @@ def _scan_workspace(N, C, backward, dev):
 
 
 @functools.lru_cache(maxsize=4096)
-def _preference_workspace(N, V, P, dev):
+def _preference_workspace(N, V, P, dtype, dev):
     with torch.cuda.device(dev):
-        return int(_tbe.load_library().tbe_preference_workspace_bytes(N, V, P))
+        return int(_tbe.load_library().tbe_preference_workspace_bytes(N, V, P, _DTYPE[dtype]))
 
 
 # ---------------------------------------------------------------------------
@@ -246,13 +246,25 @@ def tbe_gated_scan_step(x, recur, gate, decay, state, sharpness: float = 8.0, ou
 # preference loss
 # ---------------------------------------------------------------------------
 
-class PreferenceLoss(NamedTuple):
-    loss: torch.Tensor  # fp32 scalar
-    seq_logps: torch.Tensor  # fp32 [2 * pairs]
-    margins: torch.Tensor  # fp32 [pairs]
-    dlogits: torch.Tensor | None  # laid out like the logits
-    lse: torch.Tensor  # fp32 [tokens]; with coef, for tbe_preference_loss_backward
-    coef: torch.Tensor  # fp32 [tokens]
+class PreferenceLoss:
+    """Results of ``tbe_preference_loss``, views of one fp32 buffer: ``loss``
+    (scalar), ``seq_logps`` [2 * pairs], ``margins`` [pairs], ``lse`` and
+    ``coef`` [tokens] (for ``tbe_preference_loss_backward``); and ``dlogits``
+    (laid out like the logits) or None."""
+
+    __slots__ = ("_room", "_pairs", "_tokens", "dlogits")
+
+    def __init__(self, room, pairs, tokens, dlogits):
+        self._room, self._pairs, self._tokens, self.dlogits = room, pairs, tokens, dlogits
+
+    loss = property(lambda self: self._room[0])
+    seq_logps = property(lambda self: self._room.narrow(0, 1, 2 * self._pairs))
+    margins = property(lambda self: self._room.narrow(0, 1 + 2 * self._pairs, self._pairs))
+    lse = property(lambda self: self._room.narrow(0, 1 + 3 * self._pairs, self._tokens))
+    coef = property(lambda self: self._room.narrow(0, 1 + 3 * self._pairs + self._tokens, self._tokens))
+
+    def __iter__(self):
+        return iter((self.loss, self.seq_logps, self.margins, self.dlogits, self.lse, self.coef))
 
 
 def _preference_inputs(logits, labels, offsets, ref_logps, beta, label_smoothing):
@@ -302,17 +314,14 @@ def tbe_preference_loss(logits, labels, offsets, ref_logps, beta: float = 0.1, l
         dlogits, d_stride = _like_rows(logits, N, V, stride), stride
     st = None if dev_status is None else _vector(dev_status, (1,), _I32, dev, "dev_status")
     # one allocation: the results, then the workspace on 256 bytes
-    sizes = (1, 2 * P, P, N, N)
-    used = 4 * (1 + 3 * P + 2 * N)
-    start = -(-used // 256) * 256
-    nbytes = _preference_workspace(N, V, P, dev)
+    start = -(-4 * (1 + 3 * P + 2 * N) // 256) * 256
+    nbytes = _preference_workspace(N, V, P, dt, dev)
     room = ref_logps.new_empty((start + nbytes) // 4)
     at = room.data_ptr()
     _run(lib.tbe_preference_loss, "tbe_preference_loss", dev, stream, a, at, at + 4, at + 4 + 8 * P, at + 4 + 12 * P,
          at + 4 + 12 * P + 4 * N, None if dlogits is None else dlogits.data_ptr(), d_stride, grad_scale, at + start,
          nbytes, st)
-    loss, seq_logps, margins, lse, coef, _ = room.split_with_sizes((*sizes, room.numel() - used // 4))
-    return PreferenceLoss(loss.view(()), seq_logps, margins, dlogits, lse, coef)
+    return PreferenceLoss(room, P, N, dlogits)
 
 
 def tbe_preference_loss_backward(logits, labels, offsets, ref_logps, saved: PreferenceLoss, grad_scale: float = 1.0,
