@@ -83,7 +83,9 @@ struct ScanArgs {
   void* dg;
   int64_t sdx, sdr, sdg;
   float* dh0;
-  float* partial;    // [blocks * kWarps, C]: each run's share of the decay's gradient
+  float* partial;    // [blocks, C]: each block's share of the decay's gradient
+  float* ddecay;
+  uint32_t* arrived; // [cblocks]: blocks that have written their share
   float2* warp_map;  // [blocks * kWarps, Cp]
   float2* block_map; // [blocks, Cp]
   int32_t* status;
@@ -680,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<BACK>) maps_kernel(Scan
   uint8_t* mine = mem + warp * kMapBytes<DT>(BACK);
   const Map m = BACK ? run_map_back<DT, WIDE>(a, p, mine, speed, near, lane) : run_map<DT, WIDE>(a, p, mine, speed, near, lane);
   const int64_t k = blockIdx.x / a.cblocks;
+  if (BACK && k == 0 && threadIdx.x == 0) a.arrived[blockIdx.x] = 0;  // for the backward kernel, which waits for this one
   runs[warp][lane] = m;
   a.warp_map[(k * kWarps + warp) * a.Cp + p.c] = word_of(m);
   __syncthreads();
@@ -964,28 +967,47 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<true>) backward_kernel(
     ring.done();
   }
   cp_wait<0>();
-  if (p.on) a.partial[((int64_t)(blockIdx.x / a.cblocks) * kWarps + warp) * a.C + p.c] = lo(sum) + hi(sum);
-}
 
-// ddecay = sigmoid(decay) / softplus(decay) * sum over the runs, 32 channels
-// per block, its warps each a share of the runs.
-constexpr int kSumWarps = 16;
-__global__ void __launch_bounds__(kSumWarps * 32)
-    decay_grad_kernel(const float* partial, const float* decay, float* ddecay, int32_t rows, int32_t C) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float part[kSumWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  float s = 0.f;
-  if (c < C)
-    for (int64_t k = warp; k < rows; k += kSumWarps) s += partial[k * C + c];
-  part[warp][lane] = s;
+  // The decay's gradient: the warps' shares, then the blocks', always added in
+  // the same order, the blocks' by the last of them to finish.
+  __shared__ float shares[kWarps][32];
+  __shared__ bool s_last;
+  const int64_t block = blockIdx.x / a.cblocks;
+  shares[warp][lane] = lo(sum) + hi(sum);
   __syncthreads();
-  if (warp == 0 && c < C) {
-    for (int w = 1; w < kSumWarps; ++w) s += part[w][lane];
-    const float d = decay[c], sp = softplus(d);
-    // far below zero softplus(d) = sigmoid(d) = exp(d): the ratio is 1
-    ddecay[c] = d < -16.f ? s : s * (1.f / (1.f + expf(-d))) / sp;
+  float total = 0.f;
+  if (warp == 0) {
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += shares[w][lane];
+  }
+  if (!ALONE) {
+    if (warp == 0) {
+      if (p.on) a.partial[block * a.C + p.c] = total;
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) s_last = atomicAdd(a.arrived + blockIdx.x % a.cblocks, 1u) == (uint32_t)a.blocks - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    total = 0.f;
+    if (p.on) {
+#pragma unroll 8
+      for (int64_t k = warp; k < a.blocks; k += kWarps) total += __ldcg(a.partial + k * a.C + p.c);
+    }
+    shares[warp][lane] = total;
+    __syncthreads();
+    total = 0.f;
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) total += shares[w][lane];
+    }
+  }
+  if (warp == 0 && p.on) {
+    const float d = a.decay[p.c], sp = softplus(d);
+    // ddecay = sigmoid(decay) / softplus(decay) * total; far below zero both
+    // are exp(decay) and the ratio is 1
+    a.ddecay[p.c] = d < -16.f ? total : total * (1.f / (1.f + expf(-d))) / sp;
   }
 }
 
@@ -1027,23 +1049,28 @@ Split split_of(int64_t N, int32_t cblocks, bool back) {
   return s;
 }
 
-// The workspace: maps of blocks and runs, then the backward's partial sums.
+// The workspace: maps of blocks and runs, then the backward's partial sums
+// and counters.  A batch of one block needs none.
 struct Workspace {
-  size_t block, warp, partial, bytes;
+  size_t block, warp, partial, arrived, bytes;
 };
 Workspace layout(int64_t N, int32_t C, bool backward) {
   const Split sp = split_of(N, channel_blocks(C), backward);
   const size_t Cp = (size_t)channel_blocks(C) * 32;
   Workspace w;
   size_t at = 0;
-  w.block = w.warp = 0;
+  w.block = w.warp = w.arrived = 0;
   if (sp.blocks > 1) {
     at += round256((size_t)sp.blocks * Cp * sizeof(float2));
     w.warp = at;
     at += round256((size_t)sp.blocks * kWarps * Cp * sizeof(float2));
   }
   w.partial = at;
-  if (backward) at += round256((size_t)sp.blocks * kWarps * C * 4);
+  if (backward && sp.blocks > 1) {
+    at += round256((size_t)sp.blocks * C * 4);
+    w.arrived = at;
+    at += round256((size_t)channel_blocks(C) * 4);
+  }
   w.bytes = at;
   return w;
 }
@@ -1189,6 +1216,7 @@ int use_workspace(ScanArgs& a, bool backward, void* workspace, size_t bytes) {
   a.block_map = reinterpret_cast<float2*>(p + w.block);
   a.warp_map = reinterpret_cast<float2*>(p + w.warp);
   a.partial = reinterpret_cast<float*>(p + w.partial);
+  a.arrived = reinterpret_cast<uint32_t*>(p + w.arrived);
   return TBE_OK;
 }
 
@@ -1256,27 +1284,13 @@ int tbe_gated_scan_backward(const tbe_scan_inputs* in, const void* dh, int64_t d
   a.sdr = out->drecur_stride;
   a.sdg = out->dgate_stride;
   a.dh0 = out->dh0;
+  a.ddecay = out->ddecay;
   a.status = dev_status;
   trace_begin(s);
   st = use_workspace(a, true, workspace, workspace_bytes);
   if (st != TBE_OK) return st;
   st = dispatch(a, in->dtype, kBackward, s);
-  if (st != TBE_OK) return st;
   trace_mark(s, "gated_scan_backward");
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.C + 31) / 32));
-  cfg.blockDim = dim3(kSumWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, decay_grad_kernel, (const float*)a.partial, a.decay, out->ddecay, a.blocks * kWarps,
-                         a.C) != cudaSuccess)
-    return TBE_ERR_CUDA;
-  st = check_launch();
-  trace_mark(s, "decay_grad");
   return st;
 }
 
