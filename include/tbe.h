@@ -415,7 +415,7 @@ int64_t tbe_gated_scan_states(int64_t tokens);
 /* Workspace (device, 256-byte aligned; no initialisation needed; 0 bytes for
  * the smallest batches) of tbe_gated_scan (backward = 0) or
  * tbe_gated_scan_backward (1) on the current device. */
-size_t tbe_gated_scan_workspace_bytes(int64_t tokens, int32_t channels, int32_t backward);
+size_t tbe_gated_scan_workspace_bytes(int64_t tokens, int32_t channels, int32_t dtype, int32_t backward);
 
 /*   h       : device [tokens, channels] of dtype, h_stride elements from
  *             token to token: every h_t, rounded once

@@ -9,9 +9,9 @@
 // is cut (its state enters as a term of its own), so the work splits into
 // equal runs of the token axis whatever the lengths are.
 //
-// A warp takes a run of tokens and 32 channels, a block's warps neighbouring
-// runs.  h over a run is the linear map h_out = A h_in + B, so two passes do
-// it:
+// A warp takes a run of tokens and 32 or 64 channels, a block's warps
+// neighbouring runs.  h over a run is the linear map h_out = A h_in + B, so two
+// passes do it:
 //  - maps: each run's map (only from the last start in it on, if there is
 //    one), joined over the block;
 //  - apply: each block joins the maps of the blocks before it, back to the
@@ -49,7 +49,16 @@ constexpr int kThreads = kWarps * 32;
 // backward would spill there
 template <bool BACK>
 constexpr int kBlocksPerSm = BACK ? 2 : 3;
-constexpr int kPairs = kStep / 2;  // neighbouring tokens of a step, two at a time
+// Channels of a lane: VEC.  Arithmetic goes by pairs: a token's two channels (2),
+// or two neighbouring tokens of the one channel (1).  The forward takes two
+// half-precision channels, which halves what a step costs beside its
+// elements; the backward would need more registers than there are.
+template <int DT, bool BACK>
+constexpr int kVec = DT == TBE_F32 || BACK ? 1 : 2;
+template <int VEC>
+constexpr int kPairs = kStep * VEC / 2;  // of a step
+template <int VEC>
+constexpr int kChannels = 32 * VEC;  // of a warp
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct ScanArgs {
@@ -63,7 +72,7 @@ struct ScanArgs {
   int64_t N;
   int32_t S;
   int32_t C;
-  int32_t run;      // tokens per warp, whole slots of the rings
+  int32_t run;      // tokens per warp, whole steps
   int32_t blocks;   // along the tokens
   int32_t cblocks;  // along the channels
   int32_t copy;     // bytes per asynchronous copy: 16, 4, or 0 (plain loads)
@@ -178,38 +187,53 @@ template <int DT>
 __device__ __forceinline__ uint8_t* at(void* p, int64_t e) {
   return static_cast<uint8_t*>(p) + e * kSize<DT>;
 }
-// An element's bits, and as a number.
-template <int DT>
-__device__ __forceinline__ uint32_t load_bits(const uint8_t* p) {
-  if (DT == TBE_F32) return *reinterpret_cast<const uint32_t*>(p);
-  return *reinterpret_cast<const uint16_t*>(p);
-}
 template <int DT>
 __device__ __forceinline__ float number(uint32_t b) {
   if (DT == TBE_F32) return __uint_as_float(b);
   if (DT == TBE_BF16) return __uint_as_float(b << 16);
   return __half2float(__ushort_as_half((unsigned short)b));
 }
-// Stores a pair's two tokens; `both`: the second lies inside the batch.
+// Both halves of a word.
 template <int DT>
-__device__ __forceinline__ void store_pair(uint8_t* p, int64_t row, float a, float b, bool one, bool both) {
-  if (DT == TBE_F32) {
-    if (one) *reinterpret_cast<float*>(p) = a;
-    if (both) *reinterpret_cast<float*>(p + row) = b;
-    return;
-  }
-  uint32_t v;
-  if (DT == TBE_BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    v = *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    v = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  if (one) *reinterpret_cast<uint16_t*>(p) = (uint16_t)v;
-  if (both) *reinterpret_cast<uint16_t*>(p + row) = (uint16_t)(v >> 16);
+__device__ __forceinline__ Two halves(uint32_t w) {
+  if (DT == TBE_BF16) return two(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return two(f.x, f.y);
 }
-__device__ __forceinline__ float element(const Two* t, int j) { return j & 1 ? hi(t[j >> 1]) : lo(t[j >> 1]); }
+template <int DT>
+__device__ __forceinline__ uint32_t to_halves(Two v) {
+  if (DT == TBE_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo(v), hi(v));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(lo(v), hi(v));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int DT>
+__device__ __forceinline__ float load_element(const uint8_t* p) {
+  if (DT == TBE_F32) return *reinterpret_cast<const float*>(p);
+  return number<DT>(*reinterpret_cast<const uint16_t*>(p));
+}
+// Token j, channel v of an array of a step's pairs.
+template <int VEC>
+__device__ __forceinline__ float element(const Two* t, int j, int v) {
+  if (VEC == 1) return j & 1 ? hi(t[j >> 1]) : lo(t[j >> 1]);
+  return v ? hi(t[j]) : lo(t[j]);
+}
+// The token and channel of component e of pair q.
+template <int VEC>
+__device__ __forceinline__ constexpr int token_of(int q, int e) {
+  return VEC == 1 ? 2 * q + e : q;
+}
+template <int VEC>
+__device__ __forceinline__ constexpr int channel_of(int e) {
+  return VEC == 1 ? 0 : e;
+}
+// The pair with the components of tokens from `n` on replaced.
+template <int VEC>
+__device__ __forceinline__ Two upto(Two t, int q, int n, float other) {
+  return two(token_of<VEC>(q, 0) < n ? lo(t) : other, token_of<VEC>(q, 1) < n ? hi(t) : other);
+}
 
 // The linear map of a run of tokens; A < 0: it does not depend on what comes in.
 struct Map {
@@ -308,48 +332,36 @@ struct Events {
   __device__ __forceinline__ int64_t sequence(int j) const { return __shfl_sync(kFull, s, j); }
 };
 
-// A warp's ring.  A slot holds kTokens<DT> tokens of 32 channels of each input,
-// then (DOWN) the states that its steps start from.  Slots are filled upwards,
-// or downwards, from where the ring was set until the run's tokens are all
-// asked for.  WIDE: rows start
-// on 16 bytes and channels come in whole 16-byte pieces; otherwise a copy is
-// of 4 bytes, or (half precision at odd places) an element at a time.
-template <int DT>
-constexpr int kTokens = DT == TBE_F32 ? kStep : 2 * kStep;
-template <int DT, int INPUTS, int SLOTS, bool DOWN, bool WIDE>
+// A warp's ring.  A slot holds a step of each input, then (DOWN) the states
+// that the step starts from.  Slots are filled upwards, or downwards, from
+// where the ring was set until the run's tokens are all asked for.  WIDE: rows
+// start on 16 bytes and channels come in whole 16-byte pieces; otherwise a copy
+// is of 4 bytes, or (half precision at odd places) an element at a time.
+template <int DT, int VEC, int INPUTS, int SLOTS, bool DOWN, bool WIDE>
 struct Ring {
-  static constexpr int kTok = kTokens<DT>;
-  static constexpr int kRow = 32 * kSize<DT>, kBox = kTok * kRow;
-  static constexpr int kSlot = INPUTS * kBox + (DOWN ? kTok / kStep * 128 : 0);
+  static constexpr int kRow = 32 * VEC * kSize<DT>, kBox = kStep * kRow;
+  static constexpr int kSlot = INPUTS * kBox + (DOWN ? kChannels<VEC> * 4 : 0);
   static constexpr int kBytes = SLOTS * kSlot;
-  static constexpr int kLanes = kRow / 16;  // of a row, 16 bytes each
+  static constexpr int kLanes = kRow / 16, kRows = 32 / kLanes;  // 16-byte pieces of a row, rows of a copy
   const uint8_t* mem;
-  const uint8_t* now;
   const uint8_t* src[INPUTS];  // this lane's first piece of the next step
   int64_t row[INPUTS];         // bytes between tokens
-  const float* state;
+  const float* state;          // of the warp's first channel
   const ScanArgs& a;
-  uint32_t base;  // of slot 0, in shared memory
-  int bytes;      // of a lane's piece inside the array
-  bool on;        // the lane's channel lies inside the array
+  uint32_t base;   // of slot 0, in shared memory
+  int left_bytes;  // of a row inside the array
   int lane;
   int read, write;  // bytes from slot 0: the oldest slot, the next to be filled
   int left;         // tokens of the run that are not asked for yet
 
   // `tokens`: of the run; downwards the first slot takes what does not fill one
   __device__ __forceinline__ Ring(const ScanArgs& args, uint8_t* m, int64_t cb, int l, int tokens)
-      : mem(m), now(m), state(nullptr), a(args), base(smem_u32(m)), lane(l), read(0), write(0), left(tokens) {
-    const int left = (int)((a.C - cb) * kSize<DT> < kRow ? (a.C - cb) * kSize<DT> : kRow);
-    const int piece = WIDE ? 16 : a.copy == 4 ? 4 : kSize<DT>;
-    const int b = left - col();
-    bytes = b < 0 ? 0 : (b < piece ? b : piece);
-    on = cb + l < a.C;
+      : mem(m), state(nullptr), a(args), base(smem_u32(m)), lane(l), read(0), write(0), left(tokens) {
+    left_bytes = (int)((a.C - cb) * kSize<DT> < kRow ? (a.C - cb) * kSize<DT> : kRow);
   }
-  // the lane's place in a row, and the first row it copies
-  __device__ __forceinline__ int col() const {
-    return WIDE ? lane % kLanes * 16 : a.copy == 4 ? lane % (kRow / 4) * 4 : lane * kSize<DT>;
-  }
-  __device__ __forceinline__ int first_row() const { return WIDE ? lane / kLanes : a.copy == 4 ? lane / (kRow / 4) : 0; }
+  // the lane's place in a row, and the first row it copies (WIDE)
+  __device__ __forceinline__ int col() const { return WIDE ? lane % kLanes * 16 : 0; }
+  __device__ __forceinline__ int first_row() const { return WIDE ? lane / kLanes : 0; }
   __device__ __forceinline__ void input(int i, const void* p, int64_t stride, int64_t t, int64_t cb) {
     row[i] = stride * kSize<DT>;
     src[i] = at<DT>(p, t * stride + cb) + first_row() * row[i] + col();
@@ -364,66 +376,63 @@ struct Ring {
   // (in the batch's last one), or outside the channels, reads as 0.
   __device__ __forceinline__ void fill_part(int count) {
     const uint32_t to = base + write;
+    if (WIDE) {
 #pragma unroll
-    for (int i = 0; i < INPUTS; ++i) {
-      const uint8_t* from = src[i];
-      if (WIDE) {
-        constexpr int kRows = 32 / kLanes;
+      for (int k = 0; k < kStep; k += kRows) {
+        const int n = k + first_row() < count && col() < left_bytes ? 16 : 0;
 #pragma unroll
-        for (int k = 0; k < kTok / kRows; ++k) {
-          const int n = k * kRows + first_row() < count ? bytes : 0;
-          copy16(to + i * kBox + k * 512 + lane * 16, n ? from : a.x, n);
-          from += kRows * row[i];
-        }
-      } else if (a.copy == 4) {
-        constexpr int kRows = 128 / kRow;
-#pragma unroll
-        for (int k = 0; k < kTok / kRows; ++k) {
-          const int n = k * kRows + first_row() < count ? bytes : 0;
-          copy4(to + i * kBox + k * 128 + lane * 4, n ? from : a.x, n);
-          from += kRows * row[i];
-        }
-      } else {
-        uint32_t w[kTok];
-#pragma unroll
-        for (int k = 0; k < kTok; ++k) w[k] = k < count && bytes ? load_bits<DT>(from + k * row[i]) : 0;
-#pragma unroll
-        for (int k = 0; k < kTok; ++k)
-          asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + i * kBox + k * kRow + lane * 2), "h"((uint16_t)w[k]) : "memory");
+        for (int i = 0; i < INPUTS; ++i)
+          copy16(to + i * kBox + k * kRow + lane * 16, n ? src[i] + k * row[i] : a.x, n);
       }
-      src[i] += (DOWN ? -kTok : kTok) * row[i];
-    }
-    if (DOWN) {
+    } else if (a.copy == 4) {
+      constexpr int kPieces = kRow / 4;  // of a row
 #pragma unroll
-      for (int u = 0; u < kTok / kStep; ++u) {
-        const int n = u * kStep < count && on ? 4 : 0;
-        copy4(to + INPUTS * kBox + u * 128 + lane * 4, n ? (const void*)(state + (int64_t)u * a.C) : a.x, n);
+      for (int k = 0; k < kStep; k += 32 / kPieces) {
+        const int r = k + lane / kPieces, c = lane % kPieces * 4;
+        const int b = left_bytes - c, n = r >= count || b < 0 ? 0 : (b < 4 ? b : 4);
+#pragma unroll
+        for (int i = 0; i < INPUTS; ++i)
+          copy4(to + i * kBox + r * kRow + c, n ? src[i] + r * row[i] + c : a.x, n);
       }
-      state -= (int64_t)(kTok / kStep) * a.C;
+    } else {
+#pragma unroll 4
+      for (int k = 0; k < kStep; ++k)
+#pragma unroll
+        for (int i = 0; i < INPUTS; ++i)
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) {
+            const int c = (v * 32 + lane) * 2;
+            const uint16_t w = k < count && c < left_bytes ? *reinterpret_cast<const uint16_t*>(src[i] + k * row[i] + c) : 0;
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + i * kBox + k * kRow + c), "h"(w) : "memory");
+          }
     }
+#pragma unroll
+    for (int i = 0; i < INPUTS; ++i) src[i] += (DOWN ? -kStep : kStep) * row[i];
   }
   // The next slot.
   __device__ __forceinline__ void fill() {
-    int count = left < kTok ? left : kTok;
-    if (DOWN && left > kTok && left % kTok) count = left % kTok;
+    int count = left < kStep ? left : kStep;
+    if (DOWN && left > kStep && left % kStep) count = left % kStep;
     left -= count;
-    if (WIDE && count == kTok) {
+    if (WIDE && count == kStep) {
       const uint32_t to = base + write + lane * 16;
-      constexpr int kRows = 32 / kLanes;
+      const int n = col() < left_bytes ? 16 : 0;
 #pragma unroll
       for (int i = 0; i < INPUTS; ++i) {
 #pragma unroll
-        for (int k = 0; k < kTok / kRows; ++k) copy16(to + i * kBox + k * 512, src[i] + k * kRows * row[i], bytes);
-        src[i] += (DOWN ? -kTok : kTok) * row[i];
-      }
-      if (DOWN) {
-#pragma unroll
-        for (int u = 0; u < kTok / kStep; ++u)
-          copy4(base + write + lane * 4 + INPUTS * kBox + u * 128, state + (int64_t)u * a.C, on ? 4 : 0);
-        state -= (int64_t)(kTok / kStep) * a.C;
+        for (int k = 0; k < kStep; k += kRows) copy16(to + i * kBox + k * kRow, src[i] + k * row[i], n);
+        src[i] += (DOWN ? -kStep : kStep) * row[i];
       }
     } else {
       fill_part(count);
+    }
+    if (DOWN) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const bool ok = count > 0 && (v * 32 + lane) * kSize<DT> < left_bytes;
+        copy4(base + write + INPUTS * kBox + (v * 32 + lane) * 4, ok ? state + v * 32 + lane : (const float*)a.x, ok ? 4 : 0);
+      }
+      state -= a.C;
     }
     cp_commit();
     write = write + kSlot == kBytes ? 0 : write + kSlot;
@@ -439,49 +448,80 @@ struct Ring {
     fill();
     read = write;
   }
-  // step u of the slot, of which the next reads are
-  __device__ __forceinline__ void step(int u) { now = mem + read + u * (kStep * kRow) + lane * kSize<DT>; }
-  __device__ __forceinline__ uint32_t bits(int i, int j) const { return load_bits<DT>(now + (i * kBox + j * kRow)); }
+  // a token's channels of the lane
+  __device__ __forceinline__ uint32_t word(int i, int j) const {
+    const uint8_t* p = mem + read + lane * (VEC * kSize<DT>) + (i * kBox + j * kRow);
+    return VEC * kSize<DT> == 4 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
+  }
   // `again`: read anew where it was read before, so that nothing made from
   // it the first time is kept in registers for the second
-  __device__ __forceinline__ Two pair(int i, int p, bool again = false) const {
-    uint32_t w0 = bits(i, 2 * p), w1 = bits(i, 2 * p + 1);
-    if (again) asm volatile("" : "+r"(w0), "+r"(w1));
-    return two(number<DT>(w0), number<DT>(w1));
+  __device__ __forceinline__ Two pair(int i, int q, bool again = false) const {
+    if (VEC == 1) {
+      uint32_t w0 = word(i, 2 * q), w1 = word(i, 2 * q + 1);
+      if (again) asm volatile("" : "+r"(w0), "+r"(w1));
+      return two(number<DT>(w0), number<DT>(w1));
+    }
+    uint32_t w = word(i, q);
+    if (again) asm volatile("" : "+r"(w));
+    return halves<DT>(w);
   }
-  __device__ __forceinline__ float first_state(int u) const {
-    return *reinterpret_cast<const float*>(mem + read + INPUTS * kBox + u * 128 + lane * 4);
+  __device__ __forceinline__ float first_state(int v) const {
+    return *reinterpret_cast<const float*>(mem + read + INPUTS * kBox + (lane * VEC + v) * 4);
   }
 };
 
 // One output of a warp, a step at a time.  WIDE: gathered in shared memory and
 // written 16 bytes to a lane; otherwise each element on its own.
-template <int DT, bool DOWN, bool WIDE>
+template <int DT, int VEC, bool DOWN, bool WIDE>
 struct Out {
-  static constexpr int kRow = 32 * kSize<DT>, kLanes = kRow / 16, kRows = 32 / kLanes;
+  static constexpr int kRow = 32 * VEC * kSize<DT>, kLanes = kRow / 16, kRows = 32 / kLanes;
   uint8_t* to;    // this lane's first piece of the step
-  uint8_t* room;  // kStep rows of shared memory (WIDE)
+  uint8_t* room;  // a step's rows in shared memory (WIDE)
   int64_t row;
   int lane;
-  bool on;
+  int on;  // channels (WIDE: 16-byte pieces) of the lane inside the array
   __device__ __forceinline__ Out(void* p, int64_t stride, int64_t t, int64_t cb, int32_t C, uint8_t* m, int l)
       : room(m), row(stride * kSize<DT>), lane(l) {
-    const int col = WIDE ? l % kLanes * 16 : l * kSize<DT>;
-    on = cb * kSize<DT> + col < (int64_t)C * kSize<DT>;
-    to = at<DT>(p, t * stride + cb) + col + (WIDE ? l / kLanes * row : 0);
+    const int64_t left = WIDE ? (C - cb) * kSize<DT> - l % kLanes * 16 : C - cb - l * VEC;
+    on = left <= 0 ? 0 : (WIDE || left < VEC ? 1 : VEC);
+    to = at<DT>(p, t * stride + cb) + (WIDE ? l % kLanes * 16 + l / kLanes * row : l * VEC * kSize<DT>);
+  }
+  __device__ __forceinline__ void element_out(uint8_t* q, float f) {
+    if (DT == TBE_F32) *reinterpret_cast<float*>(q) = f;
+    else if (DT == TBE_F16) *reinterpret_cast<__half*>(q) = __float2half_rn(f);
+    else *reinterpret_cast<__nv_bfloat16*>(q) = __float2bfloat16_rn(f);
   }
   // pair q of the step (`n` tokens of it lie inside the batch)
-  __device__ __forceinline__ void put(int q, float a, float b, int n) {
-    if (WIDE) store_pair<DT>(room + lane * kSize<DT> + 2 * q * kRow, kRow, a, b, true, true);
-    else store_pair<DT>(to + 2 * q * row, row, a, b, on && 2 * q < n, on && 2 * q + 1 < n);
+  __device__ __forceinline__ void put(int q, Two v, int n) {
+    if (WIDE) {
+      uint8_t* r = room + lane * (VEC * kSize<DT>) + token_of<VEC>(q, 0) * kRow;
+      if (DT == TBE_F32) {
+        *reinterpret_cast<float*>(r) = lo(v);
+        *reinterpret_cast<float*>(r + kRow) = hi(v);
+      } else {
+        const uint32_t w = to_halves<DT>(v);
+        if (VEC == 2) {
+          *reinterpret_cast<uint32_t*>(r) = w;
+        } else {
+          *reinterpret_cast<uint16_t*>(r) = (uint16_t)w;
+          *reinterpret_cast<uint16_t*>(r + kRow) = (uint16_t)(w >> 16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (token_of<VEC>(q, e) < n && channel_of<VEC>(e) < on)
+          element_out(to + token_of<VEC>(q, e) * row + channel_of<VEC>(e) * kSize<DT>, e ? hi(v) : lo(v));
+    }
   }
   // the step is complete (the caller puts a __syncwarp before and after)
   __device__ __forceinline__ void flush(int n) {
     if (WIDE) {
 #pragma unroll
-      for (int k = 0; k < kStep / kRows; ++k)
-        if (on && (n == kStep || k * kRows + lane / kLanes < n))
-          *reinterpret_cast<uint4*>(to + k * kRows * row) = *reinterpret_cast<const uint4*>(room + k * 512 + lane * 16);
+      for (int k = 0; k < kStep; k += kRows) {
+        const uint4 a = *reinterpret_cast<const uint4*>(room + k * kRow + lane * 16);
+        if (on && (n == kStep || k + lane / kLanes < n)) *reinterpret_cast<uint4*>(to + k * row) = a;
+      }
     }
     to += (DOWN ? -kStep : kStep) * row;
   }
@@ -491,36 +531,39 @@ constexpr int kR = 0, kG = 1, kX = 2, kD = 3;  // inputs of the rings that hold 
 // A warp's place: its run of tokens and its lanes' channels.
 struct Place {
   int64_t t0, t1, c, cb;
-  bool on;  // the lane's channel lies inside the array
+  int on;  // channels of the lane inside the array
 };
+template <int VEC>
 __device__ __forceinline__ Place place_of(const ScanArgs& a, int warp, int lane) {
   Place p;
   const int64_t k = blockIdx.x / a.cblocks;
-  p.cb = (int64_t)(blockIdx.x % a.cblocks) * 32;
-  p.c = p.cb + lane;
+  p.cb = (int64_t)(blockIdx.x % a.cblocks) * kChannels<VEC>;
+  p.c = p.cb + lane * VEC;
   p.t0 = (k * kWarps + warp) * a.run;
   p.t1 = p.t0 + a.run < a.N ? p.t0 + a.run : a.N;
   if (p.t0 > p.t1) p.t0 = p.t1;
-  p.on = p.c < a.C;
+  p.on = p.c >= a.C ? 0 : (p.c + VEC <= a.C ? VEC : 1);
   return p;
 }
 
-// The lane's decay rate; `near`: whether the whole warp's stay where the
+// The lane's decay rates; `near`: whether the whole warp's stay where the
 // series holds (at most kNear, as sigmoids do not pass 1).
+template <int VEC>
 __device__ __forceinline__ Two speed_at(const ScanArgs& a, const Place& p, bool& near) {
-  const float s = p.on ? speed_of(a, p.c) : 0.f;
-  near = __all_sync(kFull, s < kNear);
-  return two(s);
+  const float s0 = p.on > 0 ? speed_of(a, p.c) : 0.f;
+  const float s1 = VEC == 1 ? s0 : (p.on > 1 ? speed_of(a, p.c + 1) : 0.f);
+  near = __all_sync(kFull, s0 < kNear && s1 < kNear);
+  return two(s0, s1);
 }
 
 // Sigmoids, decays a and 1 - a^2 of a step.
-template <typename RING>
+template <int VEC, typename RING>
 __device__ __forceinline__ void step_gates(const RING& ring, const Constants& k, Two speed, bool near, Two* sr, Two* sg,
                                            Two* A, Two* Q) {
   float top = 0.f;
   if (near) {
 #pragma unroll
-    for (int p = 0; p < kPairs; ++p) {
+    for (int p = 0; p < kPairs<VEC>; ++p) {
       gates_near(ring.pair(kR, p), ring.pair(kG, p), k, sr[p], sg[p], top);
       const Decay<Two> d = decay_near(speed * sr[p], k);
       A[p] = d.a;
@@ -529,7 +572,7 @@ __device__ __forceinline__ void step_gates(const RING& ring, const Constants& k,
   }
   if (!__all_sync(kFull, near && top < kTop)) {
 #pragma unroll
-    for (int p = 0; p < kPairs; ++p) {
+    for (int p = 0; p < kPairs<VEC>; ++p) {
       gates_any(ring.pair(kR, p, true), ring.pair(kG, p, true), sr[p], sg[p]);
       const Decay<Two> d = decay_any(speed * sr[p]);
       A[p] = d.a;
@@ -537,40 +580,83 @@ __device__ __forceinline__ void step_gates(const RING& ring, const Constants& k,
     }
   }
 }
+// Decays a and inputs b of a step.
+template <int VEC, typename RING>
+__device__ __forceinline__ void step_inputs(const RING& ring, const Constants& k, Two speed, bool near, Two* A, Two* B) {
+  float top = 0.f;
+  if (near) {
+#pragma unroll
+    for (int p = 0; p < kPairs<VEC>; ++p) {
+      Two sr, sg;
+      gates_near(ring.pair(kR, p), ring.pair(kG, p), k, sr, sg, top);
+      const Decay<Two> d = decay_near(speed * sr, k);
+      A[p] = d.a;
+      B[p] = root(d.q) * sg * ring.pair(kX, p);
+    }
+  }
+  if (!__all_sync(kFull, near && top < kTop)) {
+#pragma unroll
+    for (int p = 0; p < kPairs<VEC>; ++p) {
+      Two sr, sg;
+      gates_any(ring.pair(kR, p, true), ring.pair(kG, p, true), sr, sg);
+      const Decay<Two> d = decay_any(speed * sr);
+      A[p] = d.a;
+      B[p] = root(d.q) * sg * ring.pair(kX, p, true);
+    }
+  }
+}
+// One pair's step of the recurrence; returns the states.
+template <int VEC>
+__device__ __forceinline__ Two advance(Two A, Two B, float* h) {
+  if (VEC == 1) {
+    const float h0 = fmaf(lo(A), h[0], lo(B));
+    h[0] = fmaf(hi(A), h0, hi(B));
+    return two(h0, h[0]);
+  }
+  const Two t = fma2(A, two(h[0], h[VEC - 1]), B);
+  h[0] = lo(t);
+  h[VEC - 1] = hi(t);
+  return t;
+}
 
-// Slots: as many as leave room for those blocks (at most 72 KB a block
-// forward, 108 KB backward).
+// Slots: what fits three blocks forward (at most 57 KB each), two backward.
 constexpr int kForwardSlots = 2;
-constexpr int kBackwardSlots = 2;
 template <int DT>
-constexpr int kBackMapSlots = DT == TBE_F32 ? 4 : 3;
+constexpr int kBackwardSlots = DT == TBE_F32 ? 2 : 4;
+template <int DT>
+constexpr int kBackMapSlots = DT == TBE_F32 ? 3 : 6;
 template <int DT, bool WIDE>
-using ForwardRing = Ring<DT, 3, kForwardSlots, false, WIDE>;
+using ForwardRing = Ring<DT, kVec<DT, false>, 3, kForwardSlots, false, WIDE>;
 template <int DT, bool WIDE>
-using BackwardRing = Ring<DT, 4, kBackwardSlots, true, WIDE>;
+using BackwardRing = Ring<DT, kVec<DT, true>, 4, kBackwardSlots<DT>, true, WIDE>;
 template <int DT, bool WIDE>
-using BackMapRing = Ring<DT, 2, kBackMapSlots<DT>, false, WIDE>;
+using BackMapRing = Ring<DT, kVec<DT, true>, 2, kBackMapSlots<DT>, false, WIDE>;
 // shared memory of a warp, with room for its outputs
 template <int DT>
-constexpr int kForwardBytes = ForwardRing<DT, true>::kBytes + kStep * 32 * kSize<DT>;
+constexpr int kForwardBytes = ForwardRing<DT, true>::kBytes + ForwardRing<DT, true>::kBox;
 template <int DT>
-constexpr int kBackwardBytes = BackwardRing<DT, true>::kBytes + 3 * kStep * 32 * kSize<DT>;
+constexpr int kBackwardBytes = BackwardRing<DT, true>::kBytes + 3 * BackwardRing<DT, true>::kBox;
 template <int DT>
 constexpr int kMapBytes(bool back) {
   return back ? BackMapRing<DT, true>::kBytes : ForwardRing<DT, true>::kBytes;
 }
 
-// The map of a run, forward: h at its end from h at its start.  Only the
+// The maps of a run, forward: h at its end from h at its start.  Only the
 // tokens from the run's last start on count.
 template <int DT, bool WIDE>
-__device__ __forceinline__ Map run_map(const ScanArgs& a, const Place& p, uint8_t* mem, Two speed, bool near, int lane) {
-  Map m{1.f, 0.f};
-  if (p.t0 >= p.t1) return m;
+__device__ __forceinline__ void run_map(const ScanArgs& a, const Place& p, uint8_t* mem, Two speed, bool near, int lane,
+                                        Map* m) {
+  constexpr int VEC = kVec<DT, false>;
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) m[v] = Map{1.f, 0.f};
+  if (p.t0 >= p.t1) return;
   Cursor cur(a, lane);
   int64_t first, end;
   const int64_t s = cur.owner(p.t1 - 1, true, first, end);
   const bool cut = first >= p.t0 && first < p.t1;
-  if (cut && a.h0 && p.on) m.B = a.h0[s * a.C + p.c];
+  float h[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) h[v] = cut && a.h0 && v < p.on ? a.h0[s * a.C + p.c + v] : 0.f;
   const int64_t from = cut ? first : p.t0;
   int left = (int)(p.t1 - from);
   ForwardRing<DT, WIDE> ring(a, mem, p.cb, lane, left);
@@ -580,89 +666,83 @@ __device__ __forceinline__ Map run_map(const ScanArgs& a, const Place& p, uint8_
   ring.input(kX, a.x, a.sx, from, p.cb);
 #pragma unroll
   for (int i = 0; i < kForwardSlots; ++i) ring.fill();
-  while (left > 0) {
+  Two product = two(1.f);
+  for (; left > 0; left -= kStep) {
     ring.ready();
-#pragma unroll 1
-    for (int u = 0; u < kTokens<DT> / kStep && left > 0; ++u, left -= kStep) {
-      ring.step(u);
-      Two sr[kPairs], sg[kPairs], A[kPairs], B[kPairs];
-      step_gates(ring, k, speed, near, sr, sg, A, B);
+    Two A[kPairs<VEC>], B[kPairs<VEC>];
+    step_inputs<VEC>(ring, k, speed, near, A, B);
+    if (left < kStep) {  // tokens outside the run change nothing
 #pragma unroll
-      for (int q = 0; q < kPairs; ++q) B[q] = root(B[q]) * sg[q] * ring.pair(kX, q);
-      if (left < kStep) {  // tokens outside the run change nothing
-#pragma unroll
-        for (int q = 0; q < kPairs; ++q) {
-          A[q] = two(2 * q < left ? lo(A[q]) : 1.f, 2 * q + 1 < left ? hi(A[q]) : 1.f);
-          B[q] = two(2 * q < left ? lo(B[q]) : 0.f, 2 * q + 1 < left ? hi(B[q]) : 0.f);
-        }
+      for (int q = 0; q < kPairs<VEC>; ++q) {
+        A[q] = upto<VEC>(A[q], q, left, 1.f);
+        B[q] = upto<VEC>(B[q], q, left, 0.f);
       }
+    }
 #pragma unroll
-      for (int j = 0; j < kStep; ++j) m.B = fmaf(element(A, j), m.B, element(B, j));
-      const Two P = A[0] * A[1] * (A[2] * A[3]);
-      m.A *= lo(P) * hi(P);
+    for (int q = 0; q < kPairs<VEC>; ++q) {
+      advance<VEC>(A[q], B[q], h);
+      product = product * A[q];
     }
     ring.done();
   }
   cp_wait<0>();
-  if (cut) m.A = -1.f;
-  return m;
+  m[0] = Map{cut ? -1.f : (VEC == 1 ? lo(product) * hi(product) : lo(product)), h[0]};
+  if (VEC == 2) m[VEC - 1] = Map{cut ? -1.f : hi(product), h[VEC - 1]};
 }
 
-// The map of a run, backward: a G at its start from a G behind its end.
+// The maps of a run, backward: a G at its start from a G behind its end.
 // Only the tokens up to the run's first end count.
 template <int DT, bool WIDE>
-__device__ __forceinline__ Map run_map_back(const ScanArgs& a, const Place& p, uint8_t* mem, Two speed, bool near, int lane) {
-  Map m{1.f, 0.f};
-  if (p.t0 >= p.t1) return m;
+__device__ __forceinline__ void run_map_back(const ScanArgs& a, const Place& p, uint8_t* mem, Two speed, bool near, int lane,
+                                             Map* m) {
+  constexpr int VEC = kVec<DT, true>;
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) m[v] = Map{1.f, 0.f};
+  if (p.t0 >= p.t1) return;
   Cursor cur(a, lane);
   int64_t first, end;
   const int64_t s = cur.owner(p.t0, false, first, end);
   const bool cut = end > p.t0 && end <= p.t1;
   int left = (int)((cut ? end : p.t1) - p.t0);
-  const float last = cut && a.dh_last && p.on ? a.dh_last[s * a.C + p.c] : 0.f;
+  float last[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) last[v] = cut && a.dh_last && v < p.on ? a.dh_last[s * a.C + p.c + v] : 0.f;
   BackMapRing<DT, WIDE> ring(a, mem, p.cb, lane, left);
   const Constants k;
   ring.input(0, a.r, a.sr, p.t0, p.cb);
   ring.input(1, a.dh, a.sdh, p.t0, p.cb);
 #pragma unroll
   for (int i = 0; i < kBackMapSlots<DT>; ++i) ring.fill();
-  while (left > 0) {
+  for (; left > 0; left -= kStep) {
     ring.ready();
-#pragma unroll 1
-    for (int u = 0; u < kTokens<DT> / kStep && left > 0; ++u, left -= kStep) {
-      ring.step(u);
-      Two A[kPairs], D[kPairs];
-      if (near) {
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i)
-          A[i] = decay_near(speed * rcp(ex2(ring.pair(0, i) * k.minus_log2e) + k.one), k).a;
-      } else {
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          const Two r = ring.pair(0, i);
-          A[i] = decay_any(speed * two(sigmoid(lo(r)), sigmoid(hi(r)))).a;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i) D[i] = ring.pair(1, i);
+    for (int q = 0; q < kPairs<VEC>; ++q) {
+      const Two r = ring.pair(0, q);
+      Two A = near ? decay_near(speed * rcp(ex2(r * k.minus_log2e) + k.one), k).a
+                   : decay_any(speed * two(sigmoid(lo(r)), sigmoid(hi(r)))).a;
+      Two D = ring.pair(1, q);
       if (left <= kStep) {  // the run's last token, and those outside it
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          A[i] = two(2 * i < left ? lo(A[i]) : 1.f, 2 * i + 1 < left ? hi(A[i]) : 1.f);
-          D[i] = D[i] + two(2 * i + 1 == left ? last : 0.f, 2 * i + 2 == left ? last : 0.f);
-        }
+        A = upto<VEC>(A, q, left, 1.f);
+        D = D + two(token_of<VEC>(q, 0) + 1 == left ? last[0] : 0.f, token_of<VEC>(q, 1) + 1 == left ? last[VEC - 1] : 0.f);
       }
-#pragma unroll
-      for (int j = 0; j < kStep; ++j) {
-        m.A *= element(A, j);
-        m.B = fmaf(m.A, element(D, j), m.B);
+      if (VEC == 1) {
+        m[0].A *= lo(A);
+        m[0].B = fmaf(m[0].A, lo(D), m[0].B);
+        m[0].A *= hi(A);
+        m[0].B = fmaf(m[0].A, hi(D), m[0].B);
+      } else {
+        const Two P = two(m[0].A, m[VEC - 1].A) * A, B = fma2(P, D, two(m[0].B, m[VEC - 1].B));
+        m[0] = Map{lo(P), lo(B)};
+        m[VEC - 1] = Map{hi(P), hi(B)};
       }
     }
     ring.done();
   }
   cp_wait<0>();
-  if (cut) m.A = -1.f;
-  return m;
+  if (cut) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) m[v].A = -1.f;
+  }
 }
 
 __device__ __forceinline__ float2 word_of(Map m) { return make_float2(m.A, m.B); }
@@ -672,81 +752,105 @@ __device__ __forceinline__ Map map_of(float2 w) { return Map{w.x, w.y}; }
 // last run down).
 template <int DT, bool BACK, bool WIDE>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm<BACK>) maps_kernel(ScanArgs a) {
+  constexpr int VEC = kVec<DT, BACK>;
   extern __shared__ __align__(128) uint8_t mem[];
-  __shared__ Map runs[kWarps][32];
+  __shared__ Map runs[kWarps][64];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Place p = place_of(a, warp, lane);
+  const Place p = place_of<VEC>(a, warp, lane);
   bool near;
-  const Two speed = speed_at(a, p, near);
+  const Two speed = speed_at<VEC>(a, p, near);
   uint8_t* mine = mem + warp * kMapBytes<DT>(BACK);
-  const Map m = BACK ? run_map_back<DT, WIDE>(a, p, mine, speed, near, lane) : run_map<DT, WIDE>(a, p, mine, speed, near, lane);
+  Map m[VEC];
+  if (BACK) run_map_back<DT, WIDE>(a, p, mine, speed, near, lane, m);
+  else run_map<DT, WIDE>(a, p, mine, speed, near, lane, m);
   const int64_t k = blockIdx.x / a.cblocks;
   if (BACK && k == 0 && threadIdx.x == 0) a.arrived[blockIdx.x] = 0;  // for the backward kernel, which waits for this one
-  runs[warp][lane] = m;
-  a.warp_map[(k * kWarps + warp) * a.Cp + p.c] = word_of(m);
-  __syncthreads();
-  if (warp == 0) {
-    Map all = runs[BACK ? kWarps - 1 : 0][lane];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) all = join(all, runs[BACK ? kWarps - 1 - w : w][lane]);
-    a.block_map[k * a.Cp + p.c] = word_of(all);
+  for (int v = 0; v < VEC; ++v) {
+    runs[warp][lane * VEC + v] = m[v];
+    a.warp_map[(k * kWarps + warp) * a.Cp + p.c + v] = word_of(m[v]);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kChannels<VEC>; i += kThreads) {
+    Map all = runs[BACK ? kWarps - 1 : 0][i];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) all = join(all, runs[BACK ? kWarps - 1 - w : w][i]);
+    a.block_map[k * a.Cp + p.cb + i] = word_of(all);
   }
 }
 
-// What reaches a warp's run: the blocks before this one, in rounds of 128
-// from the nearest on (sixteen to a warp), until nothing further back
+// What reaches a warp's run: the blocks before this one, in rounds of 128 or 64
+// from the nearest on (sixteen or eight to a warp), until nothing further back
 // matters; then the warps before this one.  Every thread of the block calls
 // this.
-template <bool BACK>
-__device__ __forceinline__ float reach(const ScanArgs& a, const Place& p, int warp, int lane) {
-  constexpr int kEach = 16;
-  __shared__ Map part[kWarps][32];
+template <int VEC, bool BACK>
+__device__ __forceinline__ void reach(const ScanArgs& a, const Place& p, int warp, int lane, float* in) {
+  constexpr int kEach = 16 / VEC;
+  __shared__ Map part[kWarps][64];
   const int64_t k = blockIdx.x / a.cblocks;
   const int64_t before = BACK ? a.blocks - 1 - k : k;  // blocks before this one in scan order
-  float2 own[kWarps - 1];
+  float2 own[kWarps - 1][VEC];
 #pragma unroll
   for (int j = 0; j < kWarps - 1; ++j) {
     const int r = BACK ? kWarps - 1 - j : j;  // in scan order
     const bool mine = BACK ? r > warp : r < warp;
-    own[j] = mine ? __ldcg(a.warp_map + (k * kWarps + r) * a.Cp + p.c) : make_float2(1.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+      own[j][v] = mine ? __ldcg(a.warp_map + (k * kWarps + r) * a.Cp + p.c + v) : make_float2(1.f, 0.f);
   }
-  Map all{1.f, 0.f};
-  for (int64_t done = 0; done < before && !(all.A < 0.f); done += kEach * kWarps) {
+  Map all[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) all[v] = Map{1.f, 0.f};
+  for (int64_t done = 0; done < before && !(all[0].A < 0.f); done += kEach * kWarps) {
     // this warp's share, farthest first
-    Map m{1.f, 0.f};
-    float2 w[kEach];
+    Map m[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) m[v] = Map{1.f, 0.f};
+    float2 w[kEach][VEC];
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
       const int64_t away = done + kEach * warp + kEach - j;  // 1: the neighbour
       const int64_t b = BACK ? k + away : k - away;
-      w[j] = away <= before ? __ldcg(a.block_map + b * a.Cp + p.c) : make_float2(1.f, 0.f);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) w[j][v] = away <= before ? __ldcg(a.block_map + b * a.Cp + p.c + v) : make_float2(1.f, 0.f);
     }
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) m = join(m, map_of(w[j]));
-    __syncthreads();
-    part[warp][lane] = m;
-    __syncthreads();
-    Map round = part[kWarps - 1][lane];
+    for (int j = 0; j < kEach; ++j)
 #pragma unroll
-    for (int j = kWarps - 2; j >= 0; --j) round = join(round, part[j][lane]);
-    all = join(round, all);
+      for (int v = 0; v < VEC; ++v) m[v] = join(m[v], map_of(w[j][v]));
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) part[warp][lane * VEC + v] = m[v];
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      Map round = part[kWarps - 1][lane * VEC + v];
+#pragma unroll
+      for (int j = kWarps - 2; j >= 0; --j) round = join(round, part[j][lane * VEC + v]);
+      all[v] = join(round, all[v]);
+    }
   }
-  float in = apply(all, 0.f);
 #pragma unroll
-  for (int j = 0; j < kWarps - 1; ++j) in = apply(map_of(own[j]), in);
-  return in;
+  for (int v = 0; v < VEC; ++v) {
+    in[v] = apply(all[v], 0.f);
+#pragma unroll
+    for (int j = 0; j < kWarps - 1; ++j) in[v] = apply(map_of(own[j][v]), in[v]);
+  }
 }
 
 // The same where one block holds all tokens: the warps' maps are made here.
-template <bool BACK>
-__device__ __forceinline__ float reach_alone(Map m, int warp, int lane) {
-  __shared__ Map runs[kWarps][32];
-  runs[warp][lane] = m;
+template <int VEC, bool BACK>
+__device__ __forceinline__ void reach_alone(const Map* m, int warp, int lane, float* in) {
+  __shared__ Map runs[kWarps][64];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) runs[warp][lane * VEC + v] = m[v];
   __syncthreads();
-  float in = 0.f;
-  for (int j = BACK ? kWarps - 1 : 0; j != warp; j += BACK ? -1 : 1) in = apply(runs[j][lane], in);
-  return in;
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    in[v] = 0.f;
+    for (int j = BACK ? kWarps - 1 : 0; j != warp; j += BACK ? -1 : 1) in[v] = apply(runs[j][lane * VEC + v], in[v]);
+  }
 }
 
 // Empty sequences hand their states on (to[s] = from[s], 0 where there is no
@@ -780,14 +884,19 @@ __device__ __forceinline__ void empty_sequences(const ScanArgs& a, const float* 
 // ALONE: the batch is one block's tokens, no maps kernel ran.
 template <int DT, bool ALONE, bool WIDE>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm<false>) forward_kernel(ScanArgs a) {
+  constexpr int VEC = kVec<DT, false>;
   extern __shared__ __align__(128) uint8_t mem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Place p = place_of(a, warp, lane);
+  const Place p = place_of<VEC>(a, warp, lane);
   bool near;
-  const Two speed = speed_at(a, p, near);
+  const Two speed = speed_at<VEC>(a, p, near);
   uint8_t* mine = mem + warp * kForwardBytes<DT>;
-  float h = 0.f;
-  if (ALONE) h = reach_alone<false>(run_map<DT, WIDE>(a, p, mine, speed, near, lane), warp, lane);
+  float h[VEC];
+  if (ALONE) {
+    Map m[VEC];
+    run_map<DT, WIDE>(a, p, mine, speed, near, lane, m);
+    reach_alone<VEC, false>(m, warp, lane, h);
+  }
   int left = (int)(p.t1 - p.t0);
   ForwardRing<DT, WIDE> ring(a, mine, p.cb, lane, left);
   ring.input(kR, a.r, a.sr, p.t0, p.cb);
@@ -796,175 +905,178 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<false>) forward_kernel(
 #pragma unroll
   for (int i = 0; i < kForwardSlots; ++i) ring.fill();
   empty_sequences(a, a.h0, a.h_last);
-  if (!ALONE) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    h = reach<false>(a, p, warp, lane);
-  }
   Cursor cur(a, lane);
   Events ev;
+  if (left > 0) ev.find(cur, p.t0, left < kStep ? left : kStep, false, lane);
+  if (!ALONE) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    reach<VEC, false>(a, p, warp, lane, h);
+  }
   const Constants k;
-  Out<DT, false, WIDE> to(a.h, a.sh, p.t0, p.cb, a.C, mine + ForwardRing<DT, WIDE>::kBytes, lane);
+  Out<DT, VEC, false, WIDE> out(a.h, a.sh, p.t0, p.cb, a.C, mine + ForwardRing<DT, WIDE>::kBytes, lane);
   float* state = a.states ? a.states + p.t0 / kStep * a.C + p.c : nullptr;
-  int64_t t = p.t0;
-  while (left > 0) {
+  for (int64_t t = p.t0; left > 0; left -= kStep) {
+    const int n = left < kStep ? left : kStep;
     ring.ready();
-#pragma unroll 1
-    for (int u = 0; u < kTokens<DT> / kStep && left > 0; ++u, left -= kStep, t += kStep) {
-      const int n = left < kStep ? left : kStep;
-      ev.find(cur, t, n, false, lane);
-      ring.step(u);
-      Two sr[kPairs], sg[kPairs], A[kPairs], B[kPairs];
-      step_gates(ring, k, speed, near, sr, sg, A, B);
+    if (state) {
 #pragma unroll
-      for (int q = 0; q < kPairs; ++q) B[q] = root(B[q]) * sg[q] * ring.pair(kX, q);
-      if (state) {
-        if (p.on) *state = h;
-        state += a.C;
-      }
-      float out[kStep];
-      if ((ev.starts | ev.ends) == 0) {
+      for (int v = 0; v < VEC; ++v)
+        if (v < p.on) state[v] = h[v];
+      state += a.C;
+    }
+    Two A[kPairs<VEC>], B[kPairs<VEC>];
+    step_inputs<VEC>(ring, k, speed, near, A, B);
+    if ((ev.starts | ev.ends) == 0) {
 #pragma unroll
-        for (int j = 0; j < kStep; ++j) out[j] = h = fmaf(element(A, j), h, element(B, j));
-      } else {
+      for (int q = 0; q < kPairs<VEC>; ++q) out.put(q, advance<VEC>(A[q], B[q], h), n);
+    } else {
 #pragma unroll
-        for (int j = 0; j < kStep; ++j) {
+      for (int q = 0; q < kPairs<VEC>; ++q) {
+        float o[2];
+#pragma unroll
+        for (int e = 0; e < 3 - VEC; ++e) {  // the pair's tokens
+          const int j = token_of<VEC>(q, e);
           if (ev.starts >> j & 1) {
             const int64_t s = ev.sequence(j);
-            h = a.h0 && p.on ? a.h0[s * a.C + p.c] : 0.f;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) h[v] = a.h0 && v < p.on ? a.h0[s * a.C + p.c + v] : 0.f;
           }
-          out[j] = h = fmaf(element(A, j), h, element(B, j));
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) o[e + v] = h[v] = fmaf(element<VEC>(A, j, v), h[v], element<VEC>(B, j, v));
           if (ev.ends >> j & 1) {
             const int64_t s = ev.sequence(j);
-            if (p.on) a.h_last[s * a.C + p.c] = h;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+              if (v < p.on) a.h_last[s * a.C + p.c + v] = h[v];
           }
         }
+        out.put(q, two(o[0], o[1]), n);
       }
-#pragma unroll
-      for (int q = 0; q < kPairs; ++q) to.put(q, out[2 * q], out[2 * q + 1], n);
-      __syncwarp();
-      to.flush(n);
-      __syncwarp();
     }
-    ring.done();
+    ring.done();  // keeps the warp together: the step's outputs are complete
+    out.flush(n);
+    t += kStep;
+    if (left > kStep) ev.find(cur, t, left - kStep < kStep ? left - kStep : kStep, false, lane);
   }
   cp_wait<0>();
 }
 
 template <int DT, bool ALONE, bool WIDE>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm<true>) backward_kernel(ScanArgs a) {
+  constexpr int VEC = kVec<DT, true>, kP = kPairs<VEC>;
+  static_assert(VEC == 1, "a lane takes one channel");
   extern __shared__ __align__(128) uint8_t mem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Place p = place_of(a, warp, lane);
+  const Place p = place_of<VEC>(a, warp, lane);
   bool near;
-  const Two speed = speed_at(a, p, near);
+  const Two speed = speed_at<VEC>(a, p, near);
   uint8_t* mine = mem + warp * kBackwardBytes<DT>;
-  float c = 0.f;
+  float c[VEC];
   Two sum = two(0.f);
-  if (ALONE) c = reach_alone<true>(run_map_back<DT, WIDE>(a, p, mine, speed, near, lane), warp, lane);
-  // slots from the run's last one down
-  const int tokens = (int)(p.t1 - p.t0);
-  const int slots = (tokens + kTokens<DT> - 1) / kTokens<DT>;
-  const int64_t last = p.t0 + (int64_t)(slots > 0 ? slots - 1 : 0) * kTokens<DT>;
-  BackwardRing<DT, WIDE> ring(a, mine, p.cb, lane, tokens);
-  ring.input(kR, a.r, a.sr, last, p.cb);
-  ring.input(kG, a.g, a.sg, last, p.cb);
-  ring.input(kX, a.x, a.sx, last, p.cb);
-  ring.input(kD, a.dh, a.sdh, last, p.cb);
-  ring.state = a.states + last / kStep * a.C + p.c;
-#pragma unroll
-  for (int i = 0; i < kBackwardSlots; ++i) ring.fill();
-  empty_sequences(a, a.dh_last, a.dh0);
-  if (!ALONE) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    c = reach<true>(a, p, warp, lane);
+  if (ALONE) {
+    Map m[VEC];
+    run_map_back<DT, WIDE>(a, p, mine, speed, near, lane, m);
+    reach_alone<VEC, true>(m, warp, lane, c);
   }
+  // steps from the run's last one down
+  const int tokens = (int)(p.t1 - p.t0);
+  const int steps = (tokens + kStep - 1) / kStep;
+  int64_t t = p.t0 + (int64_t)(steps > 0 ? steps - 1 : 0) * kStep;
+  int n = tokens - (steps - 1) * kStep;  // of the last step; the others are whole
+  BackwardRing<DT, WIDE> ring(a, mine, p.cb, lane, tokens);
+  ring.input(kR, a.r, a.sr, t, p.cb);
+  ring.input(kG, a.g, a.sg, t, p.cb);
+  ring.input(kX, a.x, a.sx, t, p.cb);
+  ring.input(kD, a.dh, a.sdh, t, p.cb);
+  ring.state = a.states + t / kStep * a.C + p.cb;
+#pragma unroll
+  for (int i = 0; i < kBackwardSlots<DT>; ++i) ring.fill();
+  empty_sequences(a, a.dh_last, a.dh0);
   Cursor cur(a, lane);
   Events ev;
+  if (steps > 0) ev.find(cur, t, n, true, lane);
+  if (!ALONE) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    reach<VEC, true>(a, p, warp, lane, c);
+  }
   uint8_t* room = mine + BackwardRing<DT, WIDE>::kBytes;
-  constexpr int kBox = kStep * 32 * kSize<DT>;
-  const int64_t top = tokens > 0 ? p.t0 + (tokens - 1) / kStep * kStep : p.t0;  // the run's last step
-  Out<DT, true, WIDE> px(a.dx, a.sdx, top, p.cb, a.C, room, lane);
-  Out<DT, true, WIDE> pr(a.dr, a.sdr, top, p.cb, a.C, room + kBox, lane);
-  Out<DT, true, WIDE> pg(a.dg, a.sdg, top, p.cb, a.C, room + 2 * kBox, lane);
+  constexpr int kBox = BackwardRing<DT, WIDE>::kBox;
+  Out<DT, VEC, true, WIDE> px(a.dx, a.sdx, t, p.cb, a.C, room, lane);
+  Out<DT, VEC, true, WIDE> pr(a.dr, a.sdr, t, p.cb, a.C, room + kBox, lane);
+  Out<DT, VEC, true, WIDE> pg(a.dg, a.sdg, t, p.cb, a.C, room + 2 * kBox, lane);
   const Constants k;
-  int64_t t = top;
-  int n = tokens - (int)(top - p.t0);  // of the last step; the others are whole
-  for (int left = slots; left > 0; --left) {
+  for (int left = steps; left > 0; --left) {
     ring.ready();
-#pragma unroll 1
-    for (int u = (int)(t - p.t0) / kStep % (kTokens<DT> / kStep); u >= 0; --u, t -= kStep, n = kStep) {
-      ev.find(cur, t, n, true, lane);
-      ring.step(u);
-      Two sr[kPairs], sg[kPairs], A[kPairs], inv[kPairs], beta[kPairs], found[kPairs], G[kPairs];
-      step_gates(ring, k, speed, near, sr, sg, A, beta);
-      const bool plain = (ev.starts | ev.ends) == 0 && n == kStep;
-      // the states that the step's tokens find
-      float h = ring.first_state(u);
+    Two sr[kP], sg[kP], A[kP], inv[kP], beta[kP], found[kP], G[kP];
+    step_gates<VEC>(ring, k, speed, near, sr, sg, A, beta);
+    const bool plain = (ev.starts | ev.ends) == 0 && n == kStep;
+    // the states that the step's tokens find
+    float h = ring.first_state(0);
 #pragma unroll
-      for (int q = 0; q < kPairs; ++q) {
-        // where 1 - a^2 is 0 the token takes nothing in, and its gate's slope
-        // u d beta / d u = u a^2 / beta goes to 0 with u
-        const Two safe = two(fmaxf(lo(beta[q]), 1e-37f), fmaxf(hi(beta[q]), 1e-37f));
-        inv[q] = inv_root(safe);
-        beta[q] = beta[q] * inv[q];
-        const Two b = beta[q] * sg[q] * ring.pair(kX, q);
-        float f[2];
+    for (int q = 0; q < kP; ++q) {
+      // where 1 - a^2 is 0 the token takes nothing in, and its gate's slope
+      // u d beta / d u = u a^2 / beta goes to 0 with u
+      inv[q] = inv_root(two(fmaxf(lo(beta[q]), 1e-37f), fmaxf(hi(beta[q]), 1e-37f)));
+      beta[q] = beta[q] * inv[q];
+      const Two b = beta[q] * sg[q] * ring.pair(kX, q);
+      float f[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (!plain && (ev.starts >> (2 * q + e) & 1)) {
-            const int64_t s = ev.sequence(2 * q + e);
-            h = a.h0 && p.on ? a.h0[s * a.C + p.c] : 0.f;
-          }
-          f[e] = h;
-          h = fmaf(e ? hi(A[q]) : lo(A[q]), h, e ? hi(b) : lo(b));
+      for (int e = 0; e < 2; ++e) {
+        if (!plain && (ev.starts >> (2 * q + e) & 1)) {
+          const int64_t s = ev.sequence(2 * q + e);
+          h = a.h0 && p.on ? a.h0[s * a.C + p.c] : 0.f;
         }
-        found[q] = two(f[0], f[1]);
-        G[q] = ring.pair(kD, q);
+        f[e] = h;
+        h = fmaf(e ? hi(A[q]) : lo(A[q]), h, e ? hi(b) : lo(b));
       }
-      if (plain) {
-#pragma unroll
-        for (int q = kPairs - 1; q >= 0; --q) {
-          const float g1 = hi(G[q]) + c, g0 = fmaf(hi(A[q]), g1, lo(G[q]));
-          c = lo(A[q]) * g0;
-          G[q] = two(g0, g1);
-        }
-      } else {
-#pragma unroll
-        for (int j = kStep - 1; j >= 0; --j) {
-          float g = element(G, j);
-          if (j < n) {
-            if (ev.ends >> j & 1) {
-              const int64_t s = ev.sequence(j);
-              if (a.dh_last && p.on) g += a.dh_last[s * a.C + p.c];
-            } else {
-              g += c;
-            }
-            c = element(A, j) * g;
-            if (ev.starts >> j & 1) {
-              const int64_t s = ev.sequence(j);
-              if (a.dh0 && p.on) a.dh0[s * a.C + p.c] = c;
-            }
-          }
-          G[j >> 1] = j & 1 ? two(lo(G[j >> 1]), g) : two(g, hi(G[j >> 1]));
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < kPairs; ++q) {
-        const Two x = ring.pair(kX, q, true);
-        const Two w = G[q] * (speed * sr[q]) * A[q] * fma2(A[q] * inv[q], sg[q] * x, negative(found[q]));
-        const Two dx = G[q] * beta[q] * sg[q], dg = dx * x * (k.one + negative(sg[q])), dr = w * (k.one + negative(sr[q]));
-        px.put(q, lo(dx), hi(dx), n);
-        pr.put(q, lo(dr), hi(dr), n);
-        pg.put(q, lo(dg), hi(dg), n);
-        sum = sum + w;  // 0 behind the batch, where dh reads as 0
-      }
-      __syncwarp();
-      px.flush(n);
-      pr.flush(n);
-      pg.flush(n);
-      __syncwarp();
+      found[q] = two(f[0], f[1]);
+      G[q] = ring.pair(kD, q);
     }
-    ring.done();
+    if (plain) {
+#pragma unroll
+      for (int q = kP - 1; q >= 0; --q) {
+        const float g1 = hi(G[q]) + c[0], g0 = fmaf(hi(A[q]), g1, lo(G[q]));
+        c[0] = lo(A[q]) * g0;
+        G[q] = two(g0, g1);
+      }
+    } else {
+#pragma unroll
+      for (int j = kStep - 1; j >= 0; --j) {
+        float g = element<VEC>(G, j, 0);
+        if (j < n) {
+          if (ev.ends >> j & 1) {
+            const int64_t s = ev.sequence(j);
+            if (a.dh_last && p.on) g += a.dh_last[s * a.C + p.c];
+          } else {
+            g += c[0];
+          }
+          c[0] = element<VEC>(A, j, 0) * g;
+          if (ev.starts >> j & 1) {
+            const int64_t s = ev.sequence(j);
+            if (a.dh0 && p.on) a.dh0[s * a.C + p.c] = c[0];
+          }
+        }
+        G[j >> 1] = j & 1 ? two(lo(G[j >> 1]), g) : two(g, hi(G[j >> 1]));
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kP; ++q) {
+      const Two x = ring.pair(kX, q, true);
+      const Two w = G[q] * (speed * sr[q]) * A[q] * fma2(A[q] * inv[q], sg[q] * x, negative(found[q]));
+      const Two dx = G[q] * beta[q] * sg[q];
+      px.put(q, dx, n);
+      pr.put(q, w * (k.one + negative(sr[q])), n);
+      pg.put(q, dx * x * (k.one + negative(sg[q])), n);
+      sum = sum + w;  // 0 behind the batch, where dh reads as 0
+    }
+    const int wrote = n;
+    n = kStep;
+    ring.done();  // keeps the warp together: the step's outputs are complete
+    px.flush(wrote);
+    pr.flush(wrote);
+    pg.flush(wrote);
+    t -= kStep;
+    if (left > 1) ev.find(cur, t, kStep, true, lane);
   }
   cp_wait<0>();
 
@@ -975,39 +1087,42 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<true>) backward_kernel(
   const int64_t block = blockIdx.x / a.cblocks;
   shares[warp][lane] = lo(sum) + hi(sum);
   __syncthreads();
+  const int i = threadIdx.x;
+  const bool mine_to_sum = i < kChannels<VEC>, on = mine_to_sum && p.cb + i < a.C;
   float total = 0.f;
-  if (warp == 0) {
+  if (mine_to_sum) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += shares[w][lane];
+    for (int w = 0; w < kWarps; ++w) total += shares[w][i];
   }
   if (!ALONE) {
-    if (warp == 0) {
-      if (p.on) a.partial[block * a.C + p.c] = total;
-      __threadfence();
-      __syncwarp();
-      if (lane == 0) s_last = atomicAdd(a.arrived + blockIdx.x % a.cblocks, 1u) == (uint32_t)a.blocks - 1;
-    }
+    if (on) a.partial[block * a.C + p.cb + i] = total;
+    __threadfence();
+    __syncthreads();
+    if (i == 0) s_last = atomicAdd(a.arrived + blockIdx.x % a.cblocks, 1u) == (uint32_t)a.blocks - 1;
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    total = 0.f;
-    if (p.on) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      float part = 0.f;
+      if (v < p.on) {
 #pragma unroll 8
-      for (int64_t k = warp; k < a.blocks; k += kWarps) total += __ldcg(a.partial + k * a.C + p.c);
+        for (int64_t b = warp; b < a.blocks; b += kWarps) part += __ldcg(a.partial + b * a.C + p.c + v);
+      }
+      shares[warp][lane * VEC + v] = part;
     }
-    shares[warp][lane] = total;
     __syncthreads();
     total = 0.f;
-    if (warp == 0) {
+    if (mine_to_sum) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) total += shares[w][lane];
+      for (int w = 0; w < kWarps; ++w) total += shares[w][i];
     }
   }
-  if (warp == 0 && p.on) {
-    const float d = a.decay[p.c], sp = softplus(d);
+  if (on) {
+    const float d = a.decay[p.cb + i], sp = softplus(d);
     // ddecay = sigmoid(decay) / softplus(decay) * total; far below zero both
     // are exp(decay) and the ratio is 1
-    a.ddecay[p.c] = d < -16.f ? total : total * (1.f / (1.f + expf(-d))) / sp;
+    a.ddecay[p.cb + i] = d < -16.f ? total : total * (1.f / (1.f + expf(-d))) / sp;
   }
 }
 
@@ -1017,17 +1132,23 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a) {
   const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
   if (i >= (int64_t)a.S * a.C) return;
   const int64_t s = i / a.C, c = i - s * a.C;
-  const float x = number<DT>(load_bits<DT>(at<DT>(a.x, s * a.sx + c)));
-  const float r = number<DT>(load_bits<DT>(at<DT>(a.r, s * a.sr + c)));
-  const float g = number<DT>(load_bits<DT>(at<DT>(a.g, s * a.sg + c)));
+  const float x = load_element<DT>(at<DT>(a.x, s * a.sx + c));
+  const float r = load_element<DT>(at<DT>(a.r, s * a.sr + c));
+  const float g = load_element<DT>(at<DT>(a.g, s * a.sg + c));
   const Decay<float> d = decay_of(speed_of(a, c) * sigmoid(r));
   const float h = fmaf(d.a, a.h_last[i], root(d.q) * sigmoid(g) * x);
   a.h_last[i] = h;
-  store_pair<DT>(at<DT>(a.h, s * a.sh + c), 0, h, h, true, false);
+  if (DT == TBE_F32) static_cast<float*>(a.h)[s * a.sh + c] = h;
+  else if (DT == TBE_F16) static_cast<__half*>(a.h)[s * a.sh + c] = __float2half_rn(h);
+  else static_cast<__nv_bfloat16*>(a.h)[s * a.sh + c] = __float2bfloat16_rn(h);
 }
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
-int32_t channel_blocks(int32_t C) { return (C + 31) / 32; }
+int32_t channel_blocks(int32_t C, int32_t dtype, bool back) {
+  const int32_t each = dtype == TBE_F32 || back ? 32 : 64;
+  return (C + each - 1) / each;
+}
+int64_t whole_channels(int32_t C) { return ((int64_t)C + 63) / 64 * 64; }
 
 // Tokens per warp: as many as give every warp that fits on the GPU one run,
 // in whole steps.  Up to kAlone tokens one block takes the whole batch (both
@@ -1039,9 +1160,8 @@ struct Split {
 Split split_of(int64_t N, int32_t cblocks, bool back) {
   const int64_t warps = (int64_t)sm_count() * (back ? kBlocksPerSm<true> : kBlocksPerSm<false>) * kWarps / cblocks;
   const int64_t parts = N <= kAlone || warps < kWarps ? kWarps : warps / kWarps * kWarps;
-  constexpr int kUnit = 2 * kStep;  // whole slots of every type
-  int64_t run = ((N + parts - 1) / parts + kUnit - 1) / kUnit * kUnit;
-  if (run < kUnit) run = kUnit;
+  int64_t run = ((N + parts - 1) / parts + kStep - 1) / kStep * kStep;
+  if (run < kStep) run = kStep;
   Split s;
   s.run = (int32_t)run;
   s.blocks = (int32_t)((N + run * kWarps - 1) / (run * kWarps));
@@ -1054,9 +1174,10 @@ Split split_of(int64_t N, int32_t cblocks, bool back) {
 struct Workspace {
   size_t block, warp, partial, arrived, bytes;
 };
-Workspace layout(int64_t N, int32_t C, bool backward) {
-  const Split sp = split_of(N, channel_blocks(C), backward);
-  const size_t Cp = (size_t)channel_blocks(C) * 32;
+Workspace layout(int64_t N, int32_t C, int32_t dtype, bool backward) {
+  const int32_t cblocks = channel_blocks(C, dtype, backward);
+  const Split sp = split_of(N, cblocks, backward);
+  const size_t Cp = (size_t)whole_channels(C);
   Workspace w;
   size_t at = 0;
   w.block = w.warp = w.arrived = 0;
@@ -1069,7 +1190,7 @@ Workspace layout(int64_t N, int32_t C, bool backward) {
   if (backward && sp.blocks > 1) {
     at += round256((size_t)sp.blocks * C * 4);
     w.arrived = at;
-    at += round256((size_t)channel_blocks(C) * 4);
+    at += round256((size_t)cblocks * 4);
   }
   w.bytes = at;
   return w;
@@ -1191,8 +1312,7 @@ ScanArgs args_of(const tbe_scan_inputs* in) {
   a.S = in->sequences;
   a.C = in->channels;
   a.h0 = in->h0;
-  a.cblocks = channel_blocks(in->channels);
-  a.Cp = (int64_t)a.cblocks * 32;
+  a.Cp = whole_channels(in->channels);
   return a;
 }
 
@@ -1203,11 +1323,12 @@ int check_jagged(const tbe_scan_inputs* in) {
   return TBE_OK;
 }
 
-int use_workspace(ScanArgs& a, bool backward, void* workspace, size_t bytes) {
+int use_workspace(ScanArgs& a, int32_t dtype, bool backward, void* workspace, size_t bytes) {
+  a.cblocks = channel_blocks(a.C, dtype, backward);
   const Split sp = split_of(a.N, a.cblocks, backward);
   a.run = sp.run;
   a.blocks = sp.blocks;
-  const Workspace w = layout(a.N, a.C, backward);
+  const Workspace w = layout(a.N, a.C, dtype, backward);
   if (bytes < w.bytes) return TBE_ERR_WORKSPACE;
   if (w.bytes == 0) return TBE_OK;
   if (!workspace) return TBE_ERR_INVALID_ARG;
@@ -1229,9 +1350,9 @@ extern "C" {
 
 int64_t tbe_gated_scan_states(int64_t tokens) { return tokens < 1 ? 1 : (tokens + kStep - 1) / kStep; }
 
-size_t tbe_gated_scan_workspace_bytes(int64_t tokens, int32_t channels, int32_t backward) {
+size_t tbe_gated_scan_workspace_bytes(int64_t tokens, int32_t channels, int32_t dtype, int32_t backward) {
   if (tokens < 0 || channels < 1) return 0;
-  return layout(tokens, channels, backward != 0).bytes;
+  return layout(tokens, channels, dtype, backward != 0).bytes;
 }
 
 int tbe_gated_scan(const tbe_scan_inputs* in, void* h, int64_t h_stride, float* h_last, float* states,
@@ -1249,7 +1370,7 @@ int tbe_gated_scan(const tbe_scan_inputs* in, void* h, int64_t h_stride, float* 
   a.status = dev_status;
   cudaStream_t s = (cudaStream_t)stream;
   trace_begin(s);
-  st = use_workspace(a, false, workspace, workspace_bytes);
+  st = use_workspace(a, in->dtype, false, workspace, workspace_bytes);
   if (st != TBE_OK) return st;
   st = dispatch(a, in->dtype, kForward, s);
   trace_mark(s, "gated_scan");
@@ -1287,7 +1408,7 @@ int tbe_gated_scan_backward(const tbe_scan_inputs* in, const void* dh, int64_t d
   a.ddecay = out->ddecay;
   a.status = dev_status;
   trace_begin(s);
-  st = use_workspace(a, true, workspace, workspace_bytes);
+  st = use_workspace(a, in->dtype, true, workspace, workspace_bytes);
   if (st != TBE_OK) return st;
   st = dispatch(a, in->dtype, kBackward, s);
   trace_mark(s, "gated_scan_backward");

@@ -44,7 +44,7 @@ def declare(lib):
     P, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     for name, res, args in [
         ("tbe_gated_scan_states", i64, [i64]),
-        ("tbe_gated_scan_workspace_bytes", sz, [i64, i32, i32]),
+        ("tbe_gated_scan_workspace_bytes", sz, [i64, i32, i32, i32]),
         ("tbe_gated_scan", ctypes.c_int, [P, P, i64, P, P, P, sz, P, P]),
         ("tbe_gated_scan_backward", ctypes.c_int, [P, P, i64, P, P, P, P, sz, P, P]),
         ("tbe_gated_scan_step", ctypes.c_int, [P, P, P, i64, P]),
@@ -112,9 +112,9 @@ def _run(fn, what, dev, stream, *args):
 
 
 @functools.lru_cache(maxsize=4096)
-def _scan_workspace(N, C, backward, dev):
+def _scan_workspace(N, C, dtype, backward, dev):
     with torch.cuda.device(dev):
-        return int(_tbe.load_library().tbe_gated_scan_workspace_bytes(N, C, backward))
+        return int(_tbe.load_library().tbe_gated_scan_workspace_bytes(N, C, _DTYPE[dtype], backward))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -191,7 +191,7 @@ def tbe_gated_scan(x, recur, gate, decay, offsets, h0=None, sharpness: float = 8
     st = None if dev_status is None else _vector(dev_status, (1,), _I32, dev, "dev_status")
     h_last = decay.new_empty((S, C))
     states = decay.new_empty((max(1, -(-N // TBE_SCAN_STEP)), C)) if want_states else None
-    nbytes = _scan_workspace(N, C, 0, dev)
+    nbytes = _scan_workspace(N, C, dt, 0, dev)
     ws = decay.new_empty(nbytes // 4) if nbytes else None
     _run(lib.tbe_gated_scan, "tbe_gated_scan", dev, stream, a, h.data_ptr(), h_stride, h_last.data_ptr(),
          states.data_ptr() if want_states else None, ws.data_ptr() if nbytes else None, nbytes, st)
@@ -221,7 +221,7 @@ def tbe_gated_scan_backward(dh, x, recur, gate, decay, offsets, states, h0=None,
     dh0 = None if h0 is None else decay.new_empty((S, C))
     g = _SCAN_GRADS.pack(dx.data_ptr(), dr.data_ptr(), dg.data_ptr(), *strides, ddecay.data_ptr(),
                          0 if dh0 is None else dh0.data_ptr())
-    nbytes = _scan_workspace(N, C, 1, dev)
+    nbytes = _scan_workspace(N, C, dt, 1, dev)
     ws = decay.new_empty(nbytes // 4) if nbytes else None
     _run(lib.tbe_gated_scan_backward, "tbe_gated_scan_backward", dev, stream, a, dh.data_ptr(), dh_stride, last, kept, g,
          ws.data_ptr() if nbytes else None, nbytes, st)
