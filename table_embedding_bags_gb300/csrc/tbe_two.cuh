@@ -29,35 +29,15 @@ __device__ __forceinline__ float inv_root(float x) {
 
 // Two fp32 numbers in one register pair: one instruction for both.
 struct Two {
-  uint64_t v;
+  float2 v;
 };
-__device__ __forceinline__ Two two(float a, float b) {
-  Two t;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(t.v) : "f"(a), "f"(b));
-  return t;
-}
+__device__ __forceinline__ Two two(float a, float b) { return Two{make_float2(a, b)}; }
 __device__ __forceinline__ Two two(float a) { return two(a, a); }
-__device__ __forceinline__ float lo(Two t) {
-  return __uint_as_float((uint32_t)t.v);
-}
-__device__ __forceinline__ float hi(Two t) {
-  return __uint_as_float((uint32_t)(t.v >> 32));
-}
-__device__ __forceinline__ Two operator*(Two a, Two b) {
-  Two t;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t.v) : "l"(a.v), "l"(b.v));
-  return t;
-}
-__device__ __forceinline__ Two operator+(Two a, Two b) {
-  Two t;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t.v) : "l"(a.v), "l"(b.v));
-  return t;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  Two t;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return t;
-}
+__device__ __forceinline__ float lo(Two t) { return t.v.x; }
+__device__ __forceinline__ float hi(Two t) { return t.v.y; }
+__device__ __forceinline__ Two operator*(Two a, Two b) { return Two{__fmul2_rn(a.v, b.v)}; }
+__device__ __forceinline__ Two operator+(Two a, Two b) { return Two{__fadd2_rn(a.v, b.v)}; }
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) { return Two{__ffma2_rn(a.v, b.v, c.v)}; }
 __device__ __forceinline__ Two ex2(Two a) { return two(ex2(lo(a)), ex2(hi(a))); }
 __device__ __forceinline__ Two rcp(Two a) { return two(rcp(lo(a)), rcp(hi(a))); }
 __device__ __forceinline__ Two root(Two a) { return two(root(lo(a)), root(hi(a))); }
@@ -69,7 +49,7 @@ __device__ __forceinline__ Two negative(Two t) { return two(-lo(t), -hi(t)); }
 // again at each use.
 __device__ __forceinline__ Two keep(float f) {
   Two t = two(f);
-  asm volatile("" : "+l"(t.v));
+  asm volatile("" : "+f"(t.v.x), "+f"(t.v.y));
   return t;
 }
 
