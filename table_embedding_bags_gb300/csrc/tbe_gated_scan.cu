@@ -350,6 +350,7 @@ struct Ring {
   const ScanArgs& a;
   uint32_t base;   // of slot 0, in shared memory
   int left_bytes;  // of a row inside the array
+  int piece;       // bytes of a row that the lane copies at once
   int lane;
   int read, write;  // bytes from slot 0: the oldest slot, the next to be filled
   int left;         // tokens of the run that are not asked for yet
@@ -358,6 +359,8 @@ struct Ring {
   __device__ __forceinline__ Ring(const ScanArgs& args, uint8_t* m, int64_t cb, int l, int tokens)
       : mem(m), state(nullptr), a(args), base(smem_u32(m)), lane(l), read(0), write(0), left(tokens) {
     left_bytes = (int)((a.C - cb) * kSize<DT> < kRow ? (a.C - cb) * kSize<DT> : kRow);
+    const int b = left_bytes - (WIDE ? col() : lane % (kRow / 4) * 4), most = WIDE ? 16 : 4;
+    piece = b < 0 ? 0 : (b < most ? b : most);
   }
   // the lane's place in a row, and the first row it copies (WIDE)
   __device__ __forceinline__ int col() const { return WIDE ? lane % kLanes * 16 : 0; }
@@ -372,27 +375,28 @@ struct Ring {
   static __device__ __forceinline__ void copy4(uint32_t dst, const void* from, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
   }
-  // A slot of `count` tokens, by any kind of copy.  What lies outside the run
-  // (in the batch's last one), or outside the channels, reads as 0.
-  __device__ __forceinline__ void fill_part(int count) {
+  // The next slot.  What lies outside the run (in the batch's last one), or
+  // outside the channels, reads as 0: a copy of 0 bytes reads nothing.
+  __device__ __forceinline__ void fill() {
+    int count = left < kStep ? left : kStep;
+    if (DOWN && left > kStep && left % kStep) count = left % kStep;
+    left -= count;
     const uint32_t to = base + write;
     if (WIDE) {
 #pragma unroll
       for (int k = 0; k < kStep; k += kRows) {
-        const int n = k + first_row() < count && col() < left_bytes ? 16 : 0;
+        const int n = k + first_row() < count ? piece : 0;
 #pragma unroll
-        for (int i = 0; i < INPUTS; ++i)
-          copy16(to + i * kBox + k * kRow + lane * 16, n ? src[i] + k * row[i] : a.x, n);
+        for (int i = 0; i < INPUTS; ++i) copy16(to + i * kBox + k * kRow + lane * 16, src[i] + k * row[i], n);
       }
     } else if (a.copy == 4) {
       constexpr int kPieces = kRow / 4;  // of a row
 #pragma unroll
       for (int k = 0; k < kStep; k += 32 / kPieces) {
-        const int r = k + lane / kPieces, c = lane % kPieces * 4;
-        const int b = left_bytes - c, n = r >= count || b < 0 ? 0 : (b < 4 ? b : 4);
+        const int r = k + lane / kPieces, n = r < count ? piece : 0;
 #pragma unroll
         for (int i = 0; i < INPUTS; ++i)
-          copy4(to + i * kBox + r * kRow + c, n ? src[i] + r * row[i] + c : a.x, n);
+          copy4(to + i * kBox + k * kRow + lane * 4, src[i] + r * row[i] + lane % kPieces * 4, n);
       }
     } else {
 #pragma unroll 4
@@ -408,29 +412,11 @@ struct Ring {
     }
 #pragma unroll
     for (int i = 0; i < INPUTS; ++i) src[i] += (DOWN ? -kStep : kStep) * row[i];
-  }
-  // The next slot.
-  __device__ __forceinline__ void fill() {
-    int count = left < kStep ? left : kStep;
-    if (DOWN && left > kStep && left % kStep) count = left % kStep;
-    left -= count;
-    if (WIDE && count == kStep) {
-      const uint32_t to = base + write + lane * 16;
-      const int n = col() < left_bytes ? 16 : 0;
-#pragma unroll
-      for (int i = 0; i < INPUTS; ++i) {
-#pragma unroll
-        for (int k = 0; k < kStep; k += kRows) copy16(to + i * kBox + k * kRow, src[i] + k * row[i], n);
-        src[i] += (DOWN ? -kStep : kStep) * row[i];
-      }
-    } else {
-      fill_part(count);
-    }
     if (DOWN) {
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         const bool ok = count > 0 && (v * 32 + lane) * kSize<DT> < left_bytes;
-        copy4(base + write + INPUTS * kBox + (v * 32 + lane) * 4, ok ? state + v * 32 + lane : (const float*)a.x, ok ? 4 : 0);
+        copy4(to + INPUTS * kBox + (v * 32 + lane) * 4, state + v * 32 + lane, ok ? 4 : 0);
       }
       state -= a.C;
     }
