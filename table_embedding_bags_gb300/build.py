@@ -1,8 +1,10 @@
-"""In-tree build of libtbe.so for sm_103a (GB300).
+"""In-tree build of libtbe.so for sm_103a (GB300) and of the compiled binding.
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel with nvcc and the
-objects are linked into ``table_embedding_bags_gb300/libtbe.so``.  Nothing is
-installed outside the repository.
+objects are linked into ``table_embedding_bags_gb300/libtbe.so``;
+``csrc/marshal.cpp`` becomes ``table_embedding_bags_gb300/_marshal.so``, a
+Python module against the installed torch.  Nothing is installed outside the
+repository.
 """
 
 from __future__ import annotations
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtbe.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -61,16 +66,42 @@ def _compile(src: str, verbose: bool, extra) -> str:
     return obj
 
 
+def _compile_marshal(verbose: bool) -> None:
+    import torch
+
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    include = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(home, "lib")
+    tmp = MARSHAL + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-I{d}" for d in include],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", MARSHAL_SRC, "-o", tmp, f"-L{lib}", "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile (if stale) and return the path of libtbe.so."""
     deps = _deps()
+    binding = force or _stale(MARSHAL, [MARSHAL_SRC, os.path.join(INCLUDE, "tbe.h")])
     if not force and not ptxas_info and not _stale(LIB, deps):
+        if binding:
+            _compile_marshal(verbose)
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        other = ex.submit(_compile_marshal, verbose) if binding else None
         objs = list(ex.map(lambda s: _compile(s, verbose or ptxas_info, extra), srcs))
+        if other is not None:
+            other.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
