@@ -176,6 +176,21 @@ def test_empty_sequences_and_tile_edges(tbe, lengths):
     check_all(tbe, make(sum(lengths), len(lengths), 6, "f32", 3, lengths=lengths), "f32")
 
 
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("C", [6, 34, 129, 256])
+@pytest.mark.parametrize("lengths", [[1] * 700 + [5000] + [2] * 900, [4000] + [0] * 500 + [1] * 900 + [0] * 40,
+                                     [0] * 400 + [3, 40] * 90 + [2500], [37] * 300])
+def test_many_sequences_of_uneven_length(tbe, lengths, C, kind):
+    """Sequences that do not lie where equal lengths would put them, at every width of copy."""
+    check_all(tbe, make(sum(lengths), len(lengths), C, kind, C, lengths=lengths, i32=C % 2 == 0), kind)
+
+
+@pytest.mark.parametrize("kind,C", [("f16", 64), ("bf16", 34), ("bf16", 33)])
+def test_long_half_precision_sequences(tbe, kind, C):
+    """Many blocks along the tokens: a block's way back to the last start is longer than a warp's."""
+    check_all(tbe, make(40000, 2, C, kind, C, lengths=[39000, 1000]), kind)
+
+
 def test_nothing_but_empty_sequences(tbe):
     d = make(0, 5, 9, "bf16", 1, lengths=[0] * 5)
     f, b = run(tbe, d)
