@@ -12,7 +12,15 @@
 //
 // Three kernels: the rows' log-sums (one pass over the logits with a running
 // maximum and sum per thread; a long row is cut over several thread blocks
-// where there are few rows), the pairs, and the gradient.
+// where there are few rows), the pairs, and the gradient, each started while
+// the one before it ends.  A small batch goes through one kernel.
+//
+// A large batch is bound by memory: the logits are read twice and the gradient
+// written once.  3,840 rows of 100,000 bf16 logits take 373 us: the log-sums
+// 128 us (6.0 TB/s; with an exponential per element, whose rate alone would
+// take 83 us), the gradient 233 us (6.6 TB/s), the pairs the rest.  The second
+// reading finds nothing in the 129 MB L2, because the whole batch lies between
+// the two: a pair's coefficient needs both its sequences' sums.
 #include "tbe_internal.cuh"
 
 #include <cmath>
@@ -25,7 +33,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;
-// A warp takes a row where rows are short enough.
+// A warp takes a row of at most this length where one cluster has the batch
+// (80 rows of 1,000: 8.0 us, with blocks to them 14.5 us).
 constexpr int kWarpRow = 1024;
 
 struct PrefArgs {
@@ -109,7 +118,8 @@ __device__ __forceinline__ uint4 ld_plain16(const void* p) {
 
 // A run of n elements from p on, read by `workers` threads of which this is
 // number `me`: elements before the first 16-byte boundary and after the last
-// one on their own, the rest in 16-byte pieces, four in flight per thread.
+// one on their own, the rest in 16-byte pieces, four in flight per thread (2,
+// 3, 4, 6, 8: 380, 381, 374, 401, 403 us for 3,840 rows of 100,000 bf16).
 template <int DT>
 __device__ __forceinline__ Run sum_row(const uint8_t* p, int64_t n, int me, int workers) {
   constexpr int kE = Vec<DT>::kElems, kS = Vec<DT>::kSize, kFlight = 4;
@@ -177,43 +187,55 @@ __device__ __forceinline__ int64_t label_of(const PrefArgs& a, int64_t n) {
   return y < 0 ? -1 : y;
 }
 
-// A row's log-sum and its label's log-probability.  A row of which every
-// entry is -inf has nothing to choose from: it takes no part (lse = -inf).
+// A row's label, and the label's logit.
+struct Label {
+  int64_t y;
+  float logit;
+};
 template <int DT>
-__device__ __forceinline__ void finish_row(const PrefArgs& a, int64_t n, Run r) {
+__device__ __forceinline__ Label read_label(const PrefArgs& a, int64_t n) {
   const int64_t y = label_of(a, n);
+  return Label{y, y >= 0 ? load_one<DT>(a.logits, n * a.stride + y) : 0.f};
+}
+// A row's log-sum and its label's log-probability (returned).  A row of which
+// every entry is -inf has nothing to choose from: it takes no part (lse = -inf).
+__device__ __forceinline__ float finish_row(const PrefArgs& a, int64_t n, Run r, Label l) {
   const float lse = r.s == 0.f ? -INFINITY : r.m + logf(r.s);
   a.lse[n] = lse;
-  a.lp[n] = y >= 0 && lse != -INFINITY ? load_one<DT>(a.logits, n * a.stride + y) - lse : 0.f;
+  return l.y >= 0 && lse != -INFINITY ? l.logit - lse : 0.f;
 }
 
-// One thread block per (row, split), or one warp per row (WARP).
-template <int DT, bool WARP>
-__global__ void __launch_bounds__(kThreads) rows_kernel(PrefArgs a) {
-  __shared__ Run s_run[kWarps];
+// LANES threads to a row: a warp (blocks of kWarps rows), or a block of that
+// many threads to a piece of a row.
+template <int LANES>
+constexpr int kBlockThreads = LANES == 32 ? kThreads : LANES;
+template <int DT, int LANES>
+__global__ void __launch_bounds__(kBlockThreads<LANES>) rows_kernel(PrefArgs a) {
+  constexpr int kRowWarps = LANES / 32;
+  __shared__ Run s_run[kRowWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.arrived = 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (WARP) {
+  if (LANES == 32) {
     const int64_t n = (int64_t)blockIdx.x * kWarps + warp;
     if (n >= a.N) return;
     const Run r = warp_merge(sum_row<DT>(elem_ptr<DT>(a.logits, n * a.stride), a.V, lane, 32));
     if (lane == 0) {
-      finish_row<DT>(a, n, r);
+      a.lp[n] = finish_row(a, n, r, read_label<DT>(a, n));
       a.coef[n] = 0.f;
     }
     return;
   }
   const int64_t n = blockIdx.x / a.splits, part = blockIdx.x % a.splits;
   const int64_t lo = a.V * part / a.splits, hi = a.V * (part + 1) / a.splits;
-  Run r = warp_merge(sum_row<DT>(elem_ptr<DT>(a.logits, n * a.stride + lo), hi - lo, threadIdx.x, kThreads));
+  Run r = warp_merge(sum_row<DT>(elem_ptr<DT>(a.logits, n * a.stride + lo), hi - lo, threadIdx.x, LANES));
   if (lane == 0) s_run[warp] = r;
   __syncthreads();
   if (warp == 0) {
-    r = lane < kWarps ? s_run[lane] : Run{kLowest, 0.f};
+    r = lane < kRowWarps ? s_run[lane] : Run{kLowest, 0.f};
     r = warp_merge(r);
     if (lane == 0) {
-      if (a.splits == 1) finish_row<DT>(a, n, r);
+      if (a.splits == 1) a.lp[n] = finish_row(a, n, r, read_label<DT>(a, n));
       else a.part[n * a.splits + part] = make_float2(r.m, r.s);
       if (part == 0) a.coef[n] = 0.f;
     }
@@ -237,16 +259,32 @@ __device__ __forceinline__ float pair_loss(const PrefArgs& a, int64_t b, int lan
     if (lo[t] < 0) lo[t] = 0;
     if (hi[t] > a.N) hi[t] = a.N;
     float s = 0.f;
-    for (int64_t n = lo[t] + lane; n < hi[t]; n += 32) {
-      if (a.splits > 1) {
+    if (a.splits == 1) {
+      for (int64_t n = lo[t] + lane; n < hi[t]; n += 32) s += __ldcg(a.lp + n);
+    } else {
+      // 32 / each lanes to a row's pieces, so that few rows do not leave the
+      // loads to few lanes
+      const int64_t rows = hi[t] - lo[t];
+      const int each = rows >= 32 ? 32 : (rows >= 16 ? 16 : (rows >= 8 ? 8 : 4)), lanes = 32 / each, sub = lane % lanes;
+      for (int64_t i = lane / lanes; i < (rows + each - 1) / each * each; i += each) {
+        const int64_t n = lo[t] + i;
+        const bool in = i < rows;
+        const Label l = in && sub == 0 ? read_label<DT>(a, n) : Label{-1, 0.f};
         Run r{kLowest, 0.f};
-        for (int p = 0; p < a.splits; ++p) {
+#pragma unroll 8
+        for (int p = in ? sub : a.splits; p < a.splits; p += lanes) {
           const float2 v = __ldcg(a.part + n * a.splits + p);
           r = merge(r, Run{v.x, v.y});
         }
-        finish_row<DT>(a, n, r);
+        for (int o = lanes >> 1; o; o >>= 1) {
+          Run other;
+          other.m = __shfl_xor_sync(kFull, r.m, o);
+          other.s = __shfl_xor_sync(kFull, r.s, o);
+          r = merge(r, other);
+        }
+        if (in && sub == 0) s += finish_row(a, n, r, l);
       }
-      s += __ldcg(a.lp + n);
+      __syncwarp();  // the rows' log-sums are read again below, by other lanes
     }
     logp[t] = warp_sum(s);
     if (lane == 0) a.logps[q] = logp[t];
@@ -365,8 +403,9 @@ __device__ __forceinline__ void grad_row(const uint8_t* p, uint8_t* o, int64_t n
   }
 }
 
-template <int DT, bool WARP>
-__global__ void __launch_bounds__(kThreads) grad_kernel(PrefArgs a) {
+template <int DT, int LANES>
+__global__ void __launch_bounds__(kBlockThreads<LANES>) grad_kernel(PrefArgs a) {
+  constexpr bool WARP = LANES == 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n = WARP ? (int64_t)blockIdx.x * kWarps + warp : blockIdx.x / a.splits;
@@ -375,7 +414,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(PrefArgs a) {
   const int64_t lo = a.V * part / splits, hi = a.V * (part + 1) / splits;
   const float coef = a.coef[n] * a.scale;
   grad_row<DT>(elem_ptr<DT>(a.logits, n * a.stride + lo), elem_ptr<DT>(a.dlogits, n * a.dstride + lo), hi - lo,
-               a.labels[n] - lo, coef, a.lse[n], WARP ? lane : threadIdx.x, WARP ? 32 : kThreads);
+               a.labels[n] - lo, coef, a.lse[n], WARP ? lane : threadIdx.x, LANES);
 }
 
 // Small batches in one launch: one cluster of kSmallBlocks thread blocks goes
@@ -396,7 +435,7 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
     for (int64_t n = me; n < a.N; n += kSmallBlocks * kSmallWarps) {
       const Run r = warp_merge(sum_row<DT>(elem_ptr<DT>(a.logits, n * a.stride), a.V, lane, 32));
       if (lane == 0) {
-        finish_row<DT>(a, n, r);
+        a.lp[n] = finish_row(a, n, r, read_label<DT>(a, n));
         a.coef[n] = 0.f;
       }
     }
@@ -410,7 +449,7 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
       if (warp == 0) {
         r = warp_merge(lane < kSmallWarps ? s_run[lane] : Run{kLowest, 0.f});
         if (lane == 0) {
-          if (a.splits == 1) finish_row<DT>(a, n, r);
+          if (a.splits == 1) a.lp[n] = finish_row(a, n, r, read_label<DT>(a, n));
           else a.part[u] = make_float2(r.m, r.s);
           if (part == 0) a.coef[n] = 0.f;
         }
@@ -442,13 +481,22 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
 }
 
 
-// Batches of at most this many bytes of logits go through one cluster.
-constexpr int64_t kSmallBytes = 4 << 20;
+// Batches of at most this many bytes of logits go through one cluster: 2 rows
+// of 100,000 fp32 logits (0.8 MB) 10.7 us against 13.1 us of the three
+// kernels, 4 rows (1.6 MB) 13.4 against 13.5 us, 6 rows 17.5 against 13.3 us.
+constexpr int64_t kSmallBytes = 1 << 20;
 
-// Blocks per row: where there are fewer rows than would fill the GPU twice
-// over, rows are cut, into pieces of at least 2048 entries.
+// Blocks per row: where there are fewer rows than would fill the GPU four
+// times over, long rows are cut, into pieces of at least 2048 entries (pieces
+// of 512 or 8,192 make no difference).  40 rows of 100,000 bf16 logits: 19.5 us
+// against 22.7 us with a block per row; 160 rows 30.0 against 35.9 us.
 // (One cluster: as many as it has blocks.)
 bool is_small(int64_t N, int32_t V, int32_t dtype) { return N * (int64_t)V * (dtype == TBE_F32 ? 4 : 2) <= kSmallBytes; }
+// Threads to a row in the kernels of larger batches.  Loss and gradient with
+// 32, 128 and 256 threads to a row: 3,000 rows of 2,000 half-precision logits
+// 15.4, 19.6, 28.1 us; of 8,000: 36.2, 31.2, 35.4 us; 1,300 rows of 10,007:
+// 29.0, 25.2, 26.8 us; 3,840 rows of 100,000: 394, 385, 374 us.
+int lanes_of(int32_t V) { return V <= 2048 ? 32 : (V <= 16384 ? 128 : kThreads); }
 int32_t splits_of(int64_t N, int32_t V, int32_t dtype) {
   if (is_small(N, V, dtype)) {
     if (V <= kWarpRow || N < 1) return 1;
@@ -456,7 +504,7 @@ int32_t splits_of(int64_t N, int32_t V, int32_t dtype) {
     const int64_t s = want < most ? want : most;
     return s < 1 ? 1 : (int32_t)s;
   }
-  if (N <= 0 || V <= kWarpRow) return 1;
+  if (N <= 0 || lanes_of(V) == 32) return 1;
   const int64_t want = (4 * (int64_t)sm_count() + N - 1) / N, most = V / 2048;
   const int64_t s = want < most ? want : most;
   return s < 1 ? 1 : (int32_t)s;
@@ -482,10 +530,10 @@ Workspace layout(int64_t N, int32_t V, int32_t P, int32_t dtype) {
 
 // A launch that may start while the kernel before it ends (`after`).
 template <typename K>
-int start(K kernel, int64_t grid, bool after, cudaStream_t s, const PrefArgs& a) {
+int start(K kernel, int64_t grid, int threads, bool after, cudaStream_t s, const PrefArgs& a) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -496,10 +544,20 @@ int start(K kernel, int64_t grid, bool after, cudaStream_t s, const PrefArgs& a)
 }
 
 template <int DT>
+int launch_rows(const PrefArgs& a, cudaStream_t s) {
+  const int lanes = lanes_of(a.V);
+  if (lanes == 32) return start(rows_kernel<DT, 32>, (a.N + kWarps - 1) / kWarps, kThreads, false, s, a);
+  if (lanes == 128) return start(rows_kernel<DT, 128>, a.N * a.splits, 128, false, s, a);
+  return start(rows_kernel<DT, kThreads>, a.N * a.splits, kThreads, false, s, a);
+}
+
+template <int DT>
 int launch_grad(const PrefArgs& a, bool after, cudaStream_t s) {
   // (a small batch's rows may be cut finer here than a block needs: still right)
-  return a.V <= kWarpRow ? start(grad_kernel<DT, true>, (a.N + kWarps - 1) / kWarps, after, s, a)
-                         : start(grad_kernel<DT, false>, a.N * a.splits, after, s, a);
+  const int lanes = lanes_of(a.V);
+  if (lanes == 32) return start(grad_kernel<DT, 32>, (a.N + kWarps - 1) / kWarps, kThreads, after, s, a);
+  if (lanes == 128) return start(grad_kernel<DT, 128>, a.N * a.splits, 128, after, s, a);
+  return start(grad_kernel<DT, kThreads>, a.N * a.splits, kThreads, after, s, a);
 }
 
 template <int DT>
@@ -532,11 +590,10 @@ int launch_loss(const PrefArgs& a, int32_t dtype, cudaStream_t s) {
     trace_mark(s, "preference_small");
     return st;
   }
-  int st = a.V <= kWarpRow ? start(rows_kernel<DT, true>, (a.N + kWarps - 1) / kWarps, false, s, a)
-                           : start(rows_kernel<DT, false>, a.N * a.splits, false, s, a);
+  int st = launch_rows<DT>(a, s);
   if (st != TBE_OK) return st;
   trace_mark(s, "preference_rows");
-  st = start(pairs_kernel<DT>, ((int64_t)a.P + kWarps - 1) / kWarps, true, s, a);
+  st = start(pairs_kernel<DT>, ((int64_t)a.P + kWarps - 1) / kWarps, kThreads, true, s, a);
   if (st != TBE_OK) return st;
   trace_mark(s, "preference_pairs");
   if (a.dlogits) {
