@@ -16,7 +16,7 @@
 // the one before it ends.  A small batch goes through one kernel.
 //
 // A large batch is bound by memory: the logits are read twice and the gradient
-// written once.  3,840 rows of 100,000 bf16 logits take 373 us: the log-sums
+// written once.  3,840 rows of 100,000 bf16 logits take 372 us: the log-sums
 // 128 us (6.0 TB/s; with an exponential per element, whose rate alone would
 // take 83 us), the gradient 233 us (6.6 TB/s), the pairs the rest.  The second
 // reading finds nothing in the 129 MB L2, because the whole batch lies between
@@ -242,78 +242,98 @@ __global__ void __launch_bounds__(kBlockThreads<LANES>) rows_kernel(PrefArgs a) 
   }
 }
 
-// Pair b, by one warp: the sequences' sums, the margin, the loss (returned)
-// and the tokens' coefficients.
+// Pair b, by two neighbouring warps, one to a sequence: the sequences' sums,
+// the margin, the loss (returned to the first lane of the first warp, 0 to
+// the others) and the tokens' coefficients.  Every thread of the block calls
+// this; `logps` has room for its warps.  (A warp to both sequences, one after
+// the other: 1,300 rows of 10,007 f16 logits 25.1 us, so 23.4 us;
+// 6 rows of 100,000 fp32 13.3, so 10.7 us.)
 template <int DT>
-__device__ __forceinline__ float pair_loss(const PrefArgs& a, int64_t b, int lane) {
-  float logp[2];
-  int64_t lo[2], hi[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int64_t q = (int64_t)t * a.P + b;
-    lo[t] = a.offsets[q];
-    hi[t] = a.offsets[q + 1];
-    const bool bad = lo[t] < 0 || hi[t] < lo[t] || hi[t] > a.N || (q == 0 && lo[t] != 0) ||
-                     (q == 2 * (int64_t)a.P - 1 && hi[t] != a.N);
+__device__ __forceinline__ float pair_loss(const PrefArgs& a, int64_t b, int warp, int lane, float* logps) {
+  const int t = warp & 1;
+  const bool on = b < a.P;
+  const int64_t q = (int64_t)t * a.P + b;
+  int64_t lo = 0, hi = 0;
+  float ref[2] = {0.f, 0.f};
+  if (on) {
+    lo = a.offsets[q];
+    hi = a.offsets[q + 1];
+    ref[0] = a.ref[b];
+    ref[1] = a.ref[a.P + b];
+    const bool bad = lo < 0 || hi < lo || hi > a.N || (q == 0 && lo != 0) || (q == 2 * (int64_t)a.P - 1 && hi != a.N);
     if (bad && lane == 0) report(a.status, TBE_DEV_BAD_OFFSETS);
-    if (lo[t] < 0) lo[t] = 0;
-    if (hi[t] > a.N) hi[t] = a.N;
-    float s = 0.f;
-    if (a.splits == 1) {
-      for (int64_t n = lo[t] + lane; n < hi[t]; n += 32) s += __ldcg(a.lp + n);
-    } else {
-      // 32 / each lanes to a row's pieces, so that few rows do not leave the
-      // loads to few lanes
-      const int64_t rows = hi[t] - lo[t];
-      const int each = rows >= 32 ? 32 : (rows >= 16 ? 16 : (rows >= 8 ? 8 : 4)), lanes = 32 / each, sub = lane % lanes;
-      for (int64_t i = lane / lanes; i < (rows + each - 1) / each * each; i += each) {
-        const int64_t n = lo[t] + i;
-        const bool in = i < rows;
-        const Label l = in && sub == 0 ? read_label<DT>(a, n) : Label{-1, 0.f};
-        Run r{kLowest, 0.f};
-#pragma unroll 8
-        for (int p = in ? sub : a.splits; p < a.splits; p += lanes) {
-          const float2 v = __ldcg(a.part + n * a.splits + p);
-          r = merge(r, Run{v.x, v.y});
-        }
-        for (int o = lanes >> 1; o; o >>= 1) {
-          Run other;
-          other.m = __shfl_xor_sync(kFull, r.m, o);
-          other.s = __shfl_xor_sync(kFull, r.s, o);
-          r = merge(r, other);
-        }
-        if (in && sub == 0) s += finish_row(a, n, r, l);
-      }
-      __syncwarp();  // the rows' log-sums are read again below, by other lanes
-    }
-    logp[t] = warp_sum(s);
-    if (lane == 0) a.logps[q] = logp[t];
+    if (lo < 0) lo = 0;
+    if (hi > a.N) hi = a.N;
   }
-  const float d = a.beta * ((logp[0] - a.ref[b]) - (logp[1] - a.ref[a.P + b]));
+  // of this lane's first row
+  const bool have = lo + lane < hi;
+  int64_t y = -1;
+  float lse = -INFINITY;
+  float s = 0.f;
+  if (a.splits == 1) {
+    if (have) {
+      y = a.labels[lo + lane];
+      lse = __ldcg(a.lse + lo + lane);
+    }
+    for (int64_t n = lo + lane; n < hi; n += 32) s += __ldcg(a.lp + n);
+  } else {
+    // 32 / each lanes to a row's pieces, so that few rows do not leave the
+    // loads to few lanes
+    const int64_t rows = hi - lo;
+    const int each = rows >= 32 ? 32 : (rows >= 16 ? 16 : (rows >= 8 ? 8 : 4)), lanes = 32 / each, sub = lane % lanes;
+    for (int64_t i = lane / lanes; i < (rows + each - 1) / each * each; i += each) {
+      const int64_t n = lo + i;
+      const bool in = i < rows;
+      const Label l = in && sub == 0 ? read_label<DT>(a, n) : Label{-1, 0.f};
+      Run r{kLowest, 0.f};
+#pragma unroll 8
+      for (int p = in ? sub : a.splits; p < a.splits; p += lanes) {
+        const float2 v = __ldcg(a.part + n * a.splits + p);
+        r = merge(r, Run{v.x, v.y});
+      }
+      for (int o = lanes >> 1; o; o >>= 1) {
+        Run other;
+        other.m = __shfl_xor_sync(kFull, r.m, o);
+        other.s = __shfl_xor_sync(kFull, r.s, o);
+        r = merge(r, other);
+      }
+      if (in && sub == 0) s += finish_row(a, n, r, l);
+    }
+    __syncwarp();  // the rows' log-sums are read by other lanes
+    if (have) {
+      y = a.labels[lo + lane];
+      lse = __ldcg(a.lse + lo + lane);
+    }
+  }
+  s = warp_sum(s);
+  if (lane == 0) {
+    logps[warp] = s;
+    if (on) a.logps[q] = s;
+  }
+  __syncthreads();
+  const float d = a.beta * ((logps[warp & ~1] - ref[0]) - (logps[warp | 1] - ref[1]));
   // log(1 + exp(-d)) and log(1 + exp(d)) without overflow
   const float l = log1pf(expf(-fabsf(d)));
   const float loss = (1.f - a.smoothing) * (fmaxf(-d, 0.f) + l) + a.smoothing * (fmaxf(d, 0.f) + l);
   const float up = 1.f / (1.f + expf(-d)), down = 1.f / (1.f + expf(d));
-  const float c = a.beta / (float)a.P * (a.smoothing * up - (1.f - a.smoothing) * down);
-  if (lane == 0) a.margins[b] = d;
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-    for (int64_t n = lo[t] + lane; n < hi[t]; n += 32) {
-      const int64_t y = a.labels[n];
-      a.coef[n] = y < 0 || y >= a.V || __ldcg(a.lse + n) == -INFINITY ? 0.f : (t == 0 ? c : -c);
-    }
-  return loss;
+  const float both = a.beta / (float)a.P * (a.smoothing * up - (1.f - a.smoothing) * down), c = t == 0 ? both : -both;
+  if (on && t == 0 && lane == 0) a.margins[b] = d;
+  if (have) a.coef[lo + lane] = y < 0 || y >= a.V || lse == -INFINITY ? 0.f : c;
+  for (int64_t n = lo + lane + 32; n < hi; n += 32) {
+    const int64_t label = a.labels[n];
+    a.coef[n] = label < 0 || label >= a.V || __ldcg(a.lse + n) == -INFINITY ? 0.f : c;
+  }
+  return on && t == 0 && lane == 0 ? loss : 0.f;
 }
 
-// A warp per pair.
+// Two warps per pair.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) pairs_kernel(PrefArgs a) {
-  __shared__ float s_loss[kWarps];
+  __shared__ float s_logps[kWarps], s_loss[kWarps];
   __shared__ bool s_last;
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t b = (int64_t)blockIdx.x * kWarps + warp;
-  const float loss = b < a.P ? pair_loss<DT>(a, b, lane) : 0.f;
+  const float loss = pair_loss<DT>(a, (int64_t)blockIdx.x * (kWarps / 2) + warp / 2, warp, lane, s_logps);
   if (lane == 0) s_loss[warp] = loss;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -428,6 +448,7 @@ __device__ __forceinline__ void cluster_sync() {
 template <int DT>
 __global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
   __shared__ Run s_run[kSmallWarps];
+  __shared__ float s_logps[kSmallWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int me = blockIdx.x * kSmallWarps + warp;  // the grid is one cluster
   const bool by_warp = a.V <= kWarpRow;
@@ -458,9 +479,12 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
     }
   }
   cluster_sync();
-  for (int64_t b = me; b < a.P; b += kSmallBlocks * kSmallWarps) {
-    const float loss = pair_loss<DT>(a, b, lane);
-    if (lane == 0) a.block_loss[b] = loss;
+  constexpr int kPairs = kSmallWarps / 2;  // of a block at a time
+  for (int64_t b0 = blockIdx.x * kPairs; b0 < a.P; b0 += kSmallBlocks * kPairs) {
+    const int64_t b = b0 + warp / 2;
+    const float loss = pair_loss<DT>(a, b, warp, lane, s_logps);
+    if (b < a.P && lane == 0 && warp % 2 == 0) a.block_loss[b] = loss;
+    __syncthreads();  // s_logps is free again
   }
   cluster_sync();
   if (me == 0) {
@@ -481,15 +505,18 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
 }
 
 
-// Batches of at most this many bytes of logits go through one cluster: 2 rows
-// of 100,000 fp32 logits (0.8 MB) 10.7 us against 13.1 us of the three
-// kernels, 4 rows (1.6 MB) 13.4 against 13.5 us, 6 rows 17.5 against 13.3 us.
+// Batches of at most this many bytes of logits go through one cluster, whose
+// single launch is what they pay for: 80 rows of 1,000 fp32 logits without
+// gradient take 6.6 us of the GPU either way, and calls in a row 13.8 to 16.6
+// us against 17.4 to 17.9 us.  Loss and gradient, GPU: 2 rows of 100,000 fp32
+// logits (0.8 MB) 9.7 us against 11.0 us of the three kernels, 4 rows 12.0
+// against 11.3 us, 6 rows 15.6 against 10.7 us.
 constexpr int64_t kSmallBytes = 1 << 20;
 
-// Blocks per row: where there are fewer rows than would fill the GPU four
-// times over, long rows are cut, into pieces of at least 2048 entries (pieces
-// of 512 or 8,192 make no difference).  40 rows of 100,000 bf16 logits: 19.5 us
-// against 22.7 us with a block per row; 160 rows 30.0 against 35.9 us.
+// Blocks per row: where there are at most two rows to an SM, long rows are
+// cut, to four pieces an SM of at least 2048 entries each (512 or 8,192 make no
+// difference).  40 rows of 100,000 bf16 logits: 17.4 us against 21.0 us with a
+// block per row; 160 rows 28.0 against 34.3 us; 400 rows 56.1 against 53.3 us.
 // (One cluster: as many as it has blocks.)
 bool is_small(int64_t N, int32_t V, int32_t dtype) { return N * (int64_t)V * (dtype == TBE_F32 ? 4 : 2) <= kSmallBytes; }
 // Threads to a row in the kernels of larger batches.  Loss and gradient with
@@ -504,7 +531,7 @@ int32_t splits_of(int64_t N, int32_t V, int32_t dtype) {
     const int64_t s = want < most ? want : most;
     return s < 1 ? 1 : (int32_t)s;
   }
-  if (N <= 0 || lanes_of(V) == 32) return 1;
+  if (N <= 0 || N > 2 * sm_count() || lanes_of(V) == 32) return 1;
   const int64_t want = (4 * (int64_t)sm_count() + N - 1) / N, most = V / 2048;
   const int64_t s = want < most ? want : most;
   return s < 1 ? 1 : (int32_t)s;
@@ -593,7 +620,7 @@ int launch_loss(const PrefArgs& a, int32_t dtype, cudaStream_t s) {
   int st = launch_rows<DT>(a, s);
   if (st != TBE_OK) return st;
   trace_mark(s, "preference_rows");
-  st = start(pairs_kernel<DT>, ((int64_t)a.P + kWarps - 1) / kWarps, kThreads, true, s, a);
+  st = start(pairs_kernel<DT>, ((int64_t)a.P + kWarps / 2 - 1) / (kWarps / 2), kThreads, true, s, a);
   if (st != TBE_OK) return st;
   trace_mark(s, "preference_pairs");
   if (a.dlogits) {
