@@ -102,17 +102,39 @@ double number_of(PyObject* o) {
   return d;
 }
 
-// The stream's handle: an integer, or None for the current stream.
-void* stream_of(PyObject* o, at::Device dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-  void* s = PyLong_AsVoidPtr(o);
-  if (PyErr_Occurred()) throw Refused{""};
-  return s;
-}
-
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
 }
+
+// Where a call's kernels go: the stream of a handle (an integer), or the
+// current one for None.  It is made current while the call allocates, so that
+// new memory is the stream's own: a workspace that goes back at the end of the
+// call is then only handed out again behind the kernels that use it.
+class Stream {
+ public:
+  Stream(PyObject* o, at::Device dev) : device_(dev), caller_(c10::cuda::getCurrentCUDAStream(dev.index())), s_(caller_) {
+    if (o == Py_None) return;
+    void* handle = PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) throw Refused{""};
+    if (handle == caller_.stream()) return;
+    s_ = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), dev.index());
+    use_.reset_stream(s_);
+  }
+  void* handle() const { return s_.stream(); }
+  // A result.  The caller's own stream is as likely to use it, so that its
+  // memory is not handed out again before that one is through with it either.
+  at::Tensor result(at::IntArrayRef shape, at::ScalarType type) const {
+    at::Tensor t = empty(shape, type, caller_.device());
+    if (handle() != caller_.stream()) t.record_stream(caller_.unwrap());
+    return t;
+  }
+  at::Tensor workspace(size_t bytes) const { return empty({(int64_t)bytes}, at::kByte, caller_.device()); }
+
+ private:
+  c10::cuda::CUDAGuard device_;
+  c10::cuda::CUDAStream caller_, s_;
+  c10::cuda::OptionalCUDAStreamGuard use_;
+};
 
 void check(int rc, const char* what) {
   if (rc != TBE_OK) refuse(what, " failed: ", abi.status_string(rc), " (", rc, ")");
@@ -161,9 +183,10 @@ Scan scan_of(PyObject* x_, PyObject* r_, PyObject* g_, PyObject* decay_, PyObjec
 }
 
 // An output: the given tensor, or a new one.  Returns its row stride.
-int64_t output(PyObject* given, int64_t rows, int64_t cols, const Scan& s, const char* what, at::Tensor& t) {
+int64_t output(PyObject* given, int64_t rows, int64_t cols, const Scan& s, const Stream& stream, const char* what,
+               at::Tensor& t) {
   if (given == Py_None) {
-    t = empty({rows, cols}, s.type, s.dev);
+    t = stream.result({rows, cols}, s.type);
     return cols;
   }
   t = tensor(given, what);
@@ -189,16 +212,16 @@ PyObject* tuple(const T&... t) {
 PyObject* scan(PyObject* const* a) {
   const Scan s = scan_of(a[0], a[1], a[2], a[3], a[4], a[5], a[6]);
   const int64_t N = s.in.tokens, C = s.in.channels, S = s.in.sequences;
-  const c10::cuda::CUDAGuard guard(s.dev);
+  const Stream stream(a[10], s.dev);
   at::Tensor h, states, ws;
-  const int64_t stride = output(a[8], N, C, s, "out", h);
-  at::Tensor h_last = empty({S, C}, at::kFloat, s.dev);
-  if (PyObject_IsTrue(a[7])) states = empty({abi.scan_states(N), C}, at::kFloat, s.dev);
+  const int64_t stride = output(a[8], N, C, s, stream, "out", h);
+  at::Tensor h_last = stream.result({S, C}, at::kFloat);
+  if (PyObject_IsTrue(a[7])) states = stream.result({abi.scan_states(N), C}, at::kFloat);
   const size_t bytes = abi.scan_workspace(N, s.in.channels, s.in.dtype, 0);
-  if (bytes) ws = empty({(int64_t)bytes}, at::kByte, s.dev);
+  if (bytes) ws = stream.workspace(bytes);
   check(abi.scan(&s.in, h.data_ptr(), stride, static_cast<float*>(h_last.data_ptr()),
                  states.defined() ? static_cast<float*>(states.data_ptr()) : nullptr, bytes ? ws.data_ptr() : nullptr, bytes,
-                 status_of(a[9], s.dev), stream_of(a[10], s.dev)),
+                 status_of(a[9], s.dev), stream.handle()),
         "tbe_gated_scan");
   return tuple(h, h_last, states);
 }
@@ -207,7 +230,7 @@ PyObject* scan(PyObject* const* a) {
 PyObject* scan_backward(PyObject* const* a) {
   const Scan s = scan_of(a[1], a[2], a[3], a[4], a[5], a[7], a[9]);
   const int64_t N = s.in.tokens, C = s.in.channels, S = s.in.sequences;
-  const c10::cuda::CUDAGuard guard(s.dev);
+  const Stream stream(a[12], s.dev);
   const at::Tensor& dh = tensor(a[0], "dh");
   const int64_t dh_stride = rows_of(dh, N, C, s.type, s.dev, "dh");
   if (a[6] == Py_None) refuse("states is required");
@@ -220,20 +243,20 @@ PyObject* scan_backward(PyObject* const* a) {
   }
   at::Tensor dx, dr, dg, dh0, ws;
   tbe_scan_grads g = {};
-  g.dx_stride = output(given[0], N, C, s, "dx", dx);
-  g.drecur_stride = output(given[1], N, C, s, "drecur", dr);
-  g.dgate_stride = output(given[2], N, C, s, "dgate", dg);
-  at::Tensor ddecay = empty({C}, at::kFloat, s.dev);
-  if (a[7] != Py_None) dh0 = empty({S, C}, at::kFloat, s.dev);
+  g.dx_stride = output(given[0], N, C, s, stream, "dx", dx);
+  g.drecur_stride = output(given[1], N, C, s, stream, "drecur", dr);
+  g.dgate_stride = output(given[2], N, C, s, stream, "dgate", dg);
+  at::Tensor ddecay = stream.result({C}, at::kFloat);
+  if (a[7] != Py_None) dh0 = stream.result({S, C}, at::kFloat);
   g.dx = dx.data_ptr();
   g.drecur = dr.data_ptr();
   g.dgate = dg.data_ptr();
   g.ddecay = static_cast<float*>(ddecay.data_ptr());
   g.dh0 = dh0.defined() ? static_cast<float*>(dh0.data_ptr()) : nullptr;
   const size_t bytes = abi.scan_workspace(N, s.in.channels, s.in.dtype, 1);
-  if (bytes) ws = empty({(int64_t)bytes}, at::kByte, s.dev);
+  if (bytes) ws = stream.workspace(bytes);
   check(abi.scan_backward(&s.in, dh.data_ptr(), dh_stride, dh_last, states, &g, bytes ? ws.data_ptr() : nullptr, bytes,
-                          status_of(a[11], s.dev), stream_of(a[12], s.dev)),
+                          status_of(a[11], s.dev), stream.handle()),
         "tbe_gated_scan_backward");
   return tuple(dx, dr, dg, ddecay, dh0);
 }
@@ -242,12 +265,12 @@ PyObject* scan_backward(PyObject* const* a) {
 PyObject* scan_step(PyObject* const* a) {
   const Scan s = scan_of(a[0], a[1], a[2], a[3], nullptr, nullptr, a[5]);
   const int64_t S = s.in.tokens, C = s.in.channels;
-  const c10::cuda::CUDAGuard guard(s.dev);
+  const Stream stream(a[7], s.dev);
   if (a[4] == Py_None) refuse("state is required");
   float* state = floats_of<float>(a[4], {S, C}, s.dev, "state");
   at::Tensor h;
-  const int64_t stride = output(a[6], S, C, s, "out", h);
-  check(abi.scan_step(&s.in, state, h.data_ptr(), stride, stream_of(a[7], s.dev)), "tbe_gated_scan_step");
+  const int64_t stride = output(a[6], S, C, s, stream, "out", h);
+  check(abi.scan_step(&s.in, state, h.data_ptr(), stride, stream.handle()), "tbe_gated_scan_step");
   return wrap(h);
 }
 
@@ -284,13 +307,13 @@ Preference preference_of(PyObject* const* a, double beta, double smoothing) {
 }
 // The gradient's room: the given tensor, or a new one with the logits' row
 // stride, so that both rows start on the same alignment.
-int64_t gradient_room(Preference& p, PyObject* given) {
+int64_t gradient_room(Preference& p, PyObject* given, const Stream& s) {
   const int64_t N = p.in.tokens, V = p.in.vocab, stride = p.in.logits_stride;
   if (given != Py_None) {
     p.dlogits = tensor(given, "dlogits");
     return rows_of(p.dlogits, N, V, p.type, p.dev, "dlogits");
   }
-  p.dlogits = empty({N, stride}, p.type, p.dev);
+  p.dlogits = s.result({N, stride}, p.type);
   if (stride != V) p.dlogits = p.dlogits.narrow(1, 0, V);
   return stride;
 }
@@ -300,17 +323,17 @@ int64_t gradient_room(Preference& p, PyObject* given) {
 PyObject* preference(PyObject* const* a) {
   Preference p = preference_of(a, number_of(a[4]), number_of(a[5]));
   const double scale = number_of(a[7]);
-  const c10::cuda::CUDAGuard guard(p.dev);
+  const Stream stream(a[10], p.dev);
   int64_t d_stride = 0;
-  if (a[8] != Py_None || PyObject_IsTrue(a[6])) d_stride = gradient_room(p, a[8]);
+  if (a[8] != Py_None || PyObject_IsTrue(a[6])) d_stride = gradient_room(p, a[8], stream);
   const int64_t N = p.in.tokens, P = p.in.pairs;
   const int64_t start = (4 * (1 + 3 * P + 2 * N) + 255) / 256 * 256;
   const size_t bytes = abi.preference_workspace(N, p.in.vocab, p.in.pairs, p.in.dtype);
-  at::Tensor room = empty({(start + (int64_t)bytes) / 4}, at::kFloat, p.dev);
+  at::Tensor room = stream.result({(start + (int64_t)bytes) / 4}, at::kFloat);
   float* f = static_cast<float*>(room.data_ptr());
   check(abi.preference(&p.in, f, f + 1, f + 1 + 2 * P, f + 1 + 3 * P, f + 1 + 3 * P + N,
                        p.dlogits.defined() ? p.dlogits.data_ptr() : nullptr, d_stride, (float)scale, f + start / 4, bytes,
-                       status_of(a[9], p.dev), stream_of(a[10], p.dev)),
+                       status_of(a[9], p.dev), stream.handle()),
         "tbe_preference_loss");
   return tuple(room, p.dlogits);
 }
@@ -319,13 +342,13 @@ PyObject* preference(PyObject* const* a) {
 PyObject* preference_backward(PyObject* const* a) {
   Preference p = preference_of(a, 1.0, 0.0);
   const double scale = number_of(a[6]);
-  const c10::cuda::CUDAGuard guard(p.dev);
+  const Stream stream(a[8], p.dev);
   const int64_t N = p.in.tokens;
   if (a[4] == Py_None || a[5] == Py_None) refuse("lse and coef are required");
   const float* lse = floats_of<const float>(a[4], {N}, p.dev, "lse");
   const float* coef = floats_of<const float>(a[5], {N}, p.dev, "coef");
-  const int64_t stride = gradient_room(p, a[7]);
-  check(abi.preference_backward(&p.in, lse, coef, (float)scale, p.dlogits.data_ptr(), stride, stream_of(a[8], p.dev)),
+  const int64_t stride = gradient_room(p, a[7], stream);
+  check(abi.preference_backward(&p.in, lse, coef, (float)scale, p.dlogits.data_ptr(), stride, stream.handle()),
         "tbe_preference_loss_backward");
   return wrap(p.dlogits);
 }

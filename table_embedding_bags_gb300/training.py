@@ -4,7 +4,9 @@ A gated recurrence over jagged sequences, a preference loss over catalogue
 logits and an AdamW step over a list of tensors.  As in the package's
 ``__init__``: argument checks and marshalling only, names as in
 ``include/tbe.h``, outputs allocated where none are given, everything
-enqueued on the current stream (or ``stream``).  The recurrence's and the
+enqueued on the current stream (or ``stream``, whose own memory then holds
+what the call allocates; the caller orders the streams, and keeps its tensors
+alive, as under ``with torch.cuda.stream(stream)``).  The recurrence's and the
 loss's checks are compiled (``csrc/marshal.cpp``): their smallest calls take
 the GPU a few microseconds.
 """

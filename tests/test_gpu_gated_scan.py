@@ -401,3 +401,47 @@ def test_refusals(tbe):
         tbe.tbe_gated_scan_backward(d["dh"][:, :3], *ins, f.states)
     with pytest.raises(tbe.TBEError):
         tbe.tbe_gated_scan_step(*ins[:4], d["h0"])  # ten tokens, two states
+
+
+def pool_of(t):
+    """The handle of the stream whose memory a tensor lies in."""
+    at = t.data_ptr()
+    return next(s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= at < s["address"] + s["total_size"])
+
+
+def test_calls_on_a_given_stream_keep_their_buffers(tbe):
+    """``stream=``: what a call allocates is the given stream's memory, and is not handed out again before that
+    stream, and the caller's, are through with it."""
+    data = [make(40_000, 3, 96, "bf16", 30 + i, lengths=[30_000, 0, 10_000]) for i in range(2)]
+    want = [run(tbe, d) for d in data]
+    sides = [torch.cuda.Stream() for _ in data]
+    torch.cuda.synchronize()
+    got = []
+    for d, side in zip(data, sides):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(40_000_000)  # the calls wait behind it, so that both streams' kernels run together
+        ins = [d[k] for k in ("x", "recur", "gate", "decay", "offsets")]
+        f = tbe.tbe_gated_scan(*ins, h0=d["h0"], want_states=True, stream=side)
+        got.append((f, tbe.tbe_gated_scan_backward(d["dh"], *ins, f.states, h0=d["h0"], dh_last=d["dh_last"], stream=side)))
+        junk = [torch.full((1 << k,), 255, dtype=torch.uint8, device="cuda") for k in range(8, 26) for _ in range(3)]
+        del junk
+    torch.cuda.synchronize()
+    for (f0, b0), (f, b), side in zip(want, got, sides):
+        for p, q in zip((*f0, *b0), (*f, *b)):
+            assert torch.equal(p, q)
+            assert pool_of(q) == side.cuda_stream != torch.cuda.current_stream().cuda_stream
+    state = data[0]["h0"].clone()
+    ins = [data[0][k][:3] for k in ("x", "recur", "gate")] + [data[0]["decay"]]
+    torch.cuda.synchronize()
+    h = tbe.tbe_gated_scan_step(*ins, state, stream=sides[0])
+    torch.cuda.synchronize()
+    assert pool_of(h) == sides[0].cuda_stream
+    torch.cuda._sleep(40_000_000)  # the current stream may still read f.h
+    f = got[0][0].h
+    at = f.data_ptr()
+    got[0] = None
+    del p, q, f0, b0, b, f
+    with torch.cuda.stream(sides[0]):
+        again = [torch.empty(40_000, 96, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    assert at not in [t.data_ptr() for t in again]
+    torch.cuda.synchronize()

@@ -246,3 +246,30 @@ def test_refusals(tbe):
             tbe.tbe_preference_loss(**{**d, key: value}, want_grad=True)
     with pytest.raises(tbe.TBEError):
         tbe.tbe_preference_loss(**d, want_grad=True, grad_scale=float("nan"))
+
+
+@pytest.mark.parametrize("V", [100, 7001])
+def test_calls_on_a_given_stream_keep_their_buffers(tbe, V):
+    """``stream=``: results and workspace are the given stream's memory, whatever is allocated and written on the
+    current stream behind the call."""
+    data = [make(50, 900, V, "bf16", 30 + i) for i in range(2)]
+    want = [tbe.tbe_preference_loss(**d, want_grad=True) for d in data]
+    sides = [torch.cuda.Stream() for _ in data]
+    torch.cuda.synchronize()
+    got = []
+    for d, side in zip(data, sides):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(40_000_000)  # the calls wait behind it, so that both streams' kernels run together
+        grad = tbe.tbe_preference_loss(**d, want_grad=True, stream=side).dlogits  # the rest goes back at once
+        r = tbe.tbe_preference_loss(**d, stream=side)
+        got.append((grad, r, tbe.tbe_preference_loss_backward(**d, saved=r, stream=side)))
+        junk = [torch.full((1 << k,), 255, dtype=torch.uint8, device="cuda") for k in range(8, 26) for _ in range(3)]
+        del junk
+    torch.cuda.synchronize()
+    pools = torch.cuda.memory_snapshot()
+    for w, (grad, r, alone), side in zip(want, got, sides):
+        assert torch.equal(grad, w.dlogits) and torch.equal(alone, w.dlogits)
+        assert torch.equal(r.loss, w.loss) and torch.equal(r.seq_logps, w.seq_logps) and torch.equal(r.coef, w.coef)
+        for t in (grad, alone, r.loss):
+            owner = [s["stream"] for s in pools if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
+            assert owner == [side.cuda_stream]
