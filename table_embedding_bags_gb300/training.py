@@ -210,7 +210,10 @@ class AdamWPlan:
     starting on a block of 256 elements (``slices[i]``): fp32 for
     ``state_bits`` 32, codes with one scale per block (``exp_avg_scale``,
     ``exp_avg_sq_scale``) for 8.  ``state``: a dict with those tensors, to go
-    on from (they are used as they are, not copied)."""
+    on from (they are used as they are, not copied).  A step may go to another
+    stream than the plan's (the caller orders the two): what the plan holds is
+    then kept from reuse until that stream is through with it, also where the
+    plan takes other tensors or ends before."""
 
     def __init__(self, params, grads, state_bits: int = 32, state=None, stream=None):
         params, grads = list(params), list(grads)
@@ -229,19 +232,21 @@ class AdamWPlan:
         self.slices = [slice(int(s), int(s + n)) for s, n in zip(starts, self.numel)]
         self._h = ctypes.c_void_p()
         self._bind(params, grads, stream)
+        self._state_home, self._state_seen = self._home, set()
         want = {"exp_avg": torch.float32, "exp_avg_sq": torch.float32}
         if state_bits == 8:
             want = {"exp_avg": torch.int8, "exp_avg_sq": torch.uint8, "exp_avg_scale": torch.float32,
                     "exp_avg_sq_scale": torch.float32}
         for name, dt in want.items():
             n = self.blocks if name.endswith("scale") else self.blocks * TBE_ADAMW_BLOCK
-            t = torch.zeros(n, dtype=dt, device=self.device) if state is None else state.get(name)
+            with torch.cuda.stream(stream):
+                t = torch.zeros(n, dtype=dt, device=self.device) if state is None else state.get(name)
             _vector(t, (n,), dt, self.device, f"state[{name!r}]")
             setattr(self, name, t)
         if state_bits == 32:
             self.exp_avg_scale = self.exp_avg_sq_scale = None
-        self._state_addr = tuple(None if t is None else t.data_ptr() for t in (
-            self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale))
+        self._states = (self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)
+        self._state_addr = tuple(None if t is None else t.data_ptr() for t in self._states)
 
     def _bind(self, params, grads, stream):
         n = len(params)
@@ -263,15 +268,19 @@ class AdamWPlan:
         nbytes = lib.tbe_adamw_plan_device_bytes(n, self.numel.ctypes.data, self.state_bits)
         if nbytes == 0:
             raise _tbe.TBEError("tbe_adamw_plan_device_bytes: sizes out of range")
-        meta = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        with torch.cuda.device(self.device):
+            home = _tbe._stream(stream)
+            with torch.cuda.stream(stream):
+                meta = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         L = _AdamWTensors(n, self.state_bits, self.numel.ctypes.data, p.ctypes.data, g.ctypes.data, pd.ctypes.data,
                           gd.ctypes.data)
         h = ctypes.c_void_p()
         with torch.cuda.device(self.device):
-            _tbe._check(lib.tbe_adamw_plan_create(ctypes.byref(L), meta.data_ptr(), nbytes, _tbe._stream(stream),
-                                                  ctypes.byref(h)), "tbe_adamw_plan_create")
+            _tbe._check(lib.tbe_adamw_plan_create(ctypes.byref(L), meta.data_ptr(), nbytes, home, ctypes.byref(h)),
+                        "tbe_adamw_plan_create")
         self._release()
         self._h, self._meta, self.params, self.grads = h, meta, params, grads
+        self._home, self._seen = home.value or 0, set()  # the plan's stream, others that have read it
 
     def rebind(self, params=None, grads=None, stream=None):
         """Takes new parameter and/or gradient tensors (same sizes)."""
@@ -282,6 +291,8 @@ class AdamWPlan:
         """Calls an entry point of the plan with the plan's device current."""
         fn, dev = getattr(_tbe._lib, name), self.device.index
         handle = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if handle != self._home or handle != self._state_home:
+            self._used_on(handle, torch.cuda.current_stream(dev) if stream is None else stream)
         if torch.cuda.current_device() != dev:
             with torch.cuda.device(dev):
                 rc = fn(self._h, *args, handle)
@@ -289,6 +300,17 @@ class AdamWPlan:
             rc = fn(self._h, *args, handle)
         if rc != _tbe.TBE_OK:
             _tbe._check(rc, name)
+
+    def _used_on(self, handle, stream):
+        """Keeps the memory of what the plan holds from reuse until ``stream``
+        is through with it (noted once per stream)."""
+        for home, seen, tensors in ((self._home, self._seen, (self._meta, *self.params, *self.grads)),
+                                    (self._state_home, self._state_seen, self._states)):
+            if handle != home and handle not in seen:
+                seen.add(handle)
+                for t in tensors:
+                    if t is not None:
+                        t.record_stream(stream)
 
     def _release(self):
         if self._h.value and _tbe._lib is not None:
@@ -319,7 +341,12 @@ def tbe_adamw_state(plan: AdamWPlan, stream=None):
     the states themselves for 32 bits, what the codes stand for for 8."""
     if plan.state_bits == 32:
         return plan.exp_avg, plan.exp_avg_sq
-    m = torch.empty(plan.blocks * TBE_ADAMW_BLOCK, dtype=torch.float32, device=plan.device)
-    v = torch.empty_like(m)
+    caller = torch.cuda.current_stream(plan.device)
+    with torch.cuda.stream(stream):
+        m = torch.empty(plan.blocks * TBE_ADAMW_BLOCK, dtype=torch.float32, device=plan.device)
+        v = torch.empty_like(m)
+    if stream is not None and stream != caller:  # the caller's own stream is as likely to use them
+        m.record_stream(caller)
+        v.record_stream(caller)
     plan._call("tbe_adamw_state", stream, *plan._state_addr, m.data_ptr(), v.data_ptr())
     return m, v

@@ -364,3 +364,62 @@ def test_refusals(tbe):
         with pytest.raises(E):
             tbe.tbe_adamw_step(plan, **HYPER, **kw)
     assert (p[0] == 1).all()
+
+
+def pool_of(t):
+    """The handle of the stream whose memory a tensor lies in."""
+    at = t.data_ptr()
+    return next(s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= at < s["address"] + s["total_size"])
+
+
+def churn():
+    """Takes and writes freed memory of the current stream, of all sizes."""
+    return [torch.full((1 << k,), 255, dtype=torch.uint8, device="cuda") for k in range(8, 24) for _ in range(4)]
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_steps_on_another_stream_keep_what_the_plan_holds(tbe, bits):
+    """A plan that takes other gradients, or ends, while a step on another stream still reads its table of addresses,
+    its old gradients and its states."""
+    p, g = tensors(SIZES, "bf16", 0.05, 21), tensors(SIZES, "bf16", 1e-2, 22)
+    q = [t.clone() for t in p]
+    other = tbe.AdamWPlan(q, g, state_bits=bits)
+    for step in (1, 2):
+        tbe.tbe_adamw_step(other, **{**HYPER, "step": step})
+    side = torch.cuda.Stream()
+    plan = tbe.AdamWPlan(p, g, state_bits=bits)
+    torch.cuda.synchronize()
+    held = {plan._meta.data_ptr(), plan.exp_avg.data_ptr(), *(t.data_ptr() for t in g if t.numel())}
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(60_000_000)  # the steps wait behind it
+    tbe.tbe_adamw_step(plan, stream=side, **{**HYPER, "step": 1})
+    fresh = [t.clone() for t in g]
+    side.wait_stream(torch.cuda.current_stream())
+    plan.rebind(grads=fresh)
+    side.wait_stream(torch.cuda.current_stream())
+    del g, other
+    junk = churn()
+    tbe.tbe_adamw_step(plan, stream=side, **{**HYPER, "step": 2})
+    del plan, fresh
+    junk += churn()
+    assert not held & {t.data_ptr() for t in junk}
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(p, q))
+
+
+def test_a_plan_on_a_given_stream(tbe):
+    """``stream=`` at the plan's creation: its table and states are that stream's memory, written in its order; so
+    are the values of 8-bit states read on a given stream."""
+    p, g = tensors(SIZES, "f32", 0.05, 23), tensors(SIZES, "f32", 1e-2, 24)
+    q = [t.clone() for t in p]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    plan = tbe.AdamWPlan(p, g, state_bits=8, stream=side)
+    tbe.tbe_adamw_step(plan, stream=side, **HYPER)
+    values = tbe.tbe_adamw_state(plan, stream=side)
+    torch.cuda.synchronize()
+    for t in (plan._meta, plan.exp_avg, plan.exp_avg_sq, plan.exp_avg_scale, *values):
+        assert pool_of(t) == side.cuda_stream
+    same = tbe.AdamWPlan(q, g, state_bits=8)
+    tbe.tbe_adamw_step(same, **HYPER)
+    assert all(torch.equal(a, b) for a, b in zip((*p, *values), (*q, *tbe.tbe_adamw_state(same))))
