@@ -453,7 +453,10 @@ __device__ __forceinline__ void step_8(const StepArgs& a, const Raw8<PDT, GDT>& 
   else store_out(reinterpret_cast<__nv_bfloat16*>(pp), f, kPer, true);
   float scale_m, scale_v;
   const float inv_m = block_inverse(top_m, &scale_m), inv_v = block_inverse(top_v, &scale_v);
-  // roots in codes: the codes' number goes under the root with the scale
+  // Roots in codes: the codes' number goes under the root with the scale.  For
+  // a largest magnitude below 2^-114 (m) or 2^-96 (v) that factor is infinite
+  // and distances below are NaN, which max_nan keeps: every code then comes
+  // from the division that follows.
   const Two km = two(inv_m * 16129.f), kv = two(inv_v * 4228250625.f);
   const Two magic = two(12582912.f), back = two(-12582912.f);
   uint32_t cq[kPer], cz[kPer];
@@ -464,7 +467,7 @@ __device__ __forceinline__ void step_8(const StepArgs& a, const Raw8<PDT, GDT>& 
     Two c = two(copysignf(root(fabsf(lo(ym))), lo(ym)), copysignf(root(fabsf(hi(ym))), hi(ym)));
     Two r = c + magic;
     Two d = c + negative(r + back);
-    off = fmaxf(fmaxf(off, fabsf(lo(d))), fabsf(hi(d)));
+    off = max_nan(max_nan(off, fabsf(lo(d))), fabsf(hi(d)));
     cq[2 * j] = __float_as_uint(lo(r));
     cq[2 * j + 1] = __float_as_uint(hi(r));
     c = root(root(yv));
@@ -472,11 +475,11 @@ __device__ __forceinline__ void step_8(const StepArgs& a, const Raw8<PDT, GDT>& 
     c = two(fmaxf(lo(c), __saturatef(lo(c) * 1e30f)), fmaxf(hi(c), __saturatef(hi(c) * 1e30f)));
     r = c + magic;
     d = c + negative(r + back);
-    off = fmaxf(fmaxf(off, fabsf(lo(d))), fabsf(hi(d)));
+    off = max_nan(max_nan(off, fabsf(lo(d))), fabsf(hi(d)));
     cz[2 * j] = __float_as_uint(lo(r));
     cz[2 * j + 1] = __float_as_uint(hi(r));
   }
-  if (off > kNearLevel) {  // some code is close to its neighbour: its level decides
+  if (!(off <= kNearLevel)) {  // some code is close to its neighbour: its level decides
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const float mj = j & 1 ? hi(m[j / 2]) : lo(m[j / 2]), vj = j & 1 ? hi(v[j / 2]) : lo(v[j / 2]);

@@ -423,3 +423,25 @@ def test_a_plan_on_a_given_stream(tbe):
     same = tbe.AdamWPlan(q, g, state_bits=8)
     tbe.tbe_adamw_step(same, **HYPER)
     assert all(torch.equal(a, b) for a, b in zip((*p, *values), (*q, *tbe.tbe_adamw_state(same))))
+
+
+@pytest.mark.parametrize("misaligned", [False, True])
+def test_codes_of_tiny_moments(tbe, misaligned):
+    """Second moments down to 2^-126, and first moments below 1e-34 beside second ones of zero: codes and scales of
+    whole aligned blocks and of single elements equal the restatement's bit for bit, zeros among them."""
+    rng = np.random.default_rng(13)
+    size = 10.0 ** np.repeat(np.concatenate([np.arange(-11, -20, -0.5), np.arange(-32, -38, -0.5)]), BLOCK)
+    values = (rng.standard_normal(len(size)) * size).astype(F)
+    values[rng.random(len(size)) < 0.2] = 0
+    values[3 * BLOCK:3 * BLOCK + 8] = 0  # nothing but zeros in a lane's eight elements
+    n = len(values)
+    g = torch.from_numpy(np.concatenate([[F(0)], values])).cuda()
+    g = g[1:] if misaligned else g[1:].clone()
+    zero = (np.zeros(n, np.int8), np.zeros(n, np.uint8), np.zeros(n // BLOCK, F), np.zeros(n // BLOCK, F))
+    plan = plan8(tbe, [torch.zeros(n, device="cuda")], [g], zero)
+    tbe.tbe_adamw_step(plan, **HYPER)
+    _, v, *want = step8(values, *zero, HYPER)
+    for name, got, exp in zip(("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"), codes(plan), want):
+        assert np.array_equal(got, exp), f"{name}: {np.sum(got != exp)} differ"
+    held = np.repeat(codes(plan)[3] > 0, BLOCK)
+    assert (codes(plan)[1][held & (v > 0)] > 0).all()
