@@ -188,10 +188,19 @@ __device__ __forceinline__ void store(int dt, void* base, int64_t at, int lane, 
   }
 }
 
-// Byte b of w as a float: its bits under 2^23's exponent, less 2^23.
-__device__ __forceinline__ float byte_float(uint32_t w, int b) {
-  return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + b)) - 8388608.f;
-}
+// Codes as floats: a byte's bits under the exponent of 2^17 (2^16) are
+// 2^17 + byte / 64 (2^16 + byte / 128).  A code of a first moment counts in
+// units of 1/64, one of a second moment in units of 1/128, so that a block's
+// scale is multiplied by 64^2 / 127^2 = 0.25 (128^4 / 255^4 = 0.06): by 1 / 127^2
+// (1 / 255^4) a scale below 2e-34 (5e-29) would leave the normal numbers, and
+// with them its precision, before the codes are multiplied in.
+constexpr float kUnitM = (float)(64.0 * 64.0 / (127.0 * 127.0));
+constexpr float kUnitV = (float)(128.0 * 128.0 * 128.0 * 128.0 / (255.0 * 255.0 * 255.0 * 255.0));
+constexpr float kBaseM = 131072.f + 2.f, kBaseV = 65536.f;  // 2: a first moment's code comes plus 128
+__device__ __forceinline__ float byte_m(uint32_t w, int b) { return __uint_as_float(__byte_perm(w, 0x48000000u, 0x7640 + b)); }
+__device__ __forceinline__ float byte_v(uint32_t w, int b) { return __uint_as_float(__byte_perm(w, 0x47800000u, 0x7640 + b)); }
+__device__ __forceinline__ float code_m(uint32_t w, int b) { return byte_m(w ^ 0x80808080u, b) - kBaseM; }
+__device__ __forceinline__ float code_v(uint32_t w, int b) { return byte_v(w, b) - kBaseV; }
 
 // The scale that divides a block whose largest magnitude is `top`: its
 // inverse, or 0 where there is nothing to divide by: a block below the
@@ -250,14 +259,13 @@ __device__ __forceinline__ void update_block(const StepArgs& a, const TensorMeta
     unpack<VEC>(TBE_F32, rm, m);
     unpack<VEC>(TBE_F32, rv, v);
   } else {
-    const float cm = __fmul_rn(sm, (float)(1.0 / (127.0 * 127.0)));
-    const float cv = __fmul_rn(sv, (float)(1.0 / (255.0 * 255.0 * 255.0 * 255.0)));
+    const float cm = __fmul_rn(sm, kUnitM), cv = __fmul_rn(sv, kUnitV);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const uint32_t wm = VEC ? rm[j / 4] : rm[j], wv = VEC ? rv[j / 4] : rv[j];
-      const float q = byte_float(wm ^ 0x80808080u, VEC ? j % 4 : 0) - 128.f;
+      const float q = code_m(wm, VEC ? j % 4 : 0);
       m[j] = __fmul_rn(q * fabsf(q), cm);
-      const float z = byte_float(wv, VEC ? j % 4 : 0);
+      const float z = code_v(wv, VEC ? j % 4 : 0);
       const float z2 = z * z;
       v[j] = __fmul_rn(__fmul_rn(z2, z2), cv);
     }
@@ -407,17 +415,15 @@ __device__ __forceinline__ uint32_t pack4(const uint32_t* c) {
 template <int PDT, int GDT>
 __device__ __forceinline__ void step_8(const StepArgs& a, const Raw8<PDT, GDT>& x, uint8_t* pp, int64_t block, int lane,
                                        Two gscale) {
-  const Two cm = two(__fmul_rn(x.sm, (float)(1.0 / (127.0 * 127.0))));
-  const Two cv = two(__fmul_rn(x.sv, (float)(1.0 / (255.0 * 255.0 * 255.0 * 255.0))));
+  const Two cm = two(__fmul_rn(x.sm, kUnitM)), cv = two(__fmul_rn(x.sv, kUnitV));
   Two m[kPer / 2], v[kPer / 2];
   float top_m = 0.f, top_v = 0.f;
 #pragma unroll
   for (int j = 0; j < kPer / 2; ++j) {
     const uint32_t wm = x.m[j / 2] ^ 0x80808080u, wv = x.v[j / 2];  // the signed codes plus 128
     const int b = 2 * j % 4;
-    auto byte = [](uint32_t w, int i) { return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + i)); };
-    const Two q = two(byte(wm, b), byte(wm, b + 1)) + two(-8388608.f - 128.f);
-    const Two z = two(byte(wv, b), byte(wv, b + 1)) + two(-8388608.f);
+    const Two q = two(byte_m(wm, b), byte_m(wm, b + 1)) + two(-kBaseM);
+    const Two z = two(byte_v(wv, b), byte_v(wv, b + 1)) + two(-kBaseV);
     const Two z2 = z * z;
     const Two g = raw_pair<GDT>(x.g, j) * gscale;
     m[j] = rounded_sum(two(lo(q) * fabsf(lo(q)), hi(q) * fabsf(hi(q))) * cm * two(a.b1), g * two(a.c1));
@@ -589,14 +595,13 @@ __global__ void __launch_bounds__(kThreads)
   ld2(m + i * 8, rm);
   ld2(v + i * 8, rv);
   const int64_t block = i / (kBlock / 8);
-  const float cm = __fmul_rn(__ldg(ms + block), (float)(1.0 / (127.0 * 127.0)));
-  const float cv = __fmul_rn(__ldg(vs + block), (float)(1.0 / (255.0 * 255.0 * 255.0 * 255.0)));
+  const float cm = __fmul_rn(__ldg(ms + block), kUnitM), cv = __fmul_rn(__ldg(vs + block), kUnitV);
   float fm[8], fv[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float q = byte_float(rm[j / 4] ^ 0x80808080u, j % 4) - 128.f;
+    const float q = code_m(rm[j / 4], j % 4);
     fm[j] = __fmul_rn(q * fabsf(q), cm);
-    const float z = byte_float(rv[j / 4], j % 4);
+    const float z = code_v(rv[j / 4], j % 4);
     const float z2 = z * z;
     fv[j] = __fmul_rn(__fmul_rn(z2, z2), cv);
   }

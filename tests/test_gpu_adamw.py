@@ -445,3 +445,30 @@ def test_codes_of_tiny_moments(tbe, misaligned):
         assert np.array_equal(got, exp), f"{name}: {np.sum(got != exp)} differ"
     held = np.repeat(codes(plan)[3] > 0, BLOCK)
     assert (codes(plan)[1][held & (v > 0)] > 0).all()
+
+
+@pytest.mark.parametrize("misaligned", [False, True])
+def test_small_scales_stand_for_their_values(tbe, misaligned):
+    """Scales down to the smallest normal number: what codes stand for, read back and in a step.  Bounds: five
+    roundings of 2^-24, of which one may be of a number up to 2^-4 below the normal ones (2^-20), and half the
+    smallest number (2^-150)."""
+    rng = np.random.default_rng(14)
+    scales = np.concatenate([2.0 ** np.arange(-125, -60.0), [2.0 ** -125 * 1.7, 1e-36, 1e-3, 1e30]]).astype(F)
+    blocks = len(scales)
+    n = blocks * BLOCK
+    qm, qv = rng.integers(-127, 128, n).astype(np.int8), rng.integers(0, 256, n).astype(np.uint8)
+    qm[::BLOCK], qv[::BLOCK] = 127, 255
+    room = torch.zeros(n + 1, device="cuda")
+    p, g = (room[1:], torch.zeros(n + 1, device="cuda")[1:]) if misaligned else (room[:n], torch.zeros(n, device="cuda"))
+    plan = plan8(tbe, [p], [g], (qm, qv, scales, scales))
+    s = np.repeat(scales, BLOCK).astype(np.float64)
+    want_m = np.sign(qm) * (np.abs(qm) / 127.0) ** 2 * s
+    want_v = (qv / 255.0) ** 4 * s
+    for got, want in zip(tbe.tbe_adamw_state(plan), (want_m, want_v)):
+        assert np.all(np.abs(f64(got) - want) <= 2.0 ** -19 * np.abs(want) + 2.0 ** -149)
+    tbe.tbe_adamw_step(plan, **HYPER)  # no gradients: the largest moments shrink by the betas
+    _, _, sm, sv = codes(plan)
+    for got, beta in ((sm, HYPER["beta1"]), (sv, HYPER["beta2"])):
+        want = beta * scales.astype(np.float64)
+        on = want >= 1.001 * np.finfo(F).tiny
+        assert np.all(np.abs(got[on] - want[on]) <= 2.0 ** -19 * want[on])
