@@ -468,7 +468,9 @@ int tbe_gated_scan_step(const tbe_scan_inputs* in, float* state, void* h, int64_
  *   loss = mean_b (1 - label_smoothing) log(1 + exp(-d_b)) + label_smoothing log(1 + exp(d_b))
  * A token with y < 0 takes no part and gets a zero gradient; so does one
  * with y >= vocab (TBE_DEV_BAD_INDEX is set) and one whose logits are all
- * -inf.  Single -inf entries have probability 0.
+ * -inf.  Single -inf entries have probability 0; where one is a label's the
+ * sequence's sum is -inf, the margin infinite, and a term of the loss whose
+ * weight is 0 counts as 0.
  *   logits    : device, [tokens, vocab] of dtype, logits_stride apart
  *   labels    : device int64 [tokens]
  *   offsets   : device int64 [2 * pairs + 1], from 0 to tokens, else

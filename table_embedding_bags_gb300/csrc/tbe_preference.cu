@@ -314,7 +314,11 @@ __device__ __forceinline__ float pair_loss(const PrefArgs& a, int64_t b, int war
   const float d = a.beta * ((logps[warp & ~1] - ref[0]) - (logps[warp | 1] - ref[1]));
   // log(1 + exp(-d)) and log(1 + exp(d)) without overflow
   const float l = log1pf(expf(-fabsf(d)));
-  const float loss = (1.f - a.smoothing) * (fmaxf(-d, 0.f) + l) + a.smoothing * (fmaxf(d, 0.f) + l);
+  // A term of weight 0 counts as 0: d is infinite where a label's logit is
+  // -inf, and the other term is then the whole loss.
+  float loss = 0.f;
+  if (a.smoothing != 1.f) loss = (1.f - a.smoothing) * (fmaxf(-d, 0.f) + l);
+  if (a.smoothing != 0.f) loss += a.smoothing * (fmaxf(d, 0.f) + l);
   const float up = 1.f / (1.f + expf(-d)), down = 1.f / (1.f + expf(d));
   const float both = a.beta / (float)a.P * (a.smoothing * up - (1.f - a.smoothing) * down), c = t == 0 ? both : -both;
   if (on && t == 0 && lane == 0) a.margins[b] = d;

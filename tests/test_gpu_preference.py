@@ -273,3 +273,26 @@ def test_calls_on_a_given_stream_keep_their_buffers(tbe, V):
         for t in (grad, alone, r.loss):
             owner = [s["stream"] for s in pools if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
             assert owner == [side.cuda_stream]
+
+
+@pytest.mark.parametrize("V", [90, 9000])
+@pytest.mark.parametrize("eps,seq,want", [(0.0, 1, 0.0), (0.0, 0, np.inf), (1.0, 0, 0.0), (1.0, 1, np.inf),
+                                          (0.1, 0, np.inf), (0.1, 1, np.inf)])
+def test_masked_labels(tbe, V, eps, seq, want):
+    """A label whose logit is -inf in one sequence of a pair: its margin is infinite, its loss 0 or infinite by the
+    definition (a term of weight 0 counts as 0), the other pairs are as they were."""
+    d = make(3, 60, V, "f32", 14, lengths=[10] * 6, ignore=0.0)
+    clean = tbe.tbe_preference_loss(**d, label_smoothing=eps, want_grad=True)
+    row = (seq * 3 + 1) * 10 + 4  # pair 1
+    d["logits"][row, d["labels"][row]] = float("-inf")
+    r = tbe.tbe_preference_loss(**d, label_smoothing=eps, want_grad=True)
+    m = clean.margins.double().cpu().numpy()
+    each = (1 - eps) * np.logaddexp(0, -m) + eps * np.logaddexp(0, m)
+    each[1] = want
+    assert float(r.margins[1]) == (-np.inf if seq == 0 else np.inf)
+    assert torch.equal(r.margins[[0, 2]], clean.margins[[0, 2]])
+    got = float(r.loss)
+    assert got == np.inf if want == np.inf else abs(got - each.mean()) <= 2.0 ** -20 * each.mean()
+    assert torch.isfinite(r.dlogits).all()
+    other = torch.tensor([n for n in range(60) if n // 10 % 3 != 1], device="cuda")
+    assert torch.equal(r.dlogits[other], clean.dlogits[other])
