@@ -403,11 +403,6 @@ __device__ __forceinline__ Two raw_pair(const uint32_t* r, int j) {
 __device__ __forceinline__ Two rounded_sum(Two a, Two b) {
   return two(__fadd_rn(lo(a), lo(b)), __fadd_rn(hi(a), hi(b)));
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack4(const uint32_t* c) {
   return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }

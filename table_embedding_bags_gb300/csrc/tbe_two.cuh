@@ -27,6 +27,13 @@ __device__ __forceinline__ float inv_root(float x) {
   return y;
 }
 
+// The larger one, NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Two fp32 numbers in one register pair: one instruction for both.
 struct Two {
   float2 v;

@@ -445,3 +445,28 @@ def test_calls_on_a_given_stream_keep_their_buffers(tbe):
         again = [torch.empty(40_000, 96, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
     assert at not in [t.data_ptr() for t in again]
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [100, 1500, 20_000])
+def test_nan_gate_stays_out_of_what_does_not_depend_on_it(tbe, N, kind):
+    """gate[t] enters h from t on, and of the gradients dx[t], dgate[t] and what h enters: drecur from t on.  The
+    others are as in the reference (channels that forget slowly: both gates from one reciprocal)."""
+    C, ch, start, end = 40, 3, N // 4, N - N // 5
+    d = make(N, 3, C, kind, 20, lengths=[start, end - start, N - end])
+    d["decay"].clamp_(max=-4.5)
+    ref = ref_of(d)
+    at = start + (end - start) // 3
+    d["gate"][at, ch] = float("nan")
+    f, b = run(tbe, d)
+    hit = {name: np.zeros((N, C), bool) for name in ("h", "dx", "drecur", "dgate")}
+    hit["h"][at:end, ch] = hit["drecur"][at:end, ch] = True
+    hit["dx"][at, ch] = hit["dgate"][at, ch] = True
+    for name, got in (("h", f.h), ("dx", b.dx), ("drecur", b.drecur), ("dgate", b.dgate)):
+        got = got.double().cpu().numpy()
+        assert np.isnan(got[hit[name]]).all(), name
+        value, err = (a[~hit[name]] for a in ref[name])
+        check(torch.from_numpy(got[~hit[name]]), (value, err), kind, name)
+    other = [c for c in range(C) if c != ch]
+    check(b.ddecay[other], tuple(a[other] for a in ref["ddecay"]), "f32", "ddecay")
+    check(b.dh0, ref["dh0"], "f32", "dh0")
