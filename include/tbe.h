@@ -493,7 +493,8 @@ typedef struct tbe_preference_inputs {
 } tbe_preference_inputs;
 
 /* Workspace on the current device (device memory, 256-byte aligned, no
- * initialisation needed). */
+ * initialisation needed).  After tbe_preference_loss it begins with lse_low,
+ * fp32 [tokens]: what the rounding of lse left. */
 size_t tbe_preference_workspace_bytes(int64_t tokens, int32_t vocab, int32_t pairs, int32_t dtype);
 
 /*   loss      : device fp32 scalar
@@ -507,9 +508,16 @@ int tbe_preference_loss(const tbe_preference_inputs* in, float* loss, float* seq
                         float* coef, void* dlogits, int64_t dlogits_stride, float grad_scale, void* workspace,
                         size_t workspace_bytes, int32_t* dev_status, void* stream);
 
-/* The gradient on its own, from the lse and coef of tbe_preference_loss. */
+/* The gradient on its own, from the lse, coef and (..._low) lse_low of
+ * tbe_preference_loss.  With lse_low it is that call's gradient bit for bit;
+ * without, probabilities carry the rounding of lse, up to 2^-24 |lse| of their
+ * size: 2^-17 where logits lie around 100, everything for a row of nothing
+ * but the type's lowest value. */
 int tbe_preference_loss_backward(const tbe_preference_inputs* in, const float* lse, const float* coef,
                                  float grad_scale, void* dlogits, int64_t dlogits_stride, void* stream);
+int tbe_preference_loss_backward_low(const tbe_preference_inputs* in, const float* lse, const float* lse_low,
+                                     const float* coef, float grad_scale, void* dlogits, int64_t dlogits_stride,
+                                     void* stream);
 
 /*
  * One AdamW step over a list of tensors in one launch:

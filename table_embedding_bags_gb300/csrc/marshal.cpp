@@ -30,7 +30,7 @@ struct Abi {
   decltype(&tbe_gated_scan_states) scan_states;
   decltype(&tbe_gated_scan_workspace_bytes) scan_workspace;
   decltype(&tbe_preference_loss) preference;
-  decltype(&tbe_preference_loss_backward) preference_backward;
+  decltype(&tbe_preference_loss_backward_low) preference_backward;
   decltype(&tbe_preference_workspace_bytes) preference_workspace;
   decltype(&tbe_status_string) status_string;
 } abi = {};
@@ -40,7 +40,7 @@ const char* const kNames[] = {"tbe_gated_scan",
                               "tbe_gated_scan_states",
                               "tbe_gated_scan_workspace_bytes",
                               "tbe_preference_loss",
-                              "tbe_preference_loss_backward",
+                              "tbe_preference_loss_backward_low",
                               "tbe_preference_workspace_bytes",
                               "tbe_status_string"};
 PyObject* error_type = nullptr;
@@ -319,7 +319,7 @@ int64_t gradient_room(Preference& p, PyObject* given, const Stream& s) {
 }
 
 // (logits, labels, offsets, ref_logps, beta, label_smoothing, want_grad, grad_scale, dlogits, dev_status, stream)
-// -> (one fp32 buffer: loss, seq_logps, margins, lse, coef and the workspace; dlogits)
+// -> (one fp32 buffer: loss, seq_logps, margins, lse, coef and the workspace, which begins with lse_low; dlogits)
 PyObject* preference(PyObject* const* a) {
   Preference p = preference_of(a, number_of(a[4]), number_of(a[5]));
   const double scale = number_of(a[7]);
@@ -338,17 +338,19 @@ PyObject* preference(PyObject* const* a) {
   return tuple(room, p.dlogits);
 }
 
-// (logits, labels, offsets, ref_logps, lse, coef, grad_scale, dlogits, stream) -> dlogits
+// (logits, labels, offsets, ref_logps, lse, lse_low, coef, grad_scale, dlogits, stream) -> dlogits
 PyObject* preference_backward(PyObject* const* a) {
   Preference p = preference_of(a, 1.0, 0.0);
-  const double scale = number_of(a[6]);
-  const Stream stream(a[8], p.dev);
+  const double scale = number_of(a[7]);
+  const Stream stream(a[9], p.dev);
   const int64_t N = p.in.tokens;
-  if (a[4] == Py_None || a[5] == Py_None) refuse("lse and coef are required");
+  for (int i = 4; i < 7; ++i)
+    if (a[i] == Py_None) refuse("lse, lse_low and coef are required");
   const float* lse = floats_of<const float>(a[4], {N}, p.dev, "lse");
-  const float* coef = floats_of<const float>(a[5], {N}, p.dev, "coef");
-  const int64_t stride = gradient_room(p, a[7], stream);
-  check(abi.preference_backward(&p.in, lse, coef, (float)scale, p.dlogits.data_ptr(), stride, stream.handle()),
+  const float* low = floats_of<const float>(a[5], {N}, p.dev, "lse_low");
+  const float* coef = floats_of<const float>(a[6], {N}, p.dev, "coef");
+  const int64_t stride = gradient_room(p, a[8], stream);
+  check(abi.preference_backward(&p.in, lse, low, coef, (float)scale, p.dlogits.data_ptr(), stride, stream.handle()),
         "tbe_preference_loss_backward");
   return wrap(p.dlogits);
 }
@@ -398,7 +400,7 @@ PyMethodDef methods[] = {{"init", init, METH_VARARGS, nullptr},
                          {"gated_scan_backward", FAST(scan_backward, 13)},
                          {"gated_scan_step", FAST(scan_step, 8)},
                          {"preference_loss", FAST(preference, 11)},
-                         {"preference_loss_backward", FAST(preference_backward, 9)},
+                         {"preference_loss_backward", FAST(preference_backward, 10)},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

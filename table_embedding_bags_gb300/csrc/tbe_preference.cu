@@ -6,6 +6,9 @@
 //   d_b   = beta ((s(0, b) - ref(0, b)) - (s(1, b) - ref(1, b)))
 //   loss  = mean_b (1 - e) log(1 + exp(-d_b)) + e log(1 + exp(d_b))
 //   dlogit[n, v] = coef_n ([v = y_n] - exp(logit[n, v] - lse_n))
+// lse_n is held as two fp32 numbers, its rounded value and what the rounding
+// left: a row's probabilities would otherwise share an error of 2^-24 |lse|,
+// all of log(V) for a row of nothing but the type's lowest value.
 // with coef_n = +- beta / P ((e - 1) / (1 + exp(d_b)) + e / (1 + exp(-d_b))),
 // + for a preferred token, - for a rejected one.  Sequences are the bags of
 // two features (0 preferred, 1 rejected) in the feature-major layout.
@@ -52,6 +55,7 @@ struct PrefArgs {
   float* logps;
   float* margins;
   float* lse;
+  float* low;        // what the rounding of lse left, or null (the gradient alone): 0
   float* coef;
   void* dlogits;
   int64_t dstride;
@@ -200,9 +204,17 @@ __device__ __forceinline__ Label read_label(const PrefArgs& a, int64_t n) {
 // A row's log-sum and its label's log-probability (returned).  A row of which
 // every entry is -inf has nothing to choose from: it takes no part (lse = -inf).
 __device__ __forceinline__ float finish_row(const PrefArgs& a, int64_t n, Run r, Label l) {
-  const float lse = r.s == 0.f ? -INFINITY : r.m + logf(r.s);
+  const float log_s = logf(r.s);
+  if (r.s == 0.f) {
+    a.lse[n] = -INFINITY;
+    a.low[n] = 0.f;
+    return 0.f;
+  }
+  // the sum of the maximum and log_s, and exactly what its rounding leaves
+  const float lse = __fadd_rn(r.m, log_s), got = __fsub_rn(lse, r.m);
   a.lse[n] = lse;
-  return l.y >= 0 && lse != -INFINITY ? l.logit - lse : 0.f;
+  a.low[n] = __fadd_rn(__fsub_rn(r.m, __fsub_rn(lse, got)), __fsub_rn(log_s, got));
+  return l.y >= 0 ? (l.logit - r.m) - log_s : 0.f;
 }
 
 // LANES threads to a row: a warp (blocks of kWarps rows), or a block of that
@@ -387,14 +399,15 @@ __device__ __forceinline__ uint4 pack<TBE_BF16>(const float* f) {
 // dlogit over n elements, y the label's place among them (or outside).
 template <int DT>
 __device__ __forceinline__ void grad_row(const uint8_t* p, uint8_t* o, int64_t n, int64_t y, float coef, float lse,
-                                         int me, int workers) {
+                                         float low, int me, int workers) {
   constexpr int kE = Vec<DT>::kElems, kS = Vec<DT>::kSize, kFlight = 4;
   // both rows in 16-byte pieces only where they lie alike
   int64_t head = (16 - ((uintptr_t)p & 15)) % 16 / kS;
   if (head > n || (((uintptr_t)p ^ (uintptr_t)o) & 15) != 0) head = n;
   const int64_t pieces = (n - head) / kE, tail = head + pieces * kE;
+  const float shift = -low * kLog2e;
   auto value = [&](float x, bool label) {
-    const float e = -coef * ex2((x - lse) * kLog2e);
+    const float e = -coef * ex2(fmaf(x - lse, kLog2e, shift));
     return label ? e + coef : e;
   };
   for (int64_t i = me; i < head; i += workers)
@@ -438,7 +451,7 @@ __global__ void __launch_bounds__(kBlockThreads<LANES>) grad_kernel(PrefArgs a) 
   const int64_t lo = a.V * part / splits, hi = a.V * (part + 1) / splits;
   const float coef = a.coef[n] * a.scale;
   grad_row<DT>(elem_ptr<DT>(a.logits, n * a.stride + lo), elem_ptr<DT>(a.dlogits, n * a.dstride + lo), hi - lo,
-               a.labels[n] - lo, coef, a.lse[n], WARP ? lane : threadIdx.x, LANES);
+               a.labels[n] - lo, coef, a.lse[n], a.low ? a.low[n] : 0.f, WARP ? lane : threadIdx.x, LANES);
 }
 
 // Small batches in one launch: one cluster of kSmallBlocks thread blocks goes
@@ -503,8 +516,8 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
     const int64_t n = u / a.splits, part = u % a.splits;
     const int64_t lo = a.V * part / a.splits, hi = a.V * (part + 1) / a.splits;
     grad_row<DT>(elem_ptr<DT>(a.logits, n * a.stride + lo), elem_ptr<DT>(a.dlogits, n * a.dstride + lo), hi - lo,
-                 a.labels[n] - lo, __ldcg(a.coef + n) * a.scale, __ldcg(a.lse + n), by_warp ? lane : threadIdx.x,
-                 by_warp ? 32 : kSmallThreads);
+                 a.labels[n] - lo, __ldcg(a.coef + n) * a.scale, __ldcg(a.lse + n), __ldcg(a.low + n),
+                 by_warp ? lane : threadIdx.x, by_warp ? 32 : kSmallThreads);
   }
 }
 
@@ -541,13 +554,17 @@ int32_t splits_of(int64_t N, int32_t V, int32_t dtype) {
   return s < 1 ? 1 : (int32_t)s;
 }
 
+// The workspace: what the rounding of the log-sums left (first, as callers
+// find it there), the arrival counter, and what passes between the kernels.
 struct Workspace {
-  size_t part, lp, block_loss, bytes;
+  size_t arrived, part, lp, block_loss, bytes;
 };
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 Workspace layout(int64_t N, int32_t V, int32_t P, int32_t dtype) {
   Workspace w;
-  size_t at = 256;  // the arrival counter
+  size_t at = round256((size_t)N * 4);
+  w.arrived = at;
+  at += 256;
   w.part = at;
   const int32_t s = splits_of(N, V, dtype);
   if (s > 1) at += round256((size_t)N * s * sizeof(float2));
@@ -696,7 +713,8 @@ int tbe_preference_loss(const tbe_preference_inputs* in, float* loss, float* seq
   a.dlogits = dlogits;
   a.dstride = dlogits_stride;
   a.scale = grad_scale;
-  a.arrived = reinterpret_cast<uint32_t*>(p);
+  a.low = reinterpret_cast<float*>(p);
+  a.arrived = reinterpret_cast<uint32_t*>(p + w.arrived);
   a.part = reinterpret_cast<float2*>(p + w.part);
   a.lp = reinterpret_cast<float*>(p + w.lp);
   a.block_loss = reinterpret_cast<float*>(p + w.block_loss);
@@ -710,13 +728,20 @@ int tbe_preference_loss(const tbe_preference_inputs* in, float* loss, float* seq
 
 int tbe_preference_loss_backward(const tbe_preference_inputs* in, const float* lse, const float* coef,
                                  float grad_scale, void* dlogits, int64_t dlogits_stride, void* stream) {
+  return tbe_preference_loss_backward_low(in, lse, nullptr, coef, grad_scale, dlogits, dlogits_stride, stream);
+}
+
+int tbe_preference_loss_backward_low(const tbe_preference_inputs* in, const float* lse, const float* lse_low,
+                                     const float* coef, float grad_scale, void* dlogits, int64_t dlogits_stride,
+                                     void* stream) {
   const int st = check(in);
   if (st != TBE_OK) return st;
   if (!lse || !coef || !dlogits || dlogits_stride < in->vocab || !std::isfinite(grad_scale)) return TBE_ERR_INVALID_ARG;
   if (!aligned_for(dlogits, in->dtype)) return TBE_ERR_UNSUPPORTED;
   PrefArgs a = args_of(in);
-  a.lse = const_cast<float*>(lse);    // only read
-  a.coef = const_cast<float*>(coef);  // only read
+  a.lse = const_cast<float*>(lse);      // only read
+  a.low = const_cast<float*>(lse_low);  // only read
+  a.coef = const_cast<float*>(coef);    // only read
   a.dlogits = dlogits;
   a.dstride = dlogits_stride;
   a.scale = grad_scale;

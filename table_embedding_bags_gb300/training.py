@@ -50,6 +50,7 @@ def declare(lib):
         ("tbe_preference_workspace_bytes", sz, [i64, i32, i32, i32]),
         ("tbe_preference_loss", ctypes.c_int, [P, P, P, P, P, P, P, i64, f32, P, sz, P, P]),
         ("tbe_preference_loss_backward", ctypes.c_int, [P, P, P, f32, P, i64, P]),
+        ("tbe_preference_loss_backward_low", ctypes.c_int, [P, P, P, P, f32, P, i64, P]),
         ("tbe_adamw_state_blocks", i64, [i32, P]),
         ("tbe_adamw_plan_device_bytes", sz, [i32, P, i32]),
         ("tbe_adamw_plan_create", ctypes.c_int, [P, P, sz, P, P]),
@@ -84,7 +85,7 @@ def _marshal():
                                 "table_embedding_bags_gb300.build.build()") from e
         m.init(_tbe.TBEError, {name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "tbe_gated_scan", "tbe_gated_scan_backward", "tbe_gated_scan_step", "tbe_gated_scan_states",
-            "tbe_gated_scan_workspace_bytes", "tbe_preference_loss", "tbe_preference_loss_backward",
+            "tbe_gated_scan_workspace_bytes", "tbe_preference_loss", "tbe_preference_loss_backward_low",
             "tbe_preference_workspace_bytes", "tbe_status_string")})
         _compiled = m
     return _compiled
@@ -148,9 +149,10 @@ def tbe_gated_scan_step(x, recur, gate, decay, state, sharpness: float = 8.0, ou
 
 class PreferenceLoss:
     """Results of ``tbe_preference_loss``, views of one fp32 buffer: ``loss``
-    (scalar), ``seq_logps`` [2 * pairs], ``margins`` [pairs], ``lse`` and
-    ``coef`` [tokens] (for ``tbe_preference_loss_backward``); and ``dlogits``
-    (laid out like the logits) or None."""
+    (scalar), ``seq_logps`` [2 * pairs], ``margins`` [pairs], ``lse`` (with
+    ``lse_low``, what its rounding left) and ``coef`` [tokens] (for
+    ``tbe_preference_loss_backward``); and ``dlogits`` (laid out like the
+    logits) or None."""
 
     __slots__ = ("_room", "_pairs", "_tokens", "dlogits")
 
@@ -162,6 +164,9 @@ class PreferenceLoss:
     margins = property(lambda self: self._room.narrow(0, 1 + 2 * self._pairs, self._pairs))
     lse = property(lambda self: self._room.narrow(0, 1 + 3 * self._pairs, self._tokens))
     coef = property(lambda self: self._room.narrow(0, 1 + 3 * self._pairs + self._tokens, self._tokens))
+    # at the beginning of the workspace, which follows on a multiple of 256 bytes
+    lse_low = property(lambda self: self._room.narrow(0, (1 + 3 * self._pairs + 2 * self._tokens + 63) // 64 * 64,
+                                                      self._tokens))
 
     def __iter__(self):
         return iter((self.loss, self.seq_logps, self.margins, self.dlogits, self.lse, self.coef))
@@ -185,11 +190,11 @@ def tbe_preference_loss(logits, labels, offsets, ref_logps, beta: float = 0.1, l
 
 def tbe_preference_loss_backward(logits, labels, offsets, ref_logps, saved: PreferenceLoss, grad_scale: float = 1.0,
                                  dlogits=None, stream=None):
-    """grad_scale * d loss / d logits from the ``lse`` and ``coef`` of the
-    ``tbe_preference_loss`` call on the same arguments."""
+    """grad_scale * d loss / d logits from what the ``tbe_preference_loss``
+    call on the same arguments saved: its gradient bit for bit."""
     m = _compiled or _marshal()
-    return m.preference_loss_backward(logits, labels, offsets, ref_logps, saved.lse, saved.coef, grad_scale, dlogits,
-                                      None if stream is None else stream.cuda_stream)
+    return m.preference_loss_backward(logits, labels, offsets, ref_logps, saved.lse, saved.lse_low, saved.coef, grad_scale,
+                                      dlogits, None if stream is None else stream.cuda_stream)
 
 
 # ---------------------------------------------------------------------------

@@ -296,3 +296,35 @@ def test_masked_labels(tbe, V, eps, seq, want):
     assert torch.isfinite(r.dlogits).all()
     other = torch.tensor([n for n in range(60) if n // 10 % 3 != 1], device="cuda")
     assert torch.equal(r.dlogits[other], clean.dlogits[other])
+
+
+@pytest.mark.parametrize("kind,shift", [("f32", 1e4), ("f32", -3e5), ("f32", None), ("f16", None), ("bf16", None)])
+@pytest.mark.parametrize("N,V", [(30, 200), (30, 9000), (40, 20_011), (200, 3000)])
+def test_logits_far_from_zero(tbe, N, V, kind, shift):
+    """Logits that share a large shift, and rows of nothing but the type's lowest value (shift None): probabilities
+    do not depend on the size of the log-sum.  Bounds: exponentials and their sum 2^-16 in all (as above), arguments
+    2^-22 of the distance to the log-sum, half a unit of the type; coefficients as the call returned them."""
+    d = make(3, N, V, kind, 15, ignore=0.0)
+    if shift is None:
+        d["logits"][2::3] = torch.finfo(DT[kind]).min
+    else:
+        d["logits"] += shift
+    r = tbe.tbe_preference_loss(**d, want_grad=True)
+    x = d["logits"].double().cpu().numpy()
+    top = x.max(1, keepdims=True)
+    log_s = np.log(np.exp(x - top).sum(1, keepdims=True))
+    gap = (x - top) - log_s
+    y, off = d["labels"].cpu().numpy(), d["offsets"].cpu().numpy()
+    hot = np.zeros_like(x)
+    hot[np.arange(N), y] = 1
+    lp = gap[np.arange(N), y]
+    e = 2.0 ** -16 + 2.0 ** -22 * (np.abs(lp) + 2 * log_s[:, 0])
+    s = np.array([lp[off[q]:off[q + 1]].sum() for q in range(6)])
+    es = np.array([e[off[q]:off[q + 1]].sum() + 2.0 ** -22 * np.abs(lp[off[q]:off[q + 1]]).sum() for q in range(6)])
+    check(r.seq_logps, (s, es / 2), "f32", "seq_logps")
+    c = r.coef.double().cpu().numpy()[:, None]
+    g = c * (hot - np.exp(gap))
+    eg = np.abs(c) * (np.exp(gap) * (2.0 ** -16 + 2.0 ** -22 * np.abs(gap)) + 2.0 ** -22 * hot)
+    check(r.dlogits, (g, eg / 2), kind, "dlogits")
+    only = tbe.tbe_preference_loss(**d)
+    assert torch.equal(tbe.tbe_preference_loss_backward(**d, saved=only), r.dlogits)
