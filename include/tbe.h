@@ -387,7 +387,8 @@ int tbe_backward_reduce(const tbe_plan* plan, const tbe_optimizer* opt, void* we
  *                     [sequences + 1], from 0 to tokens; empty sequences are
  *                     allowed.  Broken offsets set TBE_DEV_BAD_OFFSETS;
  *                     results are then unspecified, accesses in bounds
- *   h0              : device fp32 [sequences, channels] or NULL
+ *   h0              : device fp32 [sequences, channels] or NULL; not
+ *                     overlapping any output
  * Limits: tokens < 2^38, channels <= 2^20.
  */
 #define TBE_SCAN_STEP 8 /* tokens between two saved states */
@@ -420,7 +421,8 @@ size_t tbe_gated_scan_workspace_bytes(int64_t tokens, int32_t channels, int32_t 
 /*   h       : device [tokens, channels] of dtype, h_stride elements from
  *             token to token: every h_t, rounded once
  *   h_last  : device fp32 [sequences, channels]: each sequence's last state
- *             (an empty sequence's h0)
+ *             (an empty sequence's h0); refused where it overlaps h0, which
+ *             other blocks may still read
  *   states  : device fp32 [tbe_gated_scan_states(tokens), channels] or NULL:
  *             what the backward needs of the forward
  * Errors: TBE_ERR_INVALID_ARG, TBE_ERR_UNSUPPORTED (limits, alignment),
@@ -431,7 +433,8 @@ int tbe_gated_scan(const tbe_scan_inputs* in, void* h, int64_t h_stride, float* 
 /* Gradients of sum(dh * h) + sum(dh_last * h_last).
  *   in       : as given to the forward
  *   dh       : device [tokens, channels] of dtype, dh_stride apart
- *   dh_last  : device fp32 [sequences, channels] or NULL (zero)
+ *   dh_last  : device fp32 [sequences, channels] or NULL (zero); dh and
+ *              dh_last overlap no output (dh_last and dh0 are refused)
  *   states   : as the forward wrote them
  *   out      : dx, drecur, dgate (device, dtype, own strides), ddecay
  *              (device fp32 [channels]) and dh0 (device fp32 [sequences,

@@ -1306,6 +1306,14 @@ int dispatch(ScanArgs& a, int32_t dtype, int what, cudaStream_t s) {
 
 bool aligned_for(const void* p, int32_t dtype) { return ((uintptr_t)p & (dtype == TBE_F32 ? 3 : 1)) == 0; }
 
+// Whether two [sequences, channels] states share memory: what a block writes
+// of one would race with what another block reads of the other.
+bool overlap(const tbe_scan_inputs* in, const float* p, const float* q) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  const size_t bytes = sizeof(float) * (size_t)in->sequences * (size_t)in->channels;
+  return p && q && a < b + bytes && b < a + bytes;
+}
+
 // Checks shared by the entry points.
 int check(const tbe_scan_inputs* in) {
   if (!in) return TBE_ERR_INVALID_ARG;
@@ -1386,6 +1394,7 @@ int tbe_gated_scan(const tbe_scan_inputs* in, void* h, int64_t h_stride, float* 
   if (st != TBE_OK) return st;
   if (in->sequences == 0) return TBE_OK;
   if ((in->tokens > 0 && !h) || !h_last || h_stride < in->channels) return TBE_ERR_INVALID_ARG;
+  if (overlap(in, in->h0, h_last)) return TBE_ERR_INVALID_ARG;
   if (!aligned_for(h, in->dtype)) return TBE_ERR_UNSUPPORTED;
   ScanArgs a = args_of(in);
   a.h = h;
@@ -1415,6 +1424,7 @@ int tbe_gated_scan_backward(const tbe_scan_inputs* in, const void* dh, int64_t d
       out->dgate_stride < in->channels)
     return TBE_ERR_INVALID_ARG;
   if (in->tokens > 0 && (!dh || !out->dx || !out->drecur || !out->dgate)) return TBE_ERR_INVALID_ARG;
+  if (overlap(in, dh_last, out->dh0)) return TBE_ERR_INVALID_ARG;
   if (!aligned_for(dh, in->dtype) || !aligned_for(out->dx, in->dtype) || !aligned_for(out->drecur, in->dtype) ||
       !aligned_for(out->dgate, in->dtype))
     return TBE_ERR_UNSUPPORTED;

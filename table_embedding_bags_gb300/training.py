@@ -118,7 +118,8 @@ def tbe_gated_scan(x, recur, gate, decay, offsets, h0=None, sharpness: float = 8
     ``x``, ``recur`` and ``gate`` are [tokens, channels] (rows may be
     strided, so slices of one projection do); ``decay`` is fp32 [channels];
     ``offsets`` int64 or int32 [sequences + 1]; ``h0`` fp32 [sequences,
-    channels].  ``want_states`` keeps what ``tbe_gated_scan_backward`` needs."""
+    channels].  ``want_states`` keeps what ``tbe_gated_scan_backward`` needs.
+    ``out`` must not overlap an input."""
     m = _compiled or _marshal()
     return GatedScan(*m.gated_scan(x, recur, gate, decay, offsets, h0, sharpness, want_states, out, dev_status,
                                    None if stream is None else stream.cuda_stream))
@@ -129,7 +130,8 @@ def tbe_gated_scan_backward(dh, x, recur, gate, decay, offsets, states, h0=None,
     """Gradients of sum(dh * h) + sum(dh_last * h_last), from the inputs of a
     ``tbe_gated_scan`` call and the ``states`` it kept.  ``out``: the three
     [tokens, channels] tensors to write dx, drecur and dgate to (rows may be
-    strided).  dh0 is returned where ``h0`` was given."""
+    strided; not overlapping an input).  dh0 is returned where ``h0`` was
+    given."""
     m = _compiled or _marshal()
     return GatedScanGrads(*m.gated_scan_backward(dh, x, recur, gate, decay, offsets, states, h0, dh_last, sharpness, out,
                                                  dev_status, None if stream is None else stream.cuda_stream))

@@ -154,3 +154,41 @@ def test_argument_checks_before_the_abi():
     with pytest.raises(tbe.TBEError, match="required"):
         tbe._need(None, (torch.int64,), 4, "indices")
     tbe._need(None, (torch.float32,), 4, "per_sample_weights", optional=True)
+
+
+class _ScanInputs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("sequences", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("offsets_i32", ctypes.c_int32), ("x", ctypes.c_void_p),
+                ("recur", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("recur_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64), ("decay", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("h0", ctypes.c_void_p), ("sharpness", ctypes.c_float)]
+
+
+class _ScanGrads(ctypes.Structure):
+    _fields_ = [("dx", ctypes.c_void_p), ("drecur", ctypes.c_void_p), ("dgate", ctypes.c_void_p),
+                ("dx_stride", ctypes.c_int64), ("drecur_stride", ctypes.c_int64), ("dgate_stride", ctypes.c_int64),
+                ("ddecay", ctypes.c_void_p), ("dh0", ctypes.c_void_p)]
+
+
+def test_states_in_place_are_refused(lib):
+    """A sequence's last state may be written before another block has read its first one: h0 and h_last (dh_last and
+    dh0) must not overlap.  Host memory stands in for the device's; a misaligned h (dh), refused in another way, keeps
+    every call from launching anything."""
+    N, S, C = 64, 2, 8
+    room = (ctypes.c_float * 8192)()
+    base = (ctypes.addressof(room) + 255) // 256 * 256
+    x, decay, offsets, states, h0, far = (base + 4096 * i for i in range(6))
+    size = 4 * S * C
+    a = _ScanInputs(N, S, C, tbe.TBE_F32, 0, x, x, x, C, C, C, decay, offsets, h0, 8.0)
+    b = _ScanInputs(N, S, C, tbe.TBE_F32, 0, x, x, x, C, C, C, decay, offsets, None, 8.0)
+    for where, rc in ((h0, tbe.TBE_ERR_INVALID_ARG), (h0 + size - 4, tbe.TBE_ERR_INVALID_ARG),
+                      (h0 - size + 4, tbe.TBE_ERR_INVALID_ARG), (h0 + size, tbe.TBE_ERR_UNSUPPORTED),
+                      (h0 - size, tbe.TBE_ERR_UNSUPPORTED), (far, tbe.TBE_ERR_UNSUPPORTED)):
+        assert lib.tbe_gated_scan(ctypes.byref(a), x + 1, C, where, states, None, 0, None, None) == rc
+        g = _ScanGrads(x, x, x, C, C, C, decay, where)
+        assert lib.tbe_gated_scan_backward(ctypes.byref(b), x + 1, C, h0, states, ctypes.byref(g), None, 0, None,
+                                           None) == rc
+    assert lib.tbe_gated_scan(ctypes.byref(b), x + 1, C, h0, states, None, 0, None, None) == tbe.TBE_ERR_UNSUPPORTED
+    g = _ScanGrads(x, x, x, C, C, C, decay, None)
+    assert lib.tbe_gated_scan_backward(ctypes.byref(b), x + 1, C, h0, states, ctypes.byref(g), None, 0, None,
+                                       None) == tbe.TBE_ERR_UNSUPPORTED
