@@ -153,8 +153,8 @@ class PreferenceLoss:
     """Results of ``tbe_preference_loss``, views of one fp32 buffer: ``loss``
     (scalar), ``seq_logps`` [2 * pairs], ``margins`` [pairs], ``lse`` (with
     ``lse_low``, what its rounding left) and ``coef`` [tokens] (for
-    ``tbe_preference_loss_backward``); and ``dlogits`` (laid out like the
-    logits) or None."""
+    ``tbe_preference_loss_backward``); and ``dlogits`` (with the logits' row
+    stride, unless those are a narrow view of a wide tensor) or None."""
 
     __slots__ = ("_room", "_pairs", "_tokens", "dlogits")
 

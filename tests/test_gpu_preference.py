@@ -328,3 +328,18 @@ def test_logits_far_from_zero(tbe, N, V, kind, shift):
     check(r.dlogits, (g, eg / 2), kind, "dlogits")
     only = tbe.tbe_preference_loss(**d)
     assert torch.equal(tbe.tbe_preference_loss_backward(**d, saved=only), r.dlogits)
+
+
+def test_gradient_of_a_narrow_view_of_a_wide_tensor(tbe):
+    """The gradient's memory goes by the view, not by the tensor it was cut from."""
+    wide = torch.randn(64, 1_000_000, device="cuda")
+    d = make(2, 64, 100, "f32", 16)
+    d["logits"] = wide[:, 5:105]
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    r = tbe.tbe_preference_loss(**d, want_grad=True)
+    alone = tbe.tbe_preference_loss_backward(**d, saved=r)
+    assert torch.cuda.max_memory_allocated() - before < 1 << 20
+    check(r.dlogits, reference(d, 0.1, 0.0)["dlogits"], "f32", "dlogits")
+    assert torch.equal(alone, r.dlogits)
