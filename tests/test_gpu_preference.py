@@ -343,3 +343,29 @@ def test_gradient_of_a_narrow_view_of_a_wide_tensor(tbe):
     assert torch.cuda.max_memory_allocated() - before < 1 << 20
     check(r.dlogits, reference(d, 0.1, 0.0)["dlogits"], "f32", "dlogits")
     assert torch.equal(alone, r.dlogits)
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("first,width", [(0, 4100), (1, 4100), (3, 4101), (5, 100_000)])
+def test_new_gradients_lie_like_the_logits(tbe, kind, first, width):
+    """Rows of a new gradient start at the same place of a 16-byte piece as the logits' rows, also where those start
+    inside a row of a wider tensor."""
+    d = make(2, 20, 4000, kind, 17)
+    wide = torch.zeros(20, width, device="cuda", dtype=DT[kind])
+    wide[:, first:first + 4000] = d["logits"]
+    d["logits"] = wide[:, first:first + 4000]
+    r, _ = check_all_but_strides(tbe, d, kind)
+    alone = tbe.tbe_preference_loss_backward(**d, saved=tbe.tbe_preference_loss(**d, label_smoothing=0.05))
+    assert torch.equal(alone, r.dlogits)
+    for g in (r.dlogits, alone):
+        for n in range(20):
+            assert (g[n].data_ptr() - d["logits"][n].data_ptr()) % 16 == 0
+
+
+def check_all_but_strides(tbe, d, kind):
+    r = tbe.tbe_preference_loss(**d, label_smoothing=0.05, want_grad=True)
+    ref = reference(d, 0.1, 0.05)
+    for name in ("loss", "seq_logps", "margins"):
+        check(getattr(r, name), ref[name], "f32", name)
+    check(r.dlogits, ref["dlogits"], kind, "dlogits")
+    return r, 0
