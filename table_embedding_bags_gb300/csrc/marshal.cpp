@@ -106,6 +106,12 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
 }
 
+bool truth_of(PyObject* o) {
+  const int t = PyObject_IsTrue(o);
+  if (t < 0) throw Refused{""};
+  return t != 0;
+}
+
 // Where a call's kernels go: the stream of a handle (an integer), or the
 // current one for None.  It is made current while the call allocates, so that
 // new memory is the stream's own: a workspace that goes back at the end of the
@@ -216,7 +222,7 @@ PyObject* scan(PyObject* const* a) {
   at::Tensor h, states, ws;
   const int64_t stride = output(a[8], N, C, s, stream, "out", h);
   at::Tensor h_last = stream.result({S, C}, at::kFloat);
-  if (PyObject_IsTrue(a[7])) states = stream.result({abi.scan_states(N), C}, at::kFloat);
+  if (truth_of(a[7])) states = stream.result({abi.scan_states(N), C}, at::kFloat);
   const size_t bytes = abi.scan_workspace(N, s.in.channels, s.in.dtype, 0);
   if (bytes) ws = stream.workspace(bytes);
   check(abi.scan(&s.in, h.data_ptr(), stride, static_cast<float*>(h_last.data_ptr()),
@@ -334,7 +340,7 @@ PyObject* preference(PyObject* const* a) {
   const double scale = number_of(a[7]);
   const Stream stream(a[10], p.dev);
   int64_t d_stride = 0;
-  if (a[8] != Py_None || PyObject_IsTrue(a[6])) d_stride = gradient_room(p, a[8], stream);
+  if (a[8] != Py_None || truth_of(a[6])) d_stride = gradient_room(p, a[8], stream);
   const int64_t N = p.in.tokens, P = p.in.pairs;
   const int64_t start = (4 * (1 + 3 * P + 2 * N) + 255) / 256 * 256;
   const size_t bytes = abi.preference_workspace(N, p.in.vocab, p.in.pairs, p.in.dtype);

@@ -470,3 +470,15 @@ def test_nan_gate_stays_out_of_what_does_not_depend_on_it(tbe, N, kind):
     other = [c for c in range(C) if c != ch]
     check(b.ddecay[other], tuple(a[other] for a in ref["ddecay"]), "f32", "ddecay")
     check(b.dh0, ref["dh0"], "f32", "dh0")
+
+
+def test_arguments_without_a_truth_value(tbe):
+    """A flag that cannot be told true or false raises what asking it raises."""
+    d = make(10, 2, 4, "f32", 2, lengths=[5, 5])
+    ins = [d[k] for k in ("x", "recur", "gate", "decay", "offsets")]
+    with pytest.raises(ValueError):
+        tbe.tbe_gated_scan(*ins, want_states=np.zeros(2))
+    logits, labels = torch.zeros(4, 5, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda")
+    off = torch.tensor([0, 2, 4], device="cuda")
+    with pytest.raises(ValueError):
+        tbe.tbe_preference_loss(logits, labels, off, torch.zeros(2, device="cuda"), want_grad=np.zeros(2))
