@@ -370,7 +370,8 @@ PyObject* preference_backward(PyObject* const* a) {
   return wrap(p.dlogits);
 }
 
-// Calls F with its arguments, with errors as TBEError.
+// Calls F with its arguments, with refusals as TBEError and memory that runs
+// out as PyTorch's own error.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t COUNT>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != COUNT) {
@@ -385,6 +386,15 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return F(args);
   } catch (const Refused& e) {
     if (!PyErr_Occurred()) PyErr_SetString(error_type, e.what.c_str());
+  } catch (const c10::OutOfMemoryError& e) {
+    if (PyErr_Occurred()) return nullptr;
+    if (PyObject* torch = PyImport_ImportModule("torch")) {
+      if (PyObject* type = PyObject_GetAttrString(torch, "OutOfMemoryError")) {
+        PyErr_SetString(type, e.what_without_backtrace());
+        Py_DECREF(type);
+      }
+      Py_DECREF(torch);
+    }
   } catch (const std::exception& e) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
   }

@@ -482,3 +482,22 @@ def test_arguments_without_a_truth_value(tbe):
     off = torch.tensor([0, 2, 4], device="cuda")
     with pytest.raises(ValueError):
         tbe.tbe_preference_loss(logits, labels, off, torch.zeros(2, device="cuda"), want_grad=np.zeros(2))
+
+
+def test_out_of_memory_is_told_as_such(tbe):
+    """An output that does not fit raises what torch.empty raises, and the next call works."""
+    torch.cuda.empty_cache()
+    d = make(4096, 2, 2048, "f32", 2, h0=False, lengths=[2048, 2048])
+    ins = [d[k] for k in ("x", "recur", "gate", "decay", "offsets")]
+    want = tbe.tbe_gated_scan(*ins).h.clone()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    try:
+        torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (4 << 20)) / total)
+        with pytest.raises(torch.OutOfMemoryError):
+            held = [tbe.tbe_gated_scan(*ins) for _ in range(64)]  # 32 MB each, more than freed memory holds
+        held = None
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert torch.equal(tbe.tbe_gated_scan(*ins).h, want)
