@@ -228,6 +228,7 @@ class AdamWPlan:
             raise _tbe.TBEError("AdamWPlan needs at least one tensor")
         if state_bits not in (8, 32):
             raise _tbe.TBEError(f"state_bits must be 8 or 32 (got {state_bits})")
+        self._need_tensors("parameter", params)
         self.state_bits = state_bits
         self.device = params[0].device
         if self.device.type != "cuda":
@@ -255,11 +256,18 @@ class AdamWPlan:
         self._states = (self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)
         self._state_addr = tuple(None if t is None else t.data_ptr() for t in self._states)
 
+    @staticmethod
+    def _need_tensors(what, tensors):
+        for i, t in enumerate(tensors):
+            if not isinstance(t, torch.Tensor):
+                raise _tbe.TBEError(f"{what} {i} must be a tensor (got {t!r})")
+
     def _bind(self, params, grads, stream):
         n = len(params)
         if len(grads) != n:
             raise _tbe.TBEError(f"{n} parameters but {len(grads)} gradients")
         for what, tensors in (("parameter", params), ("gradient", grads)):
+            self._need_tensors(what, tensors)
             for i, t in enumerate(tensors):
                 if t.device != self.device or t.device.type != "cuda":
                     raise _tbe.TBEError(f"{what} {i} must be a CUDA tensor on {self.device} (got {t.device})")

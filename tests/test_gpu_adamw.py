@@ -472,3 +472,17 @@ def test_small_scales_stand_for_their_values(tbe, misaligned):
         want = beta * scales.astype(np.float64)
         on = want >= 1.001 * np.finfo(F).tiny
         assert np.all(np.abs(got[on] - want[on]) <= 2.0 ** -19 * want[on])
+
+
+def test_a_missing_gradient_is_refused(tbe):
+    """What a parameter that took no part in the loss has for its gradient: None."""
+    p = [torch.ones(10, device="cuda"), torch.ones(4, device="cuda")]
+    with pytest.raises(tbe.TBEError, match="gradient 1"):
+        tbe.AdamWPlan(p, [torch.ones(10, device="cuda"), None])
+    with pytest.raises(tbe.TBEError, match="parameter 0"):
+        tbe.AdamWPlan([None, p[1]], p)
+    plan = tbe.AdamWPlan(p, [torch.ones_like(t) for t in p])
+    with pytest.raises(tbe.TBEError, match="gradient 0"):
+        plan.rebind(grads=[None, p[1]])
+    tbe.tbe_adamw_step(plan, **HYPER)  # still bound to what it had
+    assert (p[0] != 1).all()
