@@ -264,6 +264,8 @@ class AdamWPlan:
 
     def _bind(self, params, grads, stream):
         n = len(params)
+        if n != len(self.numel):
+            raise _tbe.TBEError(f"the plan is for {len(self.numel)} tensors (got {n} parameters)")
         if len(grads) != n:
             raise _tbe.TBEError(f"{n} parameters but {len(grads)} gradients")
         for what, tensors in (("parameter", params), ("gradient", grads)):

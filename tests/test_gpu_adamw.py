@@ -486,3 +486,13 @@ def test_a_missing_gradient_is_refused(tbe):
         plan.rebind(grads=[None, p[1]])
     tbe.tbe_adamw_step(plan, **HYPER)  # still bound to what it had
     assert (p[0] != 1).all()
+
+
+def test_rebind_takes_as_many_tensors_as_the_plan_has(tbe):
+    p = [torch.ones(10, device="cuda"), torch.ones(4, device="cuda")]
+    plan = tbe.AdamWPlan(p, [torch.ones_like(t) for t in p])
+    for bad in (p[:1], p + p[:1]):
+        with pytest.raises(tbe.TBEError, match="2 tensors"):
+            plan.rebind(params=bad, grads=[torch.ones_like(t) for t in bad])
+    tbe.tbe_adamw_step(plan, **HYPER)  # still bound to what it had
+    assert all((t != 1).all() for t in p)
