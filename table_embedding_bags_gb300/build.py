@@ -12,6 +12,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -25,6 +26,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtbe.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_STAMP = os.path.join(BUILD, "marshal.stamp")  # what _marshal.so was built against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -66,6 +68,21 @@ def _compile(src: str, verbose: bool, extra) -> str:
     return obj
 
 
+def _marshal_stamp() -> str:
+    import torch
+
+    return f"torch {torch.__version__}, Python {sys.version}, {platform.machine()}"
+
+
+def _marshal_stale() -> bool:
+    """Whether the binding is to be built: from other sources, or against
+    another PyTorch or Python, whose C++ interface may not match."""
+    if _stale(MARSHAL, [MARSHAL_SRC, os.path.join(INCLUDE, "tbe.h")]) or not os.path.exists(MARSHAL_STAMP):
+        return True
+    with open(MARSHAL_STAMP) as f:
+        return f.read() != _marshal_stamp()
+
+
 def _compile_marshal(verbose: bool) -> None:
     import torch
 
@@ -84,12 +101,15 @@ def _compile_marshal(verbose: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, MARSHAL)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(MARSHAL_STAMP, "w") as f:
+        f.write(_marshal_stamp())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile (if stale) and return the path of libtbe.so."""
     deps = _deps()
-    binding = force or _stale(MARSHAL, [MARSHAL_SRC, os.path.join(INCLUDE, "tbe.h")])
+    binding = force or _marshal_stale()
     if not force and not ptxas_info and not _stale(LIB, deps):
         if binding:
             _compile_marshal(verbose)

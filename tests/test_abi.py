@@ -192,3 +192,26 @@ def test_states_in_place_are_refused(lib):
     g = _ScanGrads(x, x, x, C, C, C, decay, None)
     assert lib.tbe_gated_scan_backward(ctypes.byref(b), x + 1, C, h0, states, ctypes.byref(g), None, 0, None,
                                        None) == tbe.TBE_ERR_UNSUPPORTED
+
+
+def test_binding_is_built_again_for_another_pytorch(monkeypatch):
+    """The compiled binding uses PyTorch's C++ interface and Python's: one built against others is not reused."""
+    import sys
+
+    import torch
+
+    from table_embedding_bags_gb300 import build as b
+
+    b.build()
+    built = []
+    monkeypatch.setattr(b, "_compile_marshal", lambda verbose: built.append(1))
+    b.build()
+    assert not built
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    b.build()
+    assert built == [1]
+    monkeypatch.undo()
+    monkeypatch.setattr(b, "_compile_marshal", lambda verbose: built.append(1))
+    monkeypatch.setattr(sys, "version", "2.7")
+    b.build()
+    assert built == [1, 1]
