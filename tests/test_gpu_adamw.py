@@ -496,3 +496,30 @@ def test_rebind_takes_as_many_tensors_as_the_plan_has(tbe):
             plan.rebind(params=bad, grads=[torch.ones_like(t) for t in bad])
     tbe.tbe_adamw_step(plan, **HYPER)  # still bound to what it had
     assert all((t != 1).all() for t in p)
+
+
+@pytest.mark.parametrize("kinds", [(("bf16", "f32"),), (("f32", "bf16"),), (("f16", "f32"),), (("f32", "f16"),),
+                                   (("bf16", "f16"),), (("f16", "bf16"),),
+                                   (("bf16", "f32"), ("f32", "f32"), ("f16", "f16"), ("f32", "bf16"))])
+@pytest.mark.parametrize("misaligned", [False, True])
+def test_8_bit_states_of_other_types(tbe, kinds, misaligned):
+    """Parameters and gradients of unlike types, one pair of types for the list or mixed over it: codes and scales
+    equal the restatement's bit for bit, weights within their bounds."""
+    pk = [kinds[i % len(kinds)][0] for i in range(len(SIZES))]
+    gk = [kinds[i % len(kinds)][1] for i in range(len(SIZES))]
+    p = [tensors([n], k, 0.05, 40 + i, misaligned)[0] for i, (n, k) in enumerate(zip(SIZES, pk))]
+    g = [tensors([n], k, 1e-3, 60 + i, misaligned)[0] for i, (n, k) in enumerate(zip(SIZES, gk))]
+    st = state8(SIZES, 15)
+    plan = plan8(tbe, p, g, st)
+    for step in range(2):
+        h = {**HYPER, "step": 50 + step}
+        before = [f64(t) for t in p]
+        new = step8(flat_padded(g, SIZES), *st, h)[2:]
+        tbe.tbe_adamw_step(plan, **h)
+        for name, got, want in zip(("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"), codes(plan), new):
+            assert np.array_equal(got, want), f"{name}: {np.sum(got != want)} differ in step {step}"
+        dm, dv = dequantise8(*st)
+        for i, s in enumerate(slices(SIZES)):
+            wp, _, _ = want64(before[i], f64(g[i]), dm[s].astype(np.float64), dv[s].astype(np.float64), h)
+            near(f64(p[i]), wp, pk[i], f"weight {i}")
+        st = new

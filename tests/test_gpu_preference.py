@@ -369,3 +369,12 @@ def check_all_but_strides(tbe, d, kind):
         check(getattr(r, name), ref[name], "f32", name)
     check(r.dlogits, ref["dlogits"], kind, "dlogits")
     return r, 0
+
+
+@pytest.mark.parametrize("P,N,V,pad,kind", [(1, 6, 100_000, 0, "f32"), (1, 3, 99_999, 0, "f32"), (3, 40, 100_003, 5, "bf16"),
+                                            (2, 13, 70_001, 0, "f16"), (5, 310, 16_390, 3, "bf16"),
+                                            (4, 60, 20_000, 0, "f32"), (2, 300, 17_000, 1, "f16")])
+def test_few_long_rows(tbe, P, N, V, pad, kind):
+    """Batches above the small path's limit whose rows are cut over blocks of 256 threads, or just not."""
+    _, st = check_all(tbe, make(P, N, V, kind, P + N, pad), kind)
+    assert st == 0
