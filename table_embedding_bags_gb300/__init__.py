@@ -36,8 +36,8 @@ EXPORTED = [
     "tbe_backward_reduce",
     "tbe_gated_scan_states", "tbe_gated_scan_workspace_bytes", "tbe_gated_scan", "tbe_gated_scan_backward",
     "tbe_gated_scan_step", "tbe_preference_workspace_bytes", "tbe_preference_loss", "tbe_preference_loss_backward",
-    "tbe_preference_loss_backward_low", "tbe_adamw_state_blocks", "tbe_adamw_plan_device_bytes", "tbe_adamw_plan_create", "tbe_adamw_plan_destroy",
-    "tbe_adamw_step", "tbe_adamw_state",
+    "tbe_preference_loss_backward_low", "tbe_adamw_state_blocks", "tbe_adamw_plan_device_bytes",
+    "tbe_adamw_plan_create", "tbe_adamw_plan_destroy", "tbe_adamw_step", "tbe_adamw_state",
 ]
 TBE_STATIC_WORKSPACE_BYTES = 32 << 20
 

@@ -37,7 +37,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;
 // A warp takes a row of at most this length where one cluster has the batch
-// (80 rows of 1,000: 8.0 us, with blocks to them 14.5 us).
+// (loss and gradient of 80 rows of 1,000: 8.5 us, with blocks to them 18.0 us).
 constexpr int kWarpRow = 1024;
 
 struct PrefArgs {
@@ -457,7 +457,8 @@ __global__ void __launch_bounds__(kBlockThreads<LANES>) grad_kernel(PrefArgs a) 
 // Small batches in one launch: one cluster of kSmallBlocks thread blocks goes
 // through the three steps, its barrier between them.  A warp takes a short
 // row, a block a long one; long rows are cut over blocks where there are fewer
-// of them than blocks.
+// of them than blocks.  There are no more rows, or pieces of rows, than that
+// (is_small).
 constexpr int kSmallBlocks = 16, kSmallThreads = 512, kSmallWarps = kSmallThreads / 32;
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -470,7 +471,8 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
   const int me = blockIdx.x * kSmallWarps + warp;  // the grid is one cluster
   const bool by_warp = a.V <= kWarpRow;
   if (by_warp) {
-    for (int64_t n = me; n < a.N; n += kSmallBlocks * kSmallWarps) {
+    const int64_t n = me;
+    if (n < a.N) {
       const Run r = warp_merge(sum_row<DT>(elem_ptr<DT>(a.logits, n * a.stride), a.V, lane, 32));
       if (lane == 0) {
         a.lp[n] = finish_row(a, n, r, read_label<DT>(a, n));
@@ -478,7 +480,8 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
       }
     }
   } else {
-    for (int64_t u = blockIdx.x; u < a.N * a.splits; u += kSmallBlocks) {
+    const int64_t u = blockIdx.x;
+    if (u < a.N * a.splits) {
       const int64_t n = u / a.splits, part = u % a.splits;
       const int64_t lo = a.V * part / a.splits, hi = a.V * (part + 1) / a.splits;
       Run r = warp_merge(sum_row<DT>(elem_ptr<DT>(a.logits, n * a.stride + lo), hi - lo, threadIdx.x, kSmallThreads));
@@ -492,7 +495,6 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
           if (part == 0) a.coef[n] = 0.f;
         }
       }
-      __syncthreads();
     }
   }
   cluster_sync();
@@ -511,8 +513,8 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
     if (lane == 0) *a.loss = s / (float)a.P;
   }
   if (!a.dlogits) return;
-  const int64_t units = by_warp ? a.N : a.N * a.splits, step = by_warp ? kSmallBlocks * kSmallWarps : kSmallBlocks;
-  for (int64_t u = by_warp ? me : blockIdx.x; u < units; u += step) {
+  const int64_t u = by_warp ? me : blockIdx.x;
+  if (u < a.N * a.splits) {
     const int64_t n = u / a.splits, part = u % a.splits;
     const int64_t lo = a.V * part / a.splits, hi = a.V * (part + 1) / a.splits;
     grad_row<DT>(elem_ptr<DT>(a.logits, n * a.stride + lo), elem_ptr<DT>(a.dlogits, n * a.dstride + lo), hi - lo,
@@ -522,27 +524,34 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PrefArgs a) {
 }
 
 
-// Batches of at most this many bytes of logits go through one cluster, whose
-// single launch is what they pay for: 80 rows of 1,000 fp32 logits without
-// gradient take 6.6 us of the GPU either way, and calls in a row 13.8 to 16.6
-// us against 17.4 to 17.9 us.  Loss and gradient, GPU: 2 rows of 100,000 fp32
-// logits (0.8 MB) 9.7 us against 11.0 us of the three kernels, 4 rows 12.0
-// against 11.3 us, 6 rows 15.6 against 10.7 us.
+// Batches that one cluster takes in one round, a warp to a short row or a block
+// to a long one, and that are at most this many bytes of logits, go through it:
+// its single launch is what they pay for.  Loss and gradient in a row, the
+// GPU's time and that of calls in a row: 64 rows of 1,000 fp32 logits 8.1 and
+// 10.4 us against 8.1 and 11.4 us of the three kernels; 256 rows of 60 7.1 and
+// 8.5 against 6.7 and 12.2 us; 384 rows of 60 9.9 and 12.5 against 7.2 and 12.3
+// us, 4,096 rows 48 against 9 us.  Rows of 4,000: 16 of them 7.5 and 10.4
+// against 7.2 and 11.7 us, 64 17.1 and 18.6 against 8.6 and 12 us.  Two rows of
+// 100,000 (0.8 MB) 9.7 against 11.0 us, four 12.0 against 11.3, six 15.6 against
+// 10.7 us.
 constexpr int64_t kSmallBytes = 1 << 20;
+bool is_small(int64_t N, int32_t V, int32_t P, int32_t dtype) {
+  return N <= (V <= kWarpRow ? kSmallBlocks * kSmallWarps : kSmallBlocks) && P <= kSmallBlocks * kSmallWarps &&
+         N * (int64_t)V * (dtype == TBE_F32 ? 4 : 2) <= kSmallBytes;
+}
 
 // Blocks per row: where there are at most two rows to an SM, long rows are
 // cut, to four pieces an SM of at least 2048 entries each (512 or 8,192 make no
 // difference).  40 rows of 100,000 bf16 logits: 17.4 us against 21.0 us with a
 // block per row; 160 rows 28.0 against 34.3 us; 400 rows 56.1 against 53.3 us.
 // (One cluster: as many as it has blocks.)
-bool is_small(int64_t N, int32_t V, int32_t dtype) { return N * (int64_t)V * (dtype == TBE_F32 ? 4 : 2) <= kSmallBytes; }
 // Threads to a row in the kernels of larger batches.  Loss and gradient with
 // 32, 128 and 256 threads to a row: 3,000 rows of 2,000 half-precision logits
 // 15.4, 19.6, 28.1 us; of 8,000: 36.2, 31.2, 35.4 us; 1,300 rows of 10,007:
 // 29.0, 25.2, 26.8 us; 3,840 rows of 100,000: 394, 385, 374 us.
 int lanes_of(int32_t V) { return V <= 2048 ? 32 : (V <= 16384 ? 128 : kThreads); }
-int32_t splits_of(int64_t N, int32_t V, int32_t dtype) {
-  if (is_small(N, V, dtype)) {
+int32_t splits_of(int64_t N, int32_t V, int32_t P, int32_t dtype) {
+  if (is_small(N, V, P, dtype)) {
     if (V <= kWarpRow || N < 1) return 1;
     const int64_t want = kSmallBlocks / N, most = V / 2048;
     const int64_t s = want < most ? want : most;
@@ -566,7 +575,7 @@ Workspace layout(int64_t N, int32_t V, int32_t P, int32_t dtype) {
   w.arrived = at;
   at += 256;
   w.part = at;
-  const int32_t s = splits_of(N, V, dtype);
+  const int32_t s = splits_of(N, V, P, dtype);
   if (s > 1) at += round256((size_t)N * s * sizeof(float2));
   w.lp = at;
   at += round256((size_t)N * 4);
@@ -633,7 +642,7 @@ int launch_small(const PrefArgs& a, cudaStream_t s) {
 
 template <int DT>
 int launch_loss(const PrefArgs& a, int32_t dtype, cudaStream_t s) {
-  if (is_small(a.N, a.V, dtype)) {
+  if (is_small(a.N, a.V, a.P, dtype)) {
     const int st = launch_small<DT>(a, s);
     trace_mark(s, "preference_small");
     return st;
@@ -660,7 +669,8 @@ int check(const tbe_preference_inputs* in) {
   if (!std::isfinite(in->beta) || !(in->label_smoothing >= 0.f && in->label_smoothing <= 1.f)) return TBE_ERR_INVALID_ARG;
   if (!in->logits || !in->labels || !in->offsets || !in->ref_logps) return TBE_ERR_INVALID_ARG;
   if (!aligned_for(in->logits, in->dtype)) return TBE_ERR_UNSUPPORTED;
-  if (in->tokens * (int64_t)splits_of(in->tokens, in->vocab, in->dtype) >= (int64_t(1) << 31) || in->pairs >= (1 << 30))
+  if (in->tokens * (int64_t)splits_of(in->tokens, in->vocab, in->pairs, in->dtype) >= (int64_t(1) << 31) ||
+      in->pairs >= (1 << 30))
     return TBE_ERR_UNSUPPORTED;
   return TBE_OK;
 }
@@ -677,7 +687,7 @@ PrefArgs args_of(const tbe_preference_inputs* in) {
   a.P = in->pairs;
   a.beta = in->beta;
   a.smoothing = in->label_smoothing;
-  a.splits = splits_of(in->tokens, in->vocab, in->dtype);
+  a.splits = splits_of(in->tokens, in->vocab, in->pairs, in->dtype);
   return a;
 }
 

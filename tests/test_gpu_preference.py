@@ -378,3 +378,19 @@ def test_few_long_rows(tbe, P, N, V, pad, kind):
     """Batches above the small path's limit whose rows are cut over blocks of 256 threads, or just not."""
     _, st = check_all(tbe, make(P, N, V, kind, P + N, pad), kind)
     assert st == 0
+
+
+@pytest.mark.parametrize("P,N,V,small", [(10, 256, 8, True), (10, 257, 8, False), (4, 256, 1024, True), (3, 16, 4000, True),
+                                         (3, 17, 4000, False), (256, 250, 40, True), (257, 250, 40, False),
+                                         (50, 20_000, 13, False), (5, 128, 2000, False)])
+def test_one_cluster_takes_what_it_does_in_one_round(tbe, P, N, V, small):
+    """Many short rows, or more than a few long ones, go to the kernels that use the whole GPU."""
+    d = make(P, N, V, "f32", 18)
+    tbe.trace_enable(True)
+    try:
+        tbe.tbe_preference_loss(**d, want_grad=True)
+        stages = [name for name, _ in tbe.trace_read()]
+    finally:
+        tbe.trace_enable(False)
+    assert ("preference_small" in stages) == small and ("preference_rows" in stages) != small
+    check_all(tbe, d, "f32")
