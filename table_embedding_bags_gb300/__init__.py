@@ -40,6 +40,7 @@ EXPORTED = [
     "tbe_adamw_plan_create", "tbe_adamw_plan_destroy", "tbe_adamw_step", "tbe_adamw_state",
 ]
 TBE_STATIC_WORKSPACE_BYTES = 32 << 20
+TBE_SCAN_STEP, TBE_ADAMW_BLOCK = 8, 256
 
 
 class TBEError(RuntimeError):
@@ -128,9 +129,33 @@ def load_library(path: str = LIB_PATH):
                                         P]
     lib.tbe_wait_selftest.restype = ctypes.c_int
     lib.tbe_wait_selftest.argtypes = [i32, i32, P, P]
-    training.declare(lib)
+    _declare_training(lib)
     _lib = lib
     return lib
+
+
+def _declare_training(lib):
+    """Result and argument types of the library's training entry points."""
+    P, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    for name, res, args in [
+        ("tbe_gated_scan_states", i64, [i64]),
+        ("tbe_gated_scan_workspace_bytes", sz, [i64, i32, i32, i32]),
+        ("tbe_gated_scan", ctypes.c_int, [P, P, i64, P, P, P, sz, P, P]),
+        ("tbe_gated_scan_backward", ctypes.c_int, [P, P, i64, P, P, P, P, sz, P, P]),
+        ("tbe_gated_scan_step", ctypes.c_int, [P, P, P, i64, P]),
+        ("tbe_preference_workspace_bytes", sz, [i64, i32, i32, i32]),
+        ("tbe_preference_loss", ctypes.c_int, [P, P, P, P, P, P, P, i64, f32, P, sz, P, P]),
+        ("tbe_preference_loss_backward", ctypes.c_int, [P, P, P, f32, P, i64, P]),
+        ("tbe_preference_loss_backward_low", ctypes.c_int, [P, P, P, P, f32, P, i64, P]),
+        ("tbe_adamw_state_blocks", i64, [i32, P]),
+        ("tbe_adamw_plan_device_bytes", sz, [i32, P, i32]),
+        ("tbe_adamw_plan_create", ctypes.c_int, [P, P, sz, P, P]),
+        ("tbe_adamw_plan_destroy", None, [P]),
+        ("tbe_adamw_step", ctypes.c_int, [P, P, P, P, P, P, P, P, P]),
+        ("tbe_adamw_state", ctypes.c_int, [P, P, P, P, P, P, P, P]),
+    ]:
+        getattr(lib, name).restype = res
+        getattr(lib, name).argtypes = args
 
 
 def _check(rc: int, what: str):
@@ -525,7 +550,22 @@ def version() -> str:
     return load_library().tbe_version().decode()
 
 
-from . import training  # noqa: E402  (the training operators beside the tables; uses this module's helpers)
-from .training import (TBE_ADAMW_BLOCK, TBE_SCAN_STEP, AdamWPlan, GatedScan, GatedScanGrads,  # noqa: E402, F401
-                       PreferenceLoss, tbe_adamw_state, tbe_adamw_step, tbe_gated_scan, tbe_gated_scan_backward,
-                       tbe_gated_scan_step, tbe_preference_loss, tbe_preference_loss_backward)
+# The training operators beside the tables, in a module of their own that needs
+# PyTorch from its first line on: imported where one of its names is used.
+_TRAINING = ("AdamWPlan", "GatedScan", "GatedScanGrads", "PreferenceLoss", "tbe_adamw_state", "tbe_adamw_step",
+             "tbe_gated_scan", "tbe_gated_scan_backward", "tbe_gated_scan_step", "tbe_preference_loss",
+             "tbe_preference_loss_backward")
+
+
+def __getattr__(name):
+    if name != "training" and name not in _TRAINING:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+
+    module = importlib.import_module(".training", __name__)
+    globals().update({n: getattr(module, n) for n in _TRAINING})
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_TRAINING, "training"})

@@ -68,6 +68,15 @@ def _compile(src: str, verbose: bool, extra) -> str:
     return obj
 
 
+def _have_torch() -> bool:
+    """Without PyTorch there is nothing to bind to: the library alone is built."""
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
+
+
 def _marshal_stamp() -> str:
     import torch
 
@@ -109,7 +118,7 @@ def _compile_marshal(verbose: bool) -> None:
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile (if stale) and return the path of libtbe.so."""
     deps = _deps()
-    binding = force or _marshal_stale()
+    binding = _have_torch() and (force or _marshal_stale())
     if not force and not ptxas_info and not _stale(LIB, deps):
         if binding:
             _compile_marshal(verbose)

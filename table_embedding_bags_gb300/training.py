@@ -22,8 +22,8 @@ import torch
 
 import table_embedding_bags_gb300 as _tbe
 
-TBE_SCAN_STEP = 8
-TBE_ADAMW_BLOCK = 256
+TBE_SCAN_STEP = _tbe.TBE_SCAN_STEP
+TBE_ADAMW_BLOCK = _tbe.TBE_ADAMW_BLOCK
 
 _DTYPE = {torch.float32: _tbe.TBE_F32, torch.float16: _tbe.TBE_F16, torch.bfloat16: _tbe.TBE_BF16}
 
@@ -36,30 +36,6 @@ class _AdamWTensors(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int32), ("state_bits", ctypes.c_int32), ("numel", ctypes.c_void_p),
                 ("params", ctypes.c_void_p), ("grads", ctypes.c_void_p), ("param_dtype", ctypes.c_void_p),
                 ("grad_dtype", ctypes.c_void_p)]
-
-
-def declare(lib):
-    """Result and argument types of the library's training entry points."""
-    P, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
-    for name, res, args in [
-        ("tbe_gated_scan_states", i64, [i64]),
-        ("tbe_gated_scan_workspace_bytes", sz, [i64, i32, i32, i32]),
-        ("tbe_gated_scan", ctypes.c_int, [P, P, i64, P, P, P, sz, P, P]),
-        ("tbe_gated_scan_backward", ctypes.c_int, [P, P, i64, P, P, P, P, sz, P, P]),
-        ("tbe_gated_scan_step", ctypes.c_int, [P, P, P, i64, P]),
-        ("tbe_preference_workspace_bytes", sz, [i64, i32, i32, i32]),
-        ("tbe_preference_loss", ctypes.c_int, [P, P, P, P, P, P, P, i64, f32, P, sz, P, P]),
-        ("tbe_preference_loss_backward", ctypes.c_int, [P, P, P, f32, P, i64, P]),
-        ("tbe_preference_loss_backward_low", ctypes.c_int, [P, P, P, P, f32, P, i64, P]),
-        ("tbe_adamw_state_blocks", i64, [i32, P]),
-        ("tbe_adamw_plan_device_bytes", sz, [i32, P, i32]),
-        ("tbe_adamw_plan_create", ctypes.c_int, [P, P, sz, P, P]),
-        ("tbe_adamw_plan_destroy", None, [P]),
-        ("tbe_adamw_step", ctypes.c_int, [P, P, P, P, P, P, P, P, P]),
-        ("tbe_adamw_state", ctypes.c_int, [P, P, P, P, P, P, P, P]),
-    ]:
-        getattr(lib, name).restype = res
-        getattr(lib, name).argtypes = args
 
 
 def _vector(t, shape, dtype, device, what):

@@ -215,3 +215,35 @@ def test_binding_is_built_again_for_another_pytorch(monkeypatch):
     monkeypatch.setattr(sys, "version", "2.7")
     b.build()
     assert built == [1, 1]
+
+
+def test_the_package_needs_pytorch_only_where_tensors_are():
+    """Loading the library and its host-only calls work where PyTorch cannot be imported (and do not wait for it)."""
+    import subprocess
+    import sys
+
+    code = """
+import sys
+class Block:
+    def find_spec(self, name, path=None, target=None):
+        if name.split(".")[0] == "torch":
+            raise ImportError("torch")
+sys.meta_path.insert(0, Block())
+import table_embedding_bags_gb300 as tbe
+assert tbe.load_library().tbe_plan_device_bytes(1) == 256 and "sm_103a" in tbe.version()
+assert tbe.TBE_SCAN_STEP == 8 and tbe.TBE_ADAMW_BLOCK == 256
+assert "tbe_gated_scan" in dir(tbe) and not hasattr(tbe, "no_such_name")
+from table_embedding_bags_gb300 import build
+assert build.build() == build.LIB
+try:
+    tbe.tbe_gated_scan
+except ImportError:
+    print("ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(tbe.__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.stdout.strip() == "ok", r.stderr
+    from table_embedding_bags_gb300 import AdamWPlan, tbe_adamw_step, tbe_gated_scan, training
+
+    assert tbe.tbe_gated_scan is tbe_gated_scan is training.tbe_gated_scan
+    assert tbe.AdamWPlan is AdamWPlan and tbe.tbe_adamw_step is tbe_adamw_step
