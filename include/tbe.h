@@ -537,10 +537,11 @@ int tbe_preference_loss_backward_low(const tbe_preference_inputs* in, const floa
  *   state_bits 8  : int8 and uint8 codes of that many elements and one fp32
  *                   scale per block each: m = sign(q) (q / 127)^2 scale,
  *                   v = (q / 255)^4 scale, scale the block's largest
- *                   magnitude, q the code whose root is nearest (at least 1
- *                   for a v above 0).  A block that holds an infinite or NaN
- *                   moment reads back as NaN.  Start from zero codes and
- *                   scales.
+ *                   magnitude (0 where that is below 2^-126, the smallest
+ *                   normal fp32 number), q the code whose root is nearest (at
+ *                   least 1 for a v of 2^-149 of the scale or more).  A block
+ *                   that holds an infinite or NaN moment reads back as NaN.
+ *                   Start from zero codes and scales.
  * The plan packs the tensors' device pointers and sizes into caller-provided
  * device memory (tbe_adamw_plan_device_bytes, 16-byte aligned, kept alive
  * while the plan is in use) as tbe_plan_create does; the tensors must stay

@@ -21,8 +21,9 @@
 // What bounds it: 32-bit states, memory: 200 M half-precision parameters and
 // gradients, 22 bytes each, 632 us (7.0 TB/s).  8-bit states, instructions: 64
 // M elements, 10 bytes each, 136 us (4.3 TB/s, 60 instructions per element at
-// 73 % of issue slots); the states' values written out 94 us (6.1 TB/s).  A
-// list of small tensors, the launch: 4.9 us.
+// 73 % of issue slots; with fp32 parameters and gradients, 16 bytes, 1.4 times
+// that); the states' values written out 94 us (6.2 TB/s).  A list of small
+// tensors, the launch: 4.9 us.
 #include "tbe_internal.cuh"
 #include "tbe_two.cuh"
 
@@ -531,7 +532,9 @@ __device__ __forceinline__ void whole_blocks_8(const StepArgs& a, const TensorMe
 }
 
 // One launch for the whole list.  PDT, GDT: the types of every tensor, or
-// kMixed: looked up at each one.
+// kMixed: looked up at each one.  (8-bit states: the 64 registers that leave
+// room for four blocks on an SM make all but two of the nine typed variants
+// spill 16 or 24 bytes a thread, the mixed one 52.)
 constexpr int kMixed = -1;
 template <int BITS, int PDT, int GDT>
 __global__ void __launch_bounds__(kThreads, BITS == 8 ? 4 : 3) adamw_kernel(StepArgs a) {
