@@ -394,3 +394,40 @@ def test_one_cluster_takes_what_it_does_in_one_round(tbe, P, N, V, small):
         tbe.trace_enable(False)
     assert ("preference_small" in stages) == small and ("preference_rows" in stages) != small
     check_all(tbe, d, "f32")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [200, 9000])
+def test_c_entry_of_the_gradient_from_lse_and_coef_alone(tbe, V, kind):
+    """Without lse_low a row's probabilities carry the rounding of lse: 2^-24 of it (and as much again for the sum it
+    is the log of), on top of the bounds of test_logits_far_from_zero."""
+    import ctypes
+
+    class Inputs(ctypes.Structure):
+        _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64), ("labels", ctypes.c_void_p),
+                    ("offsets", ctypes.c_void_p), ("ref_logps", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                    ("vocab", ctypes.c_int32), ("pairs", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                    ("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float)]
+
+    d = make(3, 30, V, kind, 19)
+    d["logits"] += 100
+    r = tbe.tbe_preference_loss(**d, want_grad=True)
+    x = d["logits"]
+    a = Inputs(x.data_ptr(), x.stride(0), d["labels"].data_ptr(), d["offsets"].data_ptr(), d["ref_logps"].data_ptr(), 30, V,
+               3, {"f32": tbe.TBE_F32, "bf16": tbe.TBE_BF16}[kind], 0.1, 0.0)
+    lib, stream = tbe.load_library(), torch.cuda.current_stream().cuda_stream
+    lse, coef, low = r.lse.clone(), r.coef.clone(), r.lse_low.clone()
+    got, same = torch.full_like(x, 7), torch.full_like(x, 7)
+    assert lib.tbe_preference_loss_backward(ctypes.byref(a), lse.data_ptr(), coef.data_ptr(), 1.0, got.data_ptr(),
+                                            x.stride(0), stream) == tbe.TBE_OK
+    assert lib.tbe_preference_loss_backward_low(ctypes.byref(a), lse.data_ptr(), low.data_ptr(), coef.data_ptr(), 1.0,
+                                                same.data_ptr(), x.stride(0), stream) == tbe.TBE_OK
+    assert torch.equal(same, r.dlogits)
+    z = x.double()
+    gap = (z - torch.logsumexp(z, 1, keepdim=True)).cpu().numpy()
+    y = d["labels"].cpu().numpy()
+    hot = np.zeros_like(gap)
+    hot[np.flatnonzero(y >= 0), y[y >= 0]] = 1
+    c = coef.double().cpu().numpy()[:, None]
+    e = np.abs(c) * (np.exp(gap) * (2.0 ** -16 + 2.0 ** -22 * np.abs(gap) + 2.0 ** -23 * 110) + 2.0 ** -22 * hot)
+    check(got, (c * (hot - np.exp(gap)), e / 2), kind, "dlogits")
