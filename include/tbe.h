@@ -365,7 +365,8 @@ int tbe_backward_reduce(const tbe_plan* plan, const tbe_optimizer* opt, void* we
  * What one training step of a model over jagged histories needs next to the
  * tables' forward, backward and exact update: a recurrence that mixes a
  * history's rows over time (tbe_gated_scan), a loss over scored catalogue
- * rows (tbe_preference_loss) and an optimizer for the dense parameters
+ * rows (tbe_preference_loss) or over a catalogue's table itself
+ * (tbe_catalogue_loss) and an optimizer for the dense parameters
  * (tbe_adamw_step).  The conventions above hold for them too.  dtype codes
  * are TBE_F32 / TBE_F16 / TBE_BF16; arithmetic, states and sums are fp32.
  */
@@ -521,6 +522,68 @@ int tbe_preference_loss_backward(const tbe_preference_inputs* in, const float* l
 int tbe_preference_loss_backward_low(const tbe_preference_inputs* in, const float* lse, const float* lse_low,
                                      const float* coef, float grad_scale, void* dlogits, int64_t dlogits_stride,
                                      void* stream);
+
+/*
+ * Softmax cross entropy of hidden rows over every row of a catalogue's table.
+ * With x[n, v] = logit_scale * sum_d hidden[n, d] weights[v, d]:
+ *   lse_n        = log sum_v exp(x[n, v])
+ *   token_loss_n = lse_n - x[n, labels[n]]
+ *   loss         = mean of token_loss_n over the tokens that take part
+ *   dhidden, dweights = grad_scale * d loss / d hidden, d weights
+ * The logits are not kept.  A token with a negative label takes no part: it
+ * has lse and token_loss 0 and a zero dhidden row, and what stands in its
+ * hidden row is not looked at.  So does one with a label >= vocab
+ * (TBE_DEV_BAD_INDEX is set).  Where no token takes part, loss and gradients
+ * are 0.  A NaN or an infinity in a hidden row that takes part, or in the
+ * table, reaches the loss and the gradients as the formulas say.
+ *   hidden  : device [tokens, width] of dtype, hidden_stride apart
+ *   weights : device [vocab, width] of dtype, weights_stride apart (a table of
+ *             a packed weight buffer is one); read in place where rows start
+ *             on 16 bytes, else copied to the workspace first
+ *   labels  : device int64 [tokens]
+ *   dtype   : TBE_F16 or TBE_BF16 (TBE_F32: TBE_ERR_UNSUPPORTED).  Products
+ *             and sums are fp32; probabilities are rounded to dtype before
+ *             they are multiplied for the gradients.
+ * Limits: 1 <= tokens <= 2^24, vocab <= 2^30, width <= 2^16.
+ */
+typedef struct tbe_catalogue_inputs {
+  const void* hidden;
+  const void* weights;
+  const int64_t* labels;
+  int64_t hidden_stride;
+  int64_t weights_stride;
+  int64_t tokens;
+  int32_t vocab;
+  int32_t width;
+  int32_t dtype;
+  float logit_scale;
+} tbe_catalogue_inputs;
+
+/* Workspace on the current device (device memory, 256-byte aligned, no
+ * initialisation needed) of tbe_catalogue_loss without (grad = 0) or with
+ * gradients, or of tbe_catalogue_loss_backward (grad = 1); 0 for inputs that
+ * are refused. */
+size_t tbe_catalogue_workspace_bytes(const tbe_catalogue_inputs* in, int32_t grad);
+
+/*   loss            : device fp32 scalar
+ *   token_loss, lse : device fp32 [tokens]
+ *   dhidden         : device [tokens, width] of dtype, dhidden_stride apart
+ *   dweights        : device [vocab, width] of dtype, dweights_stride apart;
+ *                     both gradients are written whole, or both NULL: the
+ *                     loss alone.  They overlap no input and not each other
+ *                     (refused).
+ * Results do not depend on timing.  Errors: TBE_ERR_INVALID_ARG,
+ * TBE_ERR_UNSUPPORTED (limits, types, alignment), TBE_ERR_WORKSPACE,
+ * TBE_ERR_CUDA; TBE_DEV_BAD_INDEX, TBE_DEV_TIMEOUT. */
+int tbe_catalogue_loss(const tbe_catalogue_inputs* in, float* loss, float* token_loss, float* lse, void* dhidden,
+                       int64_t dhidden_stride, void* dweights, int64_t dweights_stride, float grad_scale,
+                       void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* The gradients on their own, from the lse of tbe_catalogue_loss: that call's
+ * up to the rounding of lse (2^-24 |lse| of each probability's size). */
+int tbe_catalogue_loss_backward(const tbe_catalogue_inputs* in, const float* lse, void* dhidden, int64_t dhidden_stride,
+                                void* dweights, int64_t dweights_stride, float grad_scale, void* workspace,
+                                size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /*
  * One AdamW step over a list of tensors in one launch:

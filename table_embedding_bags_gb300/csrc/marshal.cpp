@@ -32,6 +32,9 @@ struct Abi {
   decltype(&tbe_preference_loss) preference;
   decltype(&tbe_preference_loss_backward_low) preference_backward;
   decltype(&tbe_preference_workspace_bytes) preference_workspace;
+  decltype(&tbe_catalogue_loss) catalogue;
+  decltype(&tbe_catalogue_loss_backward) catalogue_backward;
+  decltype(&tbe_catalogue_workspace_bytes) catalogue_workspace;
   decltype(&tbe_status_string) status_string;
 } abi = {};
 const char* const kNames[] = {"tbe_gated_scan",
@@ -42,6 +45,9 @@ const char* const kNames[] = {"tbe_gated_scan",
                               "tbe_preference_loss",
                               "tbe_preference_loss_backward_low",
                               "tbe_preference_workspace_bytes",
+                              "tbe_catalogue_loss",
+                              "tbe_catalogue_loss_backward",
+                              "tbe_catalogue_workspace_bytes",
                               "tbe_status_string"};
 PyObject* error_type = nullptr;
 
@@ -370,6 +376,82 @@ PyObject* preference_backward(PyObject* const* a) {
   return wrap(p.dlogits);
 }
 
+// What the two catalogue calls share.
+struct Catalogue {
+  tbe_catalogue_inputs in;
+  at::ScalarType type;
+  at::Device dev{at::kCPU};
+  at::Tensor dhidden, dweights;
+  int64_t dhidden_stride, dweights_stride;
+};
+Catalogue catalogue_of(PyObject* hidden, PyObject* weights, PyObject* labels, PyObject* logit_scale) {
+  const at::Tensor &h = tensor(hidden, "hidden"), &w = tensor(weights, "weights");
+  Catalogue c = {};
+  c.type = h.scalar_type();
+  c.dev = h.device();
+  c.in.dtype = dtype_code(c.type);
+  if (h.dim() != 2 || (c.in.dtype != TBE_F16 && c.in.dtype != TBE_BF16))
+    refuse("hidden must be a [tokens, width] tensor of float16 or bfloat16 (got ", c.type, ", ", h.sizes(), ")");
+  if (w.dim() != 2) refuse("weights must be a [vocab, width] tensor (got ", w.sizes(), ")");
+  const int64_t N = h.size(0), D = h.size(1), V = w.size(0);
+  if (N < 1 || D < 1 || V < 1 || D > INT32_MAX || V > INT32_MAX)
+    refuse("hidden and weights must have at least one row and one column (and fewer than 2^31)");
+  c.in.hidden_stride = rows_of(h, N, D, c.type, c.dev, "hidden");
+  c.in.weights_stride = rows_of(w, V, D, c.type, c.dev, "weights");
+  c.in.labels = static_cast<const int64_t*>(vector_of(labels, {N}, at::kLong, at::kLong, c.dev, "labels"));
+  c.in.hidden = h.data_ptr();
+  c.in.weights = w.data_ptr();
+  c.in.tokens = N;
+  c.in.vocab = (int32_t)V;
+  c.in.width = (int32_t)D;
+  c.in.logit_scale = (float)number_of(logit_scale);
+  return c;
+}
+void catalogue_grads(Catalogue& c, PyObject* dhidden, PyObject* dweights, const Stream& s) {
+  auto one = [&](PyObject* given, int64_t rows, const char* what, at::Tensor& t) {
+    t = given == Py_None ? s.result({rows, c.in.width}, c.type) : tensor(given, what);
+    return rows_of(t, rows, c.in.width, c.type, c.dev, what);
+  };
+  c.dhidden_stride = one(dhidden, c.in.tokens, "dhidden", c.dhidden);
+  c.dweights_stride = one(dweights, c.in.vocab, "dweights", c.dweights);
+}
+
+// (hidden, weights, labels, logit_scale, want_grad, grad_scale, dhidden, dweights, dev_status, stream)
+// -> (loss, token_loss, lse, dhidden, dweights)
+PyObject* catalogue(PyObject* const* a) {
+  Catalogue c = catalogue_of(a[0], a[1], a[2], a[3]);
+  const double scale = number_of(a[5]);
+  const Stream stream(a[9], c.dev);
+  const bool grad = truth_of(a[4]) || a[6] != Py_None || a[7] != Py_None;
+  if (grad) catalogue_grads(c, a[6], a[7], stream);
+  at::Tensor loss = stream.result({}, at::kFloat), token_loss = stream.result({c.in.tokens}, at::kFloat),
+             lse = stream.result({c.in.tokens}, at::kFloat);
+  const size_t bytes = abi.catalogue_workspace(&c.in, grad);
+  at::Tensor ws = stream.workspace(bytes);
+  check(abi.catalogue(&c.in, static_cast<float*>(loss.data_ptr()), static_cast<float*>(token_loss.data_ptr()),
+                      static_cast<float*>(lse.data_ptr()), grad ? c.dhidden.data_ptr() : nullptr, c.dhidden_stride,
+                      grad ? c.dweights.data_ptr() : nullptr, c.dweights_stride, (float)scale, ws.data_ptr(), bytes,
+                      status_of(a[8], c.dev), stream.handle()),
+        "tbe_catalogue_loss");
+  return tuple(loss, token_loss, lse, c.dhidden, c.dweights);
+}
+
+// (hidden, weights, labels, lse, logit_scale, grad_scale, dhidden, dweights, dev_status, stream) -> (dhidden, dweights)
+PyObject* catalogue_backward(PyObject* const* a) {
+  Catalogue c = catalogue_of(a[0], a[1], a[2], a[4]);
+  const double scale = number_of(a[5]);
+  const Stream stream(a[9], c.dev);
+  if (a[3] == Py_None) refuse("lse is required");
+  const float* lse = floats_of<const float>(a[3], {c.in.tokens}, c.dev, "lse");
+  catalogue_grads(c, a[6], a[7], stream);
+  const size_t bytes = abi.catalogue_workspace(&c.in, 1);
+  at::Tensor ws = stream.workspace(bytes);
+  check(abi.catalogue_backward(&c.in, lse, c.dhidden.data_ptr(), c.dhidden_stride, c.dweights.data_ptr(), c.dweights_stride,
+                               (float)scale, ws.data_ptr(), bytes, status_of(a[8], c.dev), stream.handle()),
+        "tbe_catalogue_loss_backward");
+  return tuple(c.dhidden, c.dweights);
+}
+
 // Calls F with its arguments, with refusals as TBEError and memory that runs
 // out as PyTorch's own error.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t COUNT>
@@ -426,6 +508,8 @@ PyMethodDef methods[] = {{"init", init, METH_VARARGS, nullptr},
                          {"gated_scan_step", FAST(scan_step, 8)},
                          {"preference_loss", FAST(preference, 11)},
                          {"preference_loss_backward", FAST(preference_backward, 10)},
+                         {"catalogue_loss", FAST(catalogue, 10)},
+                         {"catalogue_loss_backward", FAST(catalogue_backward, 10)},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

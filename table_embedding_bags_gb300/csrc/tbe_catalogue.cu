@@ -1,0 +1,1047 @@
+// tbe_catalogue.cu -- softmax cross entropy of hidden rows over every row of
+// a catalogue's table, with both gradients, without keeping the logits.
+//
+//   x[n, v] = logit_scale (hidden_n . weights_v)      lse_n = log sum_v exp(x[n, v])
+//   loss    = mean over taken tokens of lse_n - x[n, y_n]
+//   g[n, v] = exp(x[n, v] - lse_n) - [v = y_n]
+//   dhidden = f g weights      dweights = f g^T hidden      f = grad_scale logit_scale / taken
+//
+// Four products of tokens x vocab x width, all on the tensor cores: the
+// logits twice (for the log-sums, then for g) and one for each gradient.  g
+// goes through memory in 16 bits, a piece of the vocabulary at a time, in two
+// buffers in turn: one launch makes the g of a piece and multiplies the piece
+// before it, so that its long tiles and its short ones fill each other's gaps.
+// The logits themselves never leave the chip.
+//
+// Tokens without a label are left out first: the rows of the others are
+// copied together, in order, so that neither their products nor what stands
+// in their rows takes part.
+//
+// g is rounded to the operands' type before the second products (half a step,
+// 2^-9 of each term for bf16, 2^-12 for fp16, where it is held 2^14 times
+// larger so that probabilities down to 4e-9 are normal numbers).  The label's
+// entry has the 1 taken off before the rounding.  Products are exact and
+// summed in fp32; dhidden is summed over the pieces in fp32.
+#include "tbe_tensor.cuh"
+
+#include <algorithm>
+#include <cmath>
+
+namespace tbe {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// which tokens take part
+// ---------------------------------------------------------------------------
+
+constexpr int kPickThreads = 1024;
+
+struct PickArgs {
+  const int64_t* labels;
+  int64_t N;
+  int64_t Np;      // N in whole tiles
+  int32_t V;
+  int32_t* rows;   // [N] token of each row taken
+  int32_t* label;  // [Np] its label, -1 behind the last
+  float* lse2;     // [Np] set to +inf (nothing) behind the last
+  int32_t* count;
+  uint32_t* zero;  // counters of the launches that follow
+  int32_t zeros;
+  float* token_loss;  // [N] 0 for tokens not taken, or null
+  float* lse;         // [N], or null
+  float* loss;        // 0 where no token is taken, or null
+  const float* given;  // [N] the log-sums of an earlier call (lse2 is made from them), or null
+  int32_t* status;
+};
+
+__device__ __forceinline__ bool taken(int64_t y, int32_t V) { return y >= 0 && y < V; }
+
+// One block: each warp counts a stretch of tokens, then writes its rows behind
+// those of the warps before it.  The order is the tokens', so sums are the
+// same in every run.
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(const PickArgs a) {
+  __shared__ int32_t sum[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t each = (a.N + 1023) / 1024 * 32, begin = min(a.N, each * warp), end = min(a.N, begin + each);
+  int32_t mine = 0;
+  bool bad = false;
+  for (int64_t n = begin; n < end; n += 32) {
+    const int64_t y = n + lane < end ? a.labels[n + lane] : -1;
+    mine += __popc(__ballot_sync(kFull, taken(y, a.V)));
+    bad |= y >= a.V;
+  }
+  if (bad) report(a.status, TBE_DEV_BAD_INDEX);
+  if (lane == 0) sum[warp] = mine;
+  __syncthreads();
+  int32_t at = 0, total = 0;
+  for (int w = 0; w < 32; ++w) {
+    at += w < warp ? sum[w] : 0;
+    total += sum[w];
+  }
+  for (int64_t n = begin; n < end; n += 32) {
+    const int64_t i = n + lane, y = i < end ? a.labels[i] : -1;
+    const bool in = taken(y, a.V);
+    const unsigned m = __ballot_sync(kFull, in);
+    if (in) {
+      const int32_t k = at + __popc(m & ((1u << lane) - 1));
+      a.rows[k] = (int32_t)i;
+      a.label[k] = (int32_t)y;
+      if (a.given) a.lse2[k] = a.given[i] * kLog2e;
+    } else if (i < end && a.lse) {
+      a.lse[i] = 0.f;
+      a.token_loss[i] = 0.f;
+    }
+    at += __popc(m);
+  }
+  for (int64_t k = total + threadIdx.x; k < a.Np; k += kPickThreads) {
+    a.label[k] = -1;
+    a.lse2[k] = INFINITY;
+  }
+  for (int k = threadIdx.x; k < a.zeros; k += kPickThreads) a.zero[k] = 0;
+  if (threadIdx.x == 0) {
+    *a.count = total;
+    if (a.loss && total == 0) *a.loss = 0.f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// rows copied together
+// ---------------------------------------------------------------------------
+
+struct CopyArgs {
+  const uint16_t* src;
+  int64_t src_stride;
+  const int32_t* rows;   // row of each destination row, or null (the same)
+  const int32_t* count;  // rows there are on the device, or null (N)
+  uint16_t* dst;         // [whole tiles, Dp], zero behind the last row and column
+  int64_t N, Np;
+  int32_t D, Dp;
+  int32_t vec;           // elements per load
+  // gradients of tokens that take no part
+  uint16_t* zero;
+  int64_t zero_stride;
+  const int64_t* labels;
+  int32_t V;
+};
+
+__global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
+  wait_predecessor();
+  const int lane = threadIdx.x & 31;
+  const int64_t k = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (k < a.N && a.zero && !taken(a.labels[k], a.V))
+    for (int c = lane; c < a.D; c += 32) a.zero[k * a.zero_stride + c] = 0;
+  const int64_t count = a.count ? *a.count : a.N;
+  if (k >= min(a.Np, (count + 127) / 128 * 128)) return;
+  uint16_t* dst = a.dst + k * a.Dp;
+  const uint16_t* src = k < count ? a.src + (a.rows ? (int64_t)a.rows[k] : k) * a.src_stride : nullptr;
+  if (a.vec == 8) {
+    for (int c = lane * 8; c < a.Dp; c += 256) {
+      const uint4 v = src && c < a.D ? __ldg(reinterpret_cast<const uint4*>(src + c)) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(dst + c) = v;
+    }
+  } else {
+    for (int c = lane * 2; c < a.Dp; c += 64) {
+      const uint32_t lo = src && c < a.D ? __ldg(src + c) : 0, hi = src && c + 1 < a.D ? __ldg(src + c + 1) : 0;
+      *reinterpret_cast<uint32_t*>(dst + c) = lo | hi << 16;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the products
+// ---------------------------------------------------------------------------
+
+// What a tile multiplies and what becomes of it.
+enum Mode : int32_t {
+  kSums,    // logits -> their row's maximum and sum of exponentials over the tile
+  kProbs,   // logits -> g of a piece
+  kTable,   // g^T hidden -> rows of dweights
+  kHidden,  // g weights -> fp32 sums of dhidden
+};
+struct Job {
+  int32_t mode;
+  int32_t v0, v1;   // its part of the vocabulary
+  int32_t buffer;   // of g
+  int32_t splits;   // kHidden: parts of the vocabulary summed apart,
+  int32_t steps;    //   each of so many steps of K
+  int32_t first;    // kHidden: stores instead of adding
+};
+constexpr int kMaxJobs = 3;
+
+constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
+constexpr int kStages = 4;
+constexpr int kStageBytes = (kTileM + kTileN) / 64 * kBlockBytes;
+constexpr int kTiles = 4;  // tiles known ahead
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarps = 8;
+
+struct GemmArgs {
+  CUtensorMap h, w, p;  // hidden [Np, D], weights [V, D], g [2 Np, vc], in boxes of 64 x 64
+  Job job[kMaxJobs];
+  int32_t jobs;
+  int32_t V, D, Dp;
+  int64_t Np;
+  const int32_t* count;
+  uint32_t* next;     // tiles given out
+  float scale2;       // logit_scale in units of log 2
+  const int32_t* label;
+  const float* lse2;
+  float* mine;        // kSums: the label's logit
+  float2* part;       // kSums: [tiles along the vocabulary, Np]
+  uint16_t* g;
+  int32_t vc;
+  uint16_t* dw;
+  int64_t dw_stride;
+  int32_t dw_piece;   // bytes that its rows can be written by
+  float factor;       // grad_scale logit_scale / what g is multiplied by
+  float* acc;         // [splits, Np, Dp]
+  int32_t* status;
+};
+
+struct Shared {
+  uint64_t full[kStages], empty[kStages];   // operands
+  uint64_t done[2], drained[2];             // accumulators
+  uint64_t known[kTiles], forgotten[kTiles];  // tiles
+  uint64_t combine[2];
+  int32_t tile[kTiles];
+  uint32_t tmem;
+  int32_t dead;
+  float2 half[2][kTileM];
+};
+
+// A tile's place.  Every role works it out from its number.
+struct Tile {
+  int32_t job, mode;
+  int32_t rb;            // block of 128 rows of the product
+  int32_t col;           // first column
+  int32_t blocks;        // columns / 64
+  int32_t split, k0, steps;
+};
+
+__device__ __forceinline__ int32_t column_tiles(int32_t D) { return (D + kTileN - 1) / kTileN; }
+__device__ __forceinline__ int32_t tiles_of(const Job& j, int32_t mt, int32_t D) {
+  const int32_t v = j.v1 - j.v0;
+  if (j.mode <= kProbs) return mt * ((v + kTileN - 1) / kTileN);
+  if (j.mode == kTable) return (v + kTileM - 1) / kTileM * column_tiles(D);
+  return j.splits * mt * column_tiles(D);
+}
+__device__ __forceinline__ Tile tile_of(const GemmArgs& g, int32_t t, int32_t count) {
+  const int32_t mt = (count + kTileM - 1) / kTileM;
+  Tile r;
+  r.job = 0;
+  for (; r.job < g.jobs - 1; ++r.job) {
+    const int32_t n = tiles_of(g.job[r.job], mt, g.D);
+    if (t < n) break;
+    t -= n;
+  }
+  const Job& j = g.job[r.job];
+  r.mode = j.mode;
+  r.split = 0;
+  r.k0 = 0;
+  if (r.mode <= kProbs) {
+    // the rows of a column tile first: what a wave of tiles reads of the table is then little
+    r.rb = t % mt;
+    r.col = j.v0 + t / mt * kTileN;
+    r.blocks = kTileN / 64;
+    r.steps = (g.D + kTileK - 1) / kTileK;
+    return r;
+  }
+  const int32_t ct = column_tiles(g.D);
+  r.col = t % ct * kTileN;
+  r.blocks = min(kTileN / 64, (g.D - r.col + 63) / 64);
+  t /= ct;
+  if (r.mode == kTable) {
+    r.rb = t;
+    r.steps = (count + kTileK - 1) / kTileK;
+  } else {
+    r.rb = t % mt;
+    r.split = t / mt;
+    r.k0 = r.split * j.steps;
+    r.steps = max(0, min(j.steps, (j.v1 - j.v0 + kTileK - 1) / kTileK - r.k0));
+  }
+  return r;
+}
+
+// A bounded wait: false (and the others give up too) after four seconds.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int32_t* dead) {
+  uint64_t begin, now;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(begin));
+  for (;;) {
+    if (mbar_wait(bar, parity, 64)) return true;
+    if (*dead) return false;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+    if (now - begin > 4000000000ull) {
+      *dead = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Shared& s) {
+  return mbar_wait(bar, parity, 4) || wait_long(bar, parity, &s.dead);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t* u) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]),
+               "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
+// 32 values as 16-bit elements, the first n of them, by pieces of `piece` bytes.
+template <int DT>
+__device__ __forceinline__ void store_row(uint16_t* p, const float* v, int n, int piece) {
+  uint32_t u[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) u[k] = pack2(v[2 * k], v[2 * k + 1], DT == TBE_BF16);
+  if (n >= 32 && piece == 32) {
+    store32(p, u);
+    store32(p + 16, u + 8);
+    return;
+  }
+  if (n >= 32 && piece == 16) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      reinterpret_cast<uint4*>(p)[k] = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    if (piece >= 4 && 2 * k + 1 < n) {
+      reinterpret_cast<uint32_t*>(p)[k] = u[k];
+    } else {
+      if (2 * k < n) p[2 * k] = (uint16_t)u[k];
+      if (2 * k + 1 < n) p[2 * k + 1] = (uint16_t)(u[k] >> 16);
+    }
+  }
+}
+
+// What g is multiplied by, as a power of two.
+template <int DT>
+constexpr int kUp = DT == TBE_F16 ? 14 : 0;
+
+template <int DT>
+__device__ __forceinline__ void epilogue(const GemmArgs& g, Shared& s, const Tile& t, uint32_t tmem, int32_t count,
+                                         int half, int row, uint32_t turn, bool& ok) {
+  const Job& j = g.job[t.job];
+  const int64_t r = (int64_t)t.rb * kTileM + row;
+  float v[32];
+  if (t.mode == kSums) {
+    float m = -INFINITY, l = 0.f;
+    const int32_t label = g.label[r];
+    for (int c = half * 128; c < half * 128 + 128; c += 32) {
+      tc_ld32(tmem + c, v);
+      tc_wait_ld();
+      const int32_t col = t.col + c;
+      if ((uint32_t)(label - col) < 32u) {
+        float x = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x = k == label - col ? v[k] : x;
+        g.mine[r] = x * g.scale2;
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        v[k] = col + k < g.V ? v[k] * g.scale2 : -INFINITY;
+        top = fmaxf(top, v[k]);
+      }
+      const float to = top == -INFINITY ? 0.f : top;
+      l *= exp2f(m - to);
+      float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 32; ++k) add[k & 3] += exp2f(v[k] - to);
+      l += (add[0] + add[1]) + (add[2] + add[3]);
+      m = top;
+    }
+    // the two halves of the columns meet
+    if (half == 1) {
+      s.half[turn & 1][row] = make_float2(m, l);
+      bar_arrive(&s.combine[turn & 1]);
+    } else {
+      ok = wait(&s.combine[turn & 1], turn >> 1 & 1, s);
+      const float2 o = s.half[turn & 1][row];
+      const float top = fmaxf(m, o.x), to = top == -INFINITY ? 0.f : top;
+      if (r < count) g.part[(int64_t)((t.col - j.v0) / kTileN) * g.Np + r] =
+          make_float2(top, l * exp2f(m - to) + o.y * exp2f(o.x - to));
+    }
+    return;
+  }
+  if (t.mode == kProbs) {
+    const int32_t label = g.label[r];
+    const float less = (float)kUp<DT> - g.lse2[r];
+    uint16_t* dst = g.g + ((int64_t)j.buffer * g.Np + r) * g.vc;
+    for (int c = half * 128; c < half * 128 + 128; c += 32) {
+      tc_ld32(tmem + c, v);
+      tc_wait_ld();
+      const int32_t col = t.col + c;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = exp2f(fmaf(v[k], g.scale2, less));
+      if ((uint32_t)(label - col) < 32u) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (k == label - col) v[k] -= (float)(1 << kUp<DT>);
+      }
+      if (r >= count || col + 32 > g.V) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = r < count && col + k < g.V ? v[k] : 0.f;
+      }
+      store_row<DT>(dst + (col - j.v0), v, 32, 32);
+    }
+    return;
+  }
+  const int end = min(half * 128 + 128, t.blocks * 64);
+  if (t.mode == kTable) {
+    const float f = g.factor / (float)max(count, 1);
+    const int64_t row_v = j.v0 + r;
+    for (int c = half * 128; c < end; c += 32) {
+      tc_ld32(tmem + c, v);
+      tc_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = t.steps > 0 ? v[k] * f : 0.f;
+      const int32_t col = t.col + c;
+      if (row_v < j.v1 && col < g.D) store_row<DT>(g.dw + row_v * g.dw_stride + col, v, g.D - col, g.dw_piece);
+    }
+    return;
+  }
+  if (t.steps == 0 && !j.first) return;
+  float* dst = g.acc + ((int64_t)t.split * g.Np + r) * g.Dp + t.col;
+  for (int c = half * 128; c < end; c += 32) {
+    tc_ld32(tmem + c, v);
+    tc_wait_ld();
+    if (t.steps == 0) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = 0.f;
+    }
+    if (j.first) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 8) store32(dst + c + k, reinterpret_cast<const uint32_t*>(v + k));
+    } else {  // no other tile adds to these: the order of the sums is that of the launches
+#pragma unroll
+      for (int k = 0; k < 32; k += 4)
+        asm volatile("red.global.add.v4.f32 [%0], {%1,%2,%3,%4};" ::"l"(dst + c + k), "f"(v[k]), "f"(v[k + 1]),
+                     "f"(v[k + 2]), "f"(v[k + 3])
+                     : "memory");
+    }
+  }
+}
+
+// Persistent blocks: one thread takes tiles and starts copies, one issues the
+// products, eight warps work on finished accumulators, of which there are two.
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ GemmArgs g) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  __shared__ Shared s;
+  uint8_t* ring = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < kStages; ++k) {
+      bar_init(&s.full[k], 1);
+      bar_init(&s.empty[k], 1);
+    }
+    for (int k = 0; k < 2; ++k) {
+      bar_init(&s.done[k], 1);
+      bar_init(&s.drained[k], kEpilogueWarps);
+      bar_init(&s.combine[k], kTileM);
+    }
+    for (int k = 0; k < kTiles; ++k) {
+      bar_init(&s.known[k], 1);
+      bar_init(&s.forgotten[k], 1 + kEpilogueWarps);
+    }
+    s.dead = 0;
+    bars_visible();
+  }
+  if (warp == 2) tc_alloc(&s.tmem, 512);
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  const uint32_t tmem = s.tmem;
+  wait_predecessor();
+  const int32_t count = *g.count;
+
+  if (warp == 0 && lane == 0) {
+    tma_prefetch(&g.h);
+    tma_prefetch(&g.w);
+    asm volatile("fence.proxy.async;" ::: "memory");  // rows and g were written by ordinary stores
+    int32_t total = 0;
+    for (int k = 0; k < g.jobs; ++k) total += tiles_of(g.job[k], (count + kTileM - 1) / kTileM, g.D);
+    uint32_t step = 0;  // steps of K so far
+    int32_t next = blockIdx.x;
+    for (uint32_t n = 0;; ++n) {
+      const int32_t now = next < total ? next : -1;
+      if (now >= 0) next = (int32_t)(gridDim.x + atomicAdd(g.next, 1u));
+      if (n >= kTiles && !wait(&s.forgotten[n % kTiles], (n / kTiles - 1) & 1, s)) break;
+      s.tile[n % kTiles] = now;
+      bar_arrive(&s.known[n % kTiles]);
+      if (now < 0) break;
+      const Tile t = tile_of(g, now, count);
+      const Job& j = g.job[t.job];
+      const CUtensorMap* a = t.mode <= kProbs ? &g.h : &g.p;
+      const CUtensorMap* b = t.mode == kTable ? &g.h : &g.w;
+      const int32_t a_row = t.mode <= kProbs ? t.rb * kTileM : (int32_t)(j.buffer * g.Np) + (t.mode == kHidden ? t.rb * kTileM : 0);
+      bool ok = true;
+      for (int k = 0; k < t.steps; ++k, ++step) {
+        const uint32_t at = step % kStages;
+        if (step >= kStages && !(ok = wait(&s.empty[at], (step / kStages - 1) & 1, s))) break;
+        bar_expect(&s.full[at], (2 + t.blocks) * kBlockBytes);
+        const uint32_t dst = smem_u32(ring) + at * kStageBytes;
+        const int32_t kk = (t.k0 + k) * kTileK;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (t.mode == kTable) tma_load(dst + i * kBlockBytes, a, t.rb * kTileM + 64 * i, a_row + kk, &s.full[at]);
+          else tma_load(dst + i * kBlockBytes, a, kk, a_row + 64 * i, &s.full[at]);
+        }
+        for (int i = 0; i < t.blocks; ++i) {
+          const uint32_t to = dst + (2 + i) * kBlockBytes;
+          if (t.mode <= kProbs) tma_load(to, b, kk, t.col + 64 * i, &s.full[at]);
+          else tma_load(to, b, t.col + 64 * i, (t.mode == kHidden ? j.v0 : 0) + kk, &s.full[at]);
+        }
+      }
+      if (!ok) break;
+    }
+    if (s.dead)  // copies in flight land before the block ends
+      for (uint32_t k = step > kStages ? step - kStages : 0; k < step; ++k)
+        mbar_wait(&s.full[k % kStages], (k / kStages) & 1, 1 << 16);
+  } else if (warp == 1 && lane == 0) {
+    uint32_t step = 0;
+    for (uint32_t n = 0;; ++n) {
+      if (!wait(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
+      const int32_t now = s.tile[n % kTiles];
+      bar_arrive(&s.forgotten[n % kTiles]);
+      if (now < 0) break;
+      const Tile t = tile_of(g, now, count);
+      if (n >= 2 && !wait(&s.drained[n & 1], (n / 2 - 1) & 1, s)) break;
+      tc_after_sync();
+      const uint32_t along_m = t.mode == kTable, along_n = t.mode >= kTable;
+      const uint32_t idesc = tc_idesc(DT == TBE_BF16, along_m, along_n, kTileM, t.blocks * 64);
+      const uint32_t a_step = (along_m ? 2048 : 32) >> 4, b_step = (along_n ? 2048 : 32) >> 4;
+      bool ok = true;
+      for (int k = 0; k < t.steps; ++k, ++step) {
+        const uint32_t at = step % kStages;
+        if (!(ok = wait(&s.full[at], (step / kStages) & 1, s))) break;
+        tc_after_sync();
+        const uint32_t src = smem_u32(ring) + at * kStageBytes;
+        const uint64_t a = tc_desc(src), b = tc_desc(src + 2 * kBlockBytes);
+#pragma unroll
+        for (int i = 0; i < kTileK / 16; ++i)
+          tc_mma(tmem + (n & 1) * kTileN, a + i * a_step, b + i * b_step, idesc, k > 0 || i > 0);
+        tc_commit(&s.empty[at]);
+      }
+      if (!ok) break;
+      tc_commit(&s.done[n & 1]);
+    }
+  } else if (warp >= 4) {
+    const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    uint32_t turn = 0;  // tiles of kSums so far
+    for (uint32_t n = 0;; ++n) {
+      if (!wait(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
+      const int32_t now = s.tile[n % kTiles];
+      __syncwarp();
+      if (lane == 0) bar_arrive(&s.forgotten[n % kTiles]);
+      if (now < 0) break;
+      const Tile t = tile_of(g, now, count);
+      if (!wait(&s.done[n & 1], (n / 2) & 1, s)) break;
+      tc_after_sync();
+      bool ok = true;
+      epilogue<DT>(g, s, t, tmem + (n & 1) * kTileN + ((uint32_t)(warp & 3) * 32 << 16), count, half, row, turn, ok);
+      turn += t.mode == kSums;
+      if (!__all_sync(kFull, ok)) break;
+      tc_before_sync();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&s.drained[n & 1]);
+    }
+  }
+  __syncwarp();
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  if (threadIdx.x == 0 && s.dead) report(g.status, TBE_DEV_TIMEOUT);
+  if (warp == 2) tc_free(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// the rows' log-sums and losses
+// ---------------------------------------------------------------------------
+
+constexpr int kRowThreads = 1024;
+constexpr int kRows = 8;  // rows of a block, kRowThreads / kRows threads to each
+
+struct RowArgs {
+  const float2* part;
+  int32_t parts;
+  int64_t Np;
+  const int32_t* count;
+  const int32_t* rows;
+  const float* mine;
+  float* lse2;
+  float* token_loss;
+  float* lse;
+  float* loss;
+  float* block_sum;
+  uint32_t* arrived;
+};
+
+__device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
+  const float top = fmaxf(m, m2), to = top == -INFINITY ? 0.f : top;
+  l = l * exp2f(m - to) + l2 * exp2f(m2 - to);
+  m = top;
+}
+
+__global__ void __launch_bounds__(kRowThreads) row_kernel(const RowArgs a) {
+  wait_predecessor();
+  __shared__ float2 part[32][kRows];
+  __shared__ float sum[32];
+  __shared__ bool last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t count = *a.count;
+  const int64_t row = (int64_t)blockIdx.x * kRows + (threadIdx.x & (kRows - 1));
+  if ((int64_t)blockIdx.x * kRows >= count) return;
+  float m = -INFINITY, l = 0.f;
+  if (row < count) {
+#pragma unroll 4
+    for (int k = threadIdx.x / kRows; k < a.parts; k += kRowThreads / kRows) {
+      const float2 p = a.part[k * a.Np + row];
+      join(m, l, p.x, p.y);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o >= kRows; o >>= 1) join(m, l, __shfl_xor_sync(kFull, m, o), __shfl_xor_sync(kFull, l, o));
+  if (lane < kRows) part[warp][lane] = make_float2(m, l);
+  __syncthreads();
+  float mine = 0.f;
+  if (threadIdx.x < kRows && row < count) {
+    for (int w = 1; w < 32; ++w) join(m, l, part[w][threadIdx.x].x, part[w][threadIdx.x].y);
+    // where one logit stands out, its loss is the logarithm of a sum close to 1: kept apart from the maximum
+    const float log_l = log2f(l);
+    const int32_t n = a.rows[row];
+    a.lse2[row] = m + log_l;
+    a.lse[n] = (m + log_l) * kLn2;
+    mine = ((m - a.mine[row]) + log_l) * kLn2;
+    a.token_loss[n] = mine;
+  }
+  if (warp != 0) return;
+  mine = warp_sum(lane < kRows ? mine : 0.f);
+  const uint32_t blocks = (uint32_t)((count + kRows - 1) / kRows);
+  if (lane == 0) {
+    a.block_sum[blockIdx.x] = mine;
+    __threadfence();
+    last = atomicAdd(a.arrived, 1u) == blocks - 1;
+  }
+  __syncwarp();
+  if (!last) return;
+  __threadfence();
+  float all = 0.f;
+  for (uint32_t b = lane; b < blocks; b += 32) all += __ldcg(a.block_sum + b);
+  all = warp_sum(all);
+  if (lane == 0) *a.loss = all / (float)count;
+}
+
+// ---------------------------------------------------------------------------
+// dhidden
+// ---------------------------------------------------------------------------
+
+struct SpreadArgs {
+  const float* acc;
+  int32_t splits;
+  int64_t Np;
+  int32_t D, Dp;
+  const int32_t* count;
+  const int32_t* rows;
+  float factor;
+  uint16_t* out;
+  int64_t stride;
+  int32_t pairs;  // rows can be written by pairs
+};
+
+template <int DT>
+__global__ void __launch_bounds__(256) spread_kernel(const SpreadArgs a) {
+  wait_predecessor();
+  const int lane = threadIdx.x & 31;
+  const int64_t k = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int32_t count = *a.count;
+  if (k >= count) return;
+  const float f = a.factor / (float)count;
+  uint16_t* out = a.out + (int64_t)a.rows[k] * a.stride;
+  for (int c = lane * 2; c < a.D; c += 64) {
+    float2 sum = make_float2(0.f, 0.f);
+    for (int p = 0; p < a.splits; ++p) {
+      const float2 v = __ldg(reinterpret_cast<const float2*>(a.acc + ((int64_t)p * a.Np + k) * a.Dp + c));
+      sum.x += v.x;
+      sum.y += v.y;
+    }
+    const uint32_t u = pack2(sum.x * f, sum.y * f, DT == TBE_BF16);
+    if (a.pairs && c + 1 < a.D) {
+      *reinterpret_cast<uint32_t*>(out + c) = u;
+    } else {
+      out[c] = (uint16_t)u;
+      if (c + 1 < a.D) out[c + 1] = (uint16_t)(u >> 16);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+int64_t whole(int64_t n, int64_t of) { return (n + of - 1) / of * of; }
+
+// Elements of a piece's g.
+constexpr int64_t kPiece = 1 << 25;
+constexpr int64_t kMaxTokens = 1 << 24;
+
+struct Layout {
+  int64_t Np;
+  int32_t Dp, vc, pieces, splits, steps, vt;
+  size_t rows, label, lse2, mine, count, next, block_sum, arrived, hidden, part, weights, g, acc, bytes;
+};
+// Tensor copies want rows that start on 16 bytes; other tables are copied.
+bool copied(const void* p, int64_t stride) { return ((uintptr_t)p & 15) || stride % 8; }
+
+Layout layout(int64_t N, int32_t V, int32_t D, bool grad, bool copy_table) {
+  Layout w;
+  w.Np = whole(N, kTileM);
+  w.Dp = (int32_t)whole(D, 64);
+  w.vt = (V + kTileN - 1) / kTileN;
+  w.vc = (int32_t)std::min<int64_t>(whole(V, kTileN), std::max<int64_t>(kTileN, kPiece / w.Np / kTileN * kTileN));
+  w.pieces = (V + w.vc - 1) / w.vc;
+  // dhidden's tiles: as many as there are SMs, where there are few rows, of at least 8 steps each
+  const int64_t tiles = w.Np / kTileM * ((D + kTileN - 1) / kTileN), steps = (w.vc + kTileK - 1) / kTileK;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>({(sm_count() + tiles - 1) / tiles, steps / 8, 32}));
+  w.steps = (int32_t)((steps + want - 1) / want);
+  w.splits = (int32_t)((steps + w.steps - 1) / w.steps);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round256(bytes);
+    return here;
+  };
+  w.rows = take(4 * (size_t)N);
+  w.label = take(4 * (size_t)w.Np);
+  w.lse2 = take(4 * (size_t)w.Np);
+  w.mine = take(4 * (size_t)w.Np);
+  w.count = take(4);
+  w.next = take(4 * (size_t)(w.pieces + 3));  // of the log-sums, the pieces and what follows the last; arrived
+  w.arrived = w.next + 4 * (size_t)(w.pieces + 2);
+  w.block_sum = take(4 * (size_t)(w.Np / kRows));
+  w.hidden = take(2 * (size_t)w.Np * w.Dp);
+  w.weights = take(copy_table ? 2 * (size_t)V * w.Dp : 0);
+  // the log-sums' parts are through before the first piece
+  const size_t parts = sizeof(float2) * (size_t)w.vt * w.Np;
+  const size_t gs = grad ? 2 * 2 * (size_t)w.Np * w.vc : 0;
+  w.part = w.g = take(std::max(parts, gs));
+  w.acc = take(grad ? 4 * (size_t)w.splits * w.Np * w.Dp : 0);
+  w.bytes = at;
+  return w;
+}
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+Encode encoder() {
+  static const Encode fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<Encode>(p);
+  }();
+  return fn;
+}
+// [rows, cols] of 16-bit elements, `stride` elements from row to row, in
+// boxes of 64 x 64; zeros outside.
+bool map_of(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t stride, int32_t dtype) {
+  const Encode fn = encoder();
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t box[2] = {64, 64}, one[2] = {1, 1};
+  return fn && fn(m, dtype == TBE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                  const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Launches `kernel`; `after`: it may start while the kernel before it ends.
+template <typename A>
+int start(void (*kernel)(A), int64_t grid, int threads, size_t smem, bool after, cudaStream_t s, const A& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? check_launch() : TBE_ERR_CUDA;
+}
+
+constexpr size_t kProductBytes = (size_t)kStages * kStageBytes + 1024;
+
+template <int DT>
+int start_products(const GemmArgs& g, cudaStream_t s) {
+  static bool allowed[64] = {};  // once per device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !allowed[dev]) {
+    if (cudaFuncSetAttribute(product_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kProductBytes) !=
+        cudaSuccess)
+      return TBE_ERR_CUDA;
+    if (dev >= 0 && dev < 64) allowed[dev] = true;
+  }
+  return start(product_kernel<DT>, sm_count(), kThreads, kProductBytes, true, s, g);
+}
+
+struct Call {
+  const tbe_catalogue_inputs* in;
+  float *loss, *token_loss, *lse;  // the forward's outputs, or null
+  const float* given;              // the log-sums of an earlier call, or null
+  void* dhidden;
+  int64_t dhidden_stride;
+  void* dweights;
+  int64_t dweights_stride;
+  float grad_scale;
+  uint8_t* ws;
+  int32_t* status;
+};
+
+template <typename T>
+T* at(uint8_t* p, size_t offset) {
+  return reinterpret_cast<T*>(p + offset);
+}
+int piece_of(const void* p, int64_t stride, int most) {
+  while (most > 2 && (((uintptr_t)p | (uintptr_t)(stride * 2)) & (most - 1))) most >>= 1;
+  return most;
+}
+
+template <int DT>
+int run(const Call& c, cudaStream_t s) {
+  const tbe_catalogue_inputs& in = *c.in;
+  const bool grad = c.dhidden != nullptr, copy = copied(in.weights, in.weights_stride);
+  const int64_t N = in.tokens;
+  const Layout w = layout(N, in.vocab, in.width, grad, copy);
+  uint8_t* ws = c.ws;
+
+  PickArgs p = {};
+  p.labels = in.labels;
+  p.N = N;
+  p.Np = w.Np;
+  p.V = in.vocab;
+  p.rows = at<int32_t>(ws, w.rows);
+  p.label = at<int32_t>(ws, w.label);
+  p.lse2 = at<float>(ws, w.lse2);
+  p.count = at<int32_t>(ws, w.count);
+  p.zero = at<uint32_t>(ws, w.next);
+  p.zeros = w.pieces + 3;
+  p.token_loss = c.token_loss;
+  p.lse = c.lse;
+  p.loss = c.loss;
+  p.given = c.given;
+  p.status = c.status;
+  int st = start(pick_kernel, 1, kPickThreads, 0, false, s, p);
+  if (st != TBE_OK) return st;
+  trace_mark(s, "catalogue_pick");
+
+  CopyArgs k = {};
+  k.src = static_cast<const uint16_t*>(in.hidden);
+  k.src_stride = in.hidden_stride;
+  k.rows = p.rows;
+  k.count = p.count;
+  k.dst = at<uint16_t>(ws, w.hidden);
+  k.N = N;
+  k.Np = w.Np;
+  k.D = in.width;
+  k.Dp = w.Dp;
+  k.vec = in.width % 8 == 0 && !copied(in.hidden, in.hidden_stride) ? 8 : 1;
+  k.zero = static_cast<uint16_t*>(c.dhidden);
+  k.zero_stride = c.dhidden_stride;
+  k.labels = in.labels;
+  k.V = in.vocab;
+  st = start(copy_kernel, w.Np / 8, 256, 0, true, s, k);
+  if (st != TBE_OK) return st;
+  trace_mark(s, "catalogue_rows");
+  const void* table = in.weights;
+  int64_t table_stride = in.weights_stride;
+  if (copy) {
+    CopyArgs t = {};
+    t.src = static_cast<const uint16_t*>(in.weights);
+    t.src_stride = in.weights_stride;
+    t.dst = at<uint16_t>(ws, w.weights);
+    t.N = t.Np = in.vocab;
+    t.D = in.width;
+    t.Dp = w.Dp;
+    t.vec = 1;
+    st = start(copy_kernel, ((int64_t)in.vocab + 7) / 8, 256, 0, true, s, t);
+    if (st != TBE_OK) return st;
+    trace_mark(s, "catalogue_table");
+    table = t.dst;
+    table_stride = w.Dp;
+  }
+
+  GemmArgs g = {};
+  if (!map_of(&g.h, k.dst, w.Np, w.Dp, w.Dp, DT) || !map_of(&g.w, table, in.vocab, in.width, table_stride, DT))
+    return TBE_ERR_CUDA;
+  if (grad && !map_of(&g.p, at<uint16_t>(ws, w.g), 2 * w.Np, w.vc, w.vc, DT)) return TBE_ERR_CUDA;
+  g.V = in.vocab;
+  g.D = in.width;
+  g.Dp = w.Dp;
+  g.Np = w.Np;
+  g.count = p.count;
+  g.scale2 = in.logit_scale * kLog2e;
+  g.label = p.label;
+  g.lse2 = p.lse2;
+  g.mine = at<float>(ws, w.mine);
+  g.part = at<float2>(ws, w.part);
+  g.g = at<uint16_t>(ws, w.g);
+  g.vc = w.vc;
+  g.dw = static_cast<uint16_t*>(c.dweights);
+  g.dw_stride = c.dweights_stride;
+  g.dw_piece = piece_of(c.dweights, c.dweights_stride, 32);
+  g.factor = (float)((double)c.grad_scale * in.logit_scale * std::ldexp(1.0, -kUp<DT>));
+  g.acc = at<float>(ws, w.acc);
+  g.status = c.status;
+  if (c.loss) {
+    g.jobs = 1;
+    g.job[0] = Job{kSums, 0, in.vocab, 0, 0, 0, 0};
+    g.next = p.zero;
+    if ((st = start_products<DT>(g, s)) != TBE_OK) return st;
+    trace_mark(s, "catalogue_sums");
+    RowArgs r = {};
+    r.part = g.part;
+    r.parts = w.vt;
+    r.Np = w.Np;
+    r.count = p.count;
+    r.rows = p.rows;
+    r.mine = g.mine;
+    r.lse2 = p.lse2;
+    r.token_loss = c.token_loss;
+    r.lse = c.lse;
+    r.loss = c.loss;
+    r.block_sum = at<float>(ws, w.block_sum);
+    r.arrived = at<uint32_t>(ws, w.arrived);
+    st = start(row_kernel, w.Np / kRows, kRowThreads, 0, true, s, r);
+    if (st != TBE_OK) return st;
+    trace_mark(s, "catalogue_loss");
+  }
+  if (!grad) return TBE_OK;
+  for (int i = 0; i <= w.pieces; ++i) {
+    g.jobs = 0;
+    if (i > 0) {  // the long tiles first
+      const int32_t v0 = (i - 1) * w.vc, v1 = (int32_t)std::min<int64_t>(in.vocab, (int64_t)v0 + w.vc);
+      g.job[g.jobs++] = Job{kTable, v0, v1, (i - 1) & 1, 0, 0, 0};
+      g.job[g.jobs++] = Job{kHidden, v0, v1, (i - 1) & 1, w.splits, w.steps, i == 1};
+    }
+    if (i < w.pieces) {
+      const int32_t v0 = i * w.vc, v1 = (int32_t)std::min<int64_t>(in.vocab, (int64_t)v0 + w.vc);
+      g.job[g.jobs++] = Job{kProbs, v0, v1, i & 1, 0, 0, 0};
+    }
+    g.next = p.zero + 1 + i;
+    if ((st = start_products<DT>(g, s)) != TBE_OK) return st;
+  }
+  trace_mark(s, "catalogue_gradients");
+  SpreadArgs d = {};
+  d.acc = g.acc;
+  d.splits = w.splits;
+  d.Np = w.Np;
+  d.D = in.width;
+  d.Dp = w.Dp;
+  d.count = p.count;
+  d.rows = p.rows;
+  d.factor = g.factor;
+  d.out = static_cast<uint16_t*>(c.dhidden);
+  d.stride = c.dhidden_stride;
+  d.pairs = piece_of(c.dhidden, c.dhidden_stride, 4) == 4;
+  st = start(spread_kernel<DT>, w.Np / 8, 256, 0, true, s, d);
+  trace_mark(s, "catalogue_dhidden");
+  return st;
+}
+
+int check(const tbe_catalogue_inputs* in) {
+  if (!in || (in->dtype != TBE_F16 && in->dtype != TBE_BF16 && in->dtype != TBE_F32)) return TBE_ERR_INVALID_ARG;
+  if (in->dtype == TBE_F32) return TBE_ERR_UNSUPPORTED;
+  if (in->tokens < 1 || in->vocab < 1 || in->width < 1 || !std::isfinite(in->logit_scale)) return TBE_ERR_INVALID_ARG;
+  if (!in->hidden || !in->weights || !in->labels || in->hidden_stride < in->width || in->weights_stride < in->width)
+    return TBE_ERR_INVALID_ARG;
+  if (in->tokens > kMaxTokens || in->vocab > (1 << 30) || in->width > (1 << 16)) return TBE_ERR_UNSUPPORTED;
+  if (((uintptr_t)in->hidden | (uintptr_t)in->weights) & 1 || ((uintptr_t)in->labels & 7)) return TBE_ERR_UNSUPPORTED;
+  return TBE_OK;
+}
+
+// Whether two [rows, width] tensors of 16-bit elements share memory.
+bool overlap(const void* p, int64_t rows, int64_t stride, const void* q, int64_t rows_q, int64_t stride_q, int32_t width) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  const size_t na = 2 * ((size_t)(rows - 1) * stride + width), nb = 2 * ((size_t)(rows_q - 1) * stride_q + width);
+  return a < b + nb && b < a + na;
+}
+
+int dispatch(const Call& c, void* workspace, size_t bytes, void* stream) {
+  const tbe_catalogue_inputs& in = *c.in;
+  if (!workspace) return TBE_ERR_INVALID_ARG;
+  if ((uintptr_t)workspace & 255) return TBE_ERR_UNSUPPORTED;
+  if ((c.dhidden != nullptr) != (c.dweights != nullptr)) return TBE_ERR_INVALID_ARG;
+  if (c.dhidden) {
+    if (c.dhidden_stride < in.width || c.dweights_stride < in.width || !std::isfinite(c.grad_scale))
+      return TBE_ERR_INVALID_ARG;
+    if (((uintptr_t)c.dhidden | (uintptr_t)c.dweights) & 1) return TBE_ERR_UNSUPPORTED;
+    // inputs are read again after the first results are written
+    const struct { const void* p; int64_t rows, stride; } t[4] = {{in.hidden, in.tokens, in.hidden_stride},
+                                                                  {in.weights, in.vocab, in.weights_stride},
+                                                                  {c.dhidden, in.tokens, c.dhidden_stride},
+                                                                  {c.dweights, in.vocab, c.dweights_stride}};
+    for (int i = 0; i < 4; ++i)
+      for (int j = std::max(i + 1, 2); j < 4; ++j)
+        if (overlap(t[i].p, t[i].rows, t[i].stride, t[j].p, t[j].rows, t[j].stride, in.width)) return TBE_ERR_INVALID_ARG;
+  }
+  const Layout w = layout(in.tokens, in.vocab, in.width, c.dhidden != nullptr, copied(in.weights, in.weights_stride));
+  if (bytes < w.bytes) return TBE_ERR_WORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  trace_begin(s);
+  return in.dtype == TBE_F16 ? run<TBE_F16>(c, s) : run<TBE_BF16>(c, s);
+}
+
+}  // namespace
+}  // namespace tbe
+
+using namespace tbe;
+
+extern "C" {
+
+size_t tbe_catalogue_workspace_bytes(const tbe_catalogue_inputs* in, int32_t grad) {
+  if (check(in) != TBE_OK) return 0;
+  return layout(in->tokens, in->vocab, in->width, grad != 0, copied(in->weights, in->weights_stride)).bytes;
+}
+
+int tbe_catalogue_loss(const tbe_catalogue_inputs* in, float* loss, float* token_loss, float* lse, void* dhidden,
+                       int64_t dhidden_stride, void* dweights, int64_t dweights_stride, float grad_scale,
+                       void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  const int st = check(in);
+  if (st != TBE_OK) return st;
+  if (!loss || !token_loss || !lse) return TBE_ERR_INVALID_ARG;
+  const Call c = {in,       loss, token_loss, lse, nullptr, dhidden, dhidden_stride, dweights, dweights_stride, grad_scale,
+                  static_cast<uint8_t*>(workspace), dev_status};
+  return dispatch(c, workspace, workspace_bytes, stream);
+}
+
+int tbe_catalogue_loss_backward(const tbe_catalogue_inputs* in, const float* lse, void* dhidden, int64_t dhidden_stride,
+                                void* dweights, int64_t dweights_stride, float grad_scale, void* workspace,
+                                size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  const int st = check(in);
+  if (st != TBE_OK) return st;
+  if (!lse || !dhidden || !dweights) return TBE_ERR_INVALID_ARG;
+  const Call c = {in,      nullptr, nullptr, nullptr, lse, dhidden, dhidden_stride, dweights, dweights_stride, grad_scale,
+                  static_cast<uint8_t*>(workspace), dev_status};
+  return dispatch(c, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,13 +1,14 @@
 """Python binding of the training operators beside the tables.
 
 A gated recurrence over jagged sequences, a preference loss over catalogue
-logits and an AdamW step over a list of tensors.  As in the package's
+logits, cross entropy over a catalogue's table and an AdamW step over a list of
+tensors.  As in the package's
 ``__init__``: argument checks and marshalling only, names as in
 ``include/tbe.h``, outputs allocated where none are given, everything
 enqueued on the current stream (or ``stream``, whose own memory then holds
 what the call allocates; the caller orders the streams, and keeps its tensors
 alive, as under ``with torch.cuda.stream(stream)``).  The recurrence's and the
-loss's checks are compiled (``csrc/marshal.cpp``): their smallest calls take
+losses' checks are compiled (``csrc/marshal.cpp``): their smallest calls take
 the GPU a few microseconds.
 """
 
@@ -62,7 +63,8 @@ def _marshal():
         m.init(_tbe.TBEError, {name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "tbe_gated_scan", "tbe_gated_scan_backward", "tbe_gated_scan_step", "tbe_gated_scan_states",
             "tbe_gated_scan_workspace_bytes", "tbe_preference_loss", "tbe_preference_loss_backward_low",
-            "tbe_preference_workspace_bytes", "tbe_status_string")})
+            "tbe_preference_workspace_bytes", "tbe_catalogue_loss", "tbe_catalogue_loss_backward",
+            "tbe_catalogue_workspace_bytes", "tbe_status_string")})
         _compiled = m
     return _compiled
 
@@ -173,6 +175,41 @@ def tbe_preference_loss_backward(logits, labels, offsets, ref_logps, saved: Pref
     m = _compiled or _marshal()
     return m.preference_loss_backward(logits, labels, offsets, ref_logps, saved.lse, saved.lse_low, saved.coef, grad_scale,
                                       dlogits, None if stream is None else stream.cuda_stream)
+
+
+# ---------------------------------------------------------------------------
+# cross entropy over a catalogue
+# ---------------------------------------------------------------------------
+
+class CatalogueLoss(NamedTuple):
+    loss: torch.Tensor  # fp32 scalar
+    token_loss: torch.Tensor  # fp32 [tokens], 0 for tokens that take no part
+    lse: torch.Tensor  # fp32 [tokens], likewise
+    dhidden: torch.Tensor | None  # [tokens, width]
+    dweights: torch.Tensor | None  # [vocab, width]
+
+
+def tbe_catalogue_loss(hidden, weights, labels, logit_scale: float = 1.0, want_grad=False, grad_scale: float = 1.0,
+                       dhidden=None, dweights=None, dev_status=None, stream=None) -> CatalogueLoss:
+    """Softmax cross entropy of ``hidden`` [tokens, width] over every row of
+    ``weights`` [vocab, width] (float16 or bfloat16, rows may be strided),
+    logits = logit_scale * hidden @ weights.T, which are not kept: the mean
+    over the tokens with a label in ``labels`` (int64; a negative one takes no
+    part, whatever its hidden row holds).  ``want_grad`` (or tensors
+    ``dhidden`` and ``dweights`` to write to) adds grad_scale times both
+    gradients."""
+    m = _compiled or _marshal()
+    return CatalogueLoss(*m.catalogue_loss(hidden, weights, labels, logit_scale, want_grad, grad_scale, dhidden, dweights,
+                                           dev_status, None if stream is None else stream.cuda_stream))
+
+
+def tbe_catalogue_loss_backward(hidden, weights, labels, lse, logit_scale: float = 1.0, grad_scale: float = 1.0,
+                                dhidden=None, dweights=None, dev_status=None, stream=None):
+    """(dhidden, dweights) from the ``lse`` of a ``tbe_catalogue_loss`` call
+    on the same arguments."""
+    m = _compiled or _marshal()
+    return m.catalogue_loss_backward(hidden, weights, labels, lse, logit_scale, grad_scale, dhidden, dweights, dev_status,
+                                     None if stream is None else stream.cuda_stream)
 
 
 # ---------------------------------------------------------------------------
