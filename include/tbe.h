@@ -364,7 +364,8 @@ int tbe_backward_reduce(const tbe_plan* plan, const tbe_optimizer* opt, void* we
  * ---------------------------------------------------------------------------
  * What one training step of a model over jagged histories needs next to the
  * tables' forward, backward and exact update: a recurrence that mixes a
- * history's rows over time (tbe_gated_scan), a loss over scored catalogue
+ * history's rows over time (tbe_gated_scan, with a vector for a state, or
+ * tbe_linear_attention, with a matrix for each head), a loss over scored catalogue
  * rows (tbe_preference_loss) or over a catalogue's table itself
  * (tbe_catalogue_loss) and an optimizer for the dense parameters
  * (tbe_adamw_step).  The conventions above hold for them too.  dtype codes
@@ -460,6 +461,101 @@ int tbe_gated_scan_backward(const tbe_scan_inputs* in, const void* dh, int64_t d
  *   state : device fp32 [sequences, channels], moved on in place
  *   h     : device [sequences, channels] of dtype */
 int tbe_gated_scan_step(const tbe_scan_inputs* in, float* state, void* h, int64_t h_stride, void* stream);
+
+/*
+ * Causal linear attention with a decay for each head over jagged sequences.
+ * For every head h and every sequence s, with gamma = exp(-decay[h]):
+ *   S_t = gamma S_{t-1} + k_t v_t^T      (head_dim x head_dim, S_{-1} = s0[s, h] or 0)
+ *   o_t = scale * S_t^T q_t
+ *   q, k, v : device [tokens, heads, head_dim] of dtype, consecutive along
+ *             head_dim, *_stride elements from token to token and
+ *             *_head_stride from head to head (so the three may be slices of
+ *             one projection; heads may also come first); not overlapping any
+ *             output
+ *   decay   : device fp32 [heads], 0 for none; not negative (a negative one
+ *             grows and may overflow).  It has no gradient: a constant.
+ *   offsets : device int64 (or int32 where offsets_i32 != 0) [sequences + 1],
+ *             from 0 to tokens; empty sequences are allowed.  Broken offsets
+ *             set TBE_DEV_BAD_OFFSETS; results are then unspecified, accesses
+ *             in bounds
+ *   s0      : device fp32 [sequences, heads, head_dim (of k), head_dim (of
+ *             v)] or NULL
+ *   dtype   : TBE_F16 or TBE_BF16 (TBE_F32: TBE_ERR_UNSUPPORTED).  Products
+ *             of inputs are exact, sums and states fp32; q k^T (times its
+ *             decay) and the state as it is read are rounded to dtype.
+ * A NaN or an infinity stays in its sequence and head, and may reach back to
+ * the 63 tokens before its own.  Limits: head_dim <= TBE_LINEAR_MAX_HEAD_DIM, heads <= 2^16,
+ * tokens < 2^36.
+ */
+#define TBE_LINEAR_MAX_HEAD_DIM 128
+typedef struct tbe_linear_attention_inputs {
+  int64_t tokens;
+  int32_t sequences;
+  int32_t heads;
+  int32_t head_dim;
+  int32_t dtype;
+  int32_t offsets_i32;
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t q_head_stride;
+  int64_t k_head_stride;
+  int64_t v_head_stride;
+  const float* decay;
+  const void* offsets;
+  const float* s0;
+} tbe_linear_attention_inputs;
+
+/* Workspace (device, 256-byte aligned; no initialisation needed; 0 bytes for
+ * the smallest batches) of tbe_linear_attention (backward = 0) or
+ * tbe_linear_attention_backward (1) on the current device. */
+size_t tbe_linear_attention_workspace_bytes(int64_t tokens, int32_t heads, int32_t head_dim, int32_t backward);
+
+/*   o      : device [tokens, heads, head_dim] of dtype with strides of its own
+ *   s_last : device fp32 [sequences, heads, head_dim, head_dim] or NULL: each
+ *            sequence's last state (an empty sequence's s0, or 0); refused
+ *            where it overlaps s0
+ * Results do not depend on timing.  Errors: TBE_ERR_INVALID_ARG,
+ * TBE_ERR_UNSUPPORTED (limits, types, alignment), TBE_ERR_WORKSPACE,
+ * TBE_ERR_CUDA; TBE_DEV_BAD_OFFSETS. */
+int tbe_linear_attention(const tbe_linear_attention_inputs* in, void* o, int64_t o_stride, int64_t o_head_stride,
+                         float* s_last, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Gradients of sum(dout * o) + sum(ds_last * s_last).
+ *   in      : as given to the forward; nothing else of it is needed
+ *   dout    : device [tokens, heads, head_dim] of dtype, with strides
+ *   ds_last : device fp32 [sequences, heads, head_dim, head_dim] or NULL (zero)
+ *   out     : dq, dk, dv (device, dtype, own strides) and ds0 (device fp32
+ *             [sequences, heads, head_dim, head_dim] or NULL; refused where
+ *             it overlaps s0 or ds_last)
+ * No input overlaps an output. */
+typedef struct tbe_linear_attention_grads {
+  void* dq;
+  void* dk;
+  void* dv;
+  int64_t dq_stride;
+  int64_t dk_stride;
+  int64_t dv_stride;
+  int64_t dq_head_stride;
+  int64_t dk_head_stride;
+  int64_t dv_head_stride;
+  float* ds0;
+} tbe_linear_attention_grads;
+int tbe_linear_attention_backward(const tbe_linear_attention_inputs* in, const void* dout, int64_t do_stride,
+                                  int64_t do_head_stride, const float* ds_last, const tbe_linear_attention_grads* out,
+                                  void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* One token of every sequence: tokens == sequences, token s is sequence s's
+ * next; offsets and s0 are not used (s0 must be NULL).
+ *   state : device fp32 [sequences, heads, head_dim, head_dim], moved on in
+ *           place
+ *   o     : device [sequences, heads, head_dim] of dtype, with strides */
+int tbe_linear_attention_step(const tbe_linear_attention_inputs* in, float* state, void* o, int64_t o_stride,
+                              int64_t o_head_stride, void* stream);
 
 /*
  * Preference loss over pairs of label sequences.  Sequences are the bags of

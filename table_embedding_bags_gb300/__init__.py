@@ -39,9 +39,11 @@ EXPORTED = [
     "tbe_preference_loss_backward_low", "tbe_adamw_state_blocks", "tbe_adamw_plan_device_bytes",
     "tbe_adamw_plan_create", "tbe_adamw_plan_destroy", "tbe_adamw_step", "tbe_adamw_state",
     "tbe_catalogue_workspace_bytes", "tbe_catalogue_loss", "tbe_catalogue_loss_backward",
+    "tbe_linear_attention_workspace_bytes", "tbe_linear_attention", "tbe_linear_attention_backward",
+    "tbe_linear_attention_step",
 ]
 TBE_STATIC_WORKSPACE_BYTES = 32 << 20
-TBE_SCAN_STEP, TBE_ADAMW_BLOCK = 8, 256
+TBE_SCAN_STEP, TBE_ADAMW_BLOCK, TBE_LINEAR_MAX_HEAD_DIM = 8, 256, 128
 
 
 class TBEError(RuntimeError):
@@ -154,6 +156,10 @@ def _declare_training(lib):
         ("tbe_adamw_plan_destroy", None, [P]),
         ("tbe_adamw_step", ctypes.c_int, [P, P, P, P, P, P, P, P, P]),
         ("tbe_adamw_state", ctypes.c_int, [P, P, P, P, P, P, P, P]),
+        ("tbe_linear_attention_workspace_bytes", sz, [i64, i32, i32, i32]),
+        ("tbe_linear_attention", ctypes.c_int, [P, P, i64, i64, P, P, sz, P, P]),
+        ("tbe_linear_attention_backward", ctypes.c_int, [P, P, i64, i64, P, P, P, sz, P, P]),
+        ("tbe_linear_attention_step", ctypes.c_int, [P, P, P, i64, i64, P]),
         ("tbe_catalogue_workspace_bytes", sz, [P, i32]),
         ("tbe_catalogue_loss", ctypes.c_int, [P, P, P, P, P, i64, P, i64, f32, P, sz, P, P]),
         ("tbe_catalogue_loss_backward", ctypes.c_int, [P, P, P, i64, P, i64, f32, P, sz, P, P]),
@@ -556,9 +562,11 @@ def version() -> str:
 
 # The training operators beside the tables, in a module of their own that needs
 # PyTorch from its first line on: imported where one of its names is used.
-_TRAINING = ("AdamWPlan", "CatalogueLoss", "GatedScan", "GatedScanGrads", "PreferenceLoss", "tbe_adamw_state",
-             "tbe_adamw_step", "tbe_catalogue_loss", "tbe_catalogue_loss_backward", "tbe_gated_scan",
-             "tbe_gated_scan_backward", "tbe_gated_scan_step", "tbe_preference_loss", "tbe_preference_loss_backward")
+_TRAINING = ("AdamWPlan", "CatalogueLoss", "GatedScan", "GatedScanGrads", "LinearAttention", "LinearAttentionGrads",
+             "PreferenceLoss", "tbe_adamw_state", "tbe_adamw_step", "tbe_catalogue_loss", "tbe_catalogue_loss_backward",
+             "tbe_gated_scan", "tbe_gated_scan_backward", "tbe_gated_scan_step", "tbe_linear_attention",
+             "tbe_linear_attention_backward", "tbe_linear_attention_step", "tbe_preference_loss",
+             "tbe_preference_loss_backward")
 
 
 def __getattr__(name):

@@ -35,6 +35,10 @@ struct Abi {
   decltype(&tbe_catalogue_loss) catalogue;
   decltype(&tbe_catalogue_loss_backward) catalogue_backward;
   decltype(&tbe_catalogue_workspace_bytes) catalogue_workspace;
+  decltype(&tbe_linear_attention) linear;
+  decltype(&tbe_linear_attention_backward) linear_backward;
+  decltype(&tbe_linear_attention_step) linear_step;
+  decltype(&tbe_linear_attention_workspace_bytes) linear_workspace;
   decltype(&tbe_status_string) status_string;
 } abi = {};
 const char* const kNames[] = {"tbe_gated_scan",
@@ -48,6 +52,10 @@ const char* const kNames[] = {"tbe_gated_scan",
                               "tbe_catalogue_loss",
                               "tbe_catalogue_loss_backward",
                               "tbe_catalogue_workspace_bytes",
+                              "tbe_linear_attention",
+                              "tbe_linear_attention_backward",
+                              "tbe_linear_attention_step",
+                              "tbe_linear_attention_workspace_bytes",
                               "tbe_status_string"};
 PyObject* error_type = nullptr;
 
@@ -452,6 +460,130 @@ PyObject* catalogue_backward(PyObject* const* a) {
   return tuple(c.dhidden, c.dweights);
 }
 
+// What the three linear attention calls share.
+struct Linear {
+  tbe_linear_attention_inputs in;
+  at::ScalarType type;
+  at::Device dev{at::kCPU};
+  int64_t S;
+};
+// A [tokens, heads, head_dim] argument; its token and head strides.
+void heads_of(const at::Tensor& t, const Linear& l, const char* what, int64_t& stride, int64_t& head) {
+  const int64_t N = l.in.tokens, H = l.in.heads, d = l.in.head_dim;
+  if (t.device() != l.dev || !l.dev.is_cuda())
+    refuse(what, " must be a CUDA tensor on the device of the other arguments (got ", t.device(), ")");
+  if (t.scalar_type() != l.type) refuse(what, " has dtype ", t.scalar_type(), "; expected ", l.type);
+  if (t.dim() != 3 || t.size(0) != N || t.size(1) != H || t.size(2) != d)
+    refuse(what, " has shape ", t.sizes(), "; expected [", N, ", ", H, ", ", d, "]");
+  head = H > 1 ? t.stride(1) : d;
+  stride = N > 1 ? t.stride(0) : H * head;
+  if ((d > 1 && N > 0 && t.stride(2) != 1) || head < d || stride < d ||
+      (stride < (H - 1) * head + d && head < (N - 1) * stride + d))
+    refuse(what, " must be consecutive along its last dimension, with tokens and heads that do not overlap");
+}
+Linear linear_of(PyObject* q_, PyObject* k_, PyObject* v_, PyObject* decay, PyObject* offsets, PyObject* s0,
+                 PyObject* scale) {
+  const at::Tensor& q = tensor(q_, "q");
+  Linear l = {};
+  l.type = q.scalar_type();
+  l.dev = q.device();
+  l.in.dtype = dtype_code(l.type);
+  if (q.dim() != 3 || (l.in.dtype != TBE_F16 && l.in.dtype != TBE_BF16))
+    refuse("q must be a [tokens, heads, head_dim] tensor of float16 or bfloat16 (got ", l.type, ", ", q.sizes(), ")");
+  if (q.size(1) < 1 || q.size(1) > (1 << 16) || q.size(2) < 1 || q.size(2) > TBE_LINEAR_MAX_HEAD_DIM)
+    refuse("heads must be 1 to 65536 and head_dim 1 to ", TBE_LINEAR_MAX_HEAD_DIM, " (got ", q.size(1), " and ", q.size(2), ")");
+  l.in.tokens = q.size(0);
+  l.in.heads = (int32_t)q.size(1);
+  l.in.head_dim = (int32_t)q.size(2);
+  const at::Tensor &k = tensor(k_, "k"), &v = tensor(v_, "v");
+  heads_of(q, l, "q", l.in.q_stride, l.in.q_head_stride);
+  heads_of(k, l, "k", l.in.k_stride, l.in.k_head_stride);
+  heads_of(v, l, "v", l.in.v_stride, l.in.v_head_stride);
+  l.S = l.in.tokens;
+  if (offsets != nullptr) {
+    const at::Tensor& o = tensor(offsets, "offsets");
+    l.S = o.numel() - 1;
+    if (l.S < 0) refuse("offsets must hold at least one entry");
+    l.in.offsets = vector_of(offsets, {l.S + 1}, at::kLong, at::kInt, l.dev, "offsets");
+    l.in.offsets_i32 = o.scalar_type() == at::kInt;
+  }
+  if (l.S > INT32_MAX) refuse("too many sequences");
+  if (decay == Py_None) refuse("decay is required");
+  l.in.decay = floats_of<const float>(decay, {l.in.heads}, l.dev, "decay");
+  l.in.sequences = (int32_t)l.S;
+  if (s0 != nullptr) l.in.s0 = floats_of<const float>(s0, {l.S, l.in.heads, l.in.head_dim, l.in.head_dim}, l.dev, "s0");
+  l.in.q = q.data_ptr();
+  l.in.k = k.data_ptr();
+  l.in.v = v.data_ptr();
+  l.in.scale = (float)number_of(scale);
+  return l;
+}
+at::Tensor linear_output(PyObject* given, const Linear& l, const Stream& s, const char* what, int64_t& stride, int64_t& head) {
+  at::Tensor t = given == Py_None ? s.result({l.in.tokens, l.in.heads, l.in.head_dim}, l.type) : tensor(given, what);
+  heads_of(t, l, what, stride, head);
+  return t;
+}
+
+// (q, k, v, decay, offsets, s0, scale, want_last, out, dev_status, stream) -> (o, s_last)
+PyObject* linear(PyObject* const* a) {
+  const Linear l = linear_of(a[0], a[1], a[2], a[3], a[4], a[5], a[6]);
+  const Stream stream(a[10], l.dev);
+  int64_t stride, head;
+  at::Tensor o = linear_output(a[8], l, stream, "out", stride, head), last, ws;
+  if (truth_of(a[7])) last = stream.result({l.S, l.in.heads, l.in.head_dim, l.in.head_dim}, at::kFloat);
+  const size_t bytes = abi.linear_workspace(l.in.tokens, l.in.heads, l.in.head_dim, 0);
+  if (bytes) ws = stream.workspace(bytes);
+  check(abi.linear(&l.in, o.data_ptr(), stride, head, last.defined() ? static_cast<float*>(last.data_ptr()) : nullptr,
+                   bytes ? ws.data_ptr() : nullptr, bytes, status_of(a[9], l.dev), stream.handle()),
+        "tbe_linear_attention");
+  return tuple(o, last);
+}
+
+// (do, q, k, v, decay, offsets, s0, ds_last, scale, out, dev_status, stream) -> (dq, dk, dv, ds0)
+PyObject* linear_backward(PyObject* const* a) {
+  const Linear l = linear_of(a[1], a[2], a[3], a[4], a[5], a[6], a[8]);
+  const Stream stream(a[11], l.dev);
+  const at::Tensor& d = tensor(a[0], "do");
+  int64_t stride, head;
+  heads_of(d, l, "do", stride, head);
+  const int64_t shape[4] = {l.S, l.in.heads, l.in.head_dim, l.in.head_dim};
+  const float* ds_last = floats_of<const float>(a[7], shape, l.dev, "ds_last");
+  PyObject* given[3] = {Py_None, Py_None, Py_None};
+  if (a[9] != Py_None) {
+    if (!PyTuple_Check(a[9]) || PyTuple_GET_SIZE(a[9]) != 3) refuse("out must be a tuple of three tensors");
+    for (int i = 0; i < 3; ++i) given[i] = PyTuple_GET_ITEM(a[9], i);
+  }
+  tbe_linear_attention_grads g = {};
+  at::Tensor dq = linear_output(given[0], l, stream, "dq", g.dq_stride, g.dq_head_stride),
+             dk = linear_output(given[1], l, stream, "dk", g.dk_stride, g.dk_head_stride),
+             dv = linear_output(given[2], l, stream, "dv", g.dv_stride, g.dv_head_stride), ds0, ws;
+  g.dq = dq.data_ptr();
+  g.dk = dk.data_ptr();
+  g.dv = dv.data_ptr();
+  if (a[6] != Py_None) {
+    ds0 = stream.result(shape, at::kFloat);
+    g.ds0 = static_cast<float*>(ds0.data_ptr());
+  }
+  const size_t bytes = abi.linear_workspace(l.in.tokens, l.in.heads, l.in.head_dim, 1);
+  if (bytes) ws = stream.workspace(bytes);
+  check(abi.linear_backward(&l.in, d.data_ptr(), stride, head, ds_last, &g, bytes ? ws.data_ptr() : nullptr, bytes,
+                            status_of(a[10], l.dev), stream.handle()),
+        "tbe_linear_attention_backward");
+  return tuple(dq, dk, dv, ds0);
+}
+
+// (q, k, v, decay, state, scale, out, stream) -> o
+PyObject* linear_step(PyObject* const* a) {
+  const Linear l = linear_of(a[0], a[1], a[2], a[3], nullptr, nullptr, a[5]);
+  const Stream stream(a[7], l.dev);
+  if (a[4] == Py_None) refuse("state is required");
+  float* state = floats_of<float>(a[4], {l.S, l.in.heads, l.in.head_dim, l.in.head_dim}, l.dev, "state");
+  int64_t stride, head;
+  at::Tensor o = linear_output(a[6], l, stream, "out", stride, head);
+  check(abi.linear_step(&l.in, state, o.data_ptr(), stride, head, stream.handle()), "tbe_linear_attention_step");
+  return wrap(o);
+}
+
 // Calls F with its arguments, with refusals as TBEError and memory that runs
 // out as PyTorch's own error.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t COUNT>
@@ -509,6 +641,9 @@ PyMethodDef methods[] = {{"init", init, METH_VARARGS, nullptr},
                          {"preference_loss", FAST(preference, 11)},
                          {"preference_loss_backward", FAST(preference_backward, 10)},
                          {"catalogue_loss", FAST(catalogue, 10)},
+                         {"linear_attention", FAST(linear, 11)},
+                         {"linear_attention_backward", FAST(linear_backward, 12)},
+                         {"linear_attention_step", FAST(linear_step, 8)},
                          {"catalogue_loss_backward", FAST(catalogue_backward, 10)},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,13 +1,13 @@
 """Python binding of the training operators beside the tables.
 
-A gated recurrence over jagged sequences, a preference loss over catalogue
+A gated recurrence and linear attention over jagged sequences, a preference loss over catalogue
 logits, cross entropy over a catalogue's table and an AdamW step over a list of
 tensors.  As in the package's
 ``__init__``: argument checks and marshalling only, names as in
 ``include/tbe.h``, outputs allocated where none are given, everything
 enqueued on the current stream (or ``stream``, whose own memory then holds
 what the call allocates; the caller orders the streams, and keeps its tensors
-alive, as under ``with torch.cuda.stream(stream)``).  The recurrence's and the
+alive, as under ``with torch.cuda.stream(stream)``).  The recurrences' and the
 losses' checks are compiled (``csrc/marshal.cpp``): their smallest calls take
 the GPU a few microseconds.
 """
@@ -64,7 +64,8 @@ def _marshal():
             "tbe_gated_scan", "tbe_gated_scan_backward", "tbe_gated_scan_step", "tbe_gated_scan_states",
             "tbe_gated_scan_workspace_bytes", "tbe_preference_loss", "tbe_preference_loss_backward_low",
             "tbe_preference_workspace_bytes", "tbe_catalogue_loss", "tbe_catalogue_loss_backward",
-            "tbe_catalogue_workspace_bytes", "tbe_status_string")})
+            "tbe_catalogue_workspace_bytes", "tbe_linear_attention", "tbe_linear_attention_backward",
+            "tbe_linear_attention_step", "tbe_linear_attention_workspace_bytes", "tbe_status_string")})
         _compiled = m
     return _compiled
 
@@ -121,6 +122,58 @@ def tbe_gated_scan_step(x, recur, gate, decay, state, sharpness: float = 8.0, ou
     m = _compiled or _marshal()
     return m.gated_scan_step(x, recur, gate, decay, state, sharpness, out,
                              None if stream is None else stream.cuda_stream)
+
+
+# ---------------------------------------------------------------------------
+# linear attention
+# ---------------------------------------------------------------------------
+
+class LinearAttention(NamedTuple):
+    o: torch.Tensor  # [tokens, heads, head_dim] in the inputs' dtype
+    s_last: torch.Tensor | None  # fp32 [sequences, heads, head_dim, head_dim]
+
+
+class LinearAttentionGrads(NamedTuple):
+    dq: torch.Tensor
+    dk: torch.Tensor
+    dv: torch.Tensor
+    ds0: torch.Tensor | None  # fp32 [sequences, heads, head_dim, head_dim]
+
+
+def tbe_linear_attention(q, k, v, decay, offsets, s0=None, scale: float = 1.0, want_last=False, out=None,
+                         dev_status=None, stream=None) -> LinearAttention:
+    """Causal linear attention with a decay for each head over the jagged
+    sequences of ``offsets``: o_t = scale S_t^T q_t with S_t = exp(-decay)
+    S_{t-1} + k_t v_t^T.
+
+    ``q``, ``k`` and ``v`` are [tokens, heads, head_dim] in float16 or
+    bfloat16 (tokens and heads may be strided, so slices of one projection
+    do); ``decay`` is fp32 [heads]; ``offsets`` int64 or int32 [sequences +
+    1]; ``s0`` fp32 [sequences, heads, head_dim, head_dim] (keys by values).
+    ``want_last`` returns each sequence's last state.  ``out`` must not overlap
+    an input."""
+    m = _compiled or _marshal()
+    return LinearAttention(*m.linear_attention(q, k, v, decay, offsets, s0, scale, want_last, out, dev_status,
+                                               None if stream is None else stream.cuda_stream))
+
+
+def tbe_linear_attention_backward(do, q, k, v, decay, offsets, s0=None, ds_last=None, scale: float = 1.0, out=None,
+                                  dev_status=None, stream=None) -> LinearAttentionGrads:
+    """Gradients of sum(do * o) + sum(ds_last * s_last) from the inputs of a
+    ``tbe_linear_attention`` call.  ``out``: the three tensors to write dq, dk
+    and dv to (strided as ``q`` may be; not overlapping an input).  ds0 is
+    returned where ``s0`` was given."""
+    m = _compiled or _marshal()
+    return LinearAttentionGrads(*m.linear_attention_backward(do, q, k, v, decay, offsets, s0, ds_last, scale, out,
+                                                             dev_status, None if stream is None else stream.cuda_stream))
+
+
+def tbe_linear_attention_step(q, k, v, decay, state, scale: float = 1.0, out=None, stream=None):
+    """One token of every sequence: ``state`` (fp32 [sequences, heads,
+    head_dim, head_dim]) moves on in place; returns o [sequences, heads,
+    head_dim] in q's dtype."""
+    m = _compiled or _marshal()
+    return m.linear_attention_step(q, k, v, decay, state, scale, out, None if stream is None else stream.cuda_stream)
 
 
 # ---------------------------------------------------------------------------
