@@ -87,9 +87,9 @@ struct Starts {
   bool back;
   __device__ __forceinline__ int64_t at(int64_t i) const { return back ? N - p.ldg(S - i) : p.ldg(i); }
   __device__ __forceinline__ int32_t sequence(int64_t i) const { return (int32_t)(back ? S - 1 - i : i); }
-  // the first i with at(i) >= x
-  __device__ int64_t first(int64_t x) const {
-    int64_t lo = 0, hi = (int64_t)S + 1;
+  // the first i with at(i) >= x, of all or of lo .. hi
+  __device__ int64_t first(int64_t x) const { return first_from(x, 0, (int64_t)S + 1); }
+  __device__ int64_t first_from(int64_t x, int64_t lo, int64_t hi) const {
     while (lo < hi) {
       const int64_t mid = (lo + hi) >> 1;
       if (at(mid) >= x) hi = mid; else lo = mid + 1;
@@ -133,6 +133,18 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c = a b alone.
+template <int DT>
+__device__ __forceinline__ void mma_first(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (DT == TBE_BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void ldsm(uint32_t* r, uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -178,25 +190,40 @@ struct Shared {
   unsigned long long starts;  // places of the tile where a sequence starts
   int32_t sequence[kTile];    // and which
   int32_t closes;             // a sequence ends at the tile's end
+  int64_t next_at;            // the first start behind it
   uint32_t top[3];            // largest magnitudes of the state, in turn
 };
 
-// ROWS x COLS of one head's rows at positions p.. to shared memory, zeros
-// behind the last row and column.
+// The kTile rows of one head from position p on, COLS of their columns, to
+// shared memory; zeros behind the last row (n) and column.
 template <int COLS, int LD>
 __device__ __forceinline__ void load_rows(uint16_t* dst, const uint16_t* src, int64_t stride, int64_t p, int n, int cols,
                                           int64_t N, bool back, int piece) {
+  const int64_t first = back ? N - 1 - p : p, step = back ? -stride : stride;  // row r is first * stride + r * step
+  if (piece == 16) {
+    constexpr int kPerRow = COLS / 8, kRowsAtOnce = kThreads / kPerRow;
+    const int r0 = threadIdx.x / kPerRow, c = threadIdx.x % kPerRow * 8;
+    const uint16_t* from = src + first * stride + r0 * step + c;
+    uint32_t to = smem_u32(dst + r0 * LD + c);
+    const int rows = c < cols ? n - r0 : 0;  // this thread's row k * kRowsAtOnce is there where that is below
+#pragma unroll
+    for (int k = 0; k < kTile / kRowsAtOnce; ++k) {
+      const bool in = k * kRowsAtOnce < rows;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(in ? from : src), "r"(in ? 16 : 0)
+                   : "memory");
+      from += kRowsAtOnce * step;
+      to += kRowsAtOnce * LD * 2;
+    }
+    return;
+  }
   const int each = piece / 2, per_row = COLS / each;
   for (int i = threadIdx.x; i < kTile * per_row; i += kThreads) {
     const int r = i / per_row, c = (i - r * per_row) * each;
     const bool in = r < n && c < cols;
-    const int64_t token = back ? N - 1 - (p + r) : p + r;
-    const uint16_t* from = in ? src + token * stride + c : src;
+    const uint16_t* from = in ? src + first * stride + r * step + c : src;
     uint16_t* to = dst + r * LD + c;
     const uint32_t bytes = in ? piece : 0;
-    if (piece == 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(bytes) : "memory");
-    else if (piece == 8)
+    if (piece == 8)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(bytes) : "memory");
     else if (piece == 4)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(bytes) : "memory");
@@ -280,6 +307,9 @@ struct State {
   }
 
   // S = gamma^(b - a) S + sum over rows a..b-1 of scale gamma^(b - 1 - row + late) k v^T.
+  // EXACT: a state that is a result.  One that is only read, rounded to 16
+  // bits, takes two terms of bf16 (16 bits) and the tensor cores' own sums.
+  template <bool EXACT>
   __device__ __forceinline__ void add(const Shared<DK>& sh, int a, int b, int late, float scale, int lane) {
     const uint32_t keys = smem_u32(sh.k) + ((lane % 8 + lane / 16 * 8) * D::LK + m0 + lane / 8 % 2 * 8) * 2;
     const uint32_t values = smem_u32(sh.v) + ((lane % 8 + lane / 8 % 2 * 8) * D::LV + n0 + lane / 16 * 8) * 2;
@@ -302,22 +332,34 @@ struct State {
       for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
       up = room_for(most);
     }
-    const float by = sh.pow[b - a] * (DT == TBE_F16 ? pow2(up) : 1.f);
+    const float down = DT == TBE_F16 ? pow2(-up) : 1.f;
+    // (not EXACT: the sum itself is moved, and moved back)
+    const float by = sh.pow[b - a] * (DT == TBE_F16 && !EXACT ? pow2(up) : 1.f);
     each(lane, [&](float& x, int, int) { x *= by; });
     const float weigh = scale * (DT == TBE_F16 ? pow2(up) : 1.f);
+    const bool cut = (a | b) & 15;  // some step of 16 has rows of others
     for (int ks = k0; ks < k1; ++ks) {
       // weights of the four tokens whose keys and values this lane holds
       float w[4];
-      uint32_t keep[2];
+      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+      const int t0 = ks * 16 + lane % 4 * 2;
+      if (cut) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = ks * 16 + lane % 4 * 2 + (e & 1) + (e >> 1) * 8;
-        const bool in = t >= a && t < b;
-        w[e] = in ? sh.pow[b - 1 - t + late] * weigh : 0.f;
-        if (e & 1) keep[e >> 1] |= in ? 0xffff0000u : 0u;
-        else keep[e >> 1] = in ? 0xffffu : 0u;
+        for (int h = 0; h < 2; ++h) {
+          const int t = t0 + h * 8;
+          const bool in0 = t >= a && t < b, in1 = t + 1 >= a && t + 1 < b;
+          w[2 * h] = in0 ? sh.pow[b - 1 - t + late] * weigh : 0.f;
+          w[2 * h + 1] = in1 ? sh.pow[b - 2 - t + late] * weigh : 0.f;
+          keep[h] = (in0 ? 0xffffu : 0u) | (in1 ? 0xffff0000u : 0u);
+        }
+      } else {
+        const float* pw = sh.pow + (b - 1 - t0 + late);
+        w[0] = pw[0] * weigh;
+        w[1] = pw[-1] * weigh;
+        w[2] = pw[-8] * weigh;
+        w[3] = pw[-9] * weigh;
       }
-      constexpr int kTerms = DT == TBE_BF16 ? 3 : 2;
+      constexpr int kTerms = DT == TBE_BF16 && EXACT ? 3 : 2;
       uint32_t f[D::MT][kTerms][4];
 #pragma unroll
       for (int m = 0; m < D::MT; ++m) {
@@ -331,10 +373,18 @@ struct State {
           x.y *= w[(e >> 1 << 1) + 1];
 #pragma unroll
           for (int t = 0; t < kTerms; ++t) {
-            f[m][t][e] = pack2<DT>(x.x, x.y);
-            const float2 y = unpack2<DT>(f[m][t][e]);
-            x.x -= y.x;
-            x.y -= y.y;
+            if (DT == TBE_BF16 && t < kTerms - 1) {  // cut off: its two halves are the numbers' upper ones
+              f[m][t][e] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+              x.x -= __uint_as_float(__float_as_uint(x.x) & 0xffff0000u);
+              x.y -= __uint_as_float(__float_as_uint(x.y) & 0xffff0000u);
+            } else {
+              f[m][t][e] = pack2<DT>(x.x, x.y);
+              if (t < kTerms - 1) {
+                const float2 y = unpack2<DT>(f[m][t][e]);
+                x.x -= y.x;
+                x.y -= y.y;
+              }
+            }
           }
         }
       }
@@ -342,21 +392,30 @@ struct State {
       for (int n = 0; n < D::NT; n += 2) {
         uint32_t r[4];
         ldsm_t(r, values + (ks * 16 * D::LV + n * 8) * 2);
+        if (cut) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] &= keep[e & 1];
+          for (int e = 0; e < 4; ++e) r[e] &= keep[e & 1];
+        }
 #pragma unroll
         for (int m = 0; m < D::MT; ++m)
 #pragma unroll
-          for (int t = kTerms - 1; t >= 0; --t) {
-            mma<DT>(s[m][n], f[m][t], r[0], r[1]);
-            mma<DT>(s[m][n + 1], f[m][t], r[2], r[3]);
+          for (int u = 0; u < 2; ++u) {
+            if (EXACT) {
+              // added up apart: the tensor cores cut sums off, which a long sum would feel
+              float c[4];
+              mma_first<DT>(c, f[m][kTerms - 1], r[2 * u], r[2 * u + 1]);
+#pragma unroll
+              for (int t = kTerms - 2; t >= 0; --t) mma<DT>(c, f[m][t], r[2 * u], r[2 * u + 1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[m][n + u][e] = DT == TBE_F16 ? fmaf(c[e], down, s[m][n + u][e]) : s[m][n + u][e] + c[e];
+            } else {
+#pragma unroll
+              for (int t = kTerms - 1; t >= 0; --t) mma<DT>(s[m][n + u], f[m][t], r[2 * u], r[2 * u + 1]);
+            }
           }
       }
     }
-    if (DT == TBE_F16) {
-      const float down = pow2(-up);
-      each(lane, [&](float& x, int, int) { x *= down; });
-    }
+    if (DT == TBE_F16 && !EXACT) each(lane, [&](float& x, int, int) { x *= down; });
   }
 };
 
@@ -364,36 +423,66 @@ struct State {
 // where sequences start in a tile
 // ---------------------------------------------------------------------------
 
-// Moves on over the starts below p + n, noting them in shared memory;
-// `next` is the first start not yet passed.  All threads call it; a barrier
-// follows before the notes are read.
+// A tile's sequences.
+struct Marks {
+  unsigned long long starts;  // places where one starts
+  int n;                      // places taken
+  bool closes;                // a sequence ends at its end
+};
+// Notes the starts below p + n, n at most kTile, in shared memory, and moves
+// `next`, the first start not yet passed (at next_at), on.  Where the tile
+// need not reach its end (`may_cut`) and its last sequence neither ends there
+// nor fills it, the tile ends where that sequence starts: short sequences are
+// then never cut, and need no state.  All threads call it.
 template <int DK>
-__device__ __forceinline__ void mark_starts(Shared<DK>& sh, const Starts& st, int64_t p, int n, int64_t& next,
-                                            int64_t& next_at) {
+__device__ __forceinline__ Marks mark_starts(Shared<DK>& sh, const Starts& st, int64_t p, int n, bool may_cut, int64_t& next,
+                                             int64_t& next_at) {
+  Marks m = {0, n, false};
+  if (next_at >= p + n) {  // none
+    m.closes = next_at == p + n;
+    return m;
+  }
   if (threadIdx.x == 0) {
     sh.starts = 0;
     sh.closes = 0;
   }
   if (threadIdx.x < kTile) sh.sequence[threadIdx.x] = -1;
   __syncthreads();
-  if (next_at >= p + n) {  // none
-    if (threadIdx.x == 0) sh.closes = next_at == p + n;
-    return;
-  }
+  const int64_t before = next;
+  int64_t i, x;
+  int c;
   for (;;) {
-    const int64_t i = next + threadIdx.x;
-    const int64_t x = i <= st.S ? st.at(i) : INT64_MAX;
+    i = next + threadIdx.x;
+    x = i <= st.S ? st.at(i) : INT64_MAX;
     const bool below = x < p + n;
     if (below && x >= p && i < st.S) {
       atomicOr(&sh.starts, 1ull << (x - p));
       atomicMax(&sh.sequence[x - p], (int32_t)i);  // empty sequences start there too: the last one has the tokens
     }
     if (x == p + n) sh.closes = 1;
-    const int c = __syncthreads_count(below);
-    next += c;
+    c = __syncthreads_count(below);
     if (c < kThreads) break;
+    next += c;
   }
-  next_at = next <= st.S ? st.at(next) : INT64_MAX;
+  m.starts = sh.starts;
+  m.closes = sh.closes != 0;
+  const int last = m.starts ? 63 - __clzll((long long)m.starts) : 0;
+  if (may_cut && !m.closes && last > 0) {
+    m.n = last;
+    m.starts &= ~(1ull << last);
+    m.closes = true;
+    c = __syncthreads_count(x < p + last);
+    if (c == 0 && next > before) {  // (more empty sequences than threads: back to the first that starts there)
+      next = st.first_from(p + last, before, next);
+      next_at = p + last;
+      return m;
+    }
+  }
+  if (threadIdx.x == c) sh.next_at = x;  // the first that is not below
+  next += c;
+  __syncthreads();
+  next_at = sh.next_at;
+  return m;
 }
 
 // ---------------------------------------------------------------------------
@@ -432,7 +521,9 @@ __global__ void __launch_bounds__(kThreads) carry_kernel(const __grid_constant__
     cp_commit();
     cp_wait<0>();
     __syncthreads();
-    state.add(sh, (int)max(from - p, (int64_t)0), kTile, ps.back, ps.scale_add, lane);
+    const int a0 = (int)max(from - p, (int64_t)0);
+    if (ps.out) state.template add<true>(sh, a0, kTile, ps.back, ps.scale_add, lane);
+    else state.template add<false>(sh, a0, kTile, ps.back, ps.scale_add, lane);
   }
   float* out = ps.carry + ((int64_t)head * a.runs + run) * DK * DK;
   state.each(lane, [&](float& x, int i, int j) { out[i * DK + part * D::DV + j] = x; });
@@ -443,30 +534,27 @@ template <int DK>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
   wait_predecessor();
   const Pass& ps = a.pass[blockIdx.y];
-  const int per_head = DK * DK / 4 / 256 > 0 ? DK * DK / 4 / 256 : 1;
-  const int head = blockIdx.x / per_head, at = blockIdx.x % per_head * 256 + threadIdx.x;
-  if (at >= DK * DK / 4) return;
+  constexpr int kPerHead = DK * DK / 256;
+  const int head = blockIdx.x / kPerHead, at = blockIdx.x % kPerHead * 256 + threadIdx.x;
   const float through = power(a.decay[head], (int64_t)a.tiles * kTile);
-  float4* c = reinterpret_cast<float4*>(ps.carry + (int64_t)head * a.runs * DK * DK) + at;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kAhead = 8;
+  float* c = ps.carry + (int64_t)head * a.runs * DK * DK + at;
+  float s = 0.f;
+  constexpr int kAhead = 16;
   for (int r = 0; r < a.runs - 1; r += kAhead) {
-    float4 x[kAhead];
+    float x[kAhead];
     int32_t kind[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      kind[k] = r + k < a.runs - 1 ? __ldcg(ps.kind + r + k) : kNothing;
-      if (kind[k] != kNothing) x[k] = __ldcg(c + (int64_t)(r + k) * (DK * DK / 4));
+    for (int k = 0; k < kAhead; ++k) {  // (what is not there to be read is not used either)
+      const int at_run = min(r + k, a.runs - 2);
+      kind[k] = __ldcg(ps.kind + at_run);
+      x[k] = __ldcg(c + (int64_t)at_run * DK * DK);
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (kind[k] == kNothing) continue;
+      if (r + k >= a.runs - 1) break;
       if (kind[k] == kThrough) {
-        s.x = fmaf(through, s.x, x[k].x);
-        s.y = fmaf(through, s.y, x[k].y);
-        s.z = fmaf(through, s.z, x[k].z);
-        s.w = fmaf(through, s.w, x[k].w);
-        c[(int64_t)(r + k) * (DK * DK / 4)] = s;
+        s = fmaf(through, s, x[k]);
+        c[(int64_t)(r + k) * DK * DK] = s;
       } else {
         s = x[k];
       }
@@ -478,21 +566,29 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
 // the outputs
 // ---------------------------------------------------------------------------
 
+// Resident blocks of an SM.
+template <int DK>
+constexpr int kBlocks = DK == 128 ? 3 : 4;
+
 // Whether any of the tile's values is an infinity or a NaN.
 template <int DT, int DK>
 __device__ __forceinline__ bool not_finite(const Shared<DK>& sh) {
   using D = Shape<DK>;
   constexpr uint32_t kInf = DT == TBE_BF16 ? 0x7f80u : 0x7c00u;
   bool bad = false;
-  for (int i = threadIdx.x; i < kTile * D::DV / 2; i += kThreads) {
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(sh.v + i / (D::DV / 2) * D::LV + i % (D::DV / 2) * 2);
-    bad |= (u & kInf) == kInf || (u >> 16 & kInf) == kInf;
+  for (int i = threadIdx.x; i < kTile * D::DV / 8; i += kThreads) {
+    const uint4 u = *reinterpret_cast<const uint4*>(sh.v + i / (D::DV / 8) * D::LV + i % (D::DV / 8) * 8);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t x = (&u.x)[e];
+      bad |= (x & kInf) == kInf || (x >> 16 & kInf) == kInf;
+    }
   }
   return bad;
 }
 
 template <int DT, int DK>
-__global__ void __launch_bounds__(kThreads, 3) output_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, kBlocks<DK>) output_kernel(const __grid_constant__ Args a) {
   using D = Shape<DK>;
   extern __shared__ __align__(16) uint8_t raw[];
   Shared<DK>& sh = *reinterpret_cast<Shared<DK>*>(raw);
@@ -558,20 +654,25 @@ __global__ void __launch_bounds__(kThreads, 3) output_kernel(const __grid_consta
   const uint32_t stored = smem_u32(sh.s) + ((lane % 8 + lane / 8 % 2 * 8) * D::LV + lane / 16 * 8) * 2;
   const int row0 = warp * 16 + lane / 4;  // this lane's rows are row0 and row0 + 8
 
-  for (int64_t p = p0; p < p1; p += kTile) {
-    const int n = (int)min((int64_t)kTile, p1 - p);
-    const bool last_tile = p + kTile >= p1;
+  // what the products of a row and a column of another 16 are multiplied by has a part for each
+  float by_col[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) by_col[e] = sh.pow[15 - (lane % 4 * 2 + (e & 1) + (e >> 1) * 8)] * ps.scale_tile;
+
+  for (int64_t p = p0; p < p1;) {
+    const int most = (int)min((int64_t)kTile, p1 - p);
     const int64_t came = next - 1;  // the sequence that comes in, where there is one
-    load_rows<DK, D::LK>(sh.q, ps.q + head * ps.hq, ps.sq, p, n, a.d, a.N, ps.back, ps.piece);
-    load_rows<DK, D::LK>(sh.k, ps.k + head * ps.hk, ps.sk, p, n, a.d, a.N, ps.back, ps.piece);
-    load_rows<D::DV, D::LV>(sh.v, ps.v + head * ps.hv + first_col, ps.sv, p, n, a.d - first_col, a.N, ps.back, ps.piece);
+    load_rows<DK, D::LK>(sh.q, ps.q + head * ps.hq, ps.sq, p, most, a.d, a.N, ps.back, ps.piece);
+    load_rows<DK, D::LK>(sh.k, ps.k + head * ps.hk, ps.sk, p, most, a.d, a.N, ps.back, ps.piece);
+    load_rows<D::DV, D::LV>(sh.v, ps.v + head * ps.hv + first_col, ps.sv, p, most, a.d - first_col, a.N, ps.back, ps.piece);
     cp_commit();
-    mark_starts(sh, st, p, n, next, next_at);
+    const Marks mk = mark_starts(sh, st, p, most, p + most < p1, next, next_at);
+    const unsigned long long starts = mk.starts;
+    const int n = mk.n;
+    const bool closes = mk.closes, last_tile = p + n >= p1;
+    const bool whole = (starts & ~1ull) == 0;  // one sequence has all of the tile
     cp_wait<0>();
     __syncthreads();
-    const unsigned long long starts = sh.starts;
-    const bool closes = sh.closes != 0;
-    const bool whole = (starts & ~1ull) == 0;  // one sequence has all of the tile
 
     float o[D::NO][4];
 #pragma unroll
@@ -604,35 +705,41 @@ __global__ void __launch_bounds__(kThreads, 3) output_kernel(const __grid_consta
         }
       }
       if (live) {
-        float r[D::NO][4];
-#pragma unroll
-        for (int j = 0; j < D::NO; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) r[j][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < D::KS; ++k)
-#pragma unroll
-          for (int j = 0; j < D::NO; j += 2) {
-            uint32_t b[4];
-            ldsm_t(b, stored + (k * 16 * D::LV + j * 8) * 2);
-            mma<DT>(r[j], qf[k], b[0], b[1]);
-            mma<DT>(r[j + 1], qf[k], b[2], b[3]);
-          }
+        float f[2];
+        bool mine[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int row = row0 + half * 8;
-          if (row >= at && row < end) {
-            const float f = sh.pow[row - at + 1 - late] * read_scale;
+          mine[half] = row >= at && row < end;
+          f[half] = mine[half] ? sh.pow[row - at + 1 - late] * read_scale : 0.f;
+        }
 #pragma unroll
-            for (int j = 0; j < D::NO; ++j) {
-              o[j][2 * half] = r[j][2 * half] * f;
-              o[j][2 * half + 1] = r[j][2 * half + 1] * f;
+        for (int j0 = 0; j0 < D::NO; j0 += 4) {
+          float r[4][4];
+#pragma unroll
+          for (int k = 0; k < D::KS; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              uint32_t b[4];
+              ldsm_t(b, stored + (k * 16 * D::LV + (j0 + j) * 8) * 2);
+              if (k == 0) {
+                mma_first<DT>(r[j], qf[k], b[0], b[1]);
+                mma_first<DT>(r[j + 1], qf[k], b[2], b[3]);
+              } else {
+                mma<DT>(r[j], qf[k], b[0], b[1]);
+                mma<DT>(r[j + 1], qf[k], b[2], b[3]);
+              }
             }
-          }
+          // (chosen by row, not added up: what the state holds stays in its sequence)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j0 + j][e] = mine[e >> 1] ? r[j][e] * f[e >> 1] : o[j0 + j][e];
         }
       }
       if (ends ? ps.out != nullptr && known : !last_tile) {
-        state.add(sh, at, end, late, ps.scale_add, lane);
+        if (ps.out) state.template add<true>(sh, at, end, late, ps.scale_add, lane);
+        else state.template add<false>(sh, at, end, late, ps.scale_add, lane);
         live = true;
         if (ends) state.write(ps.out + matrix, a.d, first_col, lane);
       }
@@ -641,7 +748,8 @@ __global__ void __launch_bounds__(kThreads, 3) output_kernel(const __grid_consta
     }
 
     // the tile's own part: 16 rows of keys at a time
-    const bool apart = !whole && __syncthreads_or(not_finite<DT, DK>(sh));
+    // (rows of other sequences, and those behind a tile that was cut, are multiplied by 0)
+    const bool apart = !(whole && n == most) && __syncthreads_or(not_finite<DT, DK>(sh));
     // first row of each of this lane's rows' sequences
     int from[2];
 #pragma unroll
@@ -661,15 +769,33 @@ __global__ void __launch_bounds__(kThreads, 3) output_kernel(const __grid_consta
         mma<DT>(c[0], qf[k], b[0], b[1]);
         mma<DT>(c[1], qf[k], b[2], b[3]);
       }
-      float top[2] = {0.f, 0.f};
+      if (j < warp) {
+        const float by_row[2] = {sh.pow[row0 - j * 16 - 15], sh.pow[row0 + 8 - j * 16 - 15]};
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int half = e >> 1, s = j * 16 + t * 8 + lane % 4 * 2 + (e & 1), away = row0 + half * 8 - s;
-          c[t][e] = away >= 0 && s >= from[half] ? c[t][e] * (sh.pow[away & 63] * ps.scale_tile) : 0.f;
-          top[half] = fmaxf(top[half], fabsf(c[t][e]));
+          for (int e = 0; e < 4; ++e) c[t][e] *= by_row[e >> 1] * by_col[t * 2 + (e & 1)];
+        if (!whole) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (j * 16 + t * 8 + lane % 4 * 2 + (e & 1) < from[e >> 1]) c[t][e] = 0.f;
         }
+      } else {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int half = e >> 1, s = j * 16 + t * 8 + lane % 4 * 2 + (e & 1), away = row0 + half * 8 - s;
+            c[t][e] = away >= 0 && s >= from[half] ? c[t][e] * (sh.pow[away & 63] * ps.scale_tile) : 0.f;
+          }
+      }
+      float top[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        top[half] = fmaxf(fmaxf(fabsf(c[0][2 * half]), fabsf(c[0][2 * half + 1])),
+                          fmaxf(fabsf(c[1][2 * half]), fabsf(c[1][2 * half + 1])));
       if (DT == TBE_F16) {
         bool moves = j == 0;
         int want[2];
@@ -766,6 +892,7 @@ __global__ void __launch_bounds__(kThreads, 3) output_kernel(const __grid_consta
     if (keep_state) note_top();
     __syncthreads();  // the tile and the state in shared memory have been read
     if (keep_state) publish();
+    p += n;
   }
 }
 
@@ -858,12 +985,12 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 int width_of(int32_t d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
 int parts_of(int32_t d) { return width_of(d) == 128 ? (d + 63) / 64 : 1; }
 
-// Runs: as many blocks as the GPU holds at once, three to an SM.
+// Runs: as many blocks as the GPU holds at once.
 struct Split {
   int32_t tiles, runs;
 };
 Split split_of(int64_t N, int32_t H, int32_t d, int passes) {
-  const int64_t all = (N + kTile - 1) / kTile, want = std::max<int64_t>(1, 3 * (int64_t)sm_count() / ((int64_t)H * parts_of(d) * passes));
+  const int64_t all = (N + kTile - 1) / kTile, want = std::max<int64_t>(1, (width_of(d) == 128 ? kBlocks<128> : kBlocks<64>) * (int64_t)sm_count() / ((int64_t)H * parts_of(d) * passes));
   Split s;
   s.tiles = (int32_t)std::max<int64_t>(1, (all + want - 1) / want);
   s.runs = (int32_t)std::max<int64_t>(1, (all + s.tiles - 1) / s.tiles);
@@ -917,7 +1044,7 @@ int launch(const Args& a, int passes, cudaStream_t s) {
     if (a.runs > 1) {
       if ((st = start(carry, dim3((unsigned)(a.runs - 1) * per_run, passes), kThreads, smem, false, s, a)) != TBE_OK) return st;
       trace_mark(s, "linear_attention_carry");
-      const unsigned blocks = (unsigned)a.H * std::max(1, DK * DK / 4 / 256);
+      const unsigned blocks = (unsigned)a.H * (DK * DK / 256);
       if ((st = start((const void*)join_kernel<DK>, dim3(blocks, passes), 256, 0, true, s, a)) != TBE_OK) return st;
       trace_mark(s, "linear_attention_join");
       after = true;

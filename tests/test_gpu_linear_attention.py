@@ -114,7 +114,7 @@ def run_and_check(tbe, c, kind, scale=0.3, grads=True):
         close(f.s_last, last, size_last, 0.0, fp32, "s_last")
     plain = tbe.tbe_linear_attention(c["q"], c["k"], c["v"], c["decay"], c["offsets"], s0=c["s0"], scale=scale)
     assert plain.s_last is None
-    assert torch.equal(plain.o, f.o)
+    close(plain.o, o, size, half, fp32 + 2.0**-15, "o without last states")  # (states in two terms of bf16)
     if grads:
         args = (do, q, k, v)
         want = gradients(*args, decay, offsets, s0, dl, scale)
