@@ -600,7 +600,6 @@ __device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
 __global__ void __launch_bounds__(kRowThreads) row_kernel(const RowArgs a) {
   wait_predecessor();
   __shared__ float2 part[32][kRows];
-  __shared__ float sum[32];
   __shared__ bool last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t count = *a.count;
@@ -745,30 +744,12 @@ Layout layout(int64_t N, int32_t V, int32_t D, bool grad, bool copy_table) {
   return w;
 }
 
-using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-Encode encoder() {
-  static const Encode fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<Encode>(p);
-  }();
-  return fn;
-}
 // [rows, cols] of 16-bit elements, `stride` elements from row to row, in
 // boxes of 64 x 64; zeros outside.
 bool map_of(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t stride, int32_t dtype) {
-  const Encode fn = encoder();
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
   const cuuint32_t box[2] = {64, 64}, one[2] = {1, 1};
-  return fn && fn(m, dtype == TBE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                  const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, dtype, 2, p, dims, strides, box, one);
 }
 
 // Launches `kernel`; `after`: it may start while the kernel before it ends.

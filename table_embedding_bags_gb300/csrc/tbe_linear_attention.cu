@@ -4,18 +4,25 @@
 //
 //   S_t = gamma S_{t-1} + k_t v_t^T      o_t = scale q_t^T S_t      gamma = exp(-decay[head])
 //
-// In tiles of 64 tokens: within a tile a masked product, o += (q k^T . gamma^
-// distance) v, and across tiles the state, o += gamma^(place + 1) q S and S =
-// gamma^64 S + sum gamma^(63 - place) k v^T.  Tiles cut the token axis, not
-// the sequences: one tile may hold many short sequences, whose products the
-// mask keeps apart, so the work goes by tokens whatever the lengths are.
+// In tiles of up to 128 tokens: within a tile a masked product, o += (q k^T .
+// gamma^distance) v, and across tiles the state, o += gamma^(place + 1) q S
+// and S = gamma^n S + sum gamma^(n - 1 - place) k v^T.  A tile may hold many
+// short sequences, whose products the mask keeps apart; it ends where its
+// last sequence starts if that one goes on behind it, so short sequences need
+// no state at all.  (Where states come in or go out, a tile has one sequence.)
 //
-// A block takes a run of tiles of one head and up to 64 value columns.  The
-// state that a run finds comes from the runs before it: a first kernel sums
-// what each run adds to the state of the sequence that leaves it, a second
-// one joins those along the runs, in order; sequences that end inside their
-// run cost neither anything.  No block waits for another inside a kernel and
-// no sum depends on timing.
+// A block takes a run of the token axis of one head.  The state that a run
+// finds comes from the runs before it: the same kernel first sums what each
+// run adds to the state of the sequence that leaves it, a second one joins
+// those along the runs, in order; sequences that end inside their run cost
+// neither anything.  No block waits for another inside a kernel and no sum
+// depends on timing.
+//
+// The four products of a tile go to the tensor cores (tcgen05), each with 128
+// rows: q k^T and q S, then the weighted (q k^T) from TMEM times v, and the
+// weighted keys times v.  One warp finds the tiles, starts the copies and
+// issues the products; eight warps weigh what comes out of one product before
+// it goes into the next, hold the state in registers and write the outputs.
 //
 // The backward needs nothing new.  With G_t = scale q_t do_t^T + gamma G_{t+1},
 //   dq_t = scale S_t do_t     is the same recurrence of (do, v, k) with S^T,
@@ -26,12 +33,14 @@
 // Numbers.  Products of inputs are exact and summed in fp32; the state is
 // held in fp32.  Two operands are rounded to the inputs' type: the weighted
 // products of a tile and the state as it is read, both half a step of the
-// type that the output is rounded to as well.  What is added to the state
-// must not be: gamma^n k goes in as the sum of as many numbers of the type as
-// hold its 24 bits (three of bf16, two of fp16).  fp16 lacks fp32's range, so
-// there each of the three is first moved by a power of two that its largest
-// value names: products by row, the state by block, keys by warp.
-#include "tbe_internal.cuh"
+// type that the output is rounded to as well.  What is added to the state is
+// not: gamma^n k goes in as the sum of two numbers of the type (16 bits of
+// bf16, 22 of fp16), or three of bf16 where the state is a result.  A tile's
+// sum begins at 0 and is added to the state in registers, because the tensor
+// cores cut sums off.  fp16 lacks fp32's range, so there each of the three is
+// first moved by a power of two that its largest value names: products by
+// row, the state and the keys by tile.
+#include "tbe_tensor.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -41,10 +50,12 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kTile = 64;     // tokens
-constexpr int kThreads = 128; // four warps: 16 rows of a tile each
+constexpr int kTile = 128;         // tokens
+constexpr int kWarps = 8;          // that work on what the products give
+constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kPowers = kTile + 2;
 constexpr int kMaxPasses = 3;
+constexpr int kMaxMaps = 4;
 
 __device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -52,27 +63,29 @@ __device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontro
 struct Pass {
   const uint16_t *q, *k, *v;
   int64_t sq, sk, sv, hq, hk, hv;
+  int32_t mq, mk, mv;  // their tensor maps
   uint16_t* o;
   int64_t so, ho;
   const float* in;     // [sequences, heads, d, d] or null
   float* out;          // likewise
   int32_t in_turned;   // `in` holds the transposes
   int32_t back;        // from the last token to the first, decay behind the read
-  int32_t piece;       // bytes that rows are read by,
-  int32_t piece_o;     //   and written by
+  int32_t piece_o;     // bytes that rows are written by
   float scale_tile, scale_add, scale_read;
-  float* carry;        // [heads, runs, DK, DK]: what each run leaves to the next
+  float* carry;        // [heads, runs, W, W]: what each run leaves to the next
   int32_t* kind;       // [runs]
 };
 struct Args {
+  CUtensorMap map[kMaxMaps];
   Pass pass[kMaxPasses];
   const float* decay;
   IdxPtr offsets;
   int64_t N;
   int32_t S, H, d;
-  int32_t tiles;   // of a run
+  int32_t run;     // tokens of a run
   int32_t runs;
-  int32_t parts;   // of the value columns
+  int32_t piece;   // bytes that rows are read by, 0 for tensor copies
+  int32_t terms;   // of the weighted keys that there is room for
   int32_t* status;
 };
 // What a run leaves: nothing, the state of a sequence that began in it, or
@@ -86,10 +99,11 @@ struct Starts {
   int32_t S;
   bool back;
   __device__ __forceinline__ int64_t at(int64_t i) const { return back ? N - p.ldg(S - i) : p.ldg(i); }
-  __device__ __forceinline__ int32_t sequence(int64_t i) const { return (int32_t)(back ? S - 1 - i : i); }
-  // the first i with at(i) >= x, of all or of lo .. hi
-  __device__ int64_t first(int64_t x) const { return first_from(x, 0, (int64_t)S + 1); }
-  __device__ int64_t first_from(int64_t x, int64_t lo, int64_t hi) const {
+  __device__ __forceinline__ int64_t at_or_end(int64_t i) const { return i <= S ? at(i) : INT64_MAX; }
+  __device__ __forceinline__ int64_t sequence(int64_t i) const { return back ? S - 1 - i : i; }
+  // the first i with at(i) >= x
+  __device__ int64_t first(int64_t x) const {
+    int64_t lo = 0, hi = (int64_t)S + 1;
     while (lo < hi) {
       const int64_t mid = (lo + hi) >> 1;
       if (at(mid) >= x) hi = mid; else lo = mid + 1;
@@ -99,10 +113,6 @@ struct Starts {
 };
 
 __device__ __forceinline__ float power(float decay, int64_t n) { return n == 0 ? 1.f : exp2f(-(float)n * decay * kLog2e); }
-
-// ---------------------------------------------------------------------------
-// fragments
-// ---------------------------------------------------------------------------
 
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -123,42 +133,6 @@ __device__ __forceinline__ float to_float(uint16_t u) {
   return unpack2<DT>(u).x;
 }
 
-template <int DT>
-__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if (DT == TBE_BF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// c = a b alone.
-template <int DT>
-__device__ __forceinline__ void mma_first(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if (DT == TBE_BF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ void ldsm(uint32_t* r, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_t(uint32_t* r, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
 // Powers of two for fp16: what brings values of magnitude `top` to 2^14 or
 // just below, as an exponent (kept where fp32 stays normal).
 __device__ __forceinline__ int room_for(float top) {
@@ -171,373 +145,799 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // a block's shared memory
 // ---------------------------------------------------------------------------
 
-// Rows are padded by 16 bytes: eight rows of a fragment then lie in different banks.
-template <int DK>
-struct Shape {
-  static constexpr int DV = DK < 64 ? DK : 64;
-  static constexpr int LK = DK + 8, LV = DV + 8;
-  // the state over the warps: MT x NT pieces of 16 x 8 each
-  static constexpr int MT = DK / 64 > 0 ? DK / 64 : 1;
-  static constexpr int NT = DK >= 64 ? DV / 8 : DV / 16;
-  static constexpr int NO = DV / 8;  // pieces of 8 columns of the outputs
-  static constexpr int KS = DK / 16;
-};
-template <int DK>
-struct Shared {
-  using D = Shape<DK>;
-  uint16_t q[kTile * D::LK], k[kTile * D::LK], v[kTile * D::LV], s[DK * D::LV];
-  float pow[kPowers];
-  unsigned long long starts;  // places of the tile where a sequence starts
-  int32_t sequence[kTile];    // and which
-  int32_t closes;             // a sequence ends at the tile's end
-  int64_t next_at;            // the first start behind it
-  uint32_t top[3];            // largest magnitudes of the state, in turn
+// Operands lie in blocks of 64 columns, [128 rows x 128 bytes] with the
+// 128-byte swizzle, as tensor copies write them: element (row, col) in the
+// 16-byte chunk (col / 8) ^ (row & 7) of its row.
+constexpr int kBlock = kTile * 128;
+template <int W>
+struct Room {  // W: columns of a head, filled up
+  static constexpr int operand = W / 64 * kBlock;
+  static constexpr int state = W * W * 2;
+  static constexpr int q = 0, k = operand, v = 2 * operand, s = 3 * operand, rest = 3 * operand + state;  // behind the terms
+  static constexpr int bytes(int n_terms) { return rest + n_terms * operand; }
+  // columns of TMEM: the products of a tile, whose weighted form takes the first half of theirs; the two parts of
+  // the outputs; the sum that goes to the state (in the second half of the products', where there is room)
+  static constexpr int cols = W == 64 ? 256 : 512;
+  static constexpr int tp = 0, to = kTile, ts = kTile + W, ta = W == 64 ? kTile / 2 : kTile + 2 * W;
 };
 
-// The kTile rows of one head from position p on, COLS of their columns, to
-// shared memory; zeros behind the last row (n) and column.
-template <int COLS, int LD>
-__device__ __forceinline__ void load_rows(uint16_t* dst, const uint16_t* src, int64_t stride, int64_t p, int n, int cols,
-                                          int64_t N, bool back, int piece) {
-  const int64_t first = back ? N - 1 - p : p, step = back ? -stride : stride;  // row r is first * stride + r * step
-  if (piece == 16) {
-    constexpr int kPerRow = COLS / 8, kRowsAtOnce = kThreads / kPerRow;
-    const int r0 = threadIdx.x / kPerRow, c = threadIdx.x % kPerRow * 8;
-    const uint16_t* from = src + first * stride + r0 * step + c;
-    uint32_t to = smem_u32(dst + r0 * LD + c);
-    const int rows = c < cols ? n - r0 : 0;  // this thread's row k * kRowsAtOnce is there where that is below
-#pragma unroll
-    for (int k = 0; k < kTile / kRowsAtOnce; ++k) {
-      const bool in = k * kRowsAtOnce < rows;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(in ? from : src), "r"(in ? 16 : 0)
-                   : "memory");
-      from += kRowsAtOnce * step;
-      to += kRowsAtOnce * LD * 2;
+// What is known of a tile.
+struct Tile {
+  int64_t p;          // its first position, -1 behind the last tile
+  uint32_t starts[4]; // places where a sequence starts
+  int32_t n;          // positions taken
+  int32_t e0;         // where its first sequence ends
+  int32_t begins;     // a sequence starts at its first place
+  int32_t live;       // its first sequence has a state
+  int32_t adds;       // it adds to the state,
+  int32_t leaves;     //   which goes on behind it
+  int32_t mixed;      // rows of other sequences have been copied with it
+  int64_t sequence;   // its first sequence
+};
+struct Control {
+  uint64_t known[2], full, products, weighted, keys, out_done, add_done, add_read, out_read, state_ready, exchange, row_max[4];
+  Tile tile[2];
+  float pow[kPowers];
+  alignas(16) float by_col[32];  // powers over 32 neighbouring columns
+  float top_row[2][kTile];
+  uint32_t top[3];
+  int32_t bad[2];
+  uint32_t tmem;
+  int32_t dead;
+};
+
+// A bounded wait: false (and the others give up too) after four seconds.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int32_t* dead) {
+  uint64_t begin, now;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(begin));
+  for (;;) {
+    if (mbar_wait(bar, parity, 64)) return true;
+    if (*dead) return false;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+    if (now - begin > 4000000000ull) {
+      *dead = 1;
+      return false;
     }
-    return;
   }
-  const int each = piece / 2, per_row = COLS / each;
-  for (int i = threadIdx.x; i < kTile * per_row; i += kThreads) {
+}
+// (whole warps)
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& c) {
+  return __all_sync(kFull, mbar_wait(bar, parity & 1, 4) || wait_long(bar, parity & 1, &c.dead));
+}
+__device__ __forceinline__ void to_products() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// which positions make a tile (all lanes of one warp)
+// ---------------------------------------------------------------------------
+
+struct Marker {
+  Starts st;
+  bool one;         // a tile has one sequence
+  int64_t next;     // the first start not yet passed
+  int64_t x;        // at(next + lane), read ahead
+
+  __device__ __forceinline__ void seek(int64_t p, int lane) {
+    next = st.first(p);
+    x = st.at_or_end(next + lane);
+  }
+  // The tile at p, of up to `most` positions; live: a state comes in.
+  __device__ __forceinline__ void mark(Tile& t, int64_t p, int64_t p1, bool live, bool has_in, bool has_out, int lane) {
+    const int most = (int)min((int64_t)kTile, p1 - p);
+    const int64_t before = next;
+    uint32_t starts[4] = {0, 0, 0, 0};
+    int64_t upto = next;  // starts at or below p
+    bool closes = false;
+    int c;
+    for (;;) {
+      const bool in = x >= p && x < p + most && next + lane < st.S;
+      const int place = in ? (int)(x - p) : 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) starts[w] |= __reduce_or_sync(kFull, in && place >> 5 == w ? 1u << (place & 31) : 0u);
+      closes |= __any_sync(kFull, x == p + most);
+      upto += __popc(__ballot_sync(kFull, x <= p));
+      c = __popc(__ballot_sync(kFull, x < p + most));
+      if (c < 32) break;
+      next += 32;
+      x = st.at_or_end(next + lane);
+    }
+    t.p = p;
+    t.n = most;
+    t.begins = starts[0] & 1;
+    // the first sequence that starts behind the first place, and the last one
+    int first = kTile, last = 0;
+#pragma unroll
+    for (int w = 3; w >= 0; --w) {
+      const uint32_t u = w == 0 ? starts[0] & ~1u : starts[w];
+      if (u) {
+        first = w * 32 + __ffs((int)u) - 1;
+        if (last == 0) last = w * 32 + 31 - __clz((int)u);
+      }
+    }
+    int cut = kTile;
+    if (one) cut = first;
+    else if (p + most < p1 && !closes && last > 0) cut = last;
+    if (cut < most) {
+      t.n = cut;
+      closes = true;
+      if (next == before) {
+        c = __popc(__ballot_sync(kFull, x < p + cut));
+      } else {  // (more starts than lanes)
+        next = st.first(p + cut);
+        c = 0;
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        starts[w] &= cut >= w * 32 + 32 ? ~0u : cut > w * 32 ? (1u << (cut - w * 32)) - 1 : 0u;
+    }
+    next += c;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) t.starts[w] = starts[w];
+    t.e0 = min(first, t.n);
+    const bool whole = t.e0 == t.n, last_tile = p + t.n >= p1;
+    // (its first sequence is always known, unless offsets are broken)
+    t.sequence = t.begins ? upto - 1 : before - 1;
+    const bool known = t.sequence >= 0 && t.sequence < st.S;
+    t.sequence = known ? st.sequence(t.sequence) : 0;
+    t.live = t.begins ? has_in : live;
+    const bool goes_on = whole && !closes && !last_tile;
+    t.adds = goes_on || (has_out && known && whole && closes);
+    t.leaves = goes_on;
+    t.mixed = !(whole && (t.n == kTile || p + t.n == st.N));
+    x = st.at_or_end(next + lane);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// the kernel: outputs, or (SUMS) what each run leaves
+// ---------------------------------------------------------------------------
+
+// One head's rows of a tile to an operand, where tensor copies cannot: from
+// token `first` on, zeros for tokens and columns that are not there.
+template <int W>
+__device__ __forceinline__ void load_rows(uint8_t* dst, const uint16_t* src, int64_t stride, int64_t first, int64_t N, int d,
+                                          int piece, int thread) {
+  const int each = piece / 2, per_row = W / each;
+  for (int i = thread; i < kTile * per_row; i += 32 * kWarps) {
     const int r = i / per_row, c = (i - r * per_row) * each;
-    const bool in = r < n && c < cols;
-    const uint16_t* from = in ? src + first * stride + r * step + c : src;
-    uint16_t* to = dst + r * LD + c;
-    const uint32_t bytes = in ? piece : 0;
-    if (piece == 8)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(bytes) : "memory");
-    else if (piece == 4)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(bytes) : "memory");
-    else
-      *to = in ? __ldg(from) : 0;
+    const int64_t token = first + r;
+    const bool in = token >= 0 && token < N && c < d;
+    const uint16_t* from = src + token * stride + c;
+    uint8_t* to = dst + c / 64 * kBlock + r * 128 + ((c % 64 / 8) ^ (r & 7)) * 16 + c % 8 * 2;
+    if (piece == 16) *reinterpret_cast<uint4*>(to) = in ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
+    else if (piece == 8) *reinterpret_cast<uint2*>(to) = in ? __ldg(reinterpret_cast<const uint2*>(from)) : make_uint2(0, 0);
+    else if (piece == 4) *reinterpret_cast<uint32_t*>(to) = in ? __ldg(reinterpret_cast<const uint32_t*>(from)) : 0;
+    else *reinterpret_cast<uint16_t*>(to) = in ? __ldg(from) : 0;
   }
 }
 
-// ---------------------------------------------------------------------------
-// the state of a block, in registers
-// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int32_t col, int32_t head, int32_t row,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(col), "r"(head), "r"(row), "r"(smem_u32(bar))
+      : "memory");
+}
 
-template <int DT, int DK>
-struct State {
-  using D = Shape<DK>;
-  float s[D::MT][D::NT][4];
-  int m0, n0;  // the warp's first key row and value column
+// Descriptor of an operand whose next 64 rows (along M or N) are `apart` bytes on.
+__device__ __forceinline__ uint64_t desc_of(uint32_t addr, uint32_t apart) {
+  return (tc_desc(addr) & ~(0x3fffull << 16)) | ((uint64_t)(apart >> 4) << 16);
+}
+__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 
-  __device__ __forceinline__ void place(int warp) {
-    if (DK >= 64) {
-      m0 = warp * D::MT * 16;
-      n0 = 0;
-    } else {
-      m0 = warp % 2 * 16;
-      n0 = warp / 2 * (DK / 2);
+template <int DT, int W, bool SUMS>
+struct Worker {
+  static constexpr int kCols = W / 2;  // of the state and the outputs, to a thread
+  const Args& a;
+  const Pass& ps;
+  Control& c;
+  uint8_t *terms, *room;
+  uint32_t tmem;
+  int warp, lane, quarter, half, row;
+  int head;
+  float s[kCols];         // the state: row `row`, columns half * kCols ..
+  float read_scale = 0.f; // what the state in shared memory is to be multiplied by
+  uint32_t exchanges = 0;
+
+  __device__ __forceinline__ uint32_t lanes() const { return (uint32_t)(quarter * 32) << 16; }
+  __device__ __forceinline__ bool holds() const { return row < W; }  // (else nothing of the state)
+  __device__ __forceinline__ void arrive(uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) bar_arrive(bar);
+  }
+  // All of the eight warps meet.  c.top has a word for each meeting in turn.
+  __device__ __forceinline__ bool meet() {
+    arrive(&c.exchange);
+    if (!wait(&c.exchange, exchanges, c)) return false;
+    if (warp == 0 && lane == 0) c.top[(exchanges + 2) % 3] = 0;
+    ++exchanges;
+    return true;
+  }
+  // The largest of all threads' values (not negative).
+  __device__ __forceinline__ bool largest(float& t) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, o));
+    uint32_t* top = &c.top[exchanges % 3];
+    if (lane == 0) atomicMax(top, __float_as_uint(t));
+    if (!meet()) return false;
+    t = __uint_as_float(*(volatile uint32_t*)top);
+    return true;
+  }
+
+  // The state from, or to, a [d, d] matrix (or its transpose), or a [W, W] one.
+  __device__ __forceinline__ void read(const float* p, int d, bool turned) {
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      const int col = half * kCols + j;
+      s[j] = row < d && col < d ? __ldg(p + (turned ? (int64_t)col * d + row : (int64_t)row * d + col)) : 0.f;
     }
   }
-  __device__ __forceinline__ void clear() {
+  __device__ __forceinline__ void write(float* p, int d) const {
+    if (row >= d) return;
+    float* to = p + (int64_t)row * d + half * kCols;
+    if (d % 4 == 0 && ((uintptr_t)p & 15) == 0) {
 #pragma unroll
-    for (int m = 0; m < D::MT; ++m)
+      for (int j = 0; j < kCols; j += 4)
+        if (half * kCols + j < d) *reinterpret_cast<float4*>(to + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+    } else {
 #pragma unroll
-      for (int n = 0; n < D::NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[m][n][e] = 0.f;
+      for (int j = 0; j < kCols; ++j)
+        if (half * kCols + j < d) to[j] = s[j];
+    }
   }
-  // Calls f(value, key row, value column) for each element held.
-  template <typename F>
-  __device__ __forceinline__ void each(int lane, F f) {
+  // The state to shared memory in the inputs' type, as the operand [key rows, value columns].
+  __device__ __forceinline__ bool publish() {
+    float f = 1.f;
+    if (DT == TBE_F16) {
+      float t = 0.f;
+      if (holds()) {
 #pragma unroll
-    for (int m = 0; m < D::MT; ++m)
-#pragma unroll
-      for (int n = 0; n < D::NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          f(s[m][n][e], m0 + m * 16 + lane / 4 + (e >> 1) * 8, n0 + n * 8 + lane % 4 * 2 + (e & 1));
-  }
-  // A [d, d] matrix, or its transpose; `first` is the block's first value column.
-  __device__ __forceinline__ void read(const float* p, int d, int first, bool turned, int lane) {
-    each(lane, [&](float& x, int i, int j) {
-      j += first;
-      x = i < d && j < d ? __ldg(p + (turned ? (int64_t)j * d + i : (int64_t)i * d + j)) : 0.f;
-    });
-  }
-  __device__ __forceinline__ void write(float* p, int d, int first, int lane) {
-    each(lane, [&](float& x, int i, int j) {
-      j += first;
-      if (i < d && j < d) p[(int64_t)i * d + j] = x;
-    });
-  }
-  __device__ __forceinline__ float largest() const {
-    float t = 0.f;
-#pragma unroll
-    for (int m = 0; m < D::MT; ++m)
-#pragma unroll
-      for (int n = 0; n < D::NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t = fmaxf(t, fabsf(s[m][n][e]));
-    return t;
-  }
-  // To shared memory in the inputs' type, times 2^up.
-  __device__ __forceinline__ void publish(Shared<DK>& sh, int lane, int up) const {
-    const float f = DT == TBE_F16 ? pow2(up) : 1.f;
-#pragma unroll
-    for (int m = 0; m < D::MT; ++m)
-#pragma unroll
-      for (int n = 0; n < D::NT; ++n) {
-        uint16_t* at = sh.s + (m0 + m * 16 + lane / 4) * D::LV + n0 + n * 8 + lane % 4 * 2;
-        *reinterpret_cast<uint32_t*>(at) = pack2<DT>(s[m][n][0] * f, s[m][n][1] * f);
-        *reinterpret_cast<uint32_t*>(at + 8 * D::LV) = pack2<DT>(s[m][n][2] * f, s[m][n][3] * f);
+        for (int j = 0; j < kCols; ++j) t = fmaxf(t, fabsf(s[j]));
       }
+      if (!largest(t)) return false;
+      const int up = room_for(t);
+      f = pow2(up);
+      read_scale = ps.scale_read * pow2(-up);
+    } else {
+      read_scale = ps.scale_read;
+    }
+    if (holds()) {
+#pragma unroll
+      for (int j = 0; j < kCols; j += 8) {
+        const int col = half * kCols + j;
+        uint4 u;
+        u.x = pack2<DT>(s[j] * f, s[j + 1] * f);
+        u.y = pack2<DT>(s[j + 2] * f, s[j + 3] * f);
+        u.z = pack2<DT>(s[j + 4] * f, s[j + 5] * f);
+        u.w = pack2<DT>(s[j + 6] * f, s[j + 7] * f);
+        *reinterpret_cast<uint4*>(room + Room<W>::s + col / 64 * (W * 128) + row * 128 + ((col % 64 / 8) ^ (row & 7)) * 16) = u;
+      }
+    }
+    to_products();
+    arrive(&c.state_ready);
+    return true;
   }
 
-  // S = gamma^(b - a) S + sum over rows a..b-1 of scale gamma^(b - 1 - row + late) k v^T.
-  // EXACT: a state that is a result.  One that is only read, rounded to 16
-  // bits, takes two terms of bf16 (16 bits) and the tensor cores' own sums.
-  template <bool EXACT>
-  __device__ __forceinline__ void add(const Shared<DK>& sh, int a, int b, int late, float scale, int lane) {
-    const uint32_t keys = smem_u32(sh.k) + ((lane % 8 + lane / 16 * 8) * D::LK + m0 + lane / 8 % 2 * 8) * 2;
-    const uint32_t values = smem_u32(sh.v) + ((lane % 8 + lane / 8 % 2 * 8) * D::LV + n0 + lane / 16 * 8) * 2;
-    const int k0 = a / 16, k1 = (b + 15) / 16;
-    int up = 0;
+  // A place's distance from the tile's first position, in the pass's direction.
+  __device__ __forceinline__ int place(int r) const { return ps.back ? kTile - 1 - r : r; }
+
+  // Whether the tile's values hold an infinity or a NaN.
+  __device__ __forceinline__ bool not_finite() const {
+    constexpr uint32_t kInf = DT == TBE_BF16 ? 0x7f80u : 0x7c00u;
+    bool bad = false;
+#pragma unroll 4
+    for (int i = warp * 32 + lane; i < Room<W>::operand / 16; i += 32 * kWarps) {
+      const uint4 u = *reinterpret_cast<const uint4*>(room + Room<W>::v + i * 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t x = (&u.x)[e];
+        bad |= (x & kInf) == kInf || (x >> 16 & kInf) == kInf;
+      }
+    }
+    return bad;
+  }
+  __device__ __forceinline__ void drop_values_from(int n) {
+    for (int i = warp * 32 + lane; i < Room<W>::operand / 16; i += 32 * kWarps)
+      if (place(i / 8 % kTile) >= n) *reinterpret_cast<uint4*>(room + Room<W>::v + i * 16) = make_uint4(0, 0, 0, 0);
+    to_products();
+  }
+
+  // The keys times scale_add gamma^(n - 1 - place + late), as a sum of terms; the weight is 0 behind the tile.
+  // Returns what the terms have to be multiplied by through `down`.
+  __device__ __forceinline__ bool weigh_keys(int n, int n_terms, float& down) {
+    constexpr int kChunks = Room<W>::operand / 16 / (32 * kWarps);
+    uint4 u[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+      u[i] = *reinterpret_cast<const uint4*>(room + Room<W>::k + (i * 32 * kWarps + warp * 32 + lane) * 16);
+    float scale = ps.scale_add;
+    down = 1.f;
     if (DT == TBE_F16) {
-      // the largest key of this warp's rows, decayed or not
       __half2 top = __half2half2(__ushort_as_half(0));
-      for (int ks = k0; ks < k1; ++ks)
 #pragma unroll
-        for (int m = 0; m < D::MT; ++m) {
-          uint32_t r[4];
-          ldsm_t(r, keys + (ks * 16 * D::LK + m * 16) * 2);
+      for (int i = 0; i < kChunks; ++i) {
+        const int r = (i * 32 * kWarps + warp * 32 + lane) / 8 % kTile;
+        if (place(r) < n) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&r[e])));
+          for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(reinterpret_cast<const __half2*>(&u[i])[e]));
         }
+      }
       const float2 t = __half22float2(top);
       float most = fmaxf(t.x, t.y) * fabsf(scale);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
-      up = room_for(most);
+      if (!largest(most)) return false;
+      const int up = room_for(most);
+      scale *= pow2(up);
+      down = pow2(-up);
     }
-    const float down = DT == TBE_F16 ? pow2(-up) : 1.f;
-    // (not EXACT: the sum itself is moved, and moved back)
-    const float by = sh.pow[b - a] * (DT == TBE_F16 && !EXACT ? pow2(up) : 1.f);
-    each(lane, [&](float& x, int, int) { x *= by; });
-    const float weigh = scale * (DT == TBE_F16 ? pow2(up) : 1.f);
-    const bool cut = (a | b) & 15;  // some step of 16 has rows of others
-    for (int ks = k0; ks < k1; ++ks) {
-      // weights of the four tokens whose keys and values this lane holds
-      float w[4];
-      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-      const int t0 = ks * 16 + lane % 4 * 2;
-      if (cut) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int t = t0 + h * 8;
-          const bool in0 = t >= a && t < b, in1 = t + 1 >= a && t + 1 < b;
-          w[2 * h] = in0 ? sh.pow[b - 1 - t + late] * weigh : 0.f;
-          w[2 * h + 1] = in1 ? sh.pow[b - 2 - t + late] * weigh : 0.f;
-          keep[h] = (in0 ? 0xffffu : 0u) | (in1 ? 0xffff0000u : 0u);
+    for (int i = 0; i < kChunks; ++i) {
+      const int at = (i * 32 * kWarps + warp * 32 + lane) * 16, far = place(at / 128 % kTile);
+      const bool in = far < n;
+      const float w = in ? c.pow[n - 1 - far + ps.back] * scale : 0.f;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 y = unpack2<DT>((&u[i].x)[e]);
+        x[2 * e] = in ? y.x * w : 0.f;
+        x[2 * e + 1] = in ? y.y * w : 0.f;
+      }
+      for (int t = 0; t < n_terms; ++t) {
+        uint4 r;
+        if (DT == TBE_BF16 && t < n_terms - 1) {  // cut off: the upper halves of the numbers
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            (&r.x)[e] = __byte_perm(__float_as_uint(x[2 * e]), __float_as_uint(x[2 * e + 1]), 0x7632);
+            x[2 * e] -= __uint_as_float(__float_as_uint(x[2 * e]) & 0xffff0000u);
+            x[2 * e + 1] -= __uint_as_float(__float_as_uint(x[2 * e + 1]) & 0xffff0000u);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            (&r.x)[e] = pack2<DT>(x[2 * e], x[2 * e + 1]);
+            const float2 y = unpack2<DT>((&r.x)[e]);
+            x[2 * e] -= y.x;
+            x[2 * e + 1] -= y.y;
+          }
         }
+        *reinterpret_cast<uint4*>(terms + t * Room<W>::operand + at) = r;
+      }
+    }
+    to_products();
+    arrive(&c.keys);
+    return true;
+  }
+
+  // S = gamma^n S + the tile's sum.
+  __device__ __forceinline__ void add(int n, float down) {
+    const float by = c.pow[n];
+    if (quarter * 32 < W) {
+#pragma unroll
+      for (int j = 0; j < kCols; j += 32) {
+        float x[32];
+        tc_ld32(tmem + Room<W>::ta + half * kCols + j + lanes(), x);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[j + e] = fmaf(s[j + e], by, DT == TBE_F16 ? x[e] * down : x[e]);
+      }
+    }
+    tc_before_sync();
+    arrive(&c.add_read);
+  }
+
+  // The products of row `row` with 64 of the columns, weighted, to TMEM in
+  // 16 bits.  fp16: multiplied by 2^up, up by row.
+  __device__ __forceinline__ bool weigh_products(const Tile& t, int n, uint32_t turn, int& up) {
+    const int far = place(row);
+    int from = 0;  // first place of this row's sequence
+    const bool whole = t.e0 >= n;
+    if (!whole) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t u = far >= w * 32 + 31 ? t.starts[w] : far >= w * 32 ? t.starts[w] & ((2u << (far - w * 32)) - 1) : 0u;
+        if (u) from = w * 32 + 31 - __clz((int)u);
+      }
+    }
+    uint32_t packed[2][16];
+    float top = 0.f;
+    float x[2][32];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int chunk = half * 2 + i;
+      const int sooner = ps.back ? chunk - quarter : quarter - chunk;  // all of it before this warp's rows, or behind
+      if (sooner < 0) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[i][e] = 0.f;
       } else {
-        const float* pw = sh.pow + (b - 1 - t0 + late);
-        w[0] = pw[0] * weigh;
-        w[1] = pw[-1] * weigh;
-        w[2] = pw[-8] * weigh;
-        w[3] = pw[-9] * weigh;
-      }
-      constexpr int kTerms = DT == TBE_BF16 && EXACT ? 3 : 2;
-      uint32_t f[D::MT][kTerms][4];
+        tc_ld32(tmem + Room<W>::tp + chunk * 32 + lanes(), x[i]);
+        tc_wait_ld();
+        if (sooner > 0) {
+          // gamma^distance in two parts: to the chunk's near end, and inside it
+          const float by = c.pow[ps.back ? chunk * 32 - row : row - chunk * 32 - 31] * ps.scale_tile;
 #pragma unroll
-      for (int m = 0; m < D::MT; ++m) {
-        uint32_t r[4];
-        ldsm_t(r, keys + (ks * 16 * D::LK + m * 16) * 2);
+          for (int e = 0; e < 32; e += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(c.by_col + e);
+            x[i][e] *= by * w.x;
+            x[i][e + 1] *= by * w.y;
+            x[i][e + 2] *= by * w.z;
+            x[i][e + 3] *= by * w.w;
+          }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // (what stands in rows of other sequences is left out before it is multiplied)
-          float2 x = unpack2<DT>(r[e] & keep[e >> 1]);
-          x.x *= w[e >> 1 << 1];
-          x.y *= w[(e >> 1 << 1) + 1];
-#pragma unroll
-          for (int t = 0; t < kTerms; ++t) {
-            if (DT == TBE_BF16 && t < kTerms - 1) {  // cut off: its two halves are the numbers' upper ones
-              f[m][t][e] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
-              x.x -= __uint_as_float(__float_as_uint(x.x) & 0xffff0000u);
-              x.y -= __uint_as_float(__float_as_uint(x.y) & 0xffff0000u);
-            } else {
-              f[m][t][e] = pack2<DT>(x.x, x.y);
-              if (t < kTerms - 1) {
-                const float2 y = unpack2<DT>(f[m][t][e]);
-                x.x -= y.x;
-                x.y -= y.y;
-              }
-            }
+          for (int e = 0; e < 32; ++e) {
+            const int away = ps.back ? e - lane : lane - e;
+            x[i][e] = away >= 0 ? x[i][e] * (c.pow[away & 31] * ps.scale_tile) : 0.f;
           }
         }
-      }
+        if (!whole) {
 #pragma unroll
-      for (int n = 0; n < D::NT; n += 2) {
-        uint32_t r[4];
-        ldsm_t(r, values + (ks * 16 * D::LV + n * 8) * 2);
-        if (cut) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) r[e] &= keep[e & 1];
+          for (int e = 0; e < 32; ++e)
+            if (place(chunk * 32 + e) < from) x[i][e] = 0.f;
         }
+      }
+      if (DT == TBE_F16) {
 #pragma unroll
-        for (int m = 0; m < D::MT; ++m)
+        for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[i][e]));
+      } else {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (EXACT) {
-              // added up apart: the tensor cores cut sums off, which a long sum would feel
-              float c[4];
-              mma_first<DT>(c, f[m][kTerms - 1], r[2 * u], r[2 * u + 1]);
-#pragma unroll
-              for (int t = kTerms - 2; t >= 0; --t) mma<DT>(c, f[m][t], r[2 * u], r[2 * u + 1]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) s[m][n + u][e] = DT == TBE_F16 ? fmaf(c[e], down, s[m][n + u][e]) : s[m][n + u][e] + c[e];
-            } else {
-#pragma unroll
-              for (int t = kTerms - 1; t >= 0; --t) mma<DT>(s[m][n + u], f[m][t], r[2 * u], r[2 * u + 1]);
-            }
-          }
+        for (int e = 0; e < 16; ++e) packed[i][e] = pack2<DT>(x[i][2 * e], x[i][2 * e + 1]);
       }
     }
-    if (DT == TBE_F16 && !EXACT) each(lane, [&](float& x, int, int) { x *= down; });
+    up = 0;
+    if (DT == TBE_F16) {
+      c.top_row[half][row] = top;
+      tc_before_sync();
+      arrive(&c.row_max[quarter]);
+      if (!wait(&c.row_max[quarter], turn, c)) return false;
+      up = room_for(fmaxf(top, *(volatile float*)&c.top_row[half ^ 1][row]));
+      const float f = pow2(up);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) packed[i][e] = pack2<DT>(x[i][2 * e] * f, x[i][2 * e + 1] * f);
+    } else {
+      tc_before_sync();
+      arrive(&c.row_max[quarter]);
+      if (!wait(&c.row_max[quarter], turn, c)) return false;
+    }
+    tc_after_sync();  // both halves of this row's columns have been read
+#pragma unroll
+    for (int i = 0; i < 2; ++i) tc_st16(tmem + Room<W>::tp + (half * 2 + i) * 16 + lanes(), packed[i]);
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    tc_before_sync();
+    arrive(&c.weighted);
+    return true;
+  }
+
+  // o = the tile's part and the state's, rounded once.
+  __device__ __forceinline__ void write_outputs(const Tile& t, int n, int up) {
+    const int far = place(row);
+    const bool live = t.live && far < t.e0;
+    const float of_state = live ? c.pow[far + 1 - ps.back] * read_scale : 0.f, of_tile = DT == TBE_F16 ? pow2(-up) : 1.f;
+    const int64_t token = ps.back ? a.N - t.p - kTile + row : t.p + row;
+    uint16_t* to = ps.o + token * ps.so + head * ps.ho + half * kCols;
+#pragma unroll
+    for (int j = 0; j < kCols; j += 32) {
+      float x[32];
+      tc_ld32(tmem + Room<W>::to + half * kCols + j + lanes(), x);
+      tc_wait_ld();
+      if (DT == TBE_F16) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] *= of_tile;
+      }
+      if (t.live) {
+        float y[32];
+        tc_ld32(tmem + Room<W>::ts + half * kCols + j + lanes(), y);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = live ? fmaf(y[e], of_state, x[e]) : x[e];
+      }
+      if (j + 32 >= kCols) {
+        tc_before_sync();
+        arrive(&c.out_read);
+      }
+      const int cols = a.d - half * kCols - j;
+      if (far >= n || cols <= 0) continue;
+      uint32_t u[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) u[e] = pack2<DT>(x[2 * e], x[2 * e + 1]);
+      if (cols >= 32 && ps.piece_o == 32) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 8)
+          asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + j + 2 * e), "r"(u[e]), "r"(u[e + 1]),
+                       "r"(u[e + 2]), "r"(u[e + 3]), "r"(u[e + 4]), "r"(u[e + 5]), "r"(u[e + 6]), "r"(u[e + 7])
+                       : "memory");
+      } else if (ps.piece_o >= 8) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 2)
+          if (2 * e < cols) *reinterpret_cast<uint2*>(to + j + 2 * e) = make_uint2(u[e], u[e + 1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (2 * e < cols) to[j + 2 * e] = (uint16_t)u[e];
+          if (2 * e + 1 < cols) to[j + 2 * e + 1] = (uint16_t)(u[e] >> 16);
+        }
+      }
+    }
   }
 };
 
-// ---------------------------------------------------------------------------
-// where sequences start in a tile
-// ---------------------------------------------------------------------------
+// Blocks of an SM: what their registers, shared memory and TMEM leave room for.
+template <int W>
+constexpr int kBlocks = W == 64 ? 2 : 1;
 
-// A tile's sequences.
-struct Marks {
-  unsigned long long starts;  // places where one starts
-  int n;                      // places taken
-  bool closes;                // a sequence ends at its end
-};
-// Notes the starts below p + n, n at most kTile, in shared memory, and moves
-// `next`, the first start not yet passed (at next_at), on.  Where the tile
-// need not reach its end (`may_cut`) and its last sequence neither ends there
-// nor fills it, the tile ends where that sequence starts: short sequences are
-// then never cut, and need no state.  All threads call it.
-template <int DK>
-__device__ __forceinline__ Marks mark_starts(Shared<DK>& sh, const Starts& st, int64_t p, int n, bool may_cut, int64_t& next,
-                                             int64_t& next_at) {
-  Marks m = {0, n, false};
-  if (next_at >= p + n) {  // none
-    m.closes = next_at == p + n;
-    return m;
-  }
-  if (threadIdx.x == 0) {
-    sh.starts = 0;
-    sh.closes = 0;
-  }
-  if (threadIdx.x < kTile) sh.sequence[threadIdx.x] = -1;
-  __syncthreads();
-  const int64_t before = next;
-  int64_t i, x;
-  int c;
-  for (;;) {
-    i = next + threadIdx.x;
-    x = i <= st.S ? st.at(i) : INT64_MAX;
-    const bool below = x < p + n;
-    if (below && x >= p && i < st.S) {
-      atomicOr(&sh.starts, 1ull << (x - p));
-      atomicMax(&sh.sequence[x - p], (int32_t)i);  // empty sequences start there too: the last one has the tokens
-    }
-    if (x == p + n) sh.closes = 1;
-    c = __syncthreads_count(below);
-    if (c < kThreads) break;
-    next += c;
-  }
-  m.starts = sh.starts;
-  m.closes = sh.closes != 0;
-  const int last = m.starts ? 63 - __clzll((long long)m.starts) : 0;
-  if (may_cut && !m.closes && last > 0) {
-    m.n = last;
-    m.starts &= ~(1ull << last);
-    m.closes = true;
-    c = __syncthreads_count(x < p + last);
-    if (c == 0 && next > before) {  // (more empty sequences than threads: back to the first that starts there)
-      next = st.first_from(p + last, before, next);
-      next_at = p + last;
-      return m;
-    }
-  }
-  if (threadIdx.x == c) sh.next_at = x;  // the first that is not below
-  next += c;
-  __syncthreads();
-  next_at = sh.next_at;
-  return m;
-}
-
-// ---------------------------------------------------------------------------
-// what runs leave
-// ---------------------------------------------------------------------------
-
-template <int DT, int DK>
-__global__ void __launch_bounds__(kThreads) carry_kernel(const __grid_constant__ Args a) {
-  using D = Shape<DK>;
-  extern __shared__ __align__(16) uint8_t raw[];
-  Shared<DK>& sh = *reinterpret_cast<Shared<DK>*>(raw);
+template <int DT, int W, bool SUMS>
+__global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const __grid_constant__ Args a) {
+  using R = Room<W>;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  uint8_t* room = raw + a.terms * R::operand;
   const Pass& ps = a.pass[blockIdx.y];
+  const int terms = DT == TBE_BF16 && ps.out ? 3 : 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int part = blockIdx.x % a.parts, head = blockIdx.x / a.parts % a.H, run = blockIdx.x / (a.parts * a.H);
-  const int64_t p0 = (int64_t)run * a.tiles * kTile, p1 = p0 + (int64_t)a.tiles * kTile;  // (the last run is not asked)
+  const int head = blockIdx.x % a.H, run = blockIdx.x / a.H;
+  const int64_t p0 = (int64_t)run * a.run, p1 = min(a.N, p0 + a.run);
   const Starts st = {a.offsets, a.N, a.S, ps.back != 0};
-  const int64_t next = st.first(p1);  // first start at or behind the run's end
-  const bool goes_on = next <= a.S && st.at(next) > p1 && next > 0;
-  const int64_t begin = goes_on ? st.at(next - 1) : p1;
-  const int32_t kind = !goes_on ? kNothing : begin >= p0 ? kBegan : kThrough;
-  if (threadIdx.x == 0 && part == 0 && head == 0) ps.kind[run] = kind;
-  if (kind == kNothing) return;
-  const float decay = a.decay[head];
-  for (int k = threadIdx.x; k < kPowers; k += kThreads) sh.pow[k] = power(decay, k);
-  State<DT, DK> state;
-  state.place(warp);
-  if (kind == kBegan && ps.in)
-    state.read(ps.in + ((int64_t)st.sequence(next - 1) * a.H + head) * a.d * a.d, a.d, part * D::DV, ps.in_turned, lane);
-  else state.clear();
-  const int64_t from = max(begin, p0);
-  for (int64_t p = from / kTile * kTile; p < p1; p += kTile) {
-    __syncthreads();
-    load_rows<DK, D::LK>(sh.k, ps.k + head * ps.hk, ps.sk, p, kTile, a.d, a.N, ps.back, ps.piece);
-    load_rows<D::DV, D::LV>(sh.v, ps.v + head * ps.hv + part * D::DV, ps.sv, p, kTile, a.d - part * D::DV, a.N, ps.back,
-                            ps.piece);
-    cp_commit();
-    cp_wait<0>();
-    __syncthreads();
-    const int a0 = (int)max(from - p, (int64_t)0);
-    if (ps.out) state.template add<true>(sh, a0, kTile, ps.back, ps.scale_add, lane);
-    else state.template add<false>(sh, a0, kTile, ps.back, ps.scale_add, lane);
+  Control& c = *reinterpret_cast<Control*>(room + R::rest);
+
+  // what a run leaves is asked of all but the last
+  int64_t begin = p0;
+  bool began = false;
+  int64_t sequence = 0;
+  if (SUMS) {
+    const int64_t next = st.first(p1);  // first start at or behind the run's end
+    const bool goes_on = next > 0 && next <= a.S && st.at(next) > p1;
+    begin = goes_on ? st.at(next - 1) : p1;
+    const int32_t kind = !goes_on ? kNothing : begin >= p0 ? kBegan : kThrough;
+    if (threadIdx.x == 0 && head == 0) ps.kind[run] = kind;
+    if (kind == kNothing) return;
+    began = kind == kBegan;
+    begin = max(begin, p0);
+    sequence = st.sequence(next - 1);
   }
-  float* out = ps.carry + ((int64_t)head * a.runs + run) * DK * DK;
-  state.each(lane, [&](float& x, int i, int j) { out[i * DK + part * D::DV + j] = x; });
+
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < 2; ++k) bar_init(&c.known[k], 1);
+    bar_init(&c.full, a.piece ? kWarps : 1);
+    bar_init(&c.products, 1);
+    bar_init(&c.weighted, kWarps);
+    bar_init(&c.keys, kWarps);
+    bar_init(&c.out_done, 1);
+    bar_init(&c.add_done, 1);
+    bar_init(&c.add_read, kWarps);
+    bar_init(&c.out_read, kWarps);
+    bar_init(&c.state_ready, kWarps);
+    bar_init(&c.exchange, kWarps);
+    for (int k = 0; k < 4; ++k) bar_init(&c.row_max[k], 2);
+    for (int k = 0; k < 3; ++k) c.top[k] = 0;
+    c.bad[0] = c.bad[1] = 0;
+    c.dead = 0;
+    bars_visible();
+  }
+  const float decay = a.decay[head];
+  for (int k = threadIdx.x; k < kPowers; k += kThreads) c.pow[k] = power(decay, k);
+  if (threadIdx.x < 32) c.by_col[threadIdx.x] = power(decay, ps.back ? threadIdx.x : 31 - threadIdx.x);
+  if (warp == kWarps) tc_alloc(&c.tmem, R::cols);
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  const uint32_t tmem = c.tmem;
+  wait_predecessor();
+  if (!SUMS && blockIdx.x == 0 && blockIdx.y == 0) {  // broken offsets are reported
+    bool bad = false;
+    for (int64_t i = threadIdx.x; i < a.S; i += kThreads) bad |= a.offsets.ldg(i) > a.offsets.ldg(i + 1);
+    if (threadIdx.x == 0) bad |= a.offsets.ldg(0) != 0 || a.offsets.ldg(a.S) != a.N;
+    if (bad) report(a.status, TBE_DEV_BAD_OFFSETS);
+  }
+
+  if (warp == kWarps) {
+    // finds the tiles, starts the copies, issues the products
+    Marker m = {st, ps.in != nullptr || ps.out != nullptr, 0, 0};
+    if (!SUMS) m.seek(p0, lane);
+    bool live = !SUMS && run > 0 && __shfl_sync(kFull, m.x, 0) > p0;  // (m.x of lane 0: the first start)
+    int64_t p = begin;
+    uint32_t states = 0, adds = 0, copies = 0;
+    bool added = false;  // by the tile before
+    const uint32_t room0 = smem_u32(room), terms0 = smem_u32(raw);
+    const uint32_t format = DT == TBE_BF16;
+    for (uint32_t i = 0;; ++i) {
+      Tile t = {};
+      if (p >= p1) t.p = -1;
+      else if (SUMS) {
+        t.p = p;
+        t.n = (int)min((int64_t)kTile, p1 - p);
+        t.e0 = t.n;
+        t.adds = 1;
+        t.mixed = t.n < kTile;
+      } else {
+        m.mark(t, p, p1, live, ps.in != nullptr, ps.out != nullptr, lane);
+      }
+      // (the products and copies of the tile before are through)
+      if (lane == 0) {
+        c.tile[i & 1] = t;
+        c.bad[i & 1] = 0;
+        bar_arrive(&c.known[i & 1]);
+        if (t.p >= 0 && a.piece == 0) {
+          bar_expect(&c.full, (SUMS ? 2 : 3) * R::operand);
+          const int32_t first = (int32_t)(ps.back ? a.N - t.p - kTile : t.p);
+#pragma unroll
+          for (int b = 0; b < W / 64; ++b) {
+            tma_load3(room0 + R::k + b * kBlock, &a.map[ps.mk], b * 64, head, first, &c.full);
+            if (!SUMS) tma_load3(room0 + R::q + b * kBlock, &a.map[ps.mq], b * 64, head, first, &c.full);
+            tma_load3(room0 + R::v + b * kBlock, &a.map[ps.mv], b * 64, head, first, &c.full);
+          }
+        }
+      }
+      __syncwarp();
+      if (t.p < 0) break;
+      copies += a.piece == 0;
+      if (!wait(&c.full, i, c)) break;
+      // the sum for the state lies where these products go (64 columns), or has its own place
+      if (added && !wait(&c.add_read, adds - 1, c)) break;
+      tc_after_sync();
+      if (!SUMS) {
+        if (lane == 0) {
+          const uint32_t idesc = tc_idesc(format, 0, 0, kTile, kTile);
+#pragma unroll
+          for (int k = 0; k < W / 16; ++k)
+            tc_mma(tmem + R::tp, tc_desc(room0 + R::q + k / 4 * kBlock + k % 4 * 32),
+                   tc_desc(room0 + R::k + k / 4 * kBlock + k % 4 * 32), idesc, k > 0);
+          tc_commit(&c.products);
+        }
+        __syncwarp();
+        if (i > 0 && !wait(&c.out_read, i - 1, c)) break;
+        if (t.live) {
+          if (!wait(&c.state_ready, states++, c)) break;
+          tc_after_sync();
+          if (lane == 0) {
+            const uint32_t idesc = tc_idesc(format, 0, 1, kTile, W);
+#pragma unroll
+            for (int k = 0; k < W / 16; ++k)
+              tc_mma(tmem + R::ts, tc_desc(room0 + R::q + k / 4 * kBlock + k % 4 * 32), desc_of(room0 + R::s + k * 2048, W * 128),
+                     idesc, k > 0);
+          }
+          __syncwarp();
+        }
+        if (!wait(&c.weighted, i, c)) break;
+        tc_after_sync();
+        if (lane == 0) {
+          const uint32_t idesc = tc_idesc(format, 0, 1, kTile, W);
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            tc_mma_tmem(tmem + R::to, tmem + R::tp + k * 8, desc_of(room0 + R::v + k * 2048, kBlock), idesc, k > 0);
+          tc_commit(&c.out_done);
+        }
+        __syncwarp();
+      }
+      if (t.adds) {
+        if (!wait(&c.keys, adds, c)) break;
+        tc_after_sync();
+        if (lane == 0) {
+          // (64 columns: the products' other 64 rows, of what follows in memory, are not looked at)
+          const uint32_t idesc = tc_idesc(format, 1, 1, kTile, W);
+          for (int x = terms - 1; x >= 0; --x)
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              tc_mma(tmem + R::ta, desc_of(terms0 + x * R::operand + k * 2048, kBlock),
+                     desc_of(room0 + R::v + k * 2048, kBlock), idesc, x < terms - 1 || k > 0);
+          tc_commit(&c.add_done);
+        }
+        __syncwarp();
+        ++adds;
+      }
+      added = t.adds;
+      int n = t.n;
+      if (!SUMS && t.mixed && *(volatile int32_t*)&c.bad[i & 1] && t.e0 < n) {
+        n = t.e0;  // the others were told so by the same word
+        m.seek(t.p + n, lane);
+      }
+      live = t.leaves;
+      p = t.p + n;
+      if (!SUMS && !wait(&c.out_done, i, c)) break;
+      if (t.adds && !wait(&c.add_done, adds - 1, c)) break;
+    }
+    // (after a wait that gave up, copies in flight have time to land)
+    if (*(volatile int32_t*)&c.dead && copies) mbar_wait(&c.full, (copies - 1) & 1, 1 << 16);
+  } else {
+    Worker<DT, W, SUMS> w = {a, ps, c, raw, room, tmem, warp, lane, warp & 3, warp >> 2, (warp & 3) * 32 + lane, head};
+#pragma unroll
+    for (int j = 0; j < w.kCols; ++j) w.s[j] = 0.f;
+    const float* carried = ps.carry + ((int64_t)head * a.runs + run - 1) * W * W;
+    const int64_t matrix = (int64_t)a.d * a.d;
+    if (SUMS && began && ps.in) w.read(ps.in + (sequence * a.H + head) * matrix, a.d, ps.in_turned);
+    uint32_t adds = 0;
+    for (uint32_t i = 0;; ++i) {
+      if (!wait(&c.known[i & 1], i >> 1, c)) break;
+      const Tile& t = c.tile[i & 1];
+      if (t.p < 0) break;
+      if (a.piece) {
+        const int64_t first = ps.back ? a.N - t.p - kTile : t.p;
+        const int thread = warp * 32 + lane;
+        load_rows<W>(room + R::k, ps.k + head * ps.hk, ps.sk, first, a.N, a.d, a.piece, thread);
+        if (!SUMS) load_rows<W>(room + R::q, ps.q + head * ps.hq, ps.sq, first, a.N, a.d, a.piece, thread);
+        load_rows<W>(room + R::v, ps.v + head * ps.hv, ps.sv, first, a.N, a.d, a.piece, thread);
+        to_products();
+        w.arrive(&c.full);
+      }
+      if (!SUMS) {
+        if (t.begins) {
+          if (ps.in) w.read(ps.in + (t.sequence * a.H + head) * matrix, a.d, ps.in_turned);
+          else {
+#pragma unroll
+            for (int j = 0; j < w.kCols; ++j) w.s[j] = 0.f;
+          }
+        } else if (i == 0 && t.live) {
+#pragma unroll
+          for (int j = 0; j < w.kCols; ++j) w.s[j] = w.holds() ? __ldcg(carried + (int64_t)w.row * W + w.half * w.kCols + j) : 0.f;
+        }
+        if (t.live && (t.begins || i == 0) && !w.publish()) break;
+      }
+      int n = t.n;
+      if (t.mixed || t.adds) {
+        if (!wait(&c.full, i, c)) break;
+      }
+      if (t.mixed) {
+        if (__any_sync(kFull, w.not_finite()) && lane == 0) c.bad[i & 1] = 1;
+        if (!w.meet()) break;
+        if (*(volatile int32_t*)&c.bad[i & 1]) {
+          n = min(n, t.e0);
+          w.drop_values_from(n);
+        }
+      }
+      float down = 1.f;
+      if (t.adds && !w.weigh_keys(n, terms, down)) break;
+      int up = 0;
+      if (!SUMS) {
+        if (!wait(&c.products, i, c)) break;
+        tc_after_sync();
+        if (!w.weigh_products(t, n, i, up)) break;
+      }
+      if (t.adds) {
+        if (!wait(&c.add_done, adds++, c)) break;
+        tc_after_sync();
+        w.add(n, down);
+        if (t.leaves) {
+          if (!w.publish()) break;
+        } else if (!SUMS) {
+          w.write(ps.out + (t.sequence * a.H + head) * matrix, a.d);
+        }
+      }
+      if (!SUMS) {
+        if (!wait(&c.out_done, i, c)) break;
+        tc_after_sync();
+        w.write_outputs(t, n, up);
+      }
+    }
+    if (SUMS && w.holds()) w.write(ps.carry + ((int64_t)head * a.runs + run) * W * W, W);
+  }
+  __syncwarp();
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  if (threadIdx.x == 0 && c.dead) report(a.status, TBE_DEV_TIMEOUT);
+  if (warp == kWarps) tc_free(tmem, R::cols);
 }
 
 // carry[run] = what run `run` leaves, with what came through it.
-template <int DK>
+template <int W>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
   wait_predecessor();
   const Pass& ps = a.pass[blockIdx.y];
-  constexpr int kPerHead = DK * DK / 256;
+  constexpr int kPerHead = W * W / 256;
   const int head = blockIdx.x / kPerHead, at = blockIdx.x % kPerHead * 256 + threadIdx.x;
-  const float through = power(a.decay[head], (int64_t)a.tiles * kTile);
-  float* c = ps.carry + (int64_t)head * a.runs * DK * DK + at;
+  const float through = power(a.decay[head], a.run);
+  float* c = ps.carry + (int64_t)head * a.runs * W * W + at;
   float s = 0.f;
   constexpr int kAhead = 16;
   for (int r = 0; r < a.runs - 1; r += kAhead) {
@@ -547,352 +947,18 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     for (int k = 0; k < kAhead; ++k) {  // (what is not there to be read is not used either)
       const int at_run = min(r + k, a.runs - 2);
       kind[k] = __ldcg(ps.kind + at_run);
-      x[k] = __ldcg(c + (int64_t)at_run * DK * DK);
+      x[k] = __ldcg(c + (int64_t)at_run * W * W);
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       if (r + k >= a.runs - 1) break;
       if (kind[k] == kThrough) {
         s = fmaf(through, s, x[k]);
-        c[(int64_t)(r + k) * DK * DK] = s;
+        c[(int64_t)(r + k) * W * W] = s;
       } else {
         s = x[k];
       }
     }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// the outputs
-// ---------------------------------------------------------------------------
-
-// Resident blocks of an SM.
-template <int DK>
-constexpr int kBlocks = DK == 128 ? 3 : 4;
-
-// Whether any of the tile's values is an infinity or a NaN.
-template <int DT, int DK>
-__device__ __forceinline__ bool not_finite(const Shared<DK>& sh) {
-  using D = Shape<DK>;
-  constexpr uint32_t kInf = DT == TBE_BF16 ? 0x7f80u : 0x7c00u;
-  bool bad = false;
-  for (int i = threadIdx.x; i < kTile * D::DV / 8; i += kThreads) {
-    const uint4 u = *reinterpret_cast<const uint4*>(sh.v + i / (D::DV / 8) * D::LV + i % (D::DV / 8) * 8);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t x = (&u.x)[e];
-      bad |= (x & kInf) == kInf || (x >> 16 & kInf) == kInf;
-    }
-  }
-  return bad;
-}
-
-template <int DT, int DK>
-__global__ void __launch_bounds__(kThreads, kBlocks<DK>) output_kernel(const __grid_constant__ Args a) {
-  using D = Shape<DK>;
-  extern __shared__ __align__(16) uint8_t raw[];
-  Shared<DK>& sh = *reinterpret_cast<Shared<DK>*>(raw);
-  const Pass& ps = a.pass[blockIdx.y];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int part = blockIdx.x % a.parts, head = blockIdx.x / a.parts % a.H, run = blockIdx.x / (a.parts * a.H);
-  const int64_t p0 = (int64_t)run * a.tiles * kTile, p1 = min(a.N, p0 + (int64_t)a.tiles * kTile);
-  const Starts st = {a.offsets, a.N, a.S, ps.back != 0};
-  const int first_col = part * D::DV;
-  const int late = ps.back;
-  wait_predecessor();
-  if (blockIdx.x == 0 && blockIdx.y == 0) {  // broken offsets are reported
-    bool bad = false;
-    for (int64_t i = threadIdx.x; i < a.S; i += kThreads) bad |= a.offsets.ldg(i) > a.offsets.ldg(i + 1);
-    if (threadIdx.x == 0) bad |= a.offsets.ldg(0) != 0 || a.offsets.ldg(a.S) != a.N;
-    if (bad) report(a.status, TBE_DEV_BAD_OFFSETS);
-  }
-  const float decay = a.decay[head];
-  for (int k = threadIdx.x; k < kPowers; k += kThreads) sh.pow[k] = power(decay, k);
-  if (threadIdx.x < 3) sh.top[threadIdx.x] = 0;
-  int64_t next = st.first(p0);
-  int64_t next_at = next <= a.S ? st.at(next) : INT64_MAX;
-
-  State<DT, DK> state;
-  state.place(warp);
-  state.clear();
-  bool live = false;      // there is a state, in registers and in shared memory
-  uint32_t turn = 0;      // of sh.top
-  float read_scale = 0.f; // what the state in shared memory is to be multiplied by
-  // All threads: the state's registers to shared memory (after a barrier
-  // behind which nobody reads the old one; a barrier must follow).
-  auto note_top = [&] {
-    if (DT == TBE_F16) {
-      float t = state.largest();
-#pragma unroll
-      for (int o = 16; o; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, o));
-      if (lane == 0) atomicMax(&sh.top[turn % 3], __float_as_uint(t));
-    }
-  };
-  auto publish = [&] {
-    int up = 0;
-    if (DT == TBE_F16) {
-      up = room_for(__uint_as_float(sh.top[turn % 3]));
-      if (threadIdx.x == 0) sh.top[(turn + 2) % 3] = 0;
-      ++turn;
-    }
-    state.publish(sh, lane, up);
-    read_scale = ps.scale_read * (DT == TBE_F16 ? pow2(-up) : 1.f);
-  };
-  __syncthreads();
-  if (next_at > p0 && run > 0) {
-    const float* c = ps.carry + ((int64_t)head * a.runs + run - 1) * DK * DK;
-    state.each(lane, [&](float& x, int i, int j) { x = __ldcg(c + i * DK + first_col + j); });
-    live = true;
-    note_top();
-    __syncthreads();
-    publish();
-  }
-
-  const uint32_t queries = smem_u32(sh.q) + ((warp * 16 + lane % 16) * D::LK + lane / 16 * 8) * 2;
-  const uint32_t keys = smem_u32(sh.k) + ((lane % 8 + lane / 16 * 8) * D::LK + lane / 8 % 2 * 8) * 2;
-  const uint32_t values = smem_u32(sh.v) + ((lane % 8 + lane / 8 % 2 * 8) * D::LV + lane / 16 * 8) * 2;
-  const uint32_t stored = smem_u32(sh.s) + ((lane % 8 + lane / 8 % 2 * 8) * D::LV + lane / 16 * 8) * 2;
-  const int row0 = warp * 16 + lane / 4;  // this lane's rows are row0 and row0 + 8
-
-  // what the products of a row and a column of another 16 are multiplied by has a part for each
-  float by_col[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) by_col[e] = sh.pow[15 - (lane % 4 * 2 + (e & 1) + (e >> 1) * 8)] * ps.scale_tile;
-
-  for (int64_t p = p0; p < p1;) {
-    const int most = (int)min((int64_t)kTile, p1 - p);
-    const int64_t came = next - 1;  // the sequence that comes in, where there is one
-    load_rows<DK, D::LK>(sh.q, ps.q + head * ps.hq, ps.sq, p, most, a.d, a.N, ps.back, ps.piece);
-    load_rows<DK, D::LK>(sh.k, ps.k + head * ps.hk, ps.sk, p, most, a.d, a.N, ps.back, ps.piece);
-    load_rows<D::DV, D::LV>(sh.v, ps.v + head * ps.hv + first_col, ps.sv, p, most, a.d - first_col, a.N, ps.back, ps.piece);
-    cp_commit();
-    const Marks mk = mark_starts(sh, st, p, most, p + most < p1, next, next_at);
-    const unsigned long long starts = mk.starts;
-    const int n = mk.n;
-    const bool closes = mk.closes, last_tile = p + n >= p1;
-    const bool whole = (starts & ~1ull) == 0;  // one sequence has all of the tile
-    cp_wait<0>();
-    __syncthreads();
-
-    float o[D::NO][4];
-#pragma unroll
-    for (int j = 0; j < D::NO; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    uint32_t qf[D::KS][4];
-#pragma unroll
-    for (int k = 0; k < D::KS; ++k) ldsm(qf[k], queries + k * 32);
-
-    // the state's part, sequence by sequence
-    for (int at = 0; at < n;) {
-      const bool begins = starts >> at & 1;
-      const unsigned long long later = at < 63 ? starts >> (at + 1) << (at + 1) : 0;
-      const int end = later ? __ffsll((long long)later) - 1 : n;
-      const int64_t which = begins ? sh.sequence[at] : came;
-      const bool known = which >= 0 && which < a.S;  // (always, unless offsets are broken)
-      const bool ends = end < n || closes;
-      const int64_t matrix = ((int64_t)st.sequence(which) * a.H + head) * a.d * a.d;
-      if (begins) {
-        live = ps.in != nullptr;
-        if (live) {
-          state.read(ps.in + matrix, a.d, first_col, ps.in_turned, lane);
-          note_top();
-          __syncthreads();  // the state before it has been read
-          publish();
-          __syncthreads();
-        } else {
-          state.clear();
-        }
-      }
-      if (live) {
-        float f[2];
-        bool mine[2];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int row = row0 + half * 8;
-          mine[half] = row >= at && row < end;
-          f[half] = mine[half] ? sh.pow[row - at + 1 - late] * read_scale : 0.f;
-        }
-#pragma unroll
-        for (int j0 = 0; j0 < D::NO; j0 += 4) {
-          float r[4][4];
-#pragma unroll
-          for (int k = 0; k < D::KS; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              uint32_t b[4];
-              ldsm_t(b, stored + (k * 16 * D::LV + (j0 + j) * 8) * 2);
-              if (k == 0) {
-                mma_first<DT>(r[j], qf[k], b[0], b[1]);
-                mma_first<DT>(r[j + 1], qf[k], b[2], b[3]);
-              } else {
-                mma<DT>(r[j], qf[k], b[0], b[1]);
-                mma<DT>(r[j + 1], qf[k], b[2], b[3]);
-              }
-            }
-          // (chosen by row, not added up: what the state holds stays in its sequence)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[j0 + j][e] = mine[e >> 1] ? r[j][e] * f[e >> 1] : o[j0 + j][e];
-        }
-      }
-      if (ends ? ps.out != nullptr && known : !last_tile) {
-        if (ps.out) state.template add<true>(sh, at, end, late, ps.scale_add, lane);
-        else state.template add<false>(sh, at, end, late, ps.scale_add, lane);
-        live = true;
-        if (ends) state.write(ps.out + matrix, a.d, first_col, lane);
-      }
-      if (ends) live = false;
-      at = end;
-    }
-
-    // the tile's own part: 16 rows of keys at a time
-    // (rows of other sequences, and those behind a tile that was cut, are multiplied by 0)
-    const bool apart = !(whole && n == most) && __syncthreads_or(not_finite<DT, DK>(sh));
-    // first row of each of this lane's rows' sequences
-    int from[2];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const unsigned long long upto = starts << (63 - (row0 + half * 8));
-      from[half] = upto ? row0 + half * 8 - __clzll((long long)upto) : 0;
-    }
-    int up[2] = {0, 0};  // fp16: what the rows' outputs are held multiplied by, as exponents
-    for (int j = 0; j <= warp; ++j) {
-      float c[2][4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c[0][e] = c[1][e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < D::KS; ++k) {
-        uint32_t b[4];
-        ldsm(b, keys + (j * 16 * D::LK + k * 16) * 2);
-        mma<DT>(c[0], qf[k], b[0], b[1]);
-        mma<DT>(c[1], qf[k], b[2], b[3]);
-      }
-      if (j < warp) {
-        const float by_row[2] = {sh.pow[row0 - j * 16 - 15], sh.pow[row0 + 8 - j * 16 - 15]};
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) c[t][e] *= by_row[e >> 1] * by_col[t * 2 + (e & 1)];
-        if (!whole) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (j * 16 + t * 8 + lane % 4 * 2 + (e & 1) < from[e >> 1]) c[t][e] = 0.f;
-        }
-      } else {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int half = e >> 1, s = j * 16 + t * 8 + lane % 4 * 2 + (e & 1), away = row0 + half * 8 - s;
-            c[t][e] = away >= 0 && s >= from[half] ? c[t][e] * (sh.pow[away & 63] * ps.scale_tile) : 0.f;
-          }
-      }
-      float top[2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-        top[half] = fmaxf(fmaxf(fabsf(c[0][2 * half]), fabsf(c[0][2 * half + 1])),
-                          fmaxf(fabsf(c[1][2 * half]), fabsf(c[1][2 * half + 1])));
-      if (DT == TBE_F16) {
-        bool moves = j == 0;
-        int want[2];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          top[half] = fmaxf(top[half], __shfl_xor_sync(kFull, top[half], 1));
-          top[half] = fmaxf(top[half], __shfl_xor_sync(kFull, top[half], 2));
-          // outputs so far are moved too: no further up than by 2^24
-          want[half] = min(24, room_for(top[half]));
-          moves |= want[half] < up[half];
-        }
-        if (__any_sync(kFull, moves)) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int to = j == 0 ? want[half] : min(want[half], up[half]);
-            const float f = pow2(to - up[half]);
-#pragma unroll
-            for (int i = 0; i < D::NO; ++i) {
-              o[i][2 * half] *= f;
-              o[i][2 * half + 1] *= f;
-            }
-            up[half] = to;
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) c[t][e] *= pow2(up[e >> 1]);
-      }
-      const uint32_t w[4] = {pack2<DT>(c[0][0], c[0][1]), pack2<DT>(c[0][2], c[0][3]), pack2<DT>(c[1][0], c[1][1]),
-                             pack2<DT>(c[1][2], c[1][3])};
-      if (!apart) {
-#pragma unroll
-        for (int i = 0; i < D::NO; i += 2) {
-          uint32_t b[4];
-          ldsm_t(b, values + (j * 16 * D::LV + i * 8) * 2);
-          mma<DT>(o[i], w, b[0], b[1]);
-          mma<DT>(o[i + 1], w, b[2], b[3]);
-        }
-      } else {
-        // some value is no number: each sequence's rows take its own values only, so that it stays in its sequence
-        for (int at = 0; at < n;) {
-          const unsigned long long later = at < 63 ? starts >> (at + 1) << (at + 1) : 0;
-          const int end = later ? __ffsll((long long)later) - 1 : n;
-          uint32_t keep[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int t = j * 16 + lane % 4 * 2 + h * 8;
-            keep[h] = (t >= at && t < end ? 0xffffu : 0u) | (t + 1 >= at && t + 1 < end ? 0xffff0000u : 0u);
-          }
-          const bool mine[2] = {row0 >= at && row0 < end, row0 + 8 >= at && row0 + 8 < end};
-#pragma unroll
-          for (int i = 0; i < D::NO; i += 2) {
-            uint32_t b[4];
-            ldsm_t(b, values + (j * 16 * D::LV + i * 8) * 2);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float r[4] = {o[i + u][0], o[i + u][1], o[i + u][2], o[i + u][3]};
-              mma<DT>(r, w, b[2 * u] & keep[0], b[2 * u + 1] & keep[1]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[i + u][e] = mine[e >> 1] ? r[e] : o[i + u][e];
-            }
-          }
-          at = end;
-        }
-      }
-    }
-    // this warp's rows go out through its own rows of the queries, which only it read
-    __syncwarp();
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const float f = DT == TBE_F16 ? pow2(-up[half]) : 1.f;
-#pragma unroll
-      for (int j = 0; j < D::NO; ++j)
-        *reinterpret_cast<uint32_t*>(sh.q + (row0 + half * 8) * D::LK + j * 8 + lane % 4 * 2) =
-            pack2<DT>(o[j][2 * half] * f, o[j][2 * half + 1] * f);
-    }
-    __syncwarp();
-    {
-      const int cols = min(D::DV, a.d - first_col), each = ps.piece_o / 2, per_row = (cols + each - 1) / each;
-      for (int i = lane; i < 16 * per_row; i += 32) {
-        const int r = warp * 16 + i / per_row, c = i % per_row * each;
-        if (r >= n) break;
-        const int64_t token = ps.back ? a.N - 1 - (p + r) : p + r;
-        uint16_t* to = ps.o + token * ps.so + head * ps.ho + first_col + c;
-        const uint16_t* src = sh.q + r * D::LK + c;
-        if (each == 8) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(src);
-        else if (each == 4) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(src);
-        else if (each == 2) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(src);
-        else *to = *src;
-      }
-    }
-    const bool keep_state = live && !last_tile;
-    if (keep_state) note_top();
-    __syncthreads();  // the tile and the state in shared memory have been read
-    if (keep_state) publish();
-    p += n;
   }
 }
 
@@ -982,18 +1048,19 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepArgs a) {
 // ---------------------------------------------------------------------------
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
-int width_of(int32_t d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
-int parts_of(int32_t d) { return width_of(d) == 128 ? (d + 63) / 64 : 1; }
+int width_of(int32_t d) { return d <= 64 ? 64 : 128; }
 
 // Runs: as many blocks as the GPU holds at once.
 struct Split {
-  int32_t tiles, runs;
+  int32_t run, runs;
 };
 Split split_of(int64_t N, int32_t H, int32_t d, int passes) {
-  const int64_t all = (N + kTile - 1) / kTile, want = std::max<int64_t>(1, (width_of(d) == 128 ? kBlocks<128> : kBlocks<64>) * (int64_t)sm_count() / ((int64_t)H * parts_of(d) * passes));
+  const int64_t tiles = (N + kTile - 1) / kTile;
+  const int64_t want = std::max<int64_t>(1, (width_of(d) == 64 ? kBlocks<64> : kBlocks<128>) * (int64_t)sm_count() / ((int64_t)H * passes));
+  const int64_t each = std::max<int64_t>(1, (tiles + want - 1) / want);
   Split s;
-  s.tiles = (int32_t)std::max<int64_t>(1, (all + want - 1) / want);
-  s.runs = (int32_t)std::max<int64_t>(1, (all + s.tiles - 1) / s.tiles);
+  s.run = (int32_t)std::min<int64_t>(each * kTile, 1 << 30);
+  s.runs = (int32_t)std::max<int64_t>(1, (N + s.run - 1) / s.run);
   return s;
 }
 struct Layout {
@@ -1003,8 +1070,8 @@ Layout layout(int64_t N, int32_t H, int32_t d, int passes) {
   const Split sp = split_of(N, H, d, passes);
   Layout w = {0, 0, 0};
   if (sp.runs > 1) {
-    const size_t dk = width_of(d);
-    w.kind = round256(sizeof(float) * (size_t)H * sp.runs * dk * dk);
+    const size_t wide = width_of(d);
+    w.kind = round256(sizeof(float) * (size_t)H * sp.runs * wide * wide);
     w.bytes = w.kind + round256(sizeof(int32_t) * (size_t)sp.runs);
   }
   return w;
@@ -1025,46 +1092,43 @@ int start(const void* kernel, dim3 grid, int threads, size_t smem, bool after, c
   return cudaLaunchKernelExC(&cfg, kernel, args) == cudaSuccess ? check_launch() : TBE_ERR_CUDA;
 }
 
-template <int DT, int DK>
-int launch(const Args& a, int passes, cudaStream_t s) {
-  constexpr size_t smem = sizeof(Shared<DK>);
-  const void *carry = (const void*)carry_kernel<DT, DK>, *output = (const void*)output_kernel<DT, DK>;
+template <int DT, int W>
+int launch(Args& a, int passes, cudaStream_t s) {
+  const void *sums = (const void*)attention_kernel<DT, W, true>, *outputs = (const void*)attention_kernel<DT, W, false>;
+  a.terms = 2;
+  for (int p = 0; p < passes; ++p)
+    if (DT == TBE_BF16 && a.pass[p].out) a.terms = 3;
+  const size_t smem = Room<W>::bytes(a.terms) + sizeof(Control);
+  static_assert(Room<W>::bytes(3) + sizeof(Control) <= 227 * 1024 / kBlocks<W> - (kBlocks<W> > 1 ? 1024 : 0), "fits an SM");
   static bool allowed[64] = {};  // once per device
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !allowed[dev]) {
-    for (const void* f : {carry, output})
-      if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return TBE_ERR_CUDA;
+    for (const void* f : {sums, outputs})
+      if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Room<W>::bytes(3) + (int)sizeof(Control)) != cudaSuccess)
+        return TBE_ERR_CUDA;
     if (dev >= 0 && dev < 64) allowed[dev] = true;
   }
-  const unsigned per_run = (unsigned)(a.H * a.parts);
-  bool after = false;
   int st;
-  if (a.N > 0) {
-    if (a.runs > 1) {
-      if ((st = start(carry, dim3((unsigned)(a.runs - 1) * per_run, passes), kThreads, smem, false, s, a)) != TBE_OK) return st;
-      trace_mark(s, "linear_attention_carry");
-      const unsigned blocks = (unsigned)a.H * (DK * DK / 256);
-      if ((st = start((const void*)join_kernel<DK>, dim3(blocks, passes), 256, 0, true, s, a)) != TBE_OK) return st;
-      trace_mark(s, "linear_attention_join");
-      after = true;
-    }
-    if ((st = start(output, dim3((unsigned)a.runs * per_run, passes), kThreads, smem, after, s, a)) != TBE_OK) return st;
-    trace_mark(s, "linear_attention_output");
-    after = true;
+  if (a.runs > 1) {
+    if ((st = start(sums, dim3((unsigned)(a.runs - 1) * a.H, passes), kThreads, smem, false, s, a)) != TBE_OK) return st;
+    trace_mark(s, "linear_attention_sums");
+    if ((st = start((const void*)join_kernel<W>, dim3((unsigned)a.H * (W * W / 256), passes), 256, 0, true, s, a)) != TBE_OK) return st;
+    trace_mark(s, "linear_attention_join");
   }
-  return TBE_OK;
+  st = start(outputs, dim3((unsigned)a.runs * a.H, passes), kThreads, smem, a.runs > 1, s, a);
+  trace_mark(s, "linear_attention_output");
+  return st;
 }
 
 template <int DT>
-int dispatch(const Args& a, int passes, cudaStream_t s) {
-  const int w = width_of(a.d);
-  return w == 32 ? launch<DT, 32>(a, passes, s) : w == 64 ? launch<DT, 64>(a, passes, s) : launch<DT, 128>(a, passes, s);
+int dispatch(Args& a, int passes, cudaStream_t s) {
+  return width_of(a.d) == 64 ? launch<DT, 64>(a, passes, s) : launch<DT, 128>(a, passes, s);
 }
 
-// Bytes (2 to 16) that rows of d elements can be moved by.
-int piece_of(const void* p, int64_t stride, int64_t head, int32_t d) {
-  int n = 16;
+// Bytes (2 to `most`) that rows of d elements can be moved by.
+int piece_of(const void* p, int64_t stride, int64_t head, int32_t d, int most) {
+  int n = most;
   while (n > 2 && (((uintptr_t)p | (uintptr_t)(stride * 2) | (uintptr_t)(head * 2) | (uintptr_t)(d * 2)) & (n - 1))) n >>= 1;
   return n;
 }
@@ -1106,28 +1170,56 @@ Args args_of(const tbe_linear_attention_inputs* in, int passes, int32_t* status)
   a.H = in->heads;
   a.d = in->head_dim;
   const Split sp = split_of(a.N, a.H, a.d, passes);
-  a.tiles = sp.tiles;
+  a.run = sp.run;
   a.runs = sp.runs;
-  a.parts = parts_of(a.d);
   a.status = status;
   return a;
 }
 
-void set_rows(Pass& p, const Rows& q, const Rows& k, const Rows& v, const Rows& o, int32_t d) {
-  p.q = static_cast<const uint16_t*>(q.p);
-  p.sq = q.stride;
-  p.hq = q.head;
-  p.k = static_cast<const uint16_t*>(k.p);
-  p.sk = k.stride;
-  p.hk = k.head;
-  p.v = static_cast<const uint16_t*>(v.p);
-  p.sv = v.stride;
-  p.hv = v.head;
+// The tensor maps of up to kMaxMaps row sets; where one cannot be copied so
+// (its rows must start on 16 bytes), none is.
+struct Maps {
+  Rows r[kMaxMaps];
+  int n = 0;
+  int of(const Rows& x) {
+    r[n] = x;
+    return n++;
+  }
+  int fill(Args& a, int32_t dtype) const {
+    a.piece = 16;
+    bool copies = a.N < (int64_t(1) << 31) - kTile;
+    for (int i = 0; i < n; ++i) {
+      copies &= piece_of(r[i].p, r[i].stride, r[i].head, 8, 16) == 16;
+      a.piece = std::min(a.piece, piece_of(r[i].p, r[i].stride, r[i].head, a.d, 16));
+    }
+    if (!copies) return TBE_OK;
+    a.piece = 0;
+    for (int i = 0; i < n; ++i) {
+      const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.H, (cuuint64_t)a.N};
+      const cuuint64_t strides[2] = {(cuuint64_t)r[i].head * 2, (cuuint64_t)r[i].stride * 2};
+      const cuuint32_t box[3] = {64, 1, kTile}, one[3] = {1, 1, 1};
+      if (!encode_map(&a.map[i], dtype, 3, r[i].p, dims, strides, box, one)) return TBE_ERR_CUDA;
+    }
+    return TBE_OK;
+  }
+};
+void set_rows(Pass& p, const Maps& m, int q, int k, int v, const Rows& o, int32_t d) {
+  p.q = static_cast<const uint16_t*>(m.r[q].p);
+  p.sq = m.r[q].stride;
+  p.hq = m.r[q].head;
+  p.mq = q;
+  p.k = static_cast<const uint16_t*>(m.r[k].p);
+  p.sk = m.r[k].stride;
+  p.hk = m.r[k].head;
+  p.mk = k;
+  p.v = static_cast<const uint16_t*>(m.r[v].p);
+  p.sv = m.r[v].stride;
+  p.hv = m.r[v].head;
+  p.mv = v;
   p.o = static_cast<uint16_t*>(const_cast<void*>(o.p));
   p.so = o.stride;
   p.ho = o.head;
-  p.piece = std::min({piece_of(q.p, q.stride, q.head, d), piece_of(k.p, k.stride, k.head, d), piece_of(v.p, v.stride, v.head, d)});
-  p.piece_o = piece_of(o.p, o.stride, o.head, d);
+  p.piece_o = piece_of(o.p, o.stride, o.head, d, 32);
 }
 
 // Whether two [sequences, heads, d, d] states share memory: blocks read the
@@ -1138,7 +1230,7 @@ bool overlap(const tbe_linear_attention_inputs* in, const float* p, const float*
   return p && q && a < b + bytes && b < a + bytes;
 }
 
-int go(Args& a, int passes, int32_t dtype, void* workspace, size_t bytes, cudaStream_t s) {
+int go(Args& a, const Maps& maps, int passes, int32_t dtype, void* workspace, size_t bytes, cudaStream_t s) {
   const Layout w = layout(a.N, a.H, a.d, passes);
   if (bytes < passes * w.bytes) return TBE_ERR_WORKSPACE;
   if (w.bytes) {
@@ -1150,10 +1242,13 @@ int go(Args& a, int passes, int32_t dtype, void* workspace, size_t bytes, cudaSt
       a.pass[p].kind = reinterpret_cast<int32_t*>(at + w.kind);
     }
   }
-  if ((int64_t)a.runs * a.H * a.parts >= (int64_t(1) << 31)) return TBE_ERR_UNSUPPORTED;
+  if ((int64_t)a.runs * a.H >= (int64_t(1) << 31)) return TBE_ERR_UNSUPPORTED;
   trace_begin(s);
-  const int st = dtype == TBE_F16 ? dispatch<TBE_F16>(a, passes, s) : dispatch<TBE_BF16>(a, passes, s);
-  if (st != TBE_OK) return st;
+  if (a.N > 0) {
+    int st = maps.fill(a, dtype);
+    if (st == TBE_OK) st = dtype == TBE_F16 ? dispatch<TBE_F16>(a, passes, s) : dispatch<TBE_BF16>(a, passes, s);
+    if (st != TBE_OK) return st;
+  }
   for (int p = 0; p < passes; ++p)
     if (a.pass[p].out) {  // one at most
       Args e = a;
@@ -1189,13 +1284,15 @@ int tbe_linear_attention(const tbe_linear_attention_inputs* in, void* o, int64_t
   if (in->sequences == 0) return TBE_OK;
   Args a = args_of(in, 1, dev_status);
   Pass& p = a.pass[0];
-  set_rows(p, {in->q, in->q_stride, in->q_head_stride}, {in->k, in->k_stride, in->k_head_stride},
-           {in->v, in->v_stride, in->v_head_stride}, out, a.d);
+  Maps maps;
+  const int q = maps.of({in->q, in->q_stride, in->q_head_stride}), k = maps.of({in->k, in->k_stride, in->k_head_stride}),
+            v = maps.of({in->v, in->v_stride, in->v_head_stride});
+  set_rows(p, maps, q, k, v, out, a.d);
   p.in = in->s0;
   p.out = s_last;
   p.scale_tile = p.scale_read = in->scale;
   p.scale_add = 1.f;
-  return go(a, 1, in->dtype, workspace, workspace_bytes, (cudaStream_t)stream);
+  return go(a, maps, 1, in->dtype, workspace, workspace_bytes, (cudaStream_t)stream);
 }
 
 int tbe_linear_attention_backward(const tbe_linear_attention_inputs* in, const void* dout, int64_t do_stride,
@@ -1216,14 +1313,16 @@ int tbe_linear_attention_backward(const tbe_linear_attention_inputs* in, const v
   if (overlap(in, ds_last, g->ds0) || overlap(in, in->s0, g->ds0)) return TBE_ERR_INVALID_ARG;
   if (in->sequences == 0) return TBE_OK;
   Args a = args_of(in, 3, dev_status);
-  set_rows(a.pass[0], d, v, k, dq, a.d);
+  Maps maps;
+  const int mq = maps.of(q), mk = maps.of(k), mv = maps.of(v), md = maps.of(d);
+  set_rows(a.pass[0], maps, md, mv, mk, dq, a.d);
   a.pass[0].in = in->s0;
   a.pass[0].in_turned = 1;
   a.pass[0].scale_tile = a.pass[0].scale_read = in->scale;
   a.pass[0].scale_add = 1.f;
-  set_rows(a.pass[1], v, d, q, dk, a.d);
+  set_rows(a.pass[1], maps, mv, md, mq, dk, a.d);
   a.pass[1].in_turned = 1;
-  set_rows(a.pass[2], k, q, d, dv, a.d);
+  set_rows(a.pass[2], maps, mk, mq, md, dv, a.d);
   a.pass[2].out = g->ds0;
   for (int i = 1; i < 3; ++i) {
     a.pass[i].in = ds_last;
@@ -1231,7 +1330,7 @@ int tbe_linear_attention_backward(const tbe_linear_attention_inputs* in, const v
     a.pass[i].scale_tile = a.pass[i].scale_add = in->scale;
     a.pass[i].scale_read = 1.f;
   }
-  return go(a, 3, in->dtype, workspace, workspace_bytes, (cudaStream_t)stream);
+  return go(a, maps, 3, in->dtype, workspace, workspace_bytes, (cudaStream_t)stream);
 }
 
 int tbe_linear_attention_step(const tbe_linear_attention_inputs* in, float* state, void* o, int64_t o_stride,
