@@ -114,6 +114,13 @@ struct Starts {
 
 __device__ __forceinline__ float power(float decay, int64_t n) { return n == 0 ? 1.f : exp2f(-(float)n * decay * kLog2e); }
 
+// 2^x to 2^-22 of its size, 0 for the lowest.
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if (DT == TBE_BF16) {
@@ -155,10 +162,11 @@ struct Room {  // W: columns of a head, filled up
   static constexpr int state = W * W * 2;
   static constexpr int q = 0, k = operand, v = 2 * operand, s = 3 * operand, rest = 3 * operand + state;  // behind the terms
   static constexpr int bytes(int n_terms) { return rest + n_terms * operand; }
-  // columns of TMEM: the products of a tile, whose weighted form takes the first half of theirs; the two parts of
-  // the outputs; the sum that goes to the state (in the second half of the products', where there is room)
+  // columns of TMEM: the products of a tile, whose weighted form in 16 bits takes the first and the last quarter of
+  // theirs; the two parts of the outputs; the sum that goes to the state (between those quarters, where that is enough)
   static constexpr int cols = W == 64 ? 256 : 512;
-  static constexpr int tp = 0, to = kTile, ts = kTile + W, ta = W == 64 ? kTile / 2 : kTile + 2 * W;
+  static constexpr int tp = 0, to = kTile, ts = kTile + W, ta = W == 64 ? 32 : kTile + 2 * W;
+  static constexpr int weighted(int part) { return tp + (part < 4 ? part * 8 : 64 + part * 8); }  // of 16 columns each
 };
 
 // What is known of a tile.
@@ -296,17 +304,44 @@ struct Marker {
 template <int W>
 __device__ __forceinline__ void load_rows(uint8_t* dst, const uint16_t* src, int64_t stride, int64_t first, int64_t N, int d,
                                           int piece, int thread) {
-  const int each = piece / 2, per_row = W / each;
-  for (int i = thread; i < kTile * per_row; i += 32 * kWarps) {
-    const int r = i / per_row, c = (i - r * per_row) * each;
-    const int64_t token = first + r;
-    const bool in = token >= 0 && token < N && c < d;
-    const uint16_t* from = src + token * stride + c;
-    uint8_t* to = dst + c / 64 * kBlock + r * 128 + ((c % 64 / 8) ^ (r & 7)) * 16 + c % 8 * 2;
-    if (piece == 16) *reinterpret_cast<uint4*>(to) = in ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
-    else if (piece == 8) *reinterpret_cast<uint2*>(to) = in ? __ldg(reinterpret_cast<const uint2*>(from)) : make_uint2(0, 0);
-    else if (piece == 4) *reinterpret_cast<uint32_t*>(to) = in ? __ldg(reinterpret_cast<const uint32_t*>(from)) : 0;
-    else *reinterpret_cast<uint16_t*>(to) = in ? __ldg(from) : 0;
+  const int each = piece / 2, rows = 31 - __clz(W / each);  // a row is 2^rows pieces
+  auto place = [&](int i, int& r, int& c) {
+    r = i >> rows;
+    c = (i & ((1 << rows) - 1)) * each;
+    return dst + c / 64 * kBlock + r * 128 + ((c % 64 / 8) ^ (r & 7)) * 16 + c % 8 * 2;
+  };
+  if (piece > 2) {
+#pragma unroll 4
+    for (int i = thread; i < kTile << rows; i += 32 * kWarps) {
+      int r, c;
+      const uint32_t to = smem_u32(place(i, r, c));
+      const int64_t token = first + r;
+      const bool in = token >= 0 && token < N && c < d;
+      const uint16_t* from = in ? src + token * stride + c : src;
+      const uint32_t bytes = in ? piece : 0;  // the rest of the piece is zeros
+      if (piece == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+      else if (piece == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+      else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    }
+    return;
+  }
+  constexpr int kAhead = 8;  // (the loads of so many elements at once)
+  for (int i0 = thread; i0 < kTile * W; i0 += kAhead * 32 * kWarps) {
+    uint16_t x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      int r, c;
+      place(i0 + k * 32 * kWarps, r, c);
+      const int64_t token = first + r;
+      const bool in = token >= 0 && token < N && c < d;
+      x[k] = __ldg(in ? src + token * stride + c : src);
+      x[k] = in ? x[k] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      int r, c;
+      *reinterpret_cast<uint16_t*>(place(i0 + k * 32 * kWarps, r, c)) = x[k];
+    }
   }
 }
 
@@ -316,6 +351,11 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, 
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(col), "r"(head), "r"(row), "r"(smem_u32(bar))
       : "memory");
+}
+
+__device__ __forceinline__ void tma_ahead3(const CUtensorMap* map, int32_t col, int32_t head, int32_t row) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(map), "r"(col), "r"(head), "r"(row)
+               : "memory");
 }
 
 // Descriptor of an operand whose next 64 rows (along M or N) are `apart` bytes on.
@@ -349,6 +389,7 @@ struct Worker {
   int warp, lane, quarter, half, row;
   int head;
   float s[kCols];         // the state: row `row`, columns half * kCols ..
+  float slope;            // -log2 gamma, at most 1e30 (times 0 it is 0)
   float read_scale = 0.f; // what the state in shared memory is to be multiplied by
   uint32_t exchanges = 0;
 
@@ -379,6 +420,19 @@ struct Worker {
 
   // The state from, or to, a [d, d] matrix (or its transpose), or a [W, W] one.
   __device__ __forceinline__ void read(const float* p, int d, bool turned) {
+    if (!turned && d % 4 == 0 && ((uintptr_t)p & 15) == 0) {
+#pragma unroll
+      for (int j = 0; j < kCols; j += 4) {
+        const int col = half * kCols + j;
+        const float4 x = row < d && col < d ? __ldg(reinterpret_cast<const float4*>(p + (int64_t)row * d + col))
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+        s[j] = x.x;
+        s[j + 1] = x.y;
+        s[j + 2] = x.z;
+        s[j + 3] = x.w;
+      }
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < kCols; ++j) {
       const int col = half * kCols + j;
@@ -482,38 +536,50 @@ struct Worker {
       scale *= pow2(up);
       down = pow2(-up);
     }
+    const bool all = n == kTile;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       const int at = (i * 32 * kWarps + warp * 32 + lane) * 16, far = place(at / 128 % kTile);
-      const bool in = far < n;
-      const float w = in ? c.pow[n - 1 - far + ps.back] * scale : 0.f;
+      const float w = exp2_of(-slope * (float)(n - 1 - far + ps.back)) * scale;
       float x[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 y = unpack2<DT>((&u[i].x)[e]);
-        x[2 * e] = in ? y.x * w : 0.f;
-        x[2 * e + 1] = in ? y.y * w : 0.f;
+        x[2 * e] = y.x * w;
+        x[2 * e + 1] = y.y * w;
       }
-      for (int t = 0; t < n_terms; ++t) {
-        uint4 r;
-        if (DT == TBE_BF16 && t < n_terms - 1) {  // cut off: the upper halves of the numbers
+      if (!all && far >= n) {  // (whatever stands there)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+      }
+      uint8_t* to = terms + at;
+      if (DT == TBE_BF16) {
+        for (int t = 1; t < n_terms; ++t, to += Room<W>::operand) {  // cut off: the upper halves of the numbers
+          uint4 r;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             (&r.x)[e] = __byte_perm(__float_as_uint(x[2 * e]), __float_as_uint(x[2 * e + 1]), 0x7632);
             x[2 * e] -= __uint_as_float(__float_as_uint(x[2 * e]) & 0xffff0000u);
             x[2 * e + 1] -= __uint_as_float(__float_as_uint(x[2 * e + 1]) & 0xffff0000u);
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            (&r.x)[e] = pack2<DT>(x[2 * e], x[2 * e + 1]);
-            const float2 y = unpack2<DT>((&r.x)[e]);
-            x[2 * e] -= y.x;
-            x[2 * e + 1] -= y.y;
-          }
+          *reinterpret_cast<uint4*>(to) = r;
         }
-        *reinterpret_cast<uint4*>(terms + t * Room<W>::operand + at) = r;
+      } else {
+        uint4 r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          (&r.x)[e] = pack2<DT>(x[2 * e], x[2 * e + 1]);
+          const float2 y = unpack2<DT>((&r.x)[e]);
+          x[2 * e] -= y.x;
+          x[2 * e + 1] -= y.y;
+        }
+        *reinterpret_cast<uint4*>(to) = r;
+        to += Room<W>::operand;
       }
+      uint4 r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) (&r.x)[e] = pack2<DT>(x[2 * e], x[2 * e + 1]);
+      *reinterpret_cast<uint4*>(to) = r;
     }
     to_products();
     arrive(&c.keys);
@@ -524,14 +590,12 @@ struct Worker {
   __device__ __forceinline__ void add(int n, float down) {
     const float by = c.pow[n];
     if (quarter * 32 < W) {
+      float x[kCols];
 #pragma unroll
-      for (int j = 0; j < kCols; j += 32) {
-        float x[32];
-        tc_ld32(tmem + Room<W>::ta + half * kCols + j + lanes(), x);
-        tc_wait_ld();
+      for (int j = 0; j < kCols; j += 32) tc_ld32(tmem + Room<W>::ta + half * kCols + j + lanes(), x + j);
+      tc_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) s[j + e] = fmaf(s[j + e], by, DT == TBE_F16 ? x[e] * down : x[e]);
-      }
+      for (int e = 0; e < kCols; ++e) s[e] = fmaf(s[e], by, DT == TBE_F16 ? x[e] * down : x[e]);
     }
     tc_before_sync();
     arrive(&c.add_read);
@@ -550,71 +614,81 @@ struct Worker {
         if (u) from = w * 32 + 31 - __clz((int)u);
       }
     }
-    uint32_t packed[2][16];
-    float top = 0.f;
-    float x[2][32];
+    // chunks of 32 columns: 0 for this warp's own rows, more for those before, less for those behind (nothing)
+    const int sooner = ps.back ? half * 2 - quarter : quarter - half * 2, step = ps.back ? 1 : -1;
+    float scale = ps.scale_tile;
+    auto weigh = [&](float* x, int i) {
+      const int chunk = half * 2 + i, before = sooner + i * step;
+      if (before < 0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int chunk = half * 2 + i;
-      const int sooner = ps.back ? chunk - quarter : quarter - chunk;  // all of it before this warp's rows, or behind
-      if (sooner < 0) {
+        for (int e = 0; e < 32; ++e) x[e] = 0.f;
+        return;
+      }
+      if (before > 0) {
+        // gamma^distance in two parts: to the chunk's near end, and inside it
+        const float by = exp2_of(-slope * (float)(ps.back ? chunk * 32 - row : row - chunk * 32 - 31)) * scale;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[i][e] = 0.f;
+        for (int e = 0; e < 32; e += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(c.by_col + e);
+          x[e] *= by * w.x;
+          x[e + 1] *= by * w.y;
+          x[e + 2] *= by * w.z;
+          x[e + 3] *= by * w.w;
+        }
       } else {
-        tc_ld32(tmem + Room<W>::tp + chunk * 32 + lanes(), x[i]);
-        tc_wait_ld();
-        if (sooner > 0) {
-          // gamma^distance in two parts: to the chunk's near end, and inside it
-          const float by = c.pow[ps.back ? chunk * 32 - row : row - chunk * 32 - 31] * ps.scale_tile;
+        const float sign = ps.back ? -1.f : 1.f;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(c.by_col + e);
-            x[i][e] *= by * w.x;
-            x[i][e + 1] *= by * w.y;
-            x[i][e + 2] *= by * w.z;
-            x[i][e + 3] *= by * w.w;
-          }
+        for (int e = 0; e < 32; ++e) {
+          const float away = sign * (float)(lane - e), w = exp2_of(-slope * away) * scale;
+          x[e] = away >= 0.f ? x[e] * w : 0.f;
+        }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = place(chunk * 32 + e) < from ? 0.f : x[e];
+      }
+    };
+    up = 0;
+    if (DT == TBE_F16) {
+      // the row's largest product that takes part, before its weight (at most the scale)
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int chunk = half * 2 + i, before = sooner + i * step;
+        if (before < 0) continue;
+        float x[32];
+        tc_ld32(tmem + Room<W>::tp + chunk * 32 + lanes(), x);
+        tc_wait_ld();
+        if (whole && before > 0) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[e]));
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const int away = ps.back ? e - lane : lane - e;
-            x[i][e] = away >= 0 ? x[i][e] * (c.pow[away & 31] * ps.scale_tile) : 0.f;
+            const int at = place(chunk * 32 + e);
+            top = fmaxf(top, at <= far && at >= from ? fabsf(x[e]) : 0.f);
           }
         }
-        if (!whole) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (place(chunk * 32 + e) < from) x[i][e] = 0.f;
-        }
       }
-      if (DT == TBE_F16) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[i][e]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) packed[i][e] = pack2<DT>(x[i][2 * e], x[i][2 * e + 1]);
-      }
-    }
-    up = 0;
-    if (DT == TBE_F16) {
       c.top_row[half][row] = top;
-      tc_before_sync();
       arrive(&c.row_max[quarter]);
       if (!wait(&c.row_max[quarter], turn, c)) return false;
-      up = room_for(fmaxf(top, *(volatile float*)&c.top_row[half ^ 1][row]));
-      const float f = pow2(up);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) packed[i][e] = pack2<DT>(x[i][2 * e] * f, x[i][2 * e + 1] * f);
-    } else {
-      tc_before_sync();
-      arrive(&c.row_max[quarter]);
-      if (!wait(&c.row_max[quarter], turn, c)) return false;
+      up = room_for(fmaxf(top, *(volatile float*)&c.top_row[half ^ 1][row]) * fabsf(scale));
+      scale *= pow2(up);
     }
-    tc_after_sync();  // both halves of this row's columns have been read
+    // Each half of the columns is written over what its own warps have read: chunk 0, then 1; chunk 3, then 2.
 #pragma unroll
-    for (int i = 0; i < 2; ++i) tc_st16(tmem + Room<W>::tp + (half * 2 + i) * 16 + lanes(), packed[i]);
+    for (int k = 0; k < 2; ++k) {
+      const int i = half ^ k;
+      float x[32];
+      tc_ld32(tmem + Room<W>::tp + (half * 2 + i) * 32 + lanes(), x);
+      tc_wait_ld();
+      weigh(x, i);
+      uint32_t packed[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) packed[e] = pack2<DT>(x[2 * e], x[2 * e + 1]);
+      tc_st16(tmem + half * 96 + i * 16 + lanes(), packed);
+    }
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
     tc_before_sync();
     arrive(&c.weighted);
@@ -632,17 +706,21 @@ struct Worker {
     for (int j = 0; j < kCols; j += 32) {
       float x[32];
       tc_ld32(tmem + Room<W>::to + half * kCols + j + lanes(), x);
-      tc_wait_ld();
-      if (DT == TBE_F16) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] *= of_tile;
-      }
       if (t.live) {
         float y[32];
         tc_ld32(tmem + Room<W>::ts + half * kCols + j + lanes(), y);
         tc_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = live ? fmaf(y[e], of_state, x[e]) : x[e];
+        for (int e = 0; e < 32; ++e) {
+          if (DT == TBE_F16) x[e] *= of_tile;
+          x[e] = live ? fmaf(y[e], of_state, x[e]) : x[e];
+        }
+      } else {
+        tc_wait_ld();
+        if (DT == TBE_F16) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] *= of_tile;
+        }
       }
       if (j + 32 >= kCols) {
         tc_before_sync();
@@ -745,24 +823,40 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
     // finds the tiles, starts the copies, issues the products
     Marker m = {st, ps.in != nullptr || ps.out != nullptr, 0, 0};
     if (!SUMS) m.seek(p0, lane);
-    bool live = !SUMS && run > 0 && __shfl_sync(kFull, m.x, 0) > p0;  // (m.x of lane 0: the first start)
-    int64_t p = begin;
+    const bool live = !SUMS && run > 0 && __shfl_sync(kFull, m.x, 0) > p0;  // (m.x of lane 0: the first start)
     uint32_t states = 0, adds = 0, copies = 0;
     bool added = false;  // by the tile before
     const uint32_t room0 = smem_u32(room), terms0 = smem_u32(raw);
     const uint32_t format = DT == TBE_BF16;
-    for (uint32_t i = 0;; ++i) {
+    auto find = [&](int64_t at, bool live) {
       Tile t = {};
-      if (p >= p1) t.p = -1;
-      else if (SUMS) {
-        t.p = p;
-        t.n = (int)min((int64_t)kTile, p1 - p);
+      if (at >= p1) {
+        t.p = -1;
+      } else if (SUMS) {
+        t.p = at;
+        t.n = (int)min((int64_t)kTile, p1 - at);
         t.e0 = t.n;
         t.adds = 1;
         t.mixed = t.n < kTile;
       } else {
-        m.mark(t, p, p1, live, ps.in != nullptr, ps.out != nullptr, lane);
+        m.mark(t, at, p1, live, ps.in != nullptr, ps.out != nullptr, lane);
       }
+      return t;
+    };
+    Tile following = find(begin, live);
+    // A tile's rows on their way to the L2.
+    auto ahead = [&](const Tile& t) {
+      if (t.p < 0 || a.piece || lane != 0) return;
+      const int32_t first = (int32_t)(ps.back ? a.N - t.p - kTile : t.p);
+#pragma unroll
+      for (int b = 0; b < W / 64; ++b) {
+        tma_ahead3(&a.map[ps.mk], b * 64, head, first);
+        if (!SUMS) tma_ahead3(&a.map[ps.mq], b * 64, head, first);
+        tma_ahead3(&a.map[ps.mv], b * 64, head, first);
+      }
+    };
+    for (uint32_t i = 0;; ++i) {
+      const Tile t = following;
       // (the products and copies of the tile before are through)
       if (lane == 0) {
         c.tile[i & 1] = t;
@@ -809,13 +903,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
           }
           __syncwarp();
         }
+        following = find(t.p + t.n, t.leaves);  // (while these products go on and are weighted)
+        ahead(following);
         if (!wait(&c.weighted, i, c)) break;
         tc_after_sync();
         if (lane == 0) {
           const uint32_t idesc = tc_idesc(format, 0, 1, kTile, W);
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
-            tc_mma_tmem(tmem + R::to, tmem + R::tp + k * 8, desc_of(room0 + R::v + k * 2048, kBlock), idesc, k > 0);
+            tc_mma_tmem(tmem + R::to, tmem + R::weighted(k), desc_of(room0 + R::v + k * 2048, kBlock), idesc, k > 0);
           tc_commit(&c.out_done);
         }
         __syncwarp();
@@ -837,13 +933,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
         ++adds;
       }
       added = t.adds;
-      int n = t.n;
-      if (!SUMS && t.mixed && *(volatile int32_t*)&c.bad[i & 1] && t.e0 < n) {
-        n = t.e0;  // the others were told so by the same word
-        m.seek(t.p + n, lane);
+      if (SUMS) {
+        following = find(t.p + t.n, false);
+        ahead(following);
+      } else if (t.mixed && *(volatile int32_t*)&c.bad[i & 1] && t.e0 < t.n) {
+        m.seek(t.p + t.e0, lane);  // the others were told by the same word that the tile ends there
+        following = find(t.p + t.e0, false);
       }
-      live = t.leaves;
-      p = t.p + n;
       if (!SUMS && !wait(&c.out_done, i, c)) break;
       if (t.adds && !wait(&c.add_done, adds - 1, c)) break;
     }
@@ -851,6 +947,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
     if (*(volatile int32_t*)&c.dead && copies) mbar_wait(&c.full, (copies - 1) & 1, 1 << 16);
   } else {
     Worker<DT, W, SUMS> w = {a, ps, c, raw, room, tmem, warp, lane, warp & 3, warp >> 2, (warp & 3) * 32 + lane, head};
+    w.slope = decay * kLog2e > 1e30f ? 1e30f : decay * kLog2e;
 #pragma unroll
     for (int j = 0; j < w.kCols; ++j) w.s[j] = 0.f;
     const float* carried = ps.carry + ((int64_t)head * a.runs + run - 1) * W * W;
@@ -867,6 +964,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
         load_rows<W>(room + R::k, ps.k + head * ps.hk, ps.sk, first, a.N, a.d, a.piece, thread);
         if (!SUMS) load_rows<W>(room + R::q, ps.q + head * ps.hq, ps.sq, first, a.N, a.d, a.piece, thread);
         load_rows<W>(room + R::v, ps.v + head * ps.hv, ps.sv, first, a.N, a.d, a.piece, thread);
+        cp_commit();
+        cp_wait<0>();
         to_products();
         w.arrive(&c.full);
       }
@@ -896,12 +995,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
         }
       }
       float down = 1.f;
-      if (t.adds && !w.weigh_keys(n, terms, down)) break;
       int up = 0;
       if (!SUMS) {
         if (!wait(&c.products, i, c)) break;
         tc_after_sync();
         if (!w.weigh_products(t, n, i, up)) break;
+      }
+      // (while the products of the values go on)
+      if (t.adds && !w.weigh_keys(n, terms, down)) break;
+      if (!SUMS) {
+        if (!wait(&c.out_done, i, c)) break;
+        tc_after_sync();
+        w.write_outputs(t, n, up);
       }
       if (t.adds) {
         if (!wait(&c.add_done, adds++, c)) break;
@@ -912,11 +1017,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
         } else if (!SUMS) {
           w.write(ps.out + (t.sequence * a.H + head) * matrix, a.d);
         }
-      }
-      if (!SUMS) {
-        if (!wait(&c.out_done, i, c)) break;
-        tc_after_sync();
-        w.write_outputs(t, n, up);
       }
     }
     if (SUMS && w.holds()) w.write(ps.carry + ((int64_t)head * a.runs + run) * W * W, W);
