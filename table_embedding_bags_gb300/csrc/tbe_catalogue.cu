@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
   if (k < a.N && a.zero && !taken(a.labels[k], a.V))
     for (int c = lane; c < a.D; c += 32) a.zero[k * a.zero_stride + c] = 0;
   const int64_t count = a.count ? *a.count : a.N;
-  if (k >= min(a.Np, (count + 127) / 128 * 128)) return;
+  if (k >= min(a.Np, (count + 255) / 256 * 256)) return;
   uint16_t* dst = a.dst + k * a.Dp;
   const uint16_t* src = k < count ? a.src + (a.rows ? (int64_t)a.rows[k] : k) * a.src_stride : nullptr;
   if (a.vec == 8) {
@@ -174,12 +174,19 @@ struct Job {
 };
 constexpr int kMaxJobs = 3;
 
-constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
-constexpr int kStages = 4;
-constexpr int kStageBytes = (kTileM + kTileN) / 64 * kBlockBytes;
+// A pair of blocks (on neighbouring SMs) takes a tile of 256 x 256: each
+// holds 128 rows of A and of the accumulators, and half of B's columns, which
+// the tensor cores of both read.  Against a tile of 128 x 256 to a block that
+// is two thirds of the copies, which are what bounds the products here.
+constexpr int kRowsM = 128;  // of a block
+constexpr int kTileM = 2 * kRowsM, kTileN = 256, kTileK = 64;
+constexpr int kHalfN = kTileN / 2;
+constexpr int kStages = 6;
+constexpr int kStageBytes = (kRowsM + kHalfN) / 64 * kBlockBytes;
 constexpr int kTiles = 4;  // tiles known ahead
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
+constexpr uint16_t kBoth = 3;  // blocks of a pair, as a mask
 
 struct GemmArgs {
   CUtensorMap h, w, p;  // hidden [Np, D], weights [V, D], g [2 Np, vc], in boxes of 64 x 64
@@ -204,24 +211,24 @@ struct GemmArgs {
   int32_t* status;
 };
 
+// A tile's place.
+struct alignas(16) Tile {
+  int32_t mode;      // -1 behind the last
+  int32_t job;
+  int32_t rb;        // block of kTileM rows of the product
+  int32_t col;       // first column
+  int32_t blocks;    // columns / 64, in whole pairs
+  int32_t split, k0, steps;
+};
 struct Shared {
   uint64_t full[kStages], empty[kStages];   // operands
   uint64_t done[2], drained[2];             // accumulators
   uint64_t known[kTiles], forgotten[kTiles];  // tiles
   uint64_t combine[2];
-  int32_t tile[kTiles];
+  Tile tile[kTiles];
   uint32_t tmem;
   int32_t dead;
-  float2 half[2][kTileM];
-};
-
-// A tile's place.  Every role works it out from its number.
-struct Tile {
-  int32_t job, mode;
-  int32_t rb;            // block of 128 rows of the product
-  int32_t col;           // first column
-  int32_t blocks;        // columns / 64
-  int32_t split, k0, steps;
+  float2 half[2][kRowsM];
 };
 
 __device__ __forceinline__ int32_t column_tiles(int32_t D) { return (D + kTileN - 1) / kTileN; }
@@ -254,7 +261,7 @@ __device__ __forceinline__ Tile tile_of(const GemmArgs& g, int32_t t, int32_t co
   }
   const int32_t ct = column_tiles(g.D);
   r.col = t % ct * kTileN;
-  r.blocks = min(kTileN / 64, (g.D - r.col + 63) / 64);
+  r.blocks = min(kTileN / 64, (g.D - r.col + 127) / 128 * 2);
   t /= ct;
   if (r.mode == kTable) {
     r.rb = t;
@@ -273,7 +280,7 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile 
   uint64_t begin, now;
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(begin));
   for (;;) {
-    if (mbar_wait(bar, parity, 64)) return true;
+    if (pair_wait(bar, parity, 64)) return true;
     if (*dead) return false;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
     if (now - begin > 4000000000ull) {
@@ -283,7 +290,7 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile 
   }
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Shared& s) {
-  return mbar_wait(bar, parity, 4) || wait_long(bar, parity, &s.dead);
+  return pair_wait(bar, parity, 4) || wait_long(bar, parity, &s.dead);
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b, bool bf16) {
@@ -331,101 +338,151 @@ __device__ __forceinline__ void store_row(uint16_t* p, const float* v, int n, in
 template <int DT>
 constexpr int kUp = DT == TBE_F16 ? 14 : 0;
 
-template <int DT>
-__device__ __forceinline__ void epilogue(const GemmArgs& g, Shared& s, const Tile& t, uint32_t tmem, int32_t count,
-                                         int half, int row, uint32_t turn, bool& ok) {
-  const Job& j = g.job[t.job];
-  const int64_t r = (int64_t)t.rb * kTileM + row;
-  float v[32];
-  if (t.mode == kSums) {
-    float m = -INFINITY, l = 0.f;
-    const int32_t label = g.label[r];
-    for (int c = half * 128; c < half * 128 + 128; c += 32) {
-      tc_ld32(tmem + c, v);
-      tc_wait_ld();
-      const int32_t col = t.col + c;
-      if ((uint32_t)(label - col) < 32u) {
-        float x = 0.f;
+// (a, b) * s + c
+__device__ __forceinline__ void fma2(float& a, float& b, float s, float c) {
+  asm("{\n\t.reg .b64 p, q, r;\n\t"
+      "mov.b64 p, {%0, %1};\n\t"
+      "mov.b64 q, {%2, %2};\n\t"
+      "mov.b64 r, {%3, %3};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(s), "f"(c));
+}
+// 2^x to 2^-22 of its size, 0 for the lowest.
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// v[0 .. 31] = 2^(v s + c)
+__device__ __forceinline__ void exps(float (&v)[32], float s, float c) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x = k == label - col ? v[k] : x;
-        g.mine[r] = x * g.scale2;
-      }
-      float top = m;
+  for (int k = 0; k < 32; k += 2) fma2(v[k], v[k + 1], s, c);
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        v[k] = col + k < g.V ? v[k] * g.scale2 : -INFINITY;
-        top = fmaxf(top, v[k]);
-      }
-      const float to = top == -INFINITY ? 0.f : top;
-      l *= exp2f(m - to);
-      float add[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < 32; ++k) add[k & 3] += exp2f(v[k] - to);
-      l += (add[0] + add[1]) + (add[2] + add[3]);
-      m = top;
-    }
-    // the two halves of the columns meet
-    if (half == 1) {
-      s.half[turn & 1][row] = make_float2(m, l);
-      bar_arrive(&s.combine[turn & 1]);
-    } else {
-      ok = wait(&s.combine[turn & 1], turn >> 1 & 1, s);
-      const float2 o = s.half[turn & 1][row];
-      const float top = fmaxf(m, o.x), to = top == -INFINITY ? 0.f : top;
-      if (r < count) g.part[(int64_t)((t.col - j.v0) / kTileN) * g.Np + r] =
-          make_float2(top, l * exp2f(m - to) + o.y * exp2f(o.x - to));
-    }
-    return;
-  }
-  if (t.mode == kProbs) {
-    const int32_t label = g.label[r];
-    const float less = (float)kUp<DT> - g.lse2[r];
-    uint16_t* dst = g.g + ((int64_t)j.buffer * g.Np + r) * g.vc;
-    for (int c = half * 128; c < half * 128 + 128; c += 32) {
-      tc_ld32(tmem + c, v);
-      tc_wait_ld();
-      const int32_t col = t.col + c;
-#pragma unroll
-      for (int k = 0; k < 32; ++k) v[k] = exp2f(fmaf(v[k], g.scale2, less));
-      if ((uint32_t)(label - col) < 32u) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (k == label - col) v[k] -= (float)(1 << kUp<DT>);
-      }
-      if (r >= count || col + 32 > g.V) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = r < count && col + k < g.V ? v[k] : 0.f;
-      }
-      store_row<DT>(dst + (col - j.v0), v, 32, 32);
-    }
-    return;
-  }
-  const int end = min(half * 128 + 128, t.blocks * 64);
-  if (t.mode == kTable) {
-    const float f = g.factor / (float)max(count, 1);
-    const int64_t row_v = j.v0 + r;
-    for (int c = half * 128; c < end; c += 32) {
-      tc_ld32(tmem + c, v);
-      tc_wait_ld();
-#pragma unroll
-      for (int k = 0; k < 32; ++k) v[k] = t.steps > 0 ? v[k] * f : 0.f;
-      const int32_t col = t.col + c;
-      if (row_v < j.v1 && col < g.D) store_row<DT>(g.dw + row_v * g.dw_stride + col, v, g.D - col, g.dw_piece);
-    }
-    return;
-  }
-  if (t.steps == 0 && !j.first) return;
-  float* dst = g.acc + ((int64_t)t.split * g.Np + r) * g.Dp + t.col;
-  for (int c = half * 128; c < end; c += 32) {
-    tc_ld32(tmem + c, v);
+  for (int k = 0; k < 32; ++k) v[k] = exp2_of(v[k]);
+}
+
+// A thread's columns of the accumulators, 32 at a time (64 is a divisor of
+// their number), the next 32 on their way while these are worked on: calls
+// f(values, first column).
+template <typename F>
+__device__ __forceinline__ void each_chunk(uint32_t tmem, int begin, int end, F& f) {
+  if (begin >= end) return;
+  float a[32], b[32];
+  tc_ld32(tmem + begin, a);
+#pragma unroll 1
+  for (int c = begin; c < end; c += 64) {
     tc_wait_ld();
+    tc_ld32(tmem + c + 32, b);
+    f(a, c);
+    tc_wait_ld();
+    if (c + 64 < end) tc_ld32(tmem + c + 64, a);
+    f(b, c + 32);
+  }
+}
+
+// What becomes of 32 columns of a row, by the tile's mode.
+struct SumsOf {
+  const GemmArgs& g;
+  const Tile& t;
+  int64_t r;
+  int32_t label;
+  bool edge, down;
+  float m, l;
+  __device__ __forceinline__ void operator()(float (&v)[32], int c) {
+    const int32_t col = t.col + c;
+    if ((uint32_t)(label - col) < 32u) {
+      float x = 0.f;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) x = k == label - col ? v[k] : x;
+      g.mine[r] = x * g.scale2;
+    }
+    if (edge) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (col + k >= g.V) v[k] = down ? INFINITY : -INFINITY;
+    }
+    float top = v[0];
+    if (down) {
+#pragma unroll
+      for (int k = 1; k < 32; ++k) top = fminf(top, v[k]);
+    } else {
+#pragma unroll
+      for (int k = 1; k < 32; ++k) top = fmaxf(top, v[k]);
+    }
+    top = fmaxf(m, g.scale2 == 0.f ? 0.f : top * g.scale2);
+    const float to = top == -INFINITY ? 0.f : top;
+    l *= exp2_of(m - to);
+    exps(v, g.scale2, -to);
+    if (edge) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (col + k >= g.V) v[k] = 0.f;
+    }
+    float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      add2(add[0], add[1], v[k], v[k + 1]);
+      add2(add[2], add[3], v[k + 2], v[k + 3]);
+    }
+    l += (add[0] + add[1]) + (add[2] + add[3]);
+    m = top;
+  }
+};
+template <int DT>
+struct ProbsOf {
+  const GemmArgs& g;
+  const Tile& t;
+  int32_t label, v0;
+  bool there, edge;
+  float less;
+  uint16_t* dst;
+  __device__ __forceinline__ void operator()(float (&v)[32], int c) {
+    const int32_t col = t.col + c;
+    exps(v, g.scale2, less);
+    if ((uint32_t)(label - col) < 32u) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (k == label - col) v[k] -= (float)(1 << kUp<DT>);
+    }
+    if (!there || edge) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = there && col + k < g.V ? v[k] : 0.f;
+    }
+    store_row<DT>(dst + (col - v0), v, 32, 32);
+  }
+};
+template <int DT>
+struct TableOf {
+  const GemmArgs& g;
+  const Tile& t;
+  uint16_t* dst;  // or null
+  float f;
+  __device__ __forceinline__ void operator()(float (&v)[32], int c) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = t.steps > 0 ? v[k] * f : 0.f;
+    const int32_t col = t.col + c;
+    if (dst && col < g.D) store_row<DT>(dst + col, v, g.D - col, g.dw_piece);
+  }
+};
+struct HiddenOf {
+  const Tile& t;
+  float* dst;
+  bool first;
+  __device__ __forceinline__ void operator()(float (&v)[32], int c) {
     if (t.steps == 0) {
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] = 0.f;
     }
-    if (j.first) {
+    if (first) {
 #pragma unroll
-      for (int k = 0; k < 32; k += 8) store32(dst + c + k, reinterpret_cast<const uint32_t*>(v + k));
+      for (int k = 0; k < 32; k += 8) {
+        uint32_t u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(v[k + e]);
+        store32(dst + c + k, u);
+      }
     } else {  // no other tile adds to these: the order of the sums is that of the launches
 #pragma unroll
       for (int k = 0; k < 32; k += 4)
@@ -434,16 +491,54 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, Shared& s, const Til
                      : "memory");
     }
   }
+};
+
+template <int DT>
+__device__ __forceinline__ bool epilogue(const GemmArgs& g, Shared& s, const Tile& t, uint32_t tmem, int32_t count,
+                                         int half, int row, uint32_t rank, uint32_t turn) {
+  const Job& j = g.job[t.job];
+  const int64_t r = (int64_t)t.rb * kTileM + rank * kRowsM + row;
+  const int begin = half * kHalfN, end = min(begin + kHalfN, t.blocks * 64);
+  const bool edge = t.col + kTileN > g.V;
+  if (t.mode == kSums) {
+    SumsOf f = {g, t, r, g.label[r], edge, g.scale2 < 0.f, -INFINITY, 0.f};
+    each_chunk(tmem, begin, end, f);
+    // the two halves of the columns meet
+    if (half == 1) {
+      s.half[turn & 1][row] = make_float2(f.m, f.l);
+      bar_arrive(&s.combine[turn & 1]);
+      return true;
+    }
+    if (!wait(&s.combine[turn & 1], turn >> 1 & 1, s)) return false;
+    const float2 o = s.half[turn & 1][row];
+    const float top = fmaxf(f.m, o.x), to = top == -INFINITY ? 0.f : top;
+    if (r < count) g.part[(int64_t)((t.col - j.v0) / kTileN) * g.Np + r] =
+        make_float2(top, f.l * exp2_of(f.m - to) + o.y * exp2_of(o.x - to));
+  } else if (t.mode == kProbs) {
+    ProbsOf<DT> f = {g, t, g.label[r], j.v0, r < count, edge, (float)kUp<DT> - g.lse2[r],
+                     g.g + ((int64_t)j.buffer * g.Np + r) * g.vc};
+    each_chunk(tmem, begin, end, f);
+  } else if (t.mode == kTable) {
+    const int64_t row_v = j.v0 + r;
+    TableOf<DT> f = {g, t, row_v < j.v1 ? g.dw + row_v * g.dw_stride : nullptr, g.factor / (float)max(count, 1)};
+    each_chunk(tmem, begin, end, f);
+  } else if (t.steps > 0 || j.first) {
+    HiddenOf f = {t, g.acc + ((int64_t)t.split * g.Np + r) * g.Dp + t.col, j.first != 0};
+    each_chunk(tmem, begin, min(end, g.Dp - t.col), f);
+  }
+  return true;
 }
 
-// Persistent blocks: one thread takes tiles and starts copies, one issues the
-// products, eight warps work on finished accumulators, of which there are two.
+// Persistent pairs of blocks.  In each block one thread starts its copies and
+// eight warps work on its finished accumulators, of which there are two; the
+// first block's threads also take the tiles and issue the products of both.
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ GemmArgs g) {
   extern __shared__ __align__(1024) uint8_t raw[];
   __shared__ Shared s;
   uint8_t* ring = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = pair_rank();
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages; ++k) {
       bar_init(&s.full[k], 1);
@@ -451,75 +546,90 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     for (int k = 0; k < 2; ++k) {
       bar_init(&s.done[k], 1);
-      bar_init(&s.drained[k], kEpilogueWarps);
-      bar_init(&s.combine[k], kTileM);
+      bar_init(&s.drained[k], 2 * kEpilogueWarps);
+      bar_init(&s.combine[k], kRowsM);
     }
     for (int k = 0; k < kTiles; ++k) {
       bar_init(&s.known[k], 1);
-      bar_init(&s.forgotten[k], 1 + kEpilogueWarps);
+      bar_init(&s.forgotten[k], 2 + 2 * kEpilogueWarps);  // the issuer, the other block's copier, all epilogue warps
     }
     s.dead = 0;
     bars_visible();
   }
-  if (warp == 2) tc_alloc(&s.tmem, 512);
+  if (warp == 2) pair_alloc(&s.tmem, 512);
   tc_before_sync();
   __syncthreads();
+  pair_sync();
   tc_after_sync();
   const uint32_t tmem = s.tmem;
   wait_predecessor();
   const int32_t count = *g.count;
 
   if (warp == 0 && lane == 0) {
-    tma_prefetch(&g.h);
-    tma_prefetch(&g.w);
     asm volatile("fence.proxy.async;" ::: "memory");  // rows and g were written by ordinary stores
     int32_t total = 0;
     for (int k = 0; k < g.jobs; ++k) total += tiles_of(g.job[k], (count + kTileM - 1) / kTileM, g.D);
     uint32_t step = 0;  // steps of K so far
-    int32_t next = blockIdx.x;
+    int32_t next = blockIdx.x >> 1;
     for (uint32_t n = 0;; ++n) {
-      const int32_t now = next < total ? next : -1;
-      if (now >= 0) next = (int32_t)(gridDim.x + atomicAdd(g.next, 1u));
-      if (n >= kTiles && !wait(&s.forgotten[n % kTiles], (n / kTiles - 1) & 1, s)) break;
-      s.tile[n % kTiles] = now;
-      bar_arrive(&s.known[n % kTiles]);
-      if (now < 0) break;
-      const Tile t = tile_of(g, now, count);
+      const uint32_t slot = n % kTiles;
+      Tile t;
+      if (rank == 0) {
+        const int32_t now = next < total ? next : -1;
+        if (now >= 0) next = (int32_t)((gridDim.x >> 1) + atomicAdd(g.next, 1u));
+        t.mode = -1;
+        if (now >= 0) t = tile_of(g, now, count);
+        if (n >= kTiles && !wait(&s.forgotten[slot], (n / kTiles - 1) & 1, s)) break;
+        s.tile[slot] = t;
+        const uint32_t other = pair_addr(&s.tile[slot], 1);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) pair_store16(other + 16 * k, reinterpret_cast<const uint4*>(&t)[k]);
+        bar_arrive(&s.known[slot]);
+        pair_arrive(pair_addr(&s.known[slot], 1));
+      } else {
+        if (!wait(&s.known[slot], (n / kTiles) & 1, s)) break;
+        t = s.tile[slot];
+        pair_arrive(pair_addr(&s.forgotten[slot], 0));
+      }
+      if (t.mode < 0) break;
       const Job& j = g.job[t.job];
       const CUtensorMap* a = t.mode <= kProbs ? &g.h : &g.p;
       const CUtensorMap* b = t.mode == kTable ? &g.h : &g.w;
-      const int32_t a_row = t.mode <= kProbs ? t.rb * kTileM : (int32_t)(j.buffer * g.Np) + (t.mode == kHidden ? t.rb * kTileM : 0);
+      const int32_t row0 = t.rb * kTileM + (int32_t)rank * kRowsM;
+      const int32_t a_row = t.mode <= kProbs ? row0 : (int32_t)(j.buffer * g.Np) + (t.mode == kHidden ? row0 : 0);
+      const int32_t mine = t.blocks / 2;                       // B's blocks of this block
+      const int32_t b_col = t.col + (int32_t)rank * mine * 64;  // its first column
       bool ok = true;
       for (int k = 0; k < t.steps; ++k, ++step) {
         const uint32_t at = step % kStages;
         if (step >= kStages && !(ok = wait(&s.empty[at], (step / kStages - 1) & 1, s))) break;
-        bar_expect(&s.full[at], (2 + t.blocks) * kBlockBytes);
+        if (rank == 0) bar_expect(&s.full[at], 2 * (2 + mine) * kBlockBytes);
+        const uint32_t bar = pair_addr(&s.full[at], 0);
         const uint32_t dst = smem_u32(ring) + at * kStageBytes;
         const int32_t kk = (t.k0 + k) * kTileK;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (t.mode == kTable) tma_load(dst + i * kBlockBytes, a, t.rb * kTileM + 64 * i, a_row + kk, &s.full[at]);
-          else tma_load(dst + i * kBlockBytes, a, kk, a_row + 64 * i, &s.full[at]);
+          if (t.mode == kTable) pair_load(dst + i * kBlockBytes, a, row0 + 64 * i, a_row + kk, bar);
+          else pair_load(dst + i * kBlockBytes, a, kk, a_row + 64 * i, bar);
         }
-        for (int i = 0; i < t.blocks; ++i) {
+        for (int i = 0; i < mine; ++i) {
           const uint32_t to = dst + (2 + i) * kBlockBytes;
-          if (t.mode <= kProbs) tma_load(to, b, kk, t.col + 64 * i, &s.full[at]);
-          else tma_load(to, b, t.col + 64 * i, (t.mode == kHidden ? j.v0 : 0) + kk, &s.full[at]);
+          if (t.mode <= kProbs) pair_load(to, b, kk, b_col + 64 * i, bar);
+          else pair_load(to, b, b_col + 64 * i, (t.mode == kHidden ? j.v0 : 0) + kk, bar);
         }
       }
       if (!ok) break;
     }
-    if (s.dead)  // copies in flight land before the block ends
+    if (*(volatile int32_t*)&s.dead && rank == 0)  // copies in flight land before the blocks end
       for (uint32_t k = step > kStages ? step - kStages : 0; k < step; ++k)
-        mbar_wait(&s.full[k % kStages], (k / kStages) & 1, 1 << 16);
-  } else if (warp == 1 && lane == 0) {
+        pair_wait(&s.full[k % kStages], (k / kStages) & 1, 1 << 14);
+  } else if (warp == 1 && lane == 0 && rank == 0) {
     uint32_t step = 0;
     for (uint32_t n = 0;; ++n) {
       if (!wait(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
-      const int32_t now = s.tile[n % kTiles];
+      const Tile t = s.tile[n % kTiles];
       bar_arrive(&s.forgotten[n % kTiles]);
-      if (now < 0) break;
-      const Tile t = tile_of(g, now, count);
+      if (t.mode < 0) break;
       if (n >= 2 && !wait(&s.drained[n & 1], (n / 2 - 1) & 1, s)) break;
       tc_after_sync();
       const uint32_t along_m = t.mode == kTable, along_n = t.mode >= kTable;
@@ -534,39 +644,39 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const uint64_t a = tc_desc(src), b = tc_desc(src + 2 * kBlockBytes);
 #pragma unroll
         for (int i = 0; i < kTileK / 16; ++i)
-          tc_mma(tmem + (n & 1) * kTileN, a + i * a_step, b + i * b_step, idesc, k > 0 || i > 0);
-        tc_commit(&s.empty[at]);
+          pair_mma(tmem + (n & 1) * kTileN, a + i * a_step, b + i * b_step, idesc, k > 0 || i > 0);
+        pair_commit(&s.empty[at], kBoth);
       }
       if (!ok) break;
-      tc_commit(&s.done[n & 1]);
+      pair_commit(&s.done[n & 1], kBoth);
     }
   } else if (warp >= 4) {
     const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     uint32_t turn = 0;  // tiles of kSums so far
     for (uint32_t n = 0;; ++n) {
       if (!wait(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
-      const int32_t now = s.tile[n % kTiles];
+      const Tile t = s.tile[n % kTiles];
       __syncwarp();
-      if (lane == 0) bar_arrive(&s.forgotten[n % kTiles]);
-      if (now < 0) break;
-      const Tile t = tile_of(g, now, count);
+      if (lane == 0) pair_arrive(pair_addr(&s.forgotten[n % kTiles], 0));
+      if (t.mode < 0) break;
       if (!wait(&s.done[n & 1], (n / 2) & 1, s)) break;
       tc_after_sync();
-      bool ok = true;
-      epilogue<DT>(g, s, t, tmem + (n & 1) * kTileN + ((uint32_t)(warp & 3) * 32 << 16), count, half, row, turn, ok);
+      const bool ok = epilogue<DT>(g, s, t, tmem + (n & 1) * kTileN + ((uint32_t)(warp & 3) * 32 << 16), count, half, row,
+                                   rank, turn);
       turn += t.mode == kSums;
       if (!__all_sync(kFull, ok)) break;
       tc_before_sync();
       __syncwarp();
-      if (lane == 0) bar_arrive(&s.drained[n & 1]);
+      if (lane == 0) pair_arrive(pair_addr(&s.drained[n & 1], 0));
     }
   }
   __syncwarp();
   tc_before_sync();
   __syncthreads();
+  pair_sync();  // neither leaves while the other's products, copies or arrivals are under way
   tc_after_sync();
   if (threadIdx.x == 0 && s.dead) report(g.status, TBE_DEV_TIMEOUT);
-  if (warp == 2) tc_free(tmem, 512);
+  if (warp == 2) pair_free(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -709,13 +819,13 @@ bool copied(const void* p, int64_t stride) { return ((uintptr_t)p & 15) || strid
 
 Layout layout(int64_t N, int32_t V, int32_t D, bool grad, bool copy_table) {
   Layout w;
-  w.Np = whole(N, kTileM);
+  w.Np = whole(N, kTileM);  // (whole tiles)
   w.Dp = (int32_t)whole(D, 64);
   w.vt = (V + kTileN - 1) / kTileN;
   w.vc = (int32_t)std::min<int64_t>(whole(V, kTileN), std::max<int64_t>(kTileN, kPiece / w.Np / kTileN * kTileN));
   w.pieces = (V + w.vc - 1) / w.vc;
   // dhidden's tiles: as many as there are SMs, where there are few rows, of at least 8 steps each
-  const int64_t tiles = w.Np / kTileM * ((D + kTileN - 1) / kTileN), steps = (w.vc + kTileK - 1) / kTileK;
+  const int64_t tiles = w.Np / kTileM * 2 * ((D + kTileN - 1) / kTileN), steps = (w.vc + kTileK - 1) / kTileK;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>({(sm_count() + tiles - 1) / tiles, steps / 8, 32}));
   w.steps = (int32_t)((steps + want - 1) / want);
   w.splits = (int32_t)((steps + w.steps - 1) / w.steps);
@@ -781,7 +891,20 @@ int start_products(const GemmArgs& g, cudaStream_t s) {
       return TBE_ERR_CUDA;
     if (dev >= 0 && dev < 64) allowed[dev] = true;
   }
-  return start(product_kernel<DT>, sm_count(), kThreads, kProductBytes, true, s, g);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::max(2, sm_count() / 2 * 2));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kProductBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, product_kernel<DT>, g) == cudaSuccess ? check_launch() : TBE_ERR_CUDA;
 }
 
 struct Call {
