@@ -189,10 +189,13 @@ constexpr int kEpilogueWarps = 8;
 constexpr uint16_t kBoth = 3;  // blocks of a pair, as a mask
 
 struct GemmArgs {
-  CUtensorMap h, w, p;  // hidden [Np, D], weights [V, D], g [2 Np, vc], in boxes of 64 x 64
+  // hidden [Np, Dp], weights [V, D] and g [2 Np, vc]: 128 rows by 64 columns (operands along K), and 64 rows by two
+  // blocks of 64 columns (along M or N)
+  CUtensorMap h, w, p, ht, wt, pt;
   Job job[kMaxJobs];
   int32_t jobs;
   int32_t V, D, Dp;
+  int32_t half;       // blocks of 64 columns of the gradients that a block of a pair reads
   int64_t Np;
   const int32_t* count;
   uint32_t* next;     // tiles given out
@@ -231,19 +234,19 @@ struct Shared {
   float2 half[2][kRowsM];
 };
 
-__device__ __forceinline__ int32_t column_tiles(int32_t D) { return (D + kTileN - 1) / kTileN; }
-__device__ __forceinline__ int32_t tiles_of(const Job& j, int32_t mt, int32_t D) {
+__device__ __forceinline__ int32_t column_tiles(int32_t D, int32_t half) { return (D + 128 * half - 1) / (128 * half); }
+__device__ __forceinline__ int32_t tiles_of(const Job& j, int32_t mt, int32_t D, int32_t half) {
   const int32_t v = j.v1 - j.v0;
   if (j.mode <= kProbs) return mt * ((v + kTileN - 1) / kTileN);
-  if (j.mode == kTable) return (v + kTileM - 1) / kTileM * column_tiles(D);
-  return j.splits * mt * column_tiles(D);
+  if (j.mode == kTable) return (v + kTileM - 1) / kTileM * column_tiles(D, half);
+  return j.splits * mt * column_tiles(D, half);
 }
 __device__ __forceinline__ Tile tile_of(const GemmArgs& g, int32_t t, int32_t count) {
   const int32_t mt = (count + kTileM - 1) / kTileM;
   Tile r;
   r.job = 0;
   for (; r.job < g.jobs - 1; ++r.job) {
-    const int32_t n = tiles_of(g.job[r.job], mt, g.D);
+    const int32_t n = tiles_of(g.job[r.job], mt, g.D, g.half);
     if (t < n) break;
     t -= n;
   }
@@ -259,9 +262,9 @@ __device__ __forceinline__ Tile tile_of(const GemmArgs& g, int32_t t, int32_t co
     r.steps = (g.D + kTileK - 1) / kTileK;
     return r;
   }
-  const int32_t ct = column_tiles(g.D);
-  r.col = t % ct * kTileN;
-  r.blocks = min(kTileN / 64, (g.D - r.col + 127) / 128 * 2);
+  const int32_t ct = column_tiles(g.D, g.half);
+  r.col = t % ct * (128 * g.half);
+  r.blocks = 2 * g.half;
   t /= ct;
   if (r.mode == kTable) {
     r.rb = t;
@@ -276,11 +279,12 @@ __device__ __forceinline__ Tile tile_of(const GemmArgs& g, int32_t t, int32_t co
 }
 
 // A bounded wait: false (and the others give up too) after four seconds.
+template <bool PAIR>
 __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int32_t* dead) {
   uint64_t begin, now;
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(begin));
   for (;;) {
-    if (pair_wait(bar, parity, 64)) return true;
+    if (PAIR ? pair_wait(bar, parity, 64) : mbar_wait(bar, parity, 64)) return true;
     if (*dead) return false;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
     if (now - begin > 4000000000ull) {
@@ -290,7 +294,11 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile 
   }
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Shared& s) {
-  return pair_wait(bar, parity, 4) || wait_long(bar, parity, &s.dead);
+  return mbar_wait(bar, parity, 4) || wait_long<false>(bar, parity, &s.dead);
+}
+// (for what the other block wrote)
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, Shared& s) {
+  return pair_wait(bar, parity, 4) || wait_long<true>(bar, parity, &s.dead);
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b, bool bf16) {
@@ -567,18 +575,22 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
   if (warp == 0 && lane == 0) {
     asm volatile("fence.proxy.async;" ::: "memory");  // rows and g were written by ordinary stores
+    const uint32_t full0 = pair_addr(&s.full[0], 0), ring0 = smem_u32(ring);
     int32_t total = 0;
-    for (int k = 0; k < g.jobs; ++k) total += tiles_of(g.job[k], (count + kTileM - 1) / kTileM, g.D);
+    for (int k = 0; k < g.jobs; ++k) total += tiles_of(g.job[k], (count + kTileM - 1) / kTileM, g.D, g.half);
     uint32_t step = 0;  // steps of K so far
-    int32_t next = blockIdx.x >> 1;
+    uint32_t taken = 0;  // (asked for a tile ahead, and looked at then)
     for (uint32_t n = 0;; ++n) {
       const uint32_t slot = n % kTiles;
       Tile t;
       if (rank == 0) {
-        const int32_t now = next < total ? next : -1;
-        if (now >= 0) next = (int32_t)((gridDim.x >> 1) + atomicAdd(g.next, 1u));
+        const int32_t now = n == 0 ? blockIdx.x >> 1 : (int32_t)((gridDim.x >> 1) + taken);
         t.mode = -1;
-        if (now >= 0) t = tile_of(g, now, count);
+        t.steps = 0;
+        if (now < total) {
+          taken = atomicAdd(g.next, 1u);
+          t = tile_of(g, now, count);
+        }
         if (n >= kTiles && !wait(&s.forgotten[slot], (n / kTiles - 1) & 1, s)) break;
         s.tile[slot] = t;
         const uint32_t other = pair_addr(&s.tile[slot], 1);
@@ -587,36 +599,33 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         bar_arrive(&s.known[slot]);
         pair_arrive(pair_addr(&s.known[slot], 1));
       } else {
-        if (!wait(&s.known[slot], (n / kTiles) & 1, s)) break;
+        if (!wait_pair(&s.known[slot], (n / kTiles) & 1, s)) break;
         t = s.tile[slot];
-        pair_arrive(pair_addr(&s.forgotten[slot], 0));
+        if (t.mode >= 0 || t.steps >= 0) pair_arrive_relaxed(pair_addr(&s.forgotten[slot], 0));  // (it has been read)
       }
       if (t.mode < 0) break;
       const Job& j = g.job[t.job];
-      const CUtensorMap* a = t.mode <= kProbs ? &g.h : &g.p;
-      const CUtensorMap* b = t.mode == kTable ? &g.h : &g.w;
       const int32_t row0 = t.rb * kTileM + (int32_t)rank * kRowsM;
-      const int32_t a_row = t.mode <= kProbs ? row0 : (int32_t)(j.buffer * g.Np) + (t.mode == kHidden ? row0 : 0);
       const int32_t mine = t.blocks / 2;                       // B's blocks of this block
       const int32_t b_col = t.col + (int32_t)rank * mine * 64;  // its first column
+      const uint32_t bytes = 2 * (2 + mine) * kBlockBytes;
+      // where A and B lie along K, a step of it is 64 columns on; else 64 rows
+      const bool a_along_m = t.mode == kTable, b_along_n = t.mode >= kTable;
+      const CUtensorMap* a = a_along_m ? &g.pt : t.mode == kHidden ? &g.p : &g.h;
+      const CUtensorMap* b = t.mode == kTable ? &g.ht : t.mode == kHidden ? &g.wt : &g.w;
+      const int32_t g_row = (int32_t)(j.buffer * g.Np), a_row = t.mode == kHidden ? g_row + row0 : row0;
+      const int32_t b_first = t.mode == kHidden ? j.v0 : 0;
       bool ok = true;
       for (int k = 0; k < t.steps; ++k, ++step) {
         const uint32_t at = step % kStages;
         if (step >= kStages && !(ok = wait(&s.empty[at], (step / kStages - 1) & 1, s))) break;
-        if (rank == 0) bar_expect(&s.full[at], 2 * (2 + mine) * kBlockBytes);
-        const uint32_t bar = pair_addr(&s.full[at], 0);
-        const uint32_t dst = smem_u32(ring) + at * kStageBytes;
+        if (rank == 0) bar_expect(&s.full[at], bytes);
+        const uint32_t bar = full0 + at * 8, dst = ring0 + at * kStageBytes;
         const int32_t kk = (t.k0 + k) * kTileK;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (t.mode == kTable) pair_load(dst + i * kBlockBytes, a, row0 + 64 * i, a_row + kk, bar);
-          else pair_load(dst + i * kBlockBytes, a, kk, a_row + 64 * i, bar);
-        }
-        for (int i = 0; i < mine; ++i) {
-          const uint32_t to = dst + (2 + i) * kBlockBytes;
-          if (t.mode <= kProbs) pair_load(to, b, kk, b_col + 64 * i, bar);
-          else pair_load(to, b, b_col + 64 * i, (t.mode == kHidden ? j.v0 : 0) + kk, bar);
-        }
+        if (a_along_m) pair_load3(dst, a, g_row + kk, row0 / 64, bar);
+        else pair_load(dst, a, kk, a_row, bar);
+        if (b_along_n) pair_load3(dst + 2 * kBlockBytes, b, b_first + kk, b_col / 64, bar);
+        else pair_load(dst + 2 * kBlockBytes, b, kk, b_col, bar);
       }
       if (!ok) break;
     }
@@ -626,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   } else if (warp == 1 && lane == 0 && rank == 0) {
     uint32_t step = 0;
     for (uint32_t n = 0;; ++n) {
-      if (!wait(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
+      if (!wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
       const Tile t = s.tile[n % kTiles];
       bar_arrive(&s.forgotten[n % kTiles]);
       if (t.mode < 0) break;
@@ -654,10 +663,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     uint32_t turn = 0;  // tiles of kSums so far
     for (uint32_t n = 0;; ++n) {
-      if (!wait(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
+      if (!wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
       const Tile t = s.tile[n % kTiles];
       __syncwarp();
-      if (lane == 0) pair_arrive(pair_addr(&s.forgotten[n % kTiles], 0));
+      if (lane == 0 && (t.mode >= 0 || t.steps >= 0)) pair_arrive_relaxed(pair_addr(&s.forgotten[n % kTiles], 0));
       if (t.mode < 0) break;
       if (!wait(&s.done[n & 1], (n / 2) & 1, s)) break;
       tc_after_sync();
@@ -667,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (!__all_sync(kFull, ok)) break;
       tc_before_sync();
       __syncwarp();
-      if (lane == 0) pair_arrive(pair_addr(&s.drained[n & 1], 0));
+      if (lane == 0) pair_arrive_relaxed(pair_addr(&s.drained[n & 1], 0));
     }
   }
   __syncwarp();
@@ -814,8 +823,12 @@ struct Layout {
   int32_t Dp, vc, pieces, splits, steps, vt;
   size_t rows, label, lse2, mine, count, next, block_sum, arrived, hidden, part, weights, g, acc, bytes;
 };
-// Tensor copies want rows that start on 16 bytes; other tables are copied.
-bool copied(const void* p, int64_t stride) { return ((uintptr_t)p & 15) || stride % 8; }
+// Tensor copies want rows that start on 16 bytes and, by blocks of 64 columns,
+// whole ones; other tables are copied.
+bool off_pieces(const void* p, int64_t stride) { return ((uintptr_t)p & 15) || stride % 8; }
+bool copied(const tbe_catalogue_inputs& in, bool grad) {
+  return off_pieces(in.weights, in.weights_stride) || (grad && in.width % 64);
+}
 
 Layout layout(int64_t N, int32_t V, int32_t D, bool grad, bool copy_table) {
   Layout w;
@@ -854,12 +867,17 @@ Layout layout(int64_t N, int32_t V, int32_t D, bool grad, bool copy_table) {
   return w;
 }
 
-// [rows, cols] of 16-bit elements, `stride` elements from row to row, in
-// boxes of 64 x 64; zeros outside.
+// [rows, cols] of 16-bit elements, `stride` elements from row to row.
 bool map_of(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t stride, int32_t dtype) {
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
-  const cuuint32_t box[2] = {64, 64}, one[2] = {1, 1};
+  const cuuint32_t box[2] = {64, kRowsM}, one[2] = {1, 1};
   return encode_map(m, dtype, 2, p, dims, strides, box, one);
+}
+// The same as blocks of 64 columns (which cols is a multiple of).
+bool blocks_of(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t stride, int32_t blocks, int32_t dtype) {
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)cols / 64}, strides[2] = {(cuuint64_t)stride * 2, 128};
+  const cuuint32_t box[3] = {64, kTileK, (cuuint32_t)blocks}, one[3] = {1, 1, 1};
+  return encode_map(m, dtype, 3, p, dims, strides, box, one);
 }
 
 // Launches `kernel`; `after`: it may start while the kernel before it ends.
@@ -932,7 +950,7 @@ int piece_of(const void* p, int64_t stride, int most) {
 template <int DT>
 int run(const Call& c, cudaStream_t s) {
   const tbe_catalogue_inputs& in = *c.in;
-  const bool grad = c.dhidden != nullptr, copy = copied(in.weights, in.weights_stride);
+  const bool grad = c.dhidden != nullptr, copy = copied(in, grad);
   const int64_t N = in.tokens;
   const Layout w = layout(N, in.vocab, in.width, grad, copy);
   uint8_t* ws = c.ws;
@@ -967,7 +985,7 @@ int run(const Call& c, cudaStream_t s) {
   k.Np = w.Np;
   k.D = in.width;
   k.Dp = w.Dp;
-  k.vec = in.width % 8 == 0 && !copied(in.hidden, in.hidden_stride) ? 8 : 1;
+  k.vec = in.width % 8 == 0 && !off_pieces(in.hidden, in.hidden_stride) ? 8 : 1;
   k.zero = static_cast<uint16_t*>(c.dhidden);
   k.zero_stride = c.dhidden_stride;
   k.labels = in.labels;
@@ -994,9 +1012,17 @@ int run(const Call& c, cudaStream_t s) {
   }
 
   GemmArgs g = {};
-  if (!map_of(&g.h, k.dst, w.Np, w.Dp, w.Dp, DT) || !map_of(&g.w, table, in.vocab, in.width, table_stride, DT))
+  const int64_t table_cols = copy ? w.Dp : in.width;
+  g.half = w.Dp <= 128 ? 1 : 2;
+  if (!map_of(&g.h, k.dst, w.Np, w.Dp, w.Dp, DT) || !map_of(&g.w, table, in.vocab, table_cols, table_stride, DT))
     return TBE_ERR_CUDA;
-  if (grad && !map_of(&g.p, at<uint16_t>(ws, w.g), 2 * w.Np, w.vc, w.vc, DT)) return TBE_ERR_CUDA;
+  if (grad) {
+    const uint16_t* gs = at<uint16_t>(ws, w.g);
+    if (!map_of(&g.p, gs, 2 * w.Np, w.vc, w.vc, DT) || !blocks_of(&g.pt, gs, 2 * w.Np, w.vc, w.vc, kRowsM / 64, DT) ||
+        !blocks_of(&g.ht, k.dst, w.Np, w.Dp, w.Dp, g.half, DT) ||
+        !blocks_of(&g.wt, table, in.vocab, table_cols, table_stride, g.half, DT))
+      return TBE_ERR_CUDA;
+  }
   g.V = in.vocab;
   g.D = in.width;
   g.Dp = w.Dp;
@@ -1107,7 +1133,7 @@ int dispatch(const Call& c, void* workspace, size_t bytes, void* stream) {
       for (int j = std::max(i + 1, 2); j < 4; ++j)
         if (overlap(t[i].p, t[i].rows, t[i].stride, t[j].p, t[j].rows, t[j].stride, in.width)) return TBE_ERR_INVALID_ARG;
   }
-  const Layout w = layout(in.tokens, in.vocab, in.width, c.dhidden != nullptr, copied(in.weights, in.weights_stride));
+  const Layout w = layout(in.tokens, in.vocab, in.width, c.dhidden != nullptr, copied(in, c.dhidden != nullptr));
   if (bytes < w.bytes) return TBE_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
   trace_begin(s);
@@ -1123,7 +1149,7 @@ extern "C" {
 
 size_t tbe_catalogue_workspace_bytes(const tbe_catalogue_inputs* in, int32_t grad) {
   if (check(in) != TBE_OK) return 0;
-  return layout(in->tokens, in->vocab, in->width, grad != 0, copied(in->weights, in->weights_stride)).bytes;
+  return layout(in->tokens, in->vocab, in->width, grad != 0, copied(*in, grad != 0)).bytes;
 }
 
 int tbe_catalogue_loss(const tbe_catalogue_inputs* in, float* loss, float* token_loss, float* lse, void* dhidden,

@@ -82,6 +82,11 @@ __device__ __forceinline__ uint32_t pair_addr(const void* p, uint32_t rank) {
 __device__ __forceinline__ void pair_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same without ordering this thread's writes before it (a release waits
+// for those to global memory as well: 1,900 cycles behind a tile's outputs).
+__device__ __forceinline__ void pair_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void pair_store16(uint32_t to, uint4 v) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
@@ -102,7 +107,15 @@ __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, int li
   }
   return false;
 }
-// A box to this block's shared memory, whose bytes count towards a barrier of either.
+// A box to this block's shared memory, whose bytes count towards a barrier of
+// either.  Three dimensions: columns of a block of 64, rows, blocks.
+__device__ __forceinline__ void pair_load3(uint32_t dst, const CUtensorMap* map, int32_t row, int32_t block, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(dst),
+      "l"(map), "r"(0), "r"(row), "r"(block), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, int32_t col, int32_t row, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
