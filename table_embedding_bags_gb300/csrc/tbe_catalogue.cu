@@ -183,7 +183,8 @@ constexpr int kTileM = 2 * kRowsM, kTileN = 256, kTileK = 64;
 constexpr int kHalfN = kTileN / 2;
 constexpr int kStages = 6;
 constexpr int kStageBytes = (kRowsM + kHalfN) / 64 * kBlockBytes;
-constexpr int kTiles = 4;  // tiles known ahead
+constexpr int kTiles = 4;  // tiles known at once
+constexpr int kAsk = 4;    // steps before the end of a tile's copies at which the next one is asked for
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
 constexpr uint16_t kBoth = 3;  // blocks of a pair, as a mask
@@ -227,7 +228,8 @@ struct Shared {
   uint64_t full[kStages], empty[kStages];   // operands
   uint64_t done[2], drained[2];             // accumulators
   uint64_t known[kTiles], forgotten[kTiles];  // tiles
-  uint64_t combine[2];
+  uint64_t combine[2][4];
+  uint64_t ask;                             // the next tile is wanted
   Tile tile[kTiles];
   uint32_t tmem;
   int32_t dead;
@@ -503,26 +505,33 @@ struct HiddenOf {
 
 template <int DT>
 __device__ __forceinline__ bool epilogue(const GemmArgs& g, Shared& s, const Tile& t, uint32_t tmem, int32_t count,
-                                         int half, int row, uint32_t rank, uint32_t turn) {
+                                         int half, int row, uint32_t rank, uint32_t& turn) {
   const Job& j = g.job[t.job];
   const int64_t r = (int64_t)t.rb * kTileM + rank * kRowsM + row;
   const int begin = half * kHalfN, end = min(begin + kHalfN, t.blocks * 64);
   const bool edge = t.col + kTileN > g.V;
+  // Rows behind the last need no log-sum, and no g but those that a step of K takes with the last.
+  const int64_t warp_r = r - (row & 31);
   if (t.mode == kSums) {
+    if (warp_r >= count) return true;
     SumsOf f = {g, t, r, g.label[r], edge, g.scale2 < 0.f, -INFINITY, 0.f};
     each_chunk(tmem, begin, end, f);
     // the two halves of the columns meet
     if (half == 1) {
       s.half[turn & 1][row] = make_float2(f.m, f.l);
-      bar_arrive(&s.combine[turn & 1]);
+      __syncwarp();
+      if ((row & 31) == 0) bar_arrive(&s.combine[turn & 1][row / 32]);
+      ++turn;
       return true;
     }
-    if (!wait(&s.combine[turn & 1], turn >> 1 & 1, s)) return false;
+    if (!wait(&s.combine[turn & 1][row / 32], turn >> 1 & 1, s)) return false;
     const float2 o = s.half[turn & 1][row];
+    ++turn;
     const float top = fmaxf(f.m, o.x), to = top == -INFINITY ? 0.f : top;
     if (r < count) g.part[(int64_t)((t.col - j.v0) / kTileN) * g.Np + r] =
         make_float2(top, f.l * exp2_of(f.m - to) + o.y * exp2_of(o.x - to));
   } else if (t.mode == kProbs) {
+    if (warp_r >= (count + kTileK - 1) / kTileK * kTileK) return true;
     ProbsOf<DT> f = {g, t, g.label[r], j.v0, r < count, edge, (float)kUp<DT> - g.lse2[r],
                      g.g + ((int64_t)j.buffer * g.Np + r) * g.vc};
     each_chunk(tmem, begin, end, f);
@@ -555,11 +564,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int k = 0; k < 2; ++k) {
       bar_init(&s.done[k], 1);
       bar_init(&s.drained[k], 2 * kEpilogueWarps);
-      bar_init(&s.combine[k], kRowsM);
+      for (int q = 0; q < 4; ++q) bar_init(&s.combine[k][q], 1);
     }
+    bar_init(&s.ask, 1);
     for (int k = 0; k < kTiles; ++k) {
       bar_init(&s.known[k], 1);
-      bar_init(&s.forgotten[k], 2 + 2 * kEpilogueWarps);  // the issuer, the other block's copier, all epilogue warps
+      bar_init(&s.forgotten[k], 3 + 2 * kEpilogueWarps);  // the issuer, both copiers, all epilogue warps
     }
     s.dead = 0;
     bars_visible();
@@ -575,34 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
   if (warp == 0 && lane == 0) {
     asm volatile("fence.proxy.async;" ::: "memory");  // rows and g were written by ordinary stores
-    const uint32_t full0 = pair_addr(&s.full[0], 0), ring0 = smem_u32(ring);
-    int32_t total = 0;
-    for (int k = 0; k < g.jobs; ++k) total += tiles_of(g.job[k], (count + kTileM - 1) / kTileM, g.D, g.half);
+    const uint32_t full0 = pair_addr(&s.full[0], 0), forgotten0 = pair_addr(&s.forgotten[0], 0), ring0 = smem_u32(ring);
     uint32_t step = 0;  // steps of K so far
-    uint32_t taken = 0;  // (asked for a tile ahead, and looked at then)
     for (uint32_t n = 0;; ++n) {
-      const uint32_t slot = n % kTiles;
-      Tile t;
-      if (rank == 0) {
-        const int32_t now = n == 0 ? blockIdx.x >> 1 : (int32_t)((gridDim.x >> 1) + taken);
-        t.mode = -1;
-        t.steps = 0;
-        if (now < total) {
-          taken = atomicAdd(g.next, 1u);
-          t = tile_of(g, now, count);
-        }
-        if (n >= kTiles && !wait(&s.forgotten[slot], (n / kTiles - 1) & 1, s)) break;
-        s.tile[slot] = t;
-        const uint32_t other = pair_addr(&s.tile[slot], 1);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) pair_store16(other + 16 * k, reinterpret_cast<const uint4*>(&t)[k]);
-        bar_arrive(&s.known[slot]);
-        pair_arrive(pair_addr(&s.known[slot], 1));
-      } else {
-        if (!wait_pair(&s.known[slot], (n / kTiles) & 1, s)) break;
-        t = s.tile[slot];
-        if (t.mode >= 0 || t.steps >= 0) pair_arrive_relaxed(pair_addr(&s.forgotten[slot], 0));  // (it has been read)
-      }
+      if (!wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
+      const Tile t = s.tile[n % kTiles];
+      if (t.mode >= 0 || t.steps >= 0) pair_arrive_relaxed(forgotten0 + n % kTiles * 8);  // (it has been read)
       if (t.mode < 0) break;
       const Job& j = g.job[t.job];
       const int32_t row0 = t.rb * kTileM + (int32_t)rank * kRowsM;
@@ -616,8 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const int32_t g_row = (int32_t)(j.buffer * g.Np), a_row = t.mode == kHidden ? g_row + row0 : row0;
       const int32_t b_first = t.mode == kHidden ? j.v0 : 0;
       bool ok = true;
+      const int ask_at = max(0, t.steps - kAsk);
+      if (rank == 0 && t.steps == 0) bar_arrive(&s.ask);
       for (int k = 0; k < t.steps; ++k, ++step) {
         const uint32_t at = step % kStages;
+        if (rank == 0 && k == ask_at) bar_arrive(&s.ask);
         if (step >= kStages && !(ok = wait(&s.empty[at], (step / kStages - 1) & 1, s))) break;
         if (rank == 0) bar_expect(&s.full[at], bytes);
         const uint32_t bar = full0 + at * 8, dst = ring0 + at * kStageBytes;
@@ -637,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (uint32_t n = 0;; ++n) {
       if (!wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
       const Tile t = s.tile[n % kTiles];
-      bar_arrive(&s.forgotten[n % kTiles]);
+      if (t.mode >= 0 || t.steps >= 0) bar_arrive(&s.forgotten[n % kTiles]);
       if (t.mode < 0) break;
       if (n >= 2 && !wait(&s.drained[n & 1], (n / 2 - 1) & 1, s)) break;
       tc_after_sync();
@@ -659,9 +650,32 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (!ok) break;
       pair_commit(&s.done[n & 1], kBoth);
     }
+  } else if (warp == 3 && lane == 0 && rank == 0) {
+    // gives out tiles, to both blocks
+    int32_t total = 0;
+    for (int k = 0; k < g.jobs; ++k) total += tiles_of(g.job[k], (count + kTileM - 1) / kTileM, g.D, g.half);
+    int32_t now = blockIdx.x >> 1;
+    for (uint32_t n = 0;; ++n) {
+      const uint32_t slot = n % kTiles;
+      alignas(16) Tile t = {};
+      t.mode = -1;
+      if (n > 0) {  // (not asked for before it is wanted: the long tiles would go to few)
+        if (!wait(&s.ask, (n - 1) & 1, s)) break;
+        now = (int32_t)((gridDim.x >> 1) + atomicAdd(g.next, 1u));
+      }
+      if (now < total) t = tile_of(g, now, count);
+      if (n >= kTiles && !wait(&s.forgotten[slot], (n / kTiles - 1) & 1, s)) break;
+      s.tile[slot] = t;
+      const uint32_t other = pair_addr(&s.tile[slot], 1);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) pair_store16(other + 16 * k, reinterpret_cast<const uint4*>(&t)[k]);
+      bar_arrive(&s.known[slot]);
+      pair_arrive(pair_addr(&s.known[slot], 1));
+      if (now >= total) break;
+    }
   } else if (warp >= 4) {
     const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
-    uint32_t turn = 0;  // tiles of kSums so far
+    uint32_t turn = 0;  // tiles of kSums that this warp had rows of
     for (uint32_t n = 0;; ++n) {
       if (!wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
       const Tile t = s.tile[n % kTiles];
@@ -672,7 +686,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       tc_after_sync();
       const bool ok = epilogue<DT>(g, s, t, tmem + (n & 1) * kTileN + ((uint32_t)(warp & 3) * 32 << 16), count, half, row,
                                    rank, turn);
-      turn += t.mode == kSums;
       if (!__all_sync(kFull, ok)) break;
       tc_before_sync();
       __syncwarp();
@@ -899,7 +912,7 @@ int start(void (*kernel)(A), int64_t grid, int threads, size_t smem, bool after,
 constexpr size_t kProductBytes = (size_t)kStages * kStageBytes + 1024;
 
 template <int DT>
-int start_products(const GemmArgs& g, cudaStream_t s) {
+int start_products(const GemmArgs& g, int64_t tiles, cudaStream_t s) {  // tiles: at most so many
   static bool allowed[64] = {};  // once per device
   int dev = 0;
   cudaGetDevice(&dev);
@@ -910,7 +923,7 @@ int start_products(const GemmArgs& g, cudaStream_t s) {
     if (dev >= 0 && dev < 64) allowed[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::max(2, sm_count() / 2 * 2));
+  cfg.gridDim = dim3(2u * (unsigned)std::max<int64_t>(1, std::min<int64_t>(sm_count() / 2, tiles)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kProductBytes;
   cfg.stream = s;
@@ -1045,7 +1058,7 @@ int run(const Call& c, cudaStream_t s) {
     g.jobs = 1;
     g.job[0] = Job{kSums, 0, in.vocab, 0, 0, 0, 0};
     g.next = p.zero;
-    if ((st = start_products<DT>(g, s)) != TBE_OK) return st;
+    if ((st = start_products<DT>(g, w.Np / kTileM * w.vt, s)) != TBE_OK) return st;
     trace_mark(s, "catalogue_sums");
     RowArgs r = {};
     r.part = g.part;
@@ -1065,19 +1078,23 @@ int run(const Call& c, cudaStream_t s) {
     trace_mark(s, "catalogue_loss");
   }
   if (!grad) return TBE_OK;
+  const int64_t row_tiles = w.Np / kTileM, column_tiles = (in.width + 128 * g.half - 1) / (128 * g.half);
   for (int i = 0; i <= w.pieces; ++i) {
+    int64_t tiles = 0;
     g.jobs = 0;
     if (i > 0) {  // the long tiles first
       const int32_t v0 = (i - 1) * w.vc, v1 = (int32_t)std::min<int64_t>(in.vocab, (int64_t)v0 + w.vc);
       g.job[g.jobs++] = Job{kTable, v0, v1, (i - 1) & 1, 0, 0, 0};
       g.job[g.jobs++] = Job{kHidden, v0, v1, (i - 1) & 1, w.splits, w.steps, i == 1};
+      tiles += ((v1 - v0 + kTileM - 1) / kTileM + w.splits * row_tiles) * column_tiles;
     }
     if (i < w.pieces) {
       const int32_t v0 = i * w.vc, v1 = (int32_t)std::min<int64_t>(in.vocab, (int64_t)v0 + w.vc);
       g.job[g.jobs++] = Job{kProbs, v0, v1, i & 1, 0, 0, 0};
+      tiles += row_tiles * ((v1 - v0 + kTileN - 1) / kTileN);
     }
     g.next = p.zero + 1 + i;
-    if ((st = start_products<DT>(g, s)) != TBE_OK) return st;
+    if ((st = start_products<DT>(g, tiles, s)) != TBE_OK) return st;
   }
   trace_mark(s, "catalogue_gradients");
   SpreadArgs d = {};
