@@ -184,7 +184,7 @@ constexpr int kHalfN = kTileN / 2;
 constexpr int kStages = 6;
 constexpr int kStageBytes = (kRowsM + kHalfN) / 64 * kBlockBytes;
 constexpr int kTiles = 4;  // tiles known at once
-constexpr int kAsk = 4;    // steps before the end of a tile's copies at which the next one is asked for
+constexpr int kAsk = 6;    // steps before the end of a tile's copies at which the next one is asked for
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
 constexpr uint16_t kBoth = 3;  // blocks of a pair, as a mask
@@ -827,8 +827,11 @@ __global__ void __launch_bounds__(256) spread_kernel(const SpreadArgs a) {
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 int64_t whole(int64_t n, int64_t of) { return (n + of - 1) / of * of; }
 
-// Elements of a piece's g.
-constexpr int64_t kPiece = 1 << 25;
+// Elements of a piece's g.  With 2^24, 2^25, 2^26 and 2^27: 8,192 x 100,000 x
+// 512 bf16 with gradients 3,115, 2,384, 2,291, 2,249 us; 4,001 x 10,007 x 256 156,
+// 144, 127, 126 us; 512 x 150,000 x 128 205, 197, 207, 186 us.  (Two buffers of
+// 128 MB each.)
+constexpr int64_t kPiece = 1 << 26;
 constexpr int64_t kMaxTokens = 1 << 24;
 
 struct Layout {

@@ -503,12 +503,6 @@ struct Worker {
     }
     return bad;
   }
-  __device__ __forceinline__ void drop_values_from(int n) {
-    for (int i = warp * 32 + lane; i < Room<W>::operand / 16; i += 32 * kWarps)
-      if (place(i / 8 % kTile) >= n) *reinterpret_cast<uint4*>(room + Room<W>::v + i * 16) = make_uint4(0, 0, 0, 0);
-    to_products();
-  }
-
   // The keys times scale_add gamma^(n - 1 - place + late), as a sum of terms; the weight is 0 behind the tile.
   // Returns what the terms have to be multiplied by through `down`.
   __device__ __forceinline__ bool weigh_keys(int n, int n_terms, float& down) {
@@ -617,7 +611,9 @@ struct Worker {
     // chunks of 32 columns: 0 for this warp's own rows, more for those before, less for those behind (nothing)
     const int sooner = ps.back ? half * 2 - quarter : quarter - half * 2, step = ps.back ? 1 : -1;
     float scale = ps.scale_tile;
-    auto weigh = [&](float* x, int i) {
+    const float lanes_f = (float)lane, sign = ps.back ? -1.f : 1.f;
+    const uint32_t span = (uint32_t)(far - from);  // places from .. far take part
+    auto weigh = [&](float (&x)[32], int i) {
       const int chunk = half * 2 + i, before = sooner + i * step;
       if (before < 0) {
 #pragma unroll
@@ -629,24 +625,25 @@ struct Worker {
         const float by = exp2_of(-slope * (float)(ps.back ? chunk * 32 - row : row - chunk * 32 - 31)) * scale;
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          const float4 w = *reinterpret_cast<const float4*>(c.by_col + e);
-          x[e] *= by * w.x;
-          x[e + 1] *= by * w.y;
-          x[e + 2] *= by * w.z;
-          x[e + 3] *= by * w.w;
+          float4 w = *reinterpret_cast<const float4*>(c.by_col + e);
+          mul2(w.x, w.y, by);
+          mul2(w.z, w.w, by);
+          x[e] *= w.x;
+          x[e + 1] *= w.y;
+          x[e + 2] *= w.z;
+          x[e + 3] *= w.w;
         }
+        if (whole) return;
       } else {
-        const float sign = ps.back ? -1.f : 1.f;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float away = sign * (float)(lane - e), w = exp2_of(-slope * away) * scale;
-          x[e] = away >= 0.f ? x[e] * w : 0.f;
+          const float away = sign * (lanes_f - (float)e);  // (exact)
+          x[e] *= exp2_of(-slope * away) * scale;
         }
       }
-      if (!whole) {
+      const int first = place(chunk * 32) - from;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = place(chunk * 32 + e) < from ? 0.f : x[e];
-      }
+      for (int e = 0; e < 32; ++e) x[e] = (uint32_t)(first + (ps.back ? -e : e)) <= span ? x[e] : 0.f;
     };
     up = 0;
     if (DT == TBE_F16) {
@@ -696,7 +693,7 @@ struct Worker {
   }
 
   // o = the tile's part and the state's, rounded once.
-  __device__ __forceinline__ void write_outputs(const Tile& t, int n, int up) {
+  __device__ __forceinline__ void write_outputs(const Tile& t, int n, int up, float read_scale) {
     const int far = place(row);
     const bool live = t.live && far < t.e0;
     const float of_state = live ? c.pow[far + 1 - ps.back] * read_scale : 0.f, of_tile = DT == TBE_F16 ? pow2(-up) : 1.f;
@@ -844,6 +841,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
       return t;
     };
     Tile following = find(begin, live);
+    // The values from place n on are set to 0: some value of the tile is an infinity or a NaN, and those of other
+    // sequences are multiplied by 0.
+    auto drop = [&](int n) {
+      for (int i = lane; i < R::operand / 16; i += 32) {
+        const int r = i / 8 % kTile;
+        if ((ps.back ? kTile - 1 - r : r) >= n) *reinterpret_cast<uint4*>(room + R::v + i * 16) = make_uint4(0, 0, 0, 0);
+      }
+      to_products();
+      __syncwarp();
+    };
     // A tile's rows on their way to the L2.
     auto ahead = [&](const Tile& t) {
       if (t.p < 0 || a.piece || lane != 0) return;
@@ -907,6 +914,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
         ahead(following);
         if (!wait(&c.weighted, i, c)) break;
         tc_after_sync();
+        if (t.mixed && *(volatile int32_t*)&c.bad[i & 1]) drop(t.e0);
         if (lane == 0) {
           const uint32_t idesc = tc_idesc(format, 0, 1, kTile, W);
 #pragma unroll
@@ -919,6 +927,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
       if (t.adds) {
         if (!wait(&c.keys, adds, c)) break;
         tc_after_sync();
+        if (SUMS && t.mixed && *(volatile int32_t*)&c.bad[i & 1]) drop(t.n);
         if (lane == 0) {
           // (64 columns: the products' other 64 rows, of what follows in memory, are not looked at)
           const uint32_t idesc = tc_idesc(format, 1, 1, kTile, W);
@@ -986,14 +995,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
       if (t.mixed || t.adds) {
         if (!wait(&c.full, i, c)) break;
       }
-      if (t.mixed) {
-        if (__any_sync(kFull, w.not_finite()) && lane == 0) c.bad[i & 1] = 1;
-        if (!w.meet()) break;
-        if (*(volatile int32_t*)&c.bad[i & 1]) {
-          n = min(n, t.e0);
-          w.drop_values_from(n);
-        }
-      }
+      if (t.mixed && __any_sync(kFull, w.not_finite()) && lane == 0) c.bad[i & 1] = 1;
       float down = 1.f;
       int up = 0;
       if (!SUMS) {
@@ -1003,11 +1005,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
       }
       // (while the products of the values go on)
       if (t.adds && !w.weigh_keys(n, terms, down)) break;
-      if (!SUMS) {
-        if (!wait(&c.out_done, i, c)) break;
-        tc_after_sync();
-        w.write_outputs(t, n, up);
-      }
+      const float read_scale = w.read_scale;
       if (t.adds) {
         if (!wait(&c.add_done, adds++, c)) break;
         tc_after_sync();
@@ -1017,6 +1015,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
         } else if (!SUMS) {
           w.write(ps.out + (t.sequence * a.H + head) * matrix, a.d);
         }
+      }
+      if (!SUMS) {
+        if (!wait(&c.out_done, i, c)) break;
+        tc_after_sync();
+        if (t.mixed && *(volatile int32_t*)&c.bad[i & 1]) n = min(n, t.e0);
+        w.write_outputs(t, n, up, read_scale);
       }
     }
     if (SUMS && w.holds()) w.write(ps.carry + ((int64_t)head * a.runs + run) * W * W, W);
