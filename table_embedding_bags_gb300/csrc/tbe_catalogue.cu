@@ -231,6 +231,7 @@ struct Shared {
   uint64_t combine[2][4];
   uint64_t ask;                             // the next tile is wanted
   Tile tile[kTiles];
+  Job job[kMaxJobs];  // (a parameter's, with an index, would take hundreds of cycles to load)
   uint32_t tmem;
   int32_t dead;
   float2 half[2][kRowsM];
@@ -243,16 +244,16 @@ __device__ __forceinline__ int32_t tiles_of(const Job& j, int32_t mt, int32_t D,
   if (j.mode == kTable) return (v + kTileM - 1) / kTileM * column_tiles(D, half);
   return j.splits * mt * column_tiles(D, half);
 }
-__device__ __forceinline__ Tile tile_of(const GemmArgs& g, int32_t t, int32_t count) {
+__device__ __forceinline__ Tile tile_of(const GemmArgs& g, const Job* job, int32_t t, int32_t count) {
   const int32_t mt = (count + kTileM - 1) / kTileM;
   Tile r;
   r.job = 0;
   for (; r.job < g.jobs - 1; ++r.job) {
-    const int32_t n = tiles_of(g.job[r.job], mt, g.D, g.half);
+    const int32_t n = tiles_of(job[r.job], mt, g.D, g.half);
     if (t < n) break;
     t -= n;
   }
-  const Job& j = g.job[r.job];
+  const Job& j = job[r.job];
   r.mode = j.mode;
   r.split = 0;
   r.k0 = 0;
@@ -506,7 +507,7 @@ struct HiddenOf {
 template <int DT>
 __device__ __forceinline__ bool epilogue(const GemmArgs& g, Shared& s, const Tile& t, uint32_t tmem, int32_t count,
                                          int half, int row, uint32_t rank, uint32_t& turn) {
-  const Job& j = g.job[t.job];
+  const Job& j = s.job[t.job];
   const int64_t r = (int64_t)t.rb * kTileM + rank * kRowsM + row;
   const int begin = half * kHalfN, end = min(begin + kHalfN, t.blocks * 64);
   const bool edge = t.col + kTileN > g.V;
@@ -572,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       bar_init(&s.forgotten[k], 3 + 2 * kEpilogueWarps);  // the issuer, both copiers, all epilogue warps
     }
     s.dead = 0;
+    for (int k = 0; k < kMaxJobs; ++k) s.job[k] = g.job[k];
     bars_visible();
   }
   if (warp == 2) pair_alloc(&s.tmem, 512);
@@ -592,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const Tile t = s.tile[n % kTiles];
       if (t.mode >= 0 || t.steps >= 0) pair_arrive_relaxed(forgotten0 + n % kTiles * 8);  // (it has been read)
       if (t.mode < 0) break;
-      const Job& j = g.job[t.job];
+      const Job& j = s.job[t.job];
       const int32_t row0 = t.rb * kTileM + (int32_t)rank * kRowsM;
       const int32_t mine = t.blocks / 2;                       // B's blocks of this block
       const int32_t b_col = t.col + (int32_t)rank * mine * 64;  // its first column
@@ -653,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   } else if (warp == 3 && lane == 0 && rank == 0) {
     // gives out tiles, to both blocks
     int32_t total = 0;
-    for (int k = 0; k < g.jobs; ++k) total += tiles_of(g.job[k], (count + kTileM - 1) / kTileM, g.D, g.half);
+    for (int k = 0; k < g.jobs; ++k) total += tiles_of(s.job[k], (count + kTileM - 1) / kTileM, g.D, g.half);
     int32_t now = blockIdx.x >> 1;
     for (uint32_t n = 0;; ++n) {
       const uint32_t slot = n % kTiles;
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         if (!wait(&s.ask, (n - 1) & 1, s)) break;
         now = (int32_t)((gridDim.x >> 1) + atomicAdd(g.next, 1u));
       }
-      if (now < total) t = tile_of(g, now, count);
+      if (now < total) t = tile_of(g, s.job, now, count);
       if (n >= kTiles && !wait(&s.forgotten[slot], (n / kTiles - 1) & 1, s)) break;
       s.tile[slot] = t;
       const uint32_t other = pair_addr(&s.tile[slot], 1);
