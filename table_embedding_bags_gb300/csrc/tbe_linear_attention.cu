@@ -186,7 +186,7 @@ struct Control {
   uint64_t known[2], full, products, weighted, keys, out_done, add_done, add_read, out_read, state_ready, exchange, row_max[4];
   Tile tile[2];
   float pow[kPowers];
-  alignas(16) float by_col[32];  // powers over 32 neighbouring columns
+  alignas(16) float by_col[16];  // powers over 16 neighbouring columns
   float top_row[2][kTile];
   uint32_t top[3];
   int32_t bad[2];
@@ -210,7 +210,7 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile 
 }
 // (whole warps)
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& c) {
-  return __all_sync(kFull, mbar_wait(bar, parity & 1, 4) || wait_long(bar, parity & 1, &c.dead));
+  return __all_sync(kFull, mbar_wait(bar, parity & 1, 1) || wait_long(bar, parity & 1, &c.dead));
 }
 __device__ __forceinline__ void to_products() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -370,14 +370,6 @@ __device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, 
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
 template <int DT, int W, bool SUMS>
 struct Worker {
   static constexpr int kCols = W / 2;  // of the state and the outputs, to a thread
@@ -507,20 +499,18 @@ struct Worker {
   // Returns what the terms have to be multiplied by through `down`.
   __device__ __forceinline__ bool weigh_keys(int n, int n_terms, float& down) {
     constexpr int kChunks = Room<W>::operand / 16 / (32 * kWarps);
-    uint4 u[kChunks];
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-      u[i] = *reinterpret_cast<const uint4*>(room + Room<W>::k + (i * 32 * kWarps + warp * 32 + lane) * 16);
+    const int own = (warp * 32 + lane) * 16;
     float scale = ps.scale_add;
     down = 1.f;
     if (DT == TBE_F16) {
       __half2 top = __half2half2(__ushort_as_half(0));
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
-        const int r = (i * 32 * kWarps + warp * 32 + lane) / 8 % kTile;
-        if (place(r) < n) {
+        const int at = i * 32 * kWarps * 16 + own;
+        const uint4 u = *reinterpret_cast<const uint4*>(room + Room<W>::k + at);
+        if (place(at / 128 % kTile) < n) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(reinterpret_cast<const __half2*>(&u[i])[e]));
+          for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(reinterpret_cast<const __half2*>(&u)[e]));
         }
       }
       const float2 t = __half22float2(top);
@@ -531,14 +521,15 @@ struct Worker {
       down = pow2(-up);
     }
     const bool all = n == kTile;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kChunks; ++i) {
-      const int at = (i * 32 * kWarps + warp * 32 + lane) * 16, far = place(at / 128 % kTile);
+      const int at = i * 32 * kWarps * 16 + own, far = place(at / 128 % kTile);
+      const uint4 u = *reinterpret_cast<const uint4*>(room + Room<W>::k + at);
       const float w = exp2_of(-slope * (float)(n - 1 - far + ps.back)) * scale;
       float x[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 y = unpack2<DT>((&u[i].x)[e]);
+        const float2 y = unpack2<DT>((&u.x)[e]);
         x[2 * e] = y.x * w;
         x[2 * e + 1] = y.y * w;
       }
@@ -601,6 +592,7 @@ struct Worker {
     const int far = place(row);
     int from = 0;  // first place of this row's sequence
     const bool whole = t.e0 >= n;
+    const int place0 = ps.back ? kTile - 32 - quarter * 32 : quarter * 32, place31 = place0 + 31;  // of this warp's rows
     if (!whole) {
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
@@ -608,63 +600,27 @@ struct Worker {
         if (u) from = w * 32 + 31 - __clz((int)u);
       }
     }
-    // chunks of 32 columns: 0 for this warp's own rows, more for those before, less for those behind (nothing)
-    const int sooner = ps.back ? half * 2 - quarter : quarter - half * 2, step = ps.back ? 1 : -1;
-    float scale = ps.scale_tile;
-    const float lanes_f = (float)lane, sign = ps.back ? -1.f : 1.f;
     const uint32_t span = (uint32_t)(far - from);  // places from .. far take part
-    auto weigh = [&](float (&x)[32], int i) {
-      const int chunk = half * 2 + i, before = sooner + i * step;
-      if (before < 0) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = 0.f;
-        return;
-      }
-      if (before > 0) {
-        // gamma^distance in two parts: to the chunk's near end, and inside it
-        const float by = exp2_of(-slope * (float)(ps.back ? chunk * 32 - row : row - chunk * 32 - 31)) * scale;
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          float4 w = *reinterpret_cast<const float4*>(c.by_col + e);
-          mul2(w.x, w.y, by);
-          mul2(w.z, w.w, by);
-          x[e] *= w.x;
-          x[e + 1] *= w.y;
-          x[e + 2] *= w.z;
-          x[e + 3] *= w.w;
-        }
-        if (whole) return;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float away = sign * (lanes_f - (float)e);  // (exact)
-          x[e] *= exp2_of(-slope * away) * scale;
-        }
-      }
-      const int first = place(chunk * 32) - from;
-#pragma unroll
-      for (int e = 0; e < 32; ++e) x[e] = (uint32_t)(first + (ps.back ? -e : e)) <= span ? x[e] : 0.f;
-    };
+    // 16 columns at a time, in a loop that stays a loop: the code of a tile is run through once a tile by every warp,
+    // and what does not stay in the instruction caches costs more than it computes (with the loops below unrolled
+    // over 64 columns a warp's own 32 took 3,500 cycles, in a loop over two times 32 1,500).
+    const int step = ps.back ? -1 : 1;
+    float scale = ps.scale_tile;
     up = 0;
     if (DT == TBE_F16) {
       // the row's largest product that takes part, before its weight (at most the scale)
       float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int chunk = half * 2 + i, before = sooner + i * step;
-        if (before < 0) continue;
-        float x[32];
-        tc_ld32(tmem + Room<W>::tp + chunk * 32 + lanes(), x);
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const int col = half * 64 + k * 16, near = place(col), last = place(col + 15);
+        if (min(near, last) > place31) continue;  // all behind this warp's rows
+        float x[16];
+        tc_ld16(tmem + Room<W>::tp + col + lanes(), x);
         tc_wait_ld();
-        if (whole && before > 0) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[e]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int at = place(chunk * 32 + e);
-            top = fmaxf(top, at <= far && at >= from ? fabsf(x[e]) : 0.f);
-          }
+        for (int e = 0; e < 16; ++e) {
+          const int at = near + step * e;
+          top = fmaxf(top, at <= far && at >= from ? fabsf(x[e]) : 0.f);
         }
       }
       c.top_row[half][row] = top;
@@ -673,18 +629,46 @@ struct Worker {
       up = room_for(fmaxf(top, *(volatile float*)&c.top_row[half ^ 1][row]) * fabsf(scale));
       scale *= pow2(up);
     }
-    // Each half of the columns is written over what its own warps have read: chunk 0, then 1; chunk 3, then 2.
+    // Each half of the columns is written over what its own warps have read: the first from its first columns on, the
+    // second from its last.
+    const float away0 = (float)far;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      const int part = half ? 3 - k : k, col = half * 64 + part * 16, near = place(col), last = place(col + 15);
+      float x[16];
+      if (min(near, last) > place31) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int i = half ^ k;
-      float x[32];
-      tc_ld32(tmem + Room<W>::tp + (half * 2 + i) * 32 + lanes(), x);
-      tc_wait_ld();
-      weigh(x, i);
-      uint32_t packed[16];
+        for (int e = 0; e < 16; ++e) x[e] = 0.f;
+      } else {
+        tc_ld16(tmem + Room<W>::tp + col + lanes(), x);
+        tc_wait_ld();
+        if (whole && max(near, last) < place0) {
+          // gamma^distance in two parts: to the nearest of these columns, and among them
+          const float by = exp2_of(-slope * (float)(far - max(near, last))) * scale;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) packed[e] = pack2<DT>(x[2 * e], x[2 * e + 1]);
-      tc_st16(tmem + half * 96 + i * 16 + lanes(), packed);
+          for (int e = 0; e < 16; e += 4) {
+            float4 w = *reinterpret_cast<const float4*>(c.by_col + e);
+            mul2(w.x, w.y, by);
+            mul2(w.z, w.w, by);
+            x[e] *= w.x;
+            x[e + 1] *= w.y;
+            x[e + 2] *= w.z;
+            x[e + 3] *= w.w;
+          }
+        } else {
+          const float at = away0 - (float)near, sign = (float)step;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float away = fmaf(sign, -(float)e, at);  // (exact)
+            const float y = x[e] * (exp2_of(-slope * away) * scale);
+            x[e] = (uint32_t)(near - from + step * e) <= span ? y : 0.f;
+          }
+        }
+      }
+      uint32_t packed[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) packed[e] = pack2<DT>(x[2 * e], x[2 * e + 1]);
+      tc_st8(tmem + half * 96 + part * 8 + lanes(), packed);
     }
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
     tc_before_sync();
@@ -699,16 +683,16 @@ struct Worker {
     const float of_state = live ? c.pow[far + 1 - ps.back] * read_scale : 0.f, of_tile = DT == TBE_F16 ? pow2(-up) : 1.f;
     const int64_t token = ps.back ? a.N - t.p - kTile + row : t.p + row;
     uint16_t* to = ps.o + token * ps.so + head * ps.ho + half * kCols;
-#pragma unroll
-    for (int j = 0; j < kCols; j += 32) {
-      float x[32];
-      tc_ld32(tmem + Room<W>::to + half * kCols + j + lanes(), x);
+#pragma unroll 1
+    for (int j = 0; j < kCols; j += 16) {
+      float x[16];
+      tc_ld16(tmem + Room<W>::to + half * kCols + j + lanes(), x);
       if (t.live) {
-        float y[32];
-        tc_ld32(tmem + Room<W>::ts + half * kCols + j + lanes(), y);
+        float y[16];
+        tc_ld16(tmem + Room<W>::ts + half * kCols + j + lanes(), y);
         tc_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < 16; ++e) {
           if (DT == TBE_F16) x[e] *= of_tile;
           x[e] = live ? fmaf(y[e], of_state, x[e]) : x[e];
         }
@@ -716,31 +700,29 @@ struct Worker {
         tc_wait_ld();
         if (DT == TBE_F16) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] *= of_tile;
+          for (int e = 0; e < 16; ++e) x[e] *= of_tile;
         }
       }
-      if (j + 32 >= kCols) {
+      if (j + 16 >= kCols) {
         tc_before_sync();
         arrive(&c.out_read);
       }
       const int cols = a.d - half * kCols - j;
       if (far >= n || cols <= 0) continue;
-      uint32_t u[16];
+      uint32_t u[8];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) u[e] = pack2<DT>(x[2 * e], x[2 * e + 1]);
-      if (cols >= 32 && ps.piece_o == 32) {
-#pragma unroll
-        for (int e = 0; e < 16; e += 8)
-          asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + j + 2 * e), "r"(u[e]), "r"(u[e + 1]),
-                       "r"(u[e + 2]), "r"(u[e + 3]), "r"(u[e + 4]), "r"(u[e + 5]), "r"(u[e + 6]), "r"(u[e + 7])
-                       : "memory");
+      for (int e = 0; e < 8; ++e) u[e] = pack2<DT>(x[2 * e], x[2 * e + 1]);
+      if (cols >= 16 && ps.piece_o == 32) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + j), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                     "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                     : "memory");
       } else if (ps.piece_o >= 8) {
 #pragma unroll
-        for (int e = 0; e < 16; e += 2)
+        for (int e = 0; e < 8; e += 2)
           if (2 * e < cols) *reinterpret_cast<uint2*>(to + j + 2 * e) = make_uint2(u[e], u[e + 1]);
       } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < 8; ++e) {
           if (2 * e < cols) to[j + 2 * e] = (uint16_t)u[e];
           if (2 * e + 1 < cols) to[j + 2 * e + 1] = (uint16_t)(u[e] >> 16);
         }
@@ -802,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
   }
   const float decay = a.decay[head];
   for (int k = threadIdx.x; k < kPowers; k += kThreads) c.pow[k] = power(decay, k);
-  if (threadIdx.x < 32) c.by_col[threadIdx.x] = power(decay, ps.back ? threadIdx.x : 31 - threadIdx.x);
+  if (threadIdx.x < 16) c.by_col[threadIdx.x] = power(decay, ps.back ? threadIdx.x : 15 - threadIdx.x);
   if (warp == kWarps) tc_alloc(&c.tmem, R::cols);
   tc_before_sync();
   __syncthreads();
