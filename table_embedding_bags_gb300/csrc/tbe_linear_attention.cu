@@ -221,6 +221,7 @@ __device__ __forceinline__ void to_products() { asm volatile("fence.proxy.async.
 struct Marker {
   Starts st;
   bool one;         // a tile has one sequence
+  bool copied;      // rows behind the last token are zeros
   int64_t next;     // the first start not yet passed
   int64_t x;        // at(next + lane), read ahead
 
@@ -290,7 +291,7 @@ struct Marker {
     const bool goes_on = whole && !closes && !last_tile;
     t.adds = goes_on || (has_out && known && whole && closes);
     t.leaves = goes_on;
-    t.mixed = !(whole && (t.n == kTile || p + t.n == st.N));
+    t.mixed = !(whole && (t.n == kTile || (p + t.n == st.N && copied)));
     x = st.at_or_end(next + lane);
   }
 };
@@ -299,48 +300,29 @@ struct Marker {
 // the kernel: outputs, or (SUMS) what each run leaves
 // ---------------------------------------------------------------------------
 
-// One head's rows of a tile to an operand, where tensor copies cannot: from
-// token `first` on, zeros for tokens and columns that are not there.
+// One head's rows of a tile to an operand, where tensor copies cannot: rows
+// r0 .. r1 - 1, of which the first is token `first`'s.  Columns behind d and
+// rows outside keep what they hold: zeros, or rows of tiles before.
 template <int W>
-__device__ __forceinline__ void load_rows(uint8_t* dst, const uint16_t* src, int64_t stride, int64_t first, int64_t N, int d,
-                                          int piece, int thread) {
-  const int each = piece / 2, rows = 31 - __clz(W / each);  // a row is 2^rows pieces
-  auto place = [&](int i, int& r, int& c) {
-    r = i >> rows;
-    c = (i & ((1 << rows) - 1)) * each;
-    return dst + c / 64 * kBlock + r * 128 + ((c % 64 / 8) ^ (r & 7)) * 16 + c % 8 * 2;
-  };
-  if (piece > 2) {
+__device__ __forceinline__ void load_rows(uint8_t* dst, const uint16_t* src, int64_t stride, int64_t first, int r0, int r1,
+                                          int d, int piece, int thread) {
+  const int each = piece / 2, per_row = d / each;
+  // a warp takes a row at a time, and parts of two where they are short
+  const int at_once = per_row <= 16 ? 16 : 32;
+  const int lane = thread % at_once, step = 32 * kWarps / at_once;
+#pragma unroll 1
+  for (int c0 = lane; c0 < per_row; c0 += at_once) {
+    const int c = c0 * each;
+    uint8_t* column = dst + c / 64 * kBlock + c % 8 * 2;
+    const int chunk = c % 64 / 8;
+    const uint16_t* from = src + (first + thread / at_once) * stride + c;
 #pragma unroll 4
-    for (int i = thread; i < kTile << rows; i += 32 * kWarps) {
-      int r, c;
-      const uint32_t to = smem_u32(place(i, r, c));
-      const int64_t token = first + r;
-      const bool in = token >= 0 && token < N && c < d;
-      const uint16_t* from = in ? src + token * stride + c : src;
-      const uint32_t bytes = in ? piece : 0;  // the rest of the piece is zeros
-      if (piece == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-      else if (piece == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-      else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-    }
-    return;
-  }
-  constexpr int kAhead = 8;  // (the loads of so many elements at once)
-  for (int i0 = thread; i0 < kTile * W; i0 += kAhead * 32 * kWarps) {
-    uint16_t x[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      int r, c;
-      place(i0 + k * 32 * kWarps, r, c);
-      const int64_t token = first + r;
-      const bool in = token >= 0 && token < N && c < d;
-      x[k] = __ldg(in ? src + token * stride + c : src);
-      x[k] = in ? x[k] : 0;
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      int r, c;
-      *reinterpret_cast<uint16_t*>(place(i0 + k * 32 * kWarps, r, c)) = x[k];
+    for (int r = r0 + thread / at_once; r < r1; r += step, from += step * stride) {
+      const uint32_t to = smem_u32(column + r * 128 + ((chunk ^ (r & 7)) * 16));
+      if (piece == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+      else if (piece == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+      else if (piece == 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+      else asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(__ldg(from)) : "memory");
     }
   }
 }
@@ -373,6 +355,7 @@ __device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, 
 template <int DT, int W, bool SUMS>
 struct Worker {
   static constexpr int kCols = W / 2;  // of the state and the outputs, to a thread
+  static constexpr int kChunks = Room<W>::operand / 16 / (32 * kWarps);  // 16-byte pieces of an operand, to a thread
   const Args& a;
   const Pass& ps;
   Control& c;
@@ -495,33 +478,31 @@ struct Worker {
     }
     return bad;
   }
-  // The keys times scale_add gamma^(n - 1 - place + late), as a sum of terms; the weight is 0 behind the tile.
-  // Returns what the terms have to be multiplied by through `down`.
-  __device__ __forceinline__ bool weigh_keys(int n, int n_terms, float& down) {
-    constexpr int kChunks = Room<W>::operand / 16 / (32 * kWarps);
-    const int own = (warp * 32 + lane) * 16;
-    float scale = ps.scale_add;
-    down = 1.f;
-    if (DT == TBE_F16) {
-      __half2 top = __half2half2(__ushort_as_half(0));
+  // fp16: the power of two that the weighted keys are moved by.
+  __device__ __forceinline__ bool room_for_keys(int n, int& up) {
+    __half2 top = __half2half2(__ushort_as_half(0));
+#pragma unroll 2
+    for (int i = 0; i < kChunks; ++i) {
+      const int at = i * 32 * kWarps * 16 + (warp * 32 + lane) * 16;
+      const uint4 u = *reinterpret_cast<const uint4*>(room + Room<W>::k + at);
+      if (place(at / 128 % kTile) < n) {
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int at = i * 32 * kWarps * 16 + own;
-        const uint4 u = *reinterpret_cast<const uint4*>(room + Room<W>::k + at);
-        if (place(at / 128 % kTile) < n) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(reinterpret_cast<const __half2*>(&u)[e]));
-        }
+        for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(reinterpret_cast<const __half2*>(&u)[e]));
       }
-      const float2 t = __half22float2(top);
-      float most = fmaxf(t.x, t.y) * fabsf(scale);
-      if (!largest(most)) return false;
-      const int up = room_for(most);
-      scale *= pow2(up);
-      down = pow2(-up);
     }
+    const float2 t = __half22float2(top);
+    float most = fmaxf(t.x, t.y) * fabsf(ps.scale_add);
+    if (!largest(most)) return false;
+    up = room_for(most);
+    return true;
+  }
+  // The keys times 2^up scale_add gamma^(n - 1 - place + late), as a sum of
+  // terms; the weight is 0 behind the tile.
+  __device__ __forceinline__ void weigh_keys(int n, int n_terms, int up) {
+    const int own = (warp * 32 + lane) * 16;
+    const float scale = ps.scale_add * (DT == TBE_F16 ? pow2(up) : 1.f);
     const bool all = n == kTile;
-#pragma unroll 1
+#pragma unroll 2
     for (int i = 0; i < kChunks; ++i) {
       const int at = i * 32 * kWarps * 16 + own, far = place(at / 128 % kTile);
       const uint4 u = *reinterpret_cast<const uint4*>(room + Room<W>::k + at);
@@ -568,7 +549,6 @@ struct Worker {
     }
     to_products();
     arrive(&c.keys);
-    return true;
   }
 
   // S = gamma^n S + the tile's sum.
@@ -784,6 +764,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
   }
   const float decay = a.decay[head];
   for (int k = threadIdx.x; k < kPowers; k += kThreads) c.pow[k] = power(decay, k);
+  if (a.piece) {  // columns and rows that no copy fills
+    for (int k = threadIdx.x; k < R::s / 16; k += kThreads) reinterpret_cast<uint4*>(room)[k] = make_uint4(0, 0, 0, 0);
+    to_products();
+  }
   if (threadIdx.x < 16) c.by_col[threadIdx.x] = power(decay, ps.back ? threadIdx.x : 15 - threadIdx.x);
   if (warp == kWarps) tc_alloc(&c.tmem, R::cols);
   tc_before_sync();
@@ -800,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
 
   if (warp == kWarps) {
     // finds the tiles, starts the copies, issues the products
-    Marker m = {st, ps.in != nullptr || ps.out != nullptr, 0, 0};
+    Marker m = {st, ps.in != nullptr || ps.out != nullptr, a.piece == 0, 0, 0};
     if (!SUMS) m.seek(p0, lane);
     const bool live = !SUMS && run > 0 && __shfl_sync(kFull, m.x, 0) > p0;  // (m.x of lane 0: the first start)
     uint32_t states = 0, adds = 0, copies = 0;
@@ -950,16 +934,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
       const Tile& t = c.tile[i & 1];
       if (t.p < 0) break;
       if (a.piece) {
-        const int64_t first = ps.back ? a.N - t.p - kTile : t.p;
-        const int thread = warp * 32 + lane;
-        load_rows<W>(room + R::k, ps.k + head * ps.hk, ps.sk, first, a.N, a.d, a.piece, thread);
-        if (!SUMS) load_rows<W>(room + R::q, ps.q + head * ps.hq, ps.sq, first, a.N, a.d, a.piece, thread);
-        load_rows<W>(room + R::v, ps.v + head * ps.hv, ps.sv, first, a.N, a.d, a.piece, thread);
+        // rows of the tile's own places
+        const int r0 = ps.back ? kTile - t.n : 0, r1 = r0 + t.n, thread = warp * 32 + lane;
+        const int64_t first = ps.back ? a.N - t.p - t.n : t.p;
+        load_rows<W>(room + R::k, ps.k + head * ps.hk, ps.sk, first, r0, r1, a.d, a.piece, thread);
+        if (!SUMS) load_rows<W>(room + R::q, ps.q + head * ps.hq, ps.sq, first, r0, r1, a.d, a.piece, thread);
+        load_rows<W>(room + R::v, ps.v + head * ps.hv, ps.sv, first, r0, r1, a.d, a.piece, thread);
         cp_commit();
         cp_wait<0>();
         to_products();
         w.arrive(&c.full);
       }
+      const bool fresh = !SUMS && t.live && (t.begins || i == 0);  // a state comes from memory
       if (!SUMS) {
         if (t.begins) {
           if (ps.in) w.read(ps.in + (t.sequence * a.H + head) * matrix, a.d, ps.in_turned);
@@ -971,27 +957,27 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
 #pragma unroll
           for (int j = 0; j < w.kCols; ++j) w.s[j] = w.holds() ? __ldcg(carried + (int64_t)w.row * W + w.half * w.kCols + j) : 0.f;
         }
-        if (t.live && (t.begins || i == 0) && !w.publish()) break;
       }
       int n = t.n;
       if (t.mixed || t.adds) {
         if (!wait(&c.full, i, c)) break;
       }
       if (t.mixed && __any_sync(kFull, w.not_finite()) && lane == 0) c.bad[i & 1] = 1;
-      float down = 1.f;
-      int up = 0;
+      int up_keys = 0, up = 0;
+      if (DT == TBE_F16 && t.adds && !w.room_for_keys(n, up_keys)) break;
       if (!SUMS) {
         if (!wait(&c.products, i, c)) break;
         tc_after_sync();
         if (!w.weigh_products(t, n, i, up)) break;
+        if (fresh && !w.publish()) break;  // (its loads have had time)
       }
       // (while the products of the values go on)
-      if (t.adds && !w.weigh_keys(n, terms, down)) break;
+      if (t.adds) w.weigh_keys(n, terms, up_keys);
       const float read_scale = w.read_scale;
       if (t.adds) {
         if (!wait(&c.add_done, adds++, c)) break;
         tc_after_sync();
-        w.add(n, down);
+        w.add(n, DT == TBE_F16 ? pow2(-up_keys) : 1.f);
         if (t.leaves) {
           if (!w.publish()) break;
         } else if (!SUMS) {
