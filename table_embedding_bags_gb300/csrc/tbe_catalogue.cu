@@ -753,7 +753,8 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const RowArgs a) {
   __syncthreads();
   float mine = 0.f;
   if (threadIdx.x < kRows && row < count) {
-    for (int w = 1; w < 32; ++w) join(m, l, part[w][threadIdx.x].x, part[w][threadIdx.x].y);
+    const int warps = min(32, (a.parts * kRows + 31) / 32);  // that had any
+    for (int w = 1; w < warps; ++w) join(m, l, part[w][threadIdx.x].x, part[w][threadIdx.x].y);
     // where one logit stands out, its loss is the logarithm of a sum close to 1: kept apart from the maximum
     const float log_l = log2f(l);
     const int32_t n = a.rows[row];

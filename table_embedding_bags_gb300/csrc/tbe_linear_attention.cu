@@ -1012,6 +1012,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   float* c = ps.carry + (int64_t)head * a.runs * W * W + at;
   float s = 0.f;
   constexpr int kAhead = 16;
+#pragma unroll 1
   for (int r = 0; r < a.runs - 1; r += kAhead) {
     float x[kAhead];
     int32_t kind[kAhead];
@@ -1060,58 +1061,72 @@ struct StepArgs {
 };
 
 constexpr int kStepThreads = 256;
+constexpr int kStepCols = 64;  // of a block
 
-// A block per sequence and head; VEC columns of the state to a lane.
-template <int DT, int VEC>
+// A block per sequence, head and 64 value columns, 16 lanes to a row of them
+// and the rows in turn to 16 half-warps.  Bound by memory: the state is read
+// and written once.
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepArgs a) {
-  __shared__ float q[128], k[128], part[kStepThreads / 32][128];
-  const int64_t s = blockIdx.x / a.H;
-  const int head = (int)(blockIdx.x % a.H), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kRows = kStepThreads / 16;
+  __shared__ float q[128], k[128];
+  __shared__ float4 part[kRows][16];
+  const int parts = (a.d + kStepCols - 1) / kStepCols;
+  const int64_t matrix = blockIdx.x / parts, s = matrix / a.H;
+  const int head = (int)(matrix % a.H), c = blockIdx.x % parts * kStepCols + threadIdx.x % 16 * 4, r0 = threadIdx.x / 16;
   const int d = a.d;
   for (int i = threadIdx.x; i < d; i += kStepThreads) {
     q[i] = to_float<DT>(a.q[s * a.sq + head * a.hq + i]) * a.scale;
     k[i] = to_float<DT>(a.k[s * a.sk + head * a.hk + i]);
   }
   const float gamma = power(a.decay[head], 1);
-  __syncthreads();
-  float* m = a.state + (int64_t)blockIdx.x * d * d;
-  for (int c = lane * VEC; c < d; c += 32 * VEC) {
-    float v[VEC], o[VEC];
+  float* m = a.state + matrix * d * d;
+  float v[4], o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      v[e] = to_float<DT>(a.v[s * a.sv + head * a.hv + c + e]);
-      o[e] = 0.f;
+  for (int e = 0; e < 4; ++e) v[e] = c + e < d ? to_float<DT>(a.v[s * a.sv + head * a.hv + c + e]) : 0.f;
+  float x[128 / kRows][4];  // this lane's part of the state
+#pragma unroll
+  for (int n = 0; n < 128 / kRows; ++n) {
+    const int i = r0 + n * kRows;
+    const float* at = m + (int64_t)i * d + c;
+    if (VEC) {
+      const float4 y = i < d && c < d ? *reinterpret_cast<const float4*>(at) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x[n][0] = y.x;
+      x[n][1] = y.y;
+      x[n][2] = y.z;
+      x[n][3] = y.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[n][e] = i < d && c + e < d ? at[e] : 0.f;
     }
-#pragma unroll 8
-    for (int i = warp; i < d; i += kStepThreads / 32) {
-      float x[VEC];
-      float* at = m + (int64_t)i * d + c;
-      if (VEC == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(at);
-        x[0] = y.x;
-        x[1 % VEC] = y.y;
-        x[2 % VEC] = y.z;
-        x[3 % VEC] = y.w;
-      } else {
-        x[0] = *at;
-      }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        x[e] = fmaf(k[i], v[e], gamma * x[e]);
-        o[e] = fmaf(q[i], x[e], o[e]);
-      }
-      if (VEC == 4) *reinterpret_cast<float4*>(at) = make_float4(x[0], x[1 % VEC], x[2 % VEC], x[3 % VEC]);
-      else *at = x[0];
-    }
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) part[warp][c + e] = o[e];
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < d; c += kStepThreads) {
-    float o = 0.f;
 #pragma unroll
-    for (int w = 0; w < kStepThreads / 32; ++w) o += part[w][c];
-    a.o[s * a.so + head * a.ho + c] = (uint16_t)pack2<DT>(o, 0.f);
+  for (int n = 0; n < 128 / kRows; ++n) {
+    const int i = r0 + n * kRows;
+    if (i >= d) break;
+    float* at = m + (int64_t)i * d + c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[n][e] = fmaf(k[i], v[e], gamma * x[n][e]);
+      o[e] = fmaf(q[i], x[n][e], o[e]);
+    }
+    if (VEC) {
+      if (c < d) *reinterpret_cast<float4*>(at) = make_float4(x[n][0], x[n][1], x[n][2], x[n][3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < d) at[e] = x[n][e];
+    }
+  }
+  part[r0][threadIdx.x % 16] = make_float4(o[0], o[1], o[2], o[3]);
+  __syncthreads();
+  const int col = blockIdx.x % parts * kStepCols + threadIdx.x;
+  if (threadIdx.x < kStepCols && col < d) {
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) sum += reinterpret_cast<const float*>(part[r])[threadIdx.x];
+    a.o[s * a.so + head * a.ho + col] = (uint16_t)pack2<DT>(sum, 0.f);
   }
 }
 
@@ -1414,7 +1429,7 @@ int tbe_linear_attention_step(const tbe_linear_attention_inputs* in, float* stat
   const Rows out = {o, o_stride, o_head_stride};
   if (!state || !o || !fits(out, in->tokens, in->heads, in->head_dim)) return TBE_ERR_INVALID_ARG;
   if (((uintptr_t)o & 1) || ((uintptr_t)state & 3)) return TBE_ERR_UNSUPPORTED;
-  const int64_t blocks = (int64_t)in->sequences * in->heads;
+  const int64_t blocks = (int64_t)in->sequences * in->heads * ((in->head_dim + kStepCols - 1) / kStepCols);
   if (blocks >= (int64_t(1) << 31)) return TBE_ERR_UNSUPPORTED;
   StepArgs a = {};
   a.q = static_cast<const uint16_t*>(in->q);
@@ -1439,11 +1454,11 @@ int tbe_linear_attention_step(const tbe_linear_attention_inputs* in, float* stat
   const bool vec = a.d % 4 == 0 && ((uintptr_t)state & 15) == 0;
   const unsigned grid = (unsigned)blocks;
   if (in->dtype == TBE_F16) {
-    if (vec) step_kernel<TBE_F16, 4><<<grid, kStepThreads, 0, s>>>(a);
-    else step_kernel<TBE_F16, 1><<<grid, kStepThreads, 0, s>>>(a);
+    if (vec) step_kernel<TBE_F16, true><<<grid, kStepThreads, 0, s>>>(a);
+    else step_kernel<TBE_F16, false><<<grid, kStepThreads, 0, s>>>(a);
   } else {
-    if (vec) step_kernel<TBE_BF16, 4><<<grid, kStepThreads, 0, s>>>(a);
-    else step_kernel<TBE_BF16, 1><<<grid, kStepThreads, 0, s>>>(a);
+    if (vec) step_kernel<TBE_BF16, true><<<grid, kStepThreads, 0, s>>>(a);
+    else step_kernel<TBE_BF16, false><<<grid, kStepThreads, 0, s>>>(a);
   }
   const int rc = check_launch();
   trace_mark(s, "linear_attention_step");
