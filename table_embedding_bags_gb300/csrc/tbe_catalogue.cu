@@ -203,7 +203,7 @@ struct GemmArgs {
   float scale2;       // logit_scale in units of log 2
   const int32_t* label;
   const float* lse2;
-  float* mine;        // kSums: the label's logit
+  float* mine;        // kSums: the label's product, not scaled
   float2* part;       // kSums: [tiles along the vocabulary, Np]
   uint16_t* g;
   int32_t vc;
@@ -407,7 +407,7 @@ struct SumsOf {
       float x = 0.f;
 #pragma unroll
       for (int k = 0; k < 32; ++k) x = k == label - col ? v[k] : x;
-      g.mine[r] = x * g.scale2;
+      g.mine[r] = x;
     }
     if (edge) {
 #pragma unroll
@@ -717,6 +717,7 @@ struct RowArgs {
   const int32_t* count;
   const int32_t* rows;
   const float* mine;
+  float scale2;
   float* lse2;
   float* token_loss;
   float* lse;
@@ -755,12 +756,13 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const RowArgs a) {
   if (threadIdx.x < kRows && row < count) {
     const int warps = min(32, (a.parts * kRows + 31) / 32);  // that had any
     for (int w = 1; w < warps; ++w) join(m, l, part[w][threadIdx.x].x, part[w][threadIdx.x].y);
-    // where one logit stands out, its loss is the logarithm of a sum close to 1: kept apart from the maximum
+    // Where one logit stands out, its loss is the logarithm of a sum close to 1, kept apart from the maximum.  The
+    // exponentials are those of scaled products less the rounded m, so the label's is taken less m in the same way.
     const float log_l = log2f(l);
     const int32_t n = a.rows[row];
     a.lse2[row] = m + log_l;
     a.lse[n] = (m + log_l) * kLn2;
-    mine = ((m - a.mine[row]) + log_l) * kLn2;
+    mine = (log_l - fmaf(a.mine[row], a.scale2, -m)) * kLn2;
     a.token_loss[n] = mine;
   }
   if (warp != 0) return;
@@ -1073,6 +1075,7 @@ int run(const Call& c, cudaStream_t s) {
     r.count = p.count;
     r.rows = p.rows;
     r.mine = g.mine;
+    r.scale2 = g.scale2;
     r.lse2 = p.lse2;
     r.token_loss = c.token_loss;
     r.lse = c.lse;

@@ -80,7 +80,7 @@ def make(lengths, H, d, kind, seed, state=False, decays=(0.7, 0.01, 0.1, 0.0, 3.
         q, k, v = (normal(N, H, d).to(DT[kind]).cuda() for _ in range(3))
     r = {"q": q, "k": k, "v": v, "do": normal(N, H, d).to(DT[kind]).cuda(),
          "decay": torch.tensor([decays[h % len(decays)] for h in range(H)], device="cuda"),
-         "offsets": torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), device="cuda"),
+         "offsets": torch.tensor(np.concatenate([[0], np.cumsum(lengths)]).astype(np.int64), device="cuda"),
          "s0": normal(S, H, d, d).cuda() if state else None, "ds_last": normal(S, H, d, d).cuda() if state else None}
     return r
 
@@ -208,3 +208,235 @@ def test_gradients_of_the_definition_against_differences():
         up[i], down[i] = inputs[i] + h * way, inputs[i] - h * way
         slope = (value(*up) - value(*down)) / (2 * h)
         assert abs(slope - (g * way).sum()) <= 1e-8 * (1 + abs(slope))
+
+
+# ---------------------------------------------------------------------------
+# values and sizes at the edges
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 100])
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("what,value", [("v", float("nan")), ("v", float("inf")), ("k", float("nan")), ("q", float("nan")),
+                                        ("do", float("-inf")), ("v", "row before a tile's end")])
+def test_what_is_no_number_stays_in_its_sequence(tbe, what, value, kind, d, state):
+    lengths = [20, 31, 0, 90, 5, 300, 17]
+    c = make(lengths, 2, d, kind, 8, state)
+    clean = {n: (t.clone() if isinstance(t, torch.Tensor) else t) for n, t in c.items()}
+    bad, token = (1, 24) if isinstance(value, float) else (3, 125)
+    c[what] = c[what].clone()
+    c[what][token, 1] = value if isinstance(value, float) else float("nan")
+    f, b = both(tbe, c)
+    g, h = both(tbe, clean)
+    ends = np.cumsum(lengths)
+    inside = torch.zeros(sum(lengths), dtype=torch.bool, device="cuda")
+    inside[ends[bad] - lengths[bad]:ends[bad]] = True
+    half = torch.finfo(DT[kind]).eps / 2
+    outs = [(f.o, g.o)] * (what != "do") + [(x, y) for x, y in zip(b[:3], h[:3])]
+    assert any(not x[inside].isfinite().all() for x, _ in outs)
+    for x, y in outs:  # other sequences, and the same one's other head: as before but for their rounding
+        assert x[~inside].isfinite().all() and x[:, 0].isfinite().all()
+        size = y.double().abs().max()
+        assert ((x - y)[~inside].double().abs() <= 4 * half * size).all()
+    if state:
+        others = [s for s in range(len(lengths)) if s != bad]
+        assert f.s_last[others].isfinite().all() and b.ds0[others].isfinite().all()
+
+
+def both(tbe, c, scale=0.3):
+    f = tbe.tbe_linear_attention(c["q"], c["k"], c["v"], c["decay"], c["offsets"], s0=c["s0"], scale=scale,
+                                 want_last=c["s0"] is not None)
+    b = tbe.tbe_linear_attention_backward(c["do"], c["q"], c["k"], c["v"], c["decay"], c["offsets"], s0=c["s0"],
+                                          ds_last=c["ds_last"], scale=scale)
+    return f, b
+
+
+@gpu
+def test_a_state_that_is_no_number_stays_in_its_sequence(tbe):
+    c = make([20, 30, 0, 70], 2, 64, "bf16", 9, True)
+    c["s0"][1, 0, 3, 5] = float("inf")
+    f, _ = both(tbe, c)
+    assert not f.o[20:50, 0].isfinite().all()
+    assert f.o[:20].isfinite().all() and f.o[50:].isfinite().all() and f.o[:, 1].isfinite().all()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q,k,v,scale", [(300.0, 300.0, 1e-2, 1e-4), (1e-3, 1e-3, 1.0, 1e3), (1.0, 200.0, 200.0, 1e-4),
+                                         (1e-4, 1e-4, 1e-3, 1e8), (8e3, 5e-4, 1.0, 0.1)])
+def test_products_and_states_beyond_half_precision(tbe, q, k, v, scale, d):
+    """fp16 inputs whose products, or states, lie outside fp16's range, with outputs inside it."""
+    c = make([10, 200, 3], 2, d, "f16", 10, True)
+    for n, f in (("q", q), ("k", k), ("v", v)):
+        c[n] = (c[n].float() * f).half()
+    c["s0"] *= k * v
+    c["do"] = (c["do"].float() * 1e-2).half()
+    c["ds_last"] *= 1e-2
+    run_and_check(tbe, c, "f16", scale, grads=False)
+
+
+@gpu
+def test_rows_of_very_different_size(tbe):
+    c = make([60, 200], 1, 64, "f16", 11)
+    c["q"] = c["q"].clone()
+    c["q"][::3] *= 2.0**-12
+    c["k"] = c["k"].clone()
+    c["k"][::5] *= 2.0**-10
+    run_and_check(tbe, c, "f16", 1.0)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_decays_at_the_ends(tbe, kind):
+    c = make([100, 1, 300], 5, 48, kind, 12, True, decays=(0.0, 1e-6, 40.0, 200.0, 1e9))
+    run_and_check(tbe, c, kind)
+    c["decay"][4] = float("inf")  # only the token itself is remembered
+    f, b = both(tbe, c)
+    own = 0.3 * (wide(c["q"]) * wide(c["k"])).sum(-1, keepdim=True) * wide(c["v"])
+    assert torch.allclose(wide(f.o)[:, 4], own[:, 4], rtol=0.02, atol=1e-2) and all(x.isfinite().all() for x in b[:3])
+
+
+@gpu
+@pytest.mark.parametrize("lengths", [[], [0], [0, 0, 0]])
+def test_nothing_to_do(tbe, lengths):
+    c = make(lengths, 2, 32, "bf16", 13, True)
+    f, b = both(tbe, c)
+    assert f.o.shape == (0, 2, 32) and torch.equal(f.s_last, c["s0"]) and torch.equal(b.ds0, c["ds_last"])
+    c["s0"] = None
+    f = tbe.tbe_linear_attention(c["q"], c["k"], c["v"], c["decay"], c["offsets"], want_last=True)
+    assert not f.s_last.any()
+
+
+@gpu
+def test_only_some_states(tbe):
+    """Gradients where states come in but no gradient of the last ones does, and the other way round."""
+    c = make([30, 100, 0], 2, 40, "bf16", 14, True)
+    run_and_check(tbe, {**c, "ds_last": torch.zeros_like(c["ds_last"])}, "bf16")
+    q, k, v, do, s0 = (wide(c[n]) for n in ("q", "k", "v", "do", "s0"))
+    b = tbe.tbe_linear_attention_backward(c["do"], c["q"], c["k"], c["v"], c["decay"], c["offsets"], s0=c["s0"], scale=0.3)
+    want = gradients(do, q, k, v, wide(c["decay"]), c["offsets"].tolist(), s0, None, 0.3)
+    for x, w in zip(b, want):
+        assert float((wide(x) - w).norm()) <= 0.01 * float(w.norm())
+
+
+@gpu
+@pytest.mark.parametrize("offsets", [[0, 50, 40, 100], [5, 50, 100, 100], [0, 50, 100, 90], [0, -7, 100, 100],
+                                     [0, 10**12, 100, 100], [100, 100, 100, 100], [0, 0, 0, 0]])
+def test_broken_offsets_are_reported(tbe, offsets):
+    c = make([30, 30, 40], 2, 64, "bf16", 15, True)
+    c["offsets"] = torch.tensor(offsets, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tbe.tbe_linear_attention(c["q"], c["k"], c["v"], c["decay"], c["offsets"], s0=c["s0"], want_last=True, dev_status=st)
+    assert st.item() == tbe.TBE_DEV_BAD_OFFSETS
+    st.zero_()
+    tbe.tbe_linear_attention_backward(c["do"], c["q"], c["k"], c["v"], c["decay"], c["offsets"], s0=c["s0"],
+                                      ds_last=c["ds_last"], dev_status=st)
+    assert st.item() == tbe.TBE_DEV_BAD_OFFSETS
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 66])
+def test_given_outputs_and_what_lies_between(tbe, d):
+    c = make([70, 200], 3, d, "f16", 16)
+    want = tbe.tbe_linear_attention(c["q"], c["k"], c["v"], c["decay"], c["offsets"]).o
+    room = torch.full((270, 3, d + 10), 7.0, dtype=torch.float16, device="cuda")
+    got = tbe.tbe_linear_attention(c["q"], c["k"], c["v"], c["decay"], c["offsets"], out=room[:, :, 2:2 + d]).o
+    assert got.data_ptr() == room[:, :, 2:].data_ptr() and torch.equal(got, want)
+    assert (room[:, :, :2] == 7).all() and (room[:, :, 2 + d:] == 7).all()
+    grads = torch.full((3, 3, 270, d + 1), 7.0, dtype=torch.float16, device="cuda")
+    b = tbe.tbe_linear_attention_backward(c["do"], c["q"], c["k"], c["v"], c["decay"], c["offsets"],
+                                          out=tuple(g[:, :, :d].transpose(0, 1) for g in grads))
+    alone = tbe.tbe_linear_attention_backward(c["do"], c["q"], c["k"], c["v"], c["decay"], c["offsets"])
+    assert all(torch.equal(x, y) for x, y in zip(b[:3], alone[:3])) and (grads[..., d] == 7).all()
+
+
+@gpu
+def test_streams_and_graphs(tbe):
+    """Side by side on two streams, and captured and replayed with other contents, as on the current stream."""
+    c, e = make([1500, 700, 3], 2, 64, "bf16", 17, True), make([900, 40, 1263], 2, 64, "bf16", 18, True)
+    want = [both(tbe, x) for x in (c, e)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = both(tbe, e)
+    here = both(tbe, c)
+    torch.cuda.current_stream().wait_stream(side)
+    same(here, want[0])
+    same(other, want[1])
+    given = tbe.tbe_linear_attention(e["q"], e["k"], e["v"], e["decay"], e["offsets"], s0=e["s0"], scale=0.3, want_last=True,
+                                     stream=side)
+    side.synchronize()
+    assert torch.equal(given.o, want[1][0].o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = both(tbe, c)
+    for n in ("q", "k", "v", "do", "offsets", "s0", "ds_last"):
+        c[n].copy_(e[n])
+    graph.replay()
+    same(captured, want[1])
+
+
+def same(a, b):
+    for x, y in zip([*a[0], *a[1]], [*b[0], *b[1]]):
+        assert torch.equal(x, y)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("B,H,d,layout", [(1, 1, 1, "plain"), (3, 2, 63, "off"), (200, 3, 64, "slices"), (5, 4, 128, "heads first"),
+                                          (7, 1, 127, "plain"), (33, 5, 100, "slices")])
+def test_single_tokens(tbe, B, H, d, layout, kind):
+    n = make([1] * B, H, d, kind, 19, True, layout=layout)
+    state = n["s0"].clone()
+    o = tbe.tbe_linear_attention_step(n["q"], n["k"], n["v"], n["decay"], state, scale=0.2)
+    args = [wide(n[x]) for x in "qkv"]
+    offsets = list(range(B + 1))
+    want_o, want = definition(*args, wide(n["decay"]), offsets, wide(n["s0"]), 0.2)
+    size_o, size = definition(*(x.abs() for x in args), wide(n["decay"]), offsets, wide(n["s0"]).abs(), 0.2)
+    close(o, want_o, size_o, torch.finfo(DT[kind]).eps / 2, (d + 4) * 2.0**-23, "o")
+    close(state, want, size, 0.0, 2.0**-21, "state")
+
+
+@gpu
+def test_refusals(tbe):
+    c = make([20, 30], 2, 64, "bf16", 20, True)
+    args = dict(q=c["q"], k=c["k"], v=c["v"], decay=c["decay"], offsets=c["offsets"], s0=c["s0"])
+
+    def refused(**other):
+        with pytest.raises(tbe.TBEError):
+            tbe.tbe_linear_attention(**{**args, **other})
+        if not {"out", "want_last"} & set(other):
+            with pytest.raises(tbe.TBEError):
+                tbe.tbe_linear_attention_backward(c["do"], **{**args, **other})
+
+    for name in "qkv":
+        refused(**{name: args[name].cpu()})
+        refused(**{name: args[name].float()})
+        refused(**{name: args[name][:-1]})
+        refused(**{name: args[name].transpose(1, 2)})
+        refused(**{name: args[name][:, :1].expand(50, 2, 64)})
+    refused(q=c["q"].float(), k=c["k"].float(), v=c["v"].float())
+    big = torch.zeros(50, 2, 129, dtype=torch.bfloat16, device="cuda")
+    refused(q=big, k=big, v=big, s0=None)
+    refused(decay=None)
+    refused(decay=c["decay"].double())
+    refused(decay=c["decay"][:1])
+    refused(offsets=c["offsets"].float())
+    refused(offsets=c["offsets"][:0])
+    refused(offsets=c["offsets"][:1])
+    refused(s0=c["s0"][:1])
+    refused(s0=c["s0"].half())
+    refused(scale=float("inf"))
+    refused(out=torch.empty(50, 2, 64, device="cuda"))
+    refused(out=c["q"][:, :, :32])
+    with pytest.raises(tbe.TBEError):
+        tbe.tbe_linear_attention_backward(c["do"][:3], **args)
+    with pytest.raises(tbe.TBEError):
+        tbe.tbe_linear_attention_backward(c["do"], **args, ds_last=c["ds_last"][:1])
+    with pytest.raises(tbe.TBEError):
+        tbe.tbe_linear_attention_backward(c["do"], **args, out=(None, None))
+    n = make([1, 1], 2, 64, "bf16", 21, True)
+    for state in (None, n["s0"][:1], n["s0"].half(), n["s0"].transpose(2, 3)):
+        with pytest.raises(tbe.TBEError):
+            tbe.tbe_linear_attention_step(n["q"], n["k"], n["v"], n["decay"], state)
