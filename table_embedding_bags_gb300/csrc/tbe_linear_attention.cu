@@ -1005,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
 template <int W>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
   wait_predecessor();
-  const Pass& ps = a.pass[blockIdx.y];
+  const Pass ps = a.pass[blockIdx.y];
   constexpr int kPerHead = W * W / 256;
   const int head = blockIdx.x / kPerHead, at = blockIdx.x % kPerHead * 256 + threadIdx.x;
   const float through = power(a.decay[head], a.run);
@@ -1014,23 +1014,20 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   constexpr int kAhead = 16;
 #pragma unroll 1
   for (int r = 0; r < a.runs - 1; r += kAhead) {
+    // (volatile: loads that the compiler moves to their uses wait one after another, 25 us for 36 runs)
     float x[kAhead];
     int32_t kind[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {  // (what is not there to be read is not used either)
-      const int at_run = min(r + k, a.runs - 2);
-      kind[k] = __ldcg(ps.kind + at_run);
-      x[k] = __ldcg(c + (int64_t)at_run * W * W);
+    for (int k = 0; k < kAhead; ++k) {  // what is not there is read from the last run, and not used
+      const int64_t at_run = min(r + k, a.runs - 2);
+      asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(kind[k]) : "l"(ps.kind + at_run));
+      asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(x[k]) : "l"(c + at_run * (W * W)));
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (r + k >= a.runs - 1) break;
-      if (kind[k] == kThrough) {
-        s = fmaf(through, s, x[k]);
-        c[(int64_t)(r + k) * W * W] = s;
-      } else {
-        s = x[k];
-      }
+      const bool through_it = kind[k] == kThrough;
+      s = through_it ? fmaf(through, s, x[k]) : x[k];
+      if (through_it && r + k < a.runs - 1) c[(int64_t)(r + k) * (W * W)] = s;
     }
   }
 }
