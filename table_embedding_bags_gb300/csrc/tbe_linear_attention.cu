@@ -40,6 +40,18 @@
 // cores cut sums off.  fp16 lacks fp32's range, so there each of the three is
 // first moved by a power of two that its largest value names: products by
 // row, the state and the keys by tile.
+//
+// What bounds it: the latency of a tile's chain, with one block of 128-wide
+// heads to an SM (its operands take 194 KB) or two of 64-wide ones.  In cycles,
+// 128 wide: copies 1,900, q k^T 1,100, weights 1,500-2,100, keys 2,100, products
+// of the values and keys 1,700, state 300, outputs 2,200 beside the next copies:
+// 9,000 a tile, where its bytes alone would take 5,600.  Under ncu the outputs of
+// 40,000 x 4 x 128 bf16 read DRAM at 28 % of its rate with 15 % of the tensor
+// cores' cycles and 27 % of the issue slots in use; 64 wide, fp16: 28, 13, 45 %.
+// Prefill of 100,003 x 4 x 128 bf16 187 us (its bytes: 60 us), training pass of
+// 65,537 x 16 x 64 f16 with states 1,147 us (159), of 2,048 sequences, 40,960 x
+// 8 x 64 bf16 232 us (50).  The same recurrences in tiles of 64 with mma.sync,
+// four warps to a block, took 418, 1,466 and 358 us.
 #include "tbe_tensor.cuh"
 
 #include <algorithm>
@@ -340,6 +352,14 @@ __device__ __forceinline__ void tma_ahead3(const CUtensorMap* map, int32_t col, 
                : "memory");
 }
 
+// Where tile i's values lie: without queries their place takes those of every
+// other tile, so that a tile's copies go on beside the products of the one
+// before (prefill of 100,003 x 4 x 128 bf16 202 -> 187 us).
+template <int W, bool SUMS>
+__device__ __forceinline__ int values_at(int piece, uint32_t i) {
+  return SUMS && piece == 0 && (i & 1) ? Room<W>::q : Room<W>::v;
+}
+
 // Descriptor of an operand whose next 64 rows (along M or N) are `apart` bytes on.
 __device__ __forceinline__ uint64_t desc_of(uint32_t addr, uint32_t apart) {
   return (tc_desc(addr) & ~(0x3fffull << 16)) | ((uint64_t)(apart >> 4) << 16);
@@ -464,12 +484,12 @@ struct Worker {
   __device__ __forceinline__ int place(int r) const { return ps.back ? kTile - 1 - r : r; }
 
   // Whether the tile's values hold an infinity or a NaN.
-  __device__ __forceinline__ bool not_finite() const {
+  __device__ __forceinline__ bool not_finite(int values) const {
     constexpr uint32_t kInf = DT == TBE_BF16 ? 0x7f80u : 0x7c00u;
     bool bad = false;
 #pragma unroll 4
     for (int i = warp * 32 + lane; i < Room<W>::operand / 16; i += 32 * kWarps) {
-      const uint4 u = *reinterpret_cast<const uint4*>(room + Room<W>::v + i * 16);
+      const uint4 u = *reinterpret_cast<const uint4*>(room + values + i * 16);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t x = (&u.x)[e];
@@ -809,10 +829,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
     Tile following = find(begin, live);
     // The values from place n on are set to 0: some value of the tile is an infinity or a NaN, and those of other
     // sequences are multiplied by 0.
-    auto drop = [&](int n) {
+    auto drop = [&](int n, int values) {
       for (int i = lane; i < R::operand / 16; i += 32) {
         const int r = i / 8 % kTile;
-        if ((ps.back ? kTile - 1 - r : r) >= n) *reinterpret_cast<uint4*>(room + R::v + i * 16) = make_uint4(0, 0, 0, 0);
+        if ((ps.back ? kTile - 1 - r : r) >= n) *reinterpret_cast<uint4*>(room + values + i * 16) = make_uint4(0, 0, 0, 0);
       }
       to_products();
       __syncwarp();
@@ -824,31 +844,35 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
 #pragma unroll
       for (int b = 0; b < W / 64; ++b) {
         tma_ahead3(&a.map[ps.mk], b * 64, head, first);
-        if (!SUMS) tma_ahead3(&a.map[ps.mq], b * 64, head, first);
+        tma_ahead3(&a.map[ps.mq], b * 64, head, first);
         tma_ahead3(&a.map[ps.mv], b * 64, head, first);
+      }
+    };
+    auto load = [&](const Tile& t, uint32_t i) {
+      if (t.p < 0 || a.piece) return;
+      ++copies;
+      if (lane != 0) return;
+      bar_expect(&c.full, (SUMS ? 2 : 3) * R::operand);
+      const int32_t first = (int32_t)(ps.back ? a.N - t.p - kTile : t.p);
+#pragma unroll
+      for (int b = 0; b < W / 64; ++b) {
+        tma_load3(room0 + R::k + b * kBlock, &a.map[ps.mk], b * 64, head, first, &c.full);
+        if (!SUMS) tma_load3(room0 + R::q + b * kBlock, &a.map[ps.mq], b * 64, head, first, &c.full);
+        tma_load3(room0 + values_at<W, SUMS>(a.piece, i) + b * kBlock, &a.map[ps.mv], b * 64, head, first, &c.full);
       }
     };
     for (uint32_t i = 0;; ++i) {
       const Tile t = following;
+      const int values = values_at<W, SUMS>(a.piece, i);
       // (the products and copies of the tile before are through)
       if (lane == 0) {
         c.tile[i & 1] = t;
         c.bad[i & 1] = 0;
         bar_arrive(&c.known[i & 1]);
-        if (t.p >= 0 && a.piece == 0) {
-          bar_expect(&c.full, (SUMS ? 2 : 3) * R::operand);
-          const int32_t first = (int32_t)(ps.back ? a.N - t.p - kTile : t.p);
-#pragma unroll
-          for (int b = 0; b < W / 64; ++b) {
-            tma_load3(room0 + R::k + b * kBlock, &a.map[ps.mk], b * 64, head, first, &c.full);
-            if (!SUMS) tma_load3(room0 + R::q + b * kBlock, &a.map[ps.mq], b * 64, head, first, &c.full);
-            tma_load3(room0 + R::v + b * kBlock, &a.map[ps.mv], b * 64, head, first, &c.full);
-          }
-        }
       }
+      if (!SUMS || i == 0) load(t, i);
       __syncwarp();
       if (t.p < 0) break;
-      copies += a.piece == 0;
       if (!wait(&c.full, i, c)) break;
       // the sum for the state lies where these products go (64 columns), or has its own place
       if (added && !wait(&c.add_read, adds - 1, c)) break;
@@ -880,12 +904,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
         ahead(following);
         if (!wait(&c.weighted, i, c)) break;
         tc_after_sync();
-        if (t.mixed && *(volatile int32_t*)&c.bad[i & 1]) drop(t.e0);
+        if (t.mixed && *(volatile int32_t*)&c.bad[i & 1]) drop(t.e0, values);
         if (lane == 0) {
           const uint32_t idesc = tc_idesc(format, 0, 1, kTile, W);
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
-            tc_mma_tmem(tmem + R::to, tmem + R::weighted(k), desc_of(room0 + R::v + k * 2048, kBlock), idesc, k > 0);
+            tc_mma_tmem(tmem + R::to, tmem + R::weighted(k), desc_of(room0 + values + k * 2048, kBlock), idesc, k > 0);
           tc_commit(&c.out_done);
         }
         __syncwarp();
@@ -893,7 +917,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
       if (t.adds) {
         if (!wait(&c.keys, adds, c)) break;
         tc_after_sync();
-        if (SUMS && t.mixed && *(volatile int32_t*)&c.bad[i & 1]) drop(t.n);
+        if (SUMS) {
+          if (t.mixed && *(volatile int32_t*)&c.bad[i & 1]) drop(t.n, values);
+          following = find(t.p + t.n, false);
+          load(following, i + 1);  // the keys have been read, and the values go elsewhere
+          __syncwarp();
+        }
         if (lane == 0) {
           // (64 columns: the products' other 64 rows, of what follows in memory, are not looked at)
           const uint32_t idesc = tc_idesc(format, 1, 1, kTile, W);
@@ -901,17 +930,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
               tc_mma(tmem + R::ta, desc_of(terms0 + x * R::operand + k * 2048, kBlock),
-                     desc_of(room0 + R::v + k * 2048, kBlock), idesc, x < terms - 1 || k > 0);
+                     desc_of(room0 + values + k * 2048, kBlock), idesc, x < terms - 1 || k > 0);
           tc_commit(&c.add_done);
         }
         __syncwarp();
         ++adds;
       }
       added = t.adds;
-      if (SUMS) {
-        following = find(t.p + t.n, false);
-        ahead(following);
-      } else if (t.mixed && *(volatile int32_t*)&c.bad[i & 1] && t.e0 < t.n) {
+      if (!SUMS && t.mixed && *(volatile int32_t*)&c.bad[i & 1] && t.e0 < t.n) {
         m.seek(t.p + t.e0, lane);  // the others were told by the same word that the tile ends there
         following = find(t.p + t.e0, false);
       }
@@ -962,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
       if (t.mixed || t.adds) {
         if (!wait(&c.full, i, c)) break;
       }
-      if (t.mixed && __any_sync(kFull, w.not_finite()) && lane == 0) c.bad[i & 1] = 1;
+      if (t.mixed && __any_sync(kFull, w.not_finite(values_at<W, SUMS>(a.piece, i))) && lane == 0) c.bad[i & 1] = 1;
       int up_keys = 0, up = 0;
       if (DT == TBE_F16 && t.adds && !w.room_for_keys(n, up_keys)) break;
       if (!SUMS) {
