@@ -640,7 +640,8 @@ int tbe_preference_loss_backward_low(const tbe_preference_inputs* in, const floa
  *   dtype   : TBE_F16 or TBE_BF16 (TBE_F32: TBE_ERR_UNSUPPORTED).  Products
  *             and sums are fp32; probabilities are rounded to dtype before
  *             they are multiplied for the gradients.
- * Limits: 1 <= tokens <= 2^24, vocab <= 2^30, width <= 2^16.
+ * Limits: 1 <= tokens <= 2^24, vocab <= 2^30, width <= 2^16, tokens * vocab <
+ * 2^47 (in whole tiles of 256 x 256).
  */
 typedef struct tbe_catalogue_inputs {
   const void* hidden;

@@ -143,16 +143,9 @@ struct CopyArgs {
   int32_t V;
 };
 
-__global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
-  wait_predecessor();
-  const int lane = threadIdx.x & 31;
-  const int64_t k = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (k < a.N && a.zero && !taken(a.labels[k], a.V))
-    for (int c = lane; c < a.D; c += 32) a.zero[k * a.zero_stride + c] = 0;
-  const int64_t count = a.count ? *a.count : a.N;
-  if (k >= min(a.Np, (count + 255) / 256 * 256)) return;
+// A warp's row: from src, or zeros.
+__device__ __forceinline__ void copy_row(const CopyArgs& a, int64_t k, const uint16_t* src, int lane) {
   uint16_t* dst = a.dst + k * a.Dp;
-  const uint16_t* src = k < count ? a.src + (a.rows ? (int64_t)a.rows[k] : k) * a.src_stride : nullptr;
   if (a.vec == 8) {
     for (int c = lane * 8; c < a.Dp; c += 256) {
       const uint4 v = src && c < a.D ? __ldg(reinterpret_cast<const uint4*>(src + c)) : make_uint4(0, 0, 0, 0);
@@ -164,6 +157,91 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
       *reinterpret_cast<uint32_t*>(dst + c) = lo | hi << 16;
     }
   }
+}
+__device__ __forceinline__ void clear_row(const CopyArgs& a, int64_t n, int lane) {
+  for (int c = lane; c < a.D; c += 32) a.zero[n * a.zero_stride + c] = 0;
+}
+
+__global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
+  wait_predecessor();
+  const int lane = threadIdx.x & 31;
+  const int64_t k = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (k < a.N && a.zero && !taken(a.labels[k], a.V)) clear_row(a, k, lane);
+  const int64_t count = a.count ? *a.count : a.N;
+  if (k >= min(a.Np, (count + 255) / 256 * 256)) return;
+  copy_row(a, k, k < count ? a.src + (a.rows ? (int64_t)a.rows[k] : k) * a.src_stride : nullptr, lane);
+}
+
+// Both steps in one launch, for batches whose labels every block can look at:
+// 8 x 1,000 x 64 bf16, the loss alone, 16.4 -> 14.0 us.
+constexpr int kFewTokens = 2048;
+struct FewArgs {
+  PickArgs p;
+  CopyArgs c;
+};
+__global__ void __launch_bounds__(256) pick_copy_kernel(const FewArgs a) {
+  __shared__ uint32_t mask[kFewTokens / 32];       // which of 32 tokens take part
+  __shared__ int32_t first[kFewTokens / 32 + 1];   // the row of the first of them
+  static_assert(kFewTokens / 32 == 64, "two groups to a lane");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int N = (int)a.p.N, groups = (N + 31) / 32;
+  bool bad = false;
+  for (int g = warp; g < 64; g += 8) {
+    const int n = g * 32 + lane;
+    const int64_t y = n < N ? a.p.labels[n] : -1;
+    const uint32_t m = __ballot_sync(kFull, taken(y, a.p.V));
+    bad |= y >= a.p.V;
+    if (lane == 0) mask[g] = m;
+  }
+  if (bad && blockIdx.x == 0) report(a.p.status, TBE_DEV_BAD_INDEX);
+  __syncthreads();
+  if (warp == 0) {
+    const int c0 = __popc(mask[2 * lane]), c1 = __popc(mask[2 * lane + 1]);
+    int sum = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int below = __shfl_up_sync(kFull, sum, o);
+      if (lane >= o) sum += below;
+    }
+    first[2 * lane] = sum - c0 - c1;
+    first[2 * lane + 1] = sum - c1;
+    if (lane == 31) first[64] = sum;
+  }
+  __syncthreads();
+  const int total = first[64];
+  if (blockIdx.x == 0) {
+    for (int g = warp; g < groups; g += 8) {
+      const int n = g * 32 + lane;
+      if (mask[g] >> lane & 1) {
+        const int k = first[g] + __popc(mask[g] & ((1u << lane) - 1));
+        a.p.rows[k] = n;
+        a.p.label[k] = (int32_t)a.p.labels[n];
+        if (a.p.given) a.p.lse2[k] = a.p.given[n] * kLog2e;
+      } else if (n < N && a.p.lse) {
+        a.p.lse[n] = 0.f;
+        a.p.token_loss[n] = 0.f;
+      }
+    }
+    for (int k = total + threadIdx.x; k < (int)a.p.Np; k += 256) {
+      a.p.label[k] = -1;
+      a.p.lse2[k] = INFINITY;
+    }
+    for (int k = threadIdx.x; k < a.p.zeros; k += 256) a.p.zero[k] = 0;
+    if (threadIdx.x == 0) {
+      *a.p.count = total;
+      if (a.p.loss && total == 0) *a.p.loss = 0.f;
+    }
+  }
+  const int k = blockIdx.x * 8 + warp;
+  if (k < N && a.c.zero && !(mask[k / 32] >> (k % 32) & 1)) clear_row(a.c, k, lane);
+  if (k >= min((int)a.p.Np, (total + 255) / 256 * 256)) return;
+  const uint16_t* src = nullptr;
+  if (k < total) {
+    // the group whose first row is the last one at or before k, and the token of its (k - first)th bit
+    const int g = __popc(__ballot_sync(kFull, first[lane] <= k)) + __popc(__ballot_sync(kFull, first[32 + lane] <= k)) - 1;
+    src = a.c.src + (int64_t)(g * 32 + (int)__fns(mask[g], 0, k - first[g] + 1)) * a.c.src_stride;
+  }
+  copy_row(a.c, k, src, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -1005,10 +1083,6 @@ int run(const Call& c, cudaStream_t s) {
   p.loss = c.loss;
   p.given = c.given;
   p.status = c.status;
-  int st = start(pick_kernel, 1, kPickThreads, 0, false, s, p);
-  if (st != TBE_OK) return st;
-  trace_mark(s, "catalogue_pick");
-
   CopyArgs k = {};
   k.src = static_cast<const uint16_t*>(in.hidden);
   k.src_stride = in.hidden_stride;
@@ -1024,7 +1098,14 @@ int run(const Call& c, cudaStream_t s) {
   k.zero_stride = c.dhidden_stride;
   k.labels = in.labels;
   k.V = in.vocab;
-  st = start(copy_kernel, w.Np / 8, 256, 0, true, s, k);
+  int st;
+  if (N <= kFewTokens) {
+    st = start(pick_copy_kernel, w.Np / 8, 256, 0, false, s, FewArgs{p, k});
+  } else {
+    if ((st = start(pick_kernel, 1, kPickThreads, 0, false, s, p)) != TBE_OK) return st;
+    trace_mark(s, "catalogue_pick");
+    st = start(copy_kernel, w.Np / 8, 256, 0, true, s, k);
+  }
   if (st != TBE_OK) return st;
   trace_mark(s, "catalogue_rows");
   const void* table = in.weights;
@@ -1143,6 +1224,8 @@ int check(const tbe_catalogue_inputs* in) {
   if (!in->hidden || !in->weights || !in->labels || in->hidden_stride < in->width || in->weights_stride < in->width)
     return TBE_ERR_INVALID_ARG;
   if (in->tokens > kMaxTokens || in->vocab > (1 << 30) || in->width > (1 << 16)) return TBE_ERR_UNSUPPORTED;
+  if (whole(in->tokens, kTileM) / kTileM * (whole(in->vocab, kTileN) / kTileN) >= (int64_t(1) << 31))
+    return TBE_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
   if (((uintptr_t)in->hidden | (uintptr_t)in->weights) & 1 || ((uintptr_t)in->labels & 7)) return TBE_ERR_UNSUPPORTED;
   return TBE_OK;
 }

@@ -1296,18 +1296,21 @@ struct Maps {
     r[n] = x;
     return n++;
   }
+  // (a stride that nothing is reached by need not be one that tensor copies take)
+  static int64_t token_stride(const Args& a, const Rows& x) { return a.N > 1 ? x.stride : 128; }
+  static int64_t head_stride(const Args& a, const Rows& x) { return a.H > 1 ? x.head : 128; }
   int fill(Args& a, int32_t dtype) const {
     a.piece = 16;
     bool copies = a.N < (int64_t(1) << 31) - kTile;
     for (int i = 0; i < n; ++i) {
-      copies &= piece_of(r[i].p, r[i].stride, r[i].head, 8, 16) == 16;
+      copies &= piece_of(r[i].p, token_stride(a, r[i]), head_stride(a, r[i]), 8, 16) == 16;
       a.piece = std::min(a.piece, piece_of(r[i].p, r[i].stride, r[i].head, a.d, 16));
     }
     if (!copies) return TBE_OK;
     a.piece = 0;
     for (int i = 0; i < n; ++i) {
       const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.H, (cuuint64_t)a.N};
-      const cuuint64_t strides[2] = {(cuuint64_t)r[i].head * 2, (cuuint64_t)r[i].stride * 2};
+      const cuuint64_t strides[2] = {(cuuint64_t)head_stride(a, r[i]) * 2, (cuuint64_t)token_stride(a, r[i]) * 2};
       const cuuint32_t box[3] = {64, 1, kTile}, one[3] = {1, 1, 1};
       if (!encode_map(&a.map[i], dtype, 3, r[i].p, dims, strides, box, one)) return TBE_ERR_CUDA;
     }

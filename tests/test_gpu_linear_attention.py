@@ -157,7 +157,7 @@ def test_against_definition(tbe, name, d, kind, state):
 
 @gpu
 @pytest.mark.parametrize("layout", ["slices", "heads first", "off", "plain"])
-@pytest.mark.parametrize("d", [1, 7, 33, 63, 65, 100, 127])
+@pytest.mark.parametrize("d", [1, 7, 8, 33, 63, 64, 65, 72, 100, 120, 127, 128])
 def test_layouts_and_odd_widths(tbe, d, layout):
     run_and_check(tbe, make([30, 0, 99], 3, d, "bf16", d, True, layout=layout), "bf16")
 
@@ -440,3 +440,15 @@ def test_refusals(tbe):
     for state in (None, n["s0"][:1], n["s0"].half(), n["s0"].transpose(2, 3)):
         with pytest.raises(tbe.TBEError):
             tbe.tbe_linear_attention_step(n["q"], n["k"], n["v"], n["decay"], state)
+
+
+@gpu
+@pytest.mark.parametrize("N,H,d,row", [(200, 1, 100, 104), (1, 3, 64, 64), (1, 1, 7, 7), (130, 1, 60, 64)])
+def test_one_head_or_one_token(tbe, N, H, d, row):
+    """A stride that nothing is reached by says nothing."""
+    c = make([N], H, d, "bf16", 22, True)
+    for n in ("q", "k", "v", "do"):
+        room = torch.zeros(N, H, row, dtype=torch.bfloat16, device="cuda")
+        room[:, :, :d] = c[n]
+        c[n] = room[:, :, :d]
+    run_and_check(tbe, c, "bf16")

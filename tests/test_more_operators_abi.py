@@ -109,6 +109,7 @@ def catalogue(room, **other):
 @pytest.mark.parametrize("other,code", [
     (dict(dtype=9), INVALID), (dict(dtype=tbe.TBE_F32), UNSUPPORTED), (dict(tokens=0), INVALID), (dict(vocab=0), INVALID),
     (dict(width=0), INVALID), (dict(tokens=(1 << 24) + 1), UNSUPPORTED), (dict(vocab=(1 << 30) + 1), UNSUPPORTED),
+    (dict(tokens=1 << 24, vocab=1 << 23), UNSUPPORTED),
     (dict(width=(1 << 16) + 1, hidden_stride=1 << 17, weights_stride=1 << 17), UNSUPPORTED), (dict(hidden=None), INVALID),
     (dict(weights=None), INVALID), (dict(labels=None), INVALID), (dict(hidden_stride=31), INVALID),
     (dict(weights_stride=31), INVALID), (dict(logit_scale=float("inf")), INVALID), (dict(hidden=1), UNSUPPORTED),
