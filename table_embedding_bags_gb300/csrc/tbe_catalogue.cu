@@ -638,10 +638,78 @@ __device__ __forceinline__ bool epilogue(const GemmArgs& g, Shared& s, const Til
   return true;
 }
 
+// Few tokens over many rows: the table's rows are the product's rows and the
+// tokens its columns, 32 to a thread, which keeps their log-sums over all of
+// its tiles: a tile of 256 rows of hidden would be mostly empty.
+constexpr int kFewRows = 64;
+struct FewSums {
+  float m[32], l[32];
+  int32_t label;  // of token first + lane, or -1
+  int first;
+
+  __device__ __forceinline__ void begin(const GemmArgs& g, int32_t count, int half, int lane) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      m[k] = -3e38f;  // (finite: a product of -inf adds nothing to it)
+      l[k] = 0.f;
+    }
+    first = half * 32;
+    label = first + lane < count ? g.label[first + lane] : -1;
+  }
+  // One row of the table, row_v, and its products.
+  __device__ __forceinline__ void add(const GemmArgs& g, const float (&v)[32], int64_t row_v, int32_t tile) {
+    uint32_t hit = __ballot_sync(kFull, label >= 0 && label / kTileM == tile);
+    while (hit) {
+      const int k = __ffs((int)hit) - 1;
+      hit &= hit - 1;
+      if (__shfl_sync(kFull, label, k) == row_v) {
+        float x = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x = e == k ? v[e] : x;
+        g.mine[first + k] = x;
+      }
+    }
+    if (row_v >= g.V) return;
+    float most = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) most = fmaxf(most, fmaf(v[k], g.scale2, -m[k]));
+    if (most < 16.f) {  // m need not be the largest: sums of 2^16 lose nothing
+#pragma unroll
+      for (int k = 0; k < 32; ++k) l[k] += exp2_of(fmaf(v[k], g.scale2, -m[k]));
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float x = v[k] * g.scale2;
+      if (x > m[k]) {
+        l[k] = fmaf(l[k], exp2_of(m[k] - x), exp2_of(fmaf(v[k], g.scale2, -x)));
+        m[k] = x;
+      } else {
+        l[k] += exp2_of(fmaf(v[k], g.scale2, -m[k]));
+      }
+    }
+  }
+  __device__ __forceinline__ void end(const GemmArgs& g, int32_t count, int64_t part, int lane) {
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const float m2 = __shfl_xor_sync(kFull, m[k], o), l2 = __shfl_xor_sync(kFull, l[k], o);
+        const float top = fmaxf(m[k], m2);
+        l[k] = l[k] * exp2_of(m[k] - top) + l2 * exp2_of(m2 - top);
+        m[k] = top;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (lane == 0 && first + k < count) g.part[part * g.Np + first + k] = make_float2(m[k], l[k]);
+  }
+};
+
 // Persistent pairs of blocks.  In each block one thread starts its copies and
 // eight warps work on its finished accumulators, of which there are two; the
 // first block's threads also take the tiles and issue the products of both.
-template <int DT>
+template <int DT, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ GemmArgs g) {
   extern __shared__ __align__(1024) uint8_t raw[];
   __shared__ Shared s;
@@ -692,16 +760,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const uint32_t bytes = 2 * (2 + mine) * kBlockBytes;
       // where A and B lie along K, a step of it is 64 columns on; else 64 rows
       const bool a_along_m = t.mode == kTable, b_along_n = t.mode >= kTable;
-      const CUtensorMap* a = a_along_m ? &g.pt : t.mode == kHidden ? &g.p : &g.h;
-      const CUtensorMap* b = t.mode == kTable ? &g.ht : t.mode == kHidden ? &g.wt : &g.w;
+      const CUtensorMap* a = FEW ? &g.w : a_along_m ? &g.pt : t.mode == kHidden ? &g.p : &g.h;
+      const CUtensorMap* b = FEW || t.mode == kTable ? (FEW ? &g.h : &g.ht) : t.mode == kHidden ? &g.wt : &g.w;
       const int32_t g_row = (int32_t)(j.buffer * g.Np), a_row = t.mode == kHidden ? g_row + row0 : row0;
       const int32_t b_first = t.mode == kHidden ? j.v0 : 0;
       bool ok = true;
       const int ask_at = max(0, t.steps - kAsk);
-      if (rank == 0 && t.steps == 0) bar_arrive(&s.ask);
+      if (!FEW && rank == 0 && t.steps == 0) bar_arrive(&s.ask);
       for (int k = 0; k < t.steps; ++k, ++step) {
         const uint32_t at = step % kStages;
-        if (rank == 0 && k == ask_at) bar_arrive(&s.ask);
+        if (!FEW && rank == 0 && k == ask_at) bar_arrive(&s.ask);
         if (step >= kStages && !(ok = wait(&s.empty[at], (step / kStages - 1) & 1, s))) break;
         if (rank == 0) bar_expect(&s.full[at], bytes);
         const uint32_t bar = full0 + at * 8, dst = ring0 + at * kStageBytes;
@@ -747,16 +815,22 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     // gives out tiles, to both blocks
     int32_t total = 0;
     for (int k = 0; k < g.jobs; ++k) total += tiles_of(s.job[k], (count + kTileM - 1) / kTileM, g.D, g.half);
+    if (FEW) total = count > 0 ? (g.V + kTileM - 1) / kTileM : 0;
     int32_t now = blockIdx.x >> 1;
     for (uint32_t n = 0;; ++n) {
       const uint32_t slot = n % kTiles;
       alignas(16) Tile t = {};
       t.mode = -1;
-      if (n > 0) {  // (not asked for before it is wanted: the long tiles would go to few)
-        if (!wait(&s.ask, (n - 1) & 1, s)) break;
-        now = (int32_t)((gridDim.x >> 1) + atomicAdd(g.next, 1u));
+      if (FEW) {  // (all alike, and in turn)
+        now = (int32_t)(blockIdx.x >> 1) + (int32_t)n * (int32_t)(gridDim.x >> 1);
+        if (now < total) t = Tile{kSums, 0, now, 0, kTileN / 64, 0, 0, (g.D + kTileK - 1) / kTileK};
+      } else {
+        if (n > 0) {  // (not asked for before it is wanted: the long tiles would go to few)
+          if (!wait(&s.ask, (n - 1) & 1, s)) break;
+          now = (int32_t)((gridDim.x >> 1) + atomicAdd(g.next, 1u));
+        }
+        if (now < total) t = tile_of(g, s.job, now, count);
       }
-      if (now < total) t = tile_of(g, s.job, now, count);
       if (n >= kTiles && !wait(&s.forgotten[slot], (n / kTiles - 1) & 1, s)) break;
       s.tile[slot] = t;
       const uint32_t other = pair_addr(&s.tile[slot], 1);
@@ -769,6 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   } else if (warp >= 4) {
     const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     uint32_t turn = 0;  // tiles of kSums that this warp had rows of
+    FewSums few;
+    if (FEW) few.begin(g, count, half, lane);
     for (uint32_t n = 0;; ++n) {
       if (!wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
       const Tile t = s.tile[n % kTiles];
@@ -777,6 +853,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (t.mode < 0) break;
       if (!wait(&s.done[n & 1], (n / 2) & 1, s)) break;
       tc_after_sync();
+      if (FEW) {
+        float v[32];
+        tc_ld32(tmem + (n & 1) * kTileN + ((uint32_t)(warp & 3) * 32 << 16) + half * 32, v);
+        tc_wait_ld();
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) pair_arrive_relaxed(pair_addr(&s.drained[n & 1], 0));
+        if (half * 32 < count) few.add(g, v, (int64_t)t.rb * kTileM + rank * kRowsM + row, t.rb);
+        continue;
+      }
       const bool ok = epilogue<DT>(g, s, t, tmem + (n & 1) * kTileN + ((uint32_t)(warp & 3) * 32 << 16), count, half, row,
                                    rank, turn);
       if (!__all_sync(kFull, ok)) break;
@@ -784,6 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) pair_arrive_relaxed(pair_addr(&s.drained[n & 1], 0));
     }
+    if (FEW) few.end(g, count, (int64_t)blockIdx.x * 4 + (warp & 3), lane);
   }
   __syncwarp();
   tc_before_sync();
@@ -929,6 +1016,10 @@ int64_t whole(int64_t n, int64_t of) { return (n + of - 1) / of * of; }
 // 128 MB each.)
 constexpr int64_t kPiece = 1 << 26;
 constexpr int64_t kMaxTokens = 1 << 24;
+constexpr int32_t kFewFrom = 1 << 15;
+
+// Whether the log-sums take the table's rows for the product's.
+bool few_rows(int64_t N, int32_t V) { return N <= kFewRows && V >= kFewFrom; }
 
 struct Layout {
   int64_t Np;
@@ -971,7 +1062,7 @@ Layout layout(int64_t N, int32_t V, int32_t D, bool grad, bool copy_table) {
   w.hidden = take(2 * (size_t)w.Np * w.Dp);
   w.weights = take(copy_table ? 2 * (size_t)V * w.Dp : 0);
   // the log-sums' parts are through before the first piece
-  const size_t parts = sizeof(float2) * (size_t)w.vt * w.Np;
+  const size_t parts = sizeof(float2) * (size_t)(few_rows(N, V) ? 4 * (sm_count() + 1) : w.vt) * w.Np;
   const size_t gs = grad ? 2 * 2 * (size_t)w.Np * w.vc : 0;
   w.part = w.g = take(std::max(parts, gs));
   w.acc = take(grad ? 4 * (size_t)w.splits * w.Np * w.Dp : 0);
@@ -1010,13 +1101,13 @@ int start(void (*kernel)(A), int64_t grid, int threads, size_t smem, bool after,
 
 constexpr size_t kProductBytes = (size_t)kStages * kStageBytes + 1024;
 
-template <int DT>
+template <int DT, bool FEW = false>
 int start_products(const GemmArgs& g, int64_t tiles, cudaStream_t s) {  // tiles: at most so many
   static bool allowed[64] = {};  // once per device
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !allowed[dev]) {
-    if (cudaFuncSetAttribute(product_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kProductBytes) !=
+    if (cudaFuncSetAttribute(product_kernel<DT, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kProductBytes) !=
         cudaSuccess)
       return TBE_ERR_CUDA;
     if (dev >= 0 && dev < 64) allowed[dev] = true;
@@ -1034,7 +1125,7 @@ int start_products(const GemmArgs& g, int64_t tiles, cudaStream_t s) {  // tiles
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, product_kernel<DT>, g) == cudaSuccess ? check_launch() : TBE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, product_kernel<DT, FEW>, g) == cudaSuccess ? check_launch() : TBE_ERR_CUDA;
 }
 
 struct Call {
@@ -1160,11 +1251,14 @@ int run(const Call& c, cudaStream_t s) {
     g.jobs = 1;
     g.job[0] = Job{kSums, 0, in.vocab, 0, 0, 0, 0};
     g.next = p.zero;
-    if ((st = start_products<DT>(g, w.Np / kTileM * w.vt, s)) != TBE_OK) return st;
+    const bool few = few_rows(N, in.vocab);
+    const int64_t pairs = std::min<int64_t>(sm_count() / 2, w.vt);
+    st = few ? start_products<DT, true>(g, w.vt, s) : start_products<DT>(g, w.Np / kTileM * w.vt, s);
+    if (st != TBE_OK) return st;
     trace_mark(s, "catalogue_sums");
     RowArgs r = {};
     r.part = g.part;
-    r.parts = w.vt;
+    r.parts = few ? (int32_t)(8 * std::max<int64_t>(1, pairs)) : w.vt;
     r.Np = w.Np;
     r.count = p.count;
     r.rows = p.rows;

@@ -273,3 +273,34 @@ def test_refusals():
         tbe.tbe_catalogue_loss_backward(hidden, weights, labels, None)
     with pytest.raises(tbe.TBEError):
         tbe.tbe_catalogue_loss_backward(hidden, weights, labels, torch.zeros(49, device="cuda"))
+
+
+@pytest.mark.parametrize("N,V,D,scale", [(1, 32768, 64, 1.0), (33, 40001, 72, -0.5), (64, 33000, 200, 20.0), (64, 100003, 128, 1.0),
+                                         (65, 33000, 64, 1.0), (32, 32767, 64, 1.0)])
+def test_few_tokens_over_many_rows(N, V, D, scale):
+    """Up to 64 tokens over 32,768 rows or more: the log-sums of a token are kept by many threads, whose own maxima need
+    not be the largest."""
+    hidden, weights, labels = make(N, V, D, torch.bfloat16, seed=14, masked=0.2 if N > 1 else 0.0)
+    labels[-1] = V - 1
+    got = tbe.tbe_catalogue_loss(hidden, weights, labels, logit_scale=scale, want_grad=True)
+    check(got, definition(hidden, weights, labels, scale))
+    alone = tbe.tbe_catalogue_loss(hidden, weights, labels, logit_scale=scale)
+    assert torch.equal(alone.loss, got.loss) and torch.equal(alone.lse, got.lse)
+
+
+def test_few_tokens_and_logits_that_grow():
+    """Each tile's logits lie far above those before it."""
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    weights = torch.randn(40000, 64, generator=gen, device="cuda") * torch.linspace(0.01, 3, 40000, device="cuda")[:, None]
+    hidden = torch.randn(20, 64, generator=gen, device="cuda").bfloat16()
+    labels = torch.randint(0, 40000, (20,), generator=gen, device="cuda")
+    for w in (weights.bfloat16(), weights.flip(0).bfloat16()):
+        check(tbe.tbe_catalogue_loss(hidden, w, labels, want_grad=True), definition(hidden, w, labels))
+
+
+def test_few_tokens_what_is_no_number():
+    hidden, weights, labels = make(40, 40000, 64, torch.bfloat16, seed=16, masked=0.0)
+    hidden[7] = float("nan")
+    got = tbe.tbe_catalogue_loss(hidden, weights, labels)
+    others = torch.arange(40, device="cuda") != 7
+    assert got.token_loss[7].isnan() and got.loss.isnan() and got.token_loss[others].isfinite().all()
