@@ -33,8 +33,9 @@
 // 3,372; one copy of 16 KB where there were two of 8, and arrivals that order
 // nothing, 2,560; tiles given out by a thread of their own, when they are wanted,
 // 2,384; larger pieces 2,291; jobs in shared memory 2,262.
-// 64 rows over 1,000,003 x 128 take 119 us where the table's bytes take 38: three
-// in four rows of a tile are empty, and its exponentials go to 4 of 16 warps.
+// 64 rows over 1,000,003 x 128 take 71 us where the table's bytes take 38: with
+// the table's rows as the product's every warp has exponentials to take, and a
+// tile's 64 KB wait for its 512 cycles of products and the copies' latency.
 #include "tbe_tensor.cuh"
 
 #include <algorithm>
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
 }
 
 // Both steps in one launch, for batches whose labels every block can look at:
-// 8 x 1,000 x 64 bf16, the loss alone, 16.4 -> 14.0 us.
+// 8 x 1,000 x 64 bf16, the loss alone, 16.4 -> 14.7 us.
 constexpr int kFewTokens = 2048;
 struct FewArgs {
   PickArgs p;
@@ -279,11 +280,13 @@ constexpr int kAsk = 6;    // steps before the end of a tile's copies at which t
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
 constexpr uint16_t kBoth = 3;  // blocks of a pair, as a mask
+constexpr int kFewRows = 64;
 
 struct GemmArgs {
   // hidden [Np, Dp], weights [V, D] and g [2 Np, vc]: 128 rows by 64 columns (operands along K), and 64 rows by two
   // blocks of 64 columns (along M or N)
   CUtensorMap h, w, p, ht, wt, pt;
+  CUtensorMap few;    // hidden in boxes of 64 rows by 64 columns
   Job job[kMaxJobs];
   int32_t jobs;
   int32_t V, D, Dp;
@@ -641,7 +644,7 @@ __device__ __forceinline__ bool epilogue(const GemmArgs& g, Shared& s, const Til
 // Few tokens over many rows: the table's rows are the product's rows and the
 // tokens its columns, 32 to a thread, which keeps their log-sums over all of
 // its tiles: a tile of 256 rows of hidden would be mostly empty.
-constexpr int kFewRows = 64;
+// (kFewRows are one block of the pair's; the other's columns are empty.)
 struct FewSums {
   float m[32], l[32];
   int32_t label;  // of token first + lane, or -1
@@ -706,6 +709,13 @@ struct FewSums {
   }
 };
 
+// Its tiles are all alike, and each pair takes every so manieth.
+__device__ __forceinline__ Tile few_tile(const GemmArgs& g, uint32_t n, int32_t count) {
+  const int32_t now = (int32_t)(blockIdx.x >> 1) + (int32_t)n * (int32_t)(gridDim.x >> 1);
+  const bool there = count > 0 && now < (g.V + kTileM - 1) / kTileM;
+  return Tile{there ? (int32_t)kSums : -1, 0, now, 0, 2 * kFewRows / 64, 0, 0, (g.D + kTileK - 1) / kTileK};
+}
+
 // Persistent pairs of blocks.  In each block one thread starts its copies and
 // eight warps work on its finished accumulators, of which there are two; the
 // first block's threads also take the tiles and issue the products of both.
@@ -749,9 +759,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const uint32_t full0 = pair_addr(&s.full[0], 0), forgotten0 = pair_addr(&s.forgotten[0], 0), ring0 = smem_u32(ring);
     uint32_t step = 0;  // steps of K so far
     for (uint32_t n = 0;; ++n) {
-      if (!wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
-      const Tile t = s.tile[n % kTiles];
-      if (t.mode >= 0 || t.steps >= 0) pair_arrive_relaxed(forgotten0 + n % kTiles * 8);  // (it has been read)
+      if (!FEW && !wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
+      const Tile t = FEW ? few_tile(g, n, count) : s.tile[n % kTiles];
+      if (!FEW && (t.mode >= 0 || t.steps >= 0)) pair_arrive_relaxed(forgotten0 + n % kTiles * 8);  // (it has been read)
       if (t.mode < 0) break;
       const Job& j = s.job[t.job];
       const int32_t row0 = t.rb * kTileM + (int32_t)rank * kRowsM;
@@ -761,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       // where A and B lie along K, a step of it is 64 columns on; else 64 rows
       const bool a_along_m = t.mode == kTable, b_along_n = t.mode >= kTable;
       const CUtensorMap* a = FEW ? &g.w : a_along_m ? &g.pt : t.mode == kHidden ? &g.p : &g.h;
-      const CUtensorMap* b = FEW || t.mode == kTable ? (FEW ? &g.h : &g.ht) : t.mode == kHidden ? &g.wt : &g.w;
+      const CUtensorMap* b = FEW ? &g.few : t.mode == kTable ? &g.ht : t.mode == kHidden ? &g.wt : &g.w;
       const int32_t g_row = (int32_t)(j.buffer * g.Np), a_row = t.mode == kHidden ? g_row + row0 : row0;
       const int32_t b_first = t.mode == kHidden ? j.v0 : 0;
       bool ok = true;
@@ -787,9 +797,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   } else if (warp == 1 && lane == 0 && rank == 0) {
     uint32_t step = 0;
     for (uint32_t n = 0;; ++n) {
-      if (!wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
-      const Tile t = s.tile[n % kTiles];
-      if (t.mode >= 0 || t.steps >= 0) bar_arrive(&s.forgotten[n % kTiles]);
+      if (!FEW && !wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
+      const Tile t = FEW ? few_tile(g, n, count) : s.tile[n % kTiles];
+      if (!FEW && (t.mode >= 0 || t.steps >= 0)) bar_arrive(&s.forgotten[n % kTiles]);
       if (t.mode < 0) break;
       if (n >= 2 && !wait(&s.drained[n & 1], (n / 2 - 1) & 1, s)) break;
       tc_after_sync();
@@ -811,26 +821,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (!ok) break;
       pair_commit(&s.done[n & 1], kBoth);
     }
-  } else if (warp == 3 && lane == 0 && rank == 0) {
+  } else if (!FEW && warp == 3 && lane == 0 && rank == 0) {
     // gives out tiles, to both blocks
     int32_t total = 0;
     for (int k = 0; k < g.jobs; ++k) total += tiles_of(s.job[k], (count + kTileM - 1) / kTileM, g.D, g.half);
-    if (FEW) total = count > 0 ? (g.V + kTileM - 1) / kTileM : 0;
     int32_t now = blockIdx.x >> 1;
     for (uint32_t n = 0;; ++n) {
       const uint32_t slot = n % kTiles;
       alignas(16) Tile t = {};
       t.mode = -1;
-      if (FEW) {  // (all alike, and in turn)
-        now = (int32_t)(blockIdx.x >> 1) + (int32_t)n * (int32_t)(gridDim.x >> 1);
-        if (now < total) t = Tile{kSums, 0, now, 0, kTileN / 64, 0, 0, (g.D + kTileK - 1) / kTileK};
-      } else {
-        if (n > 0) {  // (not asked for before it is wanted: the long tiles would go to few)
-          if (!wait(&s.ask, (n - 1) & 1, s)) break;
-          now = (int32_t)((gridDim.x >> 1) + atomicAdd(g.next, 1u));
-        }
-        if (now < total) t = tile_of(g, s.job, now, count);
+      if (n > 0) {  // (not asked for before it is wanted: the long tiles would go to few)
+        if (!wait(&s.ask, (n - 1) & 1, s)) break;
+        now = (int32_t)((gridDim.x >> 1) + atomicAdd(g.next, 1u));
       }
+      if (now < total) t = tile_of(g, s.job, now, count);
       if (n >= kTiles && !wait(&s.forgotten[slot], (n / kTiles - 1) & 1, s)) break;
       s.tile[slot] = t;
       const uint32_t other = pair_addr(&s.tile[slot], 1);
@@ -846,10 +850,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     FewSums few;
     if (FEW) few.begin(g, count, half, lane);
     for (uint32_t n = 0;; ++n) {
-      if (!wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
-      const Tile t = s.tile[n % kTiles];
+      if (!FEW && !wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
+      const Tile t = FEW ? few_tile(g, n, count) : s.tile[n % kTiles];
       __syncwarp();
-      if (lane == 0 && (t.mode >= 0 || t.steps >= 0)) pair_arrive_relaxed(pair_addr(&s.forgotten[n % kTiles], 0));
+      if (!FEW && lane == 0 && (t.mode >= 0 || t.steps >= 0)) pair_arrive_relaxed(pair_addr(&s.forgotten[n % kTiles], 0));
       if (t.mode < 0) break;
       if (!wait(&s.done[n & 1], (n / 2) & 1, s)) break;
       tc_after_sync();
@@ -1016,6 +1020,9 @@ int64_t whole(int64_t n, int64_t of) { return (n + of - 1) / of * of; }
 // 128 MB each.)
 constexpr int64_t kPiece = 1 << 26;
 constexpr int64_t kMaxTokens = 1 << 24;
+// The table's rows as the product's, from so many on: the loss alone of 64
+// tokens over 1,000,003, 100,000, 40,000 and 10,000 rows of 128 takes 70, 23.3,
+// 20.3 and 19.6 us so, and 119, 27.2, 21.0 and 16.4 us with the tokens as rows.
 constexpr int32_t kFewFrom = 1 << 15;
 
 // Whether the log-sums take the table's rows for the product's.
@@ -1071,9 +1078,9 @@ Layout layout(int64_t N, int32_t V, int32_t D, bool grad, bool copy_table) {
 }
 
 // [rows, cols] of 16-bit elements, `stride` elements from row to row.
-bool map_of(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t stride, int32_t dtype) {
+bool map_of(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t stride, int32_t dtype, uint32_t high = kRowsM) {
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
-  const cuuint32_t box[2] = {64, kRowsM}, one[2] = {1, 1};
+  const cuuint32_t box[2] = {64, high}, one[2] = {1, 1};
   return encode_map(m, dtype, 2, p, dims, strides, box, one);
 }
 // The same as blocks of 64 columns (which cols is a multiple of).
@@ -1252,6 +1259,7 @@ int run(const Call& c, cudaStream_t s) {
     g.job[0] = Job{kSums, 0, in.vocab, 0, 0, 0, 0};
     g.next = p.zero;
     const bool few = few_rows(N, in.vocab);
+    if (few && !map_of(&g.few, k.dst, w.Np, w.Dp, w.Dp, DT, kFewRows)) return TBE_ERR_CUDA;
     const int64_t pairs = std::min<int64_t>(sm_count() / 2, w.vt);
     st = few ? start_products<DT, true>(g, w.vt, s) : start_products<DT>(g, w.Np / kTileM * w.vt, s);
     if (st != TBE_OK) return st;
