@@ -1,5 +1,6 @@
 // tbe_tensor.cuh -- tensor copies (TMA), mbarriers and tensor-core products
-// (tcgen05, accumulators in TMEM) as the catalogue loss uses them.
+// (tcgen05, accumulators in TMEM) as linear attention and the catalogue loss
+// use them.
 #pragma once
 
 #include "tbe_internal.cuh"
