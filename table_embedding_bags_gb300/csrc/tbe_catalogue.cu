@@ -497,7 +497,8 @@ struct SumsOf {
   float m, l;
   __device__ __forceinline__ void operator()(float (&v)[32], int c) {
     const int32_t col = t.col + c;
-    if ((uint32_t)(label - col) < 32u) {
+    const bool own = (uint32_t)(label - col) < 32u;
+    if (own) {
       float x = 0.f;
 #pragma unroll
       for (int k = 0; k < 32; ++k) x = k == label - col ? v[k] : x;
@@ -524,6 +525,10 @@ struct SumsOf {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
         if (col + k >= g.V) v[k] = 0.f;
+    }
+    if (own) {  // (row_kernel adds the label's)
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = k == label - col ? 0.f : v[k];
     }
     float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -660,7 +665,7 @@ struct FewSums {
     label = first + lane < count ? g.label[first + lane] : -1;
   }
   // One row of the table, row_v, and its products.
-  __device__ __forceinline__ void add(const GemmArgs& g, const float (&v)[32], int64_t row_v, int32_t tile) {
+  __device__ __forceinline__ void add(const GemmArgs& g, float (&v)[32], int64_t row_v, int32_t tile) {
     uint32_t hit = __ballot_sync(kFull, label >= 0 && label / kTileM == tile);
     while (hit) {
       const int k = __ffs((int)hit) - 1;
@@ -668,7 +673,10 @@ struct FewSums {
       if (__shfl_sync(kFull, label, k) == row_v) {
         float x = 0.f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x = e == k ? v[e] : x;
+        for (int e = 0; e < 32; ++e) {
+          x = e == k ? v[e] : x;
+          v[e] = e == k ? (g.scale2 < 0.f ? INFINITY : -INFINITY) : v[e];  // (row_kernel adds the label's; no scale of 0 here)
+        }
         g.mine[first + k] = x;
       }
     }
@@ -938,13 +946,15 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const RowArgs a) {
   if (threadIdx.x < kRows && row < count) {
     const int warps = min(32, (a.parts * kRows + 31) / 32);  // that had any
     for (int w = 1; w < warps; ++w) join(m, l, part[w][threadIdx.x].x, part[w][threadIdx.x].y);
-    // Where one logit stands out, its loss is the logarithm of a sum close to 1, kept apart from the maximum.  The
-    // exponentials are those of scaled products less the rounded m, so the label's is taken less m in the same way.
-    const float log_l = log2f(l);
+    // The label's own term is not in l, which therefore keeps its digits where that logit stands out and the loss,
+    // log(1 + l 2^-d), is close to 0.  d is how far the label's logit lies above m.
     const int32_t n = a.rows[row];
-    a.lse2[row] = m + log_l;
-    a.lse[n] = (m + log_l) * kLn2;
-    mine = (log_l - fmaf(a.mine[row], a.scale2, -m)) * kLn2;
+    const float x = a.mine[row], d = fmaf(x, a.scale2, -m);
+    mine = d > -64.f ? log1pf(l * exp2f(-d)) : (log2f(l) - d) * kLn2;
+    // (l == 0: there is no other row, or none that reaches 2^-126 of it)
+    const float log_sum = l == 0.f ? x * a.scale2 : m + (d <= 0.f ? log2f(l + exp2f(d)) : d + log1pf(l * exp2f(-d)) * kLog2e);
+    a.lse2[row] = log_sum;
+    a.lse[n] = log_sum * kLn2;
     a.token_loss[n] = mine;
   }
   if (warp != 0) return;
@@ -1026,7 +1036,9 @@ constexpr int64_t kMaxTokens = 1 << 24;
 constexpr int32_t kFewFrom = 1 << 15;
 
 // Whether the log-sums take the table's rows for the product's.
-bool few_rows(int64_t N, int32_t V) { return N <= kFewRows && V >= kFewFrom; }
+bool few_rows(const tbe_catalogue_inputs& in) {
+  return in.tokens <= kFewRows && in.vocab >= kFewFrom && in.logit_scale * kLog2e != 0.f;
+}
 
 struct Layout {
   int64_t Np;
@@ -1040,7 +1052,9 @@ bool copied(const tbe_catalogue_inputs& in, bool grad) {
   return off_pieces(in.weights, in.weights_stride) || (grad && in.width % 64);
 }
 
-Layout layout(int64_t N, int32_t V, int32_t D, bool grad, bool copy_table) {
+Layout layout(const tbe_catalogue_inputs& in, bool grad) {
+  const int64_t N = in.tokens;
+  const int32_t V = in.vocab, D = in.width;
   Layout w;
   w.Np = whole(N, kTileM);  // (whole tiles)
   w.Dp = (int32_t)whole(D, 64);
@@ -1067,9 +1081,9 @@ Layout layout(int64_t N, int32_t V, int32_t D, bool grad, bool copy_table) {
   w.arrived = w.next + 4 * (size_t)(w.pieces + 2);
   w.block_sum = take(4 * (size_t)(w.Np / kRows));
   w.hidden = take(2 * (size_t)w.Np * w.Dp);
-  w.weights = take(copy_table ? 2 * (size_t)V * w.Dp : 0);
+  w.weights = take(copied(in, grad) ? 2 * (size_t)V * w.Dp : 0);
   // the log-sums' parts are through before the first piece
-  const size_t parts = sizeof(float2) * (size_t)(few_rows(N, V) ? 4 * (sm_count() + 1) : w.vt) * w.Np;
+  const size_t parts = sizeof(float2) * (size_t)(few_rows(in) ? 4 * (sm_count() + 1) : w.vt) * w.Np;
   const size_t gs = grad ? 2 * 2 * (size_t)w.Np * w.vc : 0;
   w.part = w.g = take(std::max(parts, gs));
   w.acc = take(grad ? 4 * (size_t)w.splits * w.Np * w.Dp : 0);
@@ -1162,7 +1176,7 @@ int run(const Call& c, cudaStream_t s) {
   const tbe_catalogue_inputs& in = *c.in;
   const bool grad = c.dhidden != nullptr, copy = copied(in, grad);
   const int64_t N = in.tokens;
-  const Layout w = layout(N, in.vocab, in.width, grad, copy);
+  const Layout w = layout(in, grad);
   uint8_t* ws = c.ws;
 
   PickArgs p = {};
@@ -1258,7 +1272,7 @@ int run(const Call& c, cudaStream_t s) {
     g.jobs = 1;
     g.job[0] = Job{kSums, 0, in.vocab, 0, 0, 0, 0};
     g.next = p.zero;
-    const bool few = few_rows(N, in.vocab);
+    const bool few = few_rows(in);
     if (few && !map_of(&g.few, k.dst, w.Np, w.Dp, w.Dp, DT, kFewRows)) return TBE_ERR_CUDA;
     const int64_t pairs = std::min<int64_t>(sm_count() / 2, w.vt);
     st = few ? start_products<DT, true>(g, w.vt, s) : start_products<DT>(g, w.Np / kTileM * w.vt, s);
@@ -1357,7 +1371,7 @@ int dispatch(const Call& c, void* workspace, size_t bytes, void* stream) {
       for (int j = std::max(i + 1, 2); j < 4; ++j)
         if (overlap(t[i].p, t[i].rows, t[i].stride, t[j].p, t[j].rows, t[j].stride, in.width)) return TBE_ERR_INVALID_ARG;
   }
-  const Layout w = layout(in.tokens, in.vocab, in.width, c.dhidden != nullptr, copied(in, c.dhidden != nullptr));
+  const Layout w = layout(in, c.dhidden != nullptr);
   if (bytes < w.bytes) return TBE_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
   trace_begin(s);
@@ -1373,7 +1387,7 @@ extern "C" {
 
 size_t tbe_catalogue_workspace_bytes(const tbe_catalogue_inputs* in, int32_t grad) {
   if (check(in) != TBE_OK) return 0;
-  return layout(in->tokens, in->vocab, in->width, grad != 0, copied(*in, grad != 0)).bytes;
+  return layout(*in, grad != 0).bytes;
 }
 
 int tbe_catalogue_loss(const tbe_catalogue_inputs* in, float* loss, float* token_loss, float* lse, void* dhidden,
