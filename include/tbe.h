@@ -676,11 +676,17 @@ int tbe_catalogue_loss(const tbe_catalogue_inputs* in, float* loss, float* token
                        int64_t dhidden_stride, void* dweights, int64_t dweights_stride, float grad_scale,
                        void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
 
-/* The gradients on their own, from the lse of tbe_catalogue_loss: that call's
- * up to the rounding of lse (2^-24 |lse| of each probability's size). */
+/* The gradients on their own, from the lse and (..._full) token_loss of
+ * tbe_catalogue_loss: that call's up to the rounding of lse, 2^-23 |lse| of
+ * each probability's size.  Without token_loss (or with NULL) the label's
+ * entry, its probability less 1, carries that of a probability of 1: for a
+ * token that is nearly learnt, most of what is left of it. */
 int tbe_catalogue_loss_backward(const tbe_catalogue_inputs* in, const float* lse, void* dhidden, int64_t dhidden_stride,
                                 void* dweights, int64_t dweights_stride, float grad_scale, void* workspace,
                                 size_t workspace_bytes, int32_t* dev_status, void* stream);
+int tbe_catalogue_loss_backward_full(const tbe_catalogue_inputs* in, const float* lse, const float* token_loss, void* dhidden,
+                                     int64_t dhidden_stride, void* dweights, int64_t dweights_stride, float grad_scale,
+                                     void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /*
  * One AdamW step over a list of tensors in one launch:

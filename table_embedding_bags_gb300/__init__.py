@@ -39,7 +39,7 @@ EXPORTED = [
     "tbe_preference_loss_backward_low", "tbe_adamw_state_blocks", "tbe_adamw_plan_device_bytes",
     "tbe_adamw_plan_create", "tbe_adamw_plan_destroy", "tbe_adamw_step", "tbe_adamw_state",
     "tbe_catalogue_workspace_bytes", "tbe_catalogue_loss", "tbe_catalogue_loss_backward",
-    "tbe_linear_attention_workspace_bytes", "tbe_linear_attention", "tbe_linear_attention_backward",
+    "tbe_catalogue_loss_backward_full", "tbe_linear_attention_workspace_bytes", "tbe_linear_attention", "tbe_linear_attention_backward",
     "tbe_linear_attention_step",
 ]
 TBE_STATIC_WORKSPACE_BYTES = 32 << 20
@@ -163,6 +163,7 @@ def _declare_training(lib):
         ("tbe_catalogue_workspace_bytes", sz, [P, i32]),
         ("tbe_catalogue_loss", ctypes.c_int, [P, P, P, P, P, i64, P, i64, f32, P, sz, P, P]),
         ("tbe_catalogue_loss_backward", ctypes.c_int, [P, P, P, i64, P, i64, f32, P, sz, P, P]),
+        ("tbe_catalogue_loss_backward_full", ctypes.c_int, [P, P, P, P, i64, P, i64, f32, P, sz, P, P]),
     ]:
         getattr(lib, name).restype = res
         getattr(lib, name).argtypes = args

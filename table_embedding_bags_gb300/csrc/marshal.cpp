@@ -33,7 +33,7 @@ struct Abi {
   decltype(&tbe_preference_loss_backward_low) preference_backward;
   decltype(&tbe_preference_workspace_bytes) preference_workspace;
   decltype(&tbe_catalogue_loss) catalogue;
-  decltype(&tbe_catalogue_loss_backward) catalogue_backward;
+  decltype(&tbe_catalogue_loss_backward_full) catalogue_backward;
   decltype(&tbe_catalogue_workspace_bytes) catalogue_workspace;
   decltype(&tbe_linear_attention) linear;
   decltype(&tbe_linear_attention_backward) linear_backward;
@@ -50,7 +50,7 @@ const char* const kNames[] = {"tbe_gated_scan",
                               "tbe_preference_loss_backward_low",
                               "tbe_preference_workspace_bytes",
                               "tbe_catalogue_loss",
-                              "tbe_catalogue_loss_backward",
+                              "tbe_catalogue_loss_backward_full",
                               "tbe_catalogue_workspace_bytes",
                               "tbe_linear_attention",
                               "tbe_linear_attention_backward",
@@ -444,18 +444,20 @@ PyObject* catalogue(PyObject* const* a) {
   return tuple(loss, token_loss, lse, c.dhidden, c.dweights);
 }
 
-// (hidden, weights, labels, lse, logit_scale, grad_scale, dhidden, dweights, dev_status, stream) -> (dhidden, dweights)
+// (hidden, weights, labels, lse, logit_scale, grad_scale, dhidden, dweights, dev_status, stream, token_loss)
+// -> (dhidden, dweights)
 PyObject* catalogue_backward(PyObject* const* a) {
   Catalogue c = catalogue_of(a[0], a[1], a[2], a[4]);
   const double scale = number_of(a[5]);
   const Stream stream(a[9], c.dev);
   if (a[3] == Py_None) refuse("lse is required");
   const float* lse = floats_of<const float>(a[3], {c.in.tokens}, c.dev, "lse");
+  const float* token_loss = floats_of<const float>(a[10], {c.in.tokens}, c.dev, "token_loss");
   catalogue_grads(c, a[6], a[7], stream);
   const size_t bytes = abi.catalogue_workspace(&c.in, 1);
   at::Tensor ws = stream.workspace(bytes);
-  check(abi.catalogue_backward(&c.in, lse, c.dhidden.data_ptr(), c.dhidden_stride, c.dweights.data_ptr(), c.dweights_stride,
-                               (float)scale, ws.data_ptr(), bytes, status_of(a[8], c.dev), stream.handle()),
+  check(abi.catalogue_backward(&c.in, lse, token_loss, c.dhidden.data_ptr(), c.dhidden_stride, c.dweights.data_ptr(),
+                               c.dweights_stride, (float)scale, ws.data_ptr(), bytes, status_of(a[8], c.dev), stream.handle()),
         "tbe_catalogue_loss_backward");
   return tuple(c.dhidden, c.dweights);
 }
@@ -644,7 +646,7 @@ PyMethodDef methods[] = {{"init", init, METH_VARARGS, nullptr},
                          {"linear_attention", FAST(linear, 11)},
                          {"linear_attention_backward", FAST(linear_backward, 12)},
                          {"linear_attention_step", FAST(linear_step, 8)},
-                         {"catalogue_loss_backward", FAST(catalogue_backward, 10)},
+                         {"catalogue_loss_backward", FAST(catalogue_backward, 11)},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -20,7 +20,8 @@
 // g is rounded to the operands' type before the second products (half a step,
 // 2^-9 of each term for bf16, 2^-12 for fp16, where it is held 2^14 times
 // larger so that probabilities down to 4e-9 are normal numbers).  The label's
-// entry has the 1 taken off before the rounding.  Products are exact and
+// entry is exp(-loss) - 1, made from the token's loss: where a token is nearly
+// learnt, a difference of 1 and a probability would keep little of it.  Products are exact and
 // summed in fp32; dhidden is summed over the pieces in fp32.
 //
 // What bounds it: the tensor cores where the width is 512 or more (64 % of
@@ -71,8 +72,13 @@ struct PickArgs {
   float* lse;         // [N], or null
   float* loss;        // 0 where no token is taken, or null
   const float* given;  // [N] the log-sums of an earlier call (lse2 is made from them), or null
+  const float* given_loss;  // [N] its losses (own is made from them), or null
+  float* own;               // [Np]
   int32_t* status;
 };
+
+// The label's entry of g, p - 1, from the token's loss: with p near 1 the difference would keep little of it.
+__device__ __forceinline__ float own_of(float loss) { return expm1f(-loss); }
 
 __device__ __forceinline__ bool taken(int64_t y, int32_t V) { return y >= 0 && y < V; }
 
@@ -107,6 +113,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const PickArgs a) {
       a.rows[k] = (int32_t)i;
       a.label[k] = (int32_t)y;
       if (a.given) a.lse2[k] = a.given[i] * kLog2e;
+      if (a.given_loss) a.own[k] = own_of(a.given_loss[i]);
     } else if (i < end && a.lse) {
       a.lse[i] = 0.f;
       a.token_loss[i] = 0.f;
@@ -218,6 +225,7 @@ __global__ void __launch_bounds__(256) pick_copy_kernel(const FewArgs a) {
         a.p.rows[k] = n;
         a.p.label[k] = (int32_t)a.p.labels[n];
         if (a.p.given) a.p.lse2[k] = a.p.given[n] * kLog2e;
+        if (a.p.given_loss) a.p.own[k] = own_of(a.p.given_loss[n]);
       } else if (n < N && a.p.lse) {
         a.p.lse[n] = 0.f;
         a.p.token_loss[n] = 0.f;
@@ -297,6 +305,7 @@ struct GemmArgs {
   float scale2;       // logit_scale in units of log 2
   const int32_t* label;
   const float* lse2;
+  const float* own;   // the label's entry of g, or null: exp(x - lse) - 1
   float* mine;        // kSums: the label's product, not scaled
   float2* part;       // kSums: [tiles along the vocabulary, Np]
   uint16_t* g;
@@ -547,6 +556,7 @@ struct ProbsOf {
   int32_t label, v0;
   bool there, edge;
   float less;
+  const float* own;
   uint16_t* dst;
   __device__ __forceinline__ void operator()(float (&v)[32], int c) {
     const int32_t col = t.col + c;
@@ -554,7 +564,7 @@ struct ProbsOf {
     if ((uint32_t)(label - col) < 32u) {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
-        if (k == label - col) v[k] -= (float)(1 << kUp<DT>);
+        if (k == label - col) v[k] = own ? *own * (float)(1 << kUp<DT>) : v[k] - (float)(1 << kUp<DT>);
     }
     if (!there || edge) {
 #pragma unroll
@@ -633,7 +643,7 @@ __device__ __forceinline__ bool epilogue(const GemmArgs& g, Shared& s, const Til
   } else if (t.mode == kProbs) {
     if (warp_r >= (count + kTileK - 1) / kTileK * kTileK) return true;
     ProbsOf<DT> f = {g, t, g.label[r], j.v0, r < count, edge, (float)kUp<DT> - g.lse2[r],
-                     g.g + ((int64_t)j.buffer * g.Np + r) * g.vc};
+                     g.own ? g.own + r : nullptr, g.g + ((int64_t)j.buffer * g.Np + r) * g.vc};
     each_chunk(tmem, begin, end, f);
   } else if (t.mode == kTable) {
     const int64_t row_v = j.v0 + r;
@@ -909,6 +919,7 @@ struct RowArgs {
   const float* mine;
   float scale2;
   float* lse2;
+  float* own;
   float* token_loss;
   float* lse;
   float* loss;
@@ -955,6 +966,7 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const RowArgs a) {
     const float log_sum = l == 0.f ? x * a.scale2 : m + (d <= 0.f ? log2f(l + exp2f(d)) : d + log1pf(l * exp2f(-d)) * kLog2e);
     a.lse2[row] = log_sum;
     a.lse[n] = log_sum * kLn2;
+    a.own[row] = own_of(mine);
     a.token_loss[n] = mine;
   }
   if (warp != 0) return;
@@ -1043,7 +1055,7 @@ bool few_rows(const tbe_catalogue_inputs& in) {
 struct Layout {
   int64_t Np;
   int32_t Dp, vc, pieces, splits, steps, vt;
-  size_t rows, label, lse2, mine, count, next, block_sum, arrived, hidden, part, weights, g, acc, bytes;
+  size_t rows, label, lse2, mine, own, count, next, block_sum, arrived, hidden, part, weights, g, acc, bytes;
 };
 // Tensor copies want rows that start on 16 bytes and, by blocks of 64 columns,
 // whole ones; other tables are copied.
@@ -1076,6 +1088,7 @@ Layout layout(const tbe_catalogue_inputs& in, bool grad) {
   w.label = take(4 * (size_t)w.Np);
   w.lse2 = take(4 * (size_t)w.Np);
   w.mine = take(4 * (size_t)w.Np);
+  w.own = take(4 * (size_t)w.Np);
   w.count = take(4);
   w.next = take(4 * (size_t)(w.pieces + 3));  // of the log-sums, the pieces and what follows the last; arrived
   w.arrived = w.next + 4 * (size_t)(w.pieces + 2);
@@ -1153,6 +1166,7 @@ struct Call {
   const tbe_catalogue_inputs* in;
   float *loss, *token_loss, *lse;  // the forward's outputs, or null
   const float* given;              // the log-sums of an earlier call, or null
+  const float* given_loss;         // its losses, or null
   void* dhidden;
   int64_t dhidden_stride;
   void* dweights;
@@ -1194,6 +1208,8 @@ int run(const Call& c, cudaStream_t s) {
   p.lse = c.lse;
   p.loss = c.loss;
   p.given = c.given;
+  p.given_loss = c.given_loss;
+  p.own = at<float>(ws, w.own);
   p.status = c.status;
   CopyArgs k = {};
   k.src = static_cast<const uint16_t*>(in.hidden);
@@ -1258,6 +1274,7 @@ int run(const Call& c, cudaStream_t s) {
   g.scale2 = in.logit_scale * kLog2e;
   g.label = p.label;
   g.lse2 = p.lse2;
+  g.own = c.loss || c.given_loss ? p.own : nullptr;
   g.mine = at<float>(ws, w.mine);
   g.part = at<float2>(ws, w.part);
   g.g = at<uint16_t>(ws, w.g);
@@ -1287,6 +1304,7 @@ int run(const Call& c, cudaStream_t s) {
     r.mine = g.mine;
     r.scale2 = g.scale2;
     r.lse2 = p.lse2;
+    r.own = p.own;
     r.token_loss = c.token_loss;
     r.lse = c.lse;
     r.loss = c.loss;
@@ -1396,7 +1414,7 @@ int tbe_catalogue_loss(const tbe_catalogue_inputs* in, float* loss, float* token
   const int st = check(in);
   if (st != TBE_OK) return st;
   if (!loss || !token_loss || !lse) return TBE_ERR_INVALID_ARG;
-  const Call c = {in,       loss, token_loss, lse, nullptr, dhidden, dhidden_stride, dweights, dweights_stride, grad_scale,
+  const Call c = {in,       loss, token_loss, lse, nullptr, nullptr, dhidden, dhidden_stride, dweights, dweights_stride, grad_scale,
                   static_cast<uint8_t*>(workspace), dev_status};
   return dispatch(c, workspace, workspace_bytes, stream);
 }
@@ -1404,11 +1422,18 @@ int tbe_catalogue_loss(const tbe_catalogue_inputs* in, float* loss, float* token
 int tbe_catalogue_loss_backward(const tbe_catalogue_inputs* in, const float* lse, void* dhidden, int64_t dhidden_stride,
                                 void* dweights, int64_t dweights_stride, float grad_scale, void* workspace,
                                 size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  return tbe_catalogue_loss_backward_full(in, lse, nullptr, dhidden, dhidden_stride, dweights, dweights_stride, grad_scale,
+                                          workspace, workspace_bytes, dev_status, stream);
+}
+
+int tbe_catalogue_loss_backward_full(const tbe_catalogue_inputs* in, const float* lse, const float* token_loss, void* dhidden,
+                                     int64_t dhidden_stride, void* dweights, int64_t dweights_stride, float grad_scale,
+                                     void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
   const int st = check(in);
   if (st != TBE_OK) return st;
   if (!lse || !dhidden || !dweights) return TBE_ERR_INVALID_ARG;
-  const Call c = {in,      nullptr, nullptr, nullptr, lse, dhidden, dhidden_stride, dweights, dweights_stride, grad_scale,
-                  static_cast<uint8_t*>(workspace), dev_status};
+  const Call c = {in,      nullptr, nullptr, nullptr, lse, token_loss, dhidden, dhidden_stride, dweights, dweights_stride,
+                  grad_scale, static_cast<uint8_t*>(workspace), dev_status};
   return dispatch(c, workspace, workspace_bytes, stream);
 }
 

@@ -63,7 +63,7 @@ def _marshal():
         m.init(_tbe.TBEError, {name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "tbe_gated_scan", "tbe_gated_scan_backward", "tbe_gated_scan_step", "tbe_gated_scan_states",
             "tbe_gated_scan_workspace_bytes", "tbe_preference_loss", "tbe_preference_loss_backward_low",
-            "tbe_preference_workspace_bytes", "tbe_catalogue_loss", "tbe_catalogue_loss_backward",
+            "tbe_preference_workspace_bytes", "tbe_catalogue_loss", "tbe_catalogue_loss_backward_full",
             "tbe_catalogue_workspace_bytes", "tbe_linear_attention", "tbe_linear_attention_backward",
             "tbe_linear_attention_step", "tbe_linear_attention_workspace_bytes", "tbe_status_string")})
         _compiled = m
@@ -257,12 +257,14 @@ def tbe_catalogue_loss(hidden, weights, labels, logit_scale: float = 1.0, want_g
 
 
 def tbe_catalogue_loss_backward(hidden, weights, labels, lse, logit_scale: float = 1.0, grad_scale: float = 1.0,
-                                dhidden=None, dweights=None, dev_status=None, stream=None):
-    """(dhidden, dweights) from the ``lse`` of a ``tbe_catalogue_loss`` call
-    on the same arguments."""
+                                dhidden=None, dweights=None, dev_status=None, stream=None, token_loss=None):
+    """(dhidden, dweights) from the ``lse`` and ``token_loss`` of a
+    ``tbe_catalogue_loss`` call on the same arguments.  Without
+    ``token_loss`` the gradients of tokens that are nearly learnt keep few
+    digits (a probability less 1)."""
     m = _compiled or _marshal()
     return m.catalogue_loss_backward(hidden, weights, labels, lse, logit_scale, grad_scale, dhidden, dweights, dev_status,
-                                     None if stream is None else stream.cuda_stream)
+                                     None if stream is None else stream.cuda_stream, token_loss)
 
 
 # ---------------------------------------------------------------------------

@@ -63,6 +63,35 @@ def test_losses_near_zero(N, V, D, scale, kind):
 
 
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("call", ["with the loss", "alone"])
+@pytest.mark.parametrize("N,V,D,scale", CASES)
+def test_gradients_of_tokens_that_are_nearly_learnt(N, V, D, scale, call, kind):
+    """A bound of each entry of g by its own size, the label's among them: r / (1 + r), not 1."""
+    hidden, weights, labels = learnt(N, V, D, kind, 2, scale)
+    up = 2.0**12
+    got = tbe.tbe_catalogue_loss(hidden, weights, labels, logit_scale=scale, want_grad=True, grad_scale=up)
+    dh, dw = got.dhidden, got.dweights
+    if call == "alone":
+        dh, dw = tbe.tbe_catalogue_loss_backward(hidden, weights, labels, got.lse, logit_scale=scale, grad_scale=up,
+                                                 token_loss=got.token_loss)
+    p, r, off = wanted(hidden, weights, labels, scale)
+    g = p / (1 + r)[:, None]
+    g[torch.arange(N, device="cuda"), labels] = -r / (1 + r)
+    h, w = hidden.double(), weights.double()
+    half = torch.finfo(TYPES[kind]).eps / 2
+    # half a step of its type; what r is off by, once for itself and once for 1 + r; the log-sum's rounding (which stays
+    # below 2^-22 of 64); the products' own sums; fp16's smallest numbers
+    lse = torch.log1p(r) + scale * (h * w[labels]).sum(1)
+    each = half + 2 * off[:, None] + 2.0**-21 * (1 + lse.abs())[:, None]
+    f = up * abs(scale) / N
+    for t, want, bound in ((dh, up * scale / N * (g @ w), f * ((each + V * 2.0**-23) * g.abs() + 2.0**-38) @ w.abs()),
+                           (dw, up * scale / N * (g.T @ h), f * ((each + N * 2.0**-23) * g.abs() + 2.0**-38).T @ h.abs())):
+        bound = bound + half * want.abs() + torch.finfo(t.dtype).smallest_normal * torch.finfo(t.dtype).eps
+        worst = ((t.double() - want).abs() / bound).max().item()
+        assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
 @pytest.mark.parametrize("V", [3, 700, 40000])
 def test_logits_of_nothing(V, kind):
     """Rows whose logits are all -inf, or all but the label's, or where only the label's is -inf."""
@@ -92,6 +121,14 @@ def test_one_row_and_no_scale(V):
     x = (hidden.double() @ weights[:1].double().T).squeeze(1)
     assert not one.token_loss.any()
     assert torch.allclose(one.lse.double(), x, rtol=2.0**-18, atol=2.0**-18)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_one_row_has_no_gradient(kind):
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    weights, hidden = (torch.randn(n, 32, generator=gen, device="cuda").to(TYPES[kind]) for n in (1, 9))
+    got = tbe.tbe_catalogue_loss(hidden, weights, torch.zeros(9, dtype=torch.int64, device="cuda"), want_grad=True)
+    assert not got.dhidden.any() and not got.dweights.any()
 
 
 @pytest.mark.parametrize("N,V,D,scale", [(33, 40001, 72, -0.5), (64, 100003, 128, 1.0), (1, 32768, 64, 0.0)])
