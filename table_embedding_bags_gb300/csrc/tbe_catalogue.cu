@@ -48,6 +48,7 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMost = 3.4028235e38f;  // offsets of exponentials stay finite: that of a logit of +inf is then +inf
 
 __device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -526,7 +527,7 @@ struct SumsOf {
 #pragma unroll
       for (int k = 1; k < 32; ++k) top = fmaxf(top, v[k]);
     }
-    top = fmaxf(m, g.scale2 == 0.f ? 0.f : top * g.scale2);
+    top = fmaxf(m, g.scale2 == 0.f ? 0.f : fminf(top * g.scale2, kMost));
     const float to = top == -INFINITY ? 0.f : top;
     l *= exp2_of(m - to);
     exps(v, g.scale2, -to);
@@ -703,8 +704,9 @@ struct FewSums {
     for (int k = 0; k < 32; ++k) {
       const float x = v[k] * g.scale2;
       if (x > m[k]) {
-        l[k] = fmaf(l[k], exp2_of(m[k] - x), exp2_of(fmaf(v[k], g.scale2, -x)));
-        m[k] = x;
+        const float top = fminf(x, kMost);
+        l[k] = fmaf(l[k], exp2_of(m[k] - top), exp2_of(fmaf(v[k], g.scale2, -top)));
+        m[k] = top;
       } else {
         l[k] += exp2_of(fmaf(v[k], g.scale2, -m[k]));
       }
@@ -960,10 +962,14 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const RowArgs a) {
     // The label's own term is not in l, which therefore keeps its digits where that logit stands out and the loss,
     // log(1 + l 2^-d), is close to 0.  d is how far the label's logit lies above m.
     const int32_t n = a.rows[row];
-    const float x = a.mine[row], d = fmaf(x, a.scale2, -m);
+    const float x = a.mine[row], own = x * a.scale2, d = fmaf(x, a.scale2, -m);
     mine = d > -64.f ? log1pf(l * exp2f(-d)) : (log2f(l) - d) * kLn2;
-    // (l == 0: there is no other row, or none that reaches 2^-126 of it)
-    const float log_sum = l == 0.f ? x * a.scale2 : m + (d <= 0.f ? log2f(l + exp2f(d)) : d + log1pf(l * exp2f(-d)) * kLog2e);
+    float log_sum = m + (d <= 0.f ? log2f(l + exp2f(d)) : d + log1pf(l * exp2f(-d)) * kLog2e);
+    if (l == 0.f) log_sum = own;  // there is no other row, or none that reaches 2^-126 of the label's
+    if (own == INFINITY) {
+      mine = NAN;           // (inf - inf)
+      log_sum = l + own;    // (a NaN stays one)
+    }
     a.lse2[row] = log_sum;
     a.lse[n] = log_sum * kLn2;
     a.own[row] = own_of(mine);

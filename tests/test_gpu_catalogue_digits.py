@@ -91,6 +91,43 @@ def test_gradients_of_tokens_that_are_nearly_learnt(N, V, D, scale, call, kind):
         assert worst <= 1, worst
 
 
+def by_formula(hidden, weights, labels, scale=1.0):
+    x = scale * (hidden.double() @ weights.double().T)
+    lse = torch.logsumexp(x, 1)
+    return lse, lse - x[torch.arange(len(labels), device="cuda"), labels], torch.exp(x - lse[:, None])
+
+
+def alike(a, b):
+    """The same infinities and NaN in the same places."""
+    a, b = a.double(), b.double()
+    return torch.equal(a.isnan(), b.isnan()) and torch.equal(a == math.inf, b == math.inf) and torch.equal(a == -math.inf, b == -math.inf)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("V,scale", [(700, 1.0), (700, -0.5), (40000, 1.0), (40000, -0.5)])
+def test_logits_that_are_no_finite_numbers(V, scale, kind):
+    """Infinities in a row of the table (logits of either sign), in hidden rows, and NaN, as the formulas have them."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    N, D = 40, 64
+    weights = torch.randn(V, D, generator=gen, device="cuda").to(TYPES[kind])
+    hidden = torch.randn(N, D, generator=gen, device="cuda").to(TYPES[kind])
+    labels = torch.randint(0, V, (N,), generator=gen, device="cuda")
+    weights[V // 3, 5] = math.inf
+    labels[:6] = V // 3
+    hidden[7, 5] = 0.0  # a logit of 0 * inf
+    hidden[9] = math.inf  # logits of inf - inf
+    hidden[11, 2] = math.nan
+    got = tbe.tbe_catalogue_loss(hidden, weights, labels, logit_scale=scale, want_grad=True)
+    lse, loss, p = by_formula(hidden, weights, labels, scale)
+    assert (lse == math.inf).any() and lse.isfinite().any() and lse.isnan().any()
+    assert alike(got.lse, lse) and alike(got.token_loss, loss) and got.loss.isnan()
+    ok = lse.isfinite() & loss.isfinite()
+    assert torch.allclose(got.lse[ok].double(), lse[ok], rtol=1e-4) and torch.allclose(got.token_loss[ok].double(), loss[ok], rtol=1e-3, atol=1e-3)
+    g = p.clone()
+    g[torch.arange(N, device="cuda"), labels] -= 1
+    assert alike(got.dhidden, (g @ weights.double()) * scale)
+
+
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 @pytest.mark.parametrize("V", [3, 700, 40000])
 def test_logits_of_nothing(V, kind):
