@@ -153,7 +153,9 @@ __device__ __forceinline__ float to_float(uint16_t u) {
 }
 
 // Powers of two for fp16: what brings values of magnitude `top` to 2^14 or
-// just below, as an exponent (kept where fp32 stays normal).
+// just below, as an exponent (kept where fp32 stays normal).  For states and
+// keys the finite values decide: moved down by an infinity's power, they would
+// all become 0.  (x 0 + x is NaN for an infinity, which a maximum passes over.)
 __device__ __forceinline__ int room_for(float top) {
   const int e = (int)(__float_as_uint(top) >> 23 & 255) - 127;  // 128 for infinities and NaN
   return max(-100, min(60, 13 - e));
@@ -454,7 +456,7 @@ struct Worker {
       float t = 0.f;
       if (holds()) {
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) t = fmaxf(t, fabsf(s[j]));
+        for (int j = 0; j < kCols; ++j) t = fmaxf(t, fabsf(fmaf(s[j], 0.f, s[j])));  // (room_for: finite values)
       }
       if (!largest(t)) return false;
       const int up = room_for(t);
@@ -500,14 +502,18 @@ struct Worker {
   }
   // fp16: the power of two that the weighted keys are moved by.
   __device__ __forceinline__ bool room_for_keys(int n, int& up) {
-    __half2 top = __half2half2(__ushort_as_half(0));
+    const __half2 none = __half2half2(__ushort_as_half(0));
+    __half2 top = none;
 #pragma unroll 2
     for (int i = 0; i < kChunks; ++i) {
       const int at = i * 32 * kWarps * 16 + (warp * 32 + lane) * 16;
       const uint4 u = *reinterpret_cast<const uint4*>(room + Room<W>::k + at);
       if (place(at / 128 % kTile) < n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(reinterpret_cast<const __half2*>(&u)[e]));
+        for (int e = 0; e < 4; ++e) {
+          const __half2 x = reinterpret_cast<const __half2*>(&u)[e];
+          top = __hmax2(top, __habs2(__hfma2(x, none, x)));
+        }
       }
     }
     const float2 t = __half22float2(top);

@@ -149,3 +149,43 @@ def test_runs_of_several_tiles_by_smaller_copies(d):
         close(got, w, z, 2.0**-8, fp32, what)
     close(f.s_last, want[1], size[1], 0.0, fp32, "s_last")
     close(b.ds0, want[5], size[5], 0.0, fp32, "ds0")
+
+
+
+
+def finite_where_the_definition_is(got, want, size, half, fp32, what):
+    """Where the definition's output is finite, so is the kernel's, and right."""
+    ok = want.isfinite()
+    assert ok.any() and not ok.all(), what
+    close(torch.where(ok, got.double(), 0.0), torch.where(ok, want, 0.0), size, half, fp32, what)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 100])
+@pytest.mark.parametrize("name", ["s0", "v", "k", "ds_last", "do", "q"])
+def test_an_infinity_in_a_state_leaves_the_others_their_digits(name, d, kind):
+    """In a state that comes in, or in what is added to it first: the power of two that fp16 operands are moved by comes from
+    their finite values.  (An infinite key or query makes a row of the state infinite, a value a column.)"""
+    c = make([700, 300], 16, d, kind, 4, True)
+    size = wanted(c, magnitudes=True)
+    x = dict(c)
+    x[name] = c[name].clone()
+    if name in ("s0", "ds_last"):
+        x[name][0, 1, 3, 5] = math.inf
+        x[name][1, 2, 7, 9] = -math.inf
+    else:
+        first = (0, 700) if name in "vk" else (699, 999)
+        x[name][first[0], 1, 5] = math.inf
+        x[name][first[1], 0, 9] = -math.inf
+    f, b = both(x)
+    want = wanted(x)
+    fp32 = (d + 128 + 700 / 16) * 2.0**-22
+    half = torch.finfo(DT[kind]).eps / 2
+    if name in ("s0", "v", "k"):
+        finite_where_the_definition_is(f.s_last, want[1], size[1], 0.0, fp32, "s_last")
+    else:
+        finite_where_the_definition_is(b.ds0, want[5], size[5], 0.0, fp32, "ds0")
+    if name in ("s0", "v"):
+        finite_where_the_definition_is(f.o, want[0], size[0], half, fp32, "o")
+    if name in ("ds_last", "do"):
+        finite_where_the_definition_is(b.dv, want[4], size[4], half, fp32, "dv")
