@@ -483,8 +483,8 @@ int tbe_gated_scan_step(const tbe_scan_inputs* in, float* state, void* h, int64_
  *   dtype   : TBE_F16 or TBE_BF16 (TBE_F32: TBE_ERR_UNSUPPORTED).  Products
  *             of inputs are exact, sums and states fp32; q k^T (times its
  *             decay) and the state as it is read are rounded to dtype.
- * A NaN or an infinity stays in its sequence and head; there it may reach back
- * over up to 127 tokens before its own.  Limits: head_dim <=
+ * A NaN or an infinity reaches what the formulas let it reach and nothing else
+ * (what they make infinite may be NaN).  Limits: head_dim <=
  * TBE_LINEAR_MAX_HEAD_DIM, heads <= 2^16, tokens < 2^36.
  */
 #define TBE_LINEAR_MAX_HEAD_DIM 128

@@ -41,6 +41,13 @@
 // first moved by a power of two that its largest value names: products by
 // row, the state and the keys by tile.
 //
+// Values that are no numbers.  The mask's zeros do not stop them inside a tile:
+// 0 times a NaN is one.  A tile's values are looked over while the products of
+// queries and keys go on.  Those of other sequences are set to 0, and the tile is
+// cut to its first sequence; for those of its own the product with the values is
+// taken again without the last of them and what follows, for the outputs before
+// it, and so on: tokens keep theirs up to such a value.
+//
 // What bounds it: the latency of a tile's chain, with one block of 128-wide
 // heads to an SM (its operands take 194 KB) or two of 64-wide ones.  In cycles,
 // 128 wide: copies 1,900, q k^T 1,100, weights 1,500-2,100, keys 2,100, products
@@ -197,13 +204,15 @@ struct Tile {
   int64_t sequence;   // its first sequence
 };
 struct Control {
-  uint64_t known[2], full, products, weighted, keys, out_done, add_done, add_read, out_read, state_ready, exchange, row_max[4];
+  uint64_t known[2], full, products, weighted, keys, out_done, add_done, add_read, out_read, state_ready, exchange, again_done, again_read, row_max[4];
   Tile tile[2];
   float pow[kPowers];
   alignas(16) float by_col[16];  // powers over 16 neighbouring columns
   float top_row[2][kTile];
   uint32_t top[3];
-  int32_t bad[2];
+  int32_t bad[2];          // some value of the tile is an infinity or a NaN:
+  int32_t again;           //   outputs before this place are made again (0: no more)
+  uint32_t passes[kWarps]; //   times that a warp has waited for that
   uint32_t tmem;
   int32_t dead;
 };
@@ -374,6 +383,53 @@ __device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, 
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+
+// Whether 16 bytes of values hold an infinity or a NaN: 0 times them, added to `sum`, is NaN then.
+template <int DT>
+__device__ __forceinline__ void look_at(const uint4& u, uint32_t& sum) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (DT == TBE_BF16) {
+      const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&(&u.x)[e]),
+                                       __bfloat162bfloat162(__ushort_as_bfloat16(0)), *reinterpret_cast<const __nv_bfloat162*>(&sum));
+      sum = *reinterpret_cast<const uint32_t*>(&r);
+    } else {
+      const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&(&u.x)[e]), __half2half2(__ushort_as_half(0)),
+                                *reinterpret_cast<const __half2*>(&sum));
+      sum = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+}
+// The last place marked before place n, or 0.
+__device__ __forceinline__ int last_before(const uint32_t (&at)[4], int n) {
+  int last = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t u = n >= w * 32 + 32 ? at[w] : n > w * 32 ? at[w] & ((1u << (n - w * 32)) - 1) : 0u;
+    if (u) last = w * 32 + 31 - __clz((int)u);
+  }
+  return last;
+}
+template <int DT>
+__device__ __forceinline__ bool seen(uint32_t sum) {
+  const float2 x = unpack2<DT>(sum);
+  return !(x.x + x.y == x.x + x.y);
+}
+// The same of all values of a tile, by STEP threads.
+template <int DT, int W, int STEP>
+__device__ __forceinline__ bool not_finite(const uint8_t* values, int thread) {
+  constexpr int kPieces = Room<W>::operand / 16 / STEP;
+  static_assert(kPieces % 4 == 0, "four at a time");
+  uint32_t sum[4] = {0, 0, 0, 0};
+#pragma unroll 2
+  for (int i = 0; i < kPieces; i += 4) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      look_at<DT>(*reinterpret_cast<const uint4*>(values + (i + k) * STEP * 16 + thread * 16), sum[k]);
+  }
+  return seen<DT>(sum[0]) || seen<DT>(sum[1]) || seen<DT>(sum[2]) || seen<DT>(sum[3]);
+}
+
 template <int DT, int W, bool SUMS>
 struct Worker {
   static constexpr int kCols = W / 2;  // of the state and the outputs, to a thread
@@ -485,21 +541,6 @@ struct Worker {
   // A place's distance from the tile's first position, in the pass's direction.
   __device__ __forceinline__ int place(int r) const { return ps.back ? kTile - 1 - r : r; }
 
-  // Whether the tile's values hold an infinity or a NaN.
-  __device__ __forceinline__ bool not_finite(int values) const {
-    constexpr uint32_t kInf = DT == TBE_BF16 ? 0x7f80u : 0x7c00u;
-    bool bad = false;
-#pragma unroll 4
-    for (int i = warp * 32 + lane; i < Room<W>::operand / 16; i += 32 * kWarps) {
-      const uint4 u = *reinterpret_cast<const uint4*>(room + values + i * 16);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t x = (&u.x)[e];
-        bad |= (x & kInf) == kInf || (x >> 16 & kInf) == kInf;
-      }
-    }
-    return bad;
-  }
   // fp16: the power of two that the weighted keys are moved by.
   __device__ __forceinline__ bool room_for_keys(int n, int& up) {
     const __half2 none = __half2half2(__ushort_as_half(0));
@@ -683,7 +724,7 @@ struct Worker {
   }
 
   // o = the tile's part and the state's, rounded once.
-  __device__ __forceinline__ void write_outputs(const Tile& t, int n, int up, float read_scale) {
+  __device__ __forceinline__ void write_outputs(const Tile& t, int n, int up, float read_scale, uint64_t* out_read) {
     const int far = place(row);
     const bool live = t.live && far < t.e0;
     const float of_state = live ? c.pow[far + 1 - ps.back] * read_scale : 0.f, of_tile = DT == TBE_F16 ? pow2(-up) : 1.f;
@@ -711,7 +752,7 @@ struct Worker {
       }
       if (j + 16 >= kCols) {
         tc_before_sync();
-        arrive(&c.out_read);
+        arrive(out_read);
       }
       const int cols = a.d - half * kCols - j;
       if (far >= n || cols <= 0) continue;
@@ -782,9 +823,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
     bar_init(&c.out_read, kWarps);
     bar_init(&c.state_ready, kWarps);
     bar_init(&c.exchange, kWarps);
+    bar_init(&c.again_done, 2);
+    bar_init(&c.again_read, kWarps);
     for (int k = 0; k < 4; ++k) bar_init(&c.row_max[k], 2);
     for (int k = 0; k < 3; ++k) c.top[k] = 0;
     c.bad[0] = c.bad[1] = 0;
+    for (int k = 0; k < kWarps; ++k) c.passes[k] = 0;
     c.dead = 0;
     bars_visible();
   }
@@ -813,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
     Marker m = {st, ps.in != nullptr || ps.out != nullptr, a.piece == 0, 0, 0};
     if (!SUMS) m.seek(p0, lane);
     const bool live = !SUMS && run > 0 && __shfl_sync(kFull, m.x, 0) > p0;  // (m.x of lane 0: the first start)
-    uint32_t states = 0, adds = 0, copies = 0;
+    uint32_t states = 0, adds = 0, copies = 0, reads = 0;
     bool added = false;  // by the tile before
     const uint32_t room0 = smem_u32(room), terms0 = smem_u32(raw);
     const uint32_t format = DT == TBE_BF16;
@@ -833,14 +877,38 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
       return t;
     };
     Tile following = find(begin, live);
-    // The values from place n on are set to 0: some value of the tile is an infinity or a NaN, and those of other
-    // sequences are multiplied by 0.
+    // The values from place n on are set to 0.
     auto drop = [&](int n, int values) {
+#pragma unroll 1
       for (int i = lane; i < R::operand / 16; i += 32) {
         const int r = i / 8 % kTile;
         if ((ps.back ? kTile - 1 - r : r) >= n) *reinterpret_cast<uint4*>(room + values + i * 16) = make_uint4(0, 0, 0, 0);
       }
       to_products();
+      __syncwarp();
+    };
+    // The places of the tile's values that hold one.
+    auto where = [&](uint32_t (&places)[4], int values) {
+#pragma unroll 1
+      for (int i = lane; i < R::operand / 16; i += 32) {
+        uint32_t sum = 0;
+        look_at<DT>(*reinterpret_cast<const uint4*>(room + values + i * 16), sum);
+        const int r = i / 8 % kTile, place = ps.back ? kTile - 1 - r : r;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) places[w] |= seen<DT>(sum) && place >> 5 == w ? 1u << (place & 31) : 0u;
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) places[w] = __reduce_or_sync(kFull, places[w]);
+    };
+    // The weighted products times the values.
+    auto multiply = [&](int values, uint64_t* done) {
+      if (lane == 0) {
+        const uint32_t idesc = tc_idesc(format, 0, 1, kTile, W);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          tc_mma_tmem(tmem + R::to, tmem + R::weighted(k), desc_of(room0 + values + k * 2048, kBlock), idesc, k > 0);
+        tc_commit(done);
+      }
       __syncwarp();
     };
     // A tile's rows on their way to the L2.
@@ -869,6 +937,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
     };
     for (uint32_t i = 0;; ++i) {
       const Tile t = following;
+      bool bad = false;
       const int values = values_at<W, SUMS>(a.piece, i);
       // (the products and copies of the tile before are through)
       if (lane == 0) {
@@ -910,15 +979,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
         ahead(following);
         if (!wait(&c.weighted, i, c)) break;
         tc_after_sync();
-        if (t.mixed && *(volatile int32_t*)&c.bad[i & 1]) drop(t.e0, values);
-        if (lane == 0) {
-          const uint32_t idesc = tc_idesc(format, 0, 1, kTile, W);
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            tc_mma_tmem(tmem + R::to, tmem + R::weighted(k), desc_of(room0 + values + k * 2048, kBlock), idesc, k > 0);
-          tc_commit(&c.out_done);
-        }
-        __syncwarp();
+        bad = *(volatile int32_t*)&c.bad[i & 1];
+        if (bad && t.mixed) drop(t.e0, values);
+        multiply(values, &c.out_done);
       }
       if (t.adds) {
         if (!wait(&c.keys, adds, c)) break;
@@ -943,12 +1006,33 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
         ++adds;
       }
       added = t.adds;
-      if (!SUMS && t.mixed && *(volatile int32_t*)&c.bad[i & 1] && t.e0 < t.n) {
+      if (!SUMS && t.mixed && bad && t.e0 < t.n) {
         m.seek(t.p + t.e0, lane);  // the others were told by the same word that the tile ends there
         following = find(t.p + t.e0, false);
       }
       if (!SUMS && !wait(&c.out_done, i, c)) break;
       if (t.adds && !wait(&c.add_done, adds - 1, c)) break;
+      if (!SUMS && __builtin_expect(bad, 0)) {  // outputs before such a value again, without it and what follows
+        uint32_t places[4] = {0, 0, 0, 0};
+        where(places, values);
+        if (!wait(&c.out_read, i, c)) break;
+        bool ok = true;
+        for (int n = t.mixed ? t.e0 : t.n; ok && n > 0;) {
+          n = last_before(places, n);
+          tc_after_sync();
+          if (n > 0) drop(n, values);
+          if (lane == 0) {
+            c.again = n;
+            bar_arrive(&c.again_done);
+            if (n == 0) bar_arrive(&c.again_done);
+          }
+          if (n > 0) {
+            multiply(values, &c.again_done);
+            ok = wait(&c.again_read, reads++, c);
+          }
+        }
+        if (!ok) break;
+      }
     }
     // (after a wait that gave up, copies in flight have time to land)
     if (*(volatile int32_t*)&c.dead && copies) mbar_wait(&c.full, (copies - 1) & 1, 1 << 16);
@@ -991,10 +1075,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
         }
       }
       int n = t.n;
-      if (t.mixed || t.adds) {
+      // (sums take all values of their own places)
+      if (!SUMS || t.mixed || t.adds) {
         if (!wait(&c.full, i, c)) break;
       }
-      if (t.mixed && __any_sync(kFull, w.not_finite(values_at<W, SUMS>(a.piece, i))) && lane == 0) c.bad[i & 1] = 1;
+      if ((!SUMS || t.mixed) &&
+          __any_sync(kFull, not_finite<DT, W, 32 * kWarps>(room + values_at<W, SUMS>(a.piece, i), warp * 32 + lane)) && lane == 0)
+        c.bad[i & 1] = 1;
       int up_keys = 0, up = 0;
       if (DT == TBE_F16 && t.adds && !w.room_for_keys(n, up_keys)) break;
       if (!SUMS) {
@@ -1019,8 +1106,21 @@ __global__ void __launch_bounds__(kThreads, kBlocks<W>) attention_kernel(const _
       if (!SUMS) {
         if (!wait(&c.out_done, i, c)) break;
         tc_after_sync();
-        if (t.mixed && *(volatile int32_t*)&c.bad[i & 1]) n = min(n, t.e0);
-        w.write_outputs(t, n, up, read_scale);
+        const bool bad = *(volatile int32_t*)&c.bad[i & 1];
+        if (t.mixed && bad) n = t.e0;
+        w.write_outputs(t, n, up, read_scale, &c.out_read);
+        if (__builtin_expect(bad, 0)) {  // again, as often as the product is taken
+          uint32_t passes = c.passes[warp];
+          bool ok;
+          while ((ok = wait(&c.again_done, passes++, c)) && (n = *(volatile int32_t*)&c.again) > 0) {
+            tc_after_sync();
+            w.write_outputs(t, n, up, read_scale, &c.again_read);
+          }
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) c.passes[warp] = passes;
+          __syncwarp();
+        }
       }
     }
     if (SUMS && w.holds()) w.write(ps.carry + ((int64_t)head * a.runs + run) * W * W, W);

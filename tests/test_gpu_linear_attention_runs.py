@@ -189,3 +189,53 @@ def test_an_infinity_in_a_state_leaves_the_others_their_digits(name, d, kind):
         finite_where_the_definition_is(f.o, want[0], size[0], half, fp32, "o")
     if name in ("ds_last", "do"):
         finite_where_the_definition_is(b.dv, want[4], size[4], half, fp32, "dv")
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 100])
+@pytest.mark.parametrize("layout", ["slices", "off"])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("lengths,tokens", [([128], [127]), ([300], [0, 50, 130, 299]), ([40, 60, 0, 90], [70, 189]),
+                                            ([2000, 3001], [1999, 2300, 4000])])
+def test_what_is_no_number_is_not_seen_before_its_token(lengths, tokens, value, state, layout, d, kind):
+    """Single entries of the values that are no numbers: other columns, and tokens before (behind, for dk and dv), are
+    as the definition has them."""
+    H = 2 if sum(lengths) < 1000 else 16
+    c = make(lengths, H, d, kind, 3, state, layout)
+    size = wanted(c, magnitudes=True)
+    half = torch.finfo(DT[kind]).eps / 2
+    fp32 = (d + 128 + max(lengths) / 16) * 2.0**-22 + 2.0**-15
+    # the operand that takes the values' place: v for o, k for dq, q for dk, do for dv
+    for name, i in (("v", 0), ("k", 2), ("q", 3), ("do", 4)):
+        x = dict(c)
+        x[name] = c[name].clone()
+        for j, t in enumerate(tokens):
+            x[name][t, 1, 7 * j + 3] = value
+        f, b = both(x, want_last=state)
+        want = wanted(x)
+        finite_where_the_definition_is((f.o, None, *b)[i], want[i], size[i], half, fp32, name)
+        if state and name in ("v", "do"):
+            j = 1 if name == "v" else 5
+            finite_where_the_definition_is(f.s_last if name == "v" else b.ds0, want[j], size[j], 0.0, fp32, name + "'s state")
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("lengths", [[300, 500], [1] * 200, [4000, 2000]])
+def test_a_head_of_nothing_but_nan(lengths, kind):
+    """Every value of one head, or every third one: the other heads stay as they are, bit for bit."""
+    c = make(lengths, 16 if sum(lengths) > 1000 else 2, 64, kind, 5, False)
+    f, b = both(c, want_last=False)
+    for every in (1, 3):
+        x = {**c, "v": c["v"].clone(), "do": c["do"].clone()}
+        x["v"][::every, 1] = math.nan
+        x["do"][::every, 1] = math.nan
+        g, e = both(x, want_last=False)
+        others = [h for h in range(c["q"].shape[1]) if h != 1]
+        assert all(torch.equal(p[:, others], q[:, others]) for p, q in zip((f.o, *b[:3]), (g.o, *e[:3])))
+        assert g.o[::every, 1].isnan().all() and e.dv[::every, 1].isnan().all()
+        first = np.concatenate([[0], np.cumsum(lengths)])
+        for s, n in enumerate(lengths):  # up to its sequence's first such token an output is the clean one
+            at = -int(first[s]) % every
+            assert torch.equal(g.o[first[s]:first[s] + min(at, n), 1], f.o[first[s]:first[s] + min(at, n), 1])
+            assert g.o[first[s]:first[s] + min(at, n), 1].isfinite().all()
