@@ -470,8 +470,9 @@ int tbe_gated_scan_step(const tbe_scan_inputs* in, float* state, void* h, int64_
  *   q, k, v : device [tokens, heads, head_dim] of dtype, consecutive along
  *             head_dim, *_stride elements from token to token and
  *             *_head_stride from head to head (so the three may be slices of
- *             one projection; heads may also come first); not overlapping any
- *             output
+ *             one projection; heads may also come first); refused where an
+ *             output overlaps any input or another output (rows that lie
+ *             between those of another tensor with the same steps do not)
  *   decay   : device fp32 [heads], 0 for none; not negative (a negative one
  *             grows and may overflow).  It has no gradient: a constant.
  *   offsets : device int64 (or int32 where offsets_i32 != 0) [sequences + 1],
@@ -517,11 +518,10 @@ size_t tbe_linear_attention_workspace_bytes(int64_t tokens, int32_t heads, int32
 
 /*   o      : device [tokens, heads, head_dim] of dtype with strides of its own
  *   s_last : device fp32 [sequences, heads, head_dim, head_dim] or NULL: each
- *            sequence's last state (an empty sequence's s0, or 0); refused
- *            where it overlaps s0
- * Results do not depend on timing.  Errors: TBE_ERR_INVALID_ARG,
- * TBE_ERR_UNSUPPORTED (limits, types, alignment), TBE_ERR_WORKSPACE,
- * TBE_ERR_CUDA; TBE_DEV_BAD_OFFSETS. */
+ *            sequence's last state (an empty sequence's s0, or 0)
+ * Results do not depend on timing.  Errors, of the backward too:
+ * TBE_ERR_INVALID_ARG, TBE_ERR_UNSUPPORTED (limits, types, alignment),
+ * TBE_ERR_WORKSPACE, TBE_ERR_CUDA; TBE_DEV_BAD_OFFSETS, TBE_DEV_TIMEOUT. */
 int tbe_linear_attention(const tbe_linear_attention_inputs* in, void* o, int64_t o_stride, int64_t o_head_stride,
                          float* s_last, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
 
@@ -530,9 +530,7 @@ int tbe_linear_attention(const tbe_linear_attention_inputs* in, void* o, int64_t
  *   dout    : device [tokens, heads, head_dim] of dtype, with strides
  *   ds_last : device fp32 [sequences, heads, head_dim, head_dim] or NULL (zero)
  *   out     : dq, dk, dv (device, dtype, own strides) and ds0 (device fp32
- *             [sequences, heads, head_dim, head_dim] or NULL; refused where
- *             it overlaps s0 or ds_last)
- * No input overlaps an output. */
+ *             [sequences, heads, head_dim, head_dim] or NULL) */
 typedef struct tbe_linear_attention_grads {
   void* dq;
   void* dk;

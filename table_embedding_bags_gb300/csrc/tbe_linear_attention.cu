@@ -59,6 +59,7 @@
 // 65,537 x 16 x 64 f16 with states 1,147 us (159), of 2,048 sequences, 40,960 x
 // 8 x 64 bf16 232 us (50).  The same recurrences in tiles of 64 with mma.sync,
 // four warps to a block, took 418, 1,466 and 358 us.
+#include "tbe_overlap.cuh"
 #include "tbe_tensor.cuh"
 
 #include <algorithm>
@@ -1442,12 +1443,35 @@ void set_rows(Pass& p, const Maps& m, int q, int k, int v, const Rows& o, int32_
   p.piece_o = piece_of(o.p, o.stride, o.head, d, 32);
 }
 
-// Whether two [sequences, heads, d, d] states share memory: blocks read the
-// one while others write the other.
-bool overlap(const tbe_linear_attention_inputs* in, const float* p, const float* q) {
-  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  const size_t bytes = sizeof(float) * (size_t)in->sequences * in->heads * in->head_dim * in->head_dim;
-  return p && q && a < b + bytes && b < a + bytes;
+// The memory of rows, by tokens of heads or heads of tokens.
+Region region_of(const Rows& r, const tbe_linear_attention_inputs* in) {
+  const int64_t N = in->tokens, H = in->heads, d = in->head_dim;
+  const Region tokens = {(intptr_t)r.p, 2 * d, N, 2 * r.stride, H, 2 * r.head};
+  const Region heads = {(intptr_t)r.p, 2 * d, H, 2 * r.head, N, 2 * r.stride};
+  return N <= 1 || (H > 1 && r.stride < r.head * (H - 1) + d) ? heads : tokens;
+}
+Region states_of(const float* p, const tbe_linear_attention_inputs* in) {
+  return bytes_of(p, (int64_t)sizeof(float) * in->sequences * in->heads * in->head_dim * in->head_dim);
+}
+// Whether an output shares memory with an input (`more` of them beside those of `in`) or another output: blocks read
+// the one while others write the other.
+bool overlap(const tbe_linear_attention_inputs* in, const Region* more, int inputs, const Region* out, int outputs) {
+  const int64_t entry = in->offsets_i32 ? 4 : 8;
+  const Region own[6] = {region_of({in->q, in->q_stride, in->q_head_stride}, in),
+                         region_of({in->k, in->k_stride, in->k_head_stride}, in),
+                         region_of({in->v, in->v_stride, in->v_head_stride}, in),
+                         bytes_of(in->decay, (int64_t)sizeof(float) * in->heads),
+                         bytes_of(in->offsets, in->offsets ? entry * ((int64_t)in->sequences + 1) : 0),
+                         states_of(in->s0, in)};
+  for (int i = 0; i < outputs; ++i) {
+    for (const Region& r : own)
+      if (share(out[i], r)) return true;
+    for (int k = 0; k < inputs; ++k)
+      if (share(out[i], more[k])) return true;
+    for (int k = 0; k < i; ++k)
+      if (share(out[i], out[k])) return true;
+  }
+  return false;
 }
 
 int go(Args& a, const Maps& maps, int passes, int32_t dtype, void* workspace, size_t bytes, cudaStream_t s) {
@@ -1500,7 +1524,8 @@ int tbe_linear_attention(const tbe_linear_attention_inputs* in, void* o, int64_t
   const Rows out = {o, o_stride, o_head_stride};
   if ((in->tokens > 0 && !o) || !fits(out, in->tokens, in->heads, in->head_dim)) return TBE_ERR_INVALID_ARG;
   if (((uintptr_t)o & 1) || ((uintptr_t)s_last & 3)) return TBE_ERR_UNSUPPORTED;
-  if (overlap(in, in->s0, s_last)) return TBE_ERR_INVALID_ARG;
+  const Region written[2] = {region_of(out, in), states_of(s_last, in)};
+  if (overlap(in, nullptr, 0, written, 2)) return TBE_ERR_INVALID_ARG;
   if (in->sequences == 0) return TBE_OK;
   Args a = args_of(in, 1, dev_status);
   Pass& p = a.pass[0];
@@ -1530,7 +1555,9 @@ int tbe_linear_attention_backward(const tbe_linear_attention_inputs* in, const v
     if ((uintptr_t)r->p & 1) return TBE_ERR_UNSUPPORTED;
   }
   if (((uintptr_t)ds_last | (uintptr_t)g->ds0) & 3) return TBE_ERR_UNSUPPORTED;
-  if (overlap(in, ds_last, g->ds0) || overlap(in, in->s0, g->ds0)) return TBE_ERR_INVALID_ARG;
+  const Region read[2] = {region_of(d, in), states_of(ds_last, in)};
+  const Region written[4] = {region_of(dq, in), region_of(dk, in), region_of(dv, in), states_of(g->ds0, in)};
+  if (overlap(in, read, 2, written, 4)) return TBE_ERR_INVALID_ARG;
   if (in->sequences == 0) return TBE_OK;
   Args a = args_of(in, 3, dev_status);
   Maps maps;
@@ -1562,6 +1589,10 @@ int tbe_linear_attention_step(const tbe_linear_attention_inputs* in, float* stat
   const Rows out = {o, o_stride, o_head_stride};
   if (!state || !o || !fits(out, in->tokens, in->heads, in->head_dim)) return TBE_ERR_INVALID_ARG;
   if (((uintptr_t)o & 1) || ((uintptr_t)state & 3)) return TBE_ERR_UNSUPPORTED;
+  const Region written[2] = {region_of(out, in), states_of(state, in)};
+  tbe_linear_attention_inputs read = *in;  // (offsets are not)
+  read.offsets = nullptr;
+  if (overlap(&read, nullptr, 0, written, 2)) return TBE_ERR_INVALID_ARG;
   const int64_t blocks = (int64_t)in->sequences * in->heads * ((in->head_dim + kStepCols - 1) / kStepCols);
   if (blocks >= (int64_t(1) << 31)) return TBE_ERR_UNSUPPORTED;
   StepArgs a = {};

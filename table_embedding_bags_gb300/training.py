@@ -150,8 +150,8 @@ def tbe_linear_attention(q, k, v, decay, offsets, s0=None, scale: float = 1.0, w
     bfloat16 (tokens and heads may be strided, so slices of one projection
     do); ``decay`` is fp32 [heads]; ``offsets`` int64 or int32 [sequences +
     1]; ``s0`` fp32 [sequences, heads, head_dim, head_dim] (keys by values).
-    ``want_last`` returns each sequence's last state.  ``out`` must not overlap
-    an input."""
+    ``want_last`` returns each sequence's last state.  An ``out`` that overlaps
+    an input is refused."""
     m = _compiled or _marshal()
     return LinearAttention(*m.linear_attention(q, k, v, decay, offsets, s0, scale, want_last, out, dev_status,
                                                None if stream is None else stream.cuda_stream))
@@ -161,8 +161,8 @@ def tbe_linear_attention_backward(do, q, k, v, decay, offsets, s0=None, ds_last=
                                   dev_status=None, stream=None) -> LinearAttentionGrads:
     """Gradients of sum(do * o) + sum(ds_last * s_last) from the inputs of a
     ``tbe_linear_attention`` call.  ``out``: the three tensors to write dq, dk
-    and dv to (strided as ``q`` may be; not overlapping an input).  ds0 is
-    returned where ``s0`` was given."""
+    and dv to (strided as ``q`` may be; refused where they overlap an input
+    or each other).  ds0 is returned where ``s0`` was given."""
     m = _compiled or _marshal()
     return LinearAttentionGrads(*m.linear_attention_backward(do, q, k, v, decay, offsets, s0, ds_last, scale, out,
                                                              dev_status, None if stream is None else stream.cuda_stream))

@@ -239,3 +239,29 @@ def test_a_head_of_nothing_but_nan(lengths, kind):
             at = -int(first[s]) % every
             assert torch.equal(g.o[first[s]:first[s] + min(at, n), 1], f.o[first[s]:first[s] + min(at, n), 1])
             assert g.o[first[s]:first[s] + min(at, n), 1].isfinite().all()
+
+
+@pytest.mark.parametrize("order", ["slices", "slices of heads", "heads first"])
+def test_outputs_between_the_inputs(order):
+    """All of a call's rows in one buffer: what lies between is neither refused nor touched."""
+    c = make([300, 77], 3, 40, "bf16", 6, False)
+    want, grads = both(c, want_last=False)
+    N, H, d = c["q"].shape
+    if order == "slices":
+        room = torch.zeros(N, 9, H, d, dtype=torch.bfloat16, device="cuda").unbind(1)
+    elif order == "slices of heads":
+        room = torch.zeros(N, H, 9, d, dtype=torch.bfloat16, device="cuda").unbind(2)
+    else:
+        room = [x.transpose(0, 1) for x in torch.zeros(H, 9, N, d, dtype=torch.bfloat16, device="cuda").unbind(1)]
+    q, k, v, do, o, dq, dk, dv, last = room
+    for x, name in zip((q, k, v, do), ("q", "k", "v", "do")):
+        x.copy_(c[name])
+    last.fill_(7)
+    f = tbe.tbe_linear_attention(q, k, v, c["decay"], c["offsets"], scale=0.3, out=o)
+    b = tbe.tbe_linear_attention_backward(do, q, k, v, c["decay"], c["offsets"], scale=0.3, out=(dq, dk, dv))
+    assert torch.equal(f.o, want.o) and all(torch.equal(x, y) for x, y in zip(b[:3], grads[:3])) and (last == 7).all()
+    for out in ((dq, dk, dq), (q, dk, dv), (dq, dk, do)):
+        with pytest.raises(tbe.TBEError):
+            tbe.tbe_linear_attention_backward(do, q, k, v, c["decay"], c["offsets"], scale=0.3, out=out)
+    with pytest.raises(tbe.TBEError):
+        tbe.tbe_linear_attention(q, k, v, c["decay"], c["offsets"], out=v)
