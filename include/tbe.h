@@ -666,7 +666,7 @@ size_t tbe_catalogue_workspace_bytes(const tbe_catalogue_inputs* in, int32_t gra
  *   dweights        : device [vocab, width] of dtype, dweights_stride apart;
  *                     both gradients are written whole, or both NULL: the
  *                     loss alone.  They overlap no input and not each other
- *                     (refused).
+ *                     (refused); columns of one wider tensor do not
  * Results do not depend on timing.  Errors: TBE_ERR_INVALID_ARG,
  * TBE_ERR_UNSUPPORTED (limits, types, alignment), TBE_ERR_WORKSPACE,
  * TBE_ERR_CUDA; TBE_DEV_BAD_INDEX, TBE_DEV_TIMEOUT. */

@@ -37,6 +37,7 @@
 // 64 rows over 1,000,003 x 128 take 71 us where the table's bytes take 38: with
 // the table's rows as the product's every warp has exponentials to take, and a
 // tile's 64 KB wait for its 512 cycles of products and the copies' latency.
+#include "tbe_overlap.cuh"
 #include "tbe_tensor.cuh"
 
 #include <algorithm>
@@ -1370,13 +1371,6 @@ int check(const tbe_catalogue_inputs* in) {
   return TBE_OK;
 }
 
-// Whether two [rows, width] tensors of 16-bit elements share memory.
-bool overlap(const void* p, int64_t rows, int64_t stride, const void* q, int64_t rows_q, int64_t stride_q, int32_t width) {
-  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  const size_t na = 2 * ((size_t)(rows - 1) * stride + width), nb = 2 * ((size_t)(rows_q - 1) * stride_q + width);
-  return a < b + nb && b < a + na;
-}
-
 int dispatch(const Call& c, void* workspace, size_t bytes, void* stream) {
   const tbe_catalogue_inputs& in = *c.in;
   if (!workspace) return TBE_ERR_INVALID_ARG;
@@ -1387,13 +1381,16 @@ int dispatch(const Call& c, void* workspace, size_t bytes, void* stream) {
       return TBE_ERR_INVALID_ARG;
     if (((uintptr_t)c.dhidden | (uintptr_t)c.dweights) & 1) return TBE_ERR_UNSUPPORTED;
     // inputs are read again after the first results are written
-    const struct { const void* p; int64_t rows, stride; } t[4] = {{in.hidden, in.tokens, in.hidden_stride},
-                                                                  {in.weights, in.vocab, in.weights_stride},
-                                                                  {c.dhidden, in.tokens, c.dhidden_stride},
-                                                                  {c.dweights, in.vocab, c.dweights_stride}};
-    for (int i = 0; i < 4; ++i)
-      for (int j = std::max(i + 1, 2); j < 4; ++j)
-        if (overlap(t[i].p, t[i].rows, t[i].stride, t[j].p, t[j].rows, t[j].stride, in.width)) return TBE_ERR_INVALID_ARG;
+    const int64_t wide = 2 * (int64_t)in.width, each = sizeof(float) * in.tokens;
+    const Region read[5] = {rows_of(in.hidden, in.tokens, 2 * in.hidden_stride, wide),
+                            rows_of(in.weights, in.vocab, 2 * in.weights_stride, wide),
+                            bytes_of(in.labels, (int64_t)sizeof(int64_t) * in.tokens), bytes_of(c.given, each),
+                            bytes_of(c.given_loss, each)};
+    const Region dh = rows_of(c.dhidden, in.tokens, 2 * c.dhidden_stride, wide),
+                 dw = rows_of(c.dweights, in.vocab, 2 * c.dweights_stride, wide);
+    for (const Region& r : read)
+      if (share(dh, r) || share(dw, r)) return TBE_ERR_INVALID_ARG;
+    if (share(dh, dw)) return TBE_ERR_INVALID_ARG;
   }
   const Layout w = layout(in, c.dhidden != nullptr);
   if (bytes < w.bytes) return TBE_ERR_WORKSPACE;

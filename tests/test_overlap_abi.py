@@ -1,5 +1,5 @@
-"""Outputs that share memory with inputs, or with each other, are refused by the C entries of linear attention
-(CPU only: host memory stands in for the device's; no call here reaches a launch)."""
+"""Outputs that share memory with inputs, or with each other, are refused by the C entries of linear attention and the
+catalogue loss (CPU only: host memory stands in for the device's; no call here reaches a launch)."""
 
 import ctypes
 import itertools
@@ -8,7 +8,7 @@ import pytest
 
 import table_embedding_bags_gb300 as tbe
 from table_embedding_bags_gb300.build import build
-from test_more_operators_abi import Linear, LinearGrads
+from test_more_operators_abi import Catalogue, Linear, LinearGrads
 
 INVALID = tbe.TBE_ERR_INVALID_ARG
 
@@ -91,3 +91,31 @@ def test_rows_that_lie_between_others(lib, base):
     a = linear(base, stride=D, head=N * D)
     assert forward(lib, a, base(1) + 2 * N * D, stride=D, head=N * D) == INVALID
     assert forward(lib, a, base(1), stride=H * D, head=D) == INVALID
+
+
+def catalogue(lib, base, dh, dw, dhs, dws, hidden=None, hs=32, labels=None):
+    a = Catalogue(hidden or base(0), base(1), labels or base(2), hs, 32, 50, 60, 32, tbe.TBE_F16, 1.0)
+    f = base(3)
+    return lib.tbe_catalogue_loss(ctypes.byref(a), f, f, f, dh, dhs, dw, dws, 1.0, base(8), 16, None, None)
+
+
+def test_catalogue_gradients_between_other_rows(lib, base):
+    """Columns of one wider tensor are no overlap (the workspace given here is too small: that is what is found next)."""
+    passed = tbe.TBE_ERR_WORKSPACE
+    assert catalogue(lib, base, base(0) + 64, base(5), 64, 32, hs=64) == passed
+    assert catalogue(lib, base, base(5), base(5) + 64, 64, 64) == passed
+    for by in (62, 66, 0, 130):
+        assert catalogue(lib, base, base(0) + by, base(5), 64, 32, hs=64) == INVALID
+    assert catalogue(lib, base, base(5), base(5) + 62, 64, 64) == INVALID
+    assert catalogue(lib, base, base(2) + 398, base(5), 32, 32) == INVALID  # the last label
+    assert catalogue(lib, base, base(2) + 400, base(5), 32, 32) == passed
+
+
+def test_catalogue_gradients_on_their_own(lib, base):
+    a = Catalogue(base(0), base(1), base(2), 32, 32, 50, 60, 32, tbe.TBE_F16, 1.0)
+    full = lambda lse, loss, dh, dw: lib.tbe_catalogue_loss_backward_full(  # noqa: E731
+        ctypes.byref(a), lse, loss, dh, 32, dw, 32, 1.0, base(8), 16, None, None)
+    assert full(None, base(4), base(5), base(6)) == INVALID and full(base(3), base(4), None, base(6)) == INVALID
+    assert full(base(3), None, base(5), base(6)) == tbe.TBE_ERR_WORKSPACE
+    assert full(base(3), base(4), base(5), base(6)) == tbe.TBE_ERR_WORKSPACE
+    assert full(base(5), base(4), base(5), base(6)) == INVALID and full(base(3), base(6), base(5), base(6)) == INVALID
