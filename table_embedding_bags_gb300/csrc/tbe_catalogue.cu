@@ -760,7 +760,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     bar_init(&s.ask, 1);
     for (int k = 0; k < kTiles; ++k) {
       bar_init(&s.known[k], 1);
-      bar_init(&s.forgotten[k], 3 + 2 * kEpilogueWarps);  // the issuer, both copiers, all epilogue warps
+      // the copier and the epilogue warps of a block, and in the first one the issuer and the other block
+      bar_init(&s.forgotten[k], rank == 0 ? 3 + kEpilogueWarps : 1 + kEpilogueWarps);
     }
     s.dead = 0;
     for (int k = 0; k < kMaxJobs; ++k) s.job[k] = g.job[k];
@@ -777,13 +778,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
   if (warp == 0 && lane == 0) {
     asm volatile("fence.proxy.async;" ::: "memory");  // rows and g were written by ordinary stores
-    const uint32_t full0 = pair_addr(&s.full[0], 0), forgotten0 = pair_addr(&s.forgotten[0], 0), ring0 = smem_u32(ring);
+    const uint32_t full0 = pair_addr(&s.full[0], 0), ring0 = smem_u32(ring);
     uint32_t step = 0;  // steps of K so far
     for (uint32_t n = 0;; ++n) {
       if (!FEW && !wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
       const Tile t = FEW ? few_tile(g, n, count) : s.tile[n % kTiles];
-      if (!FEW && (t.mode >= 0 || t.steps >= 0)) pair_arrive_relaxed(forgotten0 + n % kTiles * 8);  // (it has been read)
       if (t.mode < 0) break;
+      if (!FEW) bar_arrive(&s.forgotten[n % kTiles]);
       const Job& j = s.job[t.job];
       const int32_t row0 = t.rb * kTileM + (int32_t)rank * kRowsM;
       const int32_t mine = t.blocks / 2;                       // B's blocks of this block
@@ -820,8 +821,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (uint32_t n = 0;; ++n) {
       if (!FEW && !wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
       const Tile t = FEW ? few_tile(g, n, count) : s.tile[n % kTiles];
-      if (!FEW && (t.mode >= 0 || t.steps >= 0)) bar_arrive(&s.forgotten[n % kTiles]);
       if (t.mode < 0) break;
+      if (!FEW) bar_arrive(&s.forgotten[n % kTiles]);
       if (n >= 2 && !wait(&s.drained[n & 1], (n / 2 - 1) & 1, s)) break;
       tc_after_sync();
       const uint32_t along_m = t.mode == kTable, along_n = t.mode >= kTable;
@@ -856,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         now = (int32_t)((gridDim.x >> 1) + atomicAdd(g.next, 1u));
       }
       if (now < total) t = tile_of(g, s.job, now, count);
-      if (n >= kTiles && !wait(&s.forgotten[slot], (n / kTiles - 1) & 1, s)) break;
+      if (n >= kTiles && !wait_pair(&s.forgotten[slot], (n / kTiles - 1) & 1, s)) break;
       s.tile[slot] = t;
       const uint32_t other = pair_addr(&s.tile[slot], 1);
 #pragma unroll
@@ -864,6 +865,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       bar_arrive(&s.known[slot]);
       pair_arrive(pair_addr(&s.known[slot], 1));
       if (now >= total) break;
+    }
+  } else if (!FEW && warp == 3 && lane == 0) {
+    // Tells the first block what this one has read.  An arrival there that orders its reads would wait for the outputs
+    // that an epilogue warp has on their way; this thread has none.
+    const uint32_t forgotten0 = pair_addr(&s.forgotten[0], 0);
+    for (uint32_t n = 0;; ++n) {
+      const uint32_t slot = n % kTiles;
+      if (!wait_pair(&s.known[slot], (n / kTiles) & 1, s) || s.tile[slot].mode < 0) break;
+      if (!wait(&s.forgotten[slot], (n / kTiles) & 1, s)) break;
+      pair_arrive(forgotten0 + slot * 8);
     }
   } else if (warp >= 4) {
     const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
@@ -874,8 +885,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (!FEW && !wait_pair(&s.known[n % kTiles], (n / kTiles) & 1, s)) break;
       const Tile t = FEW ? few_tile(g, n, count) : s.tile[n % kTiles];
       __syncwarp();
-      if (!FEW && lane == 0 && (t.mode >= 0 || t.steps >= 0)) pair_arrive_relaxed(pair_addr(&s.forgotten[n % kTiles], 0));
       if (t.mode < 0) break;
+      if (!FEW && lane == 0) bar_arrive(&s.forgotten[n % kTiles]);
       if (!wait(&s.done[n & 1], (n / 2) & 1, s)) break;
       tc_after_sync();
       if (FEW) {

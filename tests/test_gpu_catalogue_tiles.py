@@ -1,13 +1,16 @@
-"""Cross entropy over a catalogue: gradients between other tensors' columns."""
+"""Cross entropy over a catalogue: many tiles to a pair of blocks, gradients between other
+tensors' columns.  The definition and its bounds are those of test_gpu_catalogue.py."""
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import table_embedding_bags_gb300 as tbe  # noqa: E402
-from test_gpu_catalogue import make  # noqa: E402
+from test_gpu_catalogue import check, definition, make  # noqa: E402
 
 pytestmark = pytest.mark.gpu
+
+TYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
 
 
 def test_gradients_between_other_columns():
@@ -21,3 +24,25 @@ def test_gradients_between_other_columns():
     assert (rows[:, 128:] == 7).all() and (table[:, 64:128] == 7).all()
     with pytest.raises(tbe.TBEError):
         tbe.tbe_catalogue_loss(rows[:, :64], table[:, 128:], labels, dhidden=rows[:, 63:127], dweights=table[:, :64])
+
+
+def same_again(hidden, weights, labels, first, times=4, **more):
+    for _ in range(times):
+        got = tbe.tbe_catalogue_loss(hidden, weights, labels, **more)
+        assert all(x is None and y is None or torch.equal(x, y) for x, y in zip(got, first))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("N,V,D", [(6000, 60000, 16), (300, 400_000, 64), (30_000, 300, 16)])
+def test_many_tiles_to_a_pair(N, V, D, dtype):
+    """A pair's places for tiles are used again many times, by short tiles."""
+    hidden, weights, labels = make(N, V, D, TYPES[dtype], seed=21)
+    tiles = -(-N // 256) * -(-V // 256)
+    if V > 300:
+        assert tiles >= 8 * 4 * torch.cuda.get_device_properties(0).multi_processor_count // 2
+    got = tbe.tbe_catalogue_loss(hidden, weights, labels)
+    check(got, definition(hidden, weights, labels), grads=False)
+    same_again(hidden, weights, labels, got)
+    grads = tbe.tbe_catalogue_loss(hidden, weights, labels, want_grad=True, grad_scale=512.0)
+    check(grads, definition(hidden, weights, labels, grad_scale=512.0))
+    same_again(hidden, weights, labels, grads, want_grad=True, grad_scale=512.0)
