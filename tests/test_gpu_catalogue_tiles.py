@@ -1,12 +1,15 @@
-"""Cross entropy over a catalogue: many tiles to a pair of blocks, gradients between other
+"""Cross entropy over a catalogue: many tiles to a pair of blocks, many pieces of the vocabulary, gradients between other
 tensors' columns.  The definition and its bounds are those of test_gpu_catalogue.py."""
+
+import ctypes
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import table_embedding_bags_gb300 as tbe  # noqa: E402
-from test_gpu_catalogue import check, definition, make  # noqa: E402
+from test_gpu_catalogue import check, check_grads, definition, make  # noqa: E402
+from test_more_operators_abi import Catalogue  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +49,22 @@ def test_many_tiles_to_a_pair(N, V, D, dtype):
     grads = tbe.tbe_catalogue_loss(hidden, weights, labels, want_grad=True, grad_scale=512.0)
     check(grads, definition(hidden, weights, labels, grad_scale=512.0))
     same_again(hidden, weights, labels, grads, want_grad=True, grad_scale=512.0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("N,V,D", [(8000, 30_000, 96), (8192, 32_769, 64)])
+def test_many_pieces_of_the_vocabulary(N, V, D, dtype):
+    """Four pieces at least, the last one short: both buffers of g are written again behind what reads them, and one
+    launch makes a piece while it multiplies the one before."""
+    hidden, weights, labels = make(N, V, D, TYPES[dtype], seed=22)
+    kind = tbe.TBE_F16 if dtype == "f16" else tbe.TBE_BF16
+    a = Catalogue(hidden.data_ptr(), weights.data_ptr(), labels.data_ptr(), D, D, N, V, D, kind, 1.0)
+    # two buffers of a piece's g are part of the workspace: were they a third of the vocabulary wide, it would be larger
+    rows = -(-N // 256) * 256
+    assert tbe.load_library().tbe_catalogue_workspace_bytes(ctypes.byref(a), 1) < 4 * rows * V // 3
+    want = definition(hidden, weights, labels, grad_scale=512.0)
+    got = tbe.tbe_catalogue_loss(hidden, weights, labels, want_grad=True, grad_scale=512.0)
+    check(got, want)
+    same_again(hidden, weights, labels, got, want_grad=True, grad_scale=512.0)
+    dh, dw = tbe.tbe_catalogue_loss_backward(hidden, weights, labels, got.lse, grad_scale=512.0, token_loss=got.token_loss)
+    check_grads(dh, dw, want)
