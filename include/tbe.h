@@ -639,7 +639,9 @@ int tbe_preference_loss_backward_low(const tbe_preference_inputs* in, const floa
  *             and sums are fp32; probabilities are rounded to dtype before
  *             they are multiplied for the gradients.
  * Limits: 1 <= tokens <= 2^24, vocab <= 2^30, width <= 2^16, tokens * vocab <
- * 2^47 (in whole tiles of 256 x 256).
+ * 2^47 (in whole tiles of 256 x 256).  The workspace holds tokens * vocab / 32
+ * bytes of partial sums (but for up to 64 tokens over 32,768 rows or more),
+ * which memory ends before.
  */
 typedef struct tbe_catalogue_inputs {
   const void* hidden;

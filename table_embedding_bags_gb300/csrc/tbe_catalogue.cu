@@ -27,9 +27,9 @@
 // What bounds it: the tensor cores where the width is 512 or more (64 % of
 // their cycles under ncu), the exponentials and what stands around them below
 // (a tile of 256 x 256 costs 3,900 cycles beside its products, 2,050 of them the
-// rate of ex2).  8,192 x 100,000 x 512 bf16, 9 in 10 tokens taken: 2,227 us with
-// gradients, 1,355 TFLOP/s over the four products (a library's product of 8192^3
-// 1,938); every token taken, the loss alone 556 us, 1,509 TFLOP/s.  On the way
+// rate of ex2).  8,192 x 100,000 x 512 bf16, 9 in 10 tokens taken: 2,250 us with
+// gradients, 1,341 TFLOP/s over the four products (a library's product of 8192^3
+// 1,938); every token taken, the loss alone 554 us, 1,514 TFLOP/s.  On the way
 // there: 128 x 256 tiles, 4 stages, 4,087 us; 256 x 256 tiles to a pair of blocks
 // 3,372; one copy of 16 KB where there were two of 8, and arrivals that order
 // nothing, 2,560; tiles given out by a thread of their own, when they are wanted,
@@ -182,8 +182,11 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
   copy_row(a, k, k < count ? a.src + (a.rows ? (int64_t)a.rows[k] : k) * a.src_stride : nullptr, lane);
 }
 
-// Both steps in one launch, for batches whose labels every block can look at:
-// 8 x 1,000 x 64 bf16, the loss alone, 16.4 -> 14.7 us.
+// Both steps in one launch, for batches whose labels every block can look at.
+// In one and in two, the loss alone over 1,000 rows of 64 bf16: 8 tokens 16.4 and
+// 18.4 us, 512 16.5 and 18.5, 2,048 18.5 and 20.5; with gradients over 10,000 rows
+// 37.7 and 38.5, 46.1 and 48.2, 69.7 and 70.8 (a mask of 2,048 tokens is what a
+// block keeps; past it its reading of all labels would be what takes the time).
 constexpr int kFewTokens = 2048;
 struct FewArgs {
   PickArgs p;
@@ -1056,13 +1059,15 @@ int64_t whole(int64_t n, int64_t of) { return (n + of - 1) / of * of; }
 
 // Elements of a piece's g.  With 2^24, 2^25, 2^26 and 2^27: 8,192 x 100,000 x
 // 512 bf16 with gradients 3,115, 2,384, 2,291, 2,249 us; 4,001 x 10,007 x 256 156,
-// 144, 127, 126 us; 512 x 150,000 x 128 205, 197, 207, 186 us.  (Two buffers of
-// 128 MB each.)
+// 144, 127, 126 us; 512 x 150,000 x 128 205, 197, 207, 186 us.  Two buffers of 128
+// MB each, that is; 2^27 would take as much memory again for 1 to 10 %.
 constexpr int64_t kPiece = 1 << 26;
 constexpr int64_t kMaxTokens = 1 << 24;
-// The table's rows as the product's, from so many on: the loss alone of 64
-// tokens over 1,000,003, 100,000, 40,000 and 10,000 rows of 128 takes 70, 23.3,
-// 20.3 and 19.6 us so, and 119, 27.2, 21.0 and 16.4 us with the tokens as rows.
+// The table's rows as the product's, from so many on: the loss alone over 10,000,
+// 20,000, 40,000, 100,000 and 400,000 rows, so and with the tokens as rows:
+//   1 token, width 64:    18.6 18.6 18.6 20.6 28.9   16.2 18.5 20.7 27.6 61.1 us
+//   64 tokens, width 128: 20.6 20.6 20.7 24.7 39.4   16.6 18.9 21.0 28.5 61.6
+//   16 tokens, width 512: 20.6 22.7 24.9 35.3 78.9   18.6 22.6 24.7 36.5 83.7
 constexpr int32_t kFewFrom = 1 << 15;
 
 // Whether the log-sums take the table's rows for the product's.

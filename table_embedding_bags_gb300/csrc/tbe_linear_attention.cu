@@ -54,11 +54,12 @@
 // of the values and keys 1,700, state 300, outputs 2,200 beside the next copies:
 // 9,000 a tile, where its bytes alone would take 5,600.  Under ncu the outputs of
 // 40,000 x 4 x 128 bf16 read DRAM at 28 % of its rate with 15 % of the tensor
-// cores' cycles and 27 % of the issue slots in use; 64 wide, fp16: 28, 13, 45 %.
-// Prefill of 100,003 x 4 x 128 bf16 187 us (its bytes: 60 us), training pass of
-// 65,537 x 16 x 64 f16 with states 1,147 us (159), of 2,048 sequences, 40,960 x
-// 8 x 64 bf16 232 us (50).  The same recurrences in tiles of 64 with mma.sync,
-// four warps to a block, took 418, 1,466 and 358 us.
+// cores' cycles and 27 % of the issue slots in use; 64 wide, fp16: 26, 13, 45 %.
+// Prefill of 100,003 x 4 x 128 bf16 188 us (its bytes: 60 us), training pass of
+// 65,537 x 16 x 64 f16 with states 1,202 us (159), of 2,048 sequences, 40,960 x
+// 8 x 64 bf16 225 us (50), prefill of 257 sequences with states, 8,191 x 5 x 100
+// f16, 200 us (20).  The same recurrences in tiles of 64 with mma.sync, four warps
+// to a block, took 418, 1,466, 358 and 201 us.
 #include "tbe_overlap.cuh"
 #include "tbe_tensor.cuh"
 
